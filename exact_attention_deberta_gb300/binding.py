@@ -498,4 +498,96 @@ def df_layernorm(x, gamma, beta, residual=None, eps=1e-7, out=None, stream=None)
     return out
 
 
+_lib.df_embedding.argtypes = [_vp, _i, _i, _vp, _i, _i, ctypes.c_float, _vp, _i, _vp, _vp]
+_lib.df_embedding.restype = _i
+_lib.df_embedding_bwd.argtypes = [_vp, _i, _i, _vp, _i, _i, ctypes.c_float, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]
+_lib.df_embedding_bwd.restype = _i
+_lib.df_embedding_bwd_workspace_size.argtypes = [_i] * 3
+_lib.df_embedding_bwd_workspace_size.restype = _sz
+
+
+def _on_device(dev, tensors):
+    """Every tensor given is a contiguous tensor on the CUDA device ``dev``."""
+    for name, t in tensors:
+        if t is not None and (not t.is_cuda or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+
+
+def _stream_on(dev, stream) -> ctypes.c_void_p:
+    """The given stream, or the current one of the tensors' device."""
+    return _stream(torch.cuda.current_stream(dev) if stream is None else stream)
+
+
+def _int_sizes(**sizes):
+    """Sizes go to the library as C ints: refuse what would wrap around."""
+    for name, n in sizes.items():
+        if not 0 <= n < 2 ** 31:
+            raise ValueError(f"{name} = {n} is out of range")
+
+
+def _status_word(status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1):
+        raise ValueError("status must be an int32 tensor of one value")
+
+
+def _ids_64(ids) -> int:
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64")
+    return 1 if ids.dtype == torch.int64 else 0
+
+
+def df_embedding(ids, table, scale=1.0, out=None, status=None, stream=None):
+    """scale * table[ids]: ids [...] (int32 or int64), table [V, N] -> [..., N] in the
+    table's dtype.  Rows of ids outside the table are zeros (``status`` is set)."""
+    if table.dim() != 2 or table.dtype not in _DTYPE:
+        raise ValueError("table must be a bf16, fp16 or fp32 matrix [V, N]")
+    dev = table.device
+    _on_device(dev, (("ids", ids), ("table", table), ("out", out), ("status", status)))
+    _status_word(status)
+    V, N = table.shape
+    _int_sizes(ids=ids.numel(), V=V, N=N)
+    if out is None:
+        out = torch.empty(tuple(ids.shape) + (N,), dtype=table.dtype, device=dev)
+    elif out.dtype != table.dtype or tuple(out.shape) != tuple(ids.shape) + (N,):
+        raise ValueError("out must be [..., N] of the table's dtype")
+    with torch.cuda.device(dev):
+        _check(_lib.df_embedding(_ptr(ids), _ids_64(ids), ids.numel(), _ptr(table), V, N, float(scale), _ptr(out),
+                                 _DTYPE[table.dtype], _ptr(status), _stream_on(dev, stream)), "df_embedding")
+    return out
+
+
+def df_embedding_bwd_workspace_size(T, N, V) -> int:
+    return int(_lib.df_embedding_bwd_workspace_size(T, N, V))
+
+
+def df_embedding_bwd(ids, dout, vocab, scale=1.0, padding_idx=None, grad=None, accumulate=False, workspace=None,
+                     status=None, stream=None):
+    """Gradient of the table [vocab, N] in float32 for dout [..., N], the gradient of
+    ``df_embedding(ids, table, scale)``.  ``accumulate`` adds to ``grad``, which must
+    then be given; tokens with ``padding_idx`` pass no gradient."""
+    dev = dout.device
+    if dout.dtype not in _DTYPE or dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dout must be bf16, fp16 or fp32, [..., N] for ids [...]")
+    _on_device(dev, (("ids", ids), ("dout", dout), ("grad", grad), ("workspace", workspace), ("status", status)))
+    _status_word(status)
+    T, N, vocab = ids.numel(), dout.shape[-1], int(vocab)
+    _int_sizes(ids=T, N=N, vocab=vocab)
+    if grad is None:
+        if accumulate:
+            raise ValueError("accumulate needs the gradient to add to")
+        grad = torch.empty(vocab, N, dtype=torch.float32, device=dev)
+    elif grad.dtype != torch.float32 or tuple(grad.shape) != (vocab, N):
+        raise ValueError("grad must be float32 [vocab, N]")
+    if workspace is None:
+        size = df_embedding_bwd_workspace_size(T, N, vocab)
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    pad = -1 if padding_idx is None else int(padding_idx)
+    with torch.cuda.device(dev):
+        _check(_lib.df_embedding_bwd(_ptr(ids), _ids_64(ids), T, _ptr(dout), vocab, N, float(scale), pad,
+                                     1 if accumulate else 0, _ptr(grad), _DTYPE[dout.dtype], _ptr(status),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream_on(dev, stream)), "df_embedding_bwd")
+    return grad
+
+
 raw_library = _lib

@@ -459,6 +459,46 @@ df_status df_linear(const void* x, int M, int K, int n_out, const void* const* w
 df_status df_layernorm(const void* x, const void* residual, const void* gamma, const void* beta,
                        int M, int N, float eps, void* out, df_dtype dtype, df_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Token embeddings: the rows that enter the encoder (or a decoder that reads
+ * its states), and the gradient of the table.
+ *
+ * Lookup with scaling:  out[t] = scale * table[ids[t]]  for t < T.
+ *   ids     int32 (ids_64 = 0) or int64 (ids_64 = 1), [T]
+ *   table   [V, N], out [T, N], both of `dtype` (bf16, fp16 or fp32); the
+ *           product is formed in fp32 and rounded once
+ *   status  device int32 set to DF_ERR_INVALID_ARG (if it is 0) when an id lies
+ *           outside [0, V): that row of `out` is then zeros.  May be NULL; the
+ *           caller zeroes it.
+ * N a multiple of 8, at most 65536; T = 0 is a call that does nothing.  One
+ * launch.  Errors: DF_ERR_INVALID_ARG (NULL pointer, T < 0 or > 2^30, V or
+ * N < 1, dtype), DF_ERR_UNSUPPORTED (N), DF_ERR_ALIGNMENT (table or out not
+ * 16-byte aligned, ids not aligned to their own size), DF_ERR_CUDA. */
+df_status df_embedding(const void* ids, int ids_64, int T, const void* table, int V, int N,
+                       float scale, void* out, df_dtype dtype, int32_t* status,
+                       df_stream_t stream);
+
+/* Gradient of the table for a gradient dout [T, N] (`dtype`) of the lookup:
+ *     grad[v] = (accumulate ? grad[v] : 0) + scale * sum_{t: ids[t] = v} dout[t]
+ * in float32 [V, N].  Tokens with ids[t] = padding_idx (-1: none) and ids
+ * outside [0, V) (status as above) pass no gradient, whatever their row of
+ * dout holds.  accumulate = 0 writes every row (zeros where no token reached
+ * it); accumulate = 1 touches only the rows that tokens reached.  The tokens are sorted by id
+ * and each row is summed in fp32 in an order that depends on ids alone, without
+ * atomics: equal inputs give equal bits.
+ *   workspace  at least df_embedding_bwd_workspace_size() bytes, 256-byte
+ *              aligned, contents need not be initialised; calls that share it
+ *              must not overlap
+ * Errors as df_embedding, and DF_ERR_INVALID_ARG for padding_idx outside
+ * [-1, V), DF_ERR_WORKSPACE. */
+df_status df_embedding_bwd(const void* ids, int ids_64, int T, const void* dout, int V, int N,
+                           float scale, int padding_idx, int accumulate, float* grad,
+                           df_dtype dtype, int32_t* status, void* workspace,
+                           size_t workspace_bytes, df_stream_t stream);
+
+/* Bytes of workspace df_embedding_bwd needs (0 for sizes it rejects). */
+size_t df_embedding_bwd_workspace_size(int T, int N, int V);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,3 +26,4 @@ from .backward import (  # noqa: F401,E402
     backward_packed,
     backward_metric_flops,
 )
+from .embedding import embed, embed_grad  # noqa: F401,E402
