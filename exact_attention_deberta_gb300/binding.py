@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -588,6 +588,80 @@ def df_embedding_bwd(ids, dout, vocab, scale=1.0, padding_idx=None, grad=None, a
                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
                                      _stream_on(dev, stream)), "df_embedding_bwd")
     return grad
+
+
+_lib.df_cross_attn_fwd.argtypes = [_vp] * 6 + [_i] * 8 + [ctypes.c_float, _i] + [_vp] * 5
+_lib.df_cross_attn_fwd.restype = _i
+
+
+class CrossStats(NamedTuple):
+    """What the forward of a training step keeps for ``df_cross_attn_bwd``: the
+    rows' log-sum-exp (float32) and what rounding ``out`` dropped."""
+
+    lse: torch.Tensor
+    out_lo: torch.Tensor
+
+
+def _cross_shape(q, k, v, key_mask, cu_q, cu_k, max_q, max_k):
+    """(device, B, H, Hk, Lq, Lk, total_q, total_k, d) of a cross-attention call."""
+    dev = q.device
+    _on_device(dev, (("q", q), ("k", k), ("v", v), ("key_mask", key_mask), ("cu_seqlens_q", cu_q),
+                     ("cu_seqlens_k", cu_k)))
+    if q.dtype not in _DTYPE or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must share a dtype: bf16 or fp16")
+    if q.dim() != (4 if cu_q is None else 3):
+        raise ValueError("q must be [B, Lq, H, d], or [total_q, H, d] with cu_seqlens_q")
+    if k.dim() != (4 if cu_k is None else 3) or k.shape != v.shape or k.shape[-1] != q.shape[-1]:
+        raise ValueError("k and v must be [B, Lk, Hk, d], or [total_k, Hk, d] with cu_seqlens_k, with q's head size")
+    batch = set()
+    for name, cu, x, longest in (("q", cu_q, q, max_q), ("k", cu_k, k, max_k)):
+        if cu is None:
+            batch.add(x.shape[0])
+        else:
+            if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 1:
+                raise ValueError(f"cu_seqlens_{name} must be an int32 vector [B + 1]")
+            if longest is None:
+                raise ValueError(f"packed {name} needs max_seqlen_{name} (an upper bound of every length)")
+            batch.add(cu.numel() - 1)
+    if len(batch) != 1:
+        raise ValueError("q and k disagree on the number of sequences")
+    B = batch.pop()
+    H, d = q.shape[-2:]
+    Lq = q.shape[1] if cu_q is None else int(max_q)
+    Lk = k.shape[1] if cu_k is None else int(max_k)
+    total_q = B * Lq if cu_q is None else q.shape[0]
+    total_k = B * Lk if cu_k is None else k.shape[0]
+    if key_mask is not None and (cu_k is not None or key_mask.dtype != torch.uint8 or
+                                 tuple(key_mask.shape) != (B, Lk)):
+        raise ValueError("key_mask must be uint8 [B, Lk], for keys [B, Lk, Hk, d]")
+    _int_sizes(total_q=total_q, total_k=total_k, Lq=Lq, Lk=Lk)
+    return dev, B, H, k.shape[-2], Lq, Lk, total_q, total_k, d
+
+
+def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *, max_seqlen_q=None,
+                      max_seqlen_k=None, scale=None, out=None, with_stats=False, status=None, stream=None):
+    """Attention of queries [B, Lq, H, d] (or packed [T, H, d] with cu_seqlens_q) to keys
+    and values of another length, [B, Lk, Hk, d] (with an optional uint8 key_mask) or
+    packed with cu_seqlens_k.  ``scale`` defaults to 1 / sqrt(d).  Returns ``out``, or
+    (out, CrossStats) for a training step (``with_stats``)."""
+    dev, B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                                    max_seqlen_k)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must match q in shape and dtype")
+    _on_device(dev, (("out", out), ("status", status)))
+    _status_word(status)
+    stats = CrossStats(torch.empty(q.shape[:-1], dtype=torch.float32, device=dev),
+                       torch.empty_like(q)) if with_stats else None
+    with torch.cuda.device(dev):
+        st = _lib.df_cross_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(key_mask), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                    B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], _ptr(out),
+                                    _ptr(stats.out_lo) if stats else None, _ptr(stats.lse) if stats else None,
+                                    _ptr(status), _stream_on(dev, stream))
+    _check(st, "df_cross_attn_fwd")
+    return (out, stats) if with_stats else out
 
 
 raw_library = _lib

@@ -320,6 +320,13 @@ df_status build_problem(const void* q, const void* k, const void* v, const void*
 
 }  // namespace
 
+namespace dfa {
+unsigned long long wait_budget() {
+  const unsigned long long wb = g_wait_budget.load();
+  return wb ? wb : kDefaultWaitBudget;
+}
+}  // namespace dfa
+
 extern "C" {
 
 const char* df_attn_status_string(df_status s) {

@@ -1,0 +1,151 @@
+// Shared pieces of the cross-attention kernels (queries of one length against
+// keys and values of another): the call's arguments, the list of query tiles,
+// the tensor maps and the bounded waits.
+//
+// A query tile holds 128 rows: `tpt` = floor(128 / G) consecutive tokens times
+// the G query heads that share one key head, head fastest, so that row r is
+// token r / G and head r % G.  Shared key heads are then read once for all of
+// their query heads and a single-token call still fills G rows of its tile.
+// Head sizes that are not 64 or 128 run as the next of the two: the tensor
+// maps end a row at d, and a copy fills the columns behind it with zeros.
+#pragma once
+
+#include "df_tc_common.cuh"
+
+namespace dfa {
+
+struct CrossArgs {
+  const uint8_t* key_mask;   // [B, Lk] or NULL
+  const int32_t* cu_q;       // [B + 1] or NULL: queries are [B, Lq]
+  const int32_t* cu_k;       // [B + 1] or NULL: keys are [B, Lk]
+  int B, H, Hk, G, Lq, Lk, Tq, Tk, d;
+  int tpt;                   // tokens per query tile
+  float kscale;              // scale * log2(e)
+  float scale;
+  int32_t* status;
+  unsigned long long budget;
+};
+
+// One query tile against its sequence's keys.
+struct CrossItem {
+  int q0;   // first token (row of q)
+  int nq;   // tokens of the tile that belong to the sequence, 1 .. tpt
+  int k0;   // first key (row of k)
+  int nk;   // keys of the sequence
+  int hk;   // key head; -1 ends the list
+  int b;    // batch row (for key_mask)
+};
+
+__device__ __forceinline__ void cross_fail(int32_t* status, int code) {
+  if (status) atomicCAS(status, 0, code);
+}
+
+// Rows [*start, *start + n) of sequence b; a sequence whose offsets are not
+// 0 <= cu[b] <= cu[b + 1] <= total is taken as empty and reported.
+__device__ __forceinline__ int seq_rows(const int32_t* cu, int b, int len, int total, int32_t* status, int* start) {
+  if (!cu) {
+    *start = b * len;
+    return len;
+  }
+  const int s = cu[b], e = cu[b + 1];
+  if (s < 0 || e < s || e > total) {
+    cross_fail(status, (int)DF_ERR_INVALID_ARG);
+    *start = 0;
+    return 0;
+  }
+  *start = s;
+  return e - s;
+}
+
+// Bounded wait that gives up as soon as another role of the CTA has (and
+// records the timeout): the control flow after it stays the same either way.
+__device__ __forceinline__ bool cross_wait(uint64_t* bar, uint32_t parity, unsigned long long budget,
+                                           volatile int* abort, int32_t* status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (*abort) return false;
+    if ((unsigned long long)(clock64() - t0) > budget) {
+      *abort = 1;
+      cross_fail(status, (int)DF_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  }
+}
+
+// 3-D tiled load: column, head, token.
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(ptx::smem_u32(dst)),
+      "l"((uint64_t)tmap), "r"(c0), "r"(c1), "r"(c2), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
+// Finds query tiles by number, warp-collectively.  Tiles are numbered by
+// sequence, then key head, then position; in packed mode the rows behind the
+// last sequence count as one more sequence, without keys.  Numbers must not
+// decrease from call to call (the walk over the sequences never goes back).
+struct TileWalk {
+  int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones
+  long long done = 0;  // tiles of the sequences before b0
+
+  __device__ __forceinline__ CrossItem find(const CrossArgs& a, long long number) {
+    const int lane = threadIdx.x & 31;
+    const int last = a.cu_q ? a.B : a.B - 1;
+    CrossItem it;
+    it.hk = -1;
+    it.q0 = it.nq = it.k0 = it.nk = it.b = 0;
+    for (; b0 <= last; b0 += 32) {
+      const int b = b0 + lane;
+      int start = 0, n = 0;
+      if (b < a.B) {
+        n = seq_rows(a.cu_q, b, a.Lq, a.Tq, a.status, &start);
+      } else if (b == last) {
+        start = min(max(a.cu_q[a.B], 0), a.Tq);
+        n = a.Tq - start;
+      }
+      const int tiles = (n + a.tpt - 1) / a.tpt;
+      long long incl = (long long)tiles * a.Hk;
+      const long long own = incl;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const long long total = __shfl_sync(0xffffffffu, incl, 31);
+      if (number < done + total) {
+        const unsigned hit = __ballot_sync(0xffffffffu, number < done + incl);
+        const int src = __ffs(hit) - 1;
+        const int at = (int)(number - done - __shfl_sync(0xffffffffu, incl - own, src));
+        const int nt = __shfl_sync(0xffffffffu, tiles, src);
+        const int s = __shfl_sync(0xffffffffu, start, src), len = __shfl_sync(0xffffffffu, n, src);
+        it.b = b0 + src;
+        it.hk = at / nt;
+        const int tok = (at - it.hk * nt) * a.tpt;
+        it.q0 = s + tok;
+        it.nq = min(a.tpt, len - tok);
+        if (it.b < a.B) it.nk = seq_rows(a.cu_k, it.b, a.Lk, a.Tk, a.status, &it.k0);
+        return it;
+      }
+      done += total;
+    }
+    return it;
+  }
+};
+
+// Host side (df_cross.cu): [rows][heads][d] 16-bit rows in boxes of 64 columns,
+// box_heads heads and box_rows rows, 128-byte swizzle.
+bool encode_heads(CUtensorMap* m, const void* base, long long rows, int heads, int d, bool bf16, int box_heads,
+                  int box_rows);
+int device_sms();
+// Argument checks and arguments shared by the forward and the backward.
+df_status cross_check(const void* q, const void* k, const void* v, const uint8_t* key_mask, const int32_t* cu_q,
+                      const int32_t* cu_k, int B, int H, int Hk, int Lq, int Lk, int total_q, int total_k, int d,
+                      float scale, df_dtype dtype, int32_t* status, CrossArgs* a);
+// An upper bound of the number of query tiles.
+long long cross_query_tiles(const CrossArgs& a);
+unsigned long long wait_budget();
+
+}  // namespace dfa

@@ -460,6 +460,51 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
                        int M, int N, float eps, void* out, df_dtype dtype, df_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Cross attention: queries of one length (a decoder, a reader) against the
+ * keys and values of another (the encoder's states), without position terms.
+ * For query row i of sequence b and head h, whose key head is h / (H / Hk):
+ *     s_ij  = scale * q_i.k_j                   over the valid keys j of b
+ *     lse_i = log sum_j exp(s_ij)
+ *     out_i = sum_j exp(s_ij - lse_i) v_j
+ * A row without a valid key gets zeros and lse = -infinity.
+ *
+ *   q, out      [B, Lq, H, d], or with cu_seqlens_q (int32 [B + 1]) [total_q, H, d]
+ *   k, v        [B, Lk, Hk, d], or with cu_seqlens_k (int32 [B + 1]) [total_k, Hk, d]
+ *               H a multiple of Hk, at most 128 query heads per key head
+ *   key_mask    uint8 [B, Lk] (nonzero = valid, any pattern) or NULL; only
+ *               without cu_seqlens_k
+ *   Lq, Lk      padded lengths, or in packed mode upper bounds of the lengths
+ *               (they size the launch; the lengths themselves decide the result)
+ *   total_q, total_k  rows of q and k: B Lq and B Lk without cu_seqlens.  Packed
+ *               rows behind the last sequence get zeros (lse: -infinity)
+ *   d           a multiple of 8, at most 128
+ *   scale       > 0, finite
+ *   dtype       DF_BF16 or DF_FP16, shared by q, k, v, out, out_lo
+ *   out_lo      NULL, or like out: what rounding `out` to dtype dropped (rounded
+ *               itself).  df_cross_attn_bwd needs it: the gradient subtracts
+ *               dout.out from dout.v, and where few keys carry a row the
+ *               rounding of out alone would be all that is left.
+ *   lse         NULL, or float32 [B, Lq, H] / [total_q, H]
+ *   status      device int32, may be NULL; the caller zeroes it.  Receives
+ *               DF_ERR_DEVICE_TIMEOUT if a bounded wait of the kernel runs out
+ *               (df_attn_set_wait_budget), DF_ERR_INVALID_ARG if a sequence's
+ *               offsets are not 0 <= cu[b] <= cu[b + 1] <= total (it is taken
+ *               as empty; its rows of out are not written)
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to dtype
+ * as the operand of the product with v.  Keys that do not count, and rows of k
+ * and v outside the sequence, may hold anything (NaN included).  One launch, no
+ * workspace; equal inputs give equal bits.
+ * Errors: DF_ERR_INVALID_ARG (NULL pointer, sizes, H % Hk, scale, key_mask with
+ * cu_seqlens_k, dtype), DF_ERR_UNSUPPORTED (fp32, d, H / Hk > 128, over 2^30
+ * rows), DF_ERR_ALIGNMENT (tensors 16 bytes, lse and cu_seqlens 4), DF_ERR_CUDA. */
+df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
+                            const uint8_t* key_mask, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
+                            int total_q, int total_k, int d, float scale, df_dtype dtype,
+                            void* out, void* out_lo, float* lse, int32_t* status,
+                            df_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Token embeddings: the rows that enter the encoder (or a decoder that reads
  * its states), and the gradient of the table.
  *

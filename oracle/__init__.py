@@ -27,3 +27,4 @@ from .backward import (  # noqa: F401,E402
     backward_metric_flops,
 )
 from .embedding import embed, embed_grad  # noqa: F401,E402
+from .cross import cross_rows, cross_batch  # noqa: F401,E402

@@ -1,0 +1,190 @@
+"""GPU parity of the cross-attention forward against the float64 oracle on the
+same rounded inputs, within bounds counted in roundings (tests/_cross.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from _cross import call, check_forward, inputs, np64, to_dev, want
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+CASES = [  # B, H, Hk, d, Lq, Lk, dtype, q, k
+    (1, 1, 1, 64, 1, 1, BF, "padded", "full"),
+    (2, 2, 2, 64, 5, 128, HF, "padded", "full"),
+    (2, 3, 3, 64, 128, 129, BF, "padded", "full"),
+    (3, 4, 4, 64, 130, 300, HF, "padded", "masked"),
+    (5, 4, 2, 64, 257, 513, BF, "packed", "packed"),
+    (2, 2, 1, 128, 100, 700, BF, "padded", "full"),
+    (4, 6, 2, 128, 70, 390, HF, "packed", "masked"),
+    (3, 8, 1, 128, 40, 260, BF, "padded", "packed"),
+    (40, 2, 2, 64, 9, 200, BF, "packed", "packed"),
+    (2, 2, 2, 32, 65, 333, BF, "padded", "masked"),
+    (2, 3, 1, 96, 77, 150, HF, "packed", "packed"),
+    (2, 2, 2, 8, 33, 140, BF, "padded", "full"),
+    (1, 128, 1, 64, 3, 200, BF, "padded", "full"),
+    (2, 65, 1, 72, 2, 150, HF, "packed", "full"),
+    (3, 24, 8, 64, 1, 1000, BF, "padded", "packed"),
+    (1, 1, 1, 128, 1, 3000, HF, "padded", "masked"),
+    (70, 4, 4, 64, 1, 260, BF, "padded", "packed"),
+    (9, 12, 12, 64, 300, 200, BF, "padded", "masked"),
+]
+
+
+@pytest.mark.parametrize("B,H,Hk,d,Lq,Lk,dtype,q,k", CASES)
+def test_forward_matches_oracle(lib, B, H, Hk, d, Lq, Lk, dtype, q, k):
+    x = inputs(B, H, Hk, d, Lq, Lk, dtype, q, k, seed=B + H + Lq + Lk)
+    dev = to_dev(x)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(dev["q"], float("nan"))
+    got, stats = call(lib, x, dev, out=out, with_stats=True, status=status)
+    w = want(oracle, x, d ** -0.5)
+    check_forward(got, w, dtype, d, stats.lse, stats.out_lo)
+    assert int(status.item()) == lib.DF_OK
+    assert torch.equal(call(lib, x, dev), got)  # without statistics, and again: the same bits
+
+
+@pytest.mark.parametrize("sigma,scale", [(4.0, None), (16.0, None), (1.0, 2.5), (1.0, 1e-3)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_large_and_small_scores(lib, sigma, scale, dtype):
+    x = inputs(2, 4, 2, 64, 90, 400, dtype, "padded", "masked", seed=5, sigma=sigma)
+    got, stats = call(lib, x, to_dev(x), scale=scale, with_stats=True)
+    w = want(oracle, x, 64 ** -0.5 if scale is None else float(np.float32(scale)))
+    check_forward(got, w, dtype, 64, stats.lse, stats.out_lo)
+
+
+@pytest.mark.parametrize("d,Lq,Lk", [(64, 40, 300), (128, 1, 900), (96, 200, 140)])
+def test_masked_and_foreign_rows_may_hold_anything(lib, d, Lq, Lk):
+    # masked keys, keys behind a packed sequence, and the other sequences' rows
+    x = inputs(3, 4, 2, d, Lq, Lk, BF, "padded", "masked", seed=d, nk=[Lk, 0, Lk // 2])
+    dev = to_dev(x)
+    clean = call(lib, x, dev)
+    off = dev["key_mask"] == 0
+    for junk in (float("nan"), float("inf"), -float("inf"), torch.finfo(BF).min):
+        for n in ("k", "v"):
+            dev[n] = dev[n].clone()
+            dev[n][off] = junk
+        assert torch.equal(call(lib, x, dev), clean)
+    assert int((clean[1] != 0).sum()) == 0  # no valid key
+    x = inputs(3, 4, 2, d, Lq, Lk, BF, "packed", "packed", seed=d, nq=[Lq, Lq, Lq], nk=[Lk // 2 + 3, 5, Lk])
+    dev = to_dev(x)
+    clean = call(lib, x, dev)
+    a, b = int(x["cu_k"][1]), int(x["cu_k"][2])
+    for n in ("k", "v"):
+        dev[n] = dev[n].clone()
+        dev[n][a:b] = float("nan")
+    dev["q"] = dev["q"].clone()
+    dev["q"][Lq:2 * Lq] = float("nan")
+    dirty = call(lib, x, dev)
+    assert torch.equal(dirty[:Lq], clean[:Lq]) and torch.equal(dirty[2 * Lq:], clean[2 * Lq:])
+
+
+def test_rows_behind_the_last_sequence_and_empty_sequences(lib):
+    x = inputs(5, 4, 2, 64, 200, 200, BF, "packed", "packed", seed=3, nq=[0, 150, 0, 200, 7], nk=[9, 0, 30, 200, 1])
+    w = want(oracle, x, 0.125)
+    for n in ("q", "k", "v"):
+        more = torch.full((300,) + tuple(x[n].shape[1:]), float("nan"), dtype=BF)
+        x[n] = torch.cat([x[n], more])
+    dev = to_dev(x)
+    got, stats = call(lib, x, dev, with_stats=True, out=torch.full_like(dev["q"], 7.0))
+    T = 357
+    assert int((got[T:] != 0).sum()) == 0 and bool((stats.lse[T:] == -float("inf")).all())
+    check_forward(got[:T], w, BF, 64, stats.lse[:T], stats.out_lo[:T])
+    assert int((got[:150] != 0).sum()) == 0  # queries of a sequence without keys
+
+
+def test_no_keys_no_queries_no_sequences(lib):
+    z = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")  # noqa: E731
+    out, stats = lib.df_cross_attn_fwd(z(2, 3, 4, 64), z(2, 0, 4, 64), z(2, 0, 4, 64), with_stats=True)
+    assert int((out != 0).sum()) == 0 and bool((stats.lse == -float("inf")).all())
+    assert lib.df_cross_attn_fwd(z(2, 0, 4, 64), z(2, 9, 4, 64), z(2, 9, 4, 64)).numel() == 0
+    assert lib.df_cross_attn_fwd(z(0, 3, 4, 64), z(0, 9, 4, 64), z(0, 9, 4, 64)).numel() == 0
+
+
+def test_bad_offsets_are_reported(lib):
+    x = inputs(3, 2, 2, 64, 40, 100, BF, "packed", "packed", seed=1, nq=[40, 40, 40], nk=[100, 90, 80])
+    dev = to_dev(x)
+    w = want(oracle, x, 0.125)
+    for name, bad in (("cu_k", [0, 100, 90, 270]), ("cu_k", [0, 100, 190, 1 << 29]), ("cu_q", [0, 40, 80, 500])):
+        d2 = dict(dev)
+        d2[name] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = call(lib, x, d2, status=status)
+        assert int(status.item()) == lib.DF_ERR_INVALID_ARG
+        first = {n: v[:40] for n, v in w.items()}
+        check_forward(got[:40], first, BF, 64)  # the sequence before it is not touched
+
+
+def test_longer_than_the_stated_bound(lib):
+    # max_seqlen sizes the launch only
+    x = inputs(2, 4, 4, 64, 300, 500, BF, "packed", "packed", seed=2, nq=[300, 20], nk=[500, 400])
+    x["Lq"] = x["Lk"] = 1
+    check_forward(call(lib, x, to_dev(x)), want(oracle, x, 0.125), BF, 64)
+
+
+def test_other_stream_and_captured_replay(lib):
+    x = inputs(3, 4, 2, 64, 50, 400, BF, "padded", "masked", seed=4)
+    dev = to_dev(x)
+    side = torch.cuda.Stream()
+    out = torch.empty_like(dev["q"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(lib, x, dev, out=out)
+    y = inputs(3, 4, 2, 64, 50, 400, BF, "padded", "masked", seed=6)
+    for n in ("q", "k", "v", "key_mask"):
+        dev[n].copy_(y[n])
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    check_forward(out, want(oracle, y, 0.125), BF, 64)
+    with torch.cuda.stream(side):
+        again = call(lib, x, dev)
+    side.synchronize()
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("d,Lq,Lk", [(64, 700, 900), (128, 700, 900), (64, 1, 2000)])
+def test_wait_budget_runs_out_and_recovers(lib, d, Lq, Lk):
+    x = inputs(2, 2, 2, d, Lq, Lk, BF, seed=9)
+    dev = to_dev(x)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.df_attn_set_wait_budget(1)
+    try:
+        call(lib, x, dev, status=status)
+        torch.cuda.synchronize()
+    finally:
+        lib.df_attn_set_wait_budget(0)
+    assert int(status.item()) == lib.DF_ERR_DEVICE_TIMEOUT
+    check_forward(call(lib, x, dev), want(oracle, x, d ** -0.5), BF, d)
+
+
+def test_refusals(lib):
+    z = lambda *s, t=BF: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    q, k = z(2, 3, 4, 64), z(2, 9, 2, 64)
+    for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
+        with pytest.raises(lib.DFError):
+            lib.df_cross_attn_fwd(q, k, k, **bad)
+    with pytest.raises(lib.DFError):
+        lib.df_cross_attn_fwd(z(2, 3, 3, 64), k, k)  # 3 query heads, 2 key heads
+    with pytest.raises(lib.DFError):
+        lib.df_cross_attn_fwd(z(2, 3, 4, 136), z(2, 9, 2, 136), z(2, 9, 2, 136))
+    with pytest.raises(lib.DFError):
+        lib.df_cross_attn_fwd(z(2, 3, 4, 64, t=torch.float32), k.float(), k.float())
+    with pytest.raises(ValueError):
+        lib.df_cross_attn_fwd(q, k, k.half())
+    with pytest.raises(ValueError):
+        lib.df_cross_attn_fwd(q, k.transpose(1, 2), k.transpose(1, 2))
+    with pytest.raises(ValueError):
+        lib.df_cross_attn_fwd(q, k, k, key_mask=torch.ones(2, 8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        lib.df_cross_attn_fwd(q, z(3, 9, 2, 64), z(3, 9, 2, 64))
+    cu = torch.tensor([0, 9, 18], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="max_seqlen_k"):
+        lib.df_cross_attn_fwd(q, z(18, 2, 64), z(18, 2, 64), cu_seqlens_k=cu)
+    odd = torch.zeros(2 * 3 * 4 * 64 + 4, dtype=BF, device="cuda")[4:].view(2, 3, 4, 64)
+    with pytest.raises(lib.DFError):
+        lib.df_cross_attn_fwd(odd, k, k)
