@@ -664,4 +664,50 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
     return (out, stats) if with_stats else out
 
 
+_lib.df_cross_attn_bwd.argtypes = [_vp] * 10 + [_i] * 8 + [ctypes.c_float, _i] + [_vp] * 5 + [_sz, _vp]
+_lib.df_cross_attn_bwd.restype = _i
+_lib.df_cross_attn_bwd_workspace_size.argtypes = [_i, _i]
+_lib.df_cross_attn_bwd_workspace_size.restype = _sz
+
+
+def df_cross_attn_bwd_workspace_size(total_q, H) -> int:
+    return int(_lib.df_cross_attn_bwd_workspace_size(total_q, H))
+
+
+def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *,
+                      max_seqlen_q=None, max_seqlen_k=None, scale=None, grads=None, workspace=None, status=None,
+                      stream=None):
+    """Gradients (dq, dk, dv), in the inputs' dtype, of ``df_cross_attn_fwd`` with the
+    same arguments; ``out`` and ``stats`` as its call with ``with_stats`` gave them.
+    ``grads`` may pass the three tensors preallocated."""
+    dev, B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                                    max_seqlen_k)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if grads is None:
+        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+    dq, dk, dv = grads
+    for name, t, like in (("out", out, q), ("out_lo", stats.out_lo, q), ("dout", dout, q), ("dq", dq, q),
+                          ("dk", dk, k), ("dv", dv, v)):
+        if t is None and name == "out_lo":
+            continue
+        if t.dtype != like.dtype or t.shape != like.shape:
+            raise ValueError(f"{name} must match {'q' if like is q else 'k' if like is k else 'v'} in shape and dtype")
+    if stats.lse.dtype != torch.float32 or stats.lse.shape != q.shape[:-1]:
+        raise ValueError("stats.lse must be float32, [..., H]")
+    if workspace is None:
+        size = df_cross_attn_bwd_workspace_size(Tq, H)
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    _on_device(dev, (("out", out), ("out_lo", stats.out_lo), ("lse", stats.lse), ("dout", dout), ("dq", dq),
+                     ("dk", dk), ("dv", dv), ("workspace", workspace), ("status", status)))
+    _status_word(status)
+    with torch.cuda.device(dev):
+        st = _lib.df_cross_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(stats.out_lo), _ptr(stats.lse),
+                                    _ptr(dout), _ptr(key_mask), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, H, Hk, Lq,
+                                    Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], _ptr(dq), _ptr(dk), _ptr(dv), _ptr(status),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream_on(dev, stream))
+    _check(st, "df_cross_attn_bwd")
+    return dq, dk, dv
+
+
 raw_library = _lib

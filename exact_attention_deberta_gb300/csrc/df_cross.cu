@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
   const uint32_t rank = args.splits > 1 ? cluster_rank() : 0u;
   // this CTA's key tiles [t0, t0 + nt) of an item
   auto part = [&](const CrossItem& it, int* t0) {
-    const int all = (it.nk + 127) >> 7;
+    const int all = (it.no + 127) >> 7;
     *t0 = (int)((long long)all * rank / args.splits);
     return (int)((long long)all * (rank + 1) / args.splits) - *t0;
   };
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
   auto read_item = [&](uint32_t c) {
     const uint32_t slot = c % kItemRing;
     CrossItem it;
-    it.q0 = it.nq = it.k0 = it.nk = it.b = 0;
+    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
     it.hk = -1;
     if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort, status)) {
       it = *ring_slot(c);
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
     uint32_t u = 0, qc = 0, u_issued = 0, q_issued = 0;
     const int clusters = gridDim.x / args.splits, first = blockIdx.x / args.splits;
     for (uint32_t c = 0;; ++c) {
-      CrossItem it = walk.find(a, (long long)first + (long long)c * clusters);
+      CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, (long long)first + (long long)c * clusters);
       const uint32_t slot = c % kItemRing;
       bool ok = true;
       if (lane == 0) {
@@ -247,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
             const uint32_t box = (uint32_t)(a.G * a.tpt) * 128u;
             mbar_expect_tx(q_full + qb, kChunks * box);
             for (int ch = 0; ch < kChunks; ++ch)
-              tma_load_3d(sQ + qb * SL::kTileBytes + ch * kBoxBytes, &maps.q, ch * 64, it.hk * a.G, it.q0, q_full + qb);
+              tma_load_3d(sQ + qb * SL::kTileBytes + ch * kBoxBytes, &maps.q, ch * 64, it.hk * a.G, it.r0, q_full + qb);
             q_issued = qc + 1;
           }
           ++qc;
           for (int t = 0; t < nt; ++t) {
-            const int row = it.k0 + (t0 + t) * 128;
+            const int row = it.o0 + (t0 + t) * 128;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++u) {
               const uint32_t s = u % R;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
       if (it.hk < 0) break;
       int t0;
       const int nt = part(it, &t0);
-      const bool row_in = row_tok < it.nq;
+      const bool row_in = row_tok < it.nr;
       // a row block without a valid row needs no weights: its P may hold anything,
       // since a row of P only reaches its own row of O
       const bool warp_in = __any_sync(0xffffffffu, row_in);
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
         const int sb = kTriS ? (int)(G % 3) : wg;
         const uint32_t tSw = tmem + 128u * sb + lane_off;
         // which keys of the tile count, one bit each
-        const int left = it.nk - (t0 + t) * 128;
+        const int left = it.no - (t0 + t) * 128;
         uint32_t bits[4];
         bool whole = left >= 128;
         if (a.key_mask) {
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
       const float l = s0.y * f0 + s1.y * f1;
       const bool alone = args.splits == 1;
       const float inv = !alone ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-      const size_t orow = ((size_t)(it.q0 + row_tok) * a.H + (size_t)it.hk * a.G + row_head);
+      const size_t orow = ((size_t)(it.r0 + row_tok) * a.H + (size_t)it.hk * a.G + row_head);
       float* sO = reinterpret_cast<float*>(sKV);  // a cluster's join: the ring is idle by then
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
       for (int i = (int)rank * 256 + (int)threadIdx.x - 128; i < 128 * kPieces; i += 256 * args.splits) {
         const int row = i / kPieces, piece = i - row * kPieces;
         const int tok = row / a.G;
-        if (tok >= it.nq || 4 * piece >= a.d) continue;
+        if (tok >= it.nr || 4 * piece >= a.d) continue;
         float m = -INFINITY, l = 0.f;
         for (int r = 0; r < args.splits; ++r) m = fmaxf(m, ld_cluster(map_rank(ml_addr + 16 * row, r)).x);
         float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const FwdArgs ar
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] *= inv;
-        const size_t orow = (size_t)(it.q0 + tok) * a.H + (size_t)it.hk * a.G + (row - tok * a.G);
+        const size_t orow = (size_t)(it.r0 + tok) * a.H + (size_t)it.hk * a.G + (row - tok * a.G);
         const size_t at = orow * a.d + 4 * piece;
         store_rounded<T, 4>(static_cast<T*>(args.out) + at, args.out_lo ? static_cast<T*>(args.out_lo) + at : nullptr,
                             o);

@@ -26,15 +26,25 @@ struct CrossArgs {
   unsigned long long budget;
 };
 
-// One query tile against its sequence's keys.
+// A tile of one side's rows (queries, or keys in the backward's key kernel)
+// against all rows of its sequence on the other side.
 struct CrossItem {
-  int q0;   // first token (row of q)
-  int nq;   // tokens of the tile that belong to the sequence, 1 .. tpt
-  int k0;   // first key (row of k)
-  int nk;   // keys of the sequence
+  int r0;   // first token of the tile
+  int nr;   // its tokens that belong to the sequence, at least 1
+  int o0;   // first token of the sequence's other side
+  int no;   // tokens there
   int hk;   // key head; -1 ends the list
   int b;    // batch row (for key_mask)
 };
+
+// The sequences' rows on one side of a call.
+struct CrossSide {
+  const int32_t* cu;  // or NULL: B sequences of len tokens each
+  int len, total;
+};
+
+__device__ __forceinline__ CrossSide query_side(const CrossArgs& a) { return {a.cu_q, a.Lq, a.Tq}; }
+__device__ __forceinline__ CrossSide key_side(const CrossArgs& a) { return {a.cu_k, a.Lk, a.Tk}; }
 
 __device__ __forceinline__ void cross_fail(int32_t* status, int code) {
   if (status) atomicCAS(status, 0, code);
@@ -42,13 +52,13 @@ __device__ __forceinline__ void cross_fail(int32_t* status, int code) {
 
 // Rows [*start, *start + n) of sequence b; a sequence whose offsets are not
 // 0 <= cu[b] <= cu[b + 1] <= total is taken as empty and reported.
-__device__ __forceinline__ int seq_rows(const int32_t* cu, int b, int len, int total, int32_t* status, int* start) {
-  if (!cu) {
-    *start = b * len;
-    return len;
+__device__ __forceinline__ int seq_rows(const CrossSide& side, int b, int32_t* status, int* start) {
+  if (!side.cu) {
+    *start = b * side.len;
+    return side.len;
   }
-  const int s = cu[b], e = cu[b + 1];
-  if (s < 0 || e < s || e > total) {
+  const int s = side.cu[b], e = side.cu[b + 1];
+  if (s < 0 || e < s || e > side.total) {
     cross_fail(status, (int)DF_ERR_INVALID_ARG);
     *start = 0;
     return 0;
@@ -83,30 +93,32 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int c0,
       : "memory");
 }
 
-// Finds query tiles by number, warp-collectively.  Tiles are numbered by
-// sequence, then key head, then position; in packed mode the rows behind the
-// last sequence count as one more sequence, without keys.  Numbers must not
-// decrease from call to call (the walk over the sequences never goes back).
+// Finds the tiles of one side by number, warp-collectively.  Tiles of `step`
+// tokens are numbered by sequence, then key head, then position; in packed mode
+// the rows behind the last sequence count as one more sequence, whose other
+// side is empty.  Numbers must not decrease from call to call (the walk over the
+// sequences never goes back).
 struct TileWalk {
   int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones
   long long done = 0;  // tiles of the sequences before b0
 
-  __device__ __forceinline__ CrossItem find(const CrossArgs& a, long long number) {
+  __device__ __forceinline__ CrossItem find(const CrossArgs& a, const CrossSide& rows, const CrossSide& other,
+                                            int step, long long number) {
     const int lane = threadIdx.x & 31;
-    const int last = a.cu_q ? a.B : a.B - 1;
+    const int last = rows.cu ? a.B : a.B - 1;
     CrossItem it;
     it.hk = -1;
-    it.q0 = it.nq = it.k0 = it.nk = it.b = 0;
+    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
     for (; b0 <= last; b0 += 32) {
       const int b = b0 + lane;
       int start = 0, n = 0;
       if (b < a.B) {
-        n = seq_rows(a.cu_q, b, a.Lq, a.Tq, a.status, &start);
+        n = seq_rows(rows, b, a.status, &start);
       } else if (b == last) {
-        start = min(max(a.cu_q[a.B], 0), a.Tq);
-        n = a.Tq - start;
+        start = min(max(rows.cu[a.B], 0), rows.total);
+        n = rows.total - start;
       }
-      const int tiles = (n + a.tpt - 1) / a.tpt;
+      const int tiles = (n + step - 1) / step;
       long long incl = (long long)tiles * a.Hk;
       const long long own = incl;
 #pragma unroll
@@ -123,10 +135,10 @@ struct TileWalk {
         const int s = __shfl_sync(0xffffffffu, start, src), len = __shfl_sync(0xffffffffu, n, src);
         it.b = b0 + src;
         it.hk = at / nt;
-        const int tok = (at - it.hk * nt) * a.tpt;
-        it.q0 = s + tok;
-        it.nq = min(a.tpt, len - tok);
-        if (it.b < a.B) it.nk = seq_rows(a.cu_k, it.b, a.Lk, a.Tk, a.status, &it.k0);
+        const int tok = (at - it.hk * nt) * step;
+        it.r0 = s + tok;
+        it.nr = min(step, len - tok);
+        if (it.b < a.B) it.no = seq_rows(other, it.b, a.status, &it.o0);
         return it;
       }
       done += total;

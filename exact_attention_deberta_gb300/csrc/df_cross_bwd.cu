@@ -1,0 +1,670 @@
+// Cross attention, backward, on tcgen05 (bf16 / fp16 I/O, fp32 accumulation).
+// With p_ij = exp(scale q_i.k_j - lse_i), D_i = dout_i.out_i and
+// dS_ij = p_ij (dout_i.v_j - D_i):
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,
+//   dv_j = sum_i p_ij dout_i       (sums over i also run over the query heads
+//                                   that share the key head).
+//
+// Three launches.  row_stats forms D_i from out + out_lo (fp32 sums; the rounding
+// of out alone would leave 2^-9 |dout||v| where few keys carry a row) and puts it
+// beside the row's lse in log2 units.  Two runs of one kernel then recompute the
+// scores tile by tile: for a tile of keys it streams the queries past (dk, dv),
+// for a tile of queries the keys (dq).  Five products would do with atomic sums
+// into dq; seven without atomics keep every sum in tensor memory in a fixed order,
+// so equal inputs give equal bits.
+//
+// Per 128 x 128 tile and half h of the streamed rows (64 columns each):
+//   S = X0.Y0^T, dP = X1.Y1^T         into tensor memory (64 + 64 columns)
+//   P, dS                             by warpgroup h, rounded to the I/O type,
+//                                     written over S and dP
+//   acc0 += dS.Y0 (dk or dq), acc1 += P.Y1 (dv; rows of P that do not count are 0)
+// (X the resident, Y the streamed tiles.)  While warpgroup h works on its half,
+// the tensor core runs the other half's products.
+//   warp 0        items and TMA loads
+//   warp 1        every tcgen05.mma
+//   warps 2, 3    per streamed tile: the rows' (lse, D) or the keys' mask bits into
+//                 shared memory, and zeros over streamed rows that do not count
+//                 (they are the reduction dimension of the second products)
+//   warps 4-11    P and dS, one thread per resident row; the epilogue
+//
+// fp16: dS spans too wide a range for its exponent, so it is scaled by a power of
+// two that puts the largest |dout_i| at about 16, and P (at most 1) by 2^14; the
+// results are scaled back in fp32.  bf16 needs neither.
+#include "df_cross.cuh"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace dfa {
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 384;
+constexpr uint32_t kItemRing = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPShift = 14.f;  // fp16: P is held as 2^14 p
+
+struct BwdArgs {
+  CrossArgs c;
+  const float2* stat;      // [Tq][H]: lse in log2 units (+inf without keys), D
+  const uint32_t* top;     // fp16: the largest |dout_i|^2, as bits
+  void* out0;              // dk or dq
+  void* out1;              // dv
+};
+
+struct BwdMaps {
+  CUtensorMap x0, x1, y0, y1;
+};
+
+// ------------------------------------------------------------- row statistics
+// One group of 16 lanes per (token, head).
+template <typename T>
+__global__ void __launch_bounds__(256) row_stats(const T* __restrict__ out, const T* __restrict__ out_lo,
+                                                 const T* __restrict__ dout, const float* __restrict__ lse, int d,
+                                                 long long rows, const int32_t* cu_q, int B, int H,
+                                                 float2* __restrict__ stat, uint32_t* top) {
+  const long long row = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int l = threadIdx.x & 15;
+  float sum = 0.f, n2 = 0.f;
+  if (row < rows && l * 8 < d) {
+    const size_t at = (size_t)row * d + l * 8;
+    const uint4 o4 = *reinterpret_cast<const uint4*>(out + at);
+    const uint4 g4 = *reinterpret_cast<const uint4*>(dout + at);
+    uint4 r4 = make_uint4(0u, 0u, 0u, 0u);
+    if (out_lo) r4 = *reinterpret_cast<const uint4*>(out_lo + at);
+    const T* o = reinterpret_cast<const T*>(&o4);
+    const T* g = reinterpret_cast<const T*>(&g4);
+    const T* r = reinterpret_cast<const T*>(&r4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float gv = IO<T>::to_f(g[e]);
+      sum += (IO<T>::to_f(o[e]) + IO<T>::to_f(r[e])) * gv;
+      n2 += gv * gv;
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+  }
+  const bool mine = row < rows && l == 0;
+  if (mine) {
+    const float v = lse[row];
+    stat[row] = make_float2(v == -INFINITY ? INFINITY : v * kLog2e, sum);
+  }
+  if (top) {
+    // rows outside every sequence do not count; neither does what is not finite
+    bool in = mine && n2 <= 3.0e38f;
+    if (in && cu_q) {
+      const long long tok = row / H;
+      in = tok >= cu_q[0] && tok < cu_q[B];
+    }
+    uint32_t bits = in ? __float_as_uint(n2) : 0u;
+    bits = __reduce_max_sync(0xffffffffu, bits);
+    if ((threadIdx.x & 31) == 0 && bits != 0u) atomicMax(top, bits);
+  }
+}
+
+// ------------------------------------------------------------ the tile kernel
+template <int D>
+struct BwdSmem {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kRes = D == 64 ? 2 : 1;     // resident pairs
+  static constexpr int kStages = D == 64 ? 4 : 2;  // streamed pairs
+  static constexpr uint32_t kTileBytes = kChunks * kBoxBytes;
+  static constexpr uint32_t x = 0;                                   // [kRes][X0 | X1]
+  static constexpr uint32_t y = x + kRes * 2 * kTileBytes;           // [kStages][Y0 | Y1]
+  static constexpr uint32_t col = y + kStages * 2 * kTileBytes;      // [kStages]: float -lse [128], D [128]; or 4 mask words
+  static constexpr uint32_t bars = col + kStages * 1024;
+  // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full [2];
+  // acc_full, acc_free, drain; item_full, item_empty
+  static constexpr int kBars = 2 * kRes + 3 * kStages + 4 + 3 + 2 * (int)kItemRing;
+  static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;
+  static constexpr uint32_t cur = ring + 32 * kItemRing;
+  static constexpr uint32_t misc = cur + 32;
+  static constexpr uint32_t bytes = misc + 16;
+  static constexpr uint32_t alloc = bytes + 1024;
+  static_assert(alloc <= 232448, "shared memory of one CTA");
+};
+
+// KEYS: the resident rows are keys (K, V), the streamed ones queries (Q, dout).
+template <int D, bool BF16, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs args, const __grid_constant__ BwdMaps maps) {
+  using SL = BwdSmem<D>;
+  constexpr int kChunks = SL::kChunks;
+  constexpr uint32_t kRes = SL::kRes, kStages = SL::kStages;
+  constexpr uint32_t kIdescS = idesc_f16(128, 64, BF16 ? 1 : 0, 0, 0);
+  constexpr uint32_t kIdescAcc = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr uint32_t kAccCols = (KEYS ? 2u : 1u) * D, kXFirst = 256u;
+  static_assert(tmem_region_fits(0, kAccCols, kXFirst), "accumulators below the scores");
+  static_assert(tmem_region_fits(kXFirst, 256, 512), "two halves of S and dP in 512 columns");
+  constexpr uint32_t kItemReaders = 1 + 2 + 1;  // issuer, warps 2 and 3, the warpgroups' reader
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SL::bars);
+  uint64_t* x_full = bars;
+  uint64_t* x_empty = x_full + kRes;
+  uint64_t* full = x_empty + kRes;
+  uint64_t* ready = full + kStages;   // landed, rows that do not count zeroed, columns' values written
+  uint64_t* empty = ready + kStages;
+  uint64_t* s_full = empty + kStages;  // [2]
+  uint64_t* p_full = s_full + 2;       // [2]
+  uint64_t* acc_full = p_full + 2;
+  uint64_t* acc_free = acc_full + 1;
+  uint64_t* drain = acc_free + 1;
+  uint64_t* item_full = drain + 1;
+  uint64_t* item_empty = item_full + kItemRing;
+  auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
+  CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SL::misc);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + SL::misc + 4);
+
+  const CrossArgs& a = args.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (uint32_t b = 0; b < kRes; ++b) {
+      mbar_init(x_full + b, 1);
+      mbar_init(x_empty + b, 1);
+    }
+    for (uint32_t s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(ready + s, 2);
+      mbar_init(empty + s, 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(s_full + h, 1);
+      mbar_init(p_full + h, 4);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 8);
+    mbar_init(drain, 1);
+    for (uint32_t b = 0; b < kItemRing; ++b) {
+      mbar_init(item_full + b, 1);
+      mbar_init(item_empty + b, kItemReaders);
+    }
+    *s_abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&maps.x0);
+    tma_prefetch_desc(&maps.x1);
+    tma_prefetch_desc(&maps.y0);
+    tma_prefetch_desc(&maps.y1);
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const uint32_t tAcc0 = tmem, tAcc1 = tmem + D;
+  auto tS = [&](int h) { return tmem + kXFirst + 128u * h; };
+  auto tdP = [&](int h) { return tmem + kXFirst + 128u * h + 64u; };
+
+  const unsigned long long budget = a.budget;
+  int32_t* status = a.status;
+  const int x_step = KEYS ? 128 : a.tpt, y_step = KEYS ? a.tpt : 128;  // tokens per tile
+  auto y_tiles = [&](const CrossItem& it) { return (it.no + y_step - 1) / y_step; };
+  auto read_item = [&](uint32_t c) {  // one thread: the c-th item handed out, hk = -1 at the end
+    const uint32_t slot = c % kItemRing;
+    CrossItem it;
+    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    it.hk = -1;
+    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort, status)) {
+      it = *ring_slot(c);
+      mbar_arrive(item_empty + slot);
+    }
+    return it;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ items and loads
+    setmaxnreg_dec<56>();
+    TileWalk walk;
+    uint32_t g = 0, xc = 0, g_issued = 0, x_issued = 0;
+    const uint32_t q_box = (uint32_t)(a.G * a.tpt) * 128u;  // bytes of a 64-column box of a query tile
+    const uint32_t x_box = KEYS ? kBoxBytes : q_box, y_box = KEYS ? q_box : kBoxBytes;
+    for (uint32_t c = 0;; ++c) {
+      CrossItem it = walk.find(a, KEYS ? key_side(a) : query_side(a), KEYS ? query_side(a) : key_side(a), x_step,
+                               (long long)blockIdx.x + (long long)c * gridDim.x);
+      if (lane == 0) {
+        const uint32_t slot = c % kItemRing;
+        bool ok = true;
+        if (c >= kItemRing) ok = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+        if (*s_abort || !ok) it.hk = -1;
+        if (ok) {
+          *ring_slot(c) = it;
+          mbar_arrive(item_full + slot);
+        }
+        const int nt = it.hk < 0 ? 0 : y_tiles(it);
+        if (nt > 0) {
+          const int x_head = KEYS ? it.hk : it.hk * a.G, y_head = KEYS ? it.hk * a.G : it.hk;
+          const uint32_t xb = xc % kRes;
+          if (cross_wait(x_empty + xb, ((xc / kRes) & 1) ^ 1, budget, s_abort, status)) {
+            uint8_t* dst = sm + SL::x + xb * 2 * SL::kTileBytes;
+            mbar_expect_tx(x_full + xb, 2 * kChunks * x_box);
+            for (int ch = 0; ch < kChunks; ++ch) {
+              tma_load_3d(dst + ch * kBoxBytes, &maps.x0, ch * 64, x_head, it.r0, x_full + xb);
+              tma_load_3d(dst + SL::kTileBytes + ch * kBoxBytes, &maps.x1, ch * 64, x_head, it.r0, x_full + xb);
+            }
+            x_issued = xc + 1;
+          }
+          ++xc;
+          for (int t = 0; t < nt; ++t, ++g) {
+            const uint32_t s = g % kStages;
+            if (cross_wait(empty + s, ((g / kStages) & 1) ^ 1, budget, s_abort, status)) {
+              uint8_t* dst = sm + SL::y + s * 2 * SL::kTileBytes;
+              mbar_expect_tx(full + s, 2 * kChunks * y_box);
+              for (int ch = 0; ch < kChunks; ++ch) {
+                tma_load_3d(dst + ch * kBoxBytes, &maps.y0, ch * 64, y_head, it.o0 + t * y_step, full + s);
+                tma_load_3d(dst + SL::kTileBytes + ch * kBoxBytes, &maps.y1, ch * 64, y_head, it.o0 + t * y_step,
+                            full + s);
+              }
+              g_issued = g + 1;
+            }
+          }
+        }
+      }
+      if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
+    }
+    if (lane == 0) {
+      // no copy may still be landing when the CTA leaves
+      for (uint32_t k = g_issued > kStages ? g_issued - kStages : 0; k < g_issued; ++k)
+        mbar_wait(full + k % kStages, (k / kStages) & 1, kDrainBudget);
+      for (uint32_t k = x_issued > kRes ? x_issued - kRes : 0; k < x_issued; ++k)
+        mbar_wait(x_full + k % kRes, (k / kRes) & 1, kDrainBudget);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    setmaxnreg_dec<56>();
+    if (lane == 0) {
+      uint32_t g = 0, xc = 0;        // streamed tiles and items before this one
+      uint32_t pn[2] = {0, 0};       // halves h whose P and dS have been consumed
+      for (uint32_t c = 0;; ++c) {
+        const CrossItem it = read_item(c);
+        if (it.hk < 0) break;
+        const int nt = y_tiles(it);
+        if (nt == 0) continue;
+        const uint32_t xb = xc % kRes;
+        const uint8_t* sX = sm + SL::x + xb * 2 * SL::kTileBytes;
+        const bool x_ok = cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
+        auto issue_scores = [&](int t, int h) {
+          const uint32_t gs = g + t, s = gs % kStages;
+          bool ok = x_ok;
+          // both halves wait, so that each phase is waited for in order
+          ok = cross_wait(ready + s, (gs / kStages) & 1, budget, s_abort, status) && ok;
+          if (ok) {
+            const uint8_t* sY = sm + SL::y + s * 2 * SL::kTileBytes;
+            const uint64_t dx0 = kmajor_desc(sX, 0), dx1 = kmajor_desc(sX + SL::kTileBytes, 0);
+            const uint64_t dy0 = kmajor_desc(sY + h * 8192, 0), dy1 = kmajor_desc(sY + SL::kTileBytes + h * 8192, 0);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tS(h), dx0 + kmajor_step(k), dy0 + kmajor_step(k), kIdescS, k > 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tdP(h), dx1 + kmajor_step(k), dy1 + kmajor_step(k), kIdescS, k > 0);
+            mma_commit(s_full + h);
+          }
+        };
+        auto issue_sums = [&](int t, int h) {
+          const uint32_t s = (g + t) % kStages;
+          const uint32_t k0 = pn[h]++;
+          if (cross_wait(p_full + h, k0 & 1, budget, s_abort, status)) {
+            const uint32_t y_addr = smem_u32(sm + SL::y + s * 2 * SL::kTileBytes);
+            const uint64_t dy0 = vtile_desc(y_addr, 4 * h), dy1 = vtile_desc(y_addr + SL::kTileBytes, 4 * h);
+            const uint32_t first = t == 0 && h == 0 ? 0u : 1u;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tAcc0, tdP(h) + 8 * k, dy0 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
+            if (KEYS) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tAcc1, tS(h) + 8 * k, dy1 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
+            }
+            if (h == 1) mma_commit(empty + s);
+          }
+        };
+        issue_scores(0, 0);
+        issue_scores(0, 1);
+        // the epilogue has read the previous item's sums
+        if (xc > 0) cross_wait(acc_free, (xc - 1) & 1, budget, s_abort, status);
+        for (int t = 0; t < nt; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            issue_sums(t, h);
+            // the scores of (t + 1, h) follow the products that read P and dS of
+            // (t, h) in the same pipe
+            if (t + 1 < nt) issue_scores(t + 1, h);
+          }
+        mma_commit(acc_full);
+        mma_commit(x_empty + xb);
+        g += nt;
+        ++xc;
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, kDrainBudget);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ streamed rows
+    setmaxnreg_dec<56>();
+    const int w = warp - 2;  // rows 64 w .. 64 w + 63 of each tile
+    uint32_t g = 0;
+    for (uint32_t c = 0;; ++c) {
+      CrossItem it;
+      if (lane == 0) it = read_item(c);
+      it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
+      if (it.hk < 0) break;
+      it.o0 = __shfl_sync(0xffffffffu, it.o0, 0);
+      it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      it.b = __shfl_sync(0xffffffffu, it.b, 0);
+      const int nt = y_tiles(it);
+      for (int t = 0; t < nt; ++t, ++g) {
+        const uint32_t s = g % kStages;
+        const int left = it.no - t * y_step;  // tokens of the tile (and behind it)
+        bool in[2];
+        float2 st[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 64 * w + 32 * i + lane;
+          if constexpr (KEYS) {
+            const int tok = r / a.G, head = r - tok * a.G;
+            in[i] = tok < min(left, a.tpt);
+            st[i] = in[i] ? args.stat[(size_t)(it.o0 + t * y_step + tok) * a.H + it.hk * a.G + head]
+                          : make_float2(INFINITY, 0.f);
+          } else {
+            in[i] = r < left && (!a.key_mask || a.key_mask[(size_t)it.b * a.Lk + (size_t)t * 128 + r] != 0);
+          }
+        }
+        cross_wait(full + s, (g / kStages) & 1, budget, s_abort, status);
+        __syncwarp();
+        uint8_t* sY = sm + SL::y + s * 2 * SL::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 64 * w + 32 * i + lane;
+          if (!in[i]) {
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                *reinterpret_cast<uint4*>(sY + ch * kBoxBytes + r * 128 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(sY + SL::kTileBytes + ch * kBoxBytes + r * 128 + 16 * e) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+          }
+          if constexpr (KEYS) {
+            float* col = reinterpret_cast<float*>(sm + SL::col + s * 1024);
+            col[r] = (BF16 ? 0.f : kPShift) - st[i].x;
+            col[128 + r] = st[i].y;
+          } else {
+            const uint32_t bits = __ballot_sync(0xffffffffu, in[i]);
+            if (lane == 0) reinterpret_cast<uint32_t*>(sm + SL::col + s * 1024)[2 * w + i] = bits;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready + s);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS and the epilogue
+    setmaxnreg_inc<224>();
+    const int h = (warp - 4) >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;        // resident row
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const float ks = a.kscale;
+    const float2 ks2 = make_float2(ks, ks);
+    float grow = 1.f;                        // fp16: the power of two that scales dS
+    if (!BF16) {
+      const float n2 = __uint_as_float(*args.top);
+      if (n2 > 0.f) grow = exp2f(fminf(fmaxf(4.f - ceilf(0.5f * log2f(n2)), -100.f), 100.f));
+    }
+    const float ds_mul = BF16 ? 1.f : grow * exp2f(-kPShift);
+    const float2 ds_mul2 = make_float2(ds_mul, ds_mul);
+    const float scale0 = BF16 ? a.scale : a.scale / grow;        // dk, dq
+    const float scale1 = BF16 ? 1.f : exp2f(-kPShift);           // dv
+    const int row_tok = KEYS ? row : row / a.G, row_head = KEYS ? 0 : row - row_tok * a.G;
+    const bool reader = warp == 4 && lane == 0;
+    uint32_t g = 0, xc = 0, n = 0, c = 0;    // n: halves of this warpgroup so far
+    if (reader) *s_cur = read_item(c++);
+    named_sync(3, 256);
+    for (;;) {
+      const CrossItem it = *s_cur;
+      if (it.hk < 0) break;
+      const int nt = y_tiles(it);
+      const bool stored = row_tok < it.nr;   // the resident row belongs to the sequence
+      bool row_in = stored;
+      float nl = -INFINITY, dd = 0.f;
+      if (KEYS) {
+        const long long key = (long long)it.r0 + row;  // in [B, Lk] layout this is also the mask's index
+        if (row_in && a.key_mask) row_in = a.key_mask[key] != 0;
+      } else if (row_in) {
+        const float2 st = args.stat[(size_t)(it.r0 + row_tok) * a.H + it.hk * a.G + row_head];
+        nl = (BF16 ? 0.f : kPShift) - st.x;
+        dd = st.y;
+      }
+      for (int t = 0; t < nt; ++t, ++n) {
+        const uint32_t s = (g + t) % kStages;
+        cross_wait(s_full + h, n & 1, budget, s_abort, status);
+        __syncwarp();
+        tc_fence_after();
+        const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {  // 32 columns at a time
+          uint32_t rs[32], rd[32];
+          tmem_ld32(tS(h) + lane_off + 32 * q, rs);
+          tmem_ld32(tdP(h) + lane_off + 32 * q, rd);
+          tmem_ld_wait2(rs, rd);
+          uint32_t wp[16], wd[16];
+          uint32_t bits = 0xffffffffu;
+          if (!KEYS) bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 l4, d4;
+            if (KEYS) {
+              l4 = *reinterpret_cast<const float4*>(col + 64 * h + 32 * q + e);
+              d4 = *reinterpret_cast<const float4*>(col + 128 + 64 * h + 32 * q + e);
+            } else {
+              l4 = make_float4(nl, nl, nl, nl);
+              d4 = make_float4(dd, dd, dd, dd);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int j = e + 2 * u;
+              const float2 l2 = u ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+              const float2 dm = u ? make_float2(-d4.z, -d4.w) : make_float2(-d4.x, -d4.y);
+              const float2 z = fma2(make_float2(__uint_as_float(rs[j]), __uint_as_float(rs[j + 1])), ks2, l2);
+              const float2 p = make_float2(ex2(z.x), ex2(z.y));
+              float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[j]), __uint_as_float(rd[j + 1])), dm));
+              if (!BF16) ds = mul2(ds, ds_mul2);
+              wp[j / 2] = BF16 ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+              wd[j / 2] = BF16 ? pack_bf16x2(ds.x, ds.y) : pack_f16x2(ds.x, ds.y);
+            }
+          }
+          // what does not count has weight 0 whatever its row held
+          if (KEYS) {
+            if (!row_in) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) wp[e] = wd[e] = 0u;
+            }
+          } else if (bits != 0xffffffffu) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t two = (bits >> (2 * e)) & 3u;
+              wd[e] &= (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+            }
+          }
+          if (KEYS) tmem_st16(tS(h) + lane_off + 16 * q, wp);
+          tmem_st16(tdP(h) + lane_off + 16 * q, wd);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + h);
+      }
+      // ---- the item's results
+      if (nt > 0) cross_wait(acc_full, xc & 1, budget, s_abort, status);
+      __syncwarp();
+      tc_fence_after();
+      const int heads = KEYS ? a.Hk : a.H;
+      const size_t orow = (size_t)(it.r0 + row_tok) * heads + (KEYS ? it.hk : it.hk * a.G + row_head);
+      // KEYS: warpgroup 0 writes dk, 1 dv; else each half of dq's columns
+      const uint32_t tA = (KEYS && h == 1 ? tAcc1 : tAcc0) + lane_off;
+      T* dst = static_cast<T*>(KEYS && h == 1 ? args.out1 : args.out0) + orow * a.d;
+      const float mul = KEYS && h == 1 ? scale1 : scale0;
+      const int c0 = KEYS ? 0 : h * (D / 2), c1 = KEYS ? D : c0 + D / 2;
+#pragma unroll 1
+      for (int cc = c0; cc < c1; cc += 32) {
+        uint32_t r[32];
+        tmem_ld32(tA + cc, r);
+        tmem_ld_wait(r);
+        if (stored && *s_abort == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (cc + e >= a.d) break;
+            __align__(16) T v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = IO<T>::from_f(nt > 0 ? __uint_as_float(r[e + k]) * mul : 0.f);
+            *reinterpret_cast<uint4*>(dst + cc + e) = *reinterpret_cast<const uint4*>(v);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (nt > 0) {
+        if (lane == 0) mbar_arrive(acc_free);
+        ++xc;
+      }
+      g += nt;
+      named_sync(3, 256);  // every thread has read s_cur
+      if (reader) *s_cur = read_item(c++);
+      named_sync(3, 256);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF16, bool KEYS>
+cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items, cudaStream_t s) {
+  if (items == 0) return cudaSuccess;
+  auto kernel = cross_bwd_kernel<D, BF16, KEYS>;
+  const uint32_t bytes = BwdSmem<D>::alloc;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  // as in the forward: the launched registers must cover the setmaxnreg split
+  static int regs_ok = -1;
+  if (regs_ok < 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    regs_ok = fa.numRegs * kThreads >= 256 * 224 + 128 * 56 ? 1 : 0;
+  }
+  if (!regs_ok) return cudaErrorInvalidConfiguration;
+  kernel<<<(int)std::min<long long>(items, device_sms()), kThreads, bytes, s>>>(a, maps);
+  return cudaGetLastError();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_both(BwdArgs a, const BwdMaps& km, const BwdMaps& qm, void* dq, void* dk, void* dv,
+                        cudaStream_t s) {
+  const long long key_items = a.c.cu_k ? ((long long)a.c.Tk / 128 + a.c.B + 1) * a.c.Hk
+                                       : (long long)((a.c.Lk + 127) / 128) * a.c.B * a.c.Hk;
+  if (a.c.Tk > 0) {
+    a.out0 = dk;
+    a.out1 = dv;
+    const cudaError_t e = launch_tiles<D, BF16, true>(a, km, key_items, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.c.Tq > 0) {
+    a.out0 = dq;
+    a.out1 = nullptr;
+    return launch_tiles<D, BF16, false>(a, qm, cross_query_tiles(a.c), s);
+  }
+  return cudaSuccess;
+}
+
+template <typename T>
+void launch_stats(const void* out, const void* out_lo, const void* dout, const float* lse, const CrossArgs& c,
+                  float2* stat, uint32_t* top, cudaStream_t s) {
+  const long long rows = (long long)c.Tq * c.H;
+  row_stats<T><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(static_cast<const T*>(out), static_cast<const T*>(out_lo),
+                                                           static_cast<const T*>(dout), lse, c.d, rows, c.cu_q, c.B,
+                                                           c.H, stat, top);
+}
+
+bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr size_t kTopBytes = 256;
+
+}  // namespace
+}  // namespace dfa
+
+using namespace dfa;
+
+extern "C" size_t df_cross_attn_bwd_workspace_size(int total_q, int H) {
+  if (total_q < 0 || total_q > (1 << 30) || H < 1 || (long long)total_q * H > (1ll << 34)) return 0;
+  return kTopBytes + (((size_t)total_q * H * sizeof(float2) + 255) & ~(size_t)255);
+}
+
+extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* out_lo,
+                                       const float* lse, const void* dout, const uint8_t* key_mask,
+                                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
+                                       int Lq, int Lk, int total_q, int total_k, int d, float scale, df_dtype dtype,
+                                       void* dq, void* dk, void* dv, int32_t* status, void* workspace,
+                                       size_t workspace_bytes, df_stream_t stream) {
+  BwdArgs a;
+  const df_status st = cross_check(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk, Lq, Lk, total_q, total_k,
+                                   d, scale, dtype, status, &a.c);
+  if (st != DF_OK) return st;
+  if ((total_q > 0 && (!out || !lse || !dout || !dq)) || (total_k > 0 && (!dk || !dv))) return DF_ERR_INVALID_ARG;
+  if (!al16(out) || !al16(out_lo) || !al16(dout) || !al16(dq) || !al16(dk) || !al16(dv) || ((uintptr_t)lse & 3u) != 0 ||
+      ((uintptr_t)workspace & 255u) != 0)
+    return DF_ERR_ALIGNMENT;
+  const size_t need = df_cross_attn_bwd_workspace_size(total_q, H);
+  if (need == 0) return DF_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < need) return DF_ERR_WORKSPACE;
+  if (total_q == 0 && total_k == 0) return DF_OK;
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool bf16 = dtype == DF_BF16;
+  uint32_t* top = bf16 ? nullptr : static_cast<uint32_t*>(workspace);
+  float2* stat = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kTopBytes);
+  a.stat = stat;
+  a.top = top;
+  if (top && cudaMemsetAsync(top, 0, 4, s) != cudaSuccess) return DF_ERR_CUDA;
+  if (total_q > 0) {
+    if (bf16) launch_stats<__nv_bfloat16>(out, out_lo, dout, lse, a.c, stat, top, s);
+    else launch_stats<__half>(out, out_lo, dout, lse, a.c, stat, top, s);
+    if (cudaGetLastError() != cudaSuccess) return DF_ERR_CUDA;
+  }
+  // a side without rows is never copied from: its maps then describe the other one
+  const bool has_q = total_q > 0, has_k = total_k > 0;
+  const void* qp = has_q ? q : k;
+  const void* gp = has_q ? dout : k;
+  const void* kp = has_k ? k : q;
+  const void* vp = has_k ? v : q;
+  const int q_heads = has_q ? H : Hk, k_heads = has_k ? Hk : H;
+  const long long q_rows = has_q ? total_q : total_k, k_rows = has_k ? total_k : total_q;
+  CUtensorMap mq, mg, mk, mv;
+  if (!encode_heads(&mq, qp, q_rows, q_heads, d, bf16, a.c.G, a.c.tpt) ||
+      !encode_heads(&mg, gp, q_rows, q_heads, d, bf16, a.c.G, a.c.tpt) ||
+      !encode_heads(&mk, kp, k_rows, k_heads, d, bf16, 1, 128) ||
+      !encode_heads(&mv, vp, k_rows, k_heads, d, bf16, 1, 128))
+    return DF_ERR_CUDA;
+  const BwdMaps key_maps = {mk, mv, mq, mg}, query_maps = {mq, mg, mk, mv};
+  const cudaError_t e =
+      d <= 64 ? (bf16 ? launch_both<64, true>(a, key_maps, query_maps, dq, dk, dv, s)
+                      : launch_both<64, false>(a, key_maps, query_maps, dq, dk, dv, s))
+              : (bf16 ? launch_both<128, true>(a, key_maps, query_maps, dq, dk, dv, s)
+                      : launch_both<128, false>(a, key_maps, query_maps, dq, dk, dv, s));
+  return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}

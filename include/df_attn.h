@@ -504,6 +504,39 @@ df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
                             void* out, void* out_lo, float* lse, int32_t* status,
                             df_stream_t stream);
 
+/* Gradients of sum(out * dout) for df_cross_attn_fwd, with D_i = dout_i.out_i,
+ * p_ij = exp(s_ij - lse_i) and dS_ij = p_ij (dout_i.v_j - D_i):
+ *     dq_i = scale sum_j dS_ij k_j
+ *     dk_j = scale sum_i dS_ij q_i        over the rows i of every query head that
+ *     dv_j = sum_i p_ij dout_i            shares the key head
+ *   q, k, v, key_mask, cu_seqlens_*, B .. dtype, status: as in the forward call
+ *   out, out_lo, lse   as the forward gave them (out_lo may be NULL, at the cost
+ *                      of the accuracy described there)
+ *   dout       like out
+ *   dq, dk, dv like q, k, v, in `dtype`: written in full.  Keys that do not count
+ *              and rows behind the last packed sequence get zeros
+ *   workspace  at least df_cross_attn_bwd_workspace_size() bytes, 256-byte
+ *              aligned, contents need not be initialised; calls that share it
+ *              must not overlap
+ * Scores, dout.v and every sum are fp32 (dk and dv are summed over a group's
+ * heads before their only rounding); the weights and dS are rounded to dtype as
+ * operands of the second products (fp16: scaled by powers of two first, so that
+ * small gradients keep their digits while |dout_i| |v_j| of any row and key is
+ * below about 2000 times the largest |dout_i|).  No atomics in the sums: equal
+ * inputs give equal bits.  Three launches (fp16: and one 4-byte memset).
+ * Errors: as the forward, and DF_ERR_WORKSPACE. */
+df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                            const void* out_lo, const float* lse, const void* dout,
+                            const uint8_t* key_mask, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
+                            int total_q, int total_k, int d, float scale, df_dtype dtype,
+                            void* dq, void* dk, void* dv, int32_t* status, void* workspace,
+                            size_t workspace_bytes, df_stream_t stream);
+
+/* Bytes of workspace df_cross_attn_bwd needs: 8 per query row and head (0 for
+ * sizes it rejects). */
+size_t df_cross_attn_bwd_workspace_size(int total_q, int H);
+
 /* ---------------------------------------------------------------------------
  * Token embeddings: the rows that enter the encoder (or a decoder that reads
  * its states), and the gradient of the table.

@@ -89,10 +89,43 @@ def check_forward(out, w, dtype, d, lse=None, out_lo=None):
         empty = np.isinf(w["lse"])
         assert (l[empty] == -np.inf).all()
         # the sum itself is right to e; its logarithm, and the product with ln 2, round
-        assert (np.abs(l - w["lse"])[~empty] <= (e + 8 * U32 * (np.abs(np.where(empty, 0, w["lse"])) + 6))[~empty]).all()
+        tol = e[~empty] + 8 * U32 * (np.abs(w["lse"][~empty]) + 6)
+        assert (np.abs(l[~empty] - w["lse"][~empty]) <= tol).all()
     if out_lo is not None:
         lo = np64(out_lo)
         half = torch.finfo(dtype).eps / 2
         assert (np.abs(lo) <= half * np.abs(got) * 1.01 + tiny).all()
         # together they carry the fp32 result: the rounding to the type is gone
         assert (np.abs(got + lo - w["out"]) <= p_part + half * rounding + tiny).all()
+
+
+def call_bwd(binding, x, dev, out, stats, scale=None, **more):
+    return binding.df_cross_attn_bwd(dev["q"], dev["k"], dev["v"], out, stats, dev["dout"], key_mask=dev["key_mask"],
+                                     cu_seqlens_q=dev["cu_q"], cu_seqlens_k=dev["cu_k"], max_seqlen_q=x["Lq"],
+                                     max_seqlen_k=x["Lk"], scale=scale, **more)
+
+
+def check_backward(grads, w, dtype, d):
+    """Three roundings to the type meet in a gradient: of the operand (the weight, or
+    dS), of the forward's weights through D, of the result; everything else is fp32.
+
+    Entry by entry each is counted at its worst, half a step of every term.  The
+    terms' signs are independent, so over a whole gradient each rounding weighs at
+    most half a step of its norm: three halves in all (and the fp32 part, for
+    gradients that are themselves differences that cancel)."""
+    half = torch.finfo(dtype).eps / 2
+    fp32 = float(score_error(w, d).max()) + (d + 4) * U32
+    # fp16: results below its normal range are off by half a step of 2^-24
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 1e-37
+    for name, t in zip(("dq", "dk", "dv"), grads):
+        got, ref = np64(t), w[name]
+        assert np.isfinite(got).all(), name
+        err, mass = np.abs(got - ref), w[name + "_mass"]
+        if name == "dv":
+            terms = (half + fp32) * mass
+        else:
+            terms = half * w[name + "_round"] + (half + fp32) * mass
+        assert (err <= 1.01 * terms + half * (np.abs(ref) + terms) + tiny).all(), name
+        norm = lambda z: float(np.sqrt((z ** 2).sum()))  # noqa: E731
+        assert norm(err) <= 3 * half * norm(ref) + 4 * fp32 * norm(mass) + tiny * np.sqrt(err.size), \
+            (name, norm(err), norm(ref))

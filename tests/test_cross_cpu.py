@@ -67,6 +67,18 @@ def _fwd(b, **over):
         None, None)
 
 
+def _bwd(b, **over):
+    a = dict(q=0x10000, k=0x20000, v=0x30000, mask=None, cu_q=None, cu_k=None, B=2, H=4, Hk=2, Lq=3, Lk=9, Tq=6, Tk=18,
+             d=64, scale=0.125, dtype=0, out=0x40000, lo=None, lse=0x50000, dout=0x60000, dq=0x70000, dk=0x80000,
+             dv=0x90000, ws=0xa0000, bytes=1 << 20)
+    a.update(over)
+    vp = lambda x: None if x is None else ctypes.c_void_p(x)  # noqa: E731
+    return b.raw_library.df_cross_attn_bwd(
+        vp(a["q"]), vp(a["k"]), vp(a["v"]), vp(a["out"]), vp(a["lo"]), vp(a["lse"]), vp(a["dout"]), vp(a["mask"]),
+        vp(a["cu_q"]), vp(a["cu_k"]), a["B"], a["H"], a["Hk"], a["Lq"], a["Lk"], a["Tq"], a["Tk"], a["d"], a["scale"],
+        a["dtype"], vp(a["dq"]), vp(a["dk"]), vp(a["dv"]), None, vp(a["ws"]), a["bytes"], None)
+
+
 REFUSED = [  # arguments, status
     (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(B=-1), 1), (dict(H=0), 1), (dict(Hk=0), 1),
     (dict(H=3), 1), (dict(Lq=-1), 1), (dict(Lk=-1), 1), (dict(Tq=7), 1), (dict(Tk=17), 1), (dict(d=0), 1),
@@ -78,6 +90,7 @@ REFUSED = [  # arguments, status
 @pytest.mark.parametrize("over,status", REFUSED)
 def test_entry_points_refuse_on_the_host(binding, over, status):
     assert _fwd(binding, **over) == status, over
+    assert _bwd(binding, **over) == status, over
 
 
 def test_forward_refuses_its_own_arguments(binding):
@@ -90,3 +103,19 @@ def test_forward_refuses_its_own_arguments(binding):
     with pytest.raises(ValueError, match="CUDA tensor"):
         z = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
         b.df_cross_attn_fwd(z, z, z)
+
+
+def test_backward_refuses_its_own_arguments(binding):
+    b = binding
+    for name in ("out", "lse", "dout", "dq", "dk", "dv"):
+        assert _bwd(b, **{name: None}) == b.DF_ERR_INVALID_ARG, name
+    for name in ("out", "lo", "dout", "dq", "dk", "dv"):
+        assert _bwd(b, **{name: 0xb0008}) == b.DF_ERR_ALIGNMENT, name
+    assert _bwd(b, lse=0x50002) == b.DF_ERR_ALIGNMENT
+    assert _bwd(b, ws=0xa0080) == b.DF_ERR_ALIGNMENT
+    need = b.df_cross_attn_bwd_workspace_size(6, 4)
+    assert need >= 6 * 4 * 8
+    assert _bwd(b, bytes=need - 1) == b.DF_ERR_WORKSPACE
+    assert _bwd(b, ws=None) == b.DF_ERR_WORKSPACE
+    assert b.df_cross_attn_bwd_workspace_size(-1, 4) == 0
+    assert _bwd(b, Lq=0, Lk=0, Tq=0, Tk=0) == b.DF_OK  # nothing to do
