@@ -513,9 +513,21 @@ def _on_device(dev, tensors):
             raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
 
 
-def _stream_on(dev, stream) -> ctypes.c_void_p:
-    """The given stream, or the current one of the tensors' device."""
-    return _stream(torch.cuda.current_stream(dev) if stream is None else stream)
+def _call_on(dev, fn, stream, *args) -> int:
+    """fn(*args, stream) with ``dev`` current; the stream defaults to its current one.
+    (Plain integers for pointers and streams: a small call is bound by the host.)"""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _int_sizes(**sizes):
@@ -550,9 +562,8 @@ def df_embedding(ids, table, scale=1.0, out=None, status=None, stream=None):
         out = torch.empty(tuple(ids.shape) + (N,), dtype=table.dtype, device=dev)
     elif out.dtype != table.dtype or tuple(out.shape) != tuple(ids.shape) + (N,):
         raise ValueError("out must be [..., N] of the table's dtype")
-    with torch.cuda.device(dev):
-        _check(_lib.df_embedding(_ptr(ids), _ids_64(ids), ids.numel(), _ptr(table), V, N, float(scale), _ptr(out),
-                                 _DTYPE[table.dtype], _ptr(status), _stream_on(dev, stream)), "df_embedding")
+    _check(_call_on(dev, _lib.df_embedding, stream, ids.data_ptr(), _ids_64(ids), ids.numel(), table.data_ptr(), V, N,
+                    float(scale), out.data_ptr(), _DTYPE[table.dtype], _addr(status)), "df_embedding")
     return out
 
 
@@ -582,11 +593,9 @@ def df_embedding_bwd(ids, dout, vocab, scale=1.0, padding_idx=None, grad=None, a
         size = df_embedding_bwd_workspace_size(T, N, vocab)
         workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
     pad = -1 if padding_idx is None else int(padding_idx)
-    with torch.cuda.device(dev):
-        _check(_lib.df_embedding_bwd(_ptr(ids), _ids_64(ids), T, _ptr(dout), vocab, N, float(scale), pad,
-                                     1 if accumulate else 0, _ptr(grad), _DTYPE[dout.dtype], _ptr(status),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _stream_on(dev, stream)), "df_embedding_bwd")
+    _check(_call_on(dev, _lib.df_embedding_bwd, stream, ids.data_ptr(), _ids_64(ids), T, dout.data_ptr(), vocab, N,
+                    float(scale), pad, 1 if accumulate else 0, grad.data_ptr(), _DTYPE[dout.dtype], _addr(status),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size()), "df_embedding_bwd")
     return grad
 
 
@@ -609,33 +618,32 @@ def _cross_shape(q, k, v, key_mask, cu_q, cu_k, max_q, max_k):
                      ("cu_seqlens_k", cu_k)))
     if q.dtype not in _DTYPE or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must share a dtype: bf16 or fp16")
-    if q.dim() != (4 if cu_q is None else 3):
+    qs, ks = q.shape, k.shape
+    if len(qs) != (4 if cu_q is None else 3):
         raise ValueError("q must be [B, Lq, H, d], or [total_q, H, d] with cu_seqlens_q")
-    if k.dim() != (4 if cu_k is None else 3) or k.shape != v.shape or k.shape[-1] != q.shape[-1]:
+    if len(ks) != (4 if cu_k is None else 3) or ks != v.shape or ks[-1] != qs[-1]:
         raise ValueError("k and v must be [B, Lk, Hk, d], or [total_k, Hk, d] with cu_seqlens_k, with q's head size")
-    batch = set()
-    for name, cu, x, longest in (("q", cu_q, q, max_q), ("k", cu_k, k, max_k)):
-        if cu is None:
-            batch.add(x.shape[0])
-        else:
-            if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 1:
-                raise ValueError(f"cu_seqlens_{name} must be an int32 vector [B + 1]")
-            if longest is None:
-                raise ValueError(f"packed {name} needs max_seqlen_{name} (an upper bound of every length)")
-            batch.add(cu.numel() - 1)
-    if len(batch) != 1:
+    B, Lq, Tq = _cross_rows("q", cu_q, qs, max_q)
+    Bk, Lk, Tk = _cross_rows("k", cu_k, ks, max_k)
+    if B != Bk:
         raise ValueError("q and k disagree on the number of sequences")
-    B = batch.pop()
-    H, d = q.shape[-2:]
-    Lq = q.shape[1] if cu_q is None else int(max_q)
-    Lk = k.shape[1] if cu_k is None else int(max_k)
-    total_q = B * Lq if cu_q is None else q.shape[0]
-    total_k = B * Lk if cu_k is None else k.shape[0]
     if key_mask is not None and (cu_k is not None or key_mask.dtype != torch.uint8 or
                                  tuple(key_mask.shape) != (B, Lk)):
         raise ValueError("key_mask must be uint8 [B, Lk], for keys [B, Lk, Hk, d]")
-    _int_sizes(total_q=total_q, total_k=total_k, Lq=Lq, Lk=Lk)
-    return dev, B, H, k.shape[-2], Lq, Lk, total_q, total_k, d
+    if max(Tq, Tk, Lq, Lk) >= 2 ** 31 or min(Lq, Lk) < 0:
+        raise ValueError("lengths out of range")
+    return dev, B, qs[-2], ks[-2], Lq, Lk, Tq, Tk, qs[-1]
+
+
+def _cross_rows(name, cu, shape, longest):
+    """(sequences, longest length, rows) of one side."""
+    if cu is None:
+        return shape[0], shape[1], shape[0] * shape[1]
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 1:
+        raise ValueError(f"cu_seqlens_{name} must be an int32 vector [B + 1]")
+    if longest is None:
+        raise ValueError(f"packed {name} needs max_seqlen_{name} (an upper bound of every length)")
+    return cu.numel() - 1, int(longest), shape[0]
 
 
 def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *, max_seqlen_q=None,
@@ -655,12 +663,10 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
     _status_word(status)
     stats = CrossStats(torch.empty(q.shape[:-1], dtype=torch.float32, device=dev),
                        torch.empty_like(q)) if with_stats else None
-    with torch.cuda.device(dev):
-        st = _lib.df_cross_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(key_mask), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
-                                    B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], _ptr(out),
-                                    _ptr(stats.out_lo) if stats else None, _ptr(stats.lse) if stats else None,
-                                    _ptr(status), _stream_on(dev, stream))
-    _check(st, "df_cross_attn_fwd")
+    _check(_call_on(dev, _lib.df_cross_attn_fwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask),
+                    _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype],
+                    out.data_ptr(), stats.out_lo.data_ptr() if stats else None,
+                    stats.lse.data_ptr() if stats else None, _addr(status)), "df_cross_attn_fwd")
     return (out, stats) if with_stats else out
 
 
@@ -700,13 +706,11 @@ def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=Non
     _on_device(dev, (("out", out), ("out_lo", stats.out_lo), ("lse", stats.lse), ("dout", dout), ("dq", dq),
                      ("dk", dk), ("dv", dv), ("workspace", workspace), ("status", status)))
     _status_word(status)
-    with torch.cuda.device(dev):
-        st = _lib.df_cross_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(stats.out_lo), _ptr(stats.lse),
-                                    _ptr(dout), _ptr(key_mask), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, H, Hk, Lq,
-                                    Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], _ptr(dq), _ptr(dk), _ptr(dv), _ptr(status),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream_on(dev, stream))
-    _check(st, "df_cross_attn_bwd")
+    _check(_call_on(dev, _lib.df_cross_attn_bwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                    _addr(stats.out_lo), stats.lse.data_ptr(), dout.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q),
+                    _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], dq.data_ptr(),
+                    dk.data_ptr(), dv.data_ptr(), _addr(status), workspace.data_ptr(),
+                    workspace.numel() * workspace.element_size()), "df_cross_attn_bwd")
     return dq, dk, dv
 
 

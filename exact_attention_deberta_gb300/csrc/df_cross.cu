@@ -644,18 +644,9 @@ template <int D, bool BF16>
 cudaError_t launch_fwd(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t s) {
   auto kernel = cross_fwd_kernel<D, BF16>;
   const uint32_t bytes = FwdSmem<D>::alloc;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kThreads, &done);
   if (e != cudaSuccess) return e;
-  // setmaxnreg.inc waits until the launched registers cover the split (eight
-  // softmax warps at 224, four control warps at 56): refuse a build that does not
-  static int regs_ok = -1;
-  if (regs_ok < 0) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    regs_ok = fa.numRegs * kThreads >= 256 * 224 + 128 * 56 ? 1 : 0;
-  }
-  if (!regs_ok) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
@@ -686,6 +677,21 @@ bool encode_heads(CUtensorMap* m, const void* base, long long rows, int heads, i
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t prepare_kernel(const void* kernel, int bytes, int threads, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kernel);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * threads < 256 * 224 + 128 * 56) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done->fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 int device_sms() {

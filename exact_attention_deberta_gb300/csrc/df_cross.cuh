@@ -10,6 +10,8 @@
 // maps end a row at d, and a copy fills the columns behind it with zeros.
 #pragma once
 
+#include <atomic>
+
 #include "df_tc_common.cuh"
 
 namespace dfa {
@@ -152,6 +154,10 @@ struct TileWalk {
 bool encode_heads(CUtensorMap* m, const void* base, long long rows, int heads, int d, bool bf16, int box_heads,
                   int box_rows);
 int device_sms();
+// Allows `kernel` its dynamic shared memory on the current device (once per
+// device) and checks that the registers it is launched with cover the split
+// (eight warps at 224, four at 56): setmaxnreg.inc would wait for the rest.
+cudaError_t prepare_kernel(const void* kernel, int bytes, int threads, std::atomic<uint64_t>* done);
 // Argument checks and arguments shared by the forward and the backward.
 df_status cross_check(const void* q, const void* k, const void* v, const uint8_t* key_mask, const int32_t* cu_q,
                       const int32_t* cu_k, int B, int H, int Hk, int Lq, int Lk, int total_q, int total_k, int d,

@@ -559,17 +559,9 @@ cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items,
   if (items == 0) return cudaSuccess;
   auto kernel = cross_bwd_kernel<D, BF16, KEYS>;
   const uint32_t bytes = BwdSmem<D>::alloc;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kThreads, &done);
   if (e != cudaSuccess) return e;
-  // as in the forward: the launched registers must cover the setmaxnreg split
-  static int regs_ok = -1;
-  if (regs_ok < 0) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    regs_ok = fa.numRegs * kThreads >= 256 * 224 + 128 * 56 ? 1 : 0;
-  }
-  if (!regs_ok) return cudaErrorInvalidConfiguration;
   kernel<<<(int)std::min<long long>(items, device_sms()), kThreads, bytes, s>>>(a, maps);
   return cudaGetLastError();
 }

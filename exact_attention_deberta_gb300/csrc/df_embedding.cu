@@ -9,18 +9,21 @@
 // order of arrival, so the tokens are sorted by id first (a stable radix sort
 // of (id, position) pairs) and every row of the table is then the sum of one
 // run of the sorted list, in ascending position:
-//   1. sort: least-significant digit first, at most 10 bits per pass (two
-//      passes for ids below 2^20).  A pass counts the digits of each 2048-key
-//      tile, scans the counts digit-major in one block, and scatters the tiles
-//      (rank inside the tile by warp digit matching, so that equal digits keep
-//      their order).  Ids that pass no gradient (the padding id, ids outside
-//      the table) sort behind every other one and are left out.
+//   1. sort.  Up to 8192 tokens: one block, 8 bits per pass, pairs in shared
+//      memory.  More: 2048-key tiles, at most 10 bits per pass (two passes for
+//      ids below 2^20); a pass counts the digits of each tile, scans each
+//      digit's counts over the tiles, and scatters (rank inside the tile by warp
+//      digit matching, so that equal digits keep their order).  Ids that pass no
+//      gradient (the padding id, ids outside the table) sort behind every other
+//      one and are left out.  The sort is latency bound and leaves HBM idle, so
+//      the same launches also zero the table in further blocks (rows that tokens
+//      reach are written again in step 2).
 //   2. sums: a warp takes 32 consecutive entries of the sorted list and 256
 //      columns (8 per lane), adds rows in fp32 while the id stays the same and
 //      writes each finished run.  A run that crosses a 32-entry boundary leaves
 //      one partial row per chunk in the workspace.
 //   3. join: the warp of the chunk in which such a run begins adds its partial
-//      rows in order.
+//      rows in order; long runs are shared by the eight warps of the block.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -52,6 +55,21 @@ __device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
   }
 }
 
+// Eight values as loaded, converted where they are added.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = __ldg(reinterpret_cast<const uint4*>(p) + e);
+  }
+  __device__ __forceinline__ void add_to(float (&acc)[8]) const {
+    const T* h = reinterpret_cast<const T*>(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += IO<T>::to_f(h[e]);
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 2) {
@@ -66,28 +84,49 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   }
 }
 
+template <typename T>
+__device__ __forceinline__ void store8_past_l2(T* p, const float (&f)[8]) {
+  uint4 v[sizeof(T) / 2];
+  store8<T>(reinterpret_cast<T*>(v), f);
+#pragma unroll
+  for (int e = 0; e < (int)sizeof(T) / 2; ++e) __stcs(reinterpret_cast<uint4*>(p) + e, v[e]);
+}
+
 __device__ __forceinline__ long long load_id(const void* ids, int ids64, size_t t) {
   return ids64 ? (long long)static_cast<const int64_t*>(ids)[t] : (long long)static_cast<const int32_t*>(ids)[t];
 }
 
-template <typename T>
+// A warp takes R consecutive tokens, R rows of loads in flight per 256 columns.
+// The output is written past L2 (evict first), which is left to the table's rows.
+template <typename T, int R>
 __global__ void __launch_bounds__(256) lookup_kernel(const void* __restrict__ ids, int ids64, int tokens,
                                                      const T* __restrict__ table, int V, int N, float scale,
                                                      T* __restrict__ out, int32_t* status) {
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= tokens) return;
-  const long long id = load_id(ids, ids64, t);
-  const bool in = id >= 0 && id < V;
-  if (!in && lane == 0 && status) atomicCAS(status, 0, (int32_t)DF_ERR_INVALID_ARG);
-  const T* src = table + (size_t)(in ? id : 0) * N;
-  T* dst = out + (size_t)t * N;
-  for (int c = lane * 8; c < N; c += 256) {
-    float f[8];
-    if (in) load8<T>(src + c, f);
+  const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * R;
+  if (t0 >= tokens) return;
+  const T* src[R];
+  bool in[R];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = in ? f[e] * scale : 0.f;
-    store8<T>(dst + c, f);
+  for (int r = 0; r < R; ++r) {
+    const long long id = t0 + r < tokens ? load_id(ids, ids64, t0 + r) : 0;
+    in[r] = id >= 0 && id < V;
+    if (!in[r] && lane == 0 && status) atomicCAS(status, 0, (int32_t)DF_ERR_INVALID_ARG);
+    src[r] = table + (size_t)(in[r] ? id : 0) * N;
+  }
+  T* dst = out + (size_t)t0 * N;
+  for (int c = lane * 8; c < N; c += 256) {
+    Raw8<T> raw[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r].load(src[r] + c);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      raw[r].add_to(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = in[r] ? f[e] * scale : 0.f;
+      if (t0 + r < tokens) store8_past_l2<T>(dst + (size_t)r * N + c, f);
+    }
   }
 }
 
@@ -100,10 +139,22 @@ struct SortArgs {
   const uint32_t* pos;
   uint32_t* key_out;
   uint32_t* pos_out;
-  uint32_t* hist;       // [digits][tiles]
+  uint32_t* hist;       // [tiles][digits]
+  uint32_t* total;      // [digits]
   int n, tiles, V, pad, first, shift, bits;
   int32_t* status;
+  // blocks from `blocks` on zero 16-byte pieces [fill_begin, fill_end) of the table
+  int blocks;
+  uint4* fill;
+  size_t fill_begin, fill_end;
 };
+
+// A block without sorting work: its share of the zeros.
+__device__ __forceinline__ void fill_share(const SortArgs& a) {
+  const size_t step = (size_t)(gridDim.x - a.blocks) * blockDim.x;
+  for (size_t i = a.fill_begin + (size_t)(blockIdx.x - a.blocks) * blockDim.x + threadIdx.x; i < a.fill_end; i += step)
+    a.fill[i] = make_uint4(0u, 0u, 0u, 0u);
+}
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int i) {
   if (!a.first) return a.key[i];
@@ -113,117 +164,216 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int i) {
   return in && id != a.pad ? (uint32_t)id : (uint32_t)a.V;
 }
 
+// Exclusive prefix of one value per thread over a block of at most 1024 threads.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t own, uint32_t* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  __syncthreads();
+  return before + incl - own;
+}
+
+// Rank of each lane's digit among equal ones of the warp's keys so far (rounds of
+// 32 keys in lane order); `cnt` holds the warp's counts.
+__device__ __forceinline__ uint32_t digit_rank(uint32_t d, bool valid, uint32_t* cnt, int lane) {
+  const uint32_t same = __match_any_sync(0xffffffffu, valid ? d : 0xffffffffu);
+  const uint32_t before = __popc(same & ((1u << lane) - 1u));
+  uint32_t start = 0;
+  if (valid && before == 0) {
+    start = cnt[d];
+    cnt[d] = start + __popc(same);
+  }
+  start = __shfl_sync(0xffffffffu, start, __ffs(same) - 1);
+  __syncwarp();
+  return start + before;
+}
+
 __global__ void __launch_bounds__(kSortThreads) digit_counts(const SortArgs a) {
+  if ((int)blockIdx.x >= a.blocks) return fill_share(a);
   __shared__ uint32_t cnt[1 << kMaxDigitBits];
   const int digits = 1 << a.bits;
-  for (int d = threadIdx.x; d < digits; d += kSortThreads) cnt[d] = 0;
-  __syncthreads();
+  uint32_t key[kSortItems];
   const int base = blockIdx.x * kSortTile;
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const int i = base + k * kSortThreads + threadIdx.x;
-    if (i < a.n) atomicAdd(&cnt[(sort_key(a, i) >> a.shift) & (digits - 1)], 1u);
+    key[k] = i < a.n ? sort_key(a, i) : 0u;
   }
+  for (int d = threadIdx.x; d < digits; d += kSortThreads) cnt[d] = 0;
   __syncthreads();
-  for (int d = threadIdx.x; d < digits; d += kSortThreads) a.hist[(size_t)d * a.tiles + blockIdx.x] = cnt[d];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k)
+    if (base + k * kSortThreads + (int)threadIdx.x < a.n) atomicAdd(&cnt[(key[k] >> a.shift) & (digits - 1)], 1u);
+  __syncthreads();
+  for (int d = threadIdx.x; d < digits; d += kSortThreads) a.hist[(size_t)blockIdx.x * digits + d] = cnt[d];
 }
 
-// Exclusive prefix over m counts, one block of 1024 threads; each thread owns a
-// contiguous range.
-__global__ void __launch_bounds__(1024) scan_digit_counts(uint32_t* __restrict__ h, int m) {
-  __shared__ uint32_t warp_sum[32];
+// Each digit's counts become exclusive prefixes over the tiles: block d / 32 takes
+// 32 digits (lane = digit, so rows of hist are read whole), its eight warps eight
+// ranges of tiles.
+__global__ void __launch_bounds__(256) scan_over_tiles(const SortArgs a) {
+  if ((int)blockIdx.x >= a.blocks) return fill_share(a);
+  __shared__ uint32_t sums[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t carry = 0;
-  for (int base = 0; base < m; base += 4096) {
-    const int i = base + threadIdx.x * 4;
-    uint32_t v[4];
+  const int digits = 1 << a.bits, d = blockIdx.x * 32 + lane;
+  const int per = (a.tiles + 7) / 8, t0 = min(a.tiles, warp * per), t1 = min(a.tiles, t0 + per);
+  const bool in = d < digits;
+  uint32_t s = 0;
+#pragma unroll 8
+  for (int t = t0; t < t1; ++t) s += in ? a.hist[(size_t)t * digits + d] : 0u;
+  sums[warp][lane] = s;
+  __syncthreads();
+  uint32_t run = 0, all = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = i + e < m ? h[i + e] : 0u;
-    const uint32_t own = v[0] + v[1] + v[2] + v[3];
-    uint32_t incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t w = warp_sum[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += u;
-      }
-      warp_sum[lane] = w;
-    }
-    __syncthreads();
-    uint32_t run = carry + (warp ? warp_sum[warp - 1] : 0u) + incl - own;
-    carry += warp_sum[31];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < m) {
-        h[i + e] = run;
-        run += v[e];
-      }
-    __syncthreads();  // warp_sum is written again
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) run += sums[w][lane];
+    all += sums[w][lane];
+  }
+  if (!in) return;
+  if (warp == 0) a.total[d] = all;
+#pragma unroll 8
+  for (int t = t0; t < t1; ++t) {
+    const uint32_t c = a.hist[(size_t)t * digits + d];
+    a.hist[(size_t)t * digits + d] = run;
+    run += c;
   }
 }
 
 // Writes a tile's pairs to their places.  Warp w of the tile owns keys
 // [w 256, w 256 + 256) in rounds of 32, so that (warp, round, lane) is the
-// original order; equal digits of a round are ranked by lane.
+// original order.
 __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs a) {
-  constexpr int kWarps = kSortThreads / 32;
+  if ((int)blockIdx.x >= a.blocks) return fill_share(a);
+  constexpr int kWarps = kSortThreads / 32, kPer = (1 << kMaxDigitBits) / kSortThreads;
   __shared__ uint32_t cnt[kWarps][1 << kMaxDigitBits];
+  __shared__ uint32_t warp_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int digits = 1 << a.bits;
-  for (int d = threadIdx.x; d < digits; d += kSortThreads)
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) cnt[w][d] = 0;
-  __syncthreads();
   const int base = blockIdx.x * kSortTile + warp * (kSortItems * 32);
-  uint32_t key[kSortItems], rank[kSortItems];
+  uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const int i = base + k * 32 + lane;
     key[k] = i < a.n ? sort_key(a, i) : 0u;
+    pos[k] = a.first ? (uint32_t)i : (i < a.n ? a.pos[i] : 0u);
   }
+  // thread t's digits: t kPer .. t kPer + kPer - 1
+  uint32_t tot[kPer], own = 0;
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int i = base + k * 32 + lane;
-    const bool valid = i < a.n;
-    const uint32_t d = (key[k] >> a.shift) & (digits - 1);
-    const uint32_t same = __match_any_sync(0xffffffffu, valid ? d : 0xffffffffu);
-    const uint32_t before = __popc(same & ((1u << lane) - 1u));
-    uint32_t start = 0;
-    if (valid && before == 0) {
-      start = cnt[warp][d];
-      cnt[warp][d] = start + __popc(same);
-    }
-    rank[k] = before + __shfl_sync(0xffffffffu, start, __ffs(same) - 1);
-    __syncwarp();
+  for (int e = 0; e < kPer; ++e) {
+    const int d = threadIdx.x * kPer + e;
+    tot[e] = d < digits ? a.total[d] : 0u;
+    own += tot[e];
   }
-  __syncthreads();
-  // the tile's place for each digit, then each warp's
-  for (int d = threadIdx.x; d < digits; d += kSortThreads) {
-    uint32_t at = a.hist[(size_t)d * a.tiles + blockIdx.x];
+  for (int d = threadIdx.x; d < digits; d += kSortThreads)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c = cnt[w][d];
-      cnt[w][d] = at;
-      at += c;
-    }
-  }
+    for (int w = 0; w < kWarps; ++w) cnt[w][d] = 0;
+  uint32_t at_digit = block_exclusive(own, warp_sum);  // (also: the counts are cleared)
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k)
+    rank[k] = digit_rank((key[k] >> a.shift) & (digits - 1), base + k * 32 + lane < a.n, cnt[warp], lane);
   __syncthreads();
 #pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int d = threadIdx.x * kPer + e;
+    if (d < digits) {
+      uint32_t at = at_digit + a.hist[(size_t)blockIdx.x * digits + d];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t c = cnt[w][d];
+        cnt[w][d] = at;
+        at += c;
+      }
+    }
+    at_digit += tot[e];
+  }
+  __syncthreads();
+#pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
-    const int i = base + k * 32 + lane;
-    if (i >= a.n) continue;
-    const uint32_t d = (key[k] >> a.shift) & (digits - 1);
-    const uint32_t to = cnt[warp][d] + rank[k];
+    if (base + k * 32 + lane >= a.n) continue;
+    const uint32_t to = cnt[warp][(key[k] >> a.shift) & (digits - 1)] + rank[k];
     a.key_out[to] = key[k];
-    a.pos_out[to] = a.first ? (uint32_t)i : a.pos[i];
+    a.pos_out[to] = pos[k];
+  }
+}
+
+// The whole sort of at most kSmallSort tokens in block 0.
+constexpr int kSmallSort = 8192, kSmallBits = 8, kSmallThreads = 1024;
+constexpr size_t kSmallSmem = (size_t)kSmallSort * 8 + 32 * (1 << kSmallBits) * 4 + 128;
+
+__global__ void __launch_bounds__(kSmallThreads) sort_small(const SortArgs a, int passes) {
+  if ((int)blockIdx.x >= a.blocks) return fill_share(a);
+  extern __shared__ uint32_t sh[];
+  uint32_t* s_key = sh;
+  uint32_t* s_pos = sh + kSmallSort;
+  uint32_t* cnt = s_pos + kSmallSort;  // [32 warps][256]
+  uint32_t* warp_sum = cnt + 32 * (1 << kSmallBits);
+  constexpr int kDigits = 1 << kSmallBits;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // rounds that hold keys: as few as the tokens need, the same for every warp
+  const int rounds = (a.n + kSmallThreads - 1) / kSmallThreads;
+  const int base = warp * rounds * 32;
+  uint32_t key[8], pos[8], rank[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = base + k * 32 + lane;
+    const bool in = k < rounds && i < a.n;
+    key[k] = in ? sort_key(a, i) : 0u;
+    pos[k] = (uint32_t)i;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * kSmallBits;
+    for (int d = threadIdx.x; d < 32 * kDigits; d += kSmallThreads) cnt[d] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < rounds)
+        rank[k] = digit_rank((key[k] >> shift) & (kDigits - 1), base + k * 32 + lane < a.n, cnt + warp * kDigits, lane);
+    __syncthreads();
+    uint32_t all = 0;
+    if (threadIdx.x < kDigits)
+      for (int w = 0; w < 32; ++w) {
+        const uint32_t c = cnt[w * kDigits + threadIdx.x];
+        cnt[w * kDigits + threadIdx.x] = all;
+        all += c;
+      }
+    const uint32_t start = block_exclusive(all, warp_sum);
+    if (threadIdx.x < kDigits)
+      for (int w = 0; w < 32; ++w) cnt[w * kDigits + threadIdx.x] += start;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < rounds && base + k * 32 + lane < a.n) {
+        const uint32_t to = cnt[warp * kDigits + ((key[k] >> shift) & (kDigits - 1))] + rank[k];
+        s_key[to] = key[k];
+        s_pos[to] = pos[k];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = base + k * 32 + lane;
+      if (k < rounds && i < a.n) {
+        key[k] = s_key[i];
+        pos[k] = s_pos[i];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = base + k * 32 + lane;
+    if (k < rounds && i < a.n) {
+      a.key_out[i] = key[k];
+      a.pos_out[i] = pos[k];
+    }
   }
 }
 
@@ -267,11 +417,11 @@ __global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __rest
   uint32_t cur = __shfl_sync(0xffffffffu, my_key, 0);
   bool head = before == cur;  // the current run began in an earlier chunk
   for (int k0 = 0; k0 < live; k0 += 8) {
-    float f[8][8];
+    Raw8<T> f[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const uint32_t p = __shfl_sync(0xffffffffu, my_pos, k0 + u);
-      if (col && k0 + u < live) load8<T>(dout + (size_t)p * a.N + c, f[u]);
+      if (col && k0 + u < live) f[u].load(dout + (size_t)p * a.N + c);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -287,10 +437,7 @@ __global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __rest
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
       }
-      if (col) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
-      }
+      if (col) f[u].add_to(acc);
     }
   }
   if (col) {
@@ -301,33 +448,102 @@ __global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __rest
   }
 }
 
-__global__ void __launch_bounds__(256) join_runs(const SumArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int chunk = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (chunk + 1 >= a.chunks) return;
-  const int i0 = chunk * kChunk;
-  const uint32_t v = a.key[i0 + kChunk - 1];
-  // only where a run begins in this chunk and goes on behind it
-  if (v >= (uint32_t)a.V || a.key[i0 + kChunk] != v) return;
-  if (a.key[i0] == v && chunk > 0 && a.key[i0 - 1] == v) return;
-  const int c = blockIdx.y * kSlice + lane * 8;
-  if (c >= a.N) return;
-  float acc[8], f[8];
-  load8<float>(a.part + ((size_t)chunk * 2 + 1) * a.N + c, acc);
-  for (int k = chunk + 1; k < a.chunks && a.key[(size_t)k * kChunk] == v; ++k) {
-    load8<float>(a.part + (size_t)k * 2 * a.N + c, f);
+// Runs longer than this many chunks are added by the block's eight warps together.
+constexpr int kLongRun = 16;
+
+// Sum of the partial rows of chunks [k0, k1), eight loads in flight.
+__device__ __forceinline__ void add_partials(const SumArgs& a, int k0, int k1, int c, float (&acc)[8]) {
+  for (int k = k0; k < k1; k += 8) {
+    Raw8<float> f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    for (int u = 0; u < 8; ++u)
+      if (k + u < k1) f[u].load(a.part + (size_t)(k + u) * 2 * a.N + c);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (k + u < k1) f[u].add_to(acc);
   }
-  write_row(a, v, c, acc);
+}
+
+__global__ void __launch_bounds__(256) join_runs(const SumArgs a) {
+  __shared__ int s_end[8];
+  __shared__ float s_part[8][kSlice];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = blockIdx.x * 8 + warp;
+  const int c = blockIdx.y * kSlice + lane * 8;
+  const bool col = c < a.N;
+  // only where a run begins in this chunk and goes on behind it
+  uint32_t v = 0;
+  bool begins = false;
+  if (chunk + 1 < a.chunks) {
+    const int i0 = chunk * kChunk;
+    v = a.key[i0 + kChunk - 1];
+    begins = v < (uint32_t)a.V && a.key[i0 + kChunk] == v &&
+             !(a.key[i0] == v && chunk > 0 && a.key[i0 - 1] == v);
+  }
+  int end = 0;  // the first chunk whose first entry lies behind the run
+  if (begins) {
+    end = chunk + 2;
+    while (end < a.chunks && end <= chunk + kLongRun && a.key[(size_t)end * kChunk] == v) ++end;
+    if (end < a.chunks && a.key[(size_t)end * kChunk] == v) {
+      int lo = end, hi = a.chunks;  // a.key[lo kChunk] == v, behind hi it is not
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.key[(size_t)mid * kChunk] == v) lo = mid;
+        else hi = mid;
+      }
+      end = hi;
+    }
+  }
+  const bool is_long = begins && end - chunk > kLongRun;
+  if (lane == 0) s_end[warp] = is_long ? end : 0;
+  float acc[8];
+  if (begins && !is_long && col) {
+    load8<float>(a.part + ((size_t)chunk * 2 + 1) * a.N + c, acc);
+    add_partials(a, chunk + 1, end, c, acc);
+    write_row(a, v, c, acc);
+  }
+  __syncthreads();
+  for (int w = 0; w < 8; ++w) {
+    const int e = s_end[w], first = blockIdx.x * 8 + w;
+    if (e == 0) continue;  // the same for the whole block
+    const int per = (e - first - 1 + 7) / 8, k0 = min(e, first + 1 + warp * per), k1 = min(e, k0 + per);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) acc[x] = 0.f;
+    if (col) {
+      add_partials(a, k0, k1, c, acc);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s_part[warp][lane * 8 + x] = acc[x];
+    }
+    __syncthreads();
+    if (warp == w && col) {
+      load8<float>(a.part + ((size_t)first * 2 + 1) * a.N + c, acc);
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] += s_part[u][lane * 8 + x];
+      write_row(a, v, c, acc);
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------ host side
+int sm_count() {
+  static int sms = 0;
+  if (!sms) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (sms <= 0) sms = 1;
+  }
+  return sms;
+}
+
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct GradLayout {
-  size_t key[2], pos[2], hist, part, total;
+  size_t key[2], pos[2], hist, digit_total, part, total;
   int tiles, chunks, bits, passes;
+  bool small;
 };
 
 GradLayout grad_layout(int T, int N, int V) {
@@ -336,7 +552,9 @@ GradLayout grad_layout(int T, int N, int V) {
   l.chunks = (T + kChunk - 1) / kChunk;
   int key_bits = 1;  // keys 0 .. V
   while (key_bits < 32 && ((unsigned long long)V >> key_bits) != 0) ++key_bits;
-  l.passes = (key_bits + kMaxDigitBits - 1) / kMaxDigitBits;
+  l.small = T <= kSmallSort;
+  const int most = l.small ? kSmallBits : kMaxDigitBits;
+  l.passes = (key_bits + most - 1) / most;
   l.bits = (key_bits + l.passes - 1) / l.passes;
   size_t at = 0;
   for (int b = 0; b < 2; ++b) {
@@ -347,6 +565,8 @@ GradLayout grad_layout(int T, int N, int V) {
   }
   l.hist = at;
   at += up256(((size_t)l.tiles << l.bits) * 4);
+  l.digit_total = at;
+  at += up256((size_t)4 << kMaxDigitBits);
   l.part = at;
   at += up256((size_t)l.chunks * 2 * N * 4);
   l.total = at;
@@ -364,8 +584,13 @@ df_status check_sizes(int T, int N, int V) {
 template <typename T>
 void launch_lookup(const void* ids, int ids64, int n, const void* table, int V, int N, float scale, void* out,
                    int32_t* status, cudaStream_t s) {
-  lookup_kernel<T><<<(n + 7) / 8, 256, 0, s>>>(ids, ids64, n, static_cast<const T*>(table), V, N, scale,
-                                               static_cast<T*>(out), status);
+  // four rows per warp once that still leaves every SM its resident warps
+  if (n >= 4 * 64 * sm_count())
+    lookup_kernel<T, 4><<<(n + 31) / 32, 256, 0, s>>>(ids, ids64, n, static_cast<const T*>(table), V, N, scale,
+                                                      static_cast<T*>(out), status);
+  else
+    lookup_kernel<T, 1><<<(n + 7) / 8, 256, 0, s>>>(ids, ids64, n, static_cast<const T*>(table), V, N, scale,
+                                                    static_cast<T*>(out), status);
 }
 
 template <typename T>
@@ -411,32 +636,61 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
   const GradLayout l = grad_layout(T, N, V);
   if (!workspace || workspace_bytes < std::max<size_t>(l.total, 256)) return DF_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
-  if (!accumulate && cudaMemsetAsync(grad, 0, (size_t)V * N * 4, s) != cudaSuccess) return DF_ERR_CUDA;
-  if (T == 0) return DF_OK;
+  if (T == 0) {
+    if (!accumulate && cudaMemsetAsync(grad, 0, (size_t)V * N * 4, s) != cudaSuccess) return DF_ERR_CUDA;
+    return DF_OK;
+  }
   char* base = static_cast<char*>(workspace);
   SortArgs a;
   a.ids = ids;
   a.ids64 = ids_64;
   a.hist = reinterpret_cast<uint32_t*>(base + l.hist);
+  a.total = reinterpret_cast<uint32_t*>(base + l.digit_total);
   a.n = T;
   a.tiles = l.tiles;
   a.V = V;
   a.pad = padding_idx;
   a.bits = l.bits;
   a.status = status;
-  for (int p = 0; p < l.passes; ++p) {
-    a.first = p == 0;
-    a.shift = p * l.bits;
-    a.key = reinterpret_cast<const uint32_t*>(base + l.key[(p + 1) & 1]);
-    a.pos = reinterpret_cast<const uint32_t*>(base + l.pos[(p + 1) & 1]);
-    a.key_out = reinterpret_cast<uint32_t*>(base + l.key[p & 1]);
-    a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[p & 1]);
-    digit_counts<<<l.tiles, kSortThreads, 0, s>>>(a);
-    scan_digit_counts<<<1, 1024, 0, s>>>(a.hist, l.tiles << l.bits);
-    scatter_by_digit<<<l.tiles, kSortThreads, 0, s>>>(a);
+  a.fill = reinterpret_cast<uint4*>(grad);
+  const size_t pieces = accumulate ? 0 : (size_t)V * N / 4;
+  const int launches = l.small ? 1 : 3 * l.passes;
+  int done = 0;
+  // the next launch: its sorting blocks, and blocks that zero its share of the table
+  auto grid_for = [&](int blocks, int threads) {
+    a.blocks = blocks;
+    a.fill_begin = pieces / launches * done;
+    a.fill_end = ++done == launches ? pieces : pieces / launches * done;
+    const size_t most = (size_t)sm_count() * (2048 / threads);
+    return (unsigned)(blocks + std::min(most, (a.fill_end - a.fill_begin + threads - 1) / threads));
+  };
+  if (l.small) {
+    if (cudaFuncSetAttribute(sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem) != cudaSuccess)
+      return DF_ERR_CUDA;
+    a.first = 1;
+    a.shift = 0;
+    a.key_out = reinterpret_cast<uint32_t*>(base + l.key[0]);
+    a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[0]);
+    const unsigned grid = grid_for(1, kSmallThreads);
+    sort_small<<<grid, kSmallThreads, kSmallSmem, s>>>(a, l.passes);
+  } else {
+    for (int p = 0; p < l.passes; ++p) {
+      a.first = p == 0;
+      a.shift = p * l.bits;
+      a.key = reinterpret_cast<const uint32_t*>(base + l.key[(p + 1) & 1]);
+      a.pos = reinterpret_cast<const uint32_t*>(base + l.pos[(p + 1) & 1]);
+      a.key_out = reinterpret_cast<uint32_t*>(base + l.key[p & 1]);
+      a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[p & 1]);
+      unsigned grid = grid_for(l.tiles, kSortThreads);
+      digit_counts<<<grid, kSortThreads, 0, s>>>(a);
+      grid = grid_for(((1 << l.bits) + 31) / 32, 256);
+      scan_over_tiles<<<grid, 256, 0, s>>>(a);
+      grid = grid_for(l.tiles, kSortThreads);
+      scatter_by_digit<<<grid, kSortThreads, 0, s>>>(a);
+    }
   }
   SumArgs u;
-  u.key = a.key_out;
+  u.key = a.key_out;  // of the last pass
   u.pos = a.pos_out;
   u.n = T;
   u.V = V;
