@@ -95,6 +95,55 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int c0,
       : "memory");
 }
 
+// Which of the 32 W keys of a tile count, one bit each (warp-collective): the
+// first `left` ones, and of those the ones that the mask (at the tile's first key,
+// or NULL) holds valid.  True if all do.
+template <int W>
+__device__ __forceinline__ bool key_bits(const uint8_t* mask, int left, uint32_t (&bits)[W]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t all = 0xffffffffu;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int j = 32 * w + lane;
+    bits[w] = __ballot_sync(0xffffffffu, j < left && (!mask || mask[j] != 0));
+    all &= bits[w];
+  }
+  return all == 0xffffffffu;
+}
+
+// Zeroes the rows of a tile of 32 W rows whose bit is 0 (one warp): a row is 128
+// bytes of each 64-column box, however swizzled.
+template <int W, int CHUNKS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, const uint32_t (&bits)[W]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if ((bits[w] >> lane) & 1u) continue;
+#pragma unroll 1
+    for (int ch = 0; ch < CHUNKS; ++ch)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<uint4*>(tile + (ch * 32 * W + 32 * w + lane) * 128 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  ptx::fence_proxy_async_smem();
+}
+
+// Keys of a masked row up to its last valid one (warp-collective).
+__device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
+  const int lane = threadIdx.x & 31;
+  for (int end = n; end > 0; end -= 512) {
+    int last = -1;  // 16 loads in flight per lane
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int j = end - 1 - lane - 32 * i;
+      if (j >= 0 && mask[j] != 0) last = max(last, j);
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (last >= 0) return last + 1;
+  }
+  return 0;
+}
+
 // Finds the tiles of one side by number, warp-collectively.  Tiles of `step`
 // tokens are numbered by sequence, then key head, then position; in packed mode
 // the rows behind the last sequence count as one more sequence, whose other
@@ -155,9 +204,9 @@ bool encode_heads(CUtensorMap* m, const void* base, long long rows, int heads, i
                   int box_rows);
 int device_sms();
 // Allows `kernel` its dynamic shared memory on the current device (once per
-// device) and checks that the registers it is launched with cover the split
-// (eight warps at 224, four at 56): setmaxnreg.inc would wait for the rest.
-cudaError_t prepare_kernel(const void* kernel, int bytes, int threads, std::atomic<uint64_t>* done);
+// device) and checks that it is launched with at least `regs` registers a thread,
+// those that its setmaxnreg split counts on (the .inc would wait for the rest).
+cudaError_t prepare_kernel(const void* kernel, int bytes, int regs, std::atomic<uint64_t>* done);
 // Argument checks and arguments shared by the forward and the backward.
 df_status cross_check(const void* q, const void* k, const void* v, const uint8_t* key_mask, const int32_t* cu_q,
                       const int32_t* cu_k, int B, int H, int Hk, int Lq, int Lk, int total_q, int total_k, int d,

@@ -1,0 +1,530 @@
+// Cross attention, forward, head sizes to 64 (df_cross128.cu: to 128): queries
+// [B, Lq] or packed, keys and values of another length [B, Lk] or packed, query
+// heads that share key heads, on tcgen05 (bf16 / fp16 I/O, fp32 accumulation and
+// softmax).
+//
+//   s_ij = scale q_i.k_j,  o_i = sum_j exp(s_ij - lse_i) v_j,
+//   lse_i = log sum_j exp s_ij          over the valid keys j of i's sequence;
+// a row without a valid key gets zeros and lse = -inf.
+//
+// One CTA per SM takes query tiles (128 rows, df_cross.cuh) in turn.  The key
+// tiles (128 keys) of an item alternate between two softmax warpgroups with
+// independent (max, sum, O), so that the tensor core works for one while the other
+// exponentiates; the two are merged at the end of the item.  Three score buffers
+// in tensor memory let S run ahead of the softmax.
+//   warp 0      finds the items and loads Q (two buffers), K and V (a ring each, a
+//               stage freed by the product that read it) by TMA;
+//   warp 1      issues S = Q.K^T;
+//   warps 3, 2  issue O_w += P.V for warpgroup 0 and 1, and zero the rows of V whose
+//               keys do not count first;
+//   warps 4-11  softmax: one thread per row, P (rounded to the I/O type) written
+//               over its S.
+// Keys that do not count (a tail tile's rows behind the sequence, key_mask) get
+// weight 0 by selection, not by arithmetic, and their rows of V are zeroed in
+// shared memory before P.V, so that whatever they hold (NaN, infinities, the
+// next sequence) stays out.  Warps without a valid row skip the softmax.
+//
+// Few query tiles, long keys: a cluster of CTAs shares one item, each with a
+// part of the key tiles; the partial (max, sum, O) are joined through
+// distributed shared memory, so no workspace and no second launch is needed.
+#include "df_cross_fwd.cuh"
+
+namespace dfa {
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 384;
+constexpr int kRegs = 168;  // launched; after the split eight softmax warps have 224, four others 56
+static_assert(256 * 224 + 128 * 56 <= kThreads * kRegs, "setmaxnreg.inc must not wait");
+constexpr uint32_t kItemRing = 4;
+
+struct FwdSmem {
+  static constexpr int D = 64;
+  static constexpr int kStages = 4;                                 // K tiles, and V tiles, in flight
+  static constexpr uint32_t kTileBytes = kBoxBytes;
+  static constexpr uint32_t q = 0;                                  // [2][Q tile]
+  static constexpr uint32_t k = q + 2 * kTileBytes;                 // [kStages][K tile]
+  static constexpr uint32_t v = k + kStages * kTileBytes;           // [kStages][V tile]
+  static constexpr uint32_t ml = v + kStages * kTileBytes;          // float4 [2 warpgroups, a cluster's][128]
+  static constexpr uint32_t bars = ml + 3 * 128 * 16;
+  // q_full, q_empty [2]; k_full, k_empty, v_full, v_empty [kStages]; s_full,
+  // buf_free, drain [3]; p_full [4]; item_full, item_empty
+  static constexpr int kBars = 4 + 4 * kStages + 9 + 4 + 2 * (int)kItemRing;
+  static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
+  static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax warpgroups' current item
+  static constexpr uint32_t misc = cur + 32;                        // abort flag, tmem slot
+  static constexpr uint32_t bytes = misc + 16;
+  static constexpr uint32_t alloc = bytes + 1024;
+  static_assert(alloc <= 232448, "shared memory of one CTA");
+  // the join of a cluster: O [128][D] fp32 over the (then idle) K tiles
+  static_assert(128 * D * 4 <= kStages * kTileBytes, "O fits over K");
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args, const __grid_constant__ FwdMaps maps) {
+  using SL = FwdSmem;
+  constexpr int D = SL::D;
+  constexpr uint32_t R = SL::kStages;
+  constexpr uint32_t kIdescQK = idesc_f16(128, 128, BF16 ? 1 : 0, 0, 0);
+  constexpr uint32_t kIdescPV = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  // tensor-memory columns: three score buffers (tile G of the CTA uses G % 3), two O
+  static_assert(tmem_region_fits(384, 2u * D, 512), "scores and two O accumulators in 512 columns");
+  constexpr uint32_t kItemReaders = 4;  // three issuing warps, the softmax warpgroups' reader
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = sm + SL::q;
+  float4* sML = reinterpret_cast<float4*>(sm + SL::ml);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SL::bars);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 2;
+  uint64_t* k_full = bars + 4;
+  uint64_t* k_empty = k_full + R;
+  uint64_t* v_full = k_empty + R;
+  uint64_t* v_empty = v_full + R;
+  uint64_t* s_full = v_empty + R;      // [3] S of the buffer computed
+  uint64_t* buf_free = s_full + 3;     // [3] the P.V that read the buffer is done
+  uint64_t* drain = buf_free + 3;      // [3], one per issuing warp
+  // [wg][k & 1]: the four warps of wg stored P of its k-th tile.  Two per
+  // warpgroup because a warp may finish its next tile before a sibling has stored
+  // the current one; it is never two ahead, since its next S waits for a P.V
+  // issued behind this phase.
+  uint64_t* p_full = drain + 3;
+  uint64_t* item_full = p_full + 4;
+  uint64_t* item_empty = item_full + kItemRing;
+  auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
+  CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SL::misc);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + SL::misc + 4);
+
+  const CrossArgs& a = args.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(q_full + b, 1);
+      mbar_init(q_empty + b, 1);
+    }
+    for (uint32_t s = 0; s < 4 * R; ++s) mbar_init(k_full + s, 1);
+    for (int b = 0; b < 3; ++b) {
+      mbar_init(s_full + b, 1);
+      mbar_init(buf_free + b, 1);
+      mbar_init(drain + b, 1);
+    }
+    for (int b = 0; b < 4; ++b) mbar_init(p_full + b, 4);
+    for (uint32_t b = 0; b < kItemRing; ++b) {
+      mbar_init(item_full + b, 1);
+      mbar_init(item_empty + b, kItemReaders);
+    }
+    *s_abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  auto tS = [&](int b) { return tmem + 128u * b; };
+  auto tO = [&](int b) { return tmem + 384u + (uint32_t)D * b; };
+
+  const unsigned long long budget = a.budget;
+  int32_t* status = a.status;
+  const uint32_t rank = args.splits > 1 ? cluster_rank() : 0u;
+  auto part = [&](const CrossItem& it, int* t0) { return key_part(args, it, rank, t0); };
+  // the c-th item handed out, for one thread; hk = -1 at the end or after an abort
+  auto read_item = [&](uint32_t c) {
+    const uint32_t slot = c % kItemRing;
+    CrossItem it;
+    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    it.hk = -1;
+    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort, status)) {
+      it = *ring_slot(c);
+      mbar_arrive(item_empty + slot);
+    }
+    return it;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ items and loads
+    setmaxnreg_dec<56>();
+    TileWalk walk;
+    uint32_t g = 0, qc = 0, k_issued = 0, v_issued = 0;
+    int mask_b = -1, mask_n = 0;  // the last masked row measured
+    bool failed = false;          // a wait ran out: nothing is loaded after it
+    const int clusters = gridDim.x / args.splits, first = blockIdx.x / args.splits;
+    for (uint32_t c = 0;; ++c) {
+      CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, (long long)first + (long long)c * clusters);
+      const uint32_t slot = c % kItemRing;
+      bool ok = true;
+      if (a.key_mask && it.hk >= 0) {  // key tiles behind the last valid key are not visited
+        if (it.b != mask_b) mask_n = masked_length(a.key_mask + (size_t)it.b * a.Lk, it.no);
+        mask_b = it.b;
+        it.no = mask_n;
+      }
+      if (lane == 0) {
+        if (c >= kItemRing) ok = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+        if (*s_abort || !ok) it.hk = -1;
+        if (ok) {
+          *ring_slot(c) = it;
+          mbar_arrive(item_full + slot);
+        }
+        int t0;
+        const int nt = it.hk < 0 ? 0 : part(it, &t0);
+        if (nt > 0) {
+          const uint32_t qb = qc & 1;
+          failed = failed || !cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort, status);
+          if (!failed) {
+            mbar_expect_tx(q_full + qb, (uint32_t)(a.G * a.tpt) * 128u);
+            tma_load_3d(sQ + qb * SL::kTileBytes, &maps.q, 0, it.hk * a.G, it.r0, q_full + qb);
+            ++qc;
+          }
+          // K(t + 1) goes out before V(t): the next scores must not wait until P.V has
+          // freed a V tile
+#pragma unroll 1
+          for (int j = 0; j <= 2 * nt; ++j) {
+            const bool is_v = j > 0 && (j & 1) == 0;
+            const int t = is_v ? j / 2 - 1 : (j + 1) / 2;
+            if (t >= nt || failed) continue;
+            const uint32_t gs = g + t, s = gs % R;
+            if (!cross_wait((is_v ? v_empty : k_empty) + s, ((gs / R) & 1) ^ 1, budget, s_abort, status)) {
+              failed = true;
+              continue;
+            }
+            uint64_t* f = (is_v ? v_full : k_full) + s;
+            mbar_expect_tx(f, SL::kTileBytes);
+            tma_load_3d(sm + (is_v ? SL::v : SL::k) + s * SL::kTileBytes, is_v ? &maps.v : &maps.k, 0, it.hk,
+                        it.o0 + (t0 + t) * 128, f);
+            if (is_v) v_issued = gs + 1;
+            else k_issued = gs + 1;
+          }
+          g += nt;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
+    }
+    if (lane == 0) {
+      // no copy may still be landing when the CTA leaves
+#pragma unroll 1
+      for (uint32_t n = k_issued > R ? k_issued - R : 0; n < k_issued; ++n)
+        mbar_wait(k_full + n % R, (n / R) & 1, kDrainBudget);
+#pragma unroll 1
+      for (uint32_t n = v_issued > R ? v_issued - R : 0; n < v_issued; ++n)
+        mbar_wait(v_full + n % R, (n / R) & 1, kDrainBudget);
+#pragma unroll 1
+      for (uint32_t n = qc > 2 ? qc - 2 : 0; n < qc; ++n) mbar_wait(q_full + (n & 1), (n >> 1) & 1, kDrainBudget);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ MMA issuers
+    // (whole warps, so that the one that issues a P.V can zero rows of V first)
+    setmaxnreg_dec<56>();
+    const bool qk_role = warp == 1;
+    const int pv_wg = warp == 3 ? 0 : 1;  // the warpgroup whose tiles this warp multiplies
+    uint32_t g = 0, qc = 0, pn = 0;       // key tiles and items before this one, tiles whose P has been consumed
+    const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sm + SL::k), v_addr = smem_u32(sm + SL::v);
+    bool ok = true;                       // a wait that ran out ends this warp's products
+    for (uint32_t c = 0;; ++c) {
+      CrossItem it;
+      if (lane == 0) it = read_item(c);
+      it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
+      if (it.hk < 0) break;
+      it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      it.b = __shfl_sync(0xffffffffu, it.b, 0);
+      int t0;
+      const int nt = part(it, &t0);
+      if (nt == 0) continue;
+      if (qk_role) {
+        if (lane == 0) {
+          const uint32_t qb = qc & 1;
+          ok = ok && cross_wait(q_full + qb, (qc >> 1) & 1, budget, s_abort, status);
+          const uint64_t dq = sdesc_sw128(q_addr + qb * SL::kTileBytes, 16, 1024);
+#pragma unroll 1
+          for (int t = 0; t < nt; ++t) {
+            const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
+            if (gs >= 3) ok = ok && cross_wait(buf_free + sb, ((gs - 3) / 3) & 1, budget, s_abort, status);
+            ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort, status);
+            if (!ok) continue;
+            const uint64_t dk = sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tS(sb), dq + kmajor_step(k), dk + kmajor_step(k), kIdescQK, k > 0);
+            mma_commit(s_full + sb);
+            mma_commit(k_empty + s);
+          }
+          if (ok) mma_commit(q_empty + qb);
+        }
+        ++qc;
+        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int t = pv_wg; t < nt; t += 2, ++pn) {
+          const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
+          // P of this tile says that S was there, so that P.V of the stage's previous
+          // tile is done: the wait for V sees its own phase
+          ok = ok && cross_wait(p_full + 2 * pv_wg + (pn & 1), (pn >> 1) & 1, budget, s_abort, status);
+          ok = ok && cross_wait(v_full + s, (gs / R) & 1, budget, s_abort, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          const int left = it.no - (t0 + t) * 128;
+          if (a.key_mask || left < 128) {
+            uint32_t bits[4];
+            const uint8_t* mask = a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * 128 : nullptr;
+            if (!key_bits(mask, left, bits)) zero_rows<4, 1>(sm + SL::v + s * SL::kTileBytes, bits);
+            __syncwarp();
+          }
+          if (lane == 0) {
+            const uint64_t dv = vtile_desc(v_addr + s * SL::kTileBytes, 0);
+            const uint32_t tp = tS(sb);  // P(t) overwrote its S
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 128 / 16; ++k)
+              mma_ts(tO(pv_wg), tp + 8 * k, dv + vtile_step(k), kIdescPV, (k > 0 || t >= 2) ? 1u : 0u);
+            mma_commit(buf_free + sb);
+            mma_commit(v_empty + s);
+          }
+          __syncwarp();
+        }
+      }
+      g += nt;
+    }
+    if (lane == 0) {
+      uint64_t* my_drain = drain + (warp - 1);
+      mma_commit(my_drain);
+      mbar_wait(my_drain, 0, kDrainBudget);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    setmaxnreg_inc<224>();
+    const int wg = (warp - 4) >> 2;
+    const int quad = warp & 3;               // TMEM lane quadrant of this warp
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const float ks = a.kscale;
+    const float2 ks2 = make_float2(ks, ks);
+    const uint32_t tOw = tO(wg) + lane_off;
+    const int row_tok = row / a.G, row_head = row - row_tok * a.G;
+    uint32_t own = 0, gbase = 0;  // this warpgroup's tiles, and the CTA's before the item
+    // One thread takes each item from the ring and leaves it in s_cur; all 256 read
+    // it behind their barrier, so that they run the same list even after a wait
+    // has run out.
+    const bool reader = warp == 4 && lane == 0;
+    uint32_t c = 0;
+    if (reader) *s_cur = read_item(c++);
+    named_sync(3, 256);
+    for (;;) {
+      const CrossItem it = *s_cur;
+      if (it.hk < 0) break;
+      int t0;
+      const int nt = part(it, &t0);
+      const bool row_in = row_tok < it.nr;
+      // a row block without a valid row needs no weights: its P may hold anything,
+      // since a row of P only reaches its own row of O
+      const bool warp_in = __any_sync(0xffffffffu, row_in);
+      float m_run = -INFINITY, l_run = 0.f;
+      bool o_has = false;
+      for (int t = wg; t < nt; t += 2, ++own) {
+        const uint32_t G = gbase + t;
+        const uint32_t sb = G % 3;
+        const uint32_t tSw = tmem + 128u * sb + lane_off;
+        cross_wait(s_full + sb, (G / 3) & 1, budget, s_abort, status);
+        __syncwarp();
+        tc_fence_after();
+        if (warp_in) {
+          const int left = it.no - (t0 + t) * 128;
+          if (a.key_mask || left < 128) {
+            uint32_t bits[4];
+            if (!key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * 128 : nullptr, left,
+                          bits)) {
+              // the scores of keys that do not count become -inf in place (kept out of
+              // the straight code below, which the instruction caches have to hold)
+#pragma unroll 1
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t word = w == 0 ? bits[0] : w == 1 ? bits[1] : w == 2 ? bits[2] : bits[3];
+                uint32_t r[32];
+                tmem_ld32(tSw + 32 * w, r);
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((word >> j) & 1u)) r[j] = 0xff800000u;
+                tmem_st32(tSw + 32 * w, r);
+              }
+              tmem_st_wait();
+            }
+          }
+          float x[128];
+          {
+            uint32_t r0[32], r1[32], r2[32], r3[32];
+            tmem_ld32(tSw, r0);
+            tmem_ld32(tSw + 32, r1);
+            tmem_ld32(tSw + 64, r2);
+            tmem_ld32(tSw + 96, r3);
+            tmem_ld_wait4(r0, r1, r2, r3);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              x[e] = __uint_as_float(r0[e]);
+              x[32 + e] = __uint_as_float(r1[e]);
+              x[64 + e] = __uint_as_float(r2[e]);
+              x[96 + e] = __uint_as_float(r3[e]);
+            }
+          }
+          // row maximum of the raw scores (the scale is positive)
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 128; j += 4) {
+            const int e = (j >> 2) & 3;
+            mx[2 * e] = fmax3(mx[2 * e], x[j], x[j + 1]);
+            mx[2 * e + 1] = fmax3(mx[2 * e + 1], x[j + 2], x[j + 3]);
+          }
+          const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * ks;
+          // the base of the exponentials moves only when it would grow by more
+          // than 2^8: numerator and denominator share it, so the result is exact
+          float rescale = 1.f;
+          const bool rebase = mt > m_run + 8.f;
+          if (rebase) {
+            rescale = ex2(m_run - mt);
+            m_run = mt;
+            l_run *= rescale;
+          }
+          const float shift = m_run == -INFINITY ? INFINITY : m_run;  // no finite score yet: every p is 0
+          const float2 nshift = make_float2(-shift, -shift);
+          {
+            uint32_t r[32];
+            float2 acc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float2 z = fma2(make_float2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), ks2, nshift);
+                const float2 pp = make_float2(ex2(z.x), ex2(z.y));
+                acc[e & 3] = add2(acc[e & 3], pp);
+                r[e] = BF16 ? pack_bf16x2(pp.x, pp.y) : pack_f16x2(pp.x, pp.y);
+              }
+              tmem_st32(tSw + 32 * h, r);  // P(t) overwrites the S it came from
+            }
+            const float2 s01 = add2(acc[0], acc[1]), s23 = add2(acc[2], acc[3]);
+            l_run += (s01.x + s23.x) + (s01.y + s23.y);
+          }
+          if (o_has && __any_sync(0xffffffffu, rebase)) {
+            // this warpgroup's previous P.V must be done
+            cross_wait(buf_free + (G - 2) % 3, ((G - 2) / 3) & 1, budget, s_abort, status);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t r[32];
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+              tmem_ld32(tOw + 32 * h, r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * rescale);
+              tmem_st32(tOw + 32 * h, r);
+            }
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 2 * wg + (own & 1));
+        o_has = true;
+      }
+      // ---- the item's end: both warpgroups' states together
+      if (wg < nt) {  // its last P.V
+        const uint32_t G = gbase + wg + 2 * ((nt - 1 - wg) / 2);
+        cross_wait(buf_free + G % 3, (G / 3) & 1, budget, s_abort, status);
+      }
+      __syncwarp();
+      tc_fence_after();
+      sML[wg * 128 + row] = make_float4(m_run, l_run, o_has ? 1.f : 0.f, 0.f);
+      named_sync(3, 256);
+      const float4 s0 = sML[row], s1 = sML[128 + row];
+      const bool h0 = s0.z != 0.f, h1 = s1.z != 0.f;
+      const float m = fmaxf(s0.x, s1.x);
+      const float f0 = (h0 && m != -INFINITY) ? ex2(s0.x - m) : 0.f;
+      const float f1 = (h1 && m != -INFINITY) ? ex2(s1.x - m) : 0.f;
+      const float l = s0.y * f0 + s1.y * f1;
+      const bool alone = args.splits == 1;
+      const float inv = !alone ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      const size_t orow = ((size_t)(it.r0 + row_tok) * a.H + (size_t)it.hk * a.G + row_head);
+      float* sO = reinterpret_cast<float*>(sm + SL::k);  // a cluster's join: the K tiles are idle by then
+#pragma unroll 1
+      for (int col = wg * (D / 2); warp_in && col < (wg + 1) * (D / 2); col += 16) {
+        uint32_t ra[16], rb[16];
+        tmem_ld16(tO(0) + lane_off + col, ra);
+        tmem_ld16(tO(1) + lane_off + col, rb);
+        tmem_ld_wait(ra);
+        tmem_ld_wait(rb);
+        if (!row_in || *s_abort != 0) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          float o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            o[k] = ((f0 > 0.f ? __uint_as_float(ra[e + k]) * f0 : 0.f) +
+                    (f1 > 0.f ? __uint_as_float(rb[e + k]) * f1 : 0.f)) * inv;
+          if (!alone) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4)
+              *reinterpret_cast<float4*>(sO + o_piece<D>(row, (col + e + k) / 4)) =
+                  make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          } else if (col + e < a.d) {
+            const size_t at = orow * a.d + col + e;
+            store_rounded<T, 8>(static_cast<T*>(args.out) + at,
+                                args.out_lo ? static_cast<T*>(args.out_lo) + at : nullptr, o);
+          }
+        }
+      }
+      if (!alone) {
+        if (wg == 0) sML[256 + row] = make_float4(m, l, 0.f, 0.f);
+      } else if (args.lse && wg == 0 && row_in && *s_abort == 0) {
+        args.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+      tc_fence_before();
+      named_sync(3, 256);  // every thread has read s_cur and sML
+      gbase += nt;
+      if (!alone) break;  // one item per cluster; s_cur stays for the join
+      if (reader) *s_cur = read_item(c++);
+      named_sync(3, 256);
+    }
+  }
+
+  if (args.splits > 1) {
+    cluster_sync();
+    if (warp >= 4 && s_cur->hk >= 0)
+      join_cluster<T, D>(args, *s_cur, rank, (int)threadIdx.x - 128, 256, smem_u32(sML + 256), smem_u32(sm + SL::k));
+    cluster_sync();  // no CTA leaves while another one reads its shared memory
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <bool BF16>
+cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t s) {
+  auto kernel = cross64_kernel<BF16>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = prepare_kernel((const void*)kernel, (int)FwdSmem::alloc, kRegs, &done);
+  return e != cudaSuccess ? e : launch_clusters(kernel, a, maps, grid, kThreads, FwdSmem::alloc, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s) {
+  return bf16 ? launch<true>(a, maps, grid, s) : launch<false>(a, maps, grid, s);
+}
+
+}  // namespace dfa

@@ -42,6 +42,8 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 384;
+constexpr int kRegs = 168;  // launched; eight warps at 224 and four at 56 after the split
+static_assert(256 * 224 + 128 * 56 <= kThreads * kRegs, "setmaxnreg.inc must not wait");
 constexpr uint32_t kItemRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 14.f;  // fp16: P is held as 2^14 p
@@ -560,7 +562,7 @@ cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items,
   auto kernel = cross_bwd_kernel<D, BF16, KEYS>;
   const uint32_t bytes = BwdSmem<D>::alloc;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kThreads, &done);
+  const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kRegs, &done);
   if (e != cudaSuccess) return e;
   kernel<<<(int)std::min<long long>(items, device_sms()), kThreads, bytes, s>>>(a, maps);
   return cudaGetLastError();

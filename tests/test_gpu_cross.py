@@ -31,6 +31,11 @@ CASES = [  # B, H, Hk, d, Lq, Lk, dtype, q, k
     (1, 1, 1, 128, 1, 3000, HF, "padded", "masked"),
     (70, 4, 4, 64, 1, 260, BF, "padded", "packed"),
     (9, 12, 12, 64, 300, 200, BF, "padded", "masked"),
+    # many items of one key tile for each SM, and of an odd number of tiles
+    (300, 4, 4, 128, 40, 90, BF, "padded", "full"),
+    (300, 4, 4, 64, 40, 90, HF, "padded", "full"),
+    (200, 4, 4, 128, 9, 390, HF, "padded", "packed"),
+    (200, 4, 2, 64, 9, 390, BF, "packed", "masked"),
 ]
 
 
