@@ -18,11 +18,15 @@
 //   P, dS                             by warpgroup h, rounded to the I/O type,
 //                                     written over S and dP
 //   acc0 += dS.Y0 (dk or dq), acc1 += P.Y1 (dv; rows of P that do not count are 0)
-// (X the resident, Y the streamed tiles.)  While warpgroup h works on its half,
-// the tensor core runs the other half's products.
+// (X the resident, Y the streamed tiles.)  Three such (S, dP) buffers rotate (two
+// where the sums leave no more columns: dk, dv at D = 128), so that the tensor core
+// runs the next half's products while both warpgroups are busy.
 //   warp 0        items and TMA loads
-//   warp 1        every tcgen05.mma
-//   warps 2, 3    per streamed tile: the rows' (lse, D) or the keys' mask bits into
+//   warp 1        issues the score products, warp 2 the sums: the waits between the
+//                 products of one issuer left the tensor core idle for a third of
+//                 the time (8 x 12 heads, 2048 x 8192, d = 64, both kernels: one
+//                 issuer 2.07 ms)
+//   warp 3        per streamed tile: the rows' (lse, D) or the keys' mask bits into
 //                 shared memory, and zeros over streamed rows that do not count
 //                 (they are the reduction dimension of the second products)
 //   warps 4-11    P and dS, one thread per resident row; the epilogue
@@ -118,11 +122,11 @@ struct BwdSmem {
   static constexpr uint32_t kTileBytes = kChunks * kBoxBytes;
   static constexpr uint32_t x = 0;                                   // [kRes][X0 | X1]
   static constexpr uint32_t y = x + kRes * 2 * kTileBytes;           // [kStages][Y0 | Y1]
-  static constexpr uint32_t col = y + kStages * 2 * kTileBytes;      // [kStages]: float -lse [128], D [128]; or 4 mask words
+  static constexpr uint32_t col = y + kStages * 2 * kTileBytes;      // [kStages]: float -lse [128], -D [128]; or 4 mask words
   static constexpr uint32_t bars = col + kStages * 1024;
-  // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full [2];
-  // acc_full, acc_free, drain; item_full, item_empty
-  static constexpr int kBars = 2 * kRes + 3 * kStages + 4 + 3 + 2 * (int)kItemRing;
+  // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full, s_free [3];
+  // acc_full, acc_free, drain [2]; item_full, item_empty
+  static constexpr int kBars = 2 * kRes + 3 * kStages + 9 + 4 + 2 * (int)kItemRing;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t cur = ring + 32 * kItemRing;
   static constexpr uint32_t misc = cur + 32;
@@ -140,10 +144,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   constexpr uint32_t kIdescS = idesc_f16(128, 64, BF16 ? 1 : 0, 0, 0);
   constexpr uint32_t kIdescAcc = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr uint32_t kAccCols = (KEYS ? 2u : 1u) * D, kXFirst = 256u;
-  static_assert(tmem_region_fits(0, kAccCols, kXFirst), "accumulators below the scores");
-  static_assert(tmem_region_fits(kXFirst, 256, 512), "two halves of S and dP in 512 columns");
-  constexpr uint32_t kItemReaders = 1 + 2 + 1;  // issuer, warps 2 and 3, the warpgroups' reader
+  // sums first, then the (S, dP) buffers: half u of the CTA (two per streamed tile)
+  // uses buffer u mod kBufs
+  constexpr uint32_t kAccCols = (KEYS ? 2u : 1u) * D, kBufs = kAccCols <= 128 ? 3u : 2u;
+  static_assert(tmem_region_fits(kAccCols, 128 * kBufs, 512), "sums and score buffers in 512 columns");
+  constexpr uint32_t kItemReaders = 4;  // warps 1, 2 and 3, the warpgroups' reader
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -153,12 +158,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   uint64_t* full = x_empty + kRes;
   uint64_t* ready = full + kStages;   // landed, rows that do not count zeroed, columns' values written
   uint64_t* empty = ready + kStages;
-  uint64_t* s_full = empty + kStages;  // [2]
-  uint64_t* p_full = s_full + 2;       // [2]
-  uint64_t* acc_full = p_full + 2;
+  // [buffer]: S and dP computed; P and dS written; the sums have read them
+  uint64_t* s_full = empty + kStages;
+  uint64_t* p_full = s_full + 3;
+  uint64_t* s_free = p_full + 3;
+  uint64_t* acc_full = s_free + 3;
   uint64_t* acc_free = acc_full + 1;
-  uint64_t* drain = acc_free + 1;
-  uint64_t* item_full = drain + 1;
+  uint64_t* drain = acc_free + 1;      // [2], one per issuing thread
+  uint64_t* item_full = drain + 2;
   uint64_t* item_empty = item_full + kItemRing;
   auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
   CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
@@ -174,16 +181,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     }
     for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(ready + s, 2);
+      mbar_init(ready + s, 1);
       mbar_init(empty + s, 1);
     }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(s_full + h, 1);
-      mbar_init(p_full + h, 4);
+    for (int b = 0; b < 3; ++b) {
+      mbar_init(s_full + b, 1);
+      mbar_init(p_full + b, 4);
+      mbar_init(s_free + b, 1);
     }
+    for (int b = 0; b < 2; ++b) mbar_init(drain + b, 1);
     mbar_init(acc_full, 1);
     mbar_init(acc_free, 8);
-    mbar_init(drain, 1);
     for (uint32_t b = 0; b < kItemRing; ++b) {
       mbar_init(item_full + b, 1);
       mbar_init(item_empty + b, kItemReaders);
@@ -204,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t tAcc0 = tmem, tAcc1 = tmem + D;
-  auto tS = [&](int h) { return tmem + kXFirst + 128u * h; };
-  auto tdP = [&](int h) { return tmem + kXFirst + 128u * h + 64u; };
+  auto tS = [&](uint32_t b) { return tmem + kAccCols + 128u * b; };
+  auto tdP = [&](uint32_t b) { return tmem + kAccCols + 128u * b + 64u; };
 
   const unsigned long long budget = a.budget;
   int32_t* status = a.status;
@@ -281,82 +289,97 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         mbar_wait(x_full + k % kRes, (k / kRes) & 1, kDrainBudget);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ score products
     setmaxnreg_dec<56>();
     if (lane == 0) {
-      uint32_t g = 0, xc = 0;        // streamed tiles and items before this one
-      uint32_t pn[2] = {0, 0};       // halves h whose P and dS have been consumed
+      uint32_t g = 0, xc = 0;  // streamed tiles and items before this one
+      bool ok = true;          // a wait that ran out ends this thread's products
       for (uint32_t c = 0;; ++c) {
         const CrossItem it = read_item(c);
         if (it.hk < 0) break;
         const int nt = y_tiles(it);
         if (nt == 0) continue;
         const uint32_t xb = xc % kRes;
-        const uint8_t* sX = sm + SL::x + xb * 2 * SL::kTileBytes;
-        const bool x_ok = cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
-        auto issue_scores = [&](int t, int h) {
-          const uint32_t gs = g + t, s = gs % kStages;
-          bool ok = x_ok;
-          // both halves wait, so that each phase is waited for in order
-          ok = cross_wait(ready + s, (gs / kStages) & 1, budget, s_abort, status) && ok;
-          if (ok) {
-            const uint8_t* sY = sm + SL::y + s * 2 * SL::kTileBytes;
-            const uint64_t dx0 = kmajor_desc(sX, 0), dx1 = kmajor_desc(sX + SL::kTileBytes, 0);
-            const uint64_t dy0 = kmajor_desc(sY + h * 8192, 0), dy1 = kmajor_desc(sY + SL::kTileBytes + h * 8192, 0);
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tS(h), dx0 + kmajor_step(k), dy0 + kmajor_step(k), kIdescS, k > 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tdP(h), dx1 + kmajor_step(k), dy1 + kmajor_step(k), kIdescS, k > 0);
-            mma_commit(s_full + h);
-          }
-        };
-        auto issue_sums = [&](int t, int h) {
-          const uint32_t s = (g + t) % kStages;
-          const uint32_t k0 = pn[h]++;
-          if (cross_wait(p_full + h, k0 & 1, budget, s_abort, status)) {
-            const uint32_t y_addr = smem_u32(sm + SL::y + s * 2 * SL::kTileBytes);
-            const uint64_t dy0 = vtile_desc(y_addr, 4 * h), dy1 = vtile_desc(y_addr + SL::kTileBytes, 4 * h);
-            const uint32_t first = t == 0 && h == 0 ? 0u : 1u;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tAcc0, tdP(h) + 8 * k, dy0 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
-            if (KEYS) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts(tAcc1, tS(h) + 8 * k, dy1 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
-            }
-            if (h == 1) mma_commit(empty + s);
-          }
-        };
-        issue_scores(0, 0);
-        issue_scores(0, 1);
-        // the epilogue has read the previous item's sums
-        if (xc > 0) cross_wait(acc_free, (xc - 1) & 1, budget, s_abort, status);
-        for (int t = 0; t < nt; ++t)
-#pragma unroll
+        ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
+        const uint32_t x_addr = smem_u32(sm + SL::x + xb * 2 * SL::kTileBytes);
+        const uint64_t dx0 = sdesc_sw128(x_addr, 16, 1024), dx1 = sdesc_sw128(x_addr + SL::kTileBytes, 16, 1024);
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t, ++g) {
+          const uint32_t s = g % kStages;
+          ok = ok && cross_wait(ready + s, (g / kStages) & 1, budget, s_abort, status);
+          const uint32_t y_addr = smem_u32(sm + SL::y + s * 2 * SL::kTileBytes);
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            issue_sums(t, h);
-            // the scores of (t + 1, h) follow the products that read P and dS of
-            // (t, h) in the same pipe
-            if (t + 1 < nt) issue_scores(t + 1, h);
+            const uint32_t u = 2 * g + h, b = u % kBufs;
+            if (u >= kBufs) ok = ok && cross_wait(s_free + b, (u / kBufs - 1) & 1, budget, s_abort, status);
+            if (!ok) continue;
+            const uint64_t dy0 = sdesc_sw128(y_addr + h * 8192, 16, 1024);
+            const uint64_t dy1 = sdesc_sw128(y_addr + SL::kTileBytes + h * 8192, 16, 1024);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tS(b), dx0 + kmajor_step(k), dy0 + kmajor_step(k), kIdescS, k > 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tdP(b), dx1 + kmajor_step(k), dy1 + kmajor_step(k), kIdescS, k > 0);
+            mma_commit(s_full + b);
           }
-        mma_commit(acc_full);
-        mma_commit(x_empty + xb);
-        g += nt;
+        }
+        if (ok) mma_commit(x_empty + xb);
         ++xc;
       }
       mma_commit(drain);
       mbar_wait(drain, 0, kDrainBudget);
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ sums
+    setmaxnreg_dec<56>();
+    if (lane == 0) {
+      uint32_t g = 0, xc = 0;
+      bool ok = true;
+      for (uint32_t c = 0;; ++c) {
+        const CrossItem it = read_item(c);
+        if (it.hk < 0) break;
+        const int nt = y_tiles(it);
+        if (nt == 0) continue;
+        // the epilogue has read the previous item's sums
+        if (xc > 0) ok = ok && cross_wait(acc_free, (xc - 1) & 1, budget, s_abort, status);
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t, ++g) {
+          const uint32_t s = g % kStages;
+          const uint32_t y_addr = smem_u32(sm + SL::y + s * 2 * SL::kTileBytes);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u = 2 * g + h, b = u % kBufs;
+            ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort, status);
+            if (!ok) continue;
+            const uint64_t dy0 = vtile_desc(y_addr, 4 * h), dy1 = vtile_desc(y_addr + SL::kTileBytes, 4 * h);
+            const uint32_t first = t == 0 && h == 0 ? 0u : 1u;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tAcc0, tdP(b) + 8 * k, dy0 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
+            if (KEYS) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tAcc1, tS(b) + 8 * k, dy1 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
+            }
+            mma_commit(s_free + b);
+            // (the scores of both halves, which read the stage too, stood before P)
+            if (h == 1) mma_commit(empty + s);
+          }
+        }
+        if (ok) mma_commit(acc_full);
+        ++xc;
+      }
+      mma_commit(drain + 1);
+      mbar_wait(drain + 1, 0, kDrainBudget);
+    }
+  } else if (warp == 3) {
     // ------------------------------------------------------------ streamed rows
     setmaxnreg_dec<56>();
-    const int w = warp - 2;  // rows 64 w .. 64 w + 63 of each tile
     uint32_t g = 0;
+    bool ok = true;
     for (uint32_t c = 0;; ++c) {
       CrossItem it;
       if (lane == 0) it = read_item(c);
@@ -366,49 +389,46 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
       it.b = __shfl_sync(0xffffffffu, it.b, 0);
       const int nt = y_tiles(it);
+#pragma unroll 1
       for (int t = 0; t < nt; ++t, ++g) {
         const uint32_t s = g % kStages;
         const int left = it.no - t * y_step;  // tokens of the tile (and behind it)
-        bool in[2];
-        float2 st[2];
+        uint32_t bits[4];
+        float2 st[4];
+        bool whole = true;
+        if constexpr (KEYS) {
+          const float2* stat = args.stat + (size_t)(it.o0 + t * y_step) * a.H + it.hk * a.G;
+          const int tokens = min(left, a.tpt);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 64 * w + 32 * i + lane;
-          if constexpr (KEYS) {
-            const int tok = r / a.G, head = r - tok * a.G;
-            in[i] = tok < min(left, a.tpt);
-            st[i] = in[i] ? args.stat[(size_t)(it.o0 + t * y_step + tok) * a.H + it.hk * a.G + head]
-                          : make_float2(INFINITY, 0.f);
-          } else {
-            in[i] = r < left && (!a.key_mask || a.key_mask[(size_t)it.b * a.Lk + (size_t)t * 128 + r] != 0);
+          for (int w = 0; w < 4; ++w) {
+            const int r = 32 * w + lane, tok = r / a.G;
+            const bool in = tok < tokens;
+            st[w] = in ? stat[(size_t)tok * a.H + (r - tok * a.G)] : make_float2(INFINITY, 0.f);
+            bits[w] = __ballot_sync(0xffffffffu, in);
           }
+          whole = (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu;
+        } else {
+          whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)t * 128 : nullptr, left, bits);
         }
-        cross_wait(full + s, (g / kStages) & 1, budget, s_abort, status);
-        __syncwarp();
+        ok = ok && cross_wait(full + s, (g / kStages) & 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
         uint8_t* sY = sm + SL::y + s * 2 * SL::kTileBytes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 64 * w + 32 * i + lane;
-          if (!in[i]) {
-#pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                *reinterpret_cast<uint4*>(sY + ch * kBoxBytes + r * 128 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(sY + SL::kTileBytes + ch * kBoxBytes + r * 128 + 16 * e) =
-                    make_uint4(0u, 0u, 0u, 0u);
-              }
-          }
-          if constexpr (KEYS) {
-            float* col = reinterpret_cast<float*>(sm + SL::col + s * 1024);
-            col[r] = (BF16 ? 0.f : kPShift) - st[i].x;
-            col[128 + r] = st[i].y;
-          } else {
-            const uint32_t bits = __ballot_sync(0xffffffffu, in[i]);
-            if (lane == 0) reinterpret_cast<uint32_t*>(sm + SL::col + s * 1024)[2 * w + i] = bits;
-          }
+        if (!whole) {
+          zero_rows<4, kChunks>(sY, bits);
+          if (KEYS) zero_rows<4, kChunks>(sY + SL::kTileBytes, bits);
         }
-        fence_proxy_async_smem();
+        if constexpr (KEYS) {
+          float* col = reinterpret_cast<float*>(sm + SL::col + s * 1024);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            col[32 * w + lane] = (BF16 ? 0.f : kPShift) - st[w].x;
+            col[128 + 32 * w + lane] = -st[w].y;
+          }
+        } else if (lane < 4) {
+          reinterpret_cast<uint32_t*>(sm + SL::col + s * 1024)[lane] =
+              lane == 0 ? bits[0] : lane == 1 ? bits[1] : lane == 2 ? bits[2] : bits[3];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(ready + s);
       }
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     const float scale1 = BF16 ? 1.f : exp2f(-kPShift);           // dv
     const int row_tok = KEYS ? row : row / a.G, row_head = KEYS ? 0 : row - row_tok * a.G;
     const bool reader = warp == 4 && lane == 0;
-    uint32_t g = 0, xc = 0, n = 0, c = 0;    // n: halves of this warpgroup so far
+    uint32_t g = 0, xc = 0, c = 0;
     if (reader) *s_cur = read_item(c++);
     named_sync(3, 256);
     for (;;) {
@@ -442,26 +462,28 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       const int nt = y_tiles(it);
       const bool stored = row_tok < it.nr;   // the resident row belongs to the sequence
       bool row_in = stored;
-      float nl = -INFINITY, dd = 0.f;
+      float nl = -INFINITY, nd = 0.f;  // -lse, -D
       if (KEYS) {
         const long long key = (long long)it.r0 + row;  // in [B, Lk] layout this is also the mask's index
         if (row_in && a.key_mask) row_in = a.key_mask[key] != 0;
       } else if (row_in) {
         const float2 st = args.stat[(size_t)(it.r0 + row_tok) * a.H + it.hk * a.G + row_head];
         nl = (BF16 ? 0.f : kPShift) - st.x;
-        dd = st.y;
+        nd = -st.y;
       }
-      for (int t = 0; t < nt; ++t, ++n) {
-        const uint32_t s = (g + t) % kStages;
-        cross_wait(s_full + h, n & 1, budget, s_abort, status);
+      for (int t = 0; t < nt; ++t) {
+        const uint32_t s = (g + t) % kStages, u = 2 * (g + t) + h, b = u % kBufs;
+        // (the buffer's previous half is the other warpgroup's u - 3 at three buffers;
+        // its scores stand before those of u - 2, which this warp has seen)
+        cross_wait(s_full + b, (u / kBufs) & 1, budget, s_abort, status);
         __syncwarp();
         tc_fence_after();
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {  // 32 columns at a time
           uint32_t rs[32], rd[32];
-          tmem_ld32(tS(h) + lane_off + 32 * q, rs);
-          tmem_ld32(tdP(h) + lane_off + 32 * q, rd);
+          tmem_ld32(tS(b) + lane_off + 32 * q, rs);
+          tmem_ld32(tdP(b) + lane_off + 32 * q, rd);
           tmem_ld_wait2(rs, rd);
           uint32_t wp[16], wd[16];
           uint32_t bits = 0xffffffffu;
@@ -474,13 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
               d4 = *reinterpret_cast<const float4*>(col + 128 + 64 * h + 32 * q + e);
             } else {
               l4 = make_float4(nl, nl, nl, nl);
-              d4 = make_float4(dd, dd, dd, dd);
+              d4 = make_float4(nd, nd, nd, nd);
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int j = e + 2 * u;
               const float2 l2 = u ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
-              const float2 dm = u ? make_float2(-d4.z, -d4.w) : make_float2(-d4.x, -d4.y);
+              const float2 dm = u ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
               const float2 z = fma2(make_float2(__uint_as_float(rs[j]), __uint_as_float(rs[j + 1])), ks2, l2);
               const float2 p = make_float2(ex2(z.x), ex2(z.y));
               float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[j]), __uint_as_float(rd[j + 1])), dm));
@@ -502,13 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
               wd[e] &= (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
             }
           }
-          if (KEYS) tmem_st16(tS(h) + lane_off + 16 * q, wp);
-          tmem_st16(tdP(h) + lane_off + 16 * q, wd);
+          if (KEYS) tmem_st16(tS(b) + lane_off + 16 * q, wp);
+          tmem_st16(tdP(b) + lane_off + 16 * q, wd);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + h);
+        if (lane == 0) mbar_arrive(p_full + b);
       }
       // ---- the item's results
       if (nt > 0) cross_wait(acc_full, xc & 1, budget, s_abort, status);
