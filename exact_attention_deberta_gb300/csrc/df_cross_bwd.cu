@@ -46,8 +46,9 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 384;
-constexpr int kRegs = 168;  // launched; eight warps at 224 and four at 56 after the split
-static_assert(256 * 224 + 128 * 56 <= kThreads * kRegs, "setmaxnreg.inc must not wait");
+// registers per thread: launched, and after the split (P and dS, others)
+constexpr int kRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "setmaxnreg.inc must not wait");
 constexpr uint32_t kItemRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 14.f;  // fp16: P is held as 2^14 p
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
 
   if (warp == 0) {
     // ------------------------------------------------------------ items and loads
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<kOtherRegs>();
     TileWalk walk;
     uint32_t g = 0, xc = 0, g_issued = 0, x_issued = 0;
     const uint32_t q_box = (uint32_t)(a.G * a.tpt) * 128u;  // bytes of a 64-column box of a query tile
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ score products
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<kOtherRegs>();
     if (lane == 0) {
       uint32_t g = 0, xc = 0;  // streamed tiles and items before this one
       bool ok = true;          // a wait that ran out ends this thread's products
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ sums
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<kOtherRegs>();
     if (lane == 0) {
       uint32_t g = 0, xc = 0;
       bool ok = true;
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ streamed rows
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<kOtherRegs>();
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t c = 0;; ++c) {
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     }
   } else {
     // ------------------------------------------------------------ P, dS and the epilogue
-    setmaxnreg_inc<224>();
+    setmaxnreg_inc<kSoftmaxRegs>();
     const int h = (warp - 4) >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;        // resident row
