@@ -22,14 +22,13 @@
 // where the sums leave no more columns: dk, dv at D = 128), so that the tensor core
 // runs the next half's products while both warpgroups are busy.
 //   warp 0        items and TMA loads
-//   warp 1        issues the score products, warp 2 the sums: the waits between the
-//                 products of one issuer left the tensor core idle for a third of
-//                 the time (8 x 12 heads, 2048 x 8192, d = 64, both kernels: one
-//                 issuer 2.07 ms)
-//   warp 3        per streamed tile: the rows' (lse, D) or the keys' mask bits into
+//   warps 1, 2    issue S and dP, warps 3, 4 the sums acc0 and acc1: between two
+//                 batches of products an issuer spends about as long on waits and
+//                 commits as on the products themselves
+//   warp 5        per streamed tile: the rows' (lse, D) or the keys' mask bits into
 //                 shared memory, and zeros over streamed rows that do not count
 //                 (they are the reduction dimension of the second products)
-//   warps 4-11    P and dS, one thread per resident row; the epilogue
+//   warps 8-15    P and dS, one thread per resident row; the epilogue
 //
 // fp16: dS spans too wide a range for its exponent, so it is scaled by a power of
 // two that puts the largest |dout_i| at about 16, and P (at most 1) by 2^14; the
@@ -45,10 +44,10 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512, kFirst = 8;  // warps kFirst .. form P and dS, the others feed them
 // registers per thread: launched, and after the split (P and dS, others)
-constexpr int kRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "setmaxnreg.inc must not wait");
+constexpr int kRegs = 128, kSoftmaxRegs = 176, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kRegs, "setmaxnreg.inc must not wait");
 constexpr uint32_t kItemRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 14.f;  // fp16: P is held as 2^14 p
@@ -125,9 +124,10 @@ struct BwdSmem {
   static constexpr uint32_t y = x + kRes * 2 * kTileBytes;           // [kStages][Y0 | Y1]
   static constexpr uint32_t col = y + kStages * 2 * kTileBytes;      // [kStages]: float -lse [128], -D [128]; or 4 mask words
   static constexpr uint32_t bars = col + kStages * 1024;
-  // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full, s_free [3];
-  // acc_full, acc_free, drain [2]; item_full, item_empty
-  static constexpr int kBars = 2 * kRes + 3 * kStages + 9 + 4 + 2 * (int)kItemRing;
+  // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full, ds_free,
+  // p_free [3];
+  // acc_full, acc_free; drain [4]; item_full, item_empty
+  static constexpr int kBars = 2 * kRes + 3 * kStages + 12 + 6 + 2 * (int)kItemRing;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t cur = ring + 32 * kItemRing;
   static constexpr uint32_t misc = cur + 32;
@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   // uses buffer u mod kBufs
   constexpr uint32_t kAccCols = (KEYS ? 2u : 1u) * D, kBufs = kAccCols <= 128 ? 3u : 2u;
   static_assert(tmem_region_fits(kAccCols, 128 * kBufs, 512), "sums and score buffers in 512 columns");
-  constexpr uint32_t kItemReaders = 4;  // warps 1, 2 and 3, the warpgroups' reader
+  constexpr uint32_t kSums = KEYS ? 2 : 1;           // issuers of sums
+  constexpr uint32_t kItemReaders = 2 + kSums + 2;  // the issuers, warp 5, the warpgroups' reader
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -159,14 +160,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   uint64_t* full = x_empty + kRes;
   uint64_t* ready = full + kStages;   // landed, rows that do not count zeroed, columns' values written
   uint64_t* empty = ready + kStages;
-  // [buffer]: S and dP computed; P and dS written; the sums have read them
+  // [buffer]: S and dP computed; P and dS written; the sums have read dS, and P
   uint64_t* s_full = empty + kStages;
   uint64_t* p_full = s_full + 3;
-  uint64_t* s_free = p_full + 3;
-  uint64_t* acc_full = s_free + 3;
+  uint64_t* ds_free = p_full + 3;
+  uint64_t* p_free = ds_free + 3;
+  uint64_t* acc_full = p_free + 3;
   uint64_t* acc_free = acc_full + 1;
-  uint64_t* drain = acc_free + 1;      // [2], one per issuing thread
-  uint64_t* item_full = drain + 2;
+  uint64_t* drain = acc_free + 1;      // [4], one per issuing thread
+  uint64_t* item_full = drain + 4;
   uint64_t* item_empty = item_full + kItemRing;
   auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
   CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
@@ -178,20 +180,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   if (threadIdx.x == 0) {
     for (uint32_t b = 0; b < kRes; ++b) {
       mbar_init(x_full + b, 1);
-      mbar_init(x_empty + b, 1);
+      mbar_init(x_empty + b, 2);
     }
     for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(ready + s, 1);
-      mbar_init(empty + s, 1);
+      mbar_init(empty + s, kSums);
     }
     for (int b = 0; b < 3; ++b) {
-      mbar_init(s_full + b, 1);
+      mbar_init(s_full + b, 2);
       mbar_init(p_full + b, 4);
-      mbar_init(s_free + b, 1);
+      mbar_init(ds_free + b, 1);
+      mbar_init(p_free + b, 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(drain + b, 1);
-    mbar_init(acc_full, 1);
+    for (int b = 0; b < 4; ++b) mbar_init(drain + b, 1);
+    mbar_init(acc_full, kSums);
     mbar_init(acc_free, 8);
     for (uint32_t b = 0; b < kItemRing; ++b) {
       mbar_init(item_full + b, 1);
@@ -289,10 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       for (uint32_t k = x_issued > kRes ? x_issued - kRes : 0; k < x_issued; ++k)
         mbar_wait(x_full + k % kRes, (k / kRes) & 1, kDrainBudget);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ score products
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ S (warp 1), dP (warp 2)
     setmaxnreg_dec<kOtherRegs>();
     if (lane == 0) {
+      const uint32_t which = warp - 1;
+      const uint32_t tD = tmem + kAccCols + 64u * which;
+      // a buffer's columns may be written again once the sums have read what stands
+      // there; without dv the columns of S hold no P, and its readers are done with
+      // dS's arrival
+      uint64_t* free_bar = which ? ds_free : KEYS ? p_free : p_full;
       uint32_t g = 0, xc = 0;  // streamed tiles and items before this one
       bool ok = true;          // a wait that ran out ends this thread's products
       for (uint32_t c = 0;; ++c) {
@@ -302,40 +311,38 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         if (nt == 0) continue;
         const uint32_t xb = xc % kRes;
         ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
-        const uint32_t x_addr = smem_u32(sm + SL::x + xb * 2 * SL::kTileBytes);
-        const uint64_t dx0 = sdesc_sw128(x_addr, 16, 1024), dx1 = sdesc_sw128(x_addr + SL::kTileBytes, 16, 1024);
+        const uint64_t dx = sdesc_sw128(smem_u32(sm + SL::x + (xb * 2 + which) * SL::kTileBytes), 16, 1024);
 #pragma unroll 1
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t s = g % kStages;
           ok = ok && cross_wait(ready + s, (g / kStages) & 1, budget, s_abort, status);
-          const uint32_t y_addr = smem_u32(sm + SL::y + s * 2 * SL::kTileBytes);
+          const uint32_t y_addr = smem_u32(sm + SL::y + (s * 2 + which) * SL::kTileBytes);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const uint32_t u = 2 * g + h, b = u % kBufs;
-            if (u >= kBufs) ok = ok && cross_wait(s_free + b, (u / kBufs - 1) & 1, budget, s_abort, status);
+            if (u >= kBufs) ok = ok && cross_wait(free_bar + b, (u / kBufs - 1) & 1, budget, s_abort, status);
             if (!ok) continue;
-            const uint64_t dy0 = sdesc_sw128(y_addr + h * 8192, 16, 1024);
-            const uint64_t dy1 = sdesc_sw128(y_addr + SL::kTileBytes + h * 8192, 16, 1024);
+            const uint64_t dy = sdesc_sw128(y_addr + h * 8192, 16, 1024);
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ss(tS(b), dx0 + kmajor_step(k), dy0 + kmajor_step(k), kIdescS, k > 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tdP(b), dx1 + kmajor_step(k), dy1 + kmajor_step(k), kIdescS, k > 0);
+              mma_ss(tD + 128u * b, dx + kmajor_step(k), dy + kmajor_step(k), kIdescS, k > 0);
             mma_commit(s_full + b);
           }
         }
         if (ok) mma_commit(x_empty + xb);
         ++xc;
       }
-      mma_commit(drain);
-      mbar_wait(drain, 0, kDrainBudget);
+      mma_commit(drain + which);
+      mbar_wait(drain + which, 0, kDrainBudget);
     }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ sums
+  } else if (warp <= 4) {
+    // ------------------------------------------------------------ sums: dS.Y0 (warp 3), P.Y1 (warp 4)
     setmaxnreg_dec<kOtherRegs>();
-    if (lane == 0) {
+    const uint32_t which = warp - 3;
+    if (lane == 0 && which < kSums) {
+      const uint32_t tA = tmem + kAccCols + (which ? 0u : 64u), tD = which ? tAcc1 : tAcc0;
+      uint64_t* free_bar = which ? p_free : ds_free;
       uint32_t g = 0, xc = 0;
       bool ok = true;
       for (uint32_t c = 0;; ++c) {
@@ -348,24 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
 #pragma unroll 1
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t s = g % kStages;
-          const uint32_t y_addr = smem_u32(sm + SL::y + s * 2 * SL::kTileBytes);
+          const uint32_t y_addr = smem_u32(sm + SL::y + (s * 2 + which) * SL::kTileBytes);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const uint32_t u = 2 * g + h, b = u % kBufs;
             ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort, status);
             if (!ok) continue;
-            const uint64_t dy0 = vtile_desc(y_addr, 4 * h), dy1 = vtile_desc(y_addr + SL::kTileBytes, 4 * h);
+            const uint64_t dy = vtile_desc(y_addr, 4 * h);
             const uint32_t first = t == 0 && h == 0 ? 0u : 1u;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(tAcc0, tdP(b) + 8 * k, dy0 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
-            if (KEYS) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts(tAcc1, tS(b) + 8 * k, dy1 + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
-            }
-            mma_commit(s_free + b);
+              mma_ts(tD, tA + 128u * b + 8 * k, dy + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
+            mma_commit(free_bar + b);
             // (the scores of both halves, which read the stage too, stood before P)
             if (h == 1) mma_commit(empty + s);
           }
@@ -373,10 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         if (ok) mma_commit(acc_full);
         ++xc;
       }
-      mma_commit(drain + 1);
-      mbar_wait(drain + 1, 0, kDrainBudget);
+      mma_commit(drain + 2 + which);
+      mbar_wait(drain + 2 + which, 0, kDrainBudget);
     }
-  } else if (warp == 3) {
+  } else if (warp == 5) {
     // ------------------------------------------------------------ streamed rows
     setmaxnreg_dec<kOtherRegs>();
     uint32_t g = 0;
@@ -434,10 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         if (lane == 0) mbar_arrive(ready + s);
       }
     }
+  } else if (warp < kFirst) {
+    setmaxnreg_dec<kOtherRegs>();
   } else {
     // ------------------------------------------------------------ P, dS and the epilogue
     setmaxnreg_inc<kSoftmaxRegs>();
-    const int h = (warp - 4) >> 2;
+    const int h = (warp - kFirst) >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;        // resident row
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     const float scale0 = BF16 ? a.scale : a.scale / grow;        // dk, dq
     const float scale1 = BF16 ? 1.f : exp2f(-kPShift);           // dv
     const int row_tok = KEYS ? row : row / a.G, row_head = KEYS ? 0 : row - row_tok * a.G;
-    const bool reader = warp == 4 && lane == 0;
+    const bool reader = warp == kFirst && lane == 0;
     uint32_t g = 0, xc = 0, c = 0;
     if (reader) *s_cur = read_item(c++);
     named_sync(3, 256);
