@@ -476,6 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         nl = (BF16 ? 0.f : kPShift) - st.x;
         nd = -st.y;
       }
+      const uint32_t rows_in = __ballot_sync(0xffffffffu, row_in);
+      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       for (int t = 0; t < nt; ++t) {
         const uint32_t s = (g + t) % kStages, u = 2 * (g + t) + h, b = u % kBufs;
         // (the buffer's previous half is the other warpgroup's u - 3 at three buffers;
@@ -484,53 +486,82 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         __syncwarp();
         tc_fence_after();
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
+        if constexpr (KEYS) {
+          // A thread takes two columns of every eight in four rows (lane / 4 + 8 r),
+          // not 64 columns of one row: it then reads a quarter of the columns' values
+          // from shared memory (one row per thread: 898 us against 835 on 8 x 12 heads,
+          // 2048 x 8192, d = 64)
+          const int c2 = 64 * h + 2 * (lane & 3);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // 32 columns at a time
-          uint32_t rs[32], rd[32];
-          tmem_ld32(tS(b) + lane_off + 32 * q, rs);
-          tmem_ld32(tdP(b) + lane_off + 32 * q, rd);
-          tmem_ld_wait2(rs, rd);
-          uint32_t wp[16], wd[16];
-          uint32_t bits = 0xffffffffu;
-          if (!KEYS) bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
+          for (int q = 0; q < 2; ++q) {  // 32 columns at a time
+            uint32_t rs0[16], rs1[16], rd0[16], rd1[16];
+            const uint32_t at = lane_off + 32 * q;
+            tmem_ld_rows16(tS(b) + at, rs0);
+            tmem_ld_rows16(tdP(b) + at, rd0);
+            tmem_ld_rows16(tS(b) + at + (16u << 16), rs1);
+            tmem_ld_rows16(tdP(b) + at + (16u << 16), rd1);
+            float2 nl[4], nd[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 l4, d4;
-            if (KEYS) {
-              l4 = *reinterpret_cast<const float4*>(col + 64 * h + 32 * q + e);
-              d4 = *reinterpret_cast<const float4*>(col + 128 + 64 * h + 32 * q + e);
-            } else {
-              l4 = make_float4(nl, nl, nl, nl);
-              d4 = make_float4(nd, nd, nd, nd);
+            for (int j = 0; j < 4; ++j) {
+              nl[j] = *reinterpret_cast<const float2*>(col + c2 + 32 * q + 8 * j);
+              nd[j] = *reinterpret_cast<const float2*>(col + 128 + c2 + 32 * q + 8 * j);
             }
+            tmem_ld_wait(rs0);
+            tmem_ld_wait(rd0);
+            tmem_ld_wait(rs1);
+            tmem_ld_wait(rd1);
+            auto half_rows = [&](const uint32_t (&rs)[16], const uint32_t (&rd)[16], int i) {
+              uint32_t wp[8], wd[8];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int j = e + 2 * u;
-              const float2 l2 = u ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
-              const float2 dm = u ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
-              const float2 z = fma2(make_float2(__uint_as_float(rs[j]), __uint_as_float(rs[j + 1])), ks2, l2);
-              const float2 p = make_float2(ex2(z.x), ex2(z.y));
-              float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[j]), __uint_as_float(rd[j + 1])), dm));
-              if (!BF16) ds = mul2(ds, ds_mul2);
-              wp[j / 2] = BF16 ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
-              wd[j / 2] = BF16 ? pack_bf16x2(ds.x, ds.y) : pack_f16x2(ds.x, ds.y);
-            }
+              for (int e = 0; e < 8; ++e) {
+                const int j = e >> 1, k = 4 * j + 2 * (e & 1);
+                const float2 z = fma2(make_float2(__uint_as_float(rs[k]), __uint_as_float(rs[k + 1])), ks2, nl[j]);
+                const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[k]), __uint_as_float(rd[k + 1])), nd[j]));
+                if (!BF16) ds = mul2(ds, ds_mul2);
+                wp[e] = BF16 ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+                wd[e] = BF16 ? pack_bf16x2(ds.x, ds.y) : pack_f16x2(ds.x, ds.y);
+              }
+              if (rows_in != 0xffffffffu) {
+                // what does not count has weight 0 whatever its row held
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (!((rows_in >> (16 * i + 8 * (e & 1) + (lane >> 2))) & 1u)) wp[e] = wd[e] = 0u;
+              }
+              const uint32_t to = lane_off + 16 * q + ((uint32_t)(16 * i) << 16);
+              tmem_st_rows16(tS(b) + to, wp);
+              tmem_st_rows16(tdP(b) + to, wd);
+            };
+            half_rows(rs0, rd0, 0);
+            half_rows(rs1, rd1, 1);
           }
-          // what does not count has weight 0 whatever its row held
-          if (KEYS) {
-            if (!row_in) {
+        } else {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) wp[e] = wd[e] = 0u;
-            }
-          } else if (bits != 0xffffffffu) {
+          for (int q = 0; q < 2; ++q) {
+            uint32_t rs[32], rd[32];
+            tmem_ld32(tS(b) + lane_off + 32 * q, rs);
+            tmem_ld32(tdP(b) + lane_off + 32 * q, rd);
+            tmem_ld_wait2(rs, rd);
+            uint32_t wd[16];
+            const uint32_t bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const uint32_t two = (bits >> (2 * e)) & 3u;
-              wd[e] &= (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+              const float2 z =
+                  fma2(make_float2(__uint_as_float(rs[2 * e]), __uint_as_float(rs[2 * e + 1])), ks2, nl2);
+              const float2 p = make_float2(ex2(z.x), ex2(z.y));
+              float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[2 * e]), __uint_as_float(rd[2 * e + 1])), nd2));
+              if (!BF16) ds = mul2(ds, ds_mul2);
+              wd[e] = BF16 ? pack_bf16x2(ds.x, ds.y) : pack_f16x2(ds.x, ds.y);
             }
+            if (bits != 0xffffffffu) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t two = (bits >> (2 * e)) & 3u;
+                wd[e] &= (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+              }
+            }
+            tmem_st16(tdP(b) + lane_off + 16 * q, wd);
           }
-          if (KEYS) tmem_st16(tS(b) + lane_off + 16 * q, wp);
-          tmem_st16(tdP(b) + lane_off + 16 * q, wd);
         }
         tmem_st_wait();
         tc_fence_before();

@@ -277,6 +277,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// 16 lanes x 256 bit, 32 consecutive columns: thread t holds, for each group j of 8
+// columns, r[4j], r[4j + 1] = columns 8j + 2 (t % 4), + 1 of lane t / 4 and
+// r[4j + 2], r[4j + 3] = the same columns of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : DFA_R8(0), DFA_R8(8)
+      : "r"(taddr)
+      : "memory");
+}
+// 16 lanes x 128 bit, 16 consecutive columns: thread t gives r[2j], column 4j + t % 4
+// of lane t / 4, and r[2j + 1], that of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_st_rows16(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               DFA_W8(0)
+               : "memory");
+}
+
 #undef DFA_R8
 #undef DFA_W8
 #undef DFA_U8
