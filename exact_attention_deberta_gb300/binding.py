@@ -506,23 +506,26 @@ _lib.df_embedding_bwd_workspace_size.argtypes = [_i] * 3
 _lib.df_embedding_bwd_workspace_size.restype = _sz
 
 
-def _on_device(dev, tensors):
-    """Every tensor given is a contiguous tensor on the CUDA device ``dev``."""
-    for name, t in tensors:
-        if t is not None and (not t.is_cuda or t.device != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+def _on_device(tensors, names):
+    """The device index that every tensor given (not None) is on, contiguous."""
+    idx = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != idx or idx < 0 or not t.is_contiguous()):
+            name = names.split()[[t is x for x in tensors].index(True)]
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on the same device as {names.split()[0]}")
+    return idx
 
 
-def _call_on(dev, fn, stream, *args) -> int:
-    """fn(*args, stream) with ``dev`` current; the stream defaults to its current one.
-    (Plain integers for pointers and streams: a small call is bound by the host.)"""
+def _call_on(idx, fn, stream, *args) -> int:
+    """fn(*args, stream) with device ``idx`` current; the stream defaults to its current
+    one.  (Plain integers for pointers and streams: a small call is bound by the host.)"""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        stream = torch._C._cuda_getCurrentRawStream(idx)
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == idx:
         return fn(*args, stream)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(idx):
         return fn(*args, stream)
 
 
@@ -538,7 +541,7 @@ def _int_sizes(**sizes):
 
 
 def _status_word(status):
-    if status is not None and (status.dtype != torch.int32 or status.numel() != 1):
+    if status.dtype != torch.int32 or status.numel() != 1:
         raise ValueError("status must be an int32 tensor of one value")
 
 
@@ -553,16 +556,18 @@ def df_embedding(ids, table, scale=1.0, out=None, status=None, stream=None):
     table's dtype.  Rows of ids outside the table are zeros (``status`` is set)."""
     if table.dim() != 2 or table.dtype not in _DTYPE:
         raise ValueError("table must be a bf16, fp16 or fp32 matrix [V, N]")
-    dev = table.device
-    _on_device(dev, (("ids", ids), ("table", table), ("out", out), ("status", status)))
-    _status_word(status)
+    idx = _on_device((table, ids, out, status), "table ids out status")
     V, N = table.shape
-    _int_sizes(ids=ids.numel(), V=V, N=N)
+    shape = ids.shape + (N,)
     if out is None:
-        out = torch.empty(tuple(ids.shape) + (N,), dtype=table.dtype, device=dev)
-    elif out.dtype != table.dtype or tuple(out.shape) != tuple(ids.shape) + (N,):
+        out = table.new_empty(shape)
+    elif out.dtype != table.dtype or out.shape != shape:
         raise ValueError("out must be [..., N] of the table's dtype")
-    _check(_call_on(dev, _lib.df_embedding, stream, ids.data_ptr(), _ids_64(ids), ids.numel(), table.data_ptr(), V, N,
+    if status is not None:
+        _status_word(status)
+    T = ids.numel()
+    _int_sizes(ids=T, V=V, N=N)
+    _check(_call_on(idx, _lib.df_embedding, stream, ids.data_ptr(), _ids_64(ids), T, table.data_ptr(), V, N,
                     float(scale), out.data_ptr(), _DTYPE[table.dtype], _addr(status)), "df_embedding")
     return out
 
@@ -576,24 +581,23 @@ def df_embedding_bwd(ids, dout, vocab, scale=1.0, padding_idx=None, grad=None, a
     """Gradient of the table [vocab, N] in float32 for dout [..., N], the gradient of
     ``df_embedding(ids, table, scale)``.  ``accumulate`` adds to ``grad``, which must
     then be given; tokens with ``padding_idx`` pass no gradient."""
-    dev = dout.device
-    if dout.dtype not in _DTYPE or dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
+    if dout.dtype not in _DTYPE or dout.dim() < 1 or dout.shape[:-1] != ids.shape:
         raise ValueError("dout must be bf16, fp16 or fp32, [..., N] for ids [...]")
-    _on_device(dev, (("ids", ids), ("dout", dout), ("grad", grad), ("workspace", workspace), ("status", status)))
-    _status_word(status)
+    idx = _on_device((dout, ids, grad, workspace, status), "dout ids grad workspace status")
+    if status is not None:
+        _status_word(status)
     T, N, vocab = ids.numel(), dout.shape[-1], int(vocab)
     _int_sizes(ids=T, N=N, vocab=vocab)
     if grad is None:
         if accumulate:
             raise ValueError("accumulate needs the gradient to add to")
-        grad = torch.empty(vocab, N, dtype=torch.float32, device=dev)
+        grad = dout.new_empty((vocab, N), dtype=torch.float32)
     elif grad.dtype != torch.float32 or tuple(grad.shape) != (vocab, N):
         raise ValueError("grad must be float32 [vocab, N]")
     if workspace is None:
-        size = df_embedding_bwd_workspace_size(T, N, vocab)
-        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+        workspace = dout.new_empty(max(df_embedding_bwd_workspace_size(T, N, vocab), 256), dtype=torch.uint8)
     pad = -1 if padding_idx is None else int(padding_idx)
-    _check(_call_on(dev, _lib.df_embedding_bwd, stream, ids.data_ptr(), _ids_64(ids), T, dout.data_ptr(), vocab, N,
+    _check(_call_on(idx, _lib.df_embedding_bwd, stream, ids.data_ptr(), _ids_64(ids), T, dout.data_ptr(), vocab, N,
                     float(scale), pad, 1 if accumulate else 0, grad.data_ptr(), _DTYPE[dout.dtype], _addr(status),
                     workspace.data_ptr(), workspace.numel() * workspace.element_size()), "df_embedding_bwd")
     return grad
@@ -612,10 +616,7 @@ class CrossStats(NamedTuple):
 
 
 def _cross_shape(q, k, v, key_mask, cu_q, cu_k, max_q, max_k):
-    """(device, B, H, Hk, Lq, Lk, total_q, total_k, d) of a cross-attention call."""
-    dev = q.device
-    _on_device(dev, (("q", q), ("k", k), ("v", v), ("key_mask", key_mask), ("cu_seqlens_q", cu_q),
-                     ("cu_seqlens_k", cu_k)))
+    """(B, H, Hk, Lq, Lk, total_q, total_k, d) of a cross-attention call."""
     if q.dtype not in _DTYPE or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must share a dtype: bf16 or fp16")
     qs, ks = q.shape, k.shape
@@ -630,9 +631,9 @@ def _cross_shape(q, k, v, key_mask, cu_q, cu_k, max_q, max_k):
     if key_mask is not None and (cu_k is not None or key_mask.dtype != torch.uint8 or
                                  tuple(key_mask.shape) != (B, Lk)):
         raise ValueError("key_mask must be uint8 [B, Lk], for keys [B, Lk, Hk, d]")
-    if max(Tq, Tk, Lq, Lk) >= 2 ** 31 or min(Lq, Lk) < 0:
+    if Tq >= 2 ** 31 or Tk >= 2 ** 31 or not 0 <= Lq < 2 ** 31 or not 0 <= Lk < 2 ** 31:
         raise ValueError("lengths out of range")
-    return dev, B, qs[-2], ks[-2], Lq, Lk, Tq, Tk, qs[-1]
+    return B, qs[-2], ks[-2], Lq, Lk, Tq, Tk, qs[-1]
 
 
 def _cross_rows(name, cu, shape, longest):
@@ -652,18 +653,19 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
     and values of another length, [B, Lk, Hk, d] (with an optional uint8 key_mask) or
     packed with cu_seqlens_k.  ``scale`` defaults to 1 / sqrt(d).  Returns ``out``, or
     (out, CrossStats) for a training step (``with_stats``)."""
-    dev, B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
-                                                    max_seqlen_k)
+    idx = _on_device((q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, out, status),
+                     "q k v key_mask cu_seqlens_q cu_seqlens_k out status")
+    B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                               max_seqlen_k)
     scale = d ** -0.5 if scale is None else float(scale)
     if out is None:
         out = torch.empty_like(q)
     elif out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must match q in shape and dtype")
-    _on_device(dev, (("out", out), ("status", status)))
-    _status_word(status)
-    stats = CrossStats(torch.empty(q.shape[:-1], dtype=torch.float32, device=dev),
-                       torch.empty_like(q)) if with_stats else None
-    _check(_call_on(dev, _lib.df_cross_attn_fwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask),
+    if status is not None:
+        _status_word(status)
+    stats = CrossStats(q.new_empty(q.shape[:-1], dtype=torch.float32), torch.empty_like(q)) if with_stats else None
+    _check(_call_on(idx, _lib.df_cross_attn_fwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask),
                     _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype],
                     out.data_ptr(), stats.out_lo.data_ptr() if stats else None,
                     stats.lse.data_ptr() if stats else None, _addr(status)), "df_cross_attn_fwd")
@@ -686,28 +688,27 @@ def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=Non
     """Gradients (dq, dk, dv), in the inputs' dtype, of ``df_cross_attn_fwd`` with the
     same arguments; ``out`` and ``stats`` as its call with ``with_stats`` gave them.
     ``grads`` may pass the three tensors preallocated."""
-    dev, B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
-                                                    max_seqlen_k)
-    scale = d ** -0.5 if scale is None else float(scale)
     if grads is None:
         grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
     dq, dk, dv = grads
-    for name, t, like in (("out", out, q), ("out_lo", stats.out_lo, q), ("dout", dout, q), ("dq", dq, q),
-                          ("dk", dk, k), ("dv", dv, v)):
-        if t is None and name == "out_lo":
-            continue
-        if t.dtype != like.dtype or t.shape != like.shape:
+    lse, out_lo = stats
+    idx = _on_device((q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, out, out_lo, lse, dout, dq, dk, dv, workspace, status),
+                     "q k v key_mask cu_seqlens_q cu_seqlens_k out out_lo lse dout dq dk dv workspace status")
+    B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                               max_seqlen_k)
+    scale = d ** -0.5 if scale is None else float(scale)
+    for name, x, like in (("out", out, q), ("out_lo", out_lo, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k),
+                          ("dv", dv, v)):
+        if x is not None and (x.dtype != like.dtype or x.shape != like.shape):
             raise ValueError(f"{name} must match {'q' if like is q else 'k' if like is k else 'v'} in shape and dtype")
-    if stats.lse.dtype != torch.float32 or stats.lse.shape != q.shape[:-1]:
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
         raise ValueError("stats.lse must be float32, [..., H]")
+    if status is not None:
+        _status_word(status)
     if workspace is None:
-        size = df_cross_attn_bwd_workspace_size(Tq, H)
-        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
-    _on_device(dev, (("out", out), ("out_lo", stats.out_lo), ("lse", stats.lse), ("dout", dout), ("dq", dq),
-                     ("dk", dk), ("dv", dv), ("workspace", workspace), ("status", status)))
-    _status_word(status)
-    _check(_call_on(dev, _lib.df_cross_attn_bwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                    _addr(stats.out_lo), stats.lse.data_ptr(), dout.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q),
+        workspace = q.new_empty(max(df_cross_attn_bwd_workspace_size(Tq, H), 256), dtype=torch.uint8)
+    _check(_call_on(idx, _lib.df_cross_attn_bwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                    _addr(out_lo), lse.data_ptr(), dout.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q),
                     _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], dq.data_ptr(),
                     dk.data_ptr(), dv.data_ptr(), _addr(status), workspace.data_ptr(),
                     workspace.numel() * workspace.element_size()), "df_cross_attn_bwd")

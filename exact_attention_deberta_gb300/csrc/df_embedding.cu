@@ -18,12 +18,14 @@
 //      one and are left out.  The sort is latency bound and leaves HBM idle, so
 //      the same launches also zero the table in further blocks (rows that tokens
 //      reach are written again in step 2).
-//   2. sums: a warp takes 32 consecutive entries of the sorted list and 256
-//      columns (8 per lane), adds rows in fp32 while the id stays the same and
-//      writes each finished run.  A run that crosses a 32-entry boundary leaves
-//      one partial row per chunk in the workspace.
+//   2. sums: a warp takes 32 consecutive entries of the sorted list (8 where there
+//      are few) and 256 columns (8 per lane), adds rows in fp32 while the id stays
+//      the same and writes each finished run.  A run that crosses into the next
+//      warp's entries leaves one partial row per warp in the workspace.
 //   3. join: the warp of the chunk in which such a run begins adds its partial
 //      rows in order; long runs are shared by the eight warps of the block.
+// Each launch may be scheduled while the one before it drains (programmatic
+// dependent launch); it waits before its first access to global memory.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -38,7 +40,6 @@ constexpr int kSortThreads = 256;
 constexpr int kSortItems = 8;                           // keys per thread
 constexpr int kSortTile = kSortThreads * kSortItems;    // keys per block
 constexpr int kMaxDigitBits = 10;
-constexpr int kChunk = 32;                              // sorted entries per warp of the sums
 constexpr int kSlice = 256;                             // columns per warp of the sums
 
 template <typename T>
@@ -149,6 +150,12 @@ struct SortArgs {
   size_t fill_begin, fill_end;
 };
 
+// Lets the next launch be scheduled and waits for the previous one.
+__device__ __forceinline__ void start_after_previous() {
+  allow_dependent_launch();
+  grid_dependency_wait();
+}
+
 // A block without sorting work: its share of the zeros.
 __device__ __forceinline__ void fill_share(const SortArgs& a) {
   const size_t step = (size_t)(gridDim.x - a.blocks) * blockDim.x;
@@ -197,6 +204,7 @@ __device__ __forceinline__ uint32_t digit_rank(uint32_t d, bool valid, uint32_t*
 }
 
 __global__ void __launch_bounds__(kSortThreads) digit_counts(const SortArgs a) {
+  start_after_previous();
   if ((int)blockIdx.x >= a.blocks) return fill_share(a);
   __shared__ uint32_t cnt[1 << kMaxDigitBits];
   const int digits = 1 << a.bits;
@@ -220,6 +228,7 @@ __global__ void __launch_bounds__(kSortThreads) digit_counts(const SortArgs a) {
 // 32 digits (lane = digit, so rows of hist are read whole), its eight warps eight
 // ranges of tiles.
 __global__ void __launch_bounds__(256) scan_over_tiles(const SortArgs a) {
+  start_after_previous();
   if ((int)blockIdx.x >= a.blocks) return fill_share(a);
   __shared__ uint32_t sums[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -251,6 +260,7 @@ __global__ void __launch_bounds__(256) scan_over_tiles(const SortArgs a) {
 // [w 256, w 256 + 256) in rounds of 32, so that (warp, round, lane) is the
 // original order.
 __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs a) {
+  start_after_previous();
   if ((int)blockIdx.x >= a.blocks) return fill_share(a);
   constexpr int kWarps = kSortThreads / 32, kPer = (1 << kMaxDigitBits) / kSortThreads;
   __shared__ uint32_t cnt[kWarps][1 << kMaxDigitBits];
@@ -310,6 +320,7 @@ constexpr int kSmallSort = 8192, kSmallBits = 8, kSmallThreads = 1024;
 constexpr size_t kSmallSmem = (size_t)kSmallSort * 8 + 32 * (1 << kSmallBits) * 4 + 128;
 
 __global__ void __launch_bounds__(kSmallThreads) sort_small(const SortArgs a, int passes) {
+  start_after_previous();
   if ((int)blockIdx.x >= a.blocks) return fill_share(a);
   extern __shared__ uint32_t sh[];
   uint32_t* s_key = sh;
@@ -396,18 +407,19 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t v, int c, c
   store8<float>(p, f);
 }
 
-template <typename T>
+template <typename T, int CHUNK>
 __global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __restrict__ dout) {
+  start_after_previous();
   const int lane = threadIdx.x & 31;
   const int chunk = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (chunk >= a.chunks) return;
   const int c = blockIdx.y * kSlice + lane * 8;
   const bool col = c < a.N;
-  const int i0 = chunk * kChunk, cnt = min(kChunk, a.n - i0);
+  const int i0 = chunk * CHUNK, cnt = min(CHUNK, a.n - i0);
   const uint32_t my_key = lane < cnt ? a.key[i0 + lane] : 0xffffffffu;
   const uint32_t my_pos = lane < cnt ? a.pos[i0 + lane] : 0u;
   const uint32_t before = chunk > 0 ? a.key[i0 - 1] : 0xffffffffu;
-  const uint32_t after = i0 + kChunk < a.n ? a.key[i0 + kChunk] : 0xffffffffu;
+  const uint32_t after = i0 + CHUNK < a.n ? a.key[i0 + CHUNK] : 0xffffffffu;
   // entries that pass a gradient stand at the front
   const int live = __popc(__ballot_sync(0xffffffffu, my_key < (uint32_t)a.V));
   if (live == 0) return;
@@ -441,7 +453,7 @@ __global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __rest
     }
   }
   if (col) {
-    const bool on = live == kChunk && after == cur;
+    const bool on = live == CHUNK && after == cur;
     if (head) store8<float>(a.part + (size_t)chunk * 2 * a.N + c, acc);
     else if (on) store8<float>(a.part + ((size_t)chunk * 2 + 1) * a.N + c, acc);
     else write_row(a, cur, c, acc);
@@ -464,7 +476,9 @@ __device__ __forceinline__ void add_partials(const SumArgs& a, int k0, int k1, i
   }
 }
 
+template <int CHUNK>
 __global__ void __launch_bounds__(256) join_runs(const SumArgs a) {
+  start_after_previous();
   __shared__ int s_end[8];
   __shared__ float s_part[8][kSlice];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -475,23 +489,26 @@ __global__ void __launch_bounds__(256) join_runs(const SumArgs a) {
   uint32_t v = 0;
   bool begins = false;
   if (chunk + 1 < a.chunks) {
-    const int i0 = chunk * kChunk;
-    v = a.key[i0 + kChunk - 1];
-    begins = v < (uint32_t)a.V && a.key[i0 + kChunk] == v &&
+    const int i0 = chunk * CHUNK;
+    v = a.key[i0 + CHUNK - 1];
+    begins = v < (uint32_t)a.V && a.key[i0 + CHUNK] == v &&
              !(a.key[i0] == v && chunk > 0 && a.key[i0 - 1] == v);
   }
   int end = 0;  // the first chunk whose first entry lies behind the run
   if (begins) {
-    end = chunk + 2;
-    while (end < a.chunks && end <= chunk + kLongRun && a.key[(size_t)end * kChunk] == v) ++end;
-    if (end < a.chunks && a.key[(size_t)end * kChunk] == v) {
-      int lo = end, hi = a.chunks;  // a.key[lo kChunk] == v, behind hi it is not
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.key[(size_t)mid * kChunk] == v) lo = mid;
-        else hi = mid;
+    auto in_run = [&](int k) { return k < a.chunks && a.key[(size_t)k * CHUNK] == v; };
+    uint32_t m = __ballot_sync(0xffffffffu, in_run(chunk + 2 + lane));
+    end = chunk + 2 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
+    if (m == 0xffffffffu) {
+      int hi = a.chunks;  // chunk end - 1 is in the run, hi is not; 32 probes at a time
+      while (hi - end > 0) {
+        const int step = (hi - end + 31) / 32;
+        const int k = end - 1 + step * (lane + 1);
+        m = __ballot_sync(0xffffffffu, k < hi && in_run(k));
+        const int n = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        end += step * n;
+        hi = min(hi, end - 1 + step);
       }
-      end = hi;
     }
   }
   const bool is_long = begins && end - chunk > kLongRun;
@@ -542,14 +559,17 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct GradLayout {
   size_t key[2], pos[2], hist, digit_total, part, total;
-  int tiles, chunks, bits, passes;
+  int tiles, chunk, chunks, bits, passes;
   bool small;
 };
 
 GradLayout grad_layout(int T, int N, int V) {
   GradLayout l;
   l.tiles = (T + kSortTile - 1) / kSortTile;
-  l.chunks = (T + kChunk - 1) / kChunk;
+  // short chunks spread few tokens over more warps, long ones leave fewer partial
+  // rows (8192 x 1024: 10 us at 32, 5 at 8; 131072 x 768: 50 us at 32)
+  l.chunk = T <= 32768 ? 8 : 32;
+  l.chunks = (T + l.chunk - 1) / l.chunk;
   int key_bits = 1;  // keys 0 .. V
   while (key_bits < 32 && ((unsigned long long)V >> key_bits) != 0) ++key_bits;
   l.small = T <= kSmallSort;
@@ -593,9 +613,31 @@ void launch_lookup(const void* ids, int ids64, int n, const void* table, int V, 
                                                     static_cast<T*>(out), status);
 }
 
+template <typename... Params, typename... Args>
+bool launch_next(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+template <typename T, int CHUNK>
+bool launch_sums(const SumArgs& a, const void* dout, cudaStream_t s) {
+  const dim3 grid((a.chunks + 7) / 8, (a.N + kSlice - 1) / kSlice);
+  return launch_next(sum_runs<T, CHUNK>, grid, 256, 0, s, a, static_cast<const T*>(dout)) &&
+         launch_next(join_runs<CHUNK>, grid, 256, 0, s, a);
+}
+
 template <typename T>
-void launch_sums(const SumArgs& a, const void* dout, dim3 grid, cudaStream_t s) {
-  sum_runs<T><<<grid, 256, 0, s>>>(a, static_cast<const T*>(dout));
+bool launch_sums(const SumArgs& a, int chunk, const void* dout, cudaStream_t s) {
+  return chunk == 8 ? launch_sums<T, 8>(a, dout, s) : launch_sums<T, 32>(a, dout, s);
 }
 
 }  // namespace
@@ -654,15 +696,17 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
   a.status = status;
   a.fill = reinterpret_cast<uint4*>(grad);
   const size_t pieces = accumulate ? 0 : (size_t)V * N / 4;
-  const int launches = l.small ? 1 : 3 * l.passes;
-  int done = 0;
-  // the next launch: its sorting blocks, and blocks that zero its share of the table
-  auto grid_for = [&](int blocks, int threads) {
+  // The launches' shares of the zeros, as long as each takes by itself: 3 : 3 : 5 for
+  // counts, scan and scatter.
+  const size_t unit = pieces / (l.small ? 1 : 11 * (size_t)l.passes) + 1;
+  size_t filled = 0;
+  // the next launch's grid: its sorting blocks, and blocks that zero its share
+  auto grid_for = [&](int blocks, int threads, int share) {
     a.blocks = blocks;
-    a.fill_begin = pieces / launches * done;
-    a.fill_end = ++done == launches ? pieces : pieces / launches * done;
+    a.fill_begin = filled;
+    filled = a.fill_end = std::min(pieces, filled + share * unit);
     const size_t most = (size_t)sm_count() * (2048 / threads);
-    return (unsigned)(blocks + std::min(most, (a.fill_end - a.fill_begin + threads - 1) / threads));
+    return dim3((unsigned)(blocks + std::min(most, (a.fill_end - a.fill_begin + threads - 1) / threads)));
   };
   if (l.small) {
     if (cudaFuncSetAttribute(sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem) != cudaSuccess)
@@ -671,8 +715,8 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
     a.shift = 0;
     a.key_out = reinterpret_cast<uint32_t*>(base + l.key[0]);
     a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[0]);
-    const unsigned grid = grid_for(1, kSmallThreads);
-    sort_small<<<grid, kSmallThreads, kSmallSmem, s>>>(a, l.passes);
+    const dim3 grid = grid_for(1, kSmallThreads, 1);
+    if (!launch_next(sort_small, grid, kSmallThreads, kSmallSmem, s, a, l.passes)) return DF_ERR_CUDA;
   } else {
     for (int p = 0; p < l.passes; ++p) {
       a.first = p == 0;
@@ -681,12 +725,12 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
       a.pos = reinterpret_cast<const uint32_t*>(base + l.pos[(p + 1) & 1]);
       a.key_out = reinterpret_cast<uint32_t*>(base + l.key[p & 1]);
       a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[p & 1]);
-      unsigned grid = grid_for(l.tiles, kSortThreads);
-      digit_counts<<<grid, kSortThreads, 0, s>>>(a);
-      grid = grid_for(((1 << l.bits) + 31) / 32, 256);
-      scan_over_tiles<<<grid, 256, 0, s>>>(a);
-      grid = grid_for(l.tiles, kSortThreads);
-      scatter_by_digit<<<grid, kSortThreads, 0, s>>>(a);
+      dim3 grid = grid_for(l.tiles, kSortThreads, 3);
+      if (!launch_next(digit_counts, grid, kSortThreads, 0, s, a)) return DF_ERR_CUDA;
+      grid = grid_for(((1 << l.bits) + 31) / 32, 256, 3);
+      if (!launch_next(scan_over_tiles, grid, 256, 0, s, a)) return DF_ERR_CUDA;
+      grid = grid_for(l.tiles, kSortThreads, 5);
+      if (!launch_next(scatter_by_digit, grid, kSortThreads, 0, s, a)) return DF_ERR_CUDA;
     }
   }
   SumArgs u;
@@ -700,10 +744,8 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
   u.scale = scale;
   u.part = reinterpret_cast<float*>(base + l.part);
   u.grad = grad;
-  const dim3 grid((l.chunks + 7) / 8, (N + kSlice - 1) / kSlice);
-  if (dtype == DF_BF16) launch_sums<__nv_bfloat16>(u, dout, grid, s);
-  else if (dtype == DF_FP16) launch_sums<__half>(u, dout, grid, s);
-  else launch_sums<float>(u, dout, grid, s);
-  join_runs<<<grid, 256, 0, s>>>(u);
-  return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+  const bool ok = dtype == DF_BF16   ? launch_sums<__nv_bfloat16>(u, l.chunk, dout, s)
+                  : dtype == DF_FP16 ? launch_sums<__half>(u, l.chunk, dout, s)
+                                     : launch_sums<float>(u, l.chunk, dout, s);
+  return ok ? DF_OK : DF_ERR_CUDA;
 }

@@ -9,6 +9,9 @@ the layer's key and query projections of the layer-normalised relative
 embeddings (shared attention keys); disentangled attention (df_attn_fwd,
 packed); the output projection and a residual LayerNorm; the feed-forward
 block (projection with GELU, projection) and a residual LayerNorm.
+``Encoder.embed`` gives the rows that enter the first layer (token embedding and
+LayerNorm), and ``CrossAttention`` is the layer of a decoder or a reader that
+attends to the encoder's states.
 Weights are synthetic (no checkpoint is available): N(0, 0.02) matrices,
 N(0, 0.02) biases, LayerNorm gain 1 and shift 0.
 """
@@ -32,6 +35,7 @@ class EncoderConfig:
     buckets: int = 256
     max_rel: int = 512
     eps: float = 1e-7
+    vocab: int = 0  # rows of the token embeddings; 0: the caller brings hidden rows
 
     @property
     def span(self):
@@ -55,7 +59,23 @@ def synthetic_weights(cfg: EncoderConfig, dtype=torch.bfloat16, device="cuda", s
                    w_1=rnd(f, h), b_1=rnd(f), w_2=rnd(h, f), b_2=rnd(h), ln2_g=ones(h), ln2_b=zeros(h))
               for _ in range(cfg.layers)]
     shared = dict(rel_embeddings=rnd(2 * cfg.span, h), rel_g=ones(h), rel_b=zeros(h))
+    if cfg.vocab:
+        shared.update(word_embeddings=rnd(cfg.vocab, h), emb_g=ones(h), emb_b=zeros(h))
     return layers, shared
+
+
+def synthetic_cross_weights(cfg: EncoderConfig, dtype=torch.bfloat16, device="cuda", seed=0):
+    """Weights of one CrossAttention layer of the encoder's width."""
+    g = torch.Generator().manual_seed(seed)
+
+    def rnd(*shape):
+        return (torch.randn(*shape, generator=g) * 0.02).to(dtype).to(device)
+
+    h = cfg.hidden
+    w = {n: rnd(h, h) for n in ("w_q", "w_k", "w_v", "w_o")}
+    w.update({n: rnd(h) for n in ("b_q", "b_k", "b_v", "b_o")})
+    w.update(ln_g=torch.ones(h, dtype=dtype, device=device), ln_b=torch.zeros(h, dtype=dtype, device=device))
+    return w
 
 
 class Encoder:
@@ -63,6 +83,12 @@ class Encoder:
 
     def __init__(self, cfg: EncoderConfig, layers: List[dict], shared: dict):
         self.cfg, self.layers, self.shared = cfg, layers, shared
+
+    def embed(self, input_ids, stream=None):
+        """Rows [T, hidden] of packed token ids [T]: their embeddings, normalised."""
+        sh = self.shared
+        rows = binding.df_embedding(input_ids, sh["word_embeddings"], stream=stream)
+        return binding.df_layernorm(rows, sh["emb_g"], sh["emb_b"], eps=self.cfg.eps, stream=stream)
 
     def __call__(self, hidden, cu_seqlens, max_seqlen, stream=None, trace=None):
         """``trace``: an optional list; each layer appends a dict of the tensors
@@ -94,3 +120,32 @@ class Encoder:
             (f2,) = binding.df_linear(f, [p["w_2"]], [p["b_2"]], stream=stream)
             h = binding.df_layernorm(f2, p["ln2_g"], p["ln2_b"], residual=h1, eps=cfg.eps, stream=stream)
         return h
+
+
+class CrossAttention:
+    """A layer that attends to an encoder's packed states: projections, cross
+    attention, output projection, residual LayerNorm.
+
+    ``project`` gives the states' keys and values once; a program that generates
+    keeps them and calls ``attend`` with one row per sequence."""
+
+    def __init__(self, cfg: EncoderConfig, weights: dict):
+        self.cfg, self.w = cfg, weights
+
+    def project(self, states, stream=None):
+        """states [T, hidden] -> k, v, each [T, heads, hidden / heads]."""
+        w, H = self.w, self.cfg.heads
+        outs = binding.df_linear(states, [w["w_k"], w["w_v"]], [w["b_k"], w["b_v"]], stream=stream)
+        return [o.view(states.shape[0], H, self.cfg.hidden // H) for o in outs]
+
+    def attend(self, x, k, v, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k, stream=None):
+        """x [Tq, hidden], packed by cu_seqlens_q, against the keys and values of the same
+        sequences, packed by cu_seqlens_k -> [Tq, hidden]."""
+        w, cfg = self.w, self.cfg
+        T, hid = x.shape
+        (q,) = binding.df_linear(x, [w["w_q"]], [w["b_q"]], stream=stream)
+        ctx = binding.df_cross_attn_fwd(q.view(T, cfg.heads, hid // cfg.heads), k, v, cu_seqlens_q=cu_seqlens_q,
+                                        max_seqlen_q=max_seqlen_q, cu_seqlens_k=cu_seqlens_k,
+                                        max_seqlen_k=max_seqlen_k, stream=stream)
+        (o,) = binding.df_linear(ctx.view(T, hid), [w["w_o"]], [w["b_o"]], stream=stream)
+        return binding.df_layernorm(o, w["ln_g"], w["ln_b"], residual=x, eps=cfg.eps, stream=stream)
