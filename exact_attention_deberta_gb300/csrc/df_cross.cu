@@ -84,6 +84,8 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
   if (!cu_k && (long long)B * Lk != total_k) return DF_ERR_INVALID_ARG;
   if (dtype == DF_FP32 || d % 8 != 0 || d > 128 || H / Hk > 128) return DF_ERR_UNSUPPORTED;
   if (total_q > (1 << 30) || total_k > (1 << 30)) return DF_ERR_UNSUPPORTED;
+  // a grid has a CTA for every tile
+  if ((long long)Hk * ((long long)std::max(total_q, total_k) + B + 1) > 0x7fffffffll) return DF_ERR_UNSUPPORTED;
   if ((total_q > 0 && !q) || (total_k > 0 && (!k || !v))) return DF_ERR_INVALID_ARG;
   if (!al16(q) || !al16(k) || !al16(v) || ((uintptr_t)cu_q & 3u) != 0 || ((uintptr_t)cu_k & 3u) != 0)
     return DF_ERR_ALIGNMENT;
@@ -142,7 +144,7 @@ extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void*
   const int key_tiles = (Lk + kFwdKeys - 1) / kFwdKeys;
   while (a.splits < 8 && items * a.splits * 2 <= sms && a.splits * 2 <= key_tiles) a.splits *= 2;
   a.split_bits = a.splits == 8 ? 3 : a.splits / 2;
-  const int grid = a.splits > 1 ? (int)items * a.splits : (int)std::min<long long>(items, sms);
+  const int grid = (int)items * a.splits;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = d <= 64 ? launch_cross64(a, maps, bf16, grid, s) : launch_cross128(a, maps, bf16, grid, s);
   return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;

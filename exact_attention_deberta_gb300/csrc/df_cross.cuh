@@ -10,6 +10,8 @@
 // maps end a row at d, and a copy fills the columns behind it with zeros.
 #pragma once
 
+#include <limits.h>
+
 #include <atomic>
 
 #include "df_tc_common.cuh"
@@ -147,8 +149,8 @@ __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
 // Finds the tiles of one side by number, warp-collectively.  Tiles of `step`
 // tokens are numbered by sequence, then key head, then position; in packed mode
 // the rows behind the last sequence count as one more sequence, whose other
-// side is empty.  Numbers must not decrease from call to call (the walk over the
-// sequences never goes back).
+// side is empty.  The walk over the sequences goes on from the last call's number
+// and starts over for a smaller one.
 struct TileWalk {
   int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones
   long long done = 0;  // tiles of the sequences before b0
@@ -160,6 +162,11 @@ struct TileWalk {
     CrossItem it;
     it.hk = -1;
     it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    if (number < 0) return it;
+    if (number < done) {
+      b0 = 0;
+      done = 0;
+    }
     for (; b0 <= last; b0 += 32) {
       const int b = b0 + lane;
       int start = 0, n = 0;
@@ -195,6 +202,45 @@ struct TileWalk {
       done += total;
     }
     return it;
+  }
+};
+
+// Work for the next turn of a CTA.  The grid has a CTA for every tile; one that
+// runs takes over the number of one that has not been launched yet (cluster launch
+// control), so that tiles of unequal cost spread evenly without a counter in
+// memory, which concurrent calls and replayed graphs would have to share.
+struct TileClaim {
+  uint64_t* bar;    // one arrival
+  uint4* response;  // 16 bytes of shared memory
+  uint32_t asked = 0;
+
+  // One thread; nothing may be asked again once an answer was -1.
+  __device__ __forceinline__ void ask() {
+    ptx::mbar_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     ptx::smem_u32(response)),
+                 "r"(ptx::smem_u32(bar))
+                 : "memory");
+    ++asked;
+  }
+  // The tile number taken over, or -1 when none is left.
+  __device__ __forceinline__ long long answer(unsigned long long budget, volatile int* abort, int32_t* status) {
+    const bool ok = cross_wait(bar, (asked - 1) & 1, budget, abort, status);
+    // (the response must not be written into a CTA that has left)
+    if (!ok) ptx::mbar_wait(bar, (asked - 1) & 1, kDrainBudget);
+    uint32_t taken, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}\n"
+        : "=r"(taken), "=r"(x)
+        : "r"(ptx::smem_u32(response))
+        : "memory");
+    ptx::fence_proxy_async_smem();  // this read before the next response's write
+    return ok && taken ? (long long)x : -1;
   }
 };
 

@@ -57,11 +57,12 @@ struct FwdSmem {
   static constexpr uint32_t mj = mx + 2 * 4 * 128 * 4;              // float4 [128]: a cluster's (max, sum)
   static constexpr uint32_t bars = mj + 128 * 16;
   // q_full, q_empty [2]; k_full, k_empty, v_full, v_ready, v_empty [2][kStages];
-  // s_full, p_full, exp_done, o_final, drain [2]; item_full, item_empty
-  static constexpr int kBars = 4 + 10 * kStages + 10 + 2 * (int)kItemRing;
+  // s_full, p_full, exp_done, o_final, drain [2]; item_full, item_empty; claim
+  static constexpr int kBars = 4 + 10 * kStages + 10 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax threads' current item
-  static constexpr uint32_t misc = cur + 32;                        // abort flag, tmem slot
+  static constexpr uint32_t claim = cur + 32;                       // 16 bytes
+  static constexpr uint32_t misc = claim + 16;                      // abort flag, tmem slot
   static constexpr uint32_t bytes = misc + 16;
   static constexpr uint32_t alloc = bytes + 1024;
   static_assert(alloc <= 232448, "shared memory of one CTA");
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   uint64_t* drain = o_final + 2;
   uint64_t* item_full = drain + 2;
   uint64_t* item_empty = item_full + kItemRing;
+  uint64_t* claim_bar = item_empty + kItemRing;
   auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
   CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SL::misc);
@@ -128,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       mbar_init(item_full + b, 1);
       mbar_init(item_empty + b, kItemReaders);
     }
+    mbar_init(claim_bar, 1);
     *s_abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&maps.q);
@@ -168,13 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<kOtherRegs>();
     TileWalk walk;
+    TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t kn0 = 0, kn1 = 0, vn0 = 0, vn1 = 0;  // tiles loaded for each team
     uint32_t qc = 0;
     bool failed = false;                      // a wait ran out: nothing is loaded after it
     int mask_b = -1, mask_n = 0;  // the last masked row measured
-    const int clusters = gridDim.x / args.splits, first = blockIdx.x / args.splits;
+    long long number = blockIdx.x / args.splits;
     for (uint32_t c = 0;; ++c) {
-      CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, (long long)first + (long long)c * clusters);
+      CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, number);
       const uint32_t slot = c % kItemRing;
       bool ok = true;
       if (a.key_mask && it.hk >= 0) {  // key tiles behind the last valid key are not visited
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         }
         int t0;
         const int nt = it.hk < 0 ? 0 : part(it, &t0);
+        if (it.hk >= 0 && nt == 0 && args.splits == 1) claim.ask();
         if (nt > 0) {
           const uint32_t qb = qc % kQBufs;
           failed = failed || !cross_wait(q_empty + qb, ((qc / kQBufs) & 1) ^ 1, budget, s_abort, status);
@@ -202,10 +207,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
           }
           // K(t + 2) goes out behind V(t), before V(t + 1): in the order in which
           // the products free their stages
+          // The next item is asked for two tiles before this one's end: early enough to be
+          // answered by then, late enough to leave it to a CTA that is through sooner.
+          const int first_ask = args.splits > 1 ? INT_MAX : max(-2, 2 * nt - 4);
 #pragma unroll 1
           for (int j = -2; j < 2 * nt; ++j) {
             const bool is_v = j >= 0 && (j & 1) == 0;
             const int t = j < 0 ? j + 2 : is_v ? j / 2 : j / 2 + 2;
+            if (j == first_ask) claim.ask();
             if (t >= nt || failed) continue;
             const int w = t & 1;
             const uint32_t n = is_v ? (w ? vn1 : vn0) : (w ? kn1 : kn0);
@@ -227,6 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         }
       }
       if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
+      if (lane == 0) number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
+      number = __shfl_sync(0xffffffffu, number, 0);
     }
     if (lane == 0) {
       // no copy may still be landing when the CTA leaves

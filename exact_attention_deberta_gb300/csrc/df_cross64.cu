@@ -50,11 +50,12 @@ struct FwdSmem {
   static constexpr uint32_t ml = v + kStages * kTileBytes;          // float4 [2 warpgroups, a cluster's][128]
   static constexpr uint32_t bars = ml + 3 * 128 * 16;
   // q_full, q_empty [2]; k_full, k_empty, v_full, v_empty [kStages]; s_full,
-  // buf_free, drain [3]; p_full [4]; item_full, item_empty
-  static constexpr int kBars = 4 + 4 * kStages + 9 + 4 + 2 * (int)kItemRing;
+  // buf_free, drain [3]; p_full [4]; item_full, item_empty; claim
+  static constexpr int kBars = 4 + 4 * kStages + 9 + 4 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax warpgroups' current item
-  static constexpr uint32_t misc = cur + 32;                        // abort flag, tmem slot
+  static constexpr uint32_t claim = cur + 32;                       // 16 bytes
+  static constexpr uint32_t misc = claim + 16;                      // abort flag, tmem slot
   static constexpr uint32_t bytes = misc + 16;
   static constexpr uint32_t alloc = bytes + 1024;
   static_assert(alloc <= 232448, "shared memory of one CTA");
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
   uint64_t* p_full = drain + 3;
   uint64_t* item_full = p_full + 4;
   uint64_t* item_empty = item_full + kItemRing;
+  uint64_t* claim_bar = item_empty + kItemRing;
   auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
   CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SL::misc);
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       mbar_init(item_full + b, 1);
       mbar_init(item_empty + b, kItemReaders);
     }
+    mbar_init(claim_bar, 1);
     *s_abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&maps.q);
@@ -156,12 +159,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<56>();
     TileWalk walk;
+    TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, qc = 0, k_issued = 0, v_issued = 0;
     int mask_b = -1, mask_n = 0;  // the last masked row measured
     bool failed = false;          // a wait ran out: nothing is loaded after it
-    const int clusters = gridDim.x / args.splits, first = blockIdx.x / args.splits;
+    long long number = blockIdx.x / args.splits;
     for (uint32_t c = 0;; ++c) {
-      CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, (long long)first + (long long)c * clusters);
+      CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, number);
       const uint32_t slot = c % kItemRing;
       bool ok = true;
       if (a.key_mask && it.hk >= 0) {  // key tiles behind the last valid key are not visited
@@ -178,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         }
         int t0;
         const int nt = it.hk < 0 ? 0 : part(it, &t0);
+        if (it.hk >= 0 && nt == 0 && args.splits == 1) claim.ask();
         if (nt > 0) {
           const uint32_t qb = qc & 1;
           failed = failed || !cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort, status);
@@ -188,10 +193,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
           }
           // K(t + 1) goes out before V(t): the next scores must not wait until P.V has
           // freed a V tile
+          // The next item is asked for two tiles before this one's end: early enough to be
+          // answered by then, late enough to leave it to a CTA that is through sooner.
+          const int first_ask = args.splits > 1 ? INT_MAX : max(0, 2 * nt - 4);
 #pragma unroll 1
           for (int j = 0; j <= 2 * nt; ++j) {
             const bool is_v = j > 0 && (j & 1) == 0;
             const int t = is_v ? j / 2 - 1 : (j + 1) / 2;
+            if (j == first_ask) claim.ask();
             if (t >= nt || failed) continue;
             const uint32_t gs = g + t, s = gs % R;
             if (!cross_wait((is_v ? v_empty : k_empty) + s, ((gs / R) & 1) ^ 1, budget, s_abort, status)) {
@@ -209,6 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         }
       }
       if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
+      if (lane == 0) number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
+      number = __shfl_sync(0xffffffffu, number, 0);
     }
     if (lane == 0) {
       // no copy may still be landing when the CTA leaves

@@ -126,11 +126,12 @@ struct BwdSmem {
   static constexpr uint32_t bars = col + kStages * 1024;
   // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full, ds_free,
   // p_free [3];
-  // acc_full, acc_free; drain [4]; item_full, item_empty
-  static constexpr int kBars = 2 * kRes + 3 * kStages + 12 + 6 + 2 * (int)kItemRing;
+  // acc_full, acc_free; drain [4]; item_full, item_empty; claim
+  static constexpr int kBars = 2 * kRes + 3 * kStages + 12 + 6 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t cur = ring + 32 * kItemRing;
-  static constexpr uint32_t misc = cur + 32;
+  static constexpr uint32_t claim = cur + 32;  // 16 bytes
+  static constexpr uint32_t misc = claim + 16;
   static constexpr uint32_t bytes = misc + 16;
   static constexpr uint32_t alloc = bytes + 1024;
   static_assert(alloc <= 232448, "shared memory of one CTA");
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   uint64_t* drain = acc_free + 1;      // [4], one per issuing thread
   uint64_t* item_full = drain + 4;
   uint64_t* item_empty = item_full + kItemRing;
+  uint64_t* claim_bar = item_empty + kItemRing;
   auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
   CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SL::misc);
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       mbar_init(item_full + b, 1);
       mbar_init(item_empty + b, kItemReaders);
     }
+    mbar_init(claim_bar, 1);
     *s_abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&maps.x0);
@@ -239,12 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<kOtherRegs>();
     TileWalk walk;
+    TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, xc = 0, g_issued = 0, x_issued = 0;
     const uint32_t q_box = (uint32_t)(a.G * a.tpt) * 128u;  // bytes of a 64-column box of a query tile
     const uint32_t x_box = KEYS ? kBoxBytes : q_box, y_box = KEYS ? q_box : kBoxBytes;
+    long long number = blockIdx.x;
     for (uint32_t c = 0;; ++c) {
-      CrossItem it = walk.find(a, KEYS ? key_side(a) : query_side(a), KEYS ? query_side(a) : key_side(a), x_step,
-                               (long long)blockIdx.x + (long long)c * gridDim.x);
+      CrossItem it = walk.find(a, KEYS ? key_side(a) : query_side(a), KEYS ? query_side(a) : key_side(a), x_step, number);
       if (lane == 0) {
         const uint32_t slot = c % kItemRing;
         bool ok = true;
@@ -255,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           mbar_arrive(item_full + slot);
         }
         const int nt = it.hk < 0 ? 0 : y_tiles(it);
+        if (it.hk >= 0 && nt == 0) claim.ask();
         if (nt > 0) {
           const int x_head = KEYS ? it.hk : it.hk * a.G, y_head = KEYS ? it.hk * a.G : it.hk;
           const uint32_t xb = xc % kRes;
@@ -268,7 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
             x_issued = xc + 1;
           }
           ++xc;
+          // the next item is asked for two tiles before this one's end
+          const int ask_at = max(0, nt - 2);
           for (int t = 0; t < nt; ++t, ++g) {
+            if (t == ask_at) claim.ask();
             const uint32_t s = g % kStages;
             if (cross_wait(empty + s, ((g / kStages) & 1) ^ 1, budget, s_abort, status)) {
               uint8_t* dst = sm + SL::y + s * 2 * SL::kTileBytes;
@@ -284,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         }
       }
       if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
+      if (lane == 0) number = claim.answer(budget, s_abort, status);
+      number = __shfl_sync(0xffffffffu, number, 0);
     }
     if (lane == 0) {
       // no copy may still be landing when the CTA leaves
@@ -622,7 +632,7 @@ cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items,
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kRegs, &done);
   if (e != cudaSuccess) return e;
-  kernel<<<(int)std::min<long long>(items, device_sms()), kThreads, bytes, s>>>(a, maps);
+  kernel<<<(unsigned)items, kThreads, bytes, s>>>(a, maps);
   return cudaGetLastError();
 }
 

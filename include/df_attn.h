@@ -496,7 +496,7 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  * workspace; equal inputs give equal bits.
  * Errors: DF_ERR_INVALID_ARG (NULL pointer, sizes, H % Hk, scale, key_mask with
  * cu_seqlens_k, dtype), DF_ERR_UNSUPPORTED (fp32, d, H / Hk > 128, over 2^30
- * rows), DF_ERR_ALIGNMENT (tensors 16 bytes, lse and cu_seqlens 4), DF_ERR_CUDA. */
+ * rows, over 2^31 rows times key heads), DF_ERR_ALIGNMENT (tensors 16 bytes, lse and cu_seqlens 4), DF_ERR_CUDA. */
 df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
                             const uint8_t* key_mask, const int32_t* cu_seqlens_q,
                             const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
