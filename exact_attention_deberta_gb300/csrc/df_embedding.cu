@@ -62,7 +62,7 @@ struct Raw8 {
   uint4 v[sizeof(T) / 2];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = __ldg(reinterpret_cast<const uint4*>(p) + e);
+    for (int e = 0; e < (int)sizeof(T) / 2; ++e) v[e] = reinterpret_cast<const uint4*>(p)[e];
   }
   __device__ __forceinline__ void add_to(float (&acc)[8]) const {
     const T* h = reinterpret_cast<const T*>(v);
@@ -408,7 +408,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t v, int c, c
 }
 
 template <typename T, int CHUNK>
-__global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __restrict__ dout) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) sum_runs(const SumArgs a, const T* dout) {
   start_after_previous();
   const int lane = threadIdx.x & 31;
   const int chunk = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -463,21 +463,23 @@ __global__ void __launch_bounds__(256) sum_runs(const SumArgs a, const T* __rest
 // Runs longer than this many chunks are added by the block's eight warps together.
 constexpr int kLongRun = 16;
 
-// Sum of the partial rows of chunks [k0, k1), eight loads in flight.
+// Sum of the partial rows of chunks [k0, k1), four loads in flight (eight would
+// halve the resident warps, and most runs are short).
 __device__ __forceinline__ void add_partials(const SumArgs& a, int k0, int k1, int c, float (&acc)[8]) {
-  for (int k = k0; k < k1; k += 8) {
-    Raw8<float> f[8];
+#pragma unroll 1
+  for (int k = k0; k < k1; k += 4) {
+    Raw8<float> f[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u = 0; u < 4; ++u)
       if (k + u < k1) f[u].load(a.part + (size_t)(k + u) * 2 * a.N + c);
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u = 0; u < 4; ++u)
       if (k + u < k1) f[u].add_to(acc);
   }
 }
 
 template <int CHUNK>
-__global__ void __launch_bounds__(256) join_runs(const SumArgs a) {
+__global__ void __launch_bounds__(256, 4) join_runs(const SumArgs a) {
   start_after_previous();
   __shared__ int s_end[8];
   __shared__ float s_part[8][kSlice];
