@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const float f1 = s2.x != -INFINITY ? ex2(s2.x - m) : 0.f;
       const float l = (s0.y + s1.y) * f0 + (s2.y + s3.y) * f1;
       const bool alone = args.splits == 1;
-      const float inv = !alone ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      const float inv = !alone ? 1.f : (l != 0.f ? 1.f / l : 0.f);
       const size_t orow = (size_t)(it.r0 + row_tok) * a.H + (size_t)it.hk * a.G + (row - row_tok * a.G);
       float* sO = reinterpret_cast<float*>(sm + SL::k);  // a cluster's join: K and V are idle by then
       if (warp_in) {
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       if (!alone) {
         if (group == 0) sJoin[row] = make_float4(m, l, 0.f, 0.f);
       } else if (args.lse && group == 0 && row_in && *s_abort == 0) {
-        args.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        args.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
       tc_fence_before();
       named_sync(9, kSoftmaxThreads);  // every thread has read s_cur and sML

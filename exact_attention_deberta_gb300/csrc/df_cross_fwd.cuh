@@ -98,23 +98,23 @@ __device__ __forceinline__ void join_cluster(const FwdArgs& args, const CrossIte
     for (int r = 0; r < args.splits; ++r) {
       const float4 s = ld_cluster(map_rank(ml_addr + 16 * row, r));
       const float f = m != -INFINITY ? ex2(s.x - m) : 0.f;
+      l += s.y * f;  // (NaN even where f is 0)
       if (f > 0.f) {
         const float4 v = ld_cluster(map_rank(o_addr + 4 * o_piece<D>(row, piece), r));
-        l += s.y * f;
         o[0] += v.x * f;
         o[1] += v.y * f;
         o[2] += v.z * f;
         o[3] += v.w * f;
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] *= inv;
     const size_t orow = (size_t)(it.r0 + tok) * a.H + (size_t)it.hk * a.G + (row - tok * a.G);
     const size_t at = orow * a.d + 4 * piece;
     store_rounded<T, 4>(static_cast<T*>(args.out) + at, args.out_lo ? static_cast<T*>(args.out_lo) + at : nullptr,
                         o);
-    if (args.lse && piece == 0) args.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (args.lse && piece == 0) args.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 

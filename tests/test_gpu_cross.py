@@ -101,6 +101,41 @@ def test_rows_behind_the_last_sequence_and_empty_sequences(lib):
     assert int((got[:150] != 0).sum()) == 0  # queries of a sequence without keys
 
 
+@pytest.mark.parametrize("B,d,Lq,Lk", [(2, 64, 40, 2000), (40, 64, 40, 300), (2, 128, 40, 2000), (40, 128, 40, 300)])
+def test_nan_that_counts_stays_in_its_rows(lib, B, d, Lq, Lk):
+    # few query tiles (clusters) and many; a query row of NaN, and one NaN key of one sequence
+    x = inputs(B, 4, 4, d, Lq, Lk, BF, seed=11)
+    dev = to_dev(x)
+    clean = call(lib, x, dev)
+    dev["q"][0, 7, 2] = float("nan")
+    dev["k"][1, Lk - 1, 1, 0] = float("nan")
+    got, stats = call(lib, x, dev, with_stats=True)
+    bad = torch.zeros(got.shape[:3], dtype=torch.bool, device="cuda")
+    bad[0, 7, 2] = True
+    bad[1, :, 1] = True
+    assert bool(got[bad].isnan().all()) and bool(stats.lse[bad].isnan().all())
+    assert torch.equal(got[~bad], clean[~bad])
+
+
+def test_two_calls_at_once(lib):
+    # on two streams, each with its own tiles to hand out
+    xs = [inputs(24, 4, 4, 64, 150, 700, BF, "packed", "packed", seed=s) for s in (1, 2)]
+    devs = [to_dev(x) for x in xs]
+    alone = [call(lib, x, dev) for x, dev in zip(xs, devs)]
+    outs = [[torch.empty_like(dev["q"]) for _ in range(10)] for dev in devs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(10):
+        for x, dev, out, s in zip(xs, devs, outs, streams):
+            with torch.cuda.stream(s):
+                call(lib, x, dev, out=out[i], status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == lib.DF_OK
+    assert all(torch.equal(o, a) for out, a in zip(outs, alone) for o in out)
+
+
 def test_no_keys_no_queries_no_sequences(lib):
     z = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")  # noqa: E731
     out, stats = lib.df_cross_attn_fwd(z(2, 3, 4, 64), z(2, 0, 4, 64), z(2, 0, 4, 64), with_stats=True)
