@@ -101,8 +101,9 @@ __global__ void __launch_bounds__(256) row_stats(const T* __restrict__ out, cons
     stat[row] = make_float2(v == -INFINITY ? INFINITY : v * kLog2e, sum);
   }
   if (top) {
-    // rows outside every sequence do not count; neither does what is not finite
-    bool in = mine && n2 <= 3.0e38f;
+    // rows outside every sequence or without a valid key do not count (their dS is 0);
+    // neither does what is not finite
+    bool in = mine && n2 <= 3.0e38f && lse[row] != -INFINITY;
     if (in && cu_q) {
       const long long tok = row / H;
       in = tok >= cu_q[0] && tok < cu_q[B];
@@ -247,8 +248,20 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     const uint32_t q_box = (uint32_t)(a.G * a.tpt) * 128u;  // bytes of a 64-column box of a query tile
     const uint32_t x_box = KEYS ? kBoxBytes : q_box, y_box = KEYS ? q_box : kBoxBytes;
     long long number = blockIdx.x;
+    int mask_b = -1, mask_n = 0;  // the last masked row measured
     for (uint32_t c = 0;; ++c) {
       CrossItem it = walk.find(a, KEYS ? key_side(a) : query_side(a), KEYS ? query_side(a) : key_side(a), x_step, number);
+      if (a.key_mask && it.hk >= 0) {
+        // nothing is streamed past 128 keys that do not count, and no keys behind the
+        // last one that does
+        if (KEYS) {
+          if (masked_length(a.key_mask + it.r0, it.nr) == 0) it.no = 0;
+        } else {
+          if (it.b != mask_b) mask_n = masked_length(a.key_mask + (size_t)it.b * a.Lk, it.no);
+          mask_b = it.b;
+          it.no = mask_n;
+        }
+      }
       if (lane == 0) {
         const uint32_t slot = c % kItemRing;
         bool ok = true;

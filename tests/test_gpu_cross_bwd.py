@@ -126,6 +126,44 @@ def test_rows_behind_the_last_sequence_and_empty_sequences(lib, dtype):
     check_backward((dq[:Tq], dk[:Tk], dv[:Tk]), w, dtype, 64)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_key_tiles_without_a_valid_key(lib, d):
+    # masks with holes that span whole tiles of 128 keys, at either end and inside
+    x = inputs(3, 4, 2, d, 140, 700, BF, "padded", "masked", seed=d + 1, nk=[700, 300, 700])
+    x["key_mask"][0, 120:400] = 0
+    x["key_mask"][2, :600] = 0
+    got = _step(lib, x, to_dev(x))
+    check_backward(got, want(oracle, x, d ** -0.5, with_grad=True), BF, d)
+
+
+def test_large_gradient_of_a_row_without_keys(lib):
+    # it does not set the scale that the other rows' small gradients are held at: dS of
+    # 2^-12 dout next to 2^15 would be below fp16's subnormals
+    x = inputs(2, 2, 2, 64, 70, 200, HF, "padded", "masked", seed=3, nk=[200, 0])
+    x["dout"][0] = (x["dout"][0].float() * 2.0 ** -12).to(HF)
+    x["dout"][1] = 2.0 ** 15
+    w = want(oracle, x, 0.125, with_grad=True)
+    check_backward(_step(lib, x, to_dev(x)), w, HF, 64)
+
+
+def test_two_calls_at_once(lib):
+    xs = [inputs(12, 4, 2, 128, 150, 300, HF, "packed", "packed", seed=s) for s in (1, 2)]
+    devs = [to_dev(x) for x in xs]
+    fwd = [call(lib, x, dev, with_stats=True) for x, dev in zip(xs, devs)]
+    alone = [call_bwd(lib, x, dev, *f) for x, dev, f in zip(xs, devs, fwd)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call_bwd(lib, xs[i], devs[i], *fwd[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for grads in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(grads, alone[i]))
+
+
 def test_no_keys_no_queries(lib):
     z = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")  # noqa: E731
     for Lq, Lk, B in ((3, 0, 2), (0, 9, 2), (0, 0, 2), (3, 9, 0)):
