@@ -130,6 +130,41 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, const uint32_t (&bits)[
   ptx::fence_proxy_async_smem();
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  return BF16 ? ptx::pack_bf16x2(x, y) : ptx::pack_f16x2(x, y);
+}
+
+// A warp's 32 rows of results, 32 columns each (16 words, packed), one row per
+// thread, to memory: row by row a store would touch 32 lines 16 bytes at a time,
+// so the rows change hands through 1 KB of shared memory of the warp's own (16
+// rows at a time) and go out as 64 bytes each.  `rel` is the thread's row (-1: not
+// stored) behind `dst`, the first column of row 0; `left` columns exist from there
+// on.
+constexpr int kRowStage = 1024;
+template <typename T>
+__device__ __forceinline__ void store_rows32(uint8_t* stage, const uint32_t (&w)[16], int rel, T* dst, int d, int left) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if ((lane >> 4) == half) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(stage + (lane & 15) * 64 + 16 * (e ^ ((lane >> 1) & 3))) =
+            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + 16 * (c ^ ((r >> 1) & 3)));
+      const int to = __shfl_sync(0xffffffffu, rel, 16 * half + r);
+      if (to >= 0 && 8 * c < left) *reinterpret_cast<uint4*>(dst + (size_t)to * d + 8 * c) = v;
+    }
+    __syncwarp();
+  }
+}
+
 // Keys of a masked row up to its last valid one (warp-collective).
 __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
   const int lane = threadIdx.x & 31;

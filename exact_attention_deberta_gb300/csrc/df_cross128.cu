@@ -55,7 +55,8 @@ struct FwdSmem {
   static constexpr uint32_t ml = v + 2 * kStages * kTileBytes;      // float2 (max, sum) [4 warpgroups][128]
   static constexpr uint32_t mx = ml + 4 * 128 * 8;                  // float [2 tiles][4 warpgroups][128]: row maxima
   static constexpr uint32_t mj = mx + 2 * 4 * 128 * 4;              // float4 [128]: a cluster's (max, sum)
-  static constexpr uint32_t bars = mj + 128 * 16;
+  static constexpr uint32_t stage = mj + 128 * 16;                  // [16 warps] rows on their way out
+  static constexpr uint32_t bars = stage + 16 * kRowStage;
   // q_full, q_empty [2]; k_full, k_empty, v_full, v_ready, v_empty [2][kStages];
   // s_full, p_full, exp_done, o_final, drain [2]; item_full, item_empty; claim
   static constexpr int kBars = 4 + 10 * kStages + 10 + 2 * (int)kItemRing + 1;
@@ -69,6 +70,54 @@ struct FwdSmem {
   // the join of a cluster: O [128][D] fp32 over the (then idle) K and V tiles
   static_assert(128 * D * 4 <= 4 * kStages * kTileBytes, "O fits over K and V");
 };
+
+// 32 columns of a warp's rows from the two teams' O: o = (a fa + b fb) inv (an O of
+// factor 0 may hold anything), rounded, and (out_lo) what that rounding dropped.
+template <bool BF16, typename T>
+__device__ __forceinline__ void store_merged(const FwdArgs& args, uint8_t* stage, uint32_t ta, uint32_t tb, float fa,
+                                             float fb, float inv, int rel, size_t row0, int col) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint32_t ra[16], rb[16];
+    tmem_ld16(ta + 16 * s, ra);
+    tmem_ld16(tb + 16 * s, rb);
+    tmem_ld_wait(ra);
+    tmem_ld_wait(rb);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float o[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        o[k] = ((fa > 0.f ? __uint_as_float(ra[2 * e + k]) * fa : 0.f) +
+                (fb > 0.f ? __uint_as_float(rb[2 * e + k]) * fb : 0.f)) * inv;
+      const uint32_t h = pack2<BF16>(o[0], o[1]);
+      const T* t = reinterpret_cast<const T*>(&h);
+      hi[8 * s + e] = h;
+      lo[8 * s + e] = pack2<BF16>(o[0] - IO<T>::to_f(t[0]), o[1] - IO<T>::to_f(t[1]));
+    }
+  }
+  const size_t at = row0 * args.c.d + col;
+  store_rows32<T>(stage, hi, rel, static_cast<T*>(args.out) + at, args.c.d, args.c.d - col);
+  if (args.out_lo) store_rows32<T>(stage, lo, rel, static_cast<T*>(args.out_lo) + at, args.c.d, args.c.d - col);
+}
+
+// One step of 16 columns of one row, not rounded, for a cluster's join.
+__device__ __forceinline__ void keep_merged(float* dst, uint32_t ta, uint32_t tb, float fa, float fb, int row, int col) {
+  uint32_t ra[16], rb[16];
+  tmem_ld16(ta, ra);
+  tmem_ld16(tb, rb);
+  tmem_ld_wait(ra);
+  tmem_ld_wait(rb);
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    float o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = (fa > 0.f ? __uint_as_float(ra[e + k]) * fa : 0.f) + (fb > 0.f ? __uint_as_float(rb[e + k]) * fb : 0.f);
+    *reinterpret_cast<float4*>(dst + o_piece<FwdSmem::D>(row, (col + e) / 4)) = make_float4(o[0], o[1], o[2], o[3]);
+  }
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs args, const __grid_constant__ FwdMaps maps) {
@@ -360,7 +409,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     const float2 ks2 = make_float2(ks, ks);
     const uint32_t tSw = tS(wg) + lane_off + (kKeys / 2) * half;  // this thread's scores, and its P
     const uint32_t tOw = tO(wg) + lane_off + (D / 2) * half;
-    const int row_tok = row / a.G;
     uint32_t n = 0, other_n = 0, ic = 0;  // tiles of this and the other team, items with a tile of this one
     // One thread takes each item from the ring and leaves it in s_cur; all 512 read
     // it behind their barrier, so that they run the same list even after a wait
@@ -374,10 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       if (it.hk < 0) break;
       int t0;
       const int nt = part(it, &t0);
-      const bool row_in = row_tok < it.nr;
       // a row block without a valid row needs no weights: its P may hold anything,
       // since a row of P only reaches its own row of O
-      const bool warp_in = __any_sync(0xffffffffu, row_in);
+      const bool warp_in = __any_sync(0xffffffffu, row / a.G < it.nr);
       float m_run = -INFINITY, l_run = 0.f;  // l_run: this thread's columns only
       bool o_has = false;
       // The teams take turns at the exponentials, in the order of the tiles: left
@@ -495,42 +542,29 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const float l = (s0.y + s1.y) * f0 + (s2.y + s3.y) * f1;
       const bool alone = args.splits == 1;
       const float inv = !alone ? 1.f : (l != 0.f ? 1.f / l : 0.f);
-      const size_t orow = (size_t)(it.r0 + row_tok) * a.H + (size_t)it.hk * a.G + (row - row_tok * a.G);
-      float* sO = reinterpret_cast<float*>(sm + SL::k);  // a cluster's join: K and V are idle by then
-      if (warp_in) {
-        // each of a row's four threads writes a quarter of its columns
+      // (what only the results' places need is formed again here: held over the loop
+      // above, it would spill there)
+      const CrossItem end = *s_cur;
+      uint32_t tid;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+      const int end_row = tid & 127, end_tok = end_row / a.G;
+      const size_t row0 = (size_t)end.r0 * a.H + (size_t)end.hk * a.G;
+      const int rel = end_tok < end.nr && *s_abort == 0 ? end_tok * a.H + end_row - end_tok * a.G : -1;
+      const int c0 = (((int)tid - 128) >> 7) * (D / 4);  // each of a row's four threads writes a quarter of its columns
+      const uint32_t ta = tO(0) + ((tid & 96u) << 16), tb = ta + 256u;
+      if (alone) {
+        if (warp_in && c0 < a.d)
+          store_merged<BF16, T>(args, sm + SL::stage + ((tid >> 5) - 4) * kRowStage, ta + c0, tb + c0, f0, f1, inv,
+                                      rel, row0, c0);
+        if (args.lse && c0 == 0 && rel >= 0) args.lse[row0 + rel] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      } else {
+        float* sO = reinterpret_cast<float*>(sm + SL::k);  // K and V are idle by then
+        if (warp_in) {
 #pragma unroll 1
-        for (int col = group * (D / 4); col < (group + 1) * (D / 4); col += 16) {
-          uint32_t ra[16], rb[16];
-          tmem_ld16(tO(0) + lane_off + col, ra);
-          tmem_ld16(tO(1) + lane_off + col, rb);
-          tmem_ld_wait(ra);
-          tmem_ld_wait(rb);
-          if (!row_in || *s_abort != 0) continue;
-#pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            float o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              o[k] = ((f0 > 0.f ? __uint_as_float(ra[e + k]) * f0 : 0.f) +
-                      (f1 > 0.f ? __uint_as_float(rb[e + k]) * f1 : 0.f)) * inv;
-            if (!alone) {
-#pragma unroll
-              for (int k = 0; k < 8; k += 4)
-                *reinterpret_cast<float4*>(sO + o_piece<D>(row, (col + e + k) / 4)) =
-                    make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-            } else if (col + e < a.d) {
-              const size_t at = orow * a.d + col + e;
-              store_rounded<T, 8>(static_cast<T*>(args.out) + at,
-                                  args.out_lo ? static_cast<T*>(args.out_lo) + at : nullptr, o);
-            }
-          }
+          for (int col = c0; col < c0 + D / 4; col += 16)
+            keep_merged(sO, ta + col, tb + col, f0, f1, end_row, col);
         }
-      }
-      if (!alone) {
-        if (group == 0) sJoin[row] = make_float4(m, l, 0.f, 0.f);
-      } else if (args.lse && group == 0 && row_in && *s_abort == 0) {
-        args.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (c0 == 0) sJoin[end_row] = make_float4(m, l, 0.f, 0.f);
       }
       tc_fence_before();
       named_sync(9, kSoftmaxThreads);  // every thread has read s_cur and sML

@@ -124,7 +124,8 @@ struct BwdSmem {
   static constexpr uint32_t x = 0;                                   // [kRes][X0 | X1]
   static constexpr uint32_t y = x + kRes * 2 * kTileBytes;           // [kStages][Y0 | Y1]
   static constexpr uint32_t col = y + kStages * 2 * kTileBytes;      // [kStages]: float -lse [128], -D [128]; or 4 mask words
-  static constexpr uint32_t bars = col + kStages * 1024;
+  static constexpr uint32_t stage = col + kStages * 1024;            // [8 warps] rows on their way out
+  static constexpr uint32_t bars = stage + 8 * kRowStage;
   // x_full, x_empty [kRes]; full, ready, empty [kStages]; s_full, p_full, ds_free,
   // p_free [3];
   // acc_full, acc_free; drain [4]; item_full, item_empty; claim
@@ -596,27 +597,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       __syncwarp();
       tc_fence_after();
       const int heads = KEYS ? a.Hk : a.H;
-      const size_t orow = (size_t)(it.r0 + row_tok) * heads + (KEYS ? it.hk : it.hk * a.G + row_head);
+      const size_t row0 = (size_t)it.r0 * heads + (KEYS ? it.hk : it.hk * a.G);
+      const int rel = stored && *s_abort == 0 ? row_tok * heads + row_head : -1;
       // KEYS: warpgroup 0 writes dk, 1 dv; else each half of dq's columns
       const uint32_t tA = (KEYS && h == 1 ? tAcc1 : tAcc0) + lane_off;
-      T* dst = static_cast<T*>(KEYS && h == 1 ? args.out1 : args.out0) + orow * a.d;
+      T* dst = static_cast<T*>(KEYS && h == 1 ? args.out1 : args.out0) + row0 * a.d;
       const float mul = KEYS && h == 1 ? scale1 : scale0;
       const int c0 = KEYS ? 0 : h * (D / 2), c1 = KEYS ? D : c0 + D / 2;
 #pragma unroll 1
-      for (int cc = c0; cc < c1; cc += 32) {
-        uint32_t r[32];
+      for (int cc = c0; cc < min(c1, a.d); cc += 32) {
+        uint32_t r[32], w[16];
         tmem_ld32(tA + cc, r);
         tmem_ld_wait(r);
-        if (stored && *s_abort == 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (cc + e >= a.d) break;
-            __align__(16) T v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = IO<T>::from_f(nt > 0 ? __uint_as_float(r[e + k]) * mul : 0.f);
-            *reinterpret_cast<uint4*>(dst + cc + e) = *reinterpret_cast<const uint4*>(v);
-          }
-        }
+        for (int e = 0; e < 16; ++e)
+          w[e] = nt > 0 ? pack2<BF16>(__uint_as_float(r[2 * e]) * mul, __uint_as_float(r[2 * e + 1]) * mul) : 0u;
+        store_rows32<T>(sm + SL::stage + (warp - kFirst) * kRowStage, w, rel, dst + cc, a.d, a.d - cc);
       }
       tc_fence_before();
       __syncwarp();
