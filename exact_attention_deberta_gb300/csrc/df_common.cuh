@@ -202,7 +202,7 @@ __device__ __forceinline__ void allow_dependent_launch() {
 
 // Launches `kernel` on `s` with the programmatic-serialisation attribute: it
 // may start while the kernel before it on the stream is still running, and
-// must call grid_dependency_wait() before it touches global memory.
+// must call grid_dependency_wait() before it touches what that one writes.
 template <typename... Params, typename... Args>
 cudaError_t launch_after_plan(void (*kernel)(Params...), int grid, int threads, size_t smem,
                               cudaStream_t s, Args... args) {

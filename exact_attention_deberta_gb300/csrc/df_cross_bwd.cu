@@ -58,6 +58,7 @@ struct BwdArgs {
   const uint32_t* top;     // fp16: the largest |dout_i|^2, as bits
   void* out0;              // dk or dq
   void* out1;              // dv
+  int after_keys;          // the key tiles' launch is the one before
 };
 
 struct BwdMaps {
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(256) row_stats(const T* __restrict__ out, cons
                                                  const T* __restrict__ dout, const float* __restrict__ lse, int d,
                                                  long long rows, const int32_t* cu_q, int B, int H,
                                                  float2* __restrict__ stat, uint32_t* top) {
+  allow_dependent_launch();
   const long long row = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int l = threadIdx.x & 15;
   float sum = 0.f, n2 = 0.f;
@@ -220,6 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  // Keys: row_stats has finished; once every CTA stands here (and so none is left to
+  // be launched), those of the query tiles may take the SMs that run dry.  They need
+  // nothing that the key tiles write, only the end of their launch before their own.
+  if (KEYS || !args.after_keys) grid_dependency_wait();
+  if (KEYS) allow_dependent_launch();
   const uint32_t tAcc0 = tmem, tAcc1 = tmem + D;
   auto tS = [&](uint32_t b) { return tmem + kAccCols + 128u * b; };
   auto tdP = [&](uint32_t b) { return tmem + kAccCols + 128u * b + 64u; };
@@ -631,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (!KEYS && args.after_keys) grid_dependency_wait();
 }
 
 template <int D, bool BF16, bool KEYS>
@@ -641,8 +649,7 @@ cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items,
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kRegs, &done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)items, kThreads, bytes, s>>>(a, maps);
-  return cudaGetLastError();
+  return launch_after_plan(kernel, (int)items, kThreads, bytes, s, a, maps);
 }
 
 template <int D, bool BF16>
@@ -650,7 +657,9 @@ cudaError_t launch_both(BwdArgs a, const BwdMaps& km, const BwdMaps& qm, void* d
                         cudaStream_t s) {
   const long long key_items = a.c.cu_k ? ((long long)a.c.Tk / 128 + a.c.B + 1) * a.c.Hk
                                        : (long long)((a.c.Lk + 127) / 128) * a.c.B * a.c.Hk;
-  if (a.c.Tk > 0) {
+  a.after_keys = 0;
+  if (a.c.Tk > 0 && key_items > 0) {
+    a.after_keys = 1;
     a.out0 = dk;
     a.out1 = dv;
     const cudaError_t e = launch_tiles<D, BF16, true>(a, km, key_items, s);
