@@ -249,13 +249,16 @@ struct TileClaim {
   uint4* response;  // 16 bytes of shared memory
   uint32_t asked = 0;
 
-  // One thread; nothing may be asked again once an answer was -1.
+  // (both for a converged warp) Nothing may be asked again once an answer was -1.
   __device__ __forceinline__ void ask() {
-    ptx::mbar_expect_tx(bar, 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                     ptx::smem_u32(response)),
-                 "r"(ptx::smem_u32(bar))
-                 : "memory");
+    if (ptx::elect_one()) {
+      ptx::mbar_expect_tx(bar, 16);
+      asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                       ptx::smem_u32(response)),
+                   "r"(ptx::smem_u32(bar))
+                   : "memory");
+    }
+    __syncwarp();
     ++asked;
   }
   // The tile number taken over, or -1 when none is left.
@@ -275,7 +278,8 @@ struct TileClaim {
         : "r"(ptx::smem_u32(response))
         : "memory");
     ptx::fence_proxy_async_smem();  // this read before the next response's write
-    return ok && taken ? (long long)x : -1;
+    const bool mine = __all_sync(0xffffffffu, ok) && taken;
+    return mine ? (long long)x : -1;
   }
 };
 

@@ -45,21 +45,20 @@ struct FwdSmem {
   static constexpr int kChunks = D / 64;
   static constexpr int kKeys = kFwdKeys;
   static constexpr int kQBufs = 2;   // Q tiles in flight
-  static constexpr int kStages = 1;  // K tiles, and V tiles, of each team in flight
   static constexpr uint32_t kQBytes = kChunks * kBoxBytes;
   static constexpr uint32_t kKVBox = kKeys * 128;                   // a 64-column box of a key tile
   static constexpr uint32_t kTileBytes = kChunks * kKVBox;
   static constexpr uint32_t q = 0;                                  // [kQBufs][Q tile]
-  static constexpr uint32_t k = q + kQBufs * kQBytes;               // [2 teams][kStages][K tile]
-  static constexpr uint32_t v = k + 2 * kStages * kTileBytes;       // the same of V
-  static constexpr uint32_t ml = v + 2 * kStages * kTileBytes;      // float2 (max, sum) [4 warpgroups][128]
+  static constexpr uint32_t k = q + kQBufs * kQBytes;               // [2 teams][K tile]
+  static constexpr uint32_t v = k + 2 * kTileBytes;       // the same of V
+  static constexpr uint32_t ml = v + 2 * kTileBytes;      // float2 (max, sum) [4 warpgroups][128]
   static constexpr uint32_t mx = ml + 4 * 128 * 8;                  // float [2 tiles][4 warpgroups][128]: row maxima
   static constexpr uint32_t mj = mx + 2 * 4 * 128 * 4;              // float4 [128]: a cluster's (max, sum)
   static constexpr uint32_t stage = mj + 128 * 16;                  // [16 warps] rows on their way out
   static constexpr uint32_t bars = stage + 16 * kRowStage;
-  // q_full, q_empty [2]; k_full, k_empty, v_full, v_ready, v_empty [2][kStages];
+  // q_full, q_empty [2]; k_full, k_empty, v_full, v_ready, v_empty [2];
   // s_full, p_full, exp_done, o_final, drain [2]; item_full, item_empty; claim
-  static constexpr int kBars = 4 + 10 * kStages + 10 + 2 * (int)kItemRing + 1;
+  static constexpr int kBars = 24 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax threads' current item
   static constexpr uint32_t claim = cur + 32;                       // 16 bytes
@@ -68,7 +67,7 @@ struct FwdSmem {
   static constexpr uint32_t alloc = bytes + 1024;
   static_assert(alloc <= 232448, "shared memory of one CTA");
   // the join of a cluster: O [128][D] fp32 over the (then idle) K and V tiles
-  static_assert(128 * D * 4 <= 4 * kStages * kTileBytes, "O fits over K and V");
+  static_assert(128 * D * 4 <= 4 * kTileBytes, "O fits over K and V");
 };
 
 // 32 columns of a warp's rows from the two teams' O: o = (a fa + b fb) inv (an O of
@@ -124,7 +123,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   using SL = FwdSmem;
   constexpr int D = SL::D;
   constexpr int kChunks = SL::kChunks;
-  constexpr uint32_t S = SL::kStages;
   constexpr int kKeys = SL::kKeys, kWords = kKeys / 32;
   constexpr uint32_t kQBufs = SL::kQBufs;
   constexpr uint32_t kIdescQK = idesc_f16(128, kKeys, BF16 ? 1 : 0, 0, 0);
@@ -144,12 +142,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SL::bars);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 2;
-  uint64_t* k_full = bars + 4;          // [team][stage], as the next four
-  uint64_t* k_empty = k_full + 2 * S;
-  uint64_t* v_full = k_empty + 2 * S;
-  uint64_t* v_ready = v_full + 2 * S;   // landed, rows that do not count zeroed
-  uint64_t* v_empty = v_ready + 2 * S;
-  uint64_t* s_full = v_empty + 2 * S;   // [team], as the next four: S computed
+  uint64_t* k_full = bars + 4;          // [team], as the next four
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
+  uint64_t* v_ready = v_full + 2;   // landed, rows that do not count zeroed
+  uint64_t* v_empty = v_ready + 2;
+  uint64_t* s_full = v_empty + 2;   // [team], as the next four: S computed
   uint64_t* p_full = s_full + 2;        // its eight warps have stored P
   uint64_t* exp_done = p_full + 2;     // its eight warps are through with a tile's exponentials
   uint64_t* o_final = exp_done + 2;     // every P.V of the item done
@@ -174,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       mbar_init(o_final + b, 1);
       mbar_init(drain + b, 1);
     }
-    for (uint32_t s = 0; s < 10 * S; ++s) mbar_init(k_full + s, 1);
+    for (uint32_t s = 0; s < 10; ++s) mbar_init(k_full + s, 1);
     for (uint32_t b = 0; b < kItemRing; ++b) {
       mbar_init(item_full + b, 1);
       mbar_init(item_empty + b, kItemReaders);
@@ -196,8 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   const uint32_t tmem = *tslot;
   auto tS = [&](int w) { return tmem + 256u * w; };
   auto tO = [&](int w) { return tmem + 256u * w + kKeys; };
-  // stage of a team's n-th tile
-  auto stage = [&](int w, uint32_t n) { return (uint32_t)w * S + n % S; };
 
   const unsigned long long budget = a.budget;
   int32_t* status = a.status;
@@ -219,150 +215,159 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   if (warp == 0) {
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<kOtherRegs>();
+    // (the whole warp runs every step, and one lane of it issues)
     TileWalk walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t kn0 = 0, kn1 = 0, vn0 = 0, vn1 = 0;  // tiles loaded for each team
     uint32_t qc = 0;
-    bool failed = false;                      // a wait ran out: nothing is loaded after it
     int mask_b = -1, mask_n = 0;  // the last masked row measured
+    bool ok = true;               // a wait ran out: nothing is loaded after it
     long long number = blockIdx.x / args.splits;
+    // K or V rows [row, row + 128) for a team, its n-th tile
+    auto load = [&](const CUtensorMap* map, uint32_t tiles, uint64_t* full, uint64_t* empty, int w, uint32_t& n, int head,
+                    int row) {
+      ok = ok && cross_wait(empty + w, (n & 1) ^ 1, budget, s_abort, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (elect_one()) {
+        uint8_t* dst = sm + tiles + w * SL::kTileBytes;
+        mbar_expect_tx(full + w, SL::kTileBytes);
+        for (int ch = 0; ch < kChunks; ++ch) tma_load_3d(dst + ch * SL::kKVBox, map, ch * 64, head, row, full + w);
+      }
+      __syncwarp();
+      ++n;
+    };
     for (uint32_t c = 0;; ++c) {
       CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, number);
       const uint32_t slot = c % kItemRing;
-      bool ok = true;
       if (a.key_mask && it.hk >= 0) {  // key tiles behind the last valid key are not visited
         if (it.b != mask_b) mask_n = masked_length(a.key_mask + (size_t)it.b * a.Lk, it.no);
         mask_b = it.b;
         it.no = mask_n;
       }
-      if (lane == 0) {
-        if (c >= kItemRing) ok = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
-        if (*s_abort || !ok) it.hk = -1;
+      bool room = true;
+      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+      if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
+      if (lane == 0 && room) {
+        *ring_slot(c) = it;
+        mbar_arrive(item_full + slot);
+      }
+      if (it.hk < 0) break;
+      int t0;
+      const int nt = part(it, &t0);
+      if (nt > 0) {
+        const uint32_t qb = qc % kQBufs;
+        ok = ok && cross_wait(q_empty + qb, ((qc / kQBufs) & 1) ^ 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
         if (ok) {
-          *ring_slot(c) = it;
-          mbar_arrive(item_full + slot);
-        }
-        int t0;
-        const int nt = it.hk < 0 ? 0 : part(it, &t0);
-        if (it.hk >= 0 && nt == 0 && args.splits == 1) claim.ask();
-        if (nt > 0) {
-          const uint32_t qb = qc % kQBufs;
-          failed = failed || !cross_wait(q_empty + qb, ((qc / kQBufs) & 1) ^ 1, budget, s_abort, status);
-          if (!failed) {
+          if (elect_one()) {
             mbar_expect_tx(q_full + qb, kChunks * (uint32_t)(a.G * a.tpt) * 128u);
             for (int ch = 0; ch < kChunks; ++ch)
               tma_load_3d(sQ + qb * SL::kQBytes + ch * kBoxBytes, &maps.q, ch * 64, it.hk * a.G, it.r0, q_full + qb);
-            ++qc;
           }
-          // K(t + 2) goes out behind V(t), before V(t + 1): in the order in which
-          // the products free their stages
-          // The next item is asked for two tiles before this one's end: early enough to be
-          // answered by then, late enough to leave it to a CTA that is through sooner.
-          const int first_ask = args.splits > 1 ? INT_MAX : max(-2, 2 * nt - 4);
-#pragma unroll 1
-          for (int j = -2; j < 2 * nt; ++j) {
-            const bool is_v = j >= 0 && (j & 1) == 0;
-            const int t = j < 0 ? j + 2 : is_v ? j / 2 : j / 2 + 2;
-            if (j == first_ask) claim.ask();
-            if (t >= nt || failed) continue;
-            const int w = t & 1;
-            const uint32_t n = is_v ? (w ? vn1 : vn0) : (w ? kn1 : kn0);
-            const uint32_t s = stage(w, n);
-            if (!cross_wait((is_v ? v_empty : k_empty) + s, ((n / S) & 1) ^ 1, budget, s_abort, status)) {
-              failed = true;
-              continue;
-            }
-            uint64_t* f = (is_v ? v_full : k_full) + s;
-            uint8_t* dst = sm + (is_v ? SL::v : SL::k) + s * SL::kTileBytes;
-            mbar_expect_tx(f, SL::kTileBytes);
-            for (int ch = 0; ch < kChunks; ++ch)
-              tma_load_3d(dst + ch * SL::kKVBox, is_v ? &maps.v : &maps.k, ch * 64, it.hk, it.o0 + (t0 + t) * kKeys, f);
-            kn0 += !is_v && !w;
-            kn1 += !is_v && w;
-            vn0 += is_v && !w;
-            vn1 += is_v && w;
-          }
+          __syncwarp();
+          ++qc;
         }
       }
-      if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
-      if (lane == 0) number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
-      number = __shfl_sync(0xffffffffu, number, 0);
+      // K(t + 2) goes out behind V(t), before V(t + 1): in the order in which the
+      // products free their stages.
+      // The next item is asked for two tiles before this one's end: early enough to be
+      // answered by then, late enough to leave it to a CTA that is through sooner.
+      const int ask_at = args.splits > 1 ? INT_MAX : max(-2, nt - 2);
+      const int row0 = it.o0 + t0 * kKeys;
+#pragma unroll 1
+      for (int t = -2; t < max(nt, -1); ++t) {
+        const int w = t & 1;
+        if (t == ask_at) claim.ask();
+        if (t >= 0) load(&maps.v, SL::v, v_full, v_empty, w, w ? vn1 : vn0, it.hk, row0 + t * kKeys);
+        if (t + 2 < nt) load(&maps.k, SL::k, k_full, k_empty, w, w ? kn1 : kn0, it.hk, row0 + (t + 2) * kKeys);
+      }
+      number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
     }
-    if (lane == 0) {
-      // no copy may still be landing when the CTA leaves
-#pragma unroll 1
+    // no copy may still be landing when the CTA leaves
+    if (elect_one()) {
       for (int w = 0; w < 2; ++w) {
-#pragma unroll 1
-        for (uint32_t n = w ? kn1 : kn0, i = 0; i < S && n > 0; ++i, --n)
-          mbar_wait(k_full + stage(w, n - 1), ((n - 1) / S) & 1, kDrainBudget);
-#pragma unroll 1
-        for (uint32_t n = w ? vn1 : vn0, i = 0; i < S && n > 0; ++i, --n)
-          mbar_wait(v_full + stage(w, n - 1), ((n - 1) / S) & 1, kDrainBudget);
+        const uint32_t kn = w ? kn1 : kn0, vn = w ? vn1 : vn0;
+        if (kn > 0) mbar_wait(k_full + w, (kn - 1) & 1, kDrainBudget);
+        if (vn > 0) mbar_wait(v_full + w, (vn - 1) & 1, kDrainBudget);
       }
 #pragma unroll 1
       for (uint32_t n = qc > kQBufs ? qc - kQBufs : 0; n < qc; ++n)
         mbar_wait(q_full + n % kQBufs, (n / kQBufs) & 1, kDrainBudget);
     }
+    __syncwarp();
   } else if (warp < 3) {
     // ------------------------------------------------------------ MMA issuers
     setmaxnreg_dec<kOtherRegs>();
-    if (lane == 0) {
-      const int wg = warp - 1;        // the team whose tiles (t = wg, wg + 2, ...) this thread multiplies
-      uint32_t qc = 0, kn = 0, vn = 0;
-      const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sm + SL::k), v_addr = smem_u32(sm + SL::v);
-      const uint32_t ts = tS(wg), to = tO(wg);
-      bool ok = true;                 // a wait that ran out ends this thread's products
-      for (uint32_t c = 0;; ++c) {
-        const CrossItem it = read_item(c);
-        if (it.hk < 0) break;
-        int t0;
-        const int nt = part(it, &t0);
-        if (nt == 0) continue;
-        const uint32_t qb = qc % kQBufs;
-        ok = ok && cross_wait(q_full + qb, (qc / kQBufs) & 1, budget, s_abort, status);
-        const uint64_t dq = sdesc_sw128(q_addr + qb * SL::kQBytes, 16, 1024);
-        ++qc;
-        // (P(t) overwrote its S: QK(t + 2) stands behind P(t).V in this thread's order)
-        auto issue_qk = [&]() {
-          const uint32_t s = stage(wg, kn);
-          ok = ok && cross_wait(k_full + s, (kn / S) & 1, budget, s_abort, status);
-          ++kn;
-          if (!ok) return;
-          const uint64_t dk = sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024);
-          tc_fence_after();
+    const int wg = warp - 1;        // the team whose tiles (t = wg, wg + 2, ...) this warp multiplies
+    uint32_t qc = 0, kn = 0, vn = 0;
+    const uint32_t q_addr = smem_u32(sQ);
+    const uint32_t ts = uniform(tS(wg)), to = uniform(tO(wg));
+    const uint64_t dk = uniform(sdesc_sw128(smem_u32(sm + SL::k + wg * SL::kTileBytes), 16, 1024));
+    const uint64_t dv = uniform(sdesc_sw128(smem_u32(sm + SL::v + wg * SL::kTileBytes), SL::kKVBox, 1024));
+    bool ok = true;                 // a wait that ran out ends this warp's products
+    for (uint32_t c = 0;; ++c) {
+      CrossItem it;
+      if (lane == 0) it = read_item(c);
+      it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
+      if (it.hk < 0) break;
+      it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      int t0;
+      const int nt = part(it, &t0);
+      if (nt == 0) continue;
+      const uint32_t qb = qc % kQBufs;
+      ok = ok && cross_wait(q_full + qb, (qc / kQBufs) & 1, budget, s_abort, status);
+      const uint64_t dq = uniform(sdesc_sw128(q_addr + qb * SL::kQBytes, 16, 1024));
+      ++qc;
+      // (P(t) overwrote its S: QK(t + 2) stands behind P(t).V in this warp's order)
+      auto issue_qk = [&]() {
+        ok = ok && cross_wait(k_full + wg, kn & 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
+        ++kn;
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ss(ts, dq + kmajor_step(k), dk + (((k >> 2) * SL::kKVBox + (k & 3) * 32) >> 4), kIdescQK, k > 0);
           mma_commit(s_full + wg);
-          mma_commit(k_empty + s);
-        };
-        if (wg < nt) issue_qk();
+          mma_commit(k_empty + wg);
+        }
+        __syncwarp();
+      };
+      if (wg < nt) issue_qk();
 #pragma unroll 1
-        for (int t = wg; t < nt; t += 2) {
-          const uint32_t s = stage(wg, vn);
-          ok = ok && cross_wait(v_ready + s, (vn / S) & 1, budget, s_abort, status);
-          ok = ok && cross_wait(p_full + wg, vn & 1, budget, s_abort, status);
-          ++vn;
-          if (ok) {
-            const uint64_t dv = sdesc_sw128(v_addr + s * SL::kTileBytes, SL::kKVBox, 1024);
-            tc_fence_after();
+      for (int t = wg; t < nt; t += 2) {
+        ok = ok && cross_wait(v_ready + wg, vn & 1, budget, s_abort, status);
+        ok = ok && cross_wait(p_full + wg, vn & 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
+        ++vn;
+        if (ok) {
+          const uint32_t first = uniform(t >= 2 ? 1u : 0u);
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(to, ts + 8 * k + (k >= kKeys / 32 ? kKeys / 4 : 0), dv + vtile_step(k), kIdescPV,
-                     (k > 0 || t >= 2) ? 1u : 0u);
-            mma_commit(v_empty + s);
+              mma_ts(to, ts + 8 * k + (k >= kKeys / 32 ? kKeys / 4 : 0), dv + vtile_step(k), kIdescPV, k > 0 ? 1u : first);
+            mma_commit(v_empty + wg);
           }
-          if (t + 2 < nt) issue_qk();
+          __syncwarp();
         }
-        if (ok) {
-          // (a team without a tile waits for nothing here: its issuer may be items ahead)
-          if (wg < nt) mma_commit(o_final + wg);
-          mma_commit(q_empty + qb);
-        }
+        if (t + 2 < nt) issue_qk();
       }
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && elect_one()) {
+        // (a team without a tile waits for nothing here: its issuer may be items ahead)
+        if (wg < nt) mma_commit(o_final + wg);
+        mma_commit(q_empty + qb);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(drain + wg);
       mbar_wait(drain + wg, 0, kDrainBudget);
     }
+    __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------------ V tiles
     setmaxnreg_dec<kOtherRegs>();
@@ -380,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
         const int w = t & 1;
-        const uint32_t n = w ? vn1 : vn0, s = stage(w, n);
+        const uint32_t n = w ? vn1 : vn0;
         vn0 += !w;
         vn1 += w;
         const int left = it.no - (t0 + t) * kKeys;
@@ -388,11 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         bool whole = left >= kKeys && !a.key_mask;
         if (!whole)
           whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * kKeys : nullptr, left, bits);
-        ok = ok && cross_wait(v_full + s, (n / S) & 1, budget, s_abort, status);
+        ok = ok && cross_wait(v_full + w, n & 1, budget, s_abort, status);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok && !whole) zero_rows<kWords, kChunks>(sm + SL::v + s * SL::kTileBytes, bits);
+        if (ok && !whole) zero_rows<kWords, kChunks>(sm + SL::v + w * SL::kTileBytes, bits);
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(v_ready + s);
+        if (ok && lane == 0) mbar_arrive(v_ready + w);
       }
     }
   } else {

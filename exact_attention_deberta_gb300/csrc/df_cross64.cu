@@ -158,71 +158,76 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
   if (warp == 0) {
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<56>();
+    // (the whole warp runs every step, and one lane of it issues: this loop's length
+    // in instructions is what a tile's period comes down to)
     TileWalk walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, qc = 0, k_issued = 0, v_issued = 0;
     int mask_b = -1, mask_n = 0;  // the last masked row measured
-    bool failed = false;          // a wait ran out: nothing is loaded after it
+    bool ok = true;               // a wait ran out: nothing is loaded after it
     long long number = blockIdx.x / args.splits;
+    // K or V rows [row, row + 128) into stage s
+    auto load = [&](const CUtensorMap* map, uint32_t tiles, uint64_t* full, uint64_t* empty, uint32_t gs, int head, int row,
+                    uint32_t& issued) {
+      const uint32_t s = gs % R;
+      ok = ok && cross_wait(empty + s, ((gs / R) & 1) ^ 1, budget, s_abort, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (elect_one()) {
+        mbar_expect_tx(full + s, SL::kTileBytes);
+        tma_load_3d(sm + tiles + s * SL::kTileBytes, map, 0, head, row, full + s);
+      }
+      __syncwarp();
+      issued = gs + 1;
+    };
     for (uint32_t c = 0;; ++c) {
       CrossItem it = walk.find(a, query_side(a), key_side(a), a.tpt, number);
       const uint32_t slot = c % kItemRing;
-      bool ok = true;
       if (a.key_mask && it.hk >= 0) {  // key tiles behind the last valid key are not visited
         if (it.b != mask_b) mask_n = masked_length(a.key_mask + (size_t)it.b * a.Lk, it.no);
         mask_b = it.b;
         it.no = mask_n;
       }
-      if (lane == 0) {
-        if (c >= kItemRing) ok = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
-        if (*s_abort || !ok) it.hk = -1;
+      bool room = true;
+      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+      if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
+      if (lane == 0 && room) {
+        *ring_slot(c) = it;
+        mbar_arrive(item_full + slot);
+      }
+      if (it.hk < 0) break;
+      int t0;
+      const int nt = part(it, &t0);
+      if (nt > 0) {
+        const uint32_t qb = qc & 1;
+        ok = ok && cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
         if (ok) {
-          *ring_slot(c) = it;
-          mbar_arrive(item_full + slot);
-        }
-        int t0;
-        const int nt = it.hk < 0 ? 0 : part(it, &t0);
-        if (it.hk >= 0 && nt == 0 && args.splits == 1) claim.ask();
-        if (nt > 0) {
-          const uint32_t qb = qc & 1;
-          failed = failed || !cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort, status);
-          if (!failed) {
+          if (elect_one()) {
             mbar_expect_tx(q_full + qb, (uint32_t)(a.G * a.tpt) * 128u);
             tma_load_3d(sQ + qb * SL::kTileBytes, &maps.q, 0, it.hk * a.G, it.r0, q_full + qb);
-            ++qc;
           }
-          // K(t + 1) goes out before V(t): the next scores must not wait until P.V has
-          // freed a V tile
-          // The next item is asked for two tiles before this one's end: early enough to be
-          // answered by then, late enough to leave it to a CTA that is through sooner.
-          const int first_ask = args.splits > 1 ? INT_MAX : max(0, 2 * nt - 4);
-#pragma unroll 1
-          for (int j = 0; j <= 2 * nt; ++j) {
-            const bool is_v = j > 0 && (j & 1) == 0;
-            const int t = is_v ? j / 2 - 1 : (j + 1) / 2;
-            if (j == first_ask) claim.ask();
-            if (t >= nt || failed) continue;
-            const uint32_t gs = g + t, s = gs % R;
-            if (!cross_wait((is_v ? v_empty : k_empty) + s, ((gs / R) & 1) ^ 1, budget, s_abort, status)) {
-              failed = true;
-              continue;
-            }
-            uint64_t* f = (is_v ? v_full : k_full) + s;
-            mbar_expect_tx(f, SL::kTileBytes);
-            tma_load_3d(sm + (is_v ? SL::v : SL::k) + s * SL::kTileBytes, is_v ? &maps.v : &maps.k, 0, it.hk,
-                        it.o0 + (t0 + t) * 128, f);
-            if (is_v) v_issued = gs + 1;
-            else k_issued = gs + 1;
-          }
-          g += nt;
+          __syncwarp();
+          ++qc;
         }
       }
-      if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
-      if (lane == 0) number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
-      number = __shfl_sync(0xffffffffu, number, 0);
+      // K(t) goes out before V(t - 1): the next scores must not wait until P.V has
+      // freed a V tile.
+      // The next item is asked for two tiles before this one's end: early enough to be
+      // answered by then, late enough to leave it to a CTA that is through sooner.
+      const int ask_at = args.splits > 1 ? -1 : max(0, nt - 2);
+      const int row0 = it.o0 + t0 * 128;
+#pragma unroll 1
+      for (int t = 0; t <= nt; ++t) {
+        if (t == ask_at) claim.ask();
+        if (t < nt) load(&maps.k, SL::k, k_full, k_empty, g + t, it.hk, row0 + t * 128, k_issued);
+        if (t > 0) load(&maps.v, SL::v, v_full, v_empty, g + t - 1, it.hk, row0 + t * 128 - 128, v_issued);
+      }
+      g += nt;
+      number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
     }
-    if (lane == 0) {
-      // no copy may still be landing when the CTA leaves
+    // no copy may still be landing when the CTA leaves
+    if (elect_one()) {
 #pragma unroll 1
       for (uint32_t n = k_issued > R ? k_issued - R : 0; n < k_issued; ++n)
         mbar_wait(k_full + n % R, (n / R) & 1, kDrainBudget);
@@ -232,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
 #pragma unroll 1
       for (uint32_t n = qc > 2 ? qc - 2 : 0; n < qc; ++n) mbar_wait(q_full + (n & 1), (n >> 1) & 1, kDrainBudget);
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------ MMA issuers
     // (whole warps, so that the one that issues a P.V can zero rows of V first)
@@ -252,26 +258,29 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       const int nt = part(it, &t0);
       if (nt == 0) continue;
       if (qk_role) {
-        if (lane == 0) {
-          const uint32_t qb = qc & 1;
-          ok = ok && cross_wait(q_full + qb, (qc >> 1) & 1, budget, s_abort, status);
-          const uint64_t dq = sdesc_sw128(q_addr + qb * SL::kTileBytes, 16, 1024);
+        const uint32_t qb = qc & 1;
+        ok = ok && cross_wait(q_full + qb, (qc >> 1) & 1, budget, s_abort, status);
+        const uint64_t dq = uniform(sdesc_sw128(q_addr + qb * SL::kTileBytes, 16, 1024));
 #pragma unroll 1
-          for (int t = 0; t < nt; ++t) {
-            const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
-            if (gs >= 3) ok = ok && cross_wait(buf_free + sb, ((gs - 3) / 3) & 1, budget, s_abort, status);
-            ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort, status);
-            if (!ok) continue;
-            const uint64_t dk = sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024);
-            tc_fence_after();
+        for (int t = 0; t < nt; ++t) {
+          const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
+          if (gs >= 3) ok = ok && cross_wait(buf_free + sb, ((gs - 3) / 3) & 1, budget, s_abort, status);
+          ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          const uint64_t dk = uniform(sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024));
+          const uint32_t ts = uniform(tS(sb));
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tS(sb), dq + kmajor_step(k), dk + kmajor_step(k), kIdescQK, k > 0);
+            for (int k = 0; k < D / 16; ++k) mma_ss(ts, dq + kmajor_step(k), dk + kmajor_step(k), kIdescQK, k > 0);
             mma_commit(s_full + sb);
             mma_commit(k_empty + s);
           }
-          if (ok) mma_commit(q_empty + qb);
+          __syncwarp();
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && elect_one()) mma_commit(q_empty + qb);
         ++qc;
         __syncwarp();
       } else {
@@ -291,13 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
             if (!key_bits(mask, left, bits)) zero_rows<4, 1>(sm + SL::v + s * SL::kTileBytes, bits);
             __syncwarp();
           }
-          if (lane == 0) {
-            const uint64_t dv = vtile_desc(v_addr + s * SL::kTileBytes, 0);
-            const uint32_t tp = tS(sb);  // P(t) overwrote its S
-            tc_fence_after();
+          const uint64_t dv = uniform(vtile_desc(v_addr + s * SL::kTileBytes, 0));
+          const uint32_t tp = uniform(tS(sb)), to = uniform(tO(pv_wg));  // P(t) overwrote its S
+          const uint32_t first = uniform(t >= 2 ? 1u : 0u);
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 128 / 16; ++k)
-              mma_ts(tO(pv_wg), tp + 8 * k, dv + vtile_step(k), kIdescPV, (k > 0 || t >= 2) ? 1u : 0u);
+              mma_ts(to, tp + 8 * k, dv + vtile_step(k), kIdescPV, k > 0 ? 1u : first);
             mma_commit(buf_free + sb);
             mma_commit(v_empty + s);
           }
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       }
       g += nt;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       uint64_t* my_drain = drain + (warp - 1);
       mma_commit(my_drain);
       mbar_wait(my_drain, 0, kDrainBudget);

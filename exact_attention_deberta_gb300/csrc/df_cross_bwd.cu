@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   if (warp == 0) {
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<kOtherRegs>();
+    // (the whole warp runs every step, and one lane of it issues; so do the warps of
+    // the products)
     TileWalk walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, xc = 0, g_issued = 0, x_issued = 0;
@@ -257,6 +259,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     const uint32_t x_box = KEYS ? kBoxBytes : q_box, y_box = KEYS ? q_box : kBoxBytes;
     long long number = blockIdx.x;
     int mask_b = -1, mask_n = 0;  // the last masked row measured
+    bool ok = true;               // a wait ran out: nothing is loaded after it
+    // a tile of each of two tensors
+    auto load = [&](const CUtensorMap* m0, const CUtensorMap* m1, uint8_t* dst, uint32_t box, int head, int row,
+                    uint64_t* bar) {
+      if (elect_one()) {
+        mbar_expect_tx(bar, 2 * kChunks * box);
+        for (int ch = 0; ch < kChunks; ++ch) {
+          tma_load_3d(dst + ch * kBoxBytes, m0, ch * 64, head, row, bar);
+          tma_load_3d(dst + SL::kTileBytes + ch * kBoxBytes, m1, ch * 64, head, row, bar);
+        }
+      }
+      __syncwarp();
+    };
     for (uint32_t c = 0;; ++c) {
       CrossItem it = walk.find(a, KEYS ? key_side(a) : query_side(a), KEYS ? query_side(a) : key_side(a), x_step, number);
       if (a.key_mask && it.hk >= 0) {
@@ -270,115 +285,121 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           it.no = mask_n;
         }
       }
-      if (lane == 0) {
-        const uint32_t slot = c % kItemRing;
-        bool ok = true;
-        if (c >= kItemRing) ok = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
-        if (*s_abort || !ok) it.hk = -1;
-        if (ok) {
-          *ring_slot(c) = it;
-          mbar_arrive(item_full + slot);
-        }
-        const int nt = it.hk < 0 ? 0 : y_tiles(it);
-        if (it.hk >= 0 && nt == 0) claim.ask();
-        if (nt > 0) {
-          const int x_head = KEYS ? it.hk : it.hk * a.G, y_head = KEYS ? it.hk * a.G : it.hk;
-          const uint32_t xb = xc % kRes;
-          if (cross_wait(x_empty + xb, ((xc / kRes) & 1) ^ 1, budget, s_abort, status)) {
-            uint8_t* dst = sm + SL::x + xb * 2 * SL::kTileBytes;
-            mbar_expect_tx(x_full + xb, 2 * kChunks * x_box);
-            for (int ch = 0; ch < kChunks; ++ch) {
-              tma_load_3d(dst + ch * kBoxBytes, &maps.x0, ch * 64, x_head, it.r0, x_full + xb);
-              tma_load_3d(dst + SL::kTileBytes + ch * kBoxBytes, &maps.x1, ch * 64, x_head, it.r0, x_full + xb);
-            }
-            x_issued = xc + 1;
-          }
-          ++xc;
-          // the next item is asked for two tiles before this one's end
-          const int ask_at = max(0, nt - 2);
-          for (int t = 0; t < nt; ++t, ++g) {
-            if (t == ask_at) claim.ask();
-            const uint32_t s = g % kStages;
-            if (cross_wait(empty + s, ((g / kStages) & 1) ^ 1, budget, s_abort, status)) {
-              uint8_t* dst = sm + SL::y + s * 2 * SL::kTileBytes;
-              mbar_expect_tx(full + s, 2 * kChunks * y_box);
-              for (int ch = 0; ch < kChunks; ++ch) {
-                tma_load_3d(dst + ch * kBoxBytes, &maps.y0, ch * 64, y_head, it.o0 + t * y_step, full + s);
-                tma_load_3d(dst + SL::kTileBytes + ch * kBoxBytes, &maps.y1, ch * 64, y_head, it.o0 + t * y_step,
-                            full + s);
-              }
-              g_issued = g + 1;
-            }
-          }
-        }
+      const uint32_t slot = c % kItemRing;
+      bool room = true;
+      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+      if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
+      if (lane == 0 && room) {
+        *ring_slot(c) = it;
+        mbar_arrive(item_full + slot);
       }
-      if (__shfl_sync(0xffffffffu, it.hk, 0) < 0) break;
-      if (lane == 0) number = claim.answer(budget, s_abort, status);
-      number = __shfl_sync(0xffffffffu, number, 0);
+      if (it.hk < 0) break;
+      const int nt = y_tiles(it);
+      const int x_head = KEYS ? it.hk : it.hk * a.G, y_head = KEYS ? it.hk * a.G : it.hk;
+      if (nt > 0) {
+        const uint32_t xb = xc % kRes;
+        ok = ok && cross_wait(x_empty + xb, ((xc / kRes) & 1) ^ 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          load(&maps.x0, &maps.x1, sm + SL::x + xb * 2 * SL::kTileBytes, x_box, x_head, it.r0, x_full + xb);
+          x_issued = xc + 1;
+        }
+        ++xc;
+      }
+      // the next item is asked for two tiles before this one's end
+      const int ask_at = max(0, nt - 2);
+#pragma unroll 1
+      for (int t = 0; t < max(nt, 1); ++t) {
+        if (t == ask_at) claim.ask();
+        if (t >= nt) break;
+        const uint32_t s = g % kStages;
+        ok = ok && cross_wait(empty + s, ((g / kStages) & 1) ^ 1, budget, s_abort, status);
+        ok = __all_sync(0xffffffffu, ok);
+        ++g;
+        if (!ok) continue;
+        load(&maps.y0, &maps.y1, sm + SL::y + s * 2 * SL::kTileBytes, y_box, y_head, it.o0 + t * y_step, full + s);
+        g_issued = g;
+      }
+      number = claim.answer(budget, s_abort, status);
     }
-    if (lane == 0) {
-      // no copy may still be landing when the CTA leaves
+    // no copy may still be landing when the CTA leaves
+    if (elect_one()) {
+#pragma unroll 1
       for (uint32_t k = g_issued > kStages ? g_issued - kStages : 0; k < g_issued; ++k)
         mbar_wait(full + k % kStages, (k / kStages) & 1, kDrainBudget);
+#pragma unroll 1
       for (uint32_t k = x_issued > kRes ? x_issued - kRes : 0; k < x_issued; ++k)
         mbar_wait(x_full + k % kRes, (k / kRes) & 1, kDrainBudget);
     }
+    __syncwarp();
   } else if (warp <= 2) {
     // ------------------------------------------------------------ S (warp 1), dP (warp 2)
     setmaxnreg_dec<kOtherRegs>();
-    if (lane == 0) {
-      const uint32_t which = warp - 1;
-      const uint32_t tD = tmem + kAccCols + 64u * which;
-      // a buffer's columns may be written again once the sums have read what stands
-      // there; without dv the columns of S hold no P, and its readers are done with
-      // dS's arrival
-      uint64_t* free_bar = which ? ds_free : KEYS ? p_free : p_full;
-      uint32_t g = 0, xc = 0;  // streamed tiles and items before this one
-      bool ok = true;          // a wait that ran out ends this thread's products
-      for (uint32_t c = 0;; ++c) {
-        const CrossItem it = read_item(c);
-        if (it.hk < 0) break;
-        const int nt = y_tiles(it);
-        if (nt == 0) continue;
-        const uint32_t xb = xc % kRes;
-        ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
-        const uint64_t dx = sdesc_sw128(smem_u32(sm + SL::x + (xb * 2 + which) * SL::kTileBytes), 16, 1024);
+    const uint32_t which = warp - 1;
+    const uint32_t tD = tmem + kAccCols + 64u * which;
+    // a buffer's columns may be written again once the sums have read what stands
+    // there; without dv the columns of S hold no P, and its readers are done with
+    // dS's arrival
+    uint64_t* free_bar = which ? ds_free : KEYS ? p_free : p_full;
+    uint32_t g = 0, xc = 0;  // streamed tiles and items before this one
+    bool ok = true;          // a wait that ran out ends this warp's products
+    for (uint32_t c = 0;; ++c) {
+      CrossItem it;
+      if (lane == 0) it = read_item(c);
+      it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
+      if (it.hk < 0) break;
+      it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      const int nt = y_tiles(it);
+      if (nt == 0) continue;
+      const uint32_t xb = xc % kRes;
+      ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
+      const uint64_t dx = uniform(sdesc_sw128(smem_u32(sm + SL::x + (xb * 2 + which) * SL::kTileBytes), 16, 1024));
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t, ++g) {
-          const uint32_t s = g % kStages;
-          ok = ok && cross_wait(ready + s, (g / kStages) & 1, budget, s_abort, status);
-          const uint32_t y_addr = smem_u32(sm + SL::y + (s * 2 + which) * SL::kTileBytes);
+      for (int t = 0; t < nt; ++t, ++g) {
+        const uint32_t s = g % kStages;
+        ok = ok && cross_wait(ready + s, (g / kStages) & 1, budget, s_abort, status);
+        const uint32_t y_addr = smem_u32(sm + SL::y + (s * 2 + which) * SL::kTileBytes);
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t u = 2 * g + h, b = u % kBufs;
-            if (u >= kBufs) ok = ok && cross_wait(free_bar + b, (u / kBufs - 1) & 1, budget, s_abort, status);
-            if (!ok) continue;
-            const uint64_t dy = sdesc_sw128(y_addr + h * 8192, 16, 1024);
-            tc_fence_after();
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t u = 2 * g + h, b = u % kBufs;
+          if (u >= kBufs) ok = ok && cross_wait(free_bar + b, (u / kBufs - 1) & 1, budget, s_abort, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          const uint64_t dy = uniform(sdesc_sw128(y_addr + h * 8192, 16, 1024));
+          const uint32_t to = uniform(tD + 128u * b);
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tD + 128u * b, dx + kmajor_step(k), dy + kmajor_step(k), kIdescS, k > 0);
+            for (int k = 0; k < D / 16; ++k) mma_ss(to, dx + kmajor_step(k), dy + kmajor_step(k), kIdescS, k > 0);
             mma_commit(s_full + b);
           }
+          __syncwarp();
         }
-        if (ok) mma_commit(x_empty + xb);
-        ++xc;
       }
+      if (ok && elect_one()) mma_commit(x_empty + xb);
+      __syncwarp();
+      ++xc;
+    }
+    if (elect_one()) {
       mma_commit(drain + which);
       mbar_wait(drain + which, 0, kDrainBudget);
     }
+    __syncwarp();
   } else if (warp <= 4) {
     // ------------------------------------------------------------ sums: dS.Y0 (warp 3), P.Y1 (warp 4)
     setmaxnreg_dec<kOtherRegs>();
     const uint32_t which = warp - 3;
-    if (lane == 0 && which < kSums) {
-      const uint32_t tA = tmem + kAccCols + (which ? 0u : 64u), tD = which ? tAcc1 : tAcc0;
+    if (which < kSums) {
+      const uint32_t tA = tmem + kAccCols + (which ? 0u : 64u), tD = uniform(which ? tAcc1 : tAcc0);
       uint64_t* free_bar = which ? p_free : ds_free;
       uint32_t g = 0, xc = 0;
       bool ok = true;
       for (uint32_t c = 0;; ++c) {
-        const CrossItem it = read_item(c);
+        CrossItem it;
+        if (lane == 0) it = read_item(c);
+        it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
         if (it.hk < 0) break;
+        it.no = __shfl_sync(0xffffffffu, it.no, 0);
         const int nt = y_tiles(it);
         if (nt == 0) continue;
         // the epilogue has read the previous item's sums
@@ -391,23 +412,31 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           for (int h = 0; h < 2; ++h) {
             const uint32_t u = 2 * g + h, b = u % kBufs;
             ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort, status);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
-            const uint64_t dy = vtile_desc(y_addr, 4 * h);
-            const uint32_t first = t == 0 && h == 0 ? 0u : 1u;
+            const uint64_t dy = uniform(vtile_desc(y_addr, 4 * h));
+            const uint32_t from = uniform(tA + 128u * b);
+            const uint32_t first = uniform(t == 0 && h == 0 ? 0u : 1u);
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tD, tA + 128u * b + 8 * k, dy + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
-            mma_commit(free_bar + b);
-            // (the scores of both halves, which read the stage too, stood before P)
-            if (h == 1) mma_commit(empty + s);
+              for (int k = 0; k < 4; ++k) mma_ts(tD, from + 8 * k, dy + vtile_step(k), kIdescAcc, k > 0 ? 1u : first);
+              mma_commit(free_bar + b);
+              // (the scores of both halves, which read the stage too, stood before P)
+              if (h == 1) mma_commit(empty + s);
+            }
+            __syncwarp();
           }
         }
-        if (ok) mma_commit(acc_full);
+        if (ok && elect_one()) mma_commit(acc_full);
+        __syncwarp();
         ++xc;
       }
-      mma_commit(drain + 2 + which);
-      mbar_wait(drain + 2 + which, 0, kDrainBudget);
+      if (elect_one()) {
+        mma_commit(drain + 2 + which);
+        mbar_wait(drain + 2 + which, 0, kDrainBudget);
+      }
+      __syncwarp();
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ streamed rows
