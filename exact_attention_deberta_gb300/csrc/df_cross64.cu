@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     const bool qk_role = warp == 1;
     const int pv_wg = warp == 3 ? 0 : 1;  // the warpgroup whose tiles this warp multiplies
     uint32_t g = 0, qc = 0, pn = 0;       // key tiles and items before this one, tiles whose P has been consumed
+    const uint32_t to = uniform(tO(pv_wg));
     const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sm + SL::k), v_addr = smem_u32(sm + SL::v);
     bool ok = true;                       // a wait that ran out ends this warp's products
     for (uint32_t c = 0;; ++c) {
@@ -264,12 +265,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
 #pragma unroll 1
         for (int t = 0; t < nt; ++t) {
           const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
+          const uint64_t dk = uniform(sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024));
+          const uint32_t ts = uniform(tS(sb));
           if (gs >= 3) ok = ok && cross_wait(buf_free + sb, ((gs - 3) / 3) & 1, budget, s_abort, status);
           ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort, status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
-          const uint64_t dk = uniform(sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024));
-          const uint32_t ts = uniform(tS(sb));
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -287,22 +288,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
 #pragma unroll 1
         for (int t = pv_wg; t < nt; t += 2, ++pn) {
           const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
+          const uint64_t dv = uniform(vtile_desc(v_addr + s * SL::kTileBytes, 0));
+          const uint32_t tp = uniform(tS(sb)), first = uniform(t >= 2 ? 1u : 0u);  // P(t) overwrote its S
+          const int left = it.no - (t0 + t) * 128;
+          const bool partial = a.key_mask || left < 128;
           // P of this tile says that S was there, so that P.V of the stage's previous
           // tile is done: the wait for V sees its own phase
           ok = ok && cross_wait(p_full + 2 * pv_wg + (pn & 1), (pn >> 1) & 1, budget, s_abort, status);
           ok = ok && cross_wait(v_full + s, (gs / R) & 1, budget, s_abort, status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
-          const int left = it.no - (t0 + t) * 128;
-          if (a.key_mask || left < 128) {
+          if (partial) {
             uint32_t bits[4];
             const uint8_t* mask = a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * 128 : nullptr;
             if (!key_bits(mask, left, bits)) zero_rows<4, 1>(sm + SL::v + s * SL::kTileBytes, bits);
             __syncwarp();
           }
-          const uint64_t dv = uniform(vtile_desc(v_addr + s * SL::kTileBytes, 0));
-          const uint32_t tp = uniform(tS(sb)), to = uniform(tO(pv_wg));  // P(t) overwrote its S
-          const uint32_t first = uniform(t >= 2 ? 1u : 0u);
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll

@@ -362,11 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const uint32_t u = 2 * g + h, b = u % kBufs;
+          const uint64_t dy = uniform(sdesc_sw128(y_addr + h * 8192, 16, 1024));
+          const uint32_t to = uniform(tD + 128u * b);
           if (u >= kBufs) ok = ok && cross_wait(free_bar + b, (u / kBufs - 1) & 1, budget, s_abort, status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
-          const uint64_t dy = uniform(sdesc_sw128(y_addr + h * 8192, 16, 1024));
-          const uint32_t to = uniform(tD + 128u * b);
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -411,12 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const uint32_t u = 2 * g + h, b = u % kBufs;
-            ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) continue;
             const uint64_t dy = uniform(vtile_desc(y_addr, 4 * h));
             const uint32_t from = uniform(tA + 128u * b);
             const uint32_t first = uniform(t == 0 && h == 0 ? 0u : 1u);
+            ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort, status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
