@@ -353,16 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       const bool warp_in = __any_sync(0xffffffffu, row_in);
       float m_run = -INFINITY, l_run = 0.f;
       bool o_has = false;
+      const int whole = a.key_mask ? 0 : it.no / 128 - t0;  // tiles of which every key counts
+      uint32_t sb = (gbase + wg) % 3, phase = ((gbase + wg) / 3) & 1;  // of tile gbase + t
       for (int t = wg; t < nt; t += 2, ++own) {
-        const uint32_t G = gbase + t;
-        const uint32_t sb = G % 3;
         const uint32_t tSw = tmem + 128u * sb + lane_off;
-        cross_wait(s_full + sb, (G / 3) & 1, budget, s_abort, status);
+        cross_wait(s_full + sb, phase, budget, s_abort, status);
         __syncwarp();
         tc_fence_after();
         if (warp_in) {
-          const int left = it.no - (t0 + t) * 128;
-          if (a.key_mask || left < 128) {
+          if (t >= whole) {
+            const int left = it.no - (t0 + t) * 128;
             uint32_t bits[4];
             if (!key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * 128 : nullptr, left,
                           bits)) {
@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
             m_run = mt;
             l_run *= rescale;
           }
+          const bool rescaled = __any_sync(0xffffffffu, rebase && o_has);
           const float shift = m_run == -INFINITY ? INFINITY : m_run;  // no finite score yet: every p is 0
           const float2 nshift = make_float2(-shift, -shift);
           {
@@ -440,8 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
             const float2 s01 = add2(acc[0], acc[1]), s23 = add2(acc[2], acc[3]);
             l_run += (s01.x + s23.x) + (s01.y + s23.y);
           }
-          if (o_has && __any_sync(0xffffffffu, rebase)) {
+          if (rescaled) {
             // this warpgroup's previous P.V must be done
+            const uint32_t G = gbase + t;
             cross_wait(buf_free + (G - 2) % 3, ((G - 2) / 3) & 1, budget, s_abort, status);
             __syncwarp();
             tc_fence_after();
@@ -459,8 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 2 * wg + (own & 1));
+        mbar_arrive_if(lane == 0, p_full + 2 * wg + (own & 1));
         o_has = true;
+        sb += 2;
+        if (sb >= 3) {
+          sb -= 3;
+          phase ^= 1;
+        }
       }
       // ---- the item's end: both warpgroups' states together
       if (wg < nt) {  // its last P.V
