@@ -50,8 +50,8 @@ struct FwdSmem {
   static constexpr uint32_t ml = v + kStages * kTileBytes;          // float4 [2 warpgroups, a cluster's][128]
   static constexpr uint32_t bars = ml + 3 * 128 * 16;
   // q_full, q_empty [2]; k_full, k_empty, v_full, v_empty [kStages]; s_full,
-  // buf_free, drain [3]; p_full [4]; item_full, item_empty; claim
-  static constexpr int kBars = 4 + 4 * kStages + 9 + 4 + 2 * (int)kItemRing + 1;
+  // buf_free, drain [3]; p_full, pv_done [4]; item_full, item_empty; claim
+  static constexpr int kBars = 4 + 4 * kStages + 9 + 8 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax warpgroups' current item
   static constexpr uint32_t claim = cur + 32;                       // 16 bytes
@@ -89,12 +89,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
   uint64_t* s_full = v_empty + R;      // [3] S of the buffer computed
   uint64_t* buf_free = s_full + 3;     // [3] the P.V that read the buffer is done
   uint64_t* drain = buf_free + 3;      // [3], one per issuing warp
-  // [wg][k & 1]: the four warps of wg stored P of its k-th tile.  Two per
-  // warpgroup because a warp may finish its next tile before a sibling has stored
-  // the current one; it is never two ahead, since its next S waits for a P.V
-  // issued behind this phase.
+  // [wg][k & 1]: the four warps of wg stored P of its k-th tile; P.V of it done.  Two
+  // of each per warpgroup because a warp may be through with its next tile before a
+  // sibling has stored this one, or before this one's P.V is done; it is never two
+  // ahead, since its next S but one waits for a P.V issued behind this phase.
   uint64_t* p_full = drain + 3;
-  uint64_t* item_full = p_full + 4;
+  uint64_t* pv_done = p_full + 4;
+  uint64_t* item_full = pv_done + 4;
   uint64_t* item_empty = item_full + kItemRing;
   uint64_t* claim_bar = item_empty + kItemRing;
   auto ring_slot = [&](uint32_t c) { return reinterpret_cast<CrossItem*>(sm + SL::ring + 32 * (c % kItemRing)); };
@@ -115,7 +116,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       mbar_init(buf_free + b, 1);
       mbar_init(drain + b, 1);
     }
-    for (int b = 0; b < 4; ++b) mbar_init(p_full + b, 4);
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(p_full + b, 4);
+      mbar_init(pv_done + b, 1);
+    }
     for (uint32_t b = 0; b < kItemRing; ++b) {
       mbar_init(item_full + b, 1);
       mbar_init(item_empty + b, kItemReaders);
@@ -310,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
             for (int k = 0; k < 128 / 16; ++k)
               mma_ts(to, tp + 8 * k, dv + vtile_step(k), kIdescPV, k > 0 ? 1u : first);
             mma_commit(buf_free + sb);
+            mma_commit(pv_done + 2 * pv_wg + (pn & 1));
             mma_commit(v_empty + s);
           }
           __syncwarp();
@@ -335,6 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     const uint32_t tOw = tO(wg) + lane_off;
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     uint32_t own = 0, gbase = 0;  // this warpgroup's tiles, and the CTA's before the item
+    auto pv_wait = [&](uint32_t n) {  // until P.V of its n-th tile is done
+      cross_wait(pv_done + 2 * wg + (n & 1), (n >> 1) & 1, budget, s_abort, status);
+    };
     // One thread takes each item from the ring and leaves it in s_cur; all 256 read
     // it behind their barrier, so that they run the same list even after a wait
     // has run out.
@@ -443,8 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
           }
           if (rescaled) {
             // this warpgroup's previous P.V must be done
-            const uint32_t G = gbase + t;
-            cross_wait(buf_free + (G - 2) % 3, ((G - 2) / 3) & 1, budget, s_abort, status);
+            pv_wait(own - 1);
             __syncwarp();
             tc_fence_after();
             uint32_t r[32];
@@ -470,10 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         }
       }
       // ---- the item's end: both warpgroups' states together
-      if (wg < nt) {  // its last P.V
-        const uint32_t G = gbase + wg + 2 * ((nt - 1 - wg) / 2);
-        cross_wait(buf_free + G % 3, (G / 3) & 1, budget, s_abort, status);
-      }
+      if (wg < nt) pv_wait(own - 1);  // its last P.V
       __syncwarp();
       tc_fence_after();
       sML[wg * 128 + row] = make_float4(m_run, l_run, o_has ? 1.f : 0.f, 0.f);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from _cross import call, check_forward, inputs, np64, to_dev, want
+from _cross import call, call_bwd, check_forward, inputs, np64, to_dev, want
 
 pytestmark = pytest.mark.gpu
 
@@ -134,6 +134,28 @@ def test_two_calls_at_once(lib):
     torch.cuda.synchronize()
     assert int(status.item()) == lib.DF_OK
     assert all(torch.equal(o, a) for out, a in zip(outs, alone) for o in out)
+
+
+@pytest.mark.parametrize("B,H,Hk,d,Lq,Lk,q,k", [
+    (200, 12, 12, 64, 140, 300, "packed", "packed"),   # many items, some of one tile or none
+    (60, 12, 4, 128, 90, 500, "packed", "packed"),
+    (80, 8, 8, 128, 1, 700, "padded", "packed"),       # single tokens
+    (3, 2, 2, 64, 30, 2000, "padded", "masked"),       # clusters
+])
+def test_repeated_launches_give_equal_bits(lib, B, H, Hk, d, Lq, Lk, q, k):
+    # back to back, so that the CTAs of one call end beside those of the next
+    x = inputs(B, H, Hk, d, Lq, Lk, BF, q, k, seed=B)
+    dev = to_dev(x)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first, stats = call(lib, x, dev, with_stats=True, status=status)
+    grads = call_bwd(lib, x, dev, first, stats, status=status)
+    other = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(40):
+        out, st = call(lib, x, dev, with_stats=True, status=status)
+        other += (out != first).sum() + (st.lse != stats.lse).sum()
+        for a, b in zip(call_bwd(lib, x, dev, out, st, status=status), grads):
+            other += (a != b).sum()
+    assert int(other.item()) == 0 and int(status.item()) == lib.DF_OK
 
 
 def test_no_keys_no_queries_no_sequences(lib):
