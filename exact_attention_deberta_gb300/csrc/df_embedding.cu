@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(256) lookup_kernel(const void* __restrict__ id
 struct SortArgs {
   const void* ids;      // first pass: the caller's ids
   int ids64;
-  const uint32_t* key;  // later passes
-  const uint32_t* pos;
+  uint32_t* key;        // sorted by the passes before; the first pass fills it from the ids
+  const uint32_t* pos;  // (so that ids which change meanwhile cannot lead it astray)
   uint32_t* key_out;
   uint32_t* pos_out;
   uint32_t* hist;       // [tiles][digits]
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kSortThreads) digit_counts(const SortArgs a) {
   for (int k = 0; k < kSortItems; ++k) {
     const int i = base + k * kSortThreads + threadIdx.x;
     key[k] = i < a.n ? sort_key(a, i) : 0u;
+    if (a.first && i < a.n) a.key[i] = key[k];
   }
   for (int d = threadIdx.x; d < digits; d += kSortThreads) cnt[d] = 0;
   __syncthreads();
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs 
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const int i = base + k * 32 + lane;
-    key[k] = i < a.n ? sort_key(a, i) : 0u;
+    key[k] = i < a.n ? a.key[i] : 0u;
     pos[k] = a.first ? (uint32_t)i : (i < a.n ? a.pos[i] : 0u);
   }
   // thread t's digits: t kPer .. t kPer + kPer - 1
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs 
   for (int k = 0; k < kSortItems; ++k) {
     if (base + k * 32 + lane >= a.n) continue;
     const uint32_t to = cnt[warp][(key[k] >> a.shift) & (digits - 1)] + rank[k];
+    if (to >= (uint32_t)a.n) continue;  // only with a workspace that another call writes
     a.key_out[to] = key[k];
     a.pos_out[to] = pos[k];
   }
@@ -399,6 +401,7 @@ struct SumArgs {
 };
 
 __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t v, int c, const float (&acc)[8]) {
+  if (v >= (uint32_t)a.V) return;
   float* p = a.grad + (size_t)v * a.N + c;
   float f[8];
   if (a.accumulate) load8<float>(p, f);
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) sum_runs(const Su
   const bool col = c < a.N;
   const int i0 = chunk * CHUNK, cnt = min(CHUNK, a.n - i0);
   const uint32_t my_key = lane < cnt ? a.key[i0 + lane] : 0xffffffffu;
-  const uint32_t my_pos = lane < cnt ? a.pos[i0 + lane] : 0u;
+  const uint32_t my_pos = lane < cnt ? min(a.pos[i0 + lane], (uint32_t)a.n - 1u) : 0u;
   const uint32_t before = chunk > 0 ? a.key[i0 - 1] : 0xffffffffu;
   const uint32_t after = i0 + CHUNK < a.n ? a.key[i0 + CHUNK] : 0xffffffffu;
   // entries that pass a gradient stand at the front
@@ -723,7 +726,7 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
     for (int p = 0; p < l.passes; ++p) {
       a.first = p == 0;
       a.shift = p * l.bits;
-      a.key = reinterpret_cast<const uint32_t*>(base + l.key[(p + 1) & 1]);
+      a.key = reinterpret_cast<uint32_t*>(base + l.key[(p + 1) & 1]);
       a.pos = reinterpret_cast<const uint32_t*>(base + l.pos[(p + 1) & 1]);
       a.key_out = reinterpret_cast<uint32_t*>(base + l.key[p & 1]);
       a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[p & 1]);

@@ -156,3 +156,29 @@ def test_other_stream_and_captured_replay(lib):
         other = lib.df_embedding_bwd(ids, dout, V)
     side.synchronize()
     assert torch.equal(other, grad)
+
+
+def test_ids_that_change_meanwhile_do_no_harm(lib):
+    # which of the ids a gradient counts is then open, but nothing is read or written
+    # outside the tensors, and the next call is right
+    T, N, V = 40000, 64, 5000
+    g = torch.Generator().manual_seed(2)
+    dout = torch.randn(T, N, generator=g).to(torch.bfloat16).cuda()
+    choices = [torch.randint(0, V, (T,), generator=g).cuda(), torch.full((T,), 3, device="cuda"),
+               torch.full((T,), 1 << 40, device="cuda")]
+    ids = choices[0].clone()
+    guard = torch.zeros(V + 64, N, device="cuda")
+    guard[V:] = 7.0
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for k in range(30):
+        lib.df_embedding_bwd(ids, dout, V, grad=guard[:V])
+        with torch.cuda.stream(other):
+            for c in choices:
+                ids.copy_(c)
+    torch.cuda.synchronize()
+    assert bool((guard[V:] == 7.0).all())
+    ids.copy_(choices[0])
+    torch.cuda.synchronize()
+    got = lib.df_embedding_bwd(ids, dout, V, grad=guard[:V])
+    assert torch.equal(got, lib.df_embedding_bwd(choices[0], dout, V))
