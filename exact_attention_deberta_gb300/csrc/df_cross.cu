@@ -140,9 +140,13 @@ extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void*
     return DF_ERR_CUDA;
   const long long items = cross_query_tiles(a.c);
   const int sms = device_sms();
+  // Fewer items than half the SMs: clusters share them, with at least two key tiles
+  // for each CTA (both warpgroups at work).  12 heads, one query, 8192 keys: 12 us
+  // against 36 without; 8 heads, d = 128, 64 queries, 4096 keys: 13 against 38; 4 x
+  // 12 heads, 33 queries, 300 keys: 9.3 against 10.9 with a tile for each.
   a.splits = 1;
   const int key_tiles = (Lk + kFwdKeys - 1) / kFwdKeys;
-  while (a.splits < 8 && items * a.splits * 2 <= sms && a.splits * 2 <= key_tiles) a.splits *= 2;
+  while (a.splits < 8 && items * a.splits * 2 <= sms && a.splits * 4 <= key_tiles) a.splits *= 2;
   a.split_bits = a.splits == 8 ? 3 : a.splits / 2;
   const int grid = (int)items * a.splits;
   cudaStream_t s = (cudaStream_t)stream;

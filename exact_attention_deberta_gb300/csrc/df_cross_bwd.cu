@@ -22,13 +22,20 @@
 // where the sums leave no more columns: dk, dv at D = 128), so that the tensor core
 // runs the next half's products while both warpgroups are busy.
 //   warp 0        items and TMA loads
-//   warps 1, 2    issue S and dP, warps 3, 4 the sums acc0 and acc1: between two
-//                 batches of products an issuer spends about as long on waits and
-//                 commits as on the products themselves
+//   warps 1, 2    issue S and dP, warps 3, 4 the sums acc0 and acc1 (one issuer for
+//                 each: two for all four took 1.81 ms where these took 1.57)
 //   warp 5        per streamed tile: the rows' (lse, D) or the keys' mask bits into
 //                 shared memory, and zeros over streamed rows that do not count
 //                 (they are the reduction dimension of the second products)
 //   warps 8-15    P and dS, one thread per resident row; the epilogue
+//
+// Measured (GB300, bf16): 16 x 12 heads, 2048 queries x 8192 keys, d = 64: 2.39 ms
+// (10 flops per score and column: 863 TFLOP/s; with the two products that are done
+// twice 1208); 19 x 8 heads, d = 128: 3.46 ms (944, 1322).  Bound by the tensor core:
+// S and dP in halves of 64 columns run at two thirds of its rate, so a 128 x 128 tile
+// takes at least 1498 (keys) or 1138 (queries) cycles at d = 64 and takes 1774 and
+// 1330; 2591 and 2074 at d = 128, and takes 3615 and 2630 (only two buffers in the
+// first).  Whole tiles (128 columns) would leave one buffer and no overlap.
 //
 // fp16: dS spans too wide a range for its exponent, so it is scaled by a power of
 // two that puts the largest |dout_i| at about 16, and P (at most 1) by 2^14; the

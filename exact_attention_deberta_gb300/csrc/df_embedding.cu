@@ -572,12 +572,13 @@ GradLayout grad_layout(int T, int N, int V) {
   GradLayout l;
   l.tiles = (T + kSortTile - 1) / kSortTile;
   // short chunks spread few tokens over more warps, long ones leave fewer partial
-  // rows (8192 x 1024: 10 us at 32, 5 at 8; 131072 x 768: 50 us at 32)
+  // rows (whole gradient, bf16; 8192 x 1024: 45 us at 8, 57 at 32; 32768 x 768: 67 at
+  // both; 131072 x 768: 164 at 8, 149 at 32)
   l.chunk = T <= 32768 ? 8 : 32;
   l.chunks = (T + l.chunk - 1) / l.chunk;
   int key_bits = 1;  // keys 0 .. V
   while (key_bits < 32 && ((unsigned long long)V >> key_bits) != 0) ++key_bits;
-  l.small = T <= kSmallSort;
+  l.small = T <= kSmallSort;  // (2048 x 768: 34 us, 40 in tiles; 8192 x 1024: 45, 54)
   const int most = l.small ? kSmallBits : kMaxDigitBits;
   l.passes = (key_bits + most - 1) / most;
   l.bits = (key_bits + l.passes - 1) / l.passes;
@@ -609,7 +610,8 @@ df_status check_sizes(int T, int N, int V) {
 template <typename T>
 void launch_lookup(const void* ids, int ids64, int n, const void* table, int V, int N, float scale, void* out,
                    int32_t* status, cudaStream_t s) {
-  // four rows per warp once that still leaves every SM its resident warps
+  // four rows per warp once that still leaves every SM its resident warps (131072 x
+  // 768: 56 us, 61 with one; 38912: 12.6, 14.2; 16384: 6.6, 6.2)
   if (n >= 4 * 64 * sm_count())
     lookup_kernel<T, 4><<<(n + 31) / 32, 256, 0, s>>>(ids, ids64, n, static_cast<const T*>(table), V, N, scale,
                                                       static_cast<T*>(out), status);

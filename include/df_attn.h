@@ -2,7 +2,8 @@
  * df_attn.h -- C ABI of the exact DeBERTa-v2/v3 disentangled attention for
  * NVIDIA GB300 (sm_103a): the fused forward pass, its backward pass, the
  * forward from host buffers, and the steps on either side of the attention
- * (padded <-> packed conversion, projections, LayerNorm).
+ * (padded <-> packed conversion, projections, LayerNorm, token embeddings, and
+ * the cross attention of a decoder or reader to the encoder's states).
  *
  * The operation (DisentangledFlash 0.2.0 README, section "Status":
  * "DeBERTa-v2/v3-style C2P/P2C disentangled attention", "factorized 2-D padding
@@ -476,7 +477,8 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  *   Lq, Lk      padded lengths, or in packed mode upper bounds of the lengths
  *               (they size the launch; the lengths themselves decide the result)
  *   total_q, total_k  rows of q and k: B Lq and B Lk without cu_seqlens.  Packed
- *               rows behind the last sequence get zeros (lse: -infinity)
+ *               rows behind the last sequence get zeros (lse: -infinity); with
+ *               cu_seqlens_q[0] > 0 the rows before the first one are left alone
  *   d           a multiple of 8, at most 128
  *   scale       > 0, finite
  *   dtype       DF_BF16 or DF_FP16, shared by q, k, v, out, out_lo
@@ -492,11 +494,13 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  *               as empty; its rows of out are not written)
  * Scores, softmax statistics and sums are fp32; the weights are rounded to dtype
  * as the operand of the product with v.  Keys that do not count, and rows of k
- * and v outside the sequence, may hold anything (NaN included).  One launch, no
- * workspace; equal inputs give equal bits.
+ * and v outside the sequence, may hold anything (NaN included); a NaN that counts
+ * makes its rows' out and lse NaN.  out, out_lo and lse must not overlap the
+ * inputs.  One launch, no workspace; equal inputs give equal bits.
  * Errors: DF_ERR_INVALID_ARG (NULL pointer, sizes, H % Hk, scale, key_mask with
  * cu_seqlens_k, dtype), DF_ERR_UNSUPPORTED (fp32, d, H / Hk > 128, over 2^30
- * rows, over 2^31 rows times key heads), DF_ERR_ALIGNMENT (tensors 16 bytes, lse and cu_seqlens 4), DF_ERR_CUDA. */
+ * rows, over 2^31 rows times key heads), DF_ERR_ALIGNMENT (tensors 16 bytes, lse
+ * and cu_seqlens 4), DF_ERR_CUDA. */
 df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
                             const uint8_t* key_mask, const int32_t* cu_seqlens_q,
                             const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
@@ -513,8 +517,9 @@ df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
  *   out, out_lo, lse   as the forward gave them (out_lo may be NULL, at the cost
  *                      of the accuracy described there)
  *   dout       like out
- *   dq, dk, dv like q, k, v, in `dtype`: written in full.  Keys that do not count
- *              and rows behind the last packed sequence get zeros
+ *   dq, dk, dv like q, k, v, in `dtype`: written in full (from cu_seqlens[0] on);
+ *              must not overlap the inputs.  Keys that do not count and rows
+ *              behind the last packed sequence get zeros
  *   workspace  at least df_cross_attn_bwd_workspace_size() bytes, 256-byte
  *              aligned, contents need not be initialised; calls that share it
  *              must not overlap
@@ -561,9 +566,9 @@ df_status df_embedding(const void* ids, int ids_64, int T, const void* table, in
  * in float32 [V, N].  Tokens with ids[t] = padding_idx (-1: none) and ids
  * outside [0, V) (status as above) pass no gradient, whatever their row of
  * dout holds.  accumulate = 0 writes every row (zeros where no token reached
- * it); accumulate = 1 touches only the rows that tokens reached.  The tokens are sorted by id
- * and each row is summed in fp32 in an order that depends on ids alone, without
- * atomics: equal inputs give equal bits.
+ * it); accumulate = 1 touches only the rows that tokens reached.  The tokens are
+ * sorted by id and each row is summed in fp32 in an order that depends on ids
+ * alone, without atomics: equal inputs give equal bits.
  *   workspace  at least df_embedding_bwd_workspace_size() bytes, 256-byte
  *              aligned, contents need not be initialised; calls that share it
  *              must not overlap
