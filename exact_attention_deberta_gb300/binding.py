@@ -516,13 +516,18 @@ def _on_device(tensors, names):
     return idx
 
 
-def _call_on(idx, fn, stream, *args) -> int:
-    """fn(*args, stream) with device ``idx`` current; the stream defaults to its current
-    one.  (Plain integers for pointers and streams: a small call is bound by the host.)"""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(idx)
-    else:
-        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _current(stream, like):
+    """A context with ``stream`` (a torch stream or its handle) current, so that what a
+    call allocates belongs to the stream that it runs on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+    return torch.cuda.stream(stream)
+
+
+def _call_on(idx, fn, *args) -> int:
+    """fn(*args, the current stream) with device ``idx`` current.  (Plain integers for
+    pointers and streams: a small call is bound by the host.)"""
+    stream = torch._C._cuda_getCurrentRawStream(idx)
     if torch._C._cuda_getDevice() == idx:
         return fn(*args, stream)
     with torch.cuda.device(idx):
@@ -554,20 +559,23 @@ def _ids_64(ids) -> int:
 def df_embedding(ids, table, scale=1.0, out=None, status=None, stream=None):
     """scale * table[ids]: ids [...] (int32 or int64), table [V, N] -> [..., N] in the
     table's dtype.  Rows of ids outside the table are zeros (``status`` is set)."""
+    if stream is not None:
+        with _current(stream, table):
+            return df_embedding(ids, table, scale, out, status)
     if table.dim() != 2 or table.dtype not in _DTYPE:
         raise ValueError("table must be a bf16, fp16 or fp32 matrix [V, N]")
     idx = _on_device((table, ids, out, status), "table ids out status")
     V, N = table.shape
     shape = ids.shape + (N,)
     if out is None:
-        out = table.new_empty(shape)
+        out = torch.empty(shape, dtype=table.dtype, device=table.device)
     elif out.dtype != table.dtype or out.shape != shape:
         raise ValueError("out must be [..., N] of the table's dtype")
     if status is not None:
         _status_word(status)
     T = ids.numel()
     _int_sizes(ids=T, V=V, N=N)
-    _check(_call_on(idx, _lib.df_embedding, stream, ids.data_ptr(), _ids_64(ids), T, table.data_ptr(), V, N,
+    _check(_call_on(idx, _lib.df_embedding, ids.data_ptr(), _ids_64(ids), T, table.data_ptr(), V, N,
                     float(scale), out.data_ptr(), _DTYPE[table.dtype], _addr(status)), "df_embedding")
     return out
 
@@ -581,6 +589,9 @@ def df_embedding_bwd(ids, dout, vocab, scale=1.0, padding_idx=None, grad=None, a
     """Gradient of the table [vocab, N] in float32 for dout [..., N], the gradient of
     ``df_embedding(ids, table, scale)``.  ``accumulate`` adds to ``grad``, which must
     then be given; tokens with ``padding_idx`` pass no gradient."""
+    if stream is not None:
+        with _current(stream, dout):
+            return df_embedding_bwd(ids, dout, vocab, scale, padding_idx, grad, accumulate, workspace, status)
     if dout.dtype not in _DTYPE or dout.dim() < 1 or dout.shape[:-1] != ids.shape:
         raise ValueError("dout must be bf16, fp16 or fp32, [..., N] for ids [...]")
     idx = _on_device((dout, ids, grad, workspace, status), "dout ids grad workspace status")
@@ -591,13 +602,14 @@ def df_embedding_bwd(ids, dout, vocab, scale=1.0, padding_idx=None, grad=None, a
     if grad is None:
         if accumulate:
             raise ValueError("accumulate needs the gradient to add to")
-        grad = dout.new_empty((vocab, N), dtype=torch.float32)
+        grad = torch.empty((vocab, N), dtype=torch.float32, device=dout.device)
     elif grad.dtype != torch.float32 or tuple(grad.shape) != (vocab, N):
         raise ValueError("grad must be float32 [vocab, N]")
     if workspace is None:
-        workspace = dout.new_empty(max(df_embedding_bwd_workspace_size(T, N, vocab), 256), dtype=torch.uint8)
+        workspace = torch.empty(max(df_embedding_bwd_workspace_size(T, N, vocab), 256), dtype=torch.uint8,
+                                device=dout.device)
     pad = -1 if padding_idx is None else int(padding_idx)
-    _check(_call_on(idx, _lib.df_embedding_bwd, stream, ids.data_ptr(), _ids_64(ids), T, dout.data_ptr(), vocab, N,
+    _check(_call_on(idx, _lib.df_embedding_bwd, ids.data_ptr(), _ids_64(ids), T, dout.data_ptr(), vocab, N,
                     float(scale), pad, 1 if accumulate else 0, grad.data_ptr(), _DTYPE[dout.dtype], _addr(status),
                     workspace.data_ptr(), workspace.numel() * workspace.element_size()), "df_embedding_bwd")
     return grad
@@ -653,6 +665,11 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
     and values of another length, [B, Lk, Hk, d] (with an optional uint8 key_mask) or
     packed with cu_seqlens_k.  ``scale`` defaults to 1 / sqrt(d).  Returns ``out``, or
     (out, CrossStats) for a training step (``with_stats``)."""
+    if stream is not None:
+        with _current(stream, q):
+            return df_cross_attn_fwd(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+                                     max_seqlen_k=max_seqlen_k, scale=scale, out=out, with_stats=with_stats,
+                                     status=status)
     idx = _on_device((q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, out, status),
                      "q k v key_mask cu_seqlens_q cu_seqlens_k out status")
     B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
@@ -664,8 +681,10 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
         raise ValueError("out must match q in shape and dtype")
     if status is not None:
         _status_word(status)
-    stats = CrossStats(q.new_empty(q.shape[:-1], dtype=torch.float32), torch.empty_like(q)) if with_stats else None
-    _check(_call_on(idx, _lib.df_cross_attn_fwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask),
+    stats = None
+    if with_stats:
+        stats = CrossStats(torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device), torch.empty_like(q))
+    _check(_call_on(idx, _lib.df_cross_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask),
                     _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype],
                     out.data_ptr(), stats.out_lo.data_ptr() if stats else None,
                     stats.lse.data_ptr() if stats else None, _addr(status)), "df_cross_attn_fwd")
@@ -688,6 +707,11 @@ def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=Non
     """Gradients (dq, dk, dv), in the inputs' dtype, of ``df_cross_attn_fwd`` with the
     same arguments; ``out`` and ``stats`` as its call with ``with_stats`` gave them.
     ``grads`` may pass the three tensors preallocated."""
+    if stream is not None:
+        with _current(stream, q):
+            return df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k,
+                                     max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, scale=scale, grads=grads,
+                                     workspace=workspace, status=status)
     if grads is None:
         grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
     dq, dk, dv = grads
@@ -706,8 +730,8 @@ def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=Non
     if status is not None:
         _status_word(status)
     if workspace is None:
-        workspace = q.new_empty(max(df_cross_attn_bwd_workspace_size(Tq, H), 256), dtype=torch.uint8)
-    _check(_call_on(idx, _lib.df_cross_attn_bwd, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        workspace = torch.empty(max(df_cross_attn_bwd_workspace_size(Tq, H), 256), dtype=torch.uint8, device=q.device)
+    _check(_call_on(idx, _lib.df_cross_attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                     _addr(out_lo), lse.data_ptr(), dout.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q),
                     _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], dq.data_ptr(),
                     dk.data_ptr(), dv.data_ptr(), _addr(status), workspace.data_ptr(),

@@ -82,3 +82,25 @@ def test_training_step_down_to_the_table(lib):
     norm = lambda z: float(np.sqrt((z ** 2).sum()))  # noqa: E731
     assert norm(np64(grad) - want) <= 3 * 2.0 ** -8 * norm(want)
     assert (np64(grad)[3] == 0).all()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_given_as_an_argument(lib, handle):
+    # results and workspaces then belong to that stream: freed ones are not handed out
+    # to the current stream while it still runs
+    g = torch.Generator().manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    q, k, v, dout = n(4, 300, 4, 64), n(4, 500, 4, 64), n(4, 500, 4, 64), n(4, 300, 4, 64)
+    table, ids, drows = n(3000, 256), torch.randint(0, 3000, (9000,), generator=g).cuda(), n(9000, 256)
+    def run(**on):
+        o, stats = lib.df_cross_attn_fwd(q, k, v, with_stats=True, **on)
+        return (o, stats.lse, *lib.df_cross_attn_bwd(q, k, v, o, stats, dout, **on),
+                lib.df_embedding(ids, table, **on), lib.df_embedding_bwd(ids, drows, 3000, **on))
+    want = run()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = run(stream=side.cuda_stream if handle else side)
+        junk = [torch.full((4, 300, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 4
