@@ -9,8 +9,8 @@
 // order of arrival, so the tokens are sorted by id first (a stable radix sort
 // of (id, position) pairs) and every row of the table is then the sum of one
 // run of the sorted list, in ascending position:
-//   1. sort.  Up to 8192 tokens: one block, 8 bits per pass, pairs in shared
-//      memory.  More: 2048-key tiles, at most 10 bits per pass (two passes for
+//   1. sort.  Few tokens (to 8192): one block, 8 bits per pass, pairs in shared
+//      memory.  More: tiles of 512 or 2048 keys, at most 10 bits per pass (two passes for
 //      ids below 2^20); a pass counts the digits of each tile, scans each
 //      digit's counts over the tiles, and scatters (rank inside the tile by warp
 //      digit matching, so that equal digits keep their order).  Ids that pass no
@@ -37,8 +37,6 @@ namespace dfa {
 namespace {
 
 constexpr int kSortThreads = 256;
-constexpr int kSortItems = 8;                           // keys per thread
-constexpr int kSortTile = kSortThreads * kSortItems;    // keys per block
 constexpr int kMaxDigitBits = 10;
 constexpr int kSlice = 256;                             // columns per warp of the sums
 
@@ -203,15 +201,17 @@ __device__ __forceinline__ uint32_t digit_rank(uint32_t d, bool valid, uint32_t*
   return start + before;
 }
 
+// (ITEMS keys per thread, in both kernels)
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) digit_counts(const SortArgs a) {
   start_after_previous();
   if ((int)blockIdx.x >= a.blocks) return fill_share(a);
   __shared__ uint32_t cnt[1 << kMaxDigitBits];
   const int digits = 1 << a.bits;
-  uint32_t key[kSortItems];
-  const int base = blockIdx.x * kSortTile;
+  uint32_t key[ITEMS];
+  const int base = blockIdx.x * (kSortThreads * ITEMS);
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
+  for (int k = 0; k < ITEMS; ++k) {
     const int i = base + k * kSortThreads + threadIdx.x;
     key[k] = i < a.n ? sort_key(a, i) : 0u;
     if (a.first && i < a.n) a.key[i] = key[k];
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kSortThreads) digit_counts(const SortArgs a) {
   for (int d = threadIdx.x; d < digits; d += kSortThreads) cnt[d] = 0;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k)
+  for (int k = 0; k < ITEMS; ++k)
     if (base + k * kSortThreads + (int)threadIdx.x < a.n) atomicAdd(&cnt[(key[k] >> a.shift) & (digits - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < digits; d += kSortThreads) a.hist[(size_t)blockIdx.x * digits + d] = cnt[d];
@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(256) scan_over_tiles(const SortArgs a) {
   }
 }
 
-// Writes a tile's pairs to their places.  Warp w of the tile owns keys
-// [w 256, w 256 + 256) in rounds of 32, so that (warp, round, lane) is the
+// Writes a tile's pairs to their places.  Each warp of the tile owns
+// 32 ITEMS consecutive keys in rounds of 32, so that (warp, round, lane) is the
 // original order.
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs a) {
   start_after_previous();
   if ((int)blockIdx.x >= a.blocks) return fill_share(a);
@@ -268,10 +269,10 @@ __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs 
   __shared__ uint32_t warp_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int digits = 1 << a.bits;
-  const int base = blockIdx.x * kSortTile + warp * (kSortItems * 32);
-  uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
+  const int base = blockIdx.x * (kSortThreads * ITEMS) + warp * (ITEMS * 32);
+  uint32_t key[ITEMS], pos[ITEMS], rank[ITEMS];
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
+  for (int k = 0; k < ITEMS; ++k) {
     const int i = base + k * 32 + lane;
     key[k] = i < a.n ? a.key[i] : 0u;
     pos[k] = a.first ? (uint32_t)i : (i < a.n ? a.pos[i] : 0u);
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs 
     for (int w = 0; w < kWarps; ++w) cnt[w][d] = 0;
   uint32_t at_digit = block_exclusive(own, warp_sum);  // (also: the counts are cleared)
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k)
+  for (int k = 0; k < ITEMS; ++k)
     rank[k] = digit_rank((key[k] >> a.shift) & (digits - 1), base + k * 32 + lane < a.n, cnt[warp], lane);
   __syncthreads();
 #pragma unroll
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_by_digit(const SortArgs 
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
+  for (int k = 0; k < ITEMS; ++k) {
     if (base + k * 32 + lane >= a.n) continue;
     const uint32_t to = cnt[warp][(key[k] >> a.shift) & (digits - 1)] + rank[k];
     if (to >= (uint32_t)a.n) continue;  // only with a workspace that another call writes
@@ -564,13 +565,17 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct GradLayout {
   size_t key[2], pos[2], hist, digit_total, part, total;
-  int tiles, chunk, chunks, bits, passes;
+  int items, tiles, chunk, chunks, bits, passes;
   bool small;
 };
 
-GradLayout grad_layout(int T, int N, int V) {
+GradLayout grad_layout(int T, int N, int V, bool zeroed) {
   GradLayout l;
-  l.tiles = (T + kSortTile - 1) / kSortTile;
+  // keys per thread of a sorting block: small tiles spread few tokens over the SMs,
+  // large ones leave fewer counts to scan (whole gradient, 768 wide: 32768 tokens 59 us
+  // at 2, 72 at 8; 65536: 77, 95; 131072: 168, 148)
+  l.items = T <= 65536 ? 2 : 8;
+  l.tiles = (T + kSortThreads * l.items - 1) / (kSortThreads * l.items);
   // short chunks spread few tokens over more warps, long ones leave fewer partial
   // rows (whole gradient, bf16; 8192 x 1024: 45 us at 8, 57 at 32; 32768 x 768: 67 at
   // both; 131072 x 768: 164 at 8, 149 at 32)
@@ -578,7 +583,9 @@ GradLayout grad_layout(int T, int N, int V) {
   l.chunks = (T + l.chunk - 1) / l.chunk;
   int key_bits = 1;  // keys 0 .. V
   while (key_bits < 32 && ((unsigned long long)V >> key_bits) != 0) ++key_bits;
-  l.small = T <= kSmallSort;  // (2048 x 768: 34 us, 40 in tiles; 8192 x 1024: 45, 54)
+  // one block sorts what the zero fill hides (2048 x 768 into 50000 rows: 33 us, 34 in
+  // tiles; 8192 x 1024: 46, 49), or few tokens (added to the table: 17, 21; 38, 28)
+  l.small = T <= (zeroed ? kSmallSort : 2048);
   const int most = l.small ? kSmallBits : kMaxDigitBits;
   l.passes = (key_bits + most - 1) / most;
   l.bits = (key_bits + l.passes - 1) / l.passes;
@@ -669,7 +676,7 @@ extern "C" df_status df_embedding(const void* ids, int ids_64, int T, const void
 
 extern "C" size_t df_embedding_bwd_workspace_size(int T, int N, int V) {
   if (check_sizes(T, N, V) != DF_OK) return 0;
-  return std::max<size_t>(grad_layout(T, N, V).total, 256);
+  return std::max({grad_layout(T, N, V, false).total, grad_layout(T, N, V, true).total, (size_t)256});
 }
 
 extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const void* dout, int V, int N,
@@ -682,7 +689,7 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
   if (!grad || padding_idx < -1 || padding_idx >= V || (T > 0 && (!ids || !dout))) return DF_ERR_INVALID_ARG;
   if (((uintptr_t)ids & (ids_64 ? 7u : 3u)) != 0 || !al16(dout) || !al16(grad) || ((uintptr_t)workspace & 255u) != 0)
     return DF_ERR_ALIGNMENT;
-  const GradLayout l = grad_layout(T, N, V);
+  const GradLayout l = grad_layout(T, N, V, !accumulate);
   if (!workspace || workspace_bytes < std::max<size_t>(l.total, 256)) return DF_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   if (T == 0) {
@@ -725,6 +732,7 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
     const dim3 grid = grid_for(1, kSmallThreads, 1);
     if (!launch_next(sort_small, grid, kSmallThreads, kSmallSmem, s, a, l.passes)) return DF_ERR_CUDA;
   } else {
+    const bool few = l.items == 2;
     for (int p = 0; p < l.passes; ++p) {
       a.first = p == 0;
       a.shift = p * l.bits;
@@ -733,11 +741,11 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
       a.key_out = reinterpret_cast<uint32_t*>(base + l.key[p & 1]);
       a.pos_out = reinterpret_cast<uint32_t*>(base + l.pos[p & 1]);
       dim3 grid = grid_for(l.tiles, kSortThreads, 3);
-      if (!launch_next(digit_counts, grid, kSortThreads, 0, s, a)) return DF_ERR_CUDA;
+      if (!launch_next(few ? digit_counts<2> : digit_counts<8>, grid, kSortThreads, 0, s, a)) return DF_ERR_CUDA;
       grid = grid_for(((1 << l.bits) + 31) / 32, 256, 3);
       if (!launch_next(scan_over_tiles, grid, 256, 0, s, a)) return DF_ERR_CUDA;
       grid = grid_for(l.tiles, kSortThreads, 5);
-      if (!launch_next(scatter_by_digit, grid, kSortThreads, 0, s, a)) return DF_ERR_CUDA;
+      if (!launch_next(few ? scatter_by_digit<2> : scatter_by_digit<8>, grid, kSortThreads, 0, s, a)) return DF_ERR_CUDA;
     }
   }
   SumArgs u;

@@ -117,6 +117,20 @@ def test_gradient_is_added_to_where_asked(lib):
         lib.df_embedding_bwd(torch.from_numpy(ids).cuda(), dout, V, accumulate=True)
 
 
+@pytest.mark.parametrize("T", [1, 2048, 2049, 8192, 8193, 65536, 65537])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_around_the_sorts_limits(lib, T, accumulate):
+    # whole sums of small integers are exact in fp32, whatever their order
+    N, V = 8, 3001
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(0, V, (T,), generator=g)
+    dout = torch.randint(-4, 5, (T, N), generator=g).to(BF)
+    want = torch.zeros(V, N, dtype=torch.float64).index_add_(0, ids, dout.double())
+    grad = torch.full((V, N), 3.0, device="cuda")
+    lib.df_embedding_bwd(ids.cuda(), dout.cuda(), V, grad=grad, accumulate=accumulate)
+    assert torch.equal(grad.cpu().double(), want + 3.0 if accumulate else want)
+
+
 def test_padding_and_outside_rows_may_hold_anything(lib):
     ids = np.array([3, 0, -7, 5, 0, 3, 99, 5], dtype=np.int64)
     dout = torch.randn(8, 64)
