@@ -79,7 +79,8 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
   if (B < 0 || H < 1 || Hk < 1 || H % Hk != 0 || Lq < 0 || Lk < 0 || total_q < 0 || total_k < 0 || d < 1)
     return DF_ERR_INVALID_ARG;
   if (dtype != DF_BF16 && dtype != DF_FP16 && dtype != DF_FP32) return DF_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !(scale <= 3.0e38f) || (key_mask && cu_k)) return DF_ERR_INVALID_ARG;
+  // (scale log2(e) is finite too)
+  if (!(scale > 0.f) || !(scale <= 2.0e38f) || (key_mask && cu_k)) return DF_ERR_INVALID_ARG;
   if (!cu_q && (long long)B * Lq != total_q) return DF_ERR_INVALID_ARG;
   if (!cu_k && (long long)B * Lk != total_k) return DF_ERR_INVALID_ARG;
   if (dtype == DF_FP32 || d % 8 != 0 || d > 128 || H / Hk > 128) return DF_ERR_UNSUPPORTED;

@@ -480,7 +480,7 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  *               rows behind the last sequence get zeros (lse: -infinity); with
  *               cu_seqlens_q[0] > 0 the rows before the first one are left alone
  *   d           a multiple of 8, at most 128
- *   scale       > 0, finite
+ *   scale       > 0, at most 2e38
  *   dtype       DF_BF16 or DF_FP16, shared by q, k, v, out, out_lo
  *   out_lo      NULL, or like out: what rounding `out` to dtype dropped (rounded
  *               itself).  df_cross_attn_bwd needs it: the gradient subtracts

@@ -166,6 +166,44 @@ def test_no_keys_no_queries_no_sequences(lib):
     assert lib.df_cross_attn_fwd(z(0, 3, 4, 64), z(0, 9, 4, 64), z(0, 9, 4, 64)).numel() == 0
 
 
+def test_packed_rows_without_a_sequence(lib):
+    z = lambda *s: torch.ones(*s, dtype=BF, device="cuda")  # noqa: E731
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, stats = lib.df_cross_attn_fwd(z(300, 4, 64), z(200, 4, 64), z(200, 4, 64), cu_seqlens_q=cu, cu_seqlens_k=cu,
+                                       max_seqlen_q=0, max_seqlen_k=0, with_stats=True)
+    assert int((out != 0).sum()) == 0 and bool((stats.lse == -float("inf")).all())
+    grads = lib.df_cross_attn_bwd(z(300, 4, 64), z(200, 4, 64), z(200, 4, 64), out, stats, z(300, 4, 64),
+                                  cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=0, max_seqlen_k=0)
+    assert all(int((g != 0).sum()) == 0 for g in grads)
+
+
+@pytest.mark.parametrize("side", ["q", "k"])
+def test_offsets_beyond_32_bits(lib, side):
+    # two sequences, the second one's rows behind 2^32 values of the first one's
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    H, d, far = 16, 128, (1 << 32) // (16 * 128) + 77
+    x = inputs(1, H, H, d, 60, 300, BF, seed=4)
+    dev = to_dev(x)
+    want_out, stats = call(lib, x, dev, with_stats=True)
+    want = call_bwd(lib, x, dev, want_out, stats)
+    rows = {n: t[0] for n, t in dev.items() if n in ("q", "k", "v", "dout")}
+    cu = {}
+    for s, names, L in (("q", ("q", "dout"), 60), ("k", ("k", "v"), 300)):
+        front = far if s == side else 0
+        cu[s] = torch.tensor([0, front, front + L], dtype=torch.int32, device="cuda")
+        for n in names:
+            big = torch.zeros(front + L, H, d, dtype=BF, device="cuda")
+            big[front:] = rows[n]
+            rows[n] = big
+    kw = dict(cu_seqlens_q=cu["q"], cu_seqlens_k=cu["k"], max_seqlen_q=60, max_seqlen_k=300)
+    out, st = lib.df_cross_attn_fwd(rows["q"], rows["k"], rows["v"], with_stats=True, **kw)
+    assert torch.equal(out[-60:], want_out[0]) and torch.equal(st.lse[-60:], stats.lse[0])
+    got = lib.df_cross_attn_bwd(rows["q"], rows["k"], rows["v"], out, st, rows["dout"], **kw)
+    for g, w in zip(got, want):
+        assert torch.equal(g[-w.shape[1]:], w[0])
+
+
 def test_bad_offsets_are_reported(lib):
     x = inputs(3, 2, 2, 64, 40, 100, BF, "packed", "packed", seed=1, nq=[40, 40, 40], nk=[100, 90, 80])
     dev = to_dev(x)

@@ -196,3 +196,29 @@ def test_ids_that_change_meanwhile_do_no_harm(lib):
     torch.cuda.synchronize()
     got = lib.df_embedding_bwd(ids, dout, V, grad=guard[:V])
     assert torch.equal(got, lib.df_embedding_bwd(choices[0], dout, V))
+
+
+def test_offsets_beyond_32_bits(lib):
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    N = 2048
+    V = (1 << 32) // N + 40
+    table = torch.zeros(V, N, dtype=BF, device="cuda")
+    table[-40:] = torch.randn(40, N, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    ids = torch.cat([torch.arange(V - 40, V), torch.arange(V - 20, V), torch.zeros(3, dtype=torch.int64)]).cuda()
+    out = lib.df_embedding(ids, table)
+    assert torch.equal(out, table[ids])
+    grad = lib.df_embedding_bwd(ids, out, V)
+    want = torch.zeros(40, N, device="cuda")
+    want += table[-40:].float()
+    want[20:] *= 2
+    assert torch.equal(grad[-40:], want) and int(grad[:-40].count_nonzero()) == 0
+    del grad
+    # and many tokens: those behind 2^32 values of dout reach two rows
+    T = V
+    ids = torch.full((T,), 5, dtype=torch.int32, device="cuda")
+    ids[-40:] = 7
+    grad = lib.df_embedding_bwd(ids, table, 9)
+    assert int(grad[:7].count_nonzero()) == 0 and int(grad[8].count_nonzero()) == 0
+    # 40 additions, of partial sums below 64
+    assert torch.allclose(grad[7].double(), table[-40:].double().sum(0), rtol=0, atol=40 * 64 * 2.0 ** -24)
