@@ -71,21 +71,22 @@ __device__ __forceinline__ int seq_rows(const CrossSide& side, int b, int32_t* s
   return e - s;
 }
 
-// Bounded wait that gives up as soon as another role of the CTA has (and
-// records the timeout): the control flow after it stays the same either way.
+// Bounded wait that gives up as soon as another role of the CTA has; the control
+// flow after it stays the same either way.  (What ran out is reported once, by
+// cross_report at the kernel's end: this code stands in the kernels some thirty times.)
 __device__ __forceinline__ bool cross_wait(uint64_t* bar, uint32_t parity, unsigned long long budget,
-                                           volatile int* abort, int32_t* status) {
+                                           volatile int* abort) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  for (;;) {
-    if (*abort) return false;
-    if ((unsigned long long)(clock64() - t0) > budget) {
-      *abort = 1;
-      cross_fail(status, (int)DF_ERR_DEVICE_TIMEOUT);
-      return false;
-    }
+  do {
     if (ptx::mbar_try_wait(bar, parity)) return true;
-  }
+    if ((unsigned long long)(clock64() - t0) > budget) *abort = 1;
+  } while (*abort == 0);
+  return false;
+}
+// One thread, behind the CTA's last wait.
+__device__ __forceinline__ void cross_report(volatile int* abort, int32_t* status) {
+  if (*abort != 0) cross_fail(status, (int)DF_ERR_DEVICE_TIMEOUT);
 }
 
 // 3-D tiled load: column, head, token.
@@ -262,8 +263,8 @@ struct TileClaim {
     ++asked;
   }
   // The tile number taken over, or -1 when none is left.
-  __device__ __forceinline__ long long answer(unsigned long long budget, volatile int* abort, int32_t* status) {
-    const bool ok = cross_wait(bar, (asked - 1) & 1, budget, abort, status);
+  __device__ __forceinline__ long long answer(unsigned long long budget, volatile int* abort) {
+    const bool ok = cross_wait(bar, (asked - 1) & 1, budget, abort);
     // (the response must not be written into a CTA that has left)
     if (!ok) ptx::mbar_wait(bar, (asked - 1) & 1, kDrainBudget);
     uint32_t taken, x;

@@ -76,35 +76,51 @@ struct FwdSmem {
   static_assert(128 * D * 4 <= 4 * kTileBytes, "O fits over K and V");
 };
 
-// 32 columns of a warp's rows from the two teams' O: o = (a fa + b fb) inv (an O of
-// factor 0 may hold anything), rounded, and (out_lo) what that rounding dropped.
+// 32 columns of a warp's rows from the two teams' O: o = a fa + b fb, rounded, and
+// (out_lo) what that rounding dropped.  A step of 16 columns at a time changes hands
+// through 1 KB of shared memory, so that rows go out as 32 bytes each.  (A short
+// loop: code that runs once per item has left the instruction caches by then.)
 template <bool BF16, typename T>
 __device__ __forceinline__ void store_merged(const FwdArgs& args, uint8_t* stage, uint32_t ta, uint32_t tb, float fa,
-                                             float fb, float inv, int rel, size_t row0, int col) {
-  uint32_t hi[16], lo[16];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
+                                             float fb, bool empty, int rel, size_t row0, int col) {
+  const int lane = threadIdx.x & 31, d = args.c.d;
+  const float2 fa2 = make_float2(fa, fa), fb2 = make_float2(fb, fb);
+  uint8_t* mine = stage + lane * 32 + 16 * ((lane >> 2) & 1);  // the row's first 8 columns; the others at ^ 16
+#pragma unroll 1
+  for (int end = min(col + 32, d); col < end; col += 16, ta += 16, tb += 16) {
     uint32_t ra[16], rb[16];
-    tmem_ld16(ta + 16 * s, ra);
-    tmem_ld16(tb + 16 * s, rb);
+    tmem_ld16(ta, ra);
+    tmem_ld16(tb, rb);
     tmem_ld_wait(ra);
     tmem_ld_wait(rb);
+    uint32_t hi[8], lo[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float o[2];
+      const float2 b = mul2(make_float2(__uint_as_float(rb[2 * e]), __uint_as_float(rb[2 * e + 1])), fb2);
+      const float2 o = fma2(make_float2(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1])), fa2, b);
+      hi[e] = empty ? 0u : pack2<BF16>(o.x, o.y);
+      const T* t = reinterpret_cast<const T*>(&hi[e]);
+      lo[e] = empty ? 0u : pack2<BF16>(o.x - IO<T>::to_f(t[0]), o.y - IO<T>::to_f(t[1]));
+    }
+    const size_t at = row0 * d + col;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        o[k] = ((fa > 0.f ? __uint_as_float(ra[2 * e + k]) * fa : 0.f) +
-                (fb > 0.f ? __uint_as_float(rb[2 * e + k]) * fb : 0.f)) * inv;
-      const uint32_t h = pack2<BF16>(o[0], o[1]);
-      const T* t = reinterpret_cast<const T*>(&h);
-      hi[8 * s + e] = h;
-      lo[8 * s + e] = pack2<BF16>(o[0] - IO<T>::to_f(t[0]), o[1] - IO<T>::to_f(t[1]));
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 1 && !args.out_lo) break;
+      const uint32_t (&w)[8] = pass ? lo : hi;
+      *reinterpret_cast<uint4*>(mine) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>((uintptr_t)mine ^ 16) = make_uint4(w[4], w[5], w[6], w[7]);
+      __syncwarp();
+      T* dst = static_cast<T*>(pass ? args.out_lo : args.out) + at + 8 * (lane & 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * i + (lane >> 1);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 32 + 16 * ((lane ^ (r >> 2)) & 1));
+        const int to = __shfl_sync(0xffffffffu, rel, r);
+        if (to >= 0 && col + 8 * (lane & 1) < d) *reinterpret_cast<uint4*>(dst + (size_t)to * d) = v;
+      }
+      __syncwarp();
     }
   }
-  const size_t at = row0 * args.c.d + col;
-  store_rows32<T>(stage, hi, rel, static_cast<T*>(args.out) + at, args.c.d, args.c.d - col);
-  if (args.out_lo) store_rows32<T>(stage, lo, rel, static_cast<T*>(args.out_lo) + at, args.c.d, args.c.d - col);
 }
 
 // One step of 16 columns of one row, not rounded, for a cluster's join.
@@ -202,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   auto tO = [&](int w) { return tmem + 256u * w + kKeys; };
 
   const unsigned long long budget = a.budget;
-  int32_t* status = a.status;
   const uint32_t rank = args.splits > 1 ? cluster_rank() : 0u;
   auto part = [&](const CrossItem& it, int* t0) { return key_part(args, it, rank, t0); };
   // the c-th item handed out, for one thread; hk = -1 at the end or after an abort
@@ -211,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     CrossItem it;
     it.r0 = it.nr = it.o0 = it.no = it.b = 0;
     it.hk = -1;
-    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort, status)) {
+    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort)) {
       it = *ring_slot(c);
       mbar_arrive(item_empty + slot);
     }
@@ -232,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     // K or V rows [row, row + 128) for a team, its n-th tile
     auto load = [&](const CUtensorMap* map, uint32_t tiles, uint64_t* full, uint64_t* empty, int w, uint32_t& n, int head,
                     int row) {
-      ok = ok && cross_wait(empty + w, (n & 1) ^ 1, budget, s_abort, status);
+      ok = ok && cross_wait(empty + w, (n & 1) ^ 1, budget, s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       if (elect_one()) {
@@ -252,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         it.no = mask_n;
       }
       bool room = true;
-      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort);
       if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
       if (lane == 0 && room) {
         *ring_slot(c) = it;
@@ -263,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const int nt = part(it, &t0);
       if (nt > 0) {
         const uint32_t qb = qc % kQBufs;
-        ok = ok && cross_wait(q_empty + qb, ((qc / kQBufs) & 1) ^ 1, budget, s_abort, status);
+        ok = ok && cross_wait(q_empty + qb, ((qc / kQBufs) & 1) ^ 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           if (elect_one()) {
@@ -288,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         if (t >= 0) load(&maps.v, SL::v, v_full, v_empty, w, w ? vn1 : vn0, it.hk, row0 + t * kKeys);
         if (t + 2 < nt) load(&maps.k, SL::k, k_full, k_empty, w, w ? kn1 : kn0, it.hk, row0 + (t + 2) * kKeys);
       }
-      number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
+      number = args.splits > 1 ? -1 : claim.answer(budget, s_abort);
     }
     // no copy may still be landing when the CTA leaves
     if (elect_one()) {
@@ -322,12 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const int nt = part(it, &t0);
       if (nt == 0) continue;
       const uint32_t qb = qc % kQBufs;
-      ok = ok && cross_wait(q_full + qb, (qc / kQBufs) & 1, budget, s_abort, status);
+      ok = ok && cross_wait(q_full + qb, (qc / kQBufs) & 1, budget, s_abort);
       const uint64_t dq = uniform(sdesc_sw128(q_addr + qb * SL::kQBytes, 16, 1024));
       ++qc;
       // (P(t) overwrote its S: QK(t + 2) stands behind P(t).V in this warp's order)
       auto issue_qk = [&]() {
-        ok = ok && cross_wait(k_full + wg, kn & 1, budget, s_abort, status);
+        ok = ok && cross_wait(k_full + wg, kn & 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         ++kn;
         if (!ok) return;
@@ -344,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       if (wg < nt) issue_qk();
 #pragma unroll 1
       for (int t = wg; t < nt; t += 2) {
-        ok = ok && cross_wait(v_ready + wg, vn & 1, budget, s_abort, status);
-        ok = ok && cross_wait(p_full + wg, vn & 1, budget, s_abort, status);
+        ok = ok && cross_wait(v_ready + wg, vn & 1, budget, s_abort);
+        ok = ok && cross_wait(p_full + wg, vn & 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         ++vn;
         if (ok) {
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         bool whole = left >= kKeys && !a.key_mask;
         if (!whole)
           whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * kKeys : nullptr, left, bits);
-        ok = ok && cross_wait(v_full + w, n & 1, budget, s_abort, status);
+        ok = ok && cross_wait(v_full + w, n & 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && !whole) zero_rows<kWords, kChunks>(sm + SL::v + w * SL::kTileBytes, bits);
         __syncwarp();
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       // tile t = 2 i + w of the item is team w's i-th: the other one's t - 1 has the
       // number other_n + (t - 1) / 2 among its own
       for (int t = wg; t < nt; t += 2, ++n) {
-        cross_wait(s_full + wg, n & 1, budget, s_abort, status);
+        cross_wait(s_full + wg, n & 1, budget, s_abort);
         __syncwarp();
         tc_fence_after();
         if (warp_in) {
@@ -490,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
             m_run = mt;
             l_run *= rescale;
           }
-          if (t > 0) cross_wait(exp_done + (1 - wg), (other_n + ((t - 1) >> 1)) & 1, budget, s_abort, status);
+          if (t > 0) cross_wait(exp_done + (1 - wg), (other_n + ((t - 1) >> 1)) & 1, budget, s_abort);
           __syncwarp();
           const float shift = m_run == -INFINITY ? INFINITY : m_run;  // no finite score yet: every p is 0
           const float2 nshift = make_float2(-shift, -shift);
@@ -539,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         o_has = true;
       }
       // ---- the item's end: both teams' states together
-      if (wg < nt) cross_wait(o_final + wg, ic++ & 1, budget, s_abort, status);
+      if (wg < nt) cross_wait(o_final + wg, ic++ & 1, budget, s_abort);
       __syncwarp();
       tc_fence_after();
       sML[group * 128 + row] = make_float2(m_run, l_run);
@@ -563,9 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const int c0 = (((int)tid - 128) >> 7) * (D / 4);  // each of a row's four threads writes a quarter of its columns
       const uint32_t ta = tO(0) + ((tid & 96u) << 16), tb = ta + 256u;
       if (alone) {
+        // a team without a tile has no O (factor 0: the other one's stands in)
         if (warp_in && c0 < a.d)
-          store_merged<BF16, T>(args, sm + SL::stage + ((tid >> 5) - 4) * kRowStage, ta + c0, tb + c0, f0, f1, inv,
-                                      rel, row0, c0);
+          store_merged<BF16, T>(args, sm + SL::stage + ((tid >> 5) - 4) * kRowStage, ta + c0, (nt > 1 ? tb : ta) + c0,
+                                f0 * inv, nt > 1 ? f1 * inv : 0.f, nt == 0, rel, row0, c0);
         if (args.lse && c0 == 0 && rel >= 0) args.lse[row0 + rel] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       } else {
         float* sO = reinterpret_cast<float*>(sm + SL::k);  // K and V are idle by then
@@ -596,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
 template <bool BF16>

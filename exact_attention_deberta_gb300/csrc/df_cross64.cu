@@ -152,7 +152,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
   auto tO = [&](int b) { return tmem + 384u + (uint32_t)D * b; };
 
   const unsigned long long budget = a.budget;
-  int32_t* status = a.status;
   const uint32_t rank = args.splits > 1 ? cluster_rank() : 0u;
   auto part = [&](const CrossItem& it, int* t0) { return key_part(args, it, rank, t0); };
   // the c-th item handed out, for one thread; hk = -1 at the end or after an abort
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     CrossItem it;
     it.r0 = it.nr = it.o0 = it.no = it.b = 0;
     it.hk = -1;
-    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort, status)) {
+    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort)) {
       it = *ring_slot(c);
       mbar_arrive(item_empty + slot);
     }
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     auto load = [&](const CUtensorMap* map, uint32_t tiles, uint64_t* full, uint64_t* empty, uint32_t gs, int head, int row,
                     uint32_t& issued) {
       const uint32_t s = gs % R;
-      ok = ok && cross_wait(empty + s, ((gs / R) & 1) ^ 1, budget, s_abort, status);
+      ok = ok && cross_wait(empty + s, ((gs / R) & 1) ^ 1, budget, s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       if (elect_one()) {
@@ -202,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         it.no = mask_n;
       }
       bool room = true;
-      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort);
       if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
       if (lane == 0 && room) {
         *ring_slot(c) = it;
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       const int nt = part(it, &t0);
       if (nt > 0) {
         const uint32_t qb = qc & 1;
-        ok = ok && cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort, status);
+        ok = ok && cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           if (elect_one()) {
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         if (t > 0) load(&maps.v, SL::v, v_full, v_empty, g + t - 1, it.hk, row0 + t * 128 - 128, v_issued);
       }
       g += nt;
-      number = args.splits > 1 ? -1 : claim.answer(budget, s_abort, status);
+      number = args.splits > 1 ? -1 : claim.answer(budget, s_abort);
     }
     // no copy may still be landing when the CTA leaves
     if (elect_one()) {
@@ -273,15 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       if (nt == 0) continue;
       if (qk_role) {
         const uint32_t qb = qc & 1;
-        ok = ok && cross_wait(q_full + qb, (qc >> 1) & 1, budget, s_abort, status);
+        ok = ok && cross_wait(q_full + qb, (qc >> 1) & 1, budget, s_abort);
         const uint64_t dq = uniform(sdesc_sw128(q_addr + qb * SL::kTileBytes, 16, 1024));
 #pragma unroll 1
         for (int t = 0; t < nt; ++t) {
           const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
           const uint64_t dk = uniform(sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024));
           const uint32_t ts = uniform(tS(sb));
-          if (gs >= 3) ok = ok && cross_wait(buf_free + sb, ((gs - 3) / 3) & 1, budget, s_abort, status);
-          ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort, status);
+          if (gs >= 3) ok = ok && cross_wait(buf_free + sb, ((gs - 3) / 3) & 1, budget, s_abort);
+          ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
           tc_fence_after();
@@ -307,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
           const bool partial = a.key_mask || left < 128;
           // P of this tile says that S was there, so that P.V of the stage's previous
           // tile is done: the wait for V sees its own phase
-          ok = ok && cross_wait(p_full + 2 * pv_wg + (pn & 1), (pn >> 1) & 1, budget, s_abort, status);
-          ok = ok && cross_wait(v_full + s, (gs / R) & 1, budget, s_abort, status);
+          ok = ok && cross_wait(p_full + 2 * pv_wg + (pn & 1), (pn >> 1) & 1, budget, s_abort);
+          ok = ok && cross_wait(v_full + s, (gs / R) & 1, budget, s_abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
           if (partial) {
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     uint32_t own = 0, gbase = 0;  // this warpgroup's tiles, and the CTA's before the item
     auto pv_wait = [&](uint32_t n) {  // until P.V of its n-th tile is done
-      cross_wait(pv_done + 2 * wg + (n & 1), (n >> 1) & 1, budget, s_abort, status);
+      cross_wait(pv_done + 2 * wg + (n & 1), (n >> 1) & 1, budget, s_abort);
     };
     // One thread takes each item from the ring and leaves it in s_cur; all 256 read
     // it behind their barrier, so that they run the same list even after a wait
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       uint32_t sb = (gbase + wg) % 3, phase = ((gbase + wg) / 3) & 1;  // of tile gbase + t
       for (int t = wg; t < nt; t += 2, ++own) {
         const uint32_t tSw = tmem + 128u * sb + lane_off;
-        cross_wait(s_full + sb, phase, budget, s_abort, status);
+        cross_wait(s_full + sb, phase, budget, s_abort);
         __syncwarp();
         tc_fence_after();
         if (warp_in) {
@@ -554,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
 template <bool BF16>

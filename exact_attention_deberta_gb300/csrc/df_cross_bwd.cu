@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   auto tdP = [&](uint32_t b) { return tmem + kAccCols + 128u * b + 64u; };
 
   const unsigned long long budget = a.budget;
-  int32_t* status = a.status;
   const int x_step = KEYS ? 128 : a.tpt, y_step = KEYS ? a.tpt : 128;  // tokens per tile
   auto y_tiles = [&](const CrossItem& it) { return (it.no + y_step - 1) / y_step; };
   auto read_item = [&](uint32_t c) {  // one thread: the c-th item handed out, hk = -1 at the end
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     CrossItem it;
     it.r0 = it.nr = it.o0 = it.no = it.b = 0;
     it.hk = -1;
-    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort, status)) {
+    if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort)) {
       it = *ring_slot(c);
       mbar_arrive(item_empty + slot);
     }
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       }
       const uint32_t slot = c % kItemRing;
       bool room = true;
-      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort, status);
+      if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort);
       if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
       if (lane == 0 && room) {
         *ring_slot(c) = it;
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       const int x_head = KEYS ? it.hk : it.hk * a.G, y_head = KEYS ? it.hk * a.G : it.hk;
       if (nt > 0) {
         const uint32_t xb = xc % kRes;
-        ok = ok && cross_wait(x_empty + xb, ((xc / kRes) & 1) ^ 1, budget, s_abort, status);
+        ok = ok && cross_wait(x_empty + xb, ((xc / kRes) & 1) ^ 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           load(&maps.x0, &maps.x1, sm + SL::x + xb * 2 * SL::kTileBytes, x_box, x_head, it.r0, x_full + xb);
@@ -320,14 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         if (t == ask_at) claim.ask();
         if (t >= nt) break;
         const uint32_t s = g % kStages;
-        ok = ok && cross_wait(empty + s, ((g / kStages) & 1) ^ 1, budget, s_abort, status);
+        ok = ok && cross_wait(empty + s, ((g / kStages) & 1) ^ 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         ++g;
         if (!ok) continue;
         load(&maps.y0, &maps.y1, sm + SL::y + s * 2 * SL::kTileBytes, y_box, y_head, it.o0 + t * y_step, full + s);
         g_issued = g;
       }
-      number = claim.answer(budget, s_abort, status);
+      number = claim.answer(budget, s_abort);
     }
     // no copy may still be landing when the CTA leaves
     if (elect_one()) {
@@ -359,19 +358,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       const int nt = y_tiles(it);
       if (nt == 0) continue;
       const uint32_t xb = xc % kRes;
-      ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort, status);
+      ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort);
       const uint64_t dx = uniform(sdesc_sw128(smem_u32(sm + SL::x + (xb * 2 + which) * SL::kTileBytes), 16, 1024));
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, ++g) {
         const uint32_t s = g % kStages;
-        ok = ok && cross_wait(ready + s, (g / kStages) & 1, budget, s_abort, status);
+        ok = ok && cross_wait(ready + s, (g / kStages) & 1, budget, s_abort);
         const uint32_t y_addr = smem_u32(sm + SL::y + (s * 2 + which) * SL::kTileBytes);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const uint32_t u = 2 * g + h, b = u % kBufs;
           const uint64_t dy = uniform(sdesc_sw128(y_addr + h * 8192, 16, 1024));
           const uint32_t to = uniform(tD + 128u * b);
-          if (u >= kBufs) ok = ok && cross_wait(free_bar + b, (u / kBufs - 1) & 1, budget, s_abort, status);
+          if (u >= kBufs) ok = ok && cross_wait(free_bar + b, (u / kBufs - 1) & 1, budget, s_abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
           tc_fence_after();
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         const int nt = y_tiles(it);
         if (nt == 0) continue;
         // the epilogue has read the previous item's sums
-        if (xc > 0) ok = ok && cross_wait(acc_free, (xc - 1) & 1, budget, s_abort, status);
+        if (xc > 0) ok = ok && cross_wait(acc_free, (xc - 1) & 1, budget, s_abort);
 #pragma unroll 1
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t s = g % kStages;
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
             const uint64_t dy = uniform(vtile_desc(y_addr, 4 * h));
             const uint32_t from = uniform(tA + 128u * b);
             const uint32_t first = uniform(t == 0 && h == 0 ? 0u : 1u);
-            ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort, status);
+            ok = ok && cross_wait(p_full + b, (u / kBufs) & 1, budget, s_abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             tc_fence_after();
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         } else {
           whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)t * 128 : nullptr, left, bits);
         }
-        ok = ok && cross_wait(full + s, (g / kStages) & 1, budget, s_abort, status);
+        ok = ok && cross_wait(full + s, (g / kStages) & 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         uint8_t* sY = sm + SL::y + s * 2 * SL::kTileBytes;
@@ -549,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         const uint32_t s = (g + t) % kStages, u = 2 * (g + t) + h, b = u % kBufs;
         // (the buffer's previous half is the other warpgroup's u - 3 at three buffers;
         // its scores stand before those of u - 2, which this warp has seen)
-        cross_wait(s_full + b, (u / kBufs) & 1, budget, s_abort, status);
+        cross_wait(s_full + b, (u / kBufs) & 1, budget, s_abort);
         __syncwarp();
         tc_fence_after();
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
@@ -636,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         if (lane == 0) mbar_arrive(p_full + b);
       }
       // ---- the item's results
-      if (nt > 0) cross_wait(acc_full, xc & 1, budget, s_abort, status);
+      if (nt > 0) cross_wait(acc_full, xc & 1, budget, s_abort);
       __syncwarp();
       tc_fence_after();
       const int heads = KEYS ? a.Hk : a.H;
@@ -674,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0) cross_report(s_abort, a.status);
   if (!KEYS && args.after_keys) grid_dependency_wait();
 }
 
