@@ -60,7 +60,8 @@ struct FwdSmem {
   static constexpr uint32_t ml = v + 2 * kTileBytes;      // float2 (max, sum) [4 warpgroups][128]
   static constexpr uint32_t mx = ml + 4 * 128 * 8;                  // float [2 tiles][4 warpgroups][128]: row maxima
   static constexpr uint32_t mj = mx + 2 * 4 * 128 * 4;              // float4 [128]: a cluster's (max, sum)
-  static constexpr uint32_t stage = mj + 128 * 16;                  // [16 warps] rows on their way out
+  static constexpr uint32_t rows = mj + 128 * 16;                   // int2 [128]: a row's token, and its place from the tile's first
+  static constexpr uint32_t stage = rows + 128 * 8;                  // [16 warps] rows on their way out
   static constexpr uint32_t bars = stage + 16 * kRowStage;
   // q_full, q_empty [2]; k_full, k_empty, v_full, v_ready, v_empty [2];
   // s_full, p_full, exp_done, o_final, drain [2]; item_full, item_empty; claim
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   float2* sML = reinterpret_cast<float2*>(sm + SL::ml);
   float* sMax = reinterpret_cast<float*>(sm + SL::mx);
   float4* sJoin = reinterpret_cast<float4*>(sm + SL::mj);
+  int2* sRow = reinterpret_cast<int2*>(sm + SL::rows);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SL::bars);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 2;
@@ -205,6 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
+  }
+  if (threadIdx.x < 128) {
+    const int tok = threadIdx.x / a.G;
+    sRow[threadIdx.x] = make_int2(tok, tok * a.H + (int)threadIdx.x - tok * a.G);
   }
   if (warp == 1) {
     tmem_alloc(tslot, 512);
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const int nt = part(it, &t0);
       // a row block without a valid row needs no weights: its P may hold anything,
       // since a row of P only reaches its own row of O
-      const bool warp_in = __any_sync(0xffffffffu, row / a.G < it.nr);
+      const bool warp_in = __any_sync(0xffffffffu, sRow[row].x < it.nr);
       float m_run = -INFINITY, l_run = 0.f;  // l_run: this thread's columns only
       bool o_has = false;
       // The teams take turns at the exponentials, in the order of the tiles: left
@@ -566,15 +572,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const float f1 = s2.x != -INFINITY ? ex2(s2.x - m) : 0.f;
       const float l = (s0.y + s1.y) * f0 + (s2.y + s3.y) * f1;
       const bool alone = args.splits == 1;
-      const float inv = !alone ? 1.f : (l != 0.f ? 1.f / l : 0.f);
+      const float inv = !alone ? 1.f : (l != 0.f ? rcp(l) : 0.f);
       // (what only the results' places need is formed again here: held over the loop
       // above, it would spill there)
       const CrossItem end = *s_cur;
       uint32_t tid;
       asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
-      const int end_row = tid & 127, end_tok = end_row / a.G;
+      const int end_row = tid & 127;
+      const int2 place = sRow[end_row];
       const size_t row0 = (size_t)end.r0 * a.H + (size_t)end.hk * a.G;
-      const int rel = end_tok < end.nr && *s_abort == 0 ? end_tok * a.H + end_row - end_tok * a.G : -1;
+      const int rel = place.x < end.nr && *s_abort == 0 ? place.y : -1;
       const int c0 = (((int)tid - 128) >> 7) * (D / 4);  // each of a row's four threads writes a quarter of its columns
       const uint32_t ta = tO(0) + ((tid & 96u) << 16), tb = ta + 256u;
       if (alone) {
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         if (warp_in && c0 < a.d)
           store_merged<BF16, T>(args, sm + SL::stage + ((tid >> 5) - 4) * kRowStage, ta + c0, (nt > 1 ? tb : ta) + c0,
                                 f0 * inv, nt > 1 ? f1 * inv : 0.f, nt == 0, rel, row0, c0);
-        if (args.lse && c0 == 0 && rel >= 0) args.lse[row0 + rel] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (args.lse && c0 == 0 && rel >= 0) args.lse[row0 + rel] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
       } else {
         float* sO = reinterpret_cast<float*>(sm + SL::k);  // K and V are idle by then
         if (warp_in) {

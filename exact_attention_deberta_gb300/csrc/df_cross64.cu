@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       const float l = s0.y * f0 + s1.y * f1;
       const bool alone = args.splits == 1;
       // (a NaN among the scores of keys that count is in l, and stays in the row)
-      const float inv = !alone ? 1.f : (l != 0.f ? 1.f / l : 0.f);
+      const float inv = !alone ? 1.f : (l != 0.f ? rcp(l) : 0.f);
       const size_t orow = ((size_t)(it.r0 + row_tok) * a.H + (size_t)it.hk * a.G + row_head);
       float* sO = reinterpret_cast<float*>(sm + SL::k);  // a cluster's join: the K tiles are idle by then
 #pragma unroll 1
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       if (!alone) {
         if (wg == 0) sML[256 + row] = make_float4(m, l, 0.f, 0.f);
       } else if (args.lse && wg == 0 && row_in && *s_abort == 0) {
-        args.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        args.lse[orow] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
       }
       tc_fence_before();
       named_sync(3, 256);  // every thread has read s_cur and sML

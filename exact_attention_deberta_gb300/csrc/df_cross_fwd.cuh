@@ -56,6 +56,20 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
+// 1 / x and log2 x by the hardware's approximations (a unit and 2^-22 off, of sums whose
+// exponentials are that much off themselves; short, for code that runs once per item
+// and has left the instruction caches by then).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Word offset of a 4-column piece of a row in a cluster's join buffer (pieces
 // rotated by row, so that the rows of a warp fall in different banks).
 template <int D>
@@ -107,14 +121,14 @@ __device__ __forceinline__ void join_cluster(const FwdArgs& args, const CrossIte
         o[3] += v.w * f;
       }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? rcp(l) : 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] *= inv;
     const size_t orow = (size_t)(it.r0 + tok) * a.H + (size_t)it.hk * a.G + (row - tok * a.G);
     const size_t at = orow * a.d + 4 * piece;
     store_rounded<T, 4>(static_cast<T*>(args.out) + at, args.out_lo ? static_cast<T*>(args.out_lo) + at : nullptr,
                         o);
-    if (args.lse && piece == 0) args.lse[orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (args.lse && piece == 0) args.lse[orow] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
   }
 }
 
