@@ -68,7 +68,7 @@ struct FwdSmem {
   static constexpr int kBars = 24 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax threads' current item
-  static constexpr uint32_t claim = cur + 32;                       // 16 bytes
+  static constexpr uint32_t claim = cur + 64;                       // 16 bytes
   static constexpr uint32_t misc = claim + 16;                      // abort flag, tmem slot
   static constexpr uint32_t bytes = misc + 16;
   static constexpr uint32_t alloc = bytes + 1024;
@@ -446,11 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     // it behind their barrier, so that they run the same list even after a wait
     // has run out.
     const bool reader = warp == 4 && lane == 0;
-    uint32_t c = 0;
-    if (reader) *s_cur = read_item(c++);
+    uint32_t c = 1;  // items taken, of which the last but one is current at an item's end
+    if (reader) s_cur[0] = read_item(0);
     named_sync(9, kSoftmaxThreads);
     for (;;) {
-      const CrossItem it = *s_cur;
+      const CrossItem it = s_cur[~c & 1];
       if (it.hk < 0) break;
       int t0;
       const int nt = part(it, &t0);
@@ -560,6 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         o_has = true;
       }
       // ---- the item's end: both teams' states together
+      if (reader) s_cur[c & 1] = read_item(c);  // the next one
+      ++c;
       if (wg < nt) cross_wait(o_final + wg, ic++ & 1, budget, s_abort);
       __syncwarp();
       tc_fence_after();
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const float inv = !alone ? 1.f : (l != 0.f ? rcp(l) : 0.f);
       // (what only the results' places need is formed again here: held over the loop
       // above, it would spill there)
-      const CrossItem end = *s_cur;
+      const CrossItem end = s_cur[c & 1];
       uint32_t tid;
       asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
       const int end_row = tid & 127;
@@ -600,11 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         if (c0 == 0) sJoin[end_row] = make_float4(m, l, 0.f, 0.f);
       }
       tc_fence_before();
-      named_sync(9, kSoftmaxThreads);  // every thread has read s_cur and sML
+      named_sync(9, kSoftmaxThreads);  // every thread has read sML and s_cur[c & 1]
       other_n += wg ? (nt + 1) >> 1 : nt >> 1;
       if (!alone) break;  // one item per cluster; s_cur stays for the join
-      if (reader) *s_cur = read_item(c++);
-      named_sync(9, kSoftmaxThreads);
     }
   }
 

@@ -63,7 +63,7 @@ struct FwdSmem {
   static constexpr int kBars = 4 + 4 * kStages + 9 + 8 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // the softmax warpgroups' current item
-  static constexpr uint32_t claim = cur + 32;                       // 16 bytes
+  static constexpr uint32_t claim = cur + 64;                       // 16 bytes
   static constexpr uint32_t misc = claim + 16;                      // abort flag, tmem slot
   static constexpr uint32_t bytes = misc + 16;
   static constexpr uint32_t alloc = bytes + 1024;
@@ -355,11 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     // it behind their barrier, so that they run the same list even after a wait
     // has run out.
     const bool reader = warp == 4 && lane == 0;
-    uint32_t c = 0;
-    if (reader) *s_cur = read_item(c++);
+    uint32_t c = 1;  // items taken, of which the last but one is current at an item's end
+    if (reader) s_cur[0] = read_item(0);
     named_sync(3, 256);
     for (;;) {
-      const CrossItem it = *s_cur;
+      const CrossItem it = s_cur[~c & 1];
       if (it.hk < 0) break;
       int t0;
       const int nt = part(it, &t0);
@@ -485,6 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         }
       }
       // ---- the item's end: both warpgroups' states together
+      if (reader) s_cur[c & 1] = read_item(c);  // the next one
+      ++c;
       if (wg < nt) pv_wait(own - 1);  // its last P.V
       __syncwarp();
       tc_fence_after();
@@ -534,11 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         args.lse[orow] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
       }
       tc_fence_before();
-      named_sync(3, 256);  // every thread has read s_cur and sML
+      named_sync(3, 256);  // every thread has read sML and s_cur[c & 1]
       gbase += nt;
       if (!alone) break;  // one item per cluster; s_cur stays for the join
-      if (reader) *s_cur = read_item(c++);
-      named_sync(3, 256);
     }
   }
 

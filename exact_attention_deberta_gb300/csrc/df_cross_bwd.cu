@@ -141,7 +141,7 @@ struct BwdSmem {
   static constexpr int kBars = 2 * kRes + 3 * kStages + 12 + 6 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t cur = ring + 32 * kItemRing;
-  static constexpr uint32_t claim = cur + 32;  // 16 bytes
+  static constexpr uint32_t claim = cur + 64;  // 16 bytes
   static constexpr uint32_t misc = claim + 16;
   static constexpr uint32_t bytes = misc + 16;
   static constexpr uint32_t alloc = bytes + 1024;
@@ -524,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     const float scale1 = BF16 ? 1.f : exp2f(-kPShift);           // dv
     const int row_tok = KEYS ? row : row / a.G, row_head = KEYS ? 0 : row - row_tok * a.G;
     const bool reader = warp == kFirst && lane == 0;
-    uint32_t g = 0, xc = 0, c = 0;
-    if (reader) *s_cur = read_item(c++);
+    uint32_t g = 0, xc = 0, c = 1;  // c: items taken, of which the last but one is current at an item's end
+    if (reader) s_cur[0] = read_item(0);
     named_sync(3, 256);
     for (;;) {
-      const CrossItem it = *s_cur;
+      const CrossItem it = s_cur[~c & 1];
       if (it.hk < 0) break;
       const int nt = y_tiles(it);
       const bool stored = row_tok < it.nr;   // the resident row belongs to the sequence
@@ -635,6 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         if (lane == 0) mbar_arrive(p_full + b);
       }
       // ---- the item's results
+      if (reader) s_cur[c & 1] = read_item(c);  // the next one
+      ++c;
       if (nt > 0) cross_wait(acc_full, xc & 1, budget, s_abort);
       __syncwarp();
       tc_fence_after();
@@ -663,9 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         ++xc;
       }
       g += nt;
-      named_sync(3, 256);  // every thread has read s_cur
-      if (reader) *s_cur = read_item(c++);
-      named_sync(3, 256);
+      named_sync(3, 256);  // the next item is there, and every thread has read s_cur[c & 1]
     }
   }
 
