@@ -28,14 +28,15 @@
 // part of the key tiles; the partial (max, sum, O) are joined through
 // distributed shared memory, so no workspace and no second launch is needed.
 //
-// Measured (GB300): 16 x 12 heads, 2048 queries x 8192 keys, bf16: 732 us, 1127
-// TFLOP/s.  A tile of 128 x 128 scores takes about 1040 cycles of an SM; its
+// Measured (GB300): 16 x 12 heads, 2048 queries x 8192 keys, bf16: 713 us, 1157
+// TFLOP/s.  A tile of 128 x 128 scores takes about 1020 cycles of an SM; its
 // products take 618 of the tensor core (P.V, 64 columns wide, runs at two thirds
 // of its rate), its exponentials 512.  What is left is latency: a score buffer goes
-// around S, softmax (1470 cycles), P.V, S in about 3 x 1040.  Of what would shorten
+// around S, softmax (1470 cycles), P.V, S in about 3 x 1020.  Of what would shorten
 // that, P in columns of its own (two score buffers: 857 us, with the warpgroups
 // taking turns 914), P.V in two halves (810), scores read twice in short loops
-// (828) and one warp issuing both products in order (1138) were slower.
+// (828) and one warp issuing both products in order (1138) were slower (735 at the
+// time).
 #include "df_cross_fwd.cuh"
 
 namespace dfa {

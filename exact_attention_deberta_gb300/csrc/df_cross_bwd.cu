@@ -29,13 +29,13 @@
 //                 (they are the reduction dimension of the second products)
 //   warps 8-15    P and dS, one thread per resident row; the epilogue
 //
-// Measured (GB300, bf16): 16 x 12 heads, 2048 queries x 8192 keys, d = 64: 2.39 ms
-// (10 flops per score and column: 863 TFLOP/s; with the two products that are done
-// twice 1208); 19 x 8 heads, d = 128: 3.46 ms (944, 1322).  Bound by the tensor core:
+// Measured (GB300, bf16): 16 x 12 heads, 2048 queries x 8192 keys, d = 64: 2.31 ms
+// (10 flops per score and column: 892 TFLOP/s; with the two products that are done
+// twice 1249); 19 x 8 heads, d = 128: 3.39 ms (963, 1348).  Bound by the tensor core:
 // S and dP in halves of 64 columns run at two thirds of its rate, so a 128 x 128 tile
-// takes at least 1498 (keys) or 1138 (queries) cycles at d = 64 and takes 1774 and
-// 1330; 2591 and 2074 at d = 128, and takes 3615 and 2630 (only two buffers in the
-// first).  Whole tiles (128 columns) would leave one buffer and no overlap.
+// takes at least 1498 (keys) or 1138 (queries) cycles at d = 64 and takes about 1700
+// and 1290; 2591 and 2074 at d = 128, and takes about 3500 and 2600 (only two buffers
+// in the first).  Whole tiles (128 columns) would leave one buffer and no overlap.
 //
 // fp16: dS spans too wide a range for its exponent, so it is scaled by a power of
 // two that puts the largest |dout_i| at about 16, and P (at most 1) by 2^14; the
@@ -604,12 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
             half_rows(rs1, rd1, 1);
           }
         } else {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t rs[32], rd[32];
-            tmem_ld32(tS(b) + lane_off + 32 * q, rs);
-            tmem_ld32(tdP(b) + lane_off + 32 * q, rd);
-            tmem_ld_wait2(rs, rd);
+          // 32 columns at a time, the second loads in flight meanwhile
+          uint32_t rs0[32], rd0[32], rs1[32], rd1[32];
+          tmem_ld32(tS(b) + lane_off, rs0);
+          tmem_ld32(tdP(b) + lane_off, rd0);
+          tmem_ld_wait2(rs0, rd0);
+          tmem_ld32(tS(b) + lane_off + 32, rs1);
+          tmem_ld32(tdP(b) + lane_off + 32, rd1);
+          auto columns = [&](const uint32_t (&rs)[32], const uint32_t (&rd)[32], int q) {
             uint32_t wd[16];
             const uint32_t bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
 #pragma unroll
@@ -629,7 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
               }
             }
             tmem_st16(tdP(b) + lane_off + 16 * q, wd);
-          }
+          };
+          columns(rs0, rd0, 0);
+          tmem_ld_wait2(rs1, rd1);
+          columns(rs1, rd1, 1);
         }
         tmem_st_wait();
         tc_fence_before();
