@@ -99,7 +99,8 @@ __device__ __forceinline__ void store_merged(const FwdArgs& args, uint8_t* stage
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float2 b = mul2(make_float2(__uint_as_float(rb[2 * e]), __uint_as_float(rb[2 * e + 1])), fb2);
+      float2 b = mul2(make_float2(__uint_as_float(rb[2 * e]), __uint_as_float(rb[2 * e + 1])), fb2);
+      if (fb == 0.f) b = make_float2(0.f, 0.f);  // (its O may hold anything)
       const float2 o = fma2(make_float2(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1])), fa2, b);
       hi[e] = empty ? 0u : pack2<BF16>(o.x, o.y);
       const T* t = reinterpret_cast<const T*>(&hi[e]);
@@ -589,10 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const int c0 = (((int)tid - 128) >> 7) * (D / 4);  // each of a row's four threads writes a quarter of its columns
       const uint32_t ta = tO(0) + ((tid & 96u) << 16), tb = ta + 256u;
       if (alone) {
-        // a team without a tile has no O (factor 0: the other one's stands in)
         if (warp_in && c0 < a.d)
-          store_merged<BF16, T>(args, sm + SL::stage + ((tid >> 5) - 4) * kRowStage, ta + c0, (nt > 1 ? tb : ta) + c0,
-                                f0 * inv, nt > 1 ? f1 * inv : 0.f, nt == 0, rel, row0, c0);
+          store_merged<BF16, T>(args, sm + SL::stage + ((tid >> 5) - 4) * kRowStage, ta + c0, tb + c0, f0 * inv, f1 * inv,
+                                nt == 0, rel, row0, c0);
         if (args.lse && c0 == 0 && rel >= 0) args.lse[row0 + rel] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
       } else {
         float* sO = reinterpret_cast<float*>(sm + SL::k);  // K and V are idle by then

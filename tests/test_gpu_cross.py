@@ -117,6 +117,19 @@ def test_nan_that_counts_stays_in_its_rows(lib, B, d, Lq, Lk):
     assert torch.equal(got[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lk", [40, 200, 300])
+def test_infinite_value_that_counts_is_the_result(lib, d, Lk):
+    x = inputs(200, 2, 2, d, 30, Lk, BF, seed=2)
+    dev = to_dev(x)
+    clean = call(lib, x, dev)
+    dev["v"][3, Lk - 1, 1, 5] = float("inf")
+    got = call(lib, x, dev)
+    assert bool((got[3, :, 1, 5] == float("inf")).all())
+    got[3, :, 1, 5] = clean[3, :, 1, 5]
+    assert torch.equal(got, clean)
+
+
 def test_two_calls_at_once(lib):
     # on two streams, each with its own tiles to hand out
     xs = [inputs(24, 4, 4, 64, 150, 700, BF, "packed", "packed", seed=s) for s in (1, 2)]
