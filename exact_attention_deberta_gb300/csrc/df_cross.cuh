@@ -185,8 +185,8 @@ __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
 // Finds the tiles of one side by number, warp-collectively.  Tiles of `step`
 // tokens are numbered by sequence, then key head, then position; in packed mode
 // the rows behind the last sequence count as one more sequence, whose other
-// side is empty.  The walk over the sequences goes on from the last call's number
-// and starts over for a smaller one.
+// side is empty.  The walk over packed sequences goes on from the last call's number,
+// in either direction.
 struct TileWalk {
   int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones
   long long done = 0;  // tiles of the sequences before b0
@@ -194,49 +194,66 @@ struct TileWalk {
   __device__ __forceinline__ CrossItem find(const CrossArgs& a, const CrossSide& rows, const CrossSide& other,
                                             int step, long long number) {
     const int lane = threadIdx.x & 31;
-    const int last = rows.cu ? a.B : a.B - 1;
     CrossItem it;
     it.hk = -1;
     it.r0 = it.nr = it.o0 = it.no = it.b = 0;
     if (number < 0) return it;
-    if (number < done) {
-      b0 = 0;
-      done = 0;
-    }
-    for (; b0 <= last; b0 += 32) {
-      const int b = b0 + lane;
-      int start = 0, n = 0;
-      if (b < a.B) {
-        n = seq_rows(rows, b, a.status, &start);
-      } else if (b == last) {
-        start = min(max(rows.cu[a.B], 0), rows.total);
-        n = rows.total - start;
-      }
-      const int tiles = (n + step - 1) / step;
-      long long incl = (long long)tiles * a.Hk;
-      const long long own = incl;
+    int first, len, tiles, at;  // the sequence's rows and tiles, the tile's number in it
+    if (!rows.cu) {
+      tiles = (rows.len + step - 1) / step;
+      const long long per = (long long)tiles * a.Hk;
+      if (number >= per * a.B) return it;
+      it.b = (int)(number / per);
+      at = (int)(number - it.b * per);
+      first = it.b * rows.len;
+      len = rows.len;
+    } else {
+      for (;;) {
+        bool back = number < done;
+        if (back && b0 == 0) {  // (only with offsets that change meanwhile)
+          back = false;
+          done = 0;
+        }
+        if (back) b0 -= 32;
+        if (b0 > a.B) return it;
+        const int b = b0 + lane;
+        int start = 0, n = 0;
+        if (b < a.B) {
+          n = seq_rows(rows, b, a.status, &start);
+        } else if (b == a.B) {
+          start = min(max(rows.cu[a.B], 0), rows.total);
+          n = rows.total - start;
+        }
+        const int nt = (n + step - 1) / step;
+        const long long own = (long long)nt * a.Hk;
+        long long incl = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      const long long total = __shfl_sync(0xffffffffu, incl, 31);
-      if (number < done + total) {
-        const unsigned hit = __ballot_sync(0xffffffffu, number < done + incl);
-        const int src = __ffs(hit) - 1;
-        const int at = (int)(number - done - __shfl_sync(0xffffffffu, incl - own, src));
-        const int nt = __shfl_sync(0xffffffffu, tiles, src);
-        const int s = __shfl_sync(0xffffffffu, start, src), len = __shfl_sync(0xffffffffu, n, src);
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += u;
+        }
+        const long long total = __shfl_sync(0xffffffffu, incl, 31);
+        if (back) done -= total;
+        if (number < done) continue;
+        if (number >= done + total) {
+          done += total;
+          b0 += 32;
+          continue;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, number < done + incl)) - 1;
+        at = (int)(number - done - __shfl_sync(0xffffffffu, incl - own, src));
+        tiles = __shfl_sync(0xffffffffu, nt, src);
+        first = __shfl_sync(0xffffffffu, start, src);
+        len = __shfl_sync(0xffffffffu, n, src);
         it.b = b0 + src;
-        it.hk = at / nt;
-        const int tok = (at - it.hk * nt) * step;
-        it.r0 = s + tok;
-        it.nr = min(step, len - tok);
-        if (it.b < a.B) it.no = seq_rows(other, it.b, a.status, &it.o0);
-        return it;
+        break;
       }
-      done += total;
     }
+    it.hk = at / tiles;
+    const int tok = (at - it.hk * tiles) * step;
+    it.r0 = first + tok;
+    it.nr = min(step, len - tok);
+    if (it.b < a.B) it.no = seq_rows(other, it.b, a.status, &it.o0);
     return it;
   }
 };

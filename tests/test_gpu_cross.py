@@ -130,6 +130,28 @@ def test_infinite_value_that_counts_is_the_result(lib, d, Lk):
     assert torch.equal(got, clean)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_very_many_short_sequences(lib, d):
+    # tiles are found by number: parts of the batch give the same bits
+    B, H, Hk = 20000, 4, 2
+    x = inputs(B, H, Hk, d, 4, 8, BF, "packed", "packed", seed=d)
+    dev = to_dev(x)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, stats = call(lib, x, dev, with_stats=True, status=status)
+    grads = call_bwd(lib, x, dev, out, stats, status=status)
+    assert int(status.item()) == lib.DF_OK
+    for b in (0, 9990, B - 100):
+        q, k = (slice(int(x[c][b]), int(x[c][b + 100])) for c in ("cu_q", "cu_k"))
+        part = dict(x, Lq=4, Lk=8)
+        on = dict(q=dev["q"][q], k=dev["k"][k], v=dev["v"][k], dout=dev["dout"][q], key_mask=None,
+                  cu_q=(dev["cu_q"][b:b + 101] - q.start).contiguous(),
+                  cu_k=(dev["cu_k"][b:b + 101] - k.start).contiguous())
+        o, s = call(lib, part, on, with_stats=True)
+        g = call_bwd(lib, part, on, o, s)
+        assert torch.equal(o, out[q]) and torch.equal(s.lse, stats.lse[q])
+        assert torch.equal(g[0], grads[0][q]) and torch.equal(g[1], grads[1][k]) and torch.equal(g[2], grads[2][k])
+
+
 def test_two_calls_at_once(lib):
     # on two streams, each with its own tiles to hand out
     xs = [inputs(24, 4, 4, 64, 150, 700, BF, "packed", "packed", seed=s) for s in (1, 2)]
