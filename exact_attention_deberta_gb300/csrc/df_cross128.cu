@@ -569,7 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       __syncwarp();
       tc_fence_after();
       sML[group * 128 + row] = make_float2(m_run, l_run);
+      // (each thread goes on to read both teams' O, and has waited for its own one's P.V
+      // only: the barrier has to order the other's tensor memory too)
+      tc_fence_before();
       named_sync(9, kSoftmaxThreads);
+      tc_fence_after();
       const float2 s0 = sML[row], s1 = sML[128 + row], s2 = sML[256 + row], s3 = sML[384 + row];
       const float m = fmaxf(s0.x, s2.x);
       // a team without a tile, or without a valid key, has -infinity: its O is not read

@@ -492,7 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       __syncwarp();
       tc_fence_after();
       sML[wg * 128 + row] = make_float4(m_run, l_run, o_has ? 1.f : 0.f, 0.f);
+      // (each thread goes on to read both warpgroups' O, and has waited for its own one's
+      // P.V only: the barrier has to order the other's tensor memory too)
+      tc_fence_before();
       named_sync(3, 256);
+      tc_fence_after();
       const float4 s0 = sML[row], s1 = sML[128 + row];
       const bool h0 = s0.z != 0.f, h1 = s1.z != 0.f;
       const float m = fmaxf(s0.x, s1.x);
