@@ -9,6 +9,8 @@ There is no fallback: if the library is missing, importing this module fails.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import NamedTuple, Optional
 
@@ -89,6 +91,31 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _current(stream, like=None):
+    """A context with ``stream`` (a torch stream or its handle, on the device of the
+    tensor ``like``) current, so that what a call allocates belongs to the stream that
+    it runs on: a freed block is then not handed out while that stream still uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        device = like.device if isinstance(like, torch.Tensor) and like.is_cuda else None
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _on_its_stream(fn):
+    """``fn`` with its ``stream`` argument, where one is given, current while it runs."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with _current(stream, args[0] if args else None):
+            return fn(*args, **kw)
+
+    return call
+
+
 def default_span(buckets: int, max_rel: int) -> int:
     """DeBERTa's attention span: position_buckets if bucketing is on, else max_rel."""
     return buckets if buckets > 0 else max_rel
@@ -151,6 +178,7 @@ def _prepare(q, k, v, pos_key, pos_query, key_mask, cu_seqlens, max_seqlen, buck
     return B, H, L, T, d, span, out, workspace
 
 
+@_on_its_stream
 def df_attn_fwd(q, k, v, pos_key, pos_query, key_mask=None, cu_seqlens=None, *, max_seqlen=None,
                 buckets=256, max_rel=512, span=None, out=None, workspace=None, stream=None):
     """Fused disentangled-attention forward; returns ``out`` (same layout as q)."""
@@ -176,6 +204,7 @@ def df_attn_fwd_fp32_fast_workspace_size(B, H, L, d, buckets=256, max_rel=512, s
     return int(_lib.df_attn_fwd_fp32_fast_workspace_size(B, H, L, d, buckets, max_rel, span))
 
 
+@_on_its_stream
 def df_attn_fwd_fp32_fast(q, k, v, pos_key, pos_query, key_mask=None, cu_seqlens=None, *,
                           max_seqlen=None, buckets=256, max_rel=512, span=None, out=None,
                           workspace=None, stream=None):
@@ -212,6 +241,7 @@ def df_attn_bwd_workspace_size(B, H, L, d, buckets=256, max_rel=512, span=None) 
     return int(_lib.df_attn_bwd_workspace_size(B, H, L, d, buckets, max_rel, span))
 
 
+@_on_its_stream
 def df_attn_bwd(q, k, v, pos_key, pos_query, dout, key_mask=None, cu_seqlens=None, *,
                 max_seqlen=None, buckets=256, max_rel=512, span=None, grads=None,
                 workspace=None, stream=None):
@@ -255,6 +285,7 @@ def df_attn_fwd_host_scratch_size(B, H, L, d, dtype, buckets=256, max_rel=512, s
     return int(_lib.df_attn_fwd_host_scratch_size(B, H, L, d, buckets, max_rel, span, dt, group_tokens))
 
 
+@_on_its_stream
 def df_attn_fwd_host(q, k, v, pos_key, pos_query, key_mask=None, cu_seqlens=None, *, max_seqlen=None,
                      buckets=256, max_rel=512, span=None, out=None, group_tokens=0, scratch=None,
                      stream=None):
@@ -282,6 +313,7 @@ def df_attn_fwd_host(q, k, v, pos_key, pos_query, key_mask=None, cu_seqlens=None
     return out
 
 
+@_on_its_stream
 def df_attn_plan(q, k, pos_key, pos_query, key_mask=None, cu_seqlens=None, *, max_seqlen=None,
                  buckets=256, max_rel=512, span=None, out=None, workspace=None, stream=None):
     """Planning step alone; returns (out, workspace)."""
@@ -328,6 +360,7 @@ def df_attn_get_device_status(workspace, stream=None) -> int:
     return int(_lib.df_attn_get_device_status(_ptr(workspace), _stream(stream)))
 
 
+@_on_its_stream
 def df_rel_index_table(buckets, max_rel, span, max_len, out=None, stream=None, device="cuda"):
     if out is None:
         out = torch.empty(2 * max_len - 1, dtype=torch.int32, device=device)
@@ -373,6 +406,7 @@ class PackedInfo:
         self.total, self.max_seqlen = total, max_seqlen
 
 
+@_on_its_stream
 def df_pack_info(mask, stream=None) -> PackedInfo:
     """Metadata of a uint8 mask [B, L] (nonzero = valid).  Reads T and
     max_seqlen back to the host (one synchronisation of the stream)."""
@@ -394,6 +428,7 @@ def _row_bytes(t, lead):
     return t[0].numel() * t.element_size() if lead == 1 else t[0, 0].numel() * t.element_size()
 
 
+@_on_its_stream
 def pack_padded_with_info(hidden_states, attention_mask, stream=None):
     """[B, L, ...] -> ([T, ...] rows, cu_seqlens, PackedInfo)."""
     if not hidden_states.is_cuda or not hidden_states.is_contiguous():
@@ -412,6 +447,7 @@ def pack_padded_with_info(hidden_states, attention_mask, stream=None):
     return tokens[:info.total], info.cu_seqlens, info
 
 
+@_on_its_stream
 def unpack_packed(packed, cu_seqlens, seqlen, packed_info, stream=None):
     """[T, ...] -> ([B, L, ...] with zeros at padding, the padded-row mask)."""
     info = packed_info
@@ -443,6 +479,7 @@ def _ptr_array(ts):
 LINEAR_NONE, LINEAR_GELU = 0, 1
 
 
+@_on_its_stream
 def df_linear(x, weights, biases=None, outs=None, status=None, stream=None, activation=LINEAR_NONE):
     """[act(x . W_i^T + b_i)] for 1..3 weights W_i [N, K] (nn.Linear layout) sharing x [M, K]."""
     if x.dim() != 2 or not x.is_cuda or not x.is_contiguous() or x.dtype not in (torch.bfloat16, torch.float16):
@@ -488,6 +525,7 @@ _lib.df_layernorm.argtypes = [_vp, _vp, _vp, _vp, _i, _i, ctypes.c_float, _vp, _
 _lib.df_layernorm.restype = _i
 
 
+@_on_its_stream
 def df_layernorm(x, gamma, beta, residual=None, eps=1e-7, out=None, stream=None):
     """LayerNorm(x + residual) * gamma + beta over the last dimension of [M, N]."""
     M, N = x.shape
@@ -514,14 +552,6 @@ def _on_device(tensors, names):
             name = names.split()[[t is x for x in tensors].index(True)]
             raise ValueError(f"{name} must be a contiguous CUDA tensor on the same device as {names.split()[0]}")
     return idx
-
-
-def _current(stream, like):
-    """A context with ``stream`` (a torch stream or its handle) current, so that what a
-    call allocates belongs to the stream that it runs on."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
-    return torch.cuda.stream(stream)
 
 
 def _call_on(idx, fn, *args) -> int:

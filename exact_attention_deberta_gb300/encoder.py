@@ -94,31 +94,33 @@ class Encoder:
         """``trace``: an optional list; each layer appends a dict of the tensors
         its attention call took and gave (q, k, v, pk, pq, ctx), which the layer
         computes anyway (nothing extra runs)."""
+        if stream is not None:
+            with binding._current(stream, hidden):
+                return self(hidden, cu_seqlens, max_seqlen, trace=trace)
         cfg = self.cfg
         hid, H = cfg.hidden, cfg.heads
         T = hidden.shape[0]
         sh = self.shared
-        rel = binding.df_layernorm(sh["rel_embeddings"], sh["rel_g"], sh["rel_b"], eps=cfg.eps, stream=stream)
+        rel = binding.df_layernorm(sh["rel_embeddings"], sh["rel_g"], sh["rel_b"], eps=cfg.eps)
         ws = None
         h = hidden
         for p in self.layers:
             w, b = p["w_qkv"], p["b_qkv"]
-            q, k, v = binding.qkv_projection(h, w, b, H, stream=stream)
-            pk, pq = binding.rel_projection(rel, w[hid:2 * hid], b[hid:2 * hid], w[:hid], b[:hid], H, stream=stream)
+            q, k, v = binding.qkv_projection(h, w, b, H)
+            pk, pq = binding.rel_projection(rel, w[hid:2 * hid], b[hid:2 * hid], w[:hid], b[:hid], H)
             if ws is None:
                 size = binding.df_attn_workspace_size(cu_seqlens.numel() - 1, H, max_seqlen, hid // H,
                                                       cfg.buckets, cfg.max_rel, cfg.span)
                 ws = torch.empty(max(size, 256), dtype=torch.uint8, device=hidden.device)
             ctx = binding.df_attn_fwd(q, k, v, pk, pq, cu_seqlens=cu_seqlens, max_seqlen=max_seqlen,
-                                      buckets=cfg.buckets, max_rel=cfg.max_rel, span=cfg.span, workspace=ws,
-                                      stream=stream)
+                                      buckets=cfg.buckets, max_rel=cfg.max_rel, span=cfg.span, workspace=ws)
             if trace is not None:
                 trace.append(dict(q=q, k=k, v=v, pk=pk, pq=pq, ctx=ctx))
-            (a,) = binding.df_linear(ctx.view(T, hid), [p["w_o"]], [p["b_o"]], stream=stream)
-            h1 = binding.df_layernorm(a, p["ln1_g"], p["ln1_b"], residual=h, eps=cfg.eps, stream=stream)
-            (f,) = binding.df_linear(h1, [p["w_1"]], [p["b_1"]], stream=stream, activation=binding.LINEAR_GELU)
-            (f2,) = binding.df_linear(f, [p["w_2"]], [p["b_2"]], stream=stream)
-            h = binding.df_layernorm(f2, p["ln2_g"], p["ln2_b"], residual=h1, eps=cfg.eps, stream=stream)
+            (a,) = binding.df_linear(ctx.view(T, hid), [p["w_o"]], [p["b_o"]])
+            h1 = binding.df_layernorm(a, p["ln1_g"], p["ln1_b"], residual=h, eps=cfg.eps)
+            (f,) = binding.df_linear(h1, [p["w_1"]], [p["b_1"]], activation=binding.LINEAR_GELU)
+            (f2,) = binding.df_linear(f, [p["w_2"]], [p["b_2"]])
+            h = binding.df_layernorm(f2, p["ln2_g"], p["ln2_b"], residual=h1, eps=cfg.eps)
         return h
 
 
