@@ -5,7 +5,7 @@
 //   dv_j = sum_i p_ij dout_i       (sums over i also run over the query heads
 //                                   that share the key head).
 //
-// Three launches.  row_stats forms D_i from out + out_lo (fp32 sums; the rounding
+// Three launches.  row_stats (fp16: group_stats) forms D_i from out + out_lo (fp32 sums; the rounding
 // of out alone would leave 2^-9 |dout||v| where few keys carry a row) and puts it
 // beside the row's lse in log2 units.  Two runs of one kernel then recompute the
 // scores tile by tile: for a tile of keys it streams the queries past (dk, dv),
@@ -26,7 +26,8 @@
 //                 each: two for all four took 1.81 ms where these took 1.57)
 //   warp 5        per streamed tile: the rows' (lse, D) or the keys' mask bits into
 //                 shared memory, and zeros over streamed rows that do not count
-//                 (they are the reduction dimension of the second products)
+//                 (they are the reduction dimension of the second products); fp16:
+//                 the resident rows' scales beside the item's first tile
 //   warps 8-15    P and dS, one thread per resident row; the epilogue
 //
 // Measured (GB300, bf16): 16 x 12 heads, 2048 queries x 8192 keys, d = 64: 2.31 ms
@@ -37,9 +38,14 @@
 // and 1290; 2591 and 2074 at d = 128, and takes about 3500 and 2600 (only two buffers
 // in the first).  Whole tiles (128 columns) would leave one buffer and no overlap.
 //
-// fp16: dS spans too wide a range for its exponent, so it is scaled by a power of
-// two that puts the largest |dout_i| at about 16, and P (at most 1) by 2^14; the
-// results are scaled back in fp32.  bf16 needs neither.
+// fp16: dS spans too wide a range for its exponent, so it is held times a power of two,
+// taken back in fp32 at the end: the one that takes a bound of |dS| just below 2^15, for
+// each resident row by itself.  Query tiles, row i: |dS_ij| <= |dout_i| max_j |v_j| +
+// |D_i|; key tiles, row j: |dS_ij| <= max_i |dout_i| |v_j| + max_i |D_i|, the maxima over
+// the sequence and the heads that share a key head (group_stats).  So nothing overflows,
+// whatever v holds, a row keeps its digits beside rows of far larger dout or v, and
+// what is lost below fp16's smallest step is 2^-40 of the row's bound.  P (at most 1) is
+// held times 2^14.  bf16 needs none of this.
 #include "df_cross.cuh"
 
 #include <algorithm>
@@ -57,12 +63,16 @@ constexpr int kRegs = 128, kSoftmaxRegs = 176, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kRegs, "setmaxnreg.inc must not wait");
 constexpr uint32_t kItemRing = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 14.f;  // fp16: P is held as 2^14 p
+constexpr float kPShift = 14.f, kPUnit = 1.f / 16384.f;  // fp16: P is held as 2^14 p
 
 struct BwdArgs {
   CrossArgs c;
   const float2* stat;      // [Tq][H]: lse in log2 units (+inf without keys), D
-  const uint32_t* top;     // fp16: the largest |dout_i|^2, as bits
+  // fp16: |dout_i| [Tq][H], and [3][Tq][H], at the first query row of a sequence and the
+  // first head of a group, the largest |dout_i|, |D_i| and |v_j| of the two, as bits.
+  // |v_j| itself stands in the first four bytes of the key's row of dv until that is written.
+  const float* norm;
+  const uint32_t* top;
   void* out0;              // dk or dq
   void* out1;              // dv
   int after_keys;          // the key tiles' launch is the one before
@@ -73,58 +83,152 @@ struct BwdMaps {
 };
 
 // ------------------------------------------------------------- row statistics
-// One group of 16 lanes per (token, head).
+// |x|^2 of the row at `x`, and x (o + r) where o (and r) is given: (x (o + r), |x|^2).  Four
+// lanes share a row, 8 columns of every 32 each.
+template <typename T>
+__device__ __forceinline__ float2 row_sums(const T* x, const T* o, const T* r, int d) {
+  float sq = 0.f, sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = 32 * k + 8 * (threadIdx.x & 3);
+    if (c >= d) break;
+    uint4 x4 = *reinterpret_cast<const uint4*>(x + c), o4 = make_uint4(0u, 0u, 0u, 0u), r4 = o4;
+    if (o) o4 = *reinterpret_cast<const uint4*>(o + c);
+    if (r) r4 = *reinterpret_cast<const uint4*>(r + c);
+    const T *xe = reinterpret_cast<const T*>(&x4), *oe = reinterpret_cast<const T*>(&o4),
+            *re = reinterpret_cast<const T*>(&r4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = IO<T>::to_f(xe[e]);
+      sq += f * f;
+      if (o) sum += (IO<T>::to_f(oe[e]) + IO<T>::to_f(re[e])) * f;
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1) {
+    sq += __shfl_xor_sync(0xffffffffu, sq, m);
+    if (o) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  }
+  return make_float2(sum, sq);
+}
+__device__ __forceinline__ float2 row_stat(float lse, float D) {
+  return make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, D);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) row_stats(const T* __restrict__ out, const T* __restrict__ out_lo,
                                                  const T* __restrict__ dout, const float* __restrict__ lse, int d,
-                                                 long long rows, const int32_t* cu_q, int B, int H,
-                                                 float2* __restrict__ stat, uint32_t* top) {
+                                                 long long rows, float2* __restrict__ stat) {
   allow_dependent_launch();
-  const long long row = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int l = threadIdx.x & 15;
-  float sum = 0.f, n2 = 0.f;
-  if (row < rows && l * 8 < d) {
-    const size_t at = (size_t)row * d + l * 8;
-    const uint4 o4 = *reinterpret_cast<const uint4*>(out + at);
-    const uint4 g4 = *reinterpret_cast<const uint4*>(dout + at);
-    uint4 r4 = make_uint4(0u, 0u, 0u, 0u);
-    if (out_lo) r4 = *reinterpret_cast<const uint4*>(out_lo + at);
-    const T* o = reinterpret_cast<const T*>(&o4);
-    const T* g = reinterpret_cast<const T*>(&g4);
-    const T* r = reinterpret_cast<const T*>(&r4);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float gv = IO<T>::to_f(g[e]);
-      sum += (IO<T>::to_f(o[e]) + IO<T>::to_f(r[e])) * gv;
-      n2 += gv * gv;
+  const long long row = (long long)blockIdx.x * 64 + (threadIdx.x >> 2);
+  const bool in = row < rows;
+  const size_t at = in ? (size_t)row * d : 0;
+  const float l = in ? lse[row] : 0.f;
+  const float D = row_sums(dout + at, out + at, out_lo ? out_lo + at : nullptr, in ? d : 0).x;
+  if (in && (threadIdx.x & 3) == 0) stat[row] = row_stat(l, D);
+}
+
+// fp16: the statistics of the rows of every sequence, their norms, those of its keys (at the
+// head of dv's rows), and the largest of each (BwdArgs::top, zero before).  `parts`
+// blocks share a sequence; a warp takes a step at a time: `span` rows of a group (a
+// token's, where more heads share a key head), or `span` keys of a head.  Rows without a
+// valid key, keys that do not count and what is not finite are left out of the maxima
+// (the order in which warps raise those does not matter).  Bound by latency where there
+// is little to do, so the code is short (eight rows at a time, in loops), and by HBM
+// else: 4 x 12 heads, 77 x 300, d = 64: 5.3 us; 2048 x 8192: 29 us (88 MB).
+__global__ void __launch_bounds__(256) group_stats(const CrossArgs a, int parts, int span, const __half* __restrict__ out,
+                                                   const __half* __restrict__ out_lo, const __half* __restrict__ dout,
+                                                   const float* __restrict__ lse, const __half* __restrict__ v,
+                                                   float2* __restrict__ stat, float* __restrict__ norm, uint32_t* top,
+                                                   __half* __restrict__ dv) {
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, b = blockIdx.x / parts;
+  const int warps = parts * 8, warp = (blockIdx.x - b * parts) * 8 + (threadIdx.x >> 5);
+  int q0, k0;
+  const int nq = seq_rows(query_side(a), b, nullptr, &q0), nk = seq_rows(key_side(a), b, nullptr, &k0);
+  if (nq == 0 || nk == 0) return;
+  const size_t plane = (size_t)a.Tq * a.H;
+  const int tokens = max(1, span / a.G), per_q = (nq + tokens - 1) / tokens, per_k = (nk + span - 1) / span;
+  const long long q_steps = (long long)per_q * a.Hk, steps = q_steps + (long long)per_k * a.Hk;
+  for (long long u = warp; u < steps; u += warps) {
+    const bool queries = u < q_steps;
+    const int i = (int)(queries ? u : u - q_steps), per = queries ? per_q : per_k, hk = i / per;
+    uint32_t* p0 = top + (size_t)q0 * a.H + hk * a.G + (queries ? 0 : 2 * plane);
+    float m0 = 0.f, m1 = 0.f;
+    if (queries) {
+      const int t0 = (i - hk * per) * tokens, n = min(tokens, nq - t0) * a.G;
+#pragma unroll 1
+      for (int r0 = 0; r0 < n; r0 += 8) {
+        const int r = min(r0 + (lane >> 2), n - 1), tok = r / a.G;  // (the last one again where there are fewer)
+        const size_t row = (size_t)(q0 + t0 + tok) * a.H + hk * a.G + (r - tok * a.G), at = row * a.d;
+        const float l = lse[row];
+        const float2 s = row_sums(dout + at, out + at, out_lo ? out_lo + at : nullptr, a.d);
+        const float x = sqrtf(s.y);
+        const bool counts = l != -INFINITY && x <= 3.0e38f;
+        if ((lane & 3) == 0) {
+          stat[row] = row_stat(l, s.x);
+          norm[row] = counts ? x : 0.f;
+        }
+        if (counts) m0 = fmaxf(m0, x);
+        if (counts && fabsf(s.x) <= 3.0e38f) m1 = fmaxf(m1, fabsf(s.x));
+      }
+    } else {
+      const int j0 = (i - hk * per) * span + (lane >> 2);
+#pragma unroll 1
+      for (int j = j0; j < j0 + span; j += 8) {
+        const bool in = j < nk;
+        const size_t at = in ? ((size_t)(k0 + j) * a.Hk + hk) * a.d : 0;
+        const bool counts = in && (!a.key_mask || a.key_mask[(size_t)b * a.Lk + j] != 0);
+        const float x = sqrtf(row_sums<__half>(v + at, nullptr, nullptr, in ? a.d : 0).y);
+        if (in && (lane & 3) == 0) *reinterpret_cast<float*>(dv + at) = x;
+        if (counts && x <= 3.0e38f) m0 = fmaxf(m0, x);
+      }
+    }
+    // not negative: their bits are in order
+    const uint32_t b0 = __reduce_max_sync(0xffffffffu, __float_as_uint(m0));
+    const uint32_t b1 = __reduce_max_sync(0xffffffffu, __float_as_uint(m1));
+    if (lane < (queries ? 2 : 1)) {
+      uint32_t* p = p0 + lane * plane;
+      const uint32_t mine = lane ? b1 : b0;
+      if (mine > *static_cast<volatile uint32_t*>(p)) atomicMax(p, mine);
     }
   }
+}
+
+// The power of two that takes x y + z, a bound of |dS| (2^-48 .. 2^40 for fp16 rows),
+// below 2^15.  (Short code: it runs once per item.  A bound of 0, or one that is not
+// finite, gets the ends of the range.)
+__device__ __forceinline__ float ds_scale(float x, float y, float z) {
+  const uint32_t e = __float_as_uint(fmaf(x, y, z)) >> 23;  // below 2^(e - 126)
+  return __uint_as_float((254u + 14u - min(max(e, 60u), 200u)) << 23);
+}
+
+// fp16: the scales of a resident tile's rows 32 w + lane (one warp).  Those of keys that do
+// not count may be any power of two.
+template <bool KEYS, typename T>
+__device__ __forceinline__ void resident_scales(const BwdArgs& args, const CrossItem& it, float (&scales)[4]) {
+  const CrossArgs& a = args.c;
+  const size_t plane = (size_t)a.Tq * a.H;
+  const int first = KEYS ? it.o0 : a.cu_q ? min(max(a.cu_q[it.b], 0), a.Tq - 1) : it.b * a.Lq;
+  const uint32_t* top = args.top + (size_t)first * a.H + it.hk * a.G;
+  const float x = __uint_as_float(top[KEYS ? 0 : 2 * plane]), z = KEYS ? __uint_as_float(top[plane]) : 0.f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-  }
-  const bool mine = row < rows && l == 0;
-  if (mine) {
-    const float v = lse[row];
-    stat[row] = make_float2(v == -INFINITY ? INFINITY : v * kLog2e, sum);
-  }
-  if (top) {
-    // rows outside every sequence or without a valid key do not count (their dS is 0);
-    // neither does what is not finite
-    bool in = mine && n2 <= 3.0e38f && lse[row] != -INFINITY;
-    if (in && cu_q) {
-      const long long tok = row / H;
-      in = tok >= cu_q[0] && tok < cu_q[B];
+  for (int w = 0; w < 4; ++w) {
+    const int r = 32 * w + (threadIdx.x & 31), tok = KEYS ? r : r / a.G;
+    scales[w] = 1.f;
+    if (tok >= it.nr) continue;
+    if (KEYS) {
+      const T* dv = static_cast<const T*>(args.out1) + ((size_t)(it.r0 + r) * a.Hk + it.hk) * a.d;
+      scales[w] = ds_scale(x, *reinterpret_cast<const float*>(dv), z);
+    } else {
+      const size_t row = (size_t)(it.r0 + tok) * a.H + it.hk * a.G + (r - tok * a.G);
+      scales[w] = ds_scale(x, args.norm[row], fabsf(args.stat[row].y));
     }
-    uint32_t bits = in ? __float_as_uint(n2) : 0u;
-    bits = __reduce_max_sync(0xffffffffu, bits);
-    if ((threadIdx.x & 31) == 0 && bits != 0u) atomicMax(top, bits);
   }
 }
 
 // ------------------------------------------------------------ the tile kernel
-template <int D>
+template <int D, bool BF16>
 struct BwdSmem {
   static constexpr int kChunks = D / 64;
   static constexpr int kRes = D == 64 ? 2 : 1;     // resident pairs
@@ -143,7 +247,8 @@ struct BwdSmem {
   static constexpr uint32_t cur = ring + 32 * kItemRing;
   static constexpr uint32_t claim = cur + 64;  // 16 bytes
   static constexpr uint32_t misc = claim + 16;
-  static constexpr uint32_t bytes = misc + 16;
+  static constexpr uint32_t scale = misc + 16;  // fp16: float [kStages][128], the resident rows' scales
+  static constexpr uint32_t bytes = scale + (BF16 ? 0 : kStages * 512);
   static constexpr uint32_t alloc = bytes + 1024;
   static_assert(alloc <= 232448, "shared memory of one CTA");
 };
@@ -151,7 +256,7 @@ struct BwdSmem {
 // KEYS: the resident rows are keys (K, V), the streamed ones queries (Q, dout).
 template <int D, bool BF16, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs args, const __grid_constant__ BwdMaps maps) {
-  using SL = BwdSmem<D>;
+  using SL = BwdSmem<D, BF16>;
   constexpr int kChunks = SL::kChunks;
   constexpr uint32_t kRes = SL::kRes, kStages = SL::kStages;
   constexpr uint32_t kIdescS = idesc_f16(128, 64, BF16 ? 1 : 0, 0, 0);
@@ -457,10 +562,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       it.o0 = __shfl_sync(0xffffffffu, it.o0, 0);
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
       it.b = __shfl_sync(0xffffffffu, it.b, 0);
+      if (!BF16) {
+        it.r0 = __shfl_sync(0xffffffffu, it.r0, 0);
+        it.nr = __shfl_sync(0xffffffffu, it.nr, 0);
+      }
       const int nt = y_tiles(it);
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, ++g) {
         const uint32_t s = g % kStages;
+        float scales[4];
+        if (!BF16 && t == 0) resident_scales<KEYS, T>(args, it, scales);
         const int left = it.no - t * y_step;  // tokens of the tile (and behind it)
         uint32_t bits[4];
         float2 st[4];
@@ -483,6 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         uint8_t* sY = sm + SL::y + s * 2 * SL::kTileBytes;
+        if (!BF16 && t == 0) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) reinterpret_cast<float*>(sm + SL::scale + s * 512)[32 * w + lane] = scales[w];
+        }
         if (!whole) {
           zero_rows<4, kChunks>(sY, bits);
           if (KEYS) zero_rows<4, kChunks>(sY + SL::kTileBytes, bits);
@@ -513,15 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const float ks = a.kscale;
     const float2 ks2 = make_float2(ks, ks);
-    float grow = 1.f;                        // fp16: the power of two that scales dS
-    if (!BF16) {
-      const float n2 = __uint_as_float(*args.top);
-      if (n2 > 0.f) grow = exp2f(fminf(fmaxf(4.f - ceilf(0.5f * log2f(n2)), -100.f), 100.f));
-    }
-    const float ds_mul = BF16 ? 1.f : grow * exp2f(-kPShift);
-    const float2 ds_mul2 = make_float2(ds_mul, ds_mul);
-    const float scale0 = BF16 ? a.scale : a.scale / grow;        // dk, dq
-    const float scale1 = BF16 ? 1.f : exp2f(-kPShift);           // dv
+    const float scale0 = a.scale;              // dk, dq
+    const float scale1 = BF16 ? 1.f : kPUnit;  // dv
     const int row_tok = KEYS ? row : row / a.G, row_head = KEYS ? 0 : row - row_tok * a.G;
     const bool reader = warp == kFirst && lane == 0;
     uint32_t g = 0, xc = 0, c = 1;  // c: items taken, of which the last but one is current at an item's end
@@ -543,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         nd = -st.y;
       }
       const uint32_t rows_in = __ballot_sync(0xffffffffu, row_in);
+      float ds_mul = kPUnit;  // fp16: the row's scale, on P as it is held
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       for (int t = 0; t < nt; ++t) {
         const uint32_t s = (g + t) % kStages, u = 2 * (g + t) + h, b = u % kBufs;
@@ -552,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         __syncwarp();
         tc_fence_after();
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
+        if (!BF16 && t == 0) ds_mul = reinterpret_cast<const float*>(sm + SL::scale + s * 512)[row] * kPUnit;
         if constexpr (KEYS) {
           // A thread takes two columns of every eight in four rows (lane / 4 + 8 r),
           // not 64 columns of one row: it then reads a quarter of the columns' values
@@ -580,13 +690,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
             tmem_ld_wait(rd1);
             auto half_rows = [&](const uint32_t (&rs)[16], const uint32_t (&rd)[16], int i) {
               uint32_t wp[8], wd[8];
+              // (fp16: the scales of this thread's rows, fetched here: held over the loop they spill)
+              const float m0 = BF16 ? 1.f : __shfl_sync(0xffffffffu, ds_mul, 16 * i + (lane >> 2));
+              const float m1 = BF16 ? 1.f : __shfl_sync(0xffffffffu, ds_mul, 16 * i + 8 + (lane >> 2));
+              const float2 mul[2] = {make_float2(m0, m0), make_float2(m1, m1)};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int j = e >> 1, k = 4 * j + 2 * (e & 1);
                 const float2 z = fma2(make_float2(__uint_as_float(rs[k]), __uint_as_float(rs[k + 1])), ks2, nl[j]);
                 const float2 p = make_float2(ex2(z.x), ex2(z.y));
                 float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[k]), __uint_as_float(rd[k + 1])), nd[j]));
-                if (!BF16) ds = mul2(ds, ds_mul2);
+                if (!BF16) ds = mul2(ds, mul[e & 1]);
                 wp[e] = BF16 ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
                 wd[e] = BF16 ? pack_bf16x2(ds.x, ds.y) : pack_f16x2(ds.x, ds.y);
               }
@@ -620,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
                   fma2(make_float2(__uint_as_float(rs[2 * e]), __uint_as_float(rs[2 * e + 1])), ks2, nl2);
               const float2 p = make_float2(ex2(z.x), ex2(z.y));
               float2 ds = mul2(p, add2(make_float2(__uint_as_float(rd[2 * e]), __uint_as_float(rd[2 * e + 1])), nd2));
-              if (!BF16) ds = mul2(ds, ds_mul2);
+              if (!BF16) ds = mul2(ds, make_float2(ds_mul, ds_mul));
               wd[e] = BF16 ? pack_bf16x2(ds.x, ds.y) : pack_f16x2(ds.x, ds.y);
             }
             if (bits != 0xffffffffu) {
@@ -653,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       // KEYS: warpgroup 0 writes dk, 1 dv; else each half of dq's columns
       const uint32_t tA = (KEYS && h == 1 ? tAcc1 : tAcc0) + lane_off;
       T* dst = static_cast<T*>(KEYS && h == 1 ? args.out1 : args.out0) + row0 * a.d;
-      const float mul = KEYS && h == 1 ? scale1 : scale0;
+      const float mul = KEYS && h == 1 ? scale1 : BF16 ? scale0 : scale0 / (ds_mul / kPUnit);
       const int c0 = KEYS ? 0 : h * (D / 2), c1 = KEYS ? D : c0 + D / 2;
 #pragma unroll 1
       for (int cc = c0; cc < min(c1, a.d); cc += 32) {
@@ -688,7 +802,7 @@ template <int D, bool BF16, bool KEYS>
 cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items, cudaStream_t s) {
   if (items == 0) return cudaSuccess;
   auto kernel = cross_bwd_kernel<D, BF16, KEYS>;
-  const uint32_t bytes = BwdSmem<D>::alloc;
+  const uint32_t bytes = BwdSmem<D, BF16>::alloc;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kRegs, &done);
   if (e != cudaSuccess) return e;
@@ -716,18 +830,33 @@ cudaError_t launch_both(BwdArgs a, const BwdMaps& km, const BwdMaps& qm, void* d
   return cudaSuccess;
 }
 
-template <typename T>
 void launch_stats(const void* out, const void* out_lo, const void* dout, const float* lse, const CrossArgs& c,
-                  float2* stat, uint32_t* top, cudaStream_t s) {
+                  float2* stat, cudaStream_t s) {
+  using T = __nv_bfloat16;
   const long long rows = (long long)c.Tq * c.H;
-  row_stats<T><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(static_cast<const T*>(out), static_cast<const T*>(out_lo),
-                                                           static_cast<const T*>(dout), lse, c.d, rows, c.cu_q, c.B,
-                                                           c.H, stat, top);
+  row_stats<T><<<(unsigned)((rows + 63) / 64), 256, 0, s>>>(static_cast<const T*>(out), static_cast<const T*>(out_lo),
+                                                           static_cast<const T*>(dout), lse, c.d, rows, stat);
+}
+
+void launch_group_stats(const void* out, const void* out_lo, const void* dout, const float* lse, const void* v,
+                        const CrossArgs& c, float2* stat, float* norm, uint32_t* top, void* dv, cudaStream_t s) {
+  using T = __half;
+  // a step for each warp, in at most eight blocks an SM (by the stated lengths); steps of
+  // eight rows, one round trip to memory each, where they are that few
+  const long long most = std::max(1ll, 8ll * device_sms() / c.B);
+  auto blocks = [&](long long span) {
+    return (c.Hk * ((c.Lk + span - 1) / span + ((long long)c.Lq * c.G + span - 1) / span) + 7) / 8;
+  };
+  const int span = blocks(8) <= most ? 8 : 32;
+  const int parts = (int)std::min(std::max(1ll, blocks(span)), most);
+  group_stats<<<parts * c.B, 256, 0, s>>>(c, parts, span, static_cast<const T*>(out), static_cast<const T*>(out_lo),
+                                          static_cast<const T*>(dout), lse, static_cast<const T*>(v), stat, norm, top,
+                                          static_cast<T*>(dv));
 }
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-constexpr size_t kTopBytes = 256;
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 }  // namespace dfa
@@ -736,7 +865,9 @@ using namespace dfa;
 
 extern "C" size_t df_cross_attn_bwd_workspace_size(int total_q, int H) {
   if (total_q < 0 || total_q > (1 << 30) || H < 1 || (long long)total_q * H > (1ll << 34)) return 0;
-  return kTopBytes + (((size_t)total_q * H * sizeof(float2) + 255) & ~(size_t)255);
+  // stat, norm and top (the last two for fp16)
+  const size_t rows = (size_t)total_q * H;
+  return up256(rows * sizeof(float2)) + up256(rows * sizeof(float)) + up256(3 * rows * sizeof(uint32_t)) + 256;
 }
 
 extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* out_lo,
@@ -759,16 +890,22 @@ extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void*
   if (total_q == 0 && total_k == 0) return DF_OK;
   cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = dtype == DF_BF16;
-  uint32_t* top = bf16 ? nullptr : static_cast<uint32_t*>(workspace);
-  float2* stat = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kTopBytes);
+  const size_t rows = (size_t)total_q * H;
+  char* base = static_cast<char*>(workspace);
+  float2* stat = reinterpret_cast<float2*>(base);
+  float* norm = bf16 ? nullptr : reinterpret_cast<float*>(base + up256(rows * sizeof(float2)));
+  uint32_t* top =
+      bf16 ? nullptr : reinterpret_cast<uint32_t*>(base + up256(rows * sizeof(float2)) + up256(rows * sizeof(float)));
   a.stat = stat;
+  a.norm = norm;
   a.top = top;
-  if (top && cudaMemsetAsync(top, 0, 4, s) != cudaSuccess) return DF_ERR_CUDA;
-  if (total_q > 0) {
-    if (bf16) launch_stats<__nv_bfloat16>(out, out_lo, dout, lse, a.c, stat, top, s);
-    else launch_stats<__half>(out, out_lo, dout, lse, a.c, stat, top, s);
-    if (cudaGetLastError() != cudaSuccess) return DF_ERR_CUDA;
+  if (total_q > 0 && bf16) {
+    launch_stats(out, out_lo, dout, lse, a.c, stat, s);
+  } else if (total_q > 0 && total_k > 0 && B > 0) {
+    if (cudaMemsetAsync(top, 0, 3 * rows * sizeof(uint32_t), s) != cudaSuccess) return DF_ERR_CUDA;
+    launch_group_stats(out, out_lo, dout, lse, v, a.c, stat, norm, top, dv, s);
   }
+  if (cudaGetLastError() != cudaSuccess) return DF_ERR_CUDA;
   // a side without rows is never copied from: its maps then describe the other one
   const bool has_q = total_q > 0, has_k = total_k > 0;
   const void* qp = has_q ? q : k;

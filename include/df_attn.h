@@ -519,16 +519,20 @@ df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
  *   dout       like out
  *   dq, dk, dv like q, k, v, in `dtype`: written in full (from cu_seqlens[0] on);
  *              must not overlap the inputs.  Keys that do not count and rows
- *              behind the last packed sequence get zeros
+ *              behind the last packed sequence get zeros.  (fp16: dv holds the
+ *              keys' norms meanwhile)
  *   workspace  at least df_cross_attn_bwd_workspace_size() bytes, 256-byte
  *              aligned, contents need not be initialised; calls that share it
  *              must not overlap
  * Scores, dout.v and every sum are fp32 (dk and dv are summed over a group's
  * heads before their only rounding); the weights and dS are rounded to dtype as
- * operands of the second products (fp16: scaled by powers of two first, so that
- * small gradients keep their digits while |dout_i| |v_j| of any row and key is
- * below about 2000 times the largest |dout_i|).  No atomics in the sums: equal
- * inputs give equal bits.  Three launches (fp16: and one 4-byte memset).
+ * operands of the second products.  fp16: both are held times powers of two, dS
+ * times that of its row of dq, or of dk, by itself, so that no value of v or dout
+ * overflows on the way, and small gradients beside large ones keep their digits: dS is
+ * rounded to 11 bits down to 2^-29 of a bound of the row's largest, |dout_i| max_j
+ * |v_j| + |D_i| for dq and max_i |dout_i| |v_j| + max_i |D_i| for dk, and below
+ * that in steps of 2^-39 of it.  No atomics in the sums: equal inputs give equal
+ * bits.  Three launches (fp16: and one memset).
  * Errors: as the forward, and DF_ERR_WORKSPACE. */
 df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                             const void* out_lo, const float* lse, const void* dout,
@@ -538,7 +542,7 @@ df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const v
                             void* dq, void* dk, void* dv, int32_t* status, void* workspace,
                             size_t workspace_bytes, df_stream_t stream);
 
-/* Bytes of workspace df_cross_attn_bwd needs: 8 per query row and head (0 for
+/* Bytes of workspace df_cross_attn_bwd needs: 24 per query row and head (0 for
  * sizes it rejects). */
 size_t df_cross_attn_bwd_workspace_size(int total_q, int H);
 
