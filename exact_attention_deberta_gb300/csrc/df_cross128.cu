@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
           float* slot = sMax + ((n & 1) * 4 + wg * 2) * 128 + row;
           slot[half * 128] = mine;
           named_sync(pair_bar, 64);
-          const float mt = fmaxf(mine, slot[(1 - half) * 128]) * ks;
+          const float mt = fmaxf(mine, slot[(1 - half) * 128]) * ks - kBelow<BF16>;
           // the base of the exponentials moves only when it would grow by more
           // than 2^8: numerator and denominator share it, so the result is exact
           float rescale = 1.f;

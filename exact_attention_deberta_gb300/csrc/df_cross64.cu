@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
             mx[2 * e + 1] = fmax3(mx[2 * e + 1], x[j + 2], x[j + 3]);
           }
           const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * ks;
+                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * ks - kBelow<BF16>;
           // the base of the exponentials moves only when it would grow by more
           // than 2^8: numerator and denominator share it, so the result is exact
           float rescale = 1.f;

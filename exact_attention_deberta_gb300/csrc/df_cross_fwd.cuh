@@ -25,6 +25,15 @@ cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int
 cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s);
 constexpr int kFwdKeys = 128;  // keys per tile
 
+// The base of a row's exponentials stands this many binary orders below its maximum.  A
+// weight is then at most 2^(kBelow + 8) (the base moves by more than 2^8 only), and fp16
+// holds weights down to 2^-21 of the largest with all their digits, and below that in steps
+// of 2^-31 of it.  With the base at the maximum, weights of 2^-25 came to nothing, which is
+// all that is left where the large ones meet values of 0.  The row's sum and O share the
+// base, so nothing else changes.  bf16 has the range anyway.
+template <bool BF16>
+constexpr float kBelow = BF16 ? 0.f : 7.f;
+
 // This CTA's key tiles [*t0, *t0 + n) of an item; returns n.
 __device__ __forceinline__ int key_part(const FwdArgs& args, const CrossItem& it, uint32_t rank, int* t0) {
   const unsigned all = (it.no + kFwdKeys - 1) / kFwdKeys;

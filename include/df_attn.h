@@ -493,7 +493,8 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  *               offsets are not 0 <= cu[b] <= cu[b + 1] <= total (it is taken
  *               as empty; its rows of out are not written)
  * Scores, softmax statistics and sums are fp32; the weights are rounded to dtype
- * as the operand of the product with v.  Keys that do not count, and rows of k
+ * as the operand of the product with v (fp16: down to 2^-21 of a row's largest,
+ * and in steps of 2^-31 of it below that).  Keys that do not count, and rows of k
  * and v outside the sequence, may hold anything (NaN included); a NaN that counts
  * makes its rows' out and lse NaN.  out, out_lo and lse must not overlap the
  * inputs.  One launch, no workspace; equal inputs give equal bits.
