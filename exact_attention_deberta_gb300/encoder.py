@@ -84,10 +84,12 @@ class Encoder:
     def __init__(self, cfg: EncoderConfig, layers: List[dict], shared: dict):
         self.cfg, self.layers, self.shared = cfg, layers, shared
 
-    def embed(self, input_ids, stream=None):
-        """Rows [T, hidden] of packed token ids [T]: their embeddings, normalised."""
+    def embed(self, input_ids, stream=None, status=None):
+        """Rows [T, hidden] of packed token ids [T]: their embeddings, normalised.  An id
+        outside the vocabulary counts as a row of zeros; ``status`` (a device int32, as for
+        ``binding.df_embedding``) reports it."""
         sh = self.shared
-        rows = binding.df_embedding(input_ids, sh["word_embeddings"], stream=stream)
+        rows = binding.df_embedding(input_ids, sh["word_embeddings"], status=status, stream=stream)
         return binding.df_layernorm(rows, sh["emb_g"], sh["emb_b"], eps=self.cfg.eps, stream=stream)
 
     def __call__(self, hidden, cu_seqlens, max_seqlen, stream=None, trace=None):
@@ -129,25 +131,27 @@ class CrossAttention:
     attention, output projection, residual LayerNorm.
 
     ``project`` gives the states' keys and values once; a program that generates
-    keeps them and calls ``attend`` with one row per sequence."""
+    keeps them and calls ``attend`` with one row per sequence.  ``status`` (a device
+    int32, zeroed by the caller) receives what the calls report: offsets that are not
+    in order, whose sequences' rows then hold anything, and waits that ran out."""
 
     def __init__(self, cfg: EncoderConfig, weights: dict):
         self.cfg, self.w = cfg, weights
 
-    def project(self, states, stream=None):
+    def project(self, states, stream=None, status=None):
         """states [T, hidden] -> k, v, each [T, heads, hidden / heads]."""
         w, H = self.w, self.cfg.heads
-        outs = binding.df_linear(states, [w["w_k"], w["w_v"]], [w["b_k"], w["b_v"]], stream=stream)
+        outs = binding.df_linear(states, [w["w_k"], w["w_v"]], [w["b_k"], w["b_v"]], status=status, stream=stream)
         return [o.view(states.shape[0], H, self.cfg.hidden // H) for o in outs]
 
-    def attend(self, x, k, v, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k, stream=None):
+    def attend(self, x, k, v, cu_seqlens_q, max_seqlen_q, cu_seqlens_k, max_seqlen_k, stream=None, status=None):
         """x [Tq, hidden], packed by cu_seqlens_q, against the keys and values of the same
         sequences, packed by cu_seqlens_k -> [Tq, hidden]."""
         w, cfg = self.w, self.cfg
         T, hid = x.shape
-        (q,) = binding.df_linear(x, [w["w_q"]], [w["b_q"]], stream=stream)
+        (q,) = binding.df_linear(x, [w["w_q"]], [w["b_q"]], status=status, stream=stream)
         ctx = binding.df_cross_attn_fwd(q.view(T, cfg.heads, hid // cfg.heads), k, v, cu_seqlens_q=cu_seqlens_q,
                                         max_seqlen_q=max_seqlen_q, cu_seqlens_k=cu_seqlens_k,
-                                        max_seqlen_k=max_seqlen_k, stream=stream)
-        (o,) = binding.df_linear(ctx.view(T, hid), [w["w_o"]], [w["b_o"]], stream=stream)
+                                        max_seqlen_k=max_seqlen_k, status=status, stream=stream)
+        (o,) = binding.df_linear(ctx.view(T, hid), [w["w_o"]], [w["b_o"]], status=status, stream=stream)
         return binding.df_layernorm(o, w["ln_g"], w["ln_b"], residual=x, eps=cfg.eps, stream=stream)
