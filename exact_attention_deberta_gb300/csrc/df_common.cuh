@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "df_attn.h"
 
 namespace dfa {
@@ -198,6 +200,26 @@ __device__ __forceinline__ void grid_dependency_wait() {
 }
 __device__ __forceinline__ void allow_dependent_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Host: a buffer of a call, and whether any that it writes overlaps one that it reads or
+// another that it writes (NULL and empty ones overlap nothing).
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+inline bool overlapping(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (const Span& r : read)
+      if (meet(*w, r)) return true;
+    for (auto o = w + 1; o != written.end(); ++o)
+      if (meet(*w, *o)) return true;
+  }
+  return false;
 }
 
 // Launches `kernel` on `s` with the programmatic-serialisation attribute: it

@@ -125,6 +125,12 @@ extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void*
   if (total_q == 0) return DF_OK;
   if (!out) return DF_ERR_INVALID_ARG;
   if (!al16(out) || !al16(out_lo) || ((uintptr_t)lse & 3u) != 0) return DF_ERR_ALIGNMENT;
+  const size_t q_bytes = (size_t)total_q * H * d * 2, k_bytes = (size_t)total_k * Hk * d * 2;
+  const size_t cu_bytes = ((size_t)B + 1) * 4;
+  if (overlapping({{out, q_bytes}, {out_lo, q_bytes}, {lse, (size_t)total_q * H * 4}},
+                  {{q, q_bytes}, {k, k_bytes}, {v, k_bytes}, {key_mask, (size_t)total_k}, {cu_seqlens_q, cu_bytes},
+                   {cu_seqlens_k, cu_bytes}}))
+    return DF_ERR_INVALID_ARG;
   a.out = out;
   a.out_lo = out_lo;
   a.lse = lse;

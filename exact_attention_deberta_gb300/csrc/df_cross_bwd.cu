@@ -891,6 +891,13 @@ extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void*
   if (need == 0) return DF_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need) return DF_ERR_WORKSPACE;
   if (total_q == 0 && total_k == 0) return DF_OK;
+  const size_t q_bytes = (size_t)total_q * H * d * 2, k_bytes = (size_t)total_k * Hk * d * 2;
+  const size_t cu_bytes = ((size_t)B + 1) * 4;
+  if (overlapping({{dq, q_bytes}, {dk, k_bytes}, {dv, k_bytes}, {workspace, need}},
+                  {{q, q_bytes}, {k, k_bytes}, {v, k_bytes}, {out, q_bytes}, {out_lo, q_bytes}, {dout, q_bytes},
+                   {lse, (size_t)total_q * H * 4}, {key_mask, (size_t)total_k}, {cu_seqlens_q, cu_bytes},
+                   {cu_seqlens_k, cu_bytes}}))
+    return DF_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = dtype == DF_BF16;
   const size_t rows = (size_t)total_q * H;

@@ -667,6 +667,8 @@ extern "C" df_status df_embedding(const void* ids, int ids_64, int T, const void
   if (T == 0) return DF_OK;
   if (!ids || !table || !out) return DF_ERR_INVALID_ARG;
   if (((uintptr_t)ids & (ids_64 ? 7u : 3u)) != 0 || !al16(table) || !al16(out)) return DF_ERR_ALIGNMENT;
+  const size_t row = (size_t)N * (dtype == DF_FP32 ? 4 : 2);
+  if (overlapping({{out, T * row}}, {{ids, (size_t)T * (ids_64 ? 8 : 4)}, {table, V * row}})) return DF_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == DF_BF16) launch_lookup<__nv_bfloat16>(ids, ids_64, T, table, V, N, scale, out, status, s);
   else if (dtype == DF_FP16) launch_lookup<__half>(ids, ids_64, T, table, V, N, scale, out, status, s);
@@ -691,6 +693,9 @@ extern "C" df_status df_embedding_bwd(const void* ids, int ids_64, int T, const 
     return DF_ERR_ALIGNMENT;
   const GradLayout l = grad_layout(T, N, V, !accumulate);
   if (!workspace || workspace_bytes < std::max<size_t>(l.total, 256)) return DF_ERR_WORKSPACE;
+  if (overlapping({{grad, (size_t)V * N * 4}, {workspace, l.total}},
+                  {{ids, (size_t)T * (ids_64 ? 8 : 4)}, {dout, (size_t)T * N * (dtype == DF_FP32 ? 4 : 2)}}))
+    return DF_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   if (T == 0) {
     if (!accumulate && cudaMemsetAsync(grad, 0, (size_t)V * N * 4, s) != cudaSuccess) return DF_ERR_CUDA;

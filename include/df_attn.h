@@ -497,9 +497,9 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  * and in steps of 2^-31 of it below that).  Keys that do not count, and rows of k
  * and v outside the sequence, may hold anything (NaN included); a NaN that counts
  * makes its rows' out and lse NaN.  out, out_lo and lse must not overlap the
- * inputs.  One launch, no workspace; equal inputs give equal bits.
+ * inputs or one another.  One launch, no workspace; equal inputs give equal bits.
  * Errors: DF_ERR_INVALID_ARG (NULL pointer, sizes, H % Hk, scale, key_mask with
- * cu_seqlens_k, dtype), DF_ERR_UNSUPPORTED (fp32, d, H / Hk > 128, over 2^30
+ * cu_seqlens_k, dtype, results that overlap), DF_ERR_UNSUPPORTED (fp32, d, H / Hk > 128, over 2^30
  * rows, over 2^31 rows times key heads), DF_ERR_ALIGNMENT (tensors 16 bytes, lse
  * and cu_seqlens 4), DF_ERR_CUDA. */
 df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
@@ -519,9 +519,9 @@ df_status df_cross_attn_fwd(const void* q, const void* k, const void* v,
  *                      of the accuracy described there)
  *   dout       like out
  *   dq, dk, dv like q, k, v, in `dtype`: written in full (from cu_seqlens[0] on);
- *              must not overlap the inputs.  Keys that do not count and rows
- *              behind the last packed sequence get zeros.  (fp16: dv holds the
- *              keys' norms meanwhile)
+ *              must not overlap the inputs, one another or the workspace.  Keys
+ *              that do not count and rows behind the last packed sequence get
+ *              zeros.  (fp16: dv holds the keys' norms meanwhile)
  *   workspace  at least df_cross_attn_bwd_workspace_size() bytes, 256-byte
  *              aligned, contents need not be initialised; calls that share it
  *              must not overlap
@@ -560,7 +560,7 @@ size_t df_cross_attn_bwd_workspace_size(int total_q, int H);
  *           caller zeroes it.
  * N a multiple of 8, at most 65536; T = 0 is a call that does nothing.  One
  * launch.  Errors: DF_ERR_INVALID_ARG (NULL pointer, T < 0 or > 2^30, V or
- * N < 1, dtype), DF_ERR_UNSUPPORTED (N), DF_ERR_ALIGNMENT (table or out not
+ * N < 1, dtype, out that overlaps ids or table), DF_ERR_UNSUPPORTED (N), DF_ERR_ALIGNMENT (table or out not
  * 16-byte aligned, ids not aligned to their own size), DF_ERR_CUDA. */
 df_status df_embedding(const void* ids, int ids_64, int T, const void* table, int V, int N,
                        float scale, void* out, df_dtype dtype, int32_t* status,
@@ -578,7 +578,8 @@ df_status df_embedding(const void* ids, int ids_64, int T, const void* table, in
  *              aligned, contents need not be initialised; calls that share it
  *              must not overlap
  * Errors as df_embedding, and DF_ERR_INVALID_ARG for padding_idx outside
- * [-1, V), DF_ERR_WORKSPACE. */
+ * [-1, V) or for grad or workspace that overlap each other, ids or dout,
+ * DF_ERR_WORKSPACE. */
 df_status df_embedding_bwd(const void* ids, int ids_64, int T, const void* dout, int V, int N,
                            float scale, int padding_idx, int accumulate, float* grad,
                            df_dtype dtype, int32_t* status, void* workspace,
