@@ -91,8 +91,13 @@ __device__ __forceinline__ void store8_past_l2(T* p, const float (&f)[8]) {
   for (int e = 0; e < (int)sizeof(T) / 2; ++e) __stcs(reinterpret_cast<uint4*>(p) + e, v[e]);
 }
 
+// The id is kept from here on and not read again, whatever the compiler would make of it: the
+// value that is checked against the table is the one that is used, also where another
+// stream writes the ids meanwhile.
 __device__ __forceinline__ long long load_id(const void* ids, int ids64, size_t t) {
-  return ids64 ? (long long)static_cast<const int64_t*>(ids)[t] : (long long)static_cast<const int32_t*>(ids)[t];
+  long long id = ids64 ? (long long)static_cast<const int64_t*>(ids)[t] : (long long)static_cast<const int32_t*>(ids)[t];
+  asm("" : "+l"(id));
+  return id;
 }
 
 // A warp takes R consecutive tokens, R rows of loads in flight per 256 columns.
