@@ -27,8 +27,8 @@
 // part of the key tiles; the partial (max, sum, O) are joined through
 // distributed shared memory, so no workspace and no second launch is needed.
 //
-// Measured (GB300): 19 x 8 heads, 2048 queries x 8192 keys, d = 128, bf16: 950 us,
-// 1374 TFLOP/s.  A tile of 128 x 128 scores takes about 1800 cycles of an SM, of
+// Measured (GB300): 19 x 8 heads, 2048 queries x 8192 keys, d = 128, bf16: 943 to
+// 959 us, 1361 to 1384 TFLOP/s.  A tile of 128 x 128 scores takes about 1800 cycles of an SM, of
 // which its products are 1034; the rest is the chain S, softmax, P.V, next S of
 // each team, which two teams do not fill (a third has no tensor memory).  Two CTAs
 // of one team each per SM, whose ends overlap better but which cannot take turns,

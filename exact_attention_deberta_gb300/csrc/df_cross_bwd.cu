@@ -30,9 +30,10 @@
 //                 the resident rows' scales beside the item's first tile
 //   warps 8-15    P and dS, one thread per resident row; the epilogue
 //
-// Measured (GB300, bf16): 16 x 12 heads, 2048 queries x 8192 keys, d = 64: 2.31 ms
-// (10 flops per score and column: 892 TFLOP/s; with the two products that are done
-// twice 1249); 19 x 8 heads, d = 128: 3.39 ms (963, 1348).  Bound by the tensor core:
+// Measured (GB300, bf16): 16 x 12 heads, 2048 queries x 8192 keys, d = 64: 2.30 to 2.35 ms
+// (10 flops per score and column: 877 to 896 TFLOP/s; with the two products that are done
+// twice 1228 to 1255); 19 x 8 heads, d = 128: 3.39 to 3.46 ms (943 to 963; 1321 to 1348);
+// fp16: 2.57 and 3.64.  Bound by the tensor core:
 // S and dP in halves of 64 columns run at two thirds of its rate, so a 128 x 128 tile
 // takes at least 1498 (keys) or 1138 (queries) cycles at d = 64 and takes about 1700
 // and 1290; 2591 and 2074 at d = 128, and takes about 3500 and 2600 (only two buffers

@@ -1,16 +1,16 @@
 // Embedding lookup with scaling, out[t] = scale * table[ids[t]], and the
 // gradient of the table, grad[v] (+)= scale * sum_{t: ids[t] = v} dout[t].
 //
-// Lookup: one warp per token, 16-byte vectors; HBM bound (each row that the
-// ids reach is read once, the repeats come from L2, each output row is written
-// once).
+// Lookup: a warp per token, or per four tokens where there are many, 16-byte vectors;
+// HBM bound (each row that the ids reach is read once, the repeats come from L2, each
+// output row is written once): 131072 x 768, bf16: 41 to 44 us.
 //
 // Gradient.  Adding rows with atomics would make the last bits depend on the
 // order of arrival, so the tokens are sorted by id first (a stable radix sort
 // of (id, position) pairs) and every row of the table is then the sum of one
 // run of the sorted list, in ascending position:
-//   1. sort.  Few tokens (to 8192): one block, 8 bits per pass, pairs in shared
-//      memory.  More: tiles of 512 or 2048 keys, at most 10 bits per pass (two passes for
+//   1. sort.  Few tokens (to 8192; to 2048 where nothing has to be zeroed): one block, 8
+//      bits per pass, pairs in shared memory.  More: tiles of 512 or 2048 keys, at most 10 bits per pass (two passes for
 //      ids below 2^20); a pass counts the digits of each tile, scans each
 //      digit's counts over the tiles, and scatters (rank inside the tile by warp
 //      digit matching, so that equal digits keep their order).  Ids that pass no
@@ -40,18 +40,10 @@ constexpr int kSortThreads = 256;
 constexpr int kMaxDigitBits = 10;
 constexpr int kSlice = 256;                             // columns per warp of the sums
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const T* h = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = IO<T>::to_f(h[e]);
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
 // Eight values as loaded, converted where they are added.
@@ -410,7 +402,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t v, int c, c
   if (v >= (uint32_t)a.V) return;
   float* p = a.grad + (size_t)v * a.N + c;
   float f[8];
-  if (a.accumulate) load8<float>(p, f);
+  if (a.accumulate) load8(p, f);
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = a.accumulate ? f[e] + acc[e] * a.scale : acc[e] * a.scale;
   store8<float>(p, f);
@@ -526,7 +518,7 @@ __global__ void __launch_bounds__(256, 4) join_runs(const SumArgs a) {
   if (lane == 0) s_end[warp] = is_long ? end : 0;
   float acc[8];
   if (begins && !is_long && col) {
-    load8<float>(a.part + ((size_t)chunk * 2 + 1) * a.N + c, acc);
+    load8(a.part + ((size_t)chunk * 2 + 1) * a.N + c, acc);
     add_partials(a, chunk + 1, end, c, acc);
     write_row(a, v, c, acc);
   }
@@ -544,7 +536,7 @@ __global__ void __launch_bounds__(256, 4) join_runs(const SumArgs a) {
     }
     __syncthreads();
     if (warp == w && col) {
-      load8<float>(a.part + ((size_t)first * 2 + 1) * a.N + c, acc);
+      load8(a.part + ((size_t)first * 2 + 1) * a.N + c, acc);
       for (int u = 0; u < 8; ++u)
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] += s_part[u][lane * 8 + x];
@@ -577,19 +569,19 @@ struct GradLayout {
 GradLayout grad_layout(int T, int N, int V, bool zeroed) {
   GradLayout l;
   // keys per thread of a sorting block: small tiles spread few tokens over the SMs,
-  // large ones leave fewer counts to scan (whole gradient, 768 wide: 32768 tokens 59 us
-  // at 2, 72 at 8; 65536: 77, 95; 131072: 168, 148)
+  // large ones leave fewer counts to scan (whole gradient, ten in a graph, 768 wide: 32768
+  // tokens into 50000 rows 57 us at 2, 63 at 8; 65536: 71, 77; 131072 into 128100: 153, 133)
   l.items = T <= 65536 ? 2 : 8;
   l.tiles = (T + kSortThreads * l.items - 1) / (kSortThreads * l.items);
   // short chunks spread few tokens over more warps, long ones leave fewer partial
-  // rows (whole gradient, bf16; 8192 x 1024: 45 us at 8, 57 at 32; 32768 x 768: 67 at
-  // both; 131072 x 768: 164 at 8, 149 at 32)
+  // rows (whole gradient, bf16; 8192 x 1024: 46 us at 8, 58 at 32; 32768 x 768: 57, 58;
+  // 65536 x 768: 85, 71; 131072 x 768: 161, 133)
   l.chunk = T <= 32768 ? 8 : 32;
   l.chunks = (T + l.chunk - 1) / l.chunk;
   int key_bits = 1;  // keys 0 .. V
   while (key_bits < 32 && ((unsigned long long)V >> key_bits) != 0) ++key_bits;
-  // one block sorts what the zero fill hides (2048 x 768 into 50000 rows: 33 us, 34 in
-  // tiles; 8192 x 1024: 46, 49), or few tokens (added to the table: 17, 21; 38, 28)
+  // one block sorts what the zero fill hides (2048 x 768 into 50000 rows: 35 us, 34 in
+  // tiles; 8192 x 1024: 46, 50), or few tokens (added to the table: 17, 22; 35, 30)
   l.small = T <= (zeroed ? kSmallSort : 2048);
   const int most = l.small ? kSmallBits : kMaxDigitBits;
   l.passes = (key_bits + most - 1) / most;
@@ -623,7 +615,7 @@ template <typename T>
 void launch_lookup(const void* ids, int ids64, int n, const void* table, int V, int N, float scale, void* out,
                    int32_t* status, cudaStream_t s) {
   // four rows per warp once that still leaves every SM its resident warps (131072 x
-  // 768: 56 us, 61 with one; 38912: 12.6, 14.2; 16384: 6.6, 6.2)
+  // 768: 40.7 us, 43.5 with one; 38912: 12.4, 12.8; 8192 x 1024: 5.5, 5.0; 2048: 4.0, 3.2)
   if (n >= 4 * 64 * sm_count())
     lookup_kernel<T, 4><<<(n + 31) / 32, 256, 0, s>>>(ids, ids64, n, static_cast<const T*>(table), V, N, scale,
                                                       static_cast<T*>(out), status);
