@@ -97,7 +97,10 @@ def _current(stream, like=None):
     it runs on: a freed block is then not handed out while that stream still uses it."""
     if not isinstance(stream, torch.cuda.Stream):
         device = like.device if isinstance(like, torch.Tensor) and like.is_cuda else None
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # (torch takes an external stream of handle 0 for a request for a new stream)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)  # cudaStreamLegacy
+                  else torch.cuda.ExternalStream(handle, device=device))
     return torch.cuda.stream(stream)
 
 

@@ -41,3 +41,27 @@ def test_layers_on_a_stream_given_as_an_argument(lib, handle):
         junk = [torch.full((n,), 9.0, dtype=torch.bfloat16, device="cuda") for n in sizes for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 4 * len(sizes)
+
+
+def test_the_default_stream_as_a_handle(lib):
+    # its handle is 0: what is called on it runs there and belongs to it, whatever the
+    # current stream is
+    default, side = torch.cuda.default_stream(), torch.cuda.Stream()
+    assert default.cuda_stream == 0
+    x = torch.zeros(4, device="cuda")
+    with torch.cuda.stream(side):
+        for given in (0, default, default.cuda_stream):
+            with lib._current(given, x):
+                assert torch.cuda.current_stream() == default
+        assert torch.cuda.current_stream() == side
+    # ordered behind the work already there: the ids are written on the default stream
+    table = torch.randn(50, 64, device="cuda")
+    ids = torch.zeros(1 << 20, dtype=torch.int64, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        with torch.cuda.stream(default):
+            torch.cuda._sleep(20_000_000)
+            ids.fill_(7)
+        out = lib.df_embedding(ids, table, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-1], table[7]) and bool((out == table[7]).all())

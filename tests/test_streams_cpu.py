@@ -138,3 +138,16 @@ def test_every_call_with_a_stream_is_listed(record):
     takes = {n for n, f in vars(b).items() if inspect.isfunction(f) and not n.startswith("_") and
              "stream" in inspect.signature(f).parameters}
     assert takes - waits <= set(NAMES)
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_streams_handles(monkeypatch, handle):
+    # (an external stream of handle 0 would be a new stream of torch's)
+    from exact_attention_deberta_gb300.build import build
+    build()
+    from exact_attention_deberta_gb300 import binding
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: f"external {handle}")
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert binding._current(handle, None) == "default"
+    assert binding._current(64, None) == "external 64"
