@@ -95,8 +95,11 @@ def _current(stream, like=None):
     """A context with ``stream`` (a torch stream or its handle, on the device of the
     tensor ``like``) current, so that what a call allocates belongs to the stream that
     it runs on: a freed block is then not handed out while that stream still uses it."""
-    if not isinstance(stream, torch.cuda.Stream):
-        device = like.device if isinstance(like, torch.Tensor) and like.is_cuda else None
+    device = like.device if isinstance(like, torch.Tensor) and like.is_cuda else None
+    if isinstance(stream, torch.cuda.Stream):
+        if device is not None and stream.device != device:
+            raise ValueError("the stream must be on the tensors' device")
+    else:
         handle = int(getattr(stream, "cuda_stream", stream))
         # (torch takes an external stream of handle 0 for a request for a new stream)
         stream = (torch.cuda.default_stream(device) if handle in (0, 1)  # cudaStreamLegacy

@@ -151,3 +151,26 @@ def test_the_default_streams_handles(monkeypatch, handle):
     monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
     assert binding._current(handle, None) == "default"
     assert binding._current(64, None) == "external 64"
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    from exact_attention_deberta_gb300.build import build
+    build()
+    from exact_attention_deberta_gb300 import binding
+
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 64
+
+    class Here(OnDevice):
+        device = torch.device("cuda", 0)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    x = torch.Tensor._make_subclass(Here, torch.zeros(2, 512))
+    with pytest.raises(ValueError, match="device"):
+        binding._current(Stream(), x)
+    with pytest.raises(ValueError, match="device"):
+        binding.df_layernorm(x, x, x, stream=Stream())
+    Here.device = Stream.device
+    assert isinstance(binding._current(Stream(), x), Stream)
