@@ -14,16 +14,16 @@ def lib():
     return binding
 
 
-# B = 2, H = 4, Hk = 2, Lq = 3, Lk = 9, d = 64, bf16
-BYTES = dict(q=3072, k=4608, v=4608, out=3072, lo=3072, lse=96, dout=3072, dq=3072, dk=4608, dv=4608, mask=18,
-             cu_q=12, cu_k=12, ws=6 * 4 * 8)
+# B = 2, H = 4, Hk = 2, Lq = 5, Lk = 9, d = 64, bf16
+BYTES = dict(q=5120, k=4608, v=4608, out=5120, lo=5120, lse=160, dout=5120, dq=5120, dk=4608, dv=4608, mask=18,
+             cu_q=12, cu_k=12, ws=10 * 4 * 8)
 AT = {n: 0x100000 * (i + 1) for i, n in enumerate(BYTES)}
 
 
 def fwd(b, **over):
     a = {**AT, "mask": None, "cu_q": None, "cu_k": None, **over}
     p = lambda n: None if a[n] is None else ctypes.c_void_p(a[n])  # noqa: E731
-    return b.raw_library.df_cross_attn_fwd(p("q"), p("k"), p("v"), p("mask"), p("cu_q"), p("cu_k"), 2, 4, 2, 3, 9, 6, 18,
+    return b.raw_library.df_cross_attn_fwd(p("q"), p("k"), p("v"), p("mask"), p("cu_q"), p("cu_k"), 2, 4, 2, 5, 9, 10, 18,
                                            64, 0.125, 0, p("out"), p("lo"), p("lse"), None, None)
 
 
@@ -31,7 +31,7 @@ def bwd(b, **over):
     a = {**AT, "mask": None, "cu_q": None, "cu_k": None, **over}
     p = lambda n: None if a[n] is None else ctypes.c_void_p(a[n])  # noqa: E731
     return b.raw_library.df_cross_attn_bwd(p("q"), p("k"), p("v"), p("out"), p("lo"), p("lse"), p("dout"), p("mask"),
-                                           p("cu_q"), p("cu_k"), 2, 4, 2, 3, 9, 6, 18, 64, 0.125, 0, p("dq"), p("dk"),
+                                           p("cu_q"), p("cu_k"), 2, 4, 2, 5, 9, 10, 18, 64, 0.125, 0, p("dq"), p("dk"),
                                            p("dv"), None, p("ws"), 1 << 16, None)
 
 
