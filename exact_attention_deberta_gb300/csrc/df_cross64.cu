@@ -28,8 +28,8 @@
 // part of the key tiles; the partial (max, sum, O) are joined through
 // distributed shared memory, so no workspace and no second launch is needed.
 //
-// Measured (GB300): 16 x 12 heads, 2048 queries x 8192 keys, bf16: 721 to 753 us by
-// machine and inputs, 1095 to 1144 TFLOP/s.  A tile of 128 x 128 scores takes about 1020 cycles of an SM; its
+// Measured (GB300): 16 x 12 heads, 2048 queries x 8192 keys, bf16: 721 to 758 us by
+// machine and inputs, 1088 to 1144 TFLOP/s.  A tile of 128 x 128 scores takes about 1020 cycles of an SM; its
 // products take 618 of the tensor core (P.V, 64 columns wide, runs at two thirds
 // of its rate), its exponentials 512.  What is left is latency: a score buffer goes
 // around S, softmax (1470 cycles), P.V, S in about 3 x 1020.  Of what would shorten

@@ -498,6 +498,8 @@ df_status df_layernorm(const void* x, const void* residual, const void* gamma, c
  * and v outside the sequence, may hold anything (NaN included); a NaN that counts
  * makes its rows' out and lse NaN.  out, out_lo and lse must not overlap the
  * inputs or one another.  One launch, no workspace; equal inputs give equal bits.
+ * (In packed mode a tile finds its sequence by a walk over the offsets: some ten
+ * thousand short sequences are slow, 100000 of a few tokens take 0.45 s.)
  * Errors: DF_ERR_INVALID_ARG (NULL pointer, sizes, H % Hk, scale, key_mask with
  * cu_seqlens_k, dtype, results that overlap), DF_ERR_UNSUPPORTED (fp32, d, H / Hk > 128, over 2^30
  * rows, over 2^31 rows times key heads), DF_ERR_ALIGNMENT (tensors 16 bytes, lse
