@@ -706,6 +706,13 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
             return df_cross_attn_fwd(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
                                      max_seqlen_k=max_seqlen_k, scale=scale, out=out, with_stats=with_stats,
                                      status=status)
+    return _attn_fwd(_lib.df_cross_attn_fwd, "df_cross_attn_fwd", (), q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k,
+                     max_seqlen_q, max_seqlen_k, scale, out, with_stats, status)
+
+
+def _attn_fwd(fn, what, reach, q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, out,
+              with_stats, status):
+    """Cross attention, or (``reach``: window and sinks) self attention."""
     idx = _on_device((q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, out, status),
                      "q k v key_mask cu_seqlens_q cu_seqlens_k out status")
     B, H, Hk, Lq, Lk, Tq, Tk, d = _cross_shape(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
@@ -720,10 +727,10 @@ def df_cross_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=No
     stats = None
     if with_stats:
         stats = CrossStats(torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device), torch.empty_like(q))
-    _check(_call_on(idx, _lib.df_cross_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask),
-                    _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype],
-                    out.data_ptr(), stats.out_lo.data_ptr() if stats else None,
-                    stats.lse.data_ptr() if stats else None, _addr(status)), "df_cross_attn_fwd")
+    _check(_call_on(idx, fn, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q),
+                    _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, *reach, _DTYPE[q.dtype], out.data_ptr(),
+                    stats.out_lo.data_ptr() if stats else None, stats.lse.data_ptr() if stats else None,
+                    _addr(status)), what)
     return (out, stats) if with_stats else out
 
 
@@ -748,6 +755,12 @@ def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=Non
             return df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k,
                                      max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, scale=scale, grads=grads,
                                      workspace=workspace, status=status)
+    return _attn_bwd(_lib.df_cross_attn_bwd, "df_cross_attn_bwd", (), q, k, v, out, stats, dout, key_mask, cu_seqlens_q,
+                     cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, grads, workspace, status)
+
+
+def _attn_bwd(fn, what, reach, q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+              max_seqlen_k, scale, grads, workspace, status):
     if grads is None:
         grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
     dq, dk, dv = grads
@@ -767,12 +780,54 @@ def df_cross_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=Non
         _status_word(status)
     if workspace is None:
         workspace = torch.empty(max(df_cross_attn_bwd_workspace_size(Tq, H), 256), dtype=torch.uint8, device=q.device)
-    _check(_call_on(idx, _lib.df_cross_attn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                    _addr(out_lo), lse.data_ptr(), dout.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q),
-                    _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq, Tk, d, scale, _DTYPE[q.dtype], dq.data_ptr(),
-                    dk.data_ptr(), dv.data_ptr(), _addr(status), workspace.data_ptr(),
-                    workspace.numel() * workspace.element_size()), "df_cross_attn_bwd")
+    _check(_call_on(idx, fn, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _addr(out_lo), lse.data_ptr(),
+                    dout.data_ptr(), _addr(key_mask), _addr(cu_seqlens_q), _addr(cu_seqlens_k), B, H, Hk, Lq, Lk, Tq,
+                    Tk, d, scale, *reach, _DTYPE[q.dtype], dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _addr(status),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size()), what)
     return dq, dk, dv
+
+
+_lib.df_self_attn_fwd.argtypes = [_vp] * 6 + [_i] * 8 + [ctypes.c_float] + [_i] * 3 + [_vp] * 5
+_lib.df_self_attn_fwd.restype = _i
+_lib.df_self_attn_bwd.argtypes = [_vp] * 10 + [_i] * 8 + [ctypes.c_float] + [_i] * 3 + [_vp] * 5 + [_sz, _vp]
+_lib.df_self_attn_bwd.restype = _i
+
+
+def _reach(window, sinks):
+    window, sinks = int(window or 0), int(sinks)
+    _int_sizes(window=window, sinks=sinks)
+    return window, sinks
+
+
+def df_self_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *, max_seqlen_q=None,
+                     max_seqlen_k=None, window=0, sinks=0, scale=None, out=None, with_stats=False, status=None,
+                     stream=None):
+    """Causal attention: the queries are the last tokens of their sequence (all of them, or
+    the next part of a prompt) and see the keys up to their own position; with ``window``
+    the last ``window`` of those and the sequence's first ``sinks``.  Layouts, arguments and
+    results as ``df_cross_attn_fwd``."""
+    if stream is not None:
+        with _current(stream, q):
+            return df_self_attn_fwd(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+                                    max_seqlen_k=max_seqlen_k, window=window, sinks=sinks, scale=scale, out=out,
+                                    with_stats=with_stats, status=status)
+    return _attn_fwd(_lib.df_self_attn_fwd, "df_self_attn_fwd", _reach(window, sinks), q, k, v, key_mask, cu_seqlens_q,
+                     cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, out, with_stats, status)
+
+
+def df_self_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *,
+                     max_seqlen_q=None, max_seqlen_k=None, window=0, sinks=0, scale=None, grads=None, workspace=None,
+                     status=None, stream=None):
+    """Gradients (dq, dk, dv), in the inputs' dtype, of ``df_self_attn_fwd`` with the same
+    arguments; ``out`` and ``stats`` as its call with ``with_stats`` gave them.  The
+    workspace is ``df_cross_attn_bwd_workspace_size``."""
+    if stream is not None:
+        with _current(stream, q):
+            return df_self_attn_bwd(q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k,
+                                    max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, window=window, sinks=sinks,
+                                    scale=scale, grads=grads, workspace=workspace, status=status)
+    return _attn_bwd(_lib.df_self_attn_bwd, "df_self_attn_bwd", _reach(window, sinks), q, k, v, out, stats, dout,
+                     key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, grads, workspace, status)
 
 
 raw_library = _lib

@@ -73,6 +73,15 @@ long long cross_query_tiles(const CrossArgs& a) {
   return ((long long)a.Tq / a.tpt + a.B + 1) * a.Hk;
 }
 
+bool self_reach(int* window, int* sinks) {
+  if (*window < 0 || *sinks < 0) return false;
+  constexpr int kAll = 1 << 30;  // no sequence is longer
+  if (*window >= kAll) *window = 0;
+  if (*window == 0) *sinks = 0;  // every earlier key is seen
+  *sinks = std::min(*sinks, kAll);
+  return true;
+}
+
 df_status cross_check(const void* q, const void* k, const void* v, const uint8_t* key_mask, const int32_t* cu_q,
                       const int32_t* cu_k, int B, int H, int Hk, int Lq, int Lk, int total_q, int total_k, int d,
                       float scale, df_dtype dtype, int32_t* status, CrossArgs* a) {
@@ -107,6 +116,7 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
   a->kscale = (float)((double)scale * 1.4426950408889634);
   a->status = status;
   a->budget = wait_budget();
+  a->window = a->sinks = 0;
   return DF_OK;
 }
 
@@ -114,10 +124,11 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
 
 using namespace dfa;
 
-extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void* v, const uint8_t* key_mask,
-                                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
-                                       int Lq, int Lk, int total_q, int total_k, int d, float scale, df_dtype dtype,
-                                       void* out, void* out_lo, float* lse, int32_t* status, df_stream_t stream) {
+// `self`: causal, with a window and sinks (the caller has checked them).
+static df_status forward(bool self, int window, int sinks, const void* q, const void* k, const void* v,
+                         const uint8_t* key_mask, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H,
+                         int Hk, int Lq, int Lk, int total_q, int total_k, int d, float scale, df_dtype dtype, void* out,
+                         void* out_lo, float* lse, int32_t* status, df_stream_t stream) {
   FwdArgs a;
   const df_status st = cross_check(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk, Lq, Lk, total_q, total_k,
                                    d, scale, dtype, status, &a.c);
@@ -131,6 +142,8 @@ extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void*
                   {{q, q_bytes}, {k, k_bytes}, {v, k_bytes}, {key_mask, (size_t)total_k}, {cu_seqlens_q, cu_bytes},
                    {cu_seqlens_k, cu_bytes}}))
     return DF_ERR_INVALID_ARG;
+  a.c.window = window;
+  a.c.sinks = sinks;
   a.out = out;
   a.out_lo = out_lo;
   a.lse = lse;
@@ -152,11 +165,32 @@ extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void*
   // against 36 without; 8 heads, d = 128, 64 queries, 4096 keys: 13 against 38; 4 x
   // 12 heads, 33 queries, 300 keys: 9.3 against 10.9 with a tile for each.
   a.splits = 1;
-  const int key_tiles = (Lk + kFwdKeys - 1) / kFwdKeys;
+  int key_tiles = (Lk + kFwdKeys - 1) / kFwdKeys;
+  // (a window's tiles, whichever position it ends at, and the sinks')
+  if (window > 0) key_tiles = (int)std::min<long long>(key_tiles, ((long long)window + 127 + 127) / 128 + 1 + (sinks + 127) / 128);
   while (a.splits < 8 && items * a.splits * 2 <= sms && a.splits * 4 <= key_tiles) a.splits *= 2;
   a.split_bits = a.splits == 8 ? 3 : a.splits / 2;
   const int grid = (int)items * a.splits;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = d <= 64 ? launch_cross64(a, maps, bf16, grid, s) : launch_cross128(a, maps, bf16, grid, s);
+  const cudaError_t e =
+      d <= 64 ? launch_cross64(a, maps, bf16, self, grid, s) : launch_cross128(a, maps, bf16, self, grid, s);
   return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+extern "C" df_status df_cross_attn_fwd(const void* q, const void* k, const void* v, const uint8_t* key_mask,
+                                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
+                                       int Lq, int Lk, int total_q, int total_k, int d, float scale, df_dtype dtype,
+                                       void* out, void* out_lo, float* lse, int32_t* status, df_stream_t stream) {
+  return forward(false, 0, 0, q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk, Lq, Lk, total_q, total_k, d, scale,
+                 dtype, out, out_lo, lse, status, stream);
+}
+
+extern "C" df_status df_self_attn_fwd(const void* q, const void* k, const void* v, const uint8_t* key_mask,
+                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
+                                      int Lq, int Lk, int total_q, int total_k, int d, float scale, int window, int sinks,
+                                      df_dtype dtype, void* out, void* out_lo, float* lse, int32_t* status,
+                                      df_stream_t stream) {
+  if (!self_reach(&window, &sinks)) return DF_ERR_INVALID_ARG;
+  return forward(true, window, sinks, q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk, Lq, Lk, total_q, total_k, d,
+                 scale, dtype, out, out_lo, lse, status, stream);
 }

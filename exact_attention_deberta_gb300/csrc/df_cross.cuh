@@ -28,6 +28,7 @@ struct CrossArgs {
   float scale;
   int32_t* status;
   unsigned long long budget;
+  int window, sinks;         // self attention: see below
 };
 
 // A tile of one side's rows (queries, or keys in the backward's key kernel)
@@ -39,7 +40,41 @@ struct CrossItem {
   int no;   // tokens there
   int hk;   // key head; -1 ends the list
   int b;    // batch row (for key_mask)
+  // self attention: the positions of r0, and (key tiles) of the first query, o0
+  int p0, q0;
 };
+
+// Causal attention with a window (the kernels' SELF form).  The queries of a sequence are the
+// last of its tokens: query row i stands at position p = i + keys - queries and sees the keys
+// j <= p with j > p - window (window 0: all) or j < sinks.  A tile of queries meets the key
+// tiles of the sinks and then a run that ends at its last position; a tile of keys meets one
+// run of queries.
+
+// The key tiles of a query tile: the first `sinks` of them, then those from sinks + skip on.
+struct CrossBand {
+  int sinks, skip;
+  __device__ __forceinline__ int tile(int t) const { return t < sinks ? t : t + skip; }
+};
+__device__ __forceinline__ CrossBand key_band(const CrossArgs& a, const CrossItem& it) {
+  CrossBand r = {0, 0};
+  if (a.window == 0) return r;
+  r.sinks = (min(a.sinks, it.no) + 127) / 128;
+  r.skip = max(max(it.p0 - a.window + 1, 0) / 128 - r.sinks, 0);
+  return r;
+}
+// No key behind a query tile's last position counts.
+__device__ __forceinline__ void clip_causal(CrossItem& it) { it.no = max(0, min(it.no, it.p0 + it.nr)); }
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+// Of the 32 keys from `first` on, those that a query at position p sees.
+__device__ __forceinline__ uint32_t seen_bits(const CrossArgs& a, int p, int first) {
+  const uint32_t upto = low_bits(p + 1 - first);
+  return a.window == 0 ? upto : upto & (~low_bits(p + 1 - a.window - first) | low_bits(a.sinks - first));
+}
+// Whether every query of `n` from position p on sees all 128 keys from `first` on.
+__device__ __forceinline__ bool seen_whole(const CrossArgs& a, int p, int n, int first) {
+  return p >= first + 127 && (a.window == 0 || p + n - a.window <= first || first + 128 <= a.sinks);
+}
 
 // The sequences' rows on one side of a call.
 struct CrossSide {
@@ -186,7 +221,9 @@ __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
 // tokens are numbered by sequence, then key head, then position; in packed mode
 // the rows behind the last sequence count as one more sequence, whose other
 // side is empty.  The walk over packed sequences goes on from the last call's number,
-// in either direction.
+// in either direction.  SELF: a sequence's query tiles are numbered from its end, which
+// sees most keys (long items first), and a key tile meets the queries that see it.
+template <bool SELF = false, bool KEYS = false>
 struct TileWalk {
   int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones
   long long done = 0;  // tiles of the sequences before b0
@@ -196,7 +233,7 @@ struct TileWalk {
     const int lane = threadIdx.x & 31;
     CrossItem it;
     it.hk = -1;
-    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    it.r0 = it.nr = it.o0 = it.no = it.b = it.p0 = it.q0 = 0;
     if (number < 0) return it;
     int first, len, tiles, at;  // the sequence's rows and tiles, the tile's number in it
     if (!rows.cu) {
@@ -250,10 +287,20 @@ struct TileWalk {
       }
     }
     it.hk = at / tiles;
-    const int tok = (at - it.hk * tiles) * step;
+    const int turn = at - it.hk * tiles, tok = (SELF && !KEYS ? tiles - 1 - turn : turn) * step;
     it.r0 = first + tok;
     it.nr = min(step, len - tok);
     if (it.b < a.B) it.no = seq_rows(other, it.b, a.status, &it.o0);
+    if (SELF && !KEYS) it.p0 = tok + it.no - len;
+    if (SELF && KEYS) {
+      const int off = len - it.no, lo = max(0, tok - off);  // (query i stands at position i + off)
+      int hi = it.no;
+      if (a.window != 0 && tok >= a.sinks) hi = min(hi, tok + it.nr + a.window - 1 - off);
+      it.p0 = tok;
+      it.q0 = lo + off;
+      it.o0 += lo;
+      it.no = max(0, hi - lo);
+    }
     return it;
   }
 };
@@ -314,6 +361,8 @@ cudaError_t prepare_kernel(const void* kernel, int bytes, int regs, std::atomic<
 df_status cross_check(const void* q, const void* k, const void* v, const uint8_t* key_mask, const int32_t* cu_q,
                       const int32_t* cu_k, int B, int H, int Hk, int Lq, int Lk, int total_q, int total_k, int d,
                       float scale, df_dtype dtype, int32_t* status, CrossArgs* a);
+// Self attention: whether window and sinks are in range; puts what sees everything as window 0.
+bool self_reach(int* window, int* sinks);
 // An upper bound of the number of query tiles.
 long long cross_query_tiles(const CrossArgs& a);
 unsigned long long wait_budget();

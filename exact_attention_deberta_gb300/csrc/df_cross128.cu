@@ -144,7 +144,7 @@ __device__ __forceinline__ void keep_merged(float* dst, uint32_t ta, uint32_t tb
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool SELF>
 __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs args, const __grid_constant__ FwdMaps maps) {
   using SL = FwdSmem;
   constexpr int D = SL::D;
@@ -228,12 +228,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
 
   const unsigned long long budget = a.budget;
   const uint32_t rank = args.splits > 1 ? cluster_rank() : 0u;
-  auto part = [&](const CrossItem& it, int* t0) { return key_part(args, it, rank, t0); };
+  // an item's key tiles, and this CTA's part of them
+  auto band_of = [&](const CrossItem& it) { return SELF ? key_band(a, it) : CrossBand{0, 0}; };
+  auto part = [&](const CrossItem& it, const CrossBand& band, int* t0) { return key_part(args, it, band, rank, t0); };
   // the c-th item handed out, for one thread; hk = -1 at the end or after an abort
   auto read_item = [&](uint32_t c) {
     const uint32_t slot = c % kItemRing;
     CrossItem it;
-    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    it.r0 = it.nr = it.o0 = it.no = it.b = it.p0 = it.q0 = 0;
     it.hk = -1;
     if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort)) {
       it = *ring_slot(c);
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
     // ------------------------------------------------------------ items and loads
     setmaxnreg_dec<kOtherRegs>();
     // (the whole warp runs every step, and one lane of it issues)
-    TileWalk walk;
+    TileWalk<SELF> walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t kn0 = 0, kn1 = 0, vn0 = 0, vn1 = 0;  // tiles loaded for each team
     uint32_t qc = 0;
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
         mask_b = it.b;
         it.no = mask_n;
       }
+      if (SELF) clip_causal(it);
       bool room = true;
       if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort);
       if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       }
       if (it.hk < 0) break;
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
       if (nt > 0) {
         const uint32_t qb = qc % kQBufs;
         ok = ok && cross_wait(q_empty + qb, ((qc / kQBufs) & 1) ^ 1, budget, s_abort);
@@ -304,13 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       // The next item is asked for two tiles before this one's end: early enough to be
       // answered by then, late enough to leave it to a CTA that is through sooner.
       const int ask_at = args.splits > 1 ? INT_MAX : max(-2, nt - 2);
-      const int row0 = it.o0 + t0 * kKeys;
+      auto row_at = [&](int t) { return it.o0 + (SELF ? band.tile(t0 + t) : t0 + t) * kKeys; };
 #pragma unroll 1
       for (int t = -2; t < max(nt, -1); ++t) {
         const int w = t & 1;
         if (t == ask_at) claim.ask();
-        if (t >= 0) load(&maps.v, SL::v, v_full, v_empty, w, w ? vn1 : vn0, it.hk, row0 + t * kKeys);
-        if (t + 2 < nt) load(&maps.k, SL::k, k_full, k_empty, w, w ? kn1 : kn0, it.hk, row0 + (t + 2) * kKeys);
+        if (t >= 0) load(&maps.v, SL::v, v_full, v_empty, w, w ? vn1 : vn0, it.hk, row_at(t));
+        if (t + 2 < nt) load(&maps.k, SL::k, k_full, k_empty, w, w ? kn1 : kn0, it.hk, row_at(t + 2));
       }
       number = args.splits > 1 ? -1 : claim.answer(budget, s_abort);
     }
@@ -342,8 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
       if (it.hk < 0) break;
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      if (SELF) it.p0 = __shfl_sync(0xffffffffu, it.p0, 0);
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
       if (nt == 0) continue;
       const uint32_t qb = qc % kQBufs;
       ok = ok && cross_wait(q_full + qb, (qc / kQBufs) & 1, budget, s_abort);
@@ -409,20 +415,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
       if (it.hk < 0) break;
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      if (SELF) it.p0 = __shfl_sync(0xffffffffu, it.p0, 0);
       it.b = __shfl_sync(0xffffffffu, it.b, 0);
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
         const int w = t & 1;
         const uint32_t n = w ? vn1 : vn0;
         vn0 += !w;
         vn1 += w;
-        const int left = it.no - (t0 + t) * kKeys;
+        const int kt = SELF ? band.tile(t0 + t) : t0 + t, left = it.no - kt * kKeys;
         uint32_t bits[kWords];
         bool whole = left >= kKeys && !a.key_mask;
         if (!whole)
-          whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * kKeys : nullptr, left, bits);
+          whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)kt * kKeys : nullptr, left, bits);
         ok = ok && cross_wait(v_full + w, n & 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && !whole) zero_rows<kWords, kChunks>(sm + SL::v + w * SL::kTileBytes, bits);
@@ -456,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
       const CrossItem it = s_cur[~c & 1];
       if (it.hk < 0) break;
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
       // a row block without a valid row needs no weights: its P may hold anything,
       // since a row of P only reaches its own row of O
       const bool warp_in = __any_sync(0xffffffffu, sRow[row].x < it.nr);
@@ -478,12 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
           tmem_ld32(tSw, r0);
           tmem_ld32(tSw + 32, r1);
           tmem_ld_wait2(r0, r1);
-          const int left = it.no - (t0 + t) * kKeys;
-          if (a.key_mask || left < kKeys) {
+          const int kt = SELF ? band.tile(t0 + t) : t0 + t, left = it.no - kt * kKeys;
+          const bool cut = SELF && !seen_whole(a, it.p0, it.nr, kt * kKeys);
+          if (a.key_mask || left < kKeys || cut) {
             uint32_t bits[kWords];
-            if (!key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * kKeys : nullptr, left,
-                          bits)) {
-              const uint32_t b0 = half ? bits[kWords / 2] : bits[0], b1 = half ? bits[kWords / 2 + 1] : bits[1];
+            const bool all =
+                key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)kt * kKeys : nullptr, left, bits);
+            if (!all || cut) {
+              uint32_t b0 = half ? bits[kWords / 2] : bits[0], b1 = half ? bits[kWords / 2 + 1] : bits[1];
+              if (SELF && cut) {
+                const int p = it.p0 + sRow[row].x, first = kt * kKeys + (kKeys / 2) * half;
+                b0 &= seen_bits(a, p, first);
+                b1 &= seen_bits(a, p, first + 32);
+              }
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 if (!((b0 >> j) & 1u)) r0[j] = 0xff800000u;  // -infinity
@@ -628,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
   if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
-template <bool BF16>
+template <bool BF16, bool SELF>
 cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t s) {
-  auto kernel = cross128_kernel<BF16>;
+  auto kernel = cross128_kernel<BF16, SELF>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)FwdSmem::alloc, kRegs, &done);
   return e != cudaSuccess ? e : launch_clusters(kernel, a, maps, grid, kThreads, FwdSmem::alloc, s);
@@ -638,8 +654,9 @@ cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t
 
 }  // namespace
 
-cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s) {
-  return bf16 ? launch<true>(a, maps, grid, s) : launch<false>(a, maps, grid, s);
+cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s) {
+  if (self) return bf16 ? launch<true, true>(a, maps, grid, s) : launch<false, true>(a, maps, grid, s);
+  return bf16 ? launch<true, false>(a, maps, grid, s) : launch<false, false>(a, maps, grid, s);
 }
 
 }  // namespace dfa

@@ -73,7 +73,7 @@ struct FwdSmem {
   static_assert(128 * D * 4 <= kStages * kTileBytes, "O fits over K");
 };
 
-template <bool BF16>
+template <bool BF16, bool SELF>
 __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args, const __grid_constant__ FwdMaps maps) {
   using SL = FwdSmem;
   constexpr int D = SL::D;
@@ -154,12 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
 
   const unsigned long long budget = a.budget;
   const uint32_t rank = args.splits > 1 ? cluster_rank() : 0u;
-  auto part = [&](const CrossItem& it, int* t0) { return key_part(args, it, rank, t0); };
+  // an item's key tiles, and this CTA's part of them
+  auto band_of = [&](const CrossItem& it) { return SELF ? key_band(a, it) : CrossBand{0, 0}; };
+  auto part = [&](const CrossItem& it, const CrossBand& band, int* t0) { return key_part(args, it, band, rank, t0); };
   // the c-th item handed out, for one thread; hk = -1 at the end or after an abort
   auto read_item = [&](uint32_t c) {
     const uint32_t slot = c % kItemRing;
     CrossItem it;
-    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    it.r0 = it.nr = it.o0 = it.no = it.b = it.p0 = it.q0 = 0;
     it.hk = -1;
     if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort)) {
       it = *ring_slot(c);
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     setmaxnreg_dec<56>();
     // (the whole warp runs every step, and one lane of it issues: this loop's length
     // in instructions is what a tile's period comes down to)
-    TileWalk walk;
+    TileWalk<SELF> walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, qc = 0, k_issued = 0, v_issued = 0;
     int mask_b = -1, mask_n = 0;  // the last masked row measured
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         mask_b = it.b;
         it.no = mask_n;
       }
+      if (SELF) clip_causal(it);
       bool room = true;
       if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort);
       if (__any_sync(0xffffffffu, *s_abort || !room)) it.hk = -1;
@@ -210,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       }
       if (it.hk < 0) break;
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
       if (nt > 0) {
         const uint32_t qb = qc & 1;
         ok = ok && cross_wait(q_empty + qb, ((qc >> 1) & 1) ^ 1, budget, s_abort);
@@ -229,12 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       // The next item is asked for two tiles before this one's end: early enough to be
       // answered by then, late enough to leave it to a CTA that is through sooner.
       const int ask_at = args.splits > 1 ? -1 : max(0, nt - 2);
-      const int row0 = it.o0 + t0 * 128;
+      auto row_at = [&](int t) { return it.o0 + (SELF ? band.tile(t0 + t) : t0 + t) * 128; };
 #pragma unroll 1
       for (int t = 0; t <= nt; ++t) {
         if (t == ask_at) claim.ask();
-        if (t < nt) load(&maps.k, SL::k, k_full, k_empty, g + t, it.hk, row0 + t * 128, k_issued);
-        if (t > 0) load(&maps.v, SL::v, v_full, v_empty, g + t - 1, it.hk, row0 + t * 128 - 128, v_issued);
+        if (t < nt) load(&maps.k, SL::k, k_full, k_empty, g + t, it.hk, row_at(t), k_issued);
+        if (t > 0) load(&maps.v, SL::v, v_full, v_empty, g + t - 1, it.hk, row_at(t - 1), v_issued);
       }
       g += nt;
       number = args.splits > 1 ? -1 : claim.answer(budget, s_abort);
@@ -267,9 +271,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
       if (it.hk < 0) break;
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
+      if (SELF) it.p0 = __shfl_sync(0xffffffffu, it.p0, 0);
       it.b = __shfl_sync(0xffffffffu, it.b, 0);
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
       if (nt == 0) continue;
       if (qk_role) {
         const uint32_t qb = qc & 1;
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
           const uint32_t gs = g + t, s = gs % R, sb = gs % 3;
           const uint64_t dv = uniform(vtile_desc(v_addr + s * SL::kTileBytes, 0));
           const uint32_t tp = uniform(tS(sb)), first = uniform(t >= 2 ? 1u : 0u);  // P(t) overwrote its S
-          const int left = it.no - (t0 + t) * 128;
+          const int kt = SELF ? band.tile(t0 + t) : t0 + t, left = it.no - kt * 128;
           const bool partial = a.key_mask || left < 128;
           // P of this tile says that S was there, so that P.V of the stage's previous
           // tile is done: the wait for V sees its own phase
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
           if (!ok) continue;
           if (partial) {
             uint32_t bits[4];
-            const uint8_t* mask = a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * 128 : nullptr;
+            const uint8_t* mask = a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)kt * 128 : nullptr;
             if (!key_bits(mask, left, bits)) zero_rows<4, 1>(sm + SL::v + s * SL::kTileBytes, bits);
             __syncwarp();
           }
@@ -363,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
       const CrossItem it = s_cur[~c & 1];
       if (it.hk < 0) break;
       int t0;
-      const int nt = part(it, &t0);
+      const CrossBand band = band_of(it);
+      const int nt = part(it, band, &t0);
       const bool row_in = row_tok < it.nr;
       // a row block without a valid row needs no weights: its P may hold anything,
       // since a row of P only reaches its own row of O
@@ -378,11 +385,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
         __syncwarp();
         tc_fence_after();
         if (warp_in) {
-          if (t >= whole) {
-            const int left = it.no - (t0 + t) * 128;
+          const int kt = SELF ? band.tile(t0 + t) : t0 + t;
+          const bool cut = SELF && !seen_whole(a, it.p0, it.nr, kt * 128);
+          if (SELF ? a.key_mask || it.no < kt * 128 + 128 || cut : t >= whole) {
+            const int left = it.no - kt * 128;
             uint32_t bits[4];
-            if (!key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)(t0 + t) * 128 : nullptr, left,
-                          bits)) {
+            const bool all = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)kt * 128 : nullptr, left, bits);
+            if (SELF && cut) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) bits[w] &= seen_bits(a, it.p0 + row_tok, kt * 128 + 32 * w);
+            }
+            if (!all || cut) {
               // the scores of keys that do not count become -inf in place (kept out of
               // the straight code below, which the instruction caches have to hold)
 #pragma unroll 1
@@ -561,9 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
   if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
-template <bool BF16>
+template <bool BF16, bool SELF>
 cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t s) {
-  auto kernel = cross64_kernel<BF16>;
+  auto kernel = cross64_kernel<BF16, SELF>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)FwdSmem::alloc, kRegs, &done);
   return e != cudaSuccess ? e : launch_clusters(kernel, a, maps, grid, kThreads, FwdSmem::alloc, s);
@@ -571,8 +584,9 @@ cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t
 
 }  // namespace
 
-cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s) {
-  return bf16 ? launch<true>(a, maps, grid, s) : launch<false>(a, maps, grid, s);
+cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s) {
+  if (self) return bf16 ? launch<true, true>(a, maps, grid, s) : launch<false, true>(a, maps, grid, s);
+  return bf16 ? launch<true, false>(a, maps, grid, s) : launch<false, false>(a, maps, grid, s);
 }
 
 }  // namespace dfa

@@ -206,11 +206,11 @@ __device__ __forceinline__ float ds_scale(float x, float y, float z) {
 
 // fp16: the scales of a resident tile's rows 32 w + lane (one warp).  Those of keys that do
 // not count may be any power of two.
-template <bool KEYS, typename T>
+template <bool KEYS, bool SELF, typename T>
 __device__ __forceinline__ void resident_scales(const BwdArgs& args, const CrossItem& it, float (&scales)[4]) {
   const CrossArgs& a = args.c;
   const size_t plane = (size_t)a.Tq * a.H;
-  const int first = KEYS ? it.o0 : a.cu_q ? min(max(a.cu_q[it.b], 0), a.Tq - 1) : it.b * a.Lq;
+  const int first = KEYS && !SELF ? it.o0 : a.cu_q ? min(max(a.cu_q[it.b], 0), a.Tq - 1) : it.b * a.Lq;
   const uint32_t* top = args.top + (size_t)first * a.H + it.hk * a.G;
   const float x = __uint_as_float(top[KEYS ? 0 : 2 * plane]), z = KEYS ? __uint_as_float(top[plane]) : 0.f;
 #pragma unroll
@@ -249,13 +249,14 @@ struct BwdSmem {
   static constexpr uint32_t claim = cur + 64;  // 16 bytes
   static constexpr uint32_t misc = claim + 16;
   static constexpr uint32_t scale = misc + 16;  // fp16: float [kStages][128], the resident rows' scales
-  static constexpr uint32_t bytes = scale + (BF16 ? 0 : kStages * 512);
+  static constexpr uint32_t tok = scale + (BF16 ? 0 : kStages * 512);  // int [128]: a streamed query row's token
+  static constexpr uint32_t bytes = tok + 512;
   static constexpr uint32_t alloc = bytes + 1024;
   static_assert(alloc <= 232448, "shared memory of one CTA");
 };
 
 // KEYS: the resident rows are keys (K, V), the streamed ones queries (Q, dout).
-template <int D, bool BF16, bool KEYS>
+template <int D, bool BF16, bool KEYS, bool SELF>
 __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs args, const __grid_constant__ BwdMaps maps) {
   using SL = BwdSmem<D, BF16>;
   constexpr int kChunks = SL::kChunks;
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     tma_prefetch_desc(&maps.y0);
     tma_prefetch_desc(&maps.y1);
   }
+  if (SELF && KEYS && threadIdx.x < 128) reinterpret_cast<int*>(sm + SL::tok)[threadIdx.x] = threadIdx.x / a.G;
   if (warp == 1) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
@@ -346,11 +348,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
 
   const unsigned long long budget = a.budget;
   const int x_step = KEYS ? 128 : a.tpt, y_step = KEYS ? a.tpt : 128;  // tokens per tile
-  auto y_tiles = [&](const CrossItem& it) { return (it.no + y_step - 1) / y_step; };
+  // self attention, a query tile: the key tiles that it meets
+  auto band_of = [&](const CrossItem& it) { return SELF && !KEYS ? key_band(a, it) : CrossBand{0, 0}; };
+  auto y_tiles = [&](const CrossItem& it, const CrossBand& band) {
+    return SELF && !KEYS ? max((it.no + 127) / 128 - band.skip, band.sinks) : (it.no + y_step - 1) / y_step;
+  };
   auto read_item = [&](uint32_t c) {  // one thread: the c-th item handed out, hk = -1 at the end
     const uint32_t slot = c % kItemRing;
     CrossItem it;
-    it.r0 = it.nr = it.o0 = it.no = it.b = 0;
+    it.r0 = it.nr = it.o0 = it.no = it.b = it.p0 = it.q0 = 0;
     it.hk = -1;
     if (cross_wait(item_full + slot, (c / kItemRing) & 1, budget, s_abort)) {
       it = *ring_slot(c);
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     setmaxnreg_dec<kOtherRegs>();
     // (the whole warp runs every step, and one lane of it issues; so do the warps of
     // the products)
-    TileWalk walk;
+    TileWalk<SELF, KEYS> walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, xc = 0, g_issued = 0, x_issued = 0;
     const uint32_t q_box = (uint32_t)(a.G * a.tpt) * 128u;  // bytes of a 64-column box of a query tile
@@ -397,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           it.no = mask_n;
         }
       }
+      if (SELF && !KEYS) clip_causal(it);
       const uint32_t slot = c % kItemRing;
       bool room = true;
       if (c >= kItemRing) room = cross_wait(item_empty + slot, ((c / kItemRing) - 1) & 1, budget, s_abort);
@@ -406,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         mbar_arrive(item_full + slot);
       }
       if (it.hk < 0) break;
-      const int nt = y_tiles(it);
+      const CrossBand band = band_of(it);
+      const int nt = y_tiles(it, band);
       const int x_head = KEYS ? it.hk : it.hk * a.G, y_head = KEYS ? it.hk * a.G : it.hk;
       if (nt > 0) {
         const uint32_t xb = xc % kRes;
@@ -429,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         ok = __all_sync(0xffffffffu, ok);
         ++g;
         if (!ok) continue;
-        load(&maps.y0, &maps.y1, sm + SL::y + s * 2 * SL::kTileBytes, y_box, y_head, it.o0 + t * y_step, full + s);
+        load(&maps.y0, &maps.y1, sm + SL::y + s * 2 * SL::kTileBytes, y_box, y_head,
+             it.o0 + (SELF && !KEYS ? band.tile(t) : t) * y_step, full + s);
         g_issued = g;
       }
       number = claim.answer(budget, s_abort);
@@ -461,7 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
       if (it.hk < 0) break;
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
-      const int nt = y_tiles(it);
+      if (SELF && !KEYS) it.p0 = __shfl_sync(0xffffffffu, it.p0, 0);
+      const CrossBand band = band_of(it);
+      const int nt = y_tiles(it, band);
       if (nt == 0) continue;
       const uint32_t xb = xc % kRes;
       ok = ok && cross_wait(x_full + xb, (xc / kRes) & 1, budget, s_abort);
@@ -512,7 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         it.hk = __shfl_sync(0xffffffffu, it.hk, 0);
         if (it.hk < 0) break;
         it.no = __shfl_sync(0xffffffffu, it.no, 0);
-        const int nt = y_tiles(it);
+        if (SELF && !KEYS) it.p0 = __shfl_sync(0xffffffffu, it.p0, 0);
+        const CrossBand band = band_of(it);
+        const int nt = y_tiles(it, band);
         if (nt == 0) continue;
         // the epilogue has read the previous item's sums
         if (xc > 0) ok = ok && cross_wait(acc_free, (xc - 1) & 1, budget, s_abort);
@@ -563,17 +576,20 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
       it.o0 = __shfl_sync(0xffffffffu, it.o0, 0);
       it.no = __shfl_sync(0xffffffffu, it.no, 0);
       it.b = __shfl_sync(0xffffffffu, it.b, 0);
+      if (SELF && !KEYS) it.p0 = __shfl_sync(0xffffffffu, it.p0, 0);
       if (!BF16) {
         it.r0 = __shfl_sync(0xffffffffu, it.r0, 0);
         it.nr = __shfl_sync(0xffffffffu, it.nr, 0);
       }
-      const int nt = y_tiles(it);
+      const CrossBand band = band_of(it);
+      const int nt = y_tiles(it, band);
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, ++g) {
         const uint32_t s = g % kStages;
         float scales[4];
-        if (!BF16 && t == 0) resident_scales<KEYS, T>(args, it, scales);
-        const int left = it.no - t * y_step;  // tokens of the tile (and behind it)
+        if (!BF16 && t == 0) resident_scales<KEYS, SELF, T>(args, it, scales);
+        const int yt = SELF && !KEYS ? band.tile(t) : t;
+        const int left = it.no - yt * y_step;  // tokens of the tile (and behind it)
         uint32_t bits[4];
         float2 st[4];
         bool whole = true;
@@ -589,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           }
           whole = (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu;
         } else {
-          whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)t * 128 : nullptr, left, bits);
+          whole = key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)yt * 128 : nullptr, left, bits);
         }
         ok = ok && cross_wait(full + s, (g / kStages) & 1, budget, s_abort);
         ok = __all_sync(0xffffffffu, ok);
@@ -639,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     for (;;) {
       const CrossItem it = s_cur[~c & 1];
       if (it.hk < 0) break;
-      const int nt = y_tiles(it);
+      const CrossBand band = band_of(it);
+      const int nt = y_tiles(it, band);
       const bool stored = row_tok < it.nr;   // the resident row belongs to the sequence
       bool row_in = stored;
       float nl = -INFINITY, nd = 0.f;  // -lse, -D
@@ -664,6 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
         if (!BF16 && t == 0) ds_mul = reinterpret_cast<const float*>(sm + SL::scale + s * 512)[row] * kPUnit;
         if constexpr (KEYS) {
+          // self attention: the keys are at or behind every query, and in its reach, or not all
+          const int pq = it.q0 + t * y_step;  // the position of the tile's first query
+          const bool cut = SELF && !(pq >= it.p0 + 127 && (a.window == 0 || pq + y_step - a.window <= it.p0 ||
+                                                          it.p0 + 128 <= a.sinks));
           // A thread takes two columns of every eight in four rows (lane / 4 + 8 r),
           // not 64 columns of one row: it then reads a quarter of the columns' values
           // from shared memory (one row per thread: 898 us against 835 on 8 x 12 heads,
@@ -711,6 +732,23 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
                 for (int e = 0; e < 8; ++e)
                   if (!((rows_in >> (16 * i + 8 * (e & 1) + (lane >> 2))) & 1u)) wp[e] = wd[e] = 0u;
               }
+              if (SELF && cut) {
+                // rows 16 i + lane / 4 and 8 on: a key at j is seen from j on, for `reach` positions
+                const int j0 = it.p0 + quad * 32 + 16 * i + (lane >> 2), all = INT_MAX;
+                const int r0 = a.window == 0 || j0 < a.sinks ? all : a.window;
+                const int r1 = a.window == 0 || j0 + 8 < a.sinks ? all : a.window;
+                const int* tok = reinterpret_cast<const int*>(sm + SL::tok) + c2 + 32 * q;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int2 tt = *reinterpret_cast<const int2*>(tok + 8 * (e >> 1));
+                  const int j = j0 + 8 * (e & 1);
+                  const uint32_t reach = e & 1 ? r1 : r0;
+                  const uint32_t keep = ((uint32_t)(pq + tt.x - j) < reach ? 0xffffu : 0u) |
+                                        ((uint32_t)(pq + tt.y - j) < reach ? 0xffff0000u : 0u);
+                  wp[e] &= keep;
+                  wd[e] &= keep;
+                }
+              }
               const uint32_t to = lane_off + 16 * q + ((uint32_t)(16 * i) << 16);
               tmem_st_rows16(tS(b) + to, wp);
               tmem_st_rows16(tdP(b) + to, wd);
@@ -728,7 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           tmem_ld32(tdP(b) + lane_off + 32, rd1);
           auto columns = [&](const uint32_t (&rs)[32], const uint32_t (&rd)[32], int q) {
             uint32_t wd[16];
-            const uint32_t bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
+            uint32_t bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
+            if (SELF) bits &= seen_bits(a, it.p0 + row_tok, band.tile(t) * 128 + 64 * h + 32 * q);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 z =
@@ -802,10 +841,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
   if (!KEYS && args.after_keys) grid_dependency_wait();
 }
 
-template <int D, bool BF16, bool KEYS>
+template <int D, bool BF16, bool KEYS, bool SELF>
 cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items, cudaStream_t s) {
   if (items == 0) return cudaSuccess;
-  auto kernel = cross_bwd_kernel<D, BF16, KEYS>;
+  auto kernel = cross_bwd_kernel<D, BF16, KEYS, SELF>;
   const uint32_t bytes = BwdSmem<D, BF16>::alloc;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)bytes, kRegs, &done);
@@ -813,7 +852,7 @@ cudaError_t launch_tiles(const BwdArgs& a, const BwdMaps& maps, long long items,
   return launch_after_plan(kernel, (int)items, kThreads, bytes, s, a, maps);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SELF>
 cudaError_t launch_both(BwdArgs a, const BwdMaps& km, const BwdMaps& qm, void* dq, void* dk, void* dv,
                         cudaStream_t s) {
   const long long key_items = a.c.cu_k ? ((long long)a.c.Tk / 128 + a.c.B + 1) * a.c.Hk
@@ -823,13 +862,13 @@ cudaError_t launch_both(BwdArgs a, const BwdMaps& km, const BwdMaps& qm, void* d
     a.after_keys = 1;
     a.out0 = dk;
     a.out1 = dv;
-    const cudaError_t e = launch_tiles<D, BF16, true>(a, km, key_items, s);
+    const cudaError_t e = launch_tiles<D, BF16, true, SELF>(a, km, key_items, s);
     if (e != cudaSuccess) return e;
   }
   if (a.c.Tq > 0) {
     a.out0 = dq;
     a.out1 = nullptr;
-    return launch_tiles<D, BF16, false>(a, qm, cross_query_tiles(a.c), s);
+    return launch_tiles<D, BF16, false, SELF>(a, qm, cross_query_tiles(a.c), s);
   }
   return cudaSuccess;
 }
@@ -874,12 +913,13 @@ extern "C" size_t df_cross_attn_bwd_workspace_size(int total_q, int H) {
   return up256(rows * sizeof(float2)) + up256(rows * sizeof(float)) + up256(3 * rows * sizeof(uint32_t)) + 256;
 }
 
-extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* out_lo,
-                                       const float* lse, const void* dout, const uint8_t* key_mask,
-                                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
-                                       int Lq, int Lk, int total_q, int total_k, int d, float scale, df_dtype dtype,
-                                       void* dq, void* dk, void* dv, int32_t* status, void* workspace,
-                                       size_t workspace_bytes, df_stream_t stream) {
+// SELF: causal, with a window and sinks (the caller has checked them).
+template <bool SELF>
+static df_status backward(int window, int sinks, const void* q, const void* k, const void* v, const void* out,
+                          const void* out_lo, const float* lse, const void* dout, const uint8_t* key_mask,
+                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
+                          int total_q, int total_k, int d, float scale, df_dtype dtype, void* dq, void* dk, void* dv,
+                          int32_t* status, void* workspace, size_t workspace_bytes, df_stream_t stream) {
   BwdArgs a;
   const df_status st = cross_check(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk, Lq, Lk, total_q, total_k,
                                    d, scale, dtype, status, &a.c);
@@ -888,6 +928,8 @@ extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void*
   if (!al16(out) || !al16(out_lo) || !al16(dout) || !al16(dq) || !al16(dk) || !al16(dv) || ((uintptr_t)lse & 3u) != 0 ||
       ((uintptr_t)workspace & 255u) != 0)
     return DF_ERR_ALIGNMENT;
+  a.c.window = window;
+  a.c.sinks = sinks;
   const size_t need = df_cross_attn_bwd_workspace_size(total_q, H);
   if (need == 0) return DF_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need) return DF_ERR_WORKSPACE;
@@ -933,9 +975,30 @@ extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void*
     return DF_ERR_CUDA;
   const BwdMaps key_maps = {mk, mv, mq, mg}, query_maps = {mq, mg, mk, mv};
   const cudaError_t e =
-      d <= 64 ? (bf16 ? launch_both<64, true>(a, key_maps, query_maps, dq, dk, dv, s)
-                      : launch_both<64, false>(a, key_maps, query_maps, dq, dk, dv, s))
-              : (bf16 ? launch_both<128, true>(a, key_maps, query_maps, dq, dk, dv, s)
-                      : launch_both<128, false>(a, key_maps, query_maps, dq, dk, dv, s));
+      d <= 64 ? (bf16 ? launch_both<64, true, SELF>(a, key_maps, query_maps, dq, dk, dv, s)
+                      : launch_both<64, false, SELF>(a, key_maps, query_maps, dq, dk, dv, s))
+              : (bf16 ? launch_both<128, true, SELF>(a, key_maps, query_maps, dq, dk, dv, s)
+                      : launch_both<128, false, SELF>(a, key_maps, query_maps, dq, dk, dv, s));
   return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+extern "C" df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* out_lo,
+                                       const float* lse, const void* dout, const uint8_t* key_mask,
+                                       const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
+                                       int Lq, int Lk, int total_q, int total_k, int d, float scale, df_dtype dtype,
+                                       void* dq, void* dk, void* dv, int32_t* status, void* workspace,
+                                       size_t workspace_bytes, df_stream_t stream) {
+  return backward<false>(0, 0, q, k, v, out, out_lo, lse, dout, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk,
+                         Lq, Lk, total_q, total_k, d, scale, dtype, dq, dk, dv, status, workspace, workspace_bytes, stream);
+}
+
+extern "C" df_status df_self_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* out_lo,
+                                      const float* lse, const void* dout, const uint8_t* key_mask,
+                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int H, int Hk,
+                                      int Lq, int Lk, int total_q, int total_k, int d, float scale, int window, int sinks,
+                                      df_dtype dtype, void* dq, void* dk, void* dv, int32_t* status, void* workspace,
+                                      size_t workspace_bytes, df_stream_t stream) {
+  if (!self_reach(&window, &sinks)) return DF_ERR_INVALID_ARG;
+  return backward<true>(window, sinks, q, k, v, out, out_lo, lse, dout, key_mask, cu_seqlens_q, cu_seqlens_k, B, H, Hk,
+                         Lq, Lk, total_q, total_k, d, scale, dtype, dq, dk, dv, status, workspace, workspace_bytes, stream);
 }

@@ -21,8 +21,8 @@ struct FwdMaps {
   CUtensorMap q, k, v;
 };
 
-cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s);
-cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s);
+cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s);
+cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s);
 constexpr int kFwdKeys = 128;  // keys per tile
 
 // The base of a row's exponentials stands this many binary orders below its maximum.  A
@@ -34,9 +34,10 @@ constexpr int kFwdKeys = 128;  // keys per tile
 template <bool BF16>
 constexpr float kBelow = BF16 ? 0.f : 7.f;
 
-// This CTA's key tiles [*t0, *t0 + n) of an item; returns n.
-__device__ __forceinline__ int key_part(const FwdArgs& args, const CrossItem& it, uint32_t rank, int* t0) {
-  const unsigned all = (it.no + kFwdKeys - 1) / kFwdKeys;
+// This CTA's key tiles [*t0, *t0 + n) of an item (of those that it meets); returns n.
+__device__ __forceinline__ int key_part(const FwdArgs& args, const CrossItem& it, const CrossBand& band, uint32_t rank,
+                                        int* t0) {
+  const unsigned all = max((it.no + kFwdKeys - 1) / kFwdKeys - band.skip, band.sinks);
   *t0 = (int)((all * rank) >> args.split_bits);
   return (int)((all * (rank + 1)) >> args.split_bits) - *t0;
 }

@@ -550,6 +550,40 @@ df_status df_cross_attn_bwd(const void* q, const void* k, const void* v, const v
 size_t df_cross_attn_bwd_workspace_size(int total_q, int H);
 
 /* ---------------------------------------------------------------------------
+ * Self attention of a decoder: causal, with an optional sliding window and a few first
+ * tokens that stay visible (sinks).  The arguments, layouts, results, rounding, status and
+ * errors are those of df_cross_attn_fwd / df_cross_attn_bwd (queries and keys may be of
+ * different lengths: the queries are then the last tokens of their sequence, the next part
+ * of a prompt for instance), and of the keys that count for a sequence, query row i of n,
+ * at position p = i + m - n among the m keys, sees
+ *     the keys j <= p with  window = 0  or  j > p - window  or  j < sinks.
+ * A row that sees none (p < 0, or all of its keys masked) gets zeros and lse = -infinity,
+ * and passes no gradient.  In the padded layout m and n are the padded lengths Lk and Lq
+ * and positions count from the first key, masked or not: sequences padded on the right.
+ *   window     0 (every earlier key), or the keys that a query sees at most, itself one of
+ *              them, beside the sinks
+ *   sinks      first keys of a sequence that its queries see at any distance
+ * Key tiles (128 keys) that no row of a query tile sees are neither read nor computed.
+ * Values must be finite in every row of q, k, v and dout that counts for its sequence: a
+ * weight of 0 on a later key's NaN is NaN within a tile.
+ * Errors: as df_cross_attn_fwd / _bwd, and DF_ERR_INVALID_ARG for window < 0 or sinks < 0.
+ * The backward's workspace is df_cross_attn_bwd_workspace_size(total_q, H). */
+df_status df_self_attn_fwd(const void* q, const void* k, const void* v,
+                           const uint8_t* key_mask, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
+                           int total_q, int total_k, int d, float scale, int window, int sinks,
+                           df_dtype dtype, void* out, void* out_lo, float* lse, int32_t* status,
+                           df_stream_t stream);
+
+df_status df_self_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                           const void* out_lo, const float* lse, const void* dout,
+                           const uint8_t* key_mask, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int B, int H, int Hk, int Lq, int Lk,
+                           int total_q, int total_k, int d, float scale, int window, int sinks,
+                           df_dtype dtype, void* dq, void* dk, void* dv, int32_t* status,
+                           void* workspace, size_t workspace_bytes, df_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Token embeddings: the rows that enter the encoder (or a decoder that reads
  * its states), and the gradient of the table.
  *
