@@ -787,47 +787,12 @@ def _attn_bwd(fn, what, reach, q, k, v, out, stats, dout, key_mask, cu_seqlens_q
     return dq, dk, dv
 
 
-_lib.df_self_attn_fwd.argtypes = [_vp] * 6 + [_i] * 8 + [ctypes.c_float] + [_i] * 3 + [_vp] * 5
-_lib.df_self_attn_fwd.restype = _i
-_lib.df_self_attn_bwd.argtypes = [_vp] * 10 + [_i] * 8 + [ctypes.c_float] + [_i] * 3 + [_vp] * 5 + [_sz, _vp]
-_lib.df_self_attn_bwd.restype = _i
-
-
-def _reach(window, sinks):
-    window, sinks = int(window or 0), int(sinks)
-    _int_sizes(window=window, sinks=sinks)
-    return window, sinks
-
-
-def df_self_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *, max_seqlen_q=None,
-                     max_seqlen_k=None, window=0, sinks=0, scale=None, out=None, with_stats=False, status=None,
-                     stream=None):
-    """Causal attention: the queries are the last tokens of their sequence (all of them, or
-    the next part of a prompt) and see the keys up to their own position; with ``window``
-    the last ``window`` of those and the sequence's first ``sinks``.  Layouts, arguments and
-    results as ``df_cross_attn_fwd``."""
-    if stream is not None:
-        with _current(stream, q):
-            return df_self_attn_fwd(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
-                                    max_seqlen_k=max_seqlen_k, window=window, sinks=sinks, scale=scale, out=out,
-                                    with_stats=with_stats, status=status)
-    return _attn_fwd(_lib.df_self_attn_fwd, "df_self_attn_fwd", _reach(window, sinks), q, k, v, key_mask, cu_seqlens_q,
-                     cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, out, with_stats, status)
-
-
-def df_self_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *,
-                     max_seqlen_q=None, max_seqlen_k=None, window=0, sinks=0, scale=None, grads=None, workspace=None,
-                     status=None, stream=None):
-    """Gradients (dq, dk, dv), in the inputs' dtype, of ``df_self_attn_fwd`` with the same
-    arguments; ``out`` and ``stats`` as its call with ``with_stats`` gave them.  The
-    workspace is ``df_cross_attn_bwd_workspace_size``."""
-    if stream is not None:
-        with _current(stream, q):
-            return df_self_attn_bwd(q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k,
-                                    max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, window=window, sinks=sinks,
-                                    scale=scale, grads=grads, workspace=workspace, status=status)
-    return _attn_bwd(_lib.df_self_attn_bwd, "df_self_attn_bwd", _reach(window, sinks), q, k, v, out, stats, dout,
-                     key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, grads, workspace, status)
-
-
 raw_library = _lib
+
+
+def __getattr__(name):
+    # the calls of a decoder's own attention (decoder_binding.py) are reached from here too
+    from . import decoder_binding
+    if name in decoder_binding.__all__:
+        return getattr(decoder_binding, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,55 @@
+"""The decoder's calls and layers with a stream as argument: everything that they allocate
+belongs to that stream (see test_streams_cpu.py, whose stand-ins these tests use)."""
+
+import inspect
+
+import pytest
+import torch
+
+from test_streams_cpu import dev, record  # noqa: F401 (the fixture)
+
+
+def calls(b, e):
+    q, cu = dev(6, 8, 64), dev(3, dtype=torch.int32)
+    at = dict(cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=4, max_seqlen_k=4, window=3, sinks=1)
+    return {
+        "df_self_attn_fwd": lambda **s: b.df_self_attn_fwd(q, q, q, with_stats=True, **at, **s),
+        "df_self_attn_bwd": lambda **s: b.df_self_attn_bwd(q, q, q, q, b.CrossStats(dev(6, 8, dtype=torch.float32), q), q,
+                                                           **at, **s),
+    }
+
+
+NAMES = ["df_self_attn_fwd", "df_self_attn_bwd"]
+
+
+@pytest.fixture
+def recorded(record, monkeypatch):  # noqa: F811
+    b, e, seen = record
+    from exact_attention_deberta_gb300 import decoder_binding
+    if hasattr(decoder_binding, "torch"):
+        monkeypatch.setattr(decoder_binding, "torch", b.torch)
+    return b, e, seen
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_allocations_belong_to_the_stream_given(recorded, name):
+    b, e, seen = recorded
+    call = calls(b, e)[name]
+    seen.clear()
+    call(stream=1234)
+    assert seen and set(seen) == {1234}, seen
+
+
+def test_every_call_with_a_stream_is_listed(recorded):
+    from exact_attention_deberta_gb300 import decoder_binding as d
+    takes = {n for n, f in vars(d).items() if inspect.isfunction(f) and not n.startswith("_") and
+             "stream" in inspect.signature(f).parameters}
+    assert takes <= set(NAMES)
+
+
+def test_calls_are_reached_through_the_binding():
+    from exact_attention_deberta_gb300 import binding, decoder_binding
+    for name in decoder_binding.__all__:
+        assert getattr(binding, name) is getattr(decoder_binding, name)
+    with pytest.raises(AttributeError):
+        binding.df_no_such_call
