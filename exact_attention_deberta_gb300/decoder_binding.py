@@ -22,7 +22,7 @@ def _reach(window, sinks):
     return window, sinks
 
 
-def df_selfb._attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *, max_seqlen_q=None,
+def df_self_attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *, max_seqlen_q=None,
                      max_seqlen_k=None, window=0, sinks=0, scale=None, out=None, with_stats=False, status=None,
                      stream=None):
     """Causal attention: the queries are the last tokens of their sequence (all of them, or
@@ -31,14 +31,14 @@ def df_selfb._attn_fwd(q, k, v, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=N
     results as ``df_cross_attn_fwd``."""
     if stream is not None:
         with b._current(stream, q):
-            return df_selfb._attn_fwd(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
+            return df_self_attn_fwd(q, k, v, key_mask, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=max_seqlen_q,
                                     max_seqlen_k=max_seqlen_k, window=window, sinks=sinks, scale=scale, out=out,
                                     with_stats=with_stats, status=status)
     return b._attn_fwd(b._lib.df_self_attn_fwd, "df_self_attn_fwd", _reach(window, sinks), q, k, v, key_mask, cu_seqlens_q,
                      cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale, out, with_stats, status)
 
 
-def df_selfb._attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *,
+def df_self_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=None, cu_seqlens_k=None, *,
                      max_seqlen_q=None, max_seqlen_k=None, window=0, sinks=0, scale=None, grads=None, workspace=None,
                      status=None, stream=None):
     """Gradients (dq, dk, dv), in the inputs' dtype, of ``df_self_attn_fwd`` with the same
@@ -46,7 +46,7 @@ def df_selfb._attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=No
     workspace is ``df_cross_attn_bwd_workspace_size``."""
     if stream is not None:
         with b._current(stream, q):
-            return df_selfb._attn_bwd(q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k,
+            return df_self_attn_bwd(q, k, v, out, stats, dout, key_mask, cu_seqlens_q, cu_seqlens_k,
                                     max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, window=window, sinks=sinks,
                                     scale=scale, grads=grads, workspace=workspace, status=status)
     return b._attn_bwd(b._lib.df_self_attn_bwd, "df_self_attn_bwd", _reach(window, sinks), q, k, v, out, stats, dout,
