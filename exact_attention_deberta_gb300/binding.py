@@ -790,9 +790,11 @@ def _attn_bwd(fn, what, reach, q, k, v, out, stats, dout, key_mask, cu_seqlens_q
 raw_library = _lib
 
 
+# the calls of a decoder's own attention are reached from here too
+from . import decoder_binding as _decoder  # noqa: E402
+
+
 def __getattr__(name):
-    # the calls of a decoder's own attention (decoder_binding.py) are reached from here too
-    from . import decoder_binding
-    if name in decoder_binding.__all__:
-        return getattr(decoder_binding, name)
+    if name in _decoder.__all__:
+        return getattr(_decoder, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
