@@ -1,0 +1,261 @@
+// Rotary positions: the columns of a head are rotated in pairs by an angle that grows with
+// the token's position, y_a = A (x_a cos t - x_b sin t), y_b = A (x_b cos t + x_a sin t),
+// t = position * f of the pair.  Pairs are (i, i + rot / 2) or (2i, 2i + 1), i < rot / 2;
+// the columns from rot on are copied.  The inverse rotation is the gradient.
+//
+// Frequencies are held as turns a position in units of 2^-64 of a turn, so that an
+// integer product modulo 2^64 is the angle without its whole turns, exactly: far positions
+// cost no digits (position * f in fp32 is off by 0.06 rad at a million) and no fp64.  Of
+// that angle the quarter turns are taken off as integers; what is left, at most an eighth
+// of a turn, is rounded to fp32 for the sine and cosine.
+//
+// A thread keeps the sines and cosines of one vector of columns in registers and rotates
+// that vector in several heads, four at a time in flight; neighbouring lanes take
+// neighbouring columns, then heads, so that a warp's loads are whole lines.  HBM bound.
+#include <math.h>
+
+#include <algorithm>
+
+#include "df_common.cuh"
+
+namespace dfa {
+namespace {
+
+struct RotaryArgs {
+  const void* x[2];
+  void* y[2];
+  long long xs[2], ys[2];  // elements between tokens
+  int heads0, heads;       // of the first tensor, of both
+  const void* pos;
+  const uint64_t* turns;
+  int T, d, rot;
+  int chunks, groups;      // vectors of a head that threads take, threads that share its heads
+  float amplitude;
+  int pos_64, inter, inverse;
+};
+
+// sin and cos of `phase` turns / 2^64.
+__device__ __forceinline__ float2 sincos_turns(uint64_t phase) {
+  const uint32_t u = (uint32_t)(phase >> 32);
+  const uint32_t q = (u + 0x20000000u) >> 30;       // the nearest quarter turn
+  const int r = (int)(u - (q << 30));               // 2^-32 turns from there, below 2^29
+  float s, c;
+  sincospif((float)r * 4.656612873077393e-10f, &s, &c);  // in half turns, at most 1 / 4
+  if (q & 1) {
+    const float t = s;
+    s = c;
+    c = -t;
+  }
+  return q & 2 ? make_float2(-s, -c) : make_float2(s, c);
+}
+
+template <typename T, int N>
+struct Vec {
+  using Word = typename std::conditional<
+      N * sizeof(T) == 16, uint4,
+      typename std::conditional<N * sizeof(T) == 8, uint2,
+                                typename std::conditional<N * sizeof(T) == 4, uint32_t, uint16_t>::type>::type>::type;
+  union {
+    Word w;
+    T e[N];
+  };
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Word*>(p) = w; }
+};
+
+// N columns a vector.  Half layout: a thread takes vector c of the first half and its
+// partner; interleaved: a vector holds N / 2 pairs (N = 1: the pair's columns one by one).
+template <typename T, int N, bool INTER>
+__global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
+  constexpr int kPairs = INTER && N > 1 ? N / 2 : N;
+  constexpr bool kTwo = !INTER || N == 1;  // two vectors
+  constexpr int kFlight = 4;
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int c = (int)(id % a.chunks);
+  const long long rest = id / a.chunks;
+  const int g = (int)(rest % a.groups);
+  const long long t = rest / a.groups;
+  if (t >= a.T) return;
+  const int turned = a.rot / 2 / kPairs;  // chunks that are rotated
+  const bool rotate = c < turned;
+  // the vector's first column, and its partner's
+  const int c0 = rotate ? (INTER ? 2 * kPairs * c : N * c) : a.rot + N * (c - turned);
+  const int c1 = INTER ? c0 + 1 : c0 + a.rot / 2;
+  float cs[kPairs], sn[kPairs];
+  if (rotate) {
+    const uint64_t p = a.pos_64 ? (uint64_t) static_cast<const int64_t*>(a.pos)[t]
+                                : (uint64_t)(int64_t) static_cast<const int32_t*>(a.pos)[t];
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      const float2 sc = sincos_turns(p * a.turns[kPairs * c + e]);
+      sn[e] = (a.inverse ? -sc.x : sc.x) * a.amplitude;
+      cs[e] = sc.y * a.amplitude;
+    }
+  }
+  auto from = [&](int h) {
+    const int i = h >= a.heads0;
+    return static_cast<const T*>(a.x[i]) + t * a.xs[i] + (long long)(i ? h - a.heads0 : h) * a.d;
+  };
+  auto to = [&](int h) {
+    const int i = h >= a.heads0;
+    return static_cast<T*>(a.y[i]) + t * a.ys[i] + (long long)(i ? h - a.heads0 : h) * a.d;
+  };
+  for (int h0 = g; h0 < a.heads; h0 += kFlight * a.groups) {
+    Vec<T, N> v[kFlight], w[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int h = h0 + k * a.groups;
+      if (h >= a.heads) break;
+      const T* x = from(h);
+      v[k].load(x + c0);
+      if (kTwo && rotate) w[k].load(x + c1);
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int h = h0 + k * a.groups;
+      if (h >= a.heads) break;
+      T* y = to(h);
+      if (rotate) {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+          T& p = kTwo ? v[k].e[e] : v[k].e[2 * e];
+          T& q = kTwo ? w[k].e[e] : v[k].e[2 * e + 1];
+          const float x0 = IO<T>::to_f(p), x1 = IO<T>::to_f(q);
+          p = IO<T>::from_f(x0 * cs[e] - x1 * sn[e]);
+          q = IO<T>::from_f(x1 * cs[e] + x0 * sn[e]);
+        }
+        if (kTwo) w[k].store(y + c1);
+      }
+      v[k].store(y + c0);
+    }
+  }
+}
+
+template <typename T, int N>
+cudaError_t launch(RotaryArgs a, cudaStream_t s) {
+  const int pairs = a.inter && N > 1 ? N / 2 : N;
+  a.chunks = a.rot / 2 / pairs + (a.d - a.rot) / N;
+  // heads a thread: as many as leave some 2^20 threads, to eight (the sines are formed once
+  // for all of them); one where there is little to do
+  const long long all = (long long)a.T * a.chunks;
+  const long long share = std::min<long long>(8, std::max<long long>(1, all * a.heads >> 20));
+  a.groups = (int)((a.heads + share - 1) / share);
+  const long long blocks = (all * a.groups + 255) / 256;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  if (a.inter)
+    rotary_kernel<T, N, true><<<(unsigned)blocks, 256, 0, s>>>(a);
+  else
+    rotary_kernel<T, N, false><<<(unsigned)blocks, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_widest(const RotaryArgs& a, int n, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (n >= 8) return launch<T, 8>(a, s);
+  if (n >= 4) return launch<T, 4>(a, s);
+  return n >= 2 ? launch<T, 2>(a, s) : launch<T, 1>(a, s);
+}
+
+// Whether rows of `w` bytes every `s` bytes from p on and others from q on share no byte.
+bool rows_apart(const void* p, long long sp, long long wp, const void* q, long long sq, long long wq, long long rows) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  const uintptr_t a1 = a + (rows - 1) * sp + wp, b1 = b + (rows - 1) * sq + wq;
+  if (a1 <= b || b1 <= a) return true;
+  if (sp != sq) return false;
+  const long long off = (long long)((b > a ? b - a : a - b) % (uintptr_t)sp);  // from the lower one's row
+  const long long low = b > a ? wp : wq, high = b > a ? wq : wp;
+  return off >= low && sp - off >= high;
+}
+
+}  // namespace
+}  // namespace dfa
+
+using namespace dfa;
+
+extern "C" df_status df_rotary_table(int rot, double base, double factor, double original_len, double low, double high,
+                                     uint64_t* turns) {
+  if (!turns || rot < 2 || rot % 2 != 0 || rot > 65536) return DF_ERR_INVALID_ARG;
+  if (!(base > 0.) || !isfinite(base) || !(factor > 0.) || !isfinite(factor)) return DF_ERR_INVALID_ARG;
+  if (!(original_len >= 0.) || !isfinite(original_len)) return DF_ERR_INVALID_ARG;
+  if (original_len > 0. && (!(low < high) || !isfinite(low) || !isfinite(high))) return DF_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = pow(base, -2.0 * i / rot);
+    double keep = 0.;
+    if (original_len > 0.) keep = fmin(1., fmax(0., (original_len * f / two_pi - low) / (high - low)));
+    const double turn = f * (keep + (1. - keep) / factor) / two_pi;
+    if (!isfinite(turn)) return DF_ERR_INVALID_ARG;
+    // 2^-64 turns: the whole turns fall out; 53 digits in two steps of 32 bits
+    const double part = turn - floor(turn);
+    const double hi = floor(ldexp(part, 32));
+    turns[i] = ((uint64_t)hi << 32) + (uint64_t)ldexp(ldexp(part, 32) - hi, 32);
+  }
+  return DF_OK;
+}
+
+extern "C" df_status df_rotary(int n, const void* const* x, const int* heads, const int64_t* x_stride, void* const* out,
+                               const int64_t* out_stride, const void* positions, int pos_64, int T, int d, int rot,
+                               int interleaved, int inverse, const uint64_t* turns, float amplitude, df_dtype dtype,
+                               df_stream_t stream) {
+  if (n < 1 || n > 2 || !x || !heads || !x_stride || !out || !out_stride || T < 0 || T > (1 << 30) || d < 1 || rot < 2 ||
+      rot % 2 != 0 || rot > d || !(fabsf(amplitude) <= 3.0e38f))
+    return DF_ERR_INVALID_ARG;
+  if (dtype != DF_BF16 && dtype != DF_FP16 && dtype != DF_FP32) return DF_ERR_INVALID_ARG;
+  if (d > 65536) return DF_ERR_UNSUPPORTED;
+  const int size = dtype == DF_FP32 ? 4 : 2;
+  RotaryArgs a = {};
+  for (int i = 0; i < n; ++i) {
+    if (heads[i] < 1 || heads[i] > 65536) return DF_ERR_INVALID_ARG;
+    const long long width = (long long)heads[i] * d;
+    if (T > 1 && (x_stride[i] < width || out_stride[i] < width)) return DF_ERR_INVALID_ARG;
+    if (x_stride[i] < 0 || out_stride[i] < 0 || x_stride[i] > (1ll << 31) || out_stride[i] > (1ll << 31))
+      return DF_ERR_INVALID_ARG;
+  }
+  if (T == 0) return DF_OK;
+  if (!positions || !turns) return DF_ERR_INVALID_ARG;
+  if (((uintptr_t)positions & (pos_64 ? 7u : 3u)) != 0 || ((uintptr_t)turns & 7u) != 0) return DF_ERR_ALIGNMENT;
+  // the widest vector that the pairs, the columns behind them and every row start on
+  int width = 16 / size;
+  while (width > 1 && ((interleaved ? rot : rot / 2) % width != 0 || (d - rot) % width != 0)) width /= 2;
+  for (int i = 0; i < n; ++i) {
+    if (!x[i] || !out[i]) return DF_ERR_INVALID_ARG;
+    if (((uintptr_t)x[i] | (uintptr_t)out[i]) % size != 0) return DF_ERR_ALIGNMENT;
+    while (width > 1 && (((uintptr_t)x[i] | (uintptr_t)out[i]) % (width * size) != 0 || d % width != 0 ||
+                         (T > 1 && (x_stride[i] % width != 0 || out_stride[i] % width != 0))))
+      width /= 2;
+    a.x[i] = x[i];
+    a.y[i] = out[i];
+    a.xs[i] = x_stride[i];
+    a.ys[i] = out_stride[i];
+    a.heads += heads[i];
+  }
+  a.heads0 = heads[0];
+  for (int i = 0; i < n; ++i) {
+    const long long wi = (long long)heads[i] * d * size, si = T > 1 ? out_stride[i] * size : wi;
+    for (int j = 0; j < n; ++j) {
+      const long long wj = (long long)heads[j] * d * size, sj = T > 1 ? x_stride[j] * size : wj;
+      const bool in_place = i == j && out[i] == x[j] && (T == 1 || out_stride[i] == x_stride[j]);
+      if (!in_place && !rows_apart(out[i], si, wi, x[j], sj, wj, T)) return DF_ERR_INVALID_ARG;
+      if (j > i && !rows_apart(out[i], si, wi, out[j], T > 1 ? out_stride[j] * size : wj, wj, T)) return DF_ERR_INVALID_ARG;
+    }
+    const size_t bytes = (size_t)((T - 1) * si + wi);
+    if (overlapping({{out[i], bytes}}, {{positions, (size_t)T * (pos_64 ? 8 : 4)}, {turns, (size_t)rot * 4}}))
+      return DF_ERR_INVALID_ARG;
+  }
+  a.pos = positions;
+  a.pos_64 = pos_64;
+  a.turns = turns;
+  a.T = T;
+  a.d = d;
+  a.rot = rot;
+  a.amplitude = amplitude;
+  a.inter = interleaved != 0;
+  a.inverse = inverse != 0;
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = dtype == DF_BF16   ? launch_widest<__nv_bfloat16>(a, width, s)
+                        : dtype == DF_FP16 ? launch_widest<__half>(a, width, s)
+                                           : launch_widest<float>(a, width, s);
+  return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}

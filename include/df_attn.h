@@ -583,6 +583,44 @@ df_status df_self_attn_bwd(const void* q, const void* k, const void* v, const vo
                            df_dtype dtype, void* dq, void* dk, void* dv, int32_t* status,
                            void* workspace, size_t workspace_bytes, df_stream_t stream);
 
+/* Rotary positions of queries and keys.  For every token t and head, the columns below rot
+ * are rotated in pairs (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`,
+ * i < rot / 2, by the angle of positions[t] times the pair's frequency; the others are copied:
+ *     out[a] = A (x[a] cos - x[b] sin),   out[b] = A (x[b] cos + x[a] sin)
+ * `inverse` negates the sines: the gradient of the call without it.
+ *   n          1 or 2 tensors (queries and keys) that share positions; x, heads, x_stride,
+ *              out, out_stride are HOST arrays of n
+ *   x[i]       [T, heads[i], d] of `dtype` (bf16, fp16 or fp32), x_stride[i] elements from
+ *              token to token (at least heads[i] d: a part of wider rows, as a fused
+ *              projection gives them), heads next to one another; out[i] likewise
+ *   positions  int32 (pos_64 = 0) or int64 (pos_64 = 1), [T]; any values
+ *   rot        even, 2 .. d
+ *   turns      device uint64 [rot / 2]: each pair's turns a position times 2^64, modulo 2^64
+ *              (df_rotary_table).  Angles are exact products of integers, so that far
+ *              positions lose nothing.
+ *   amplitude  A, 1 or what the scaling for long contexts asks for
+ * The rotation is formed in fp32 and rounded once.  out[i] may be x[i] (with its stride); any
+ * other overlap is refused.  T = 0 is a call that does nothing.  One launch; fastest where
+ * rot / 2 (interleaved: rot) and d are multiples of 16 bytes and rows start on 16 bytes.
+ * Errors: DF_ERR_INVALID_ARG (NULL pointer, n, sizes, rot, strides, amplitude not finite,
+ * overlap), DF_ERR_UNSUPPORTED (d > 65536), DF_ERR_ALIGNMENT (a pointer not aligned to its
+ * elements), DF_ERR_CUDA. */
+df_status df_rotary(int n, const void* const* x, const int* heads, const int64_t* x_stride,
+                    void* const* out, const int64_t* out_stride, const void* positions,
+                    int pos_64, int T, int d, int rot, int interleaved, int inverse,
+                    const uint64_t* turns, float amplitude, df_dtype dtype, df_stream_t stream);
+
+/* The frequencies of df_rotary for `rot` columns, into a HOST array turns [rot / 2]:
+ *     f_i = base^(-2 i / rot)   radians a position,
+ * for long contexts f_i (w + (1 - w) / factor): w = 0 with original_len = 0 (positions
+ * compressed by factor), else w = clamp((original_len f_i / 2 pi - low) / (high - low), 0, 1):
+ * pairs that turn `high` times or more within the original length keep their frequency, those
+ * that turn `low` times or less are divided by factor.  Host only, no CUDA call.  Errors:
+ * DF_ERR_INVALID_ARG (NULL pointer, rot odd, < 2 or > 65536, base, factor or original_len
+ * out of range, low >= high). */
+df_status df_rotary_table(int rot, double base, double factor, double original_len, double low,
+                          double high, uint64_t* turns);
+
 /* ---------------------------------------------------------------------------
  * Token embeddings: the rows that enter the encoder (or a decoder that reads
  * its states), and the gradient of the table.

@@ -16,10 +16,11 @@ def calls(b, e):
         "df_self_attn_fwd": lambda **s: b.df_self_attn_fwd(q, q, q, with_stats=True, **at, **s),
         "df_self_attn_bwd": lambda **s: b.df_self_attn_bwd(q, q, q, q, b.CrossStats(dev(6, 8, dtype=torch.float32), q), q,
                                                            **at, **s),
+        "df_rotary": lambda **s: b.df_rotary((q, q), dev(6, dtype=torch.int32), dev(32, dtype=torch.int64), **s),
     }
 
 
-NAMES = ["df_self_attn_fwd", "df_self_attn_bwd"]
+NAMES = ["df_self_attn_fwd", "df_self_attn_bwd", "df_rotary"]
 
 
 @pytest.fixture
