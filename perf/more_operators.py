@@ -486,7 +486,7 @@ def run(s):
             dq, dk, dv = binding.df_self_attn_bwd(s["q"], s["k"], s["v"], out, stats, s["dout"], **kw)
             return {"out": out, "dq": dq, "dk": dk, "dv": dv}
         if s["op"] == "cache_store":
-            binding.df_cache_append(s["k"], s["v"], s["cache"], s["table"], s["held"], s["cu"], max_new=s["new"])
+            binding.df_cache_append(s["k"], s["v"], s["cache"], s["table"], s["held"], s["cu"])
             return binding.df_cache_read(s["cache"], s["table"], s["ends"], s["cu_all"], rows=s["total"],
                                          dtype=s["dtype"])
         return binding.df_cache_attn(s["q"], s["cache"], s["table"], s["held"], max_length=s["L"], causal=s["causal"],
