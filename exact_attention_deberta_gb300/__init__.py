@@ -14,7 +14,7 @@ def __getattr__(name):
     if name in ("df_attn_fwd", "df_attn_plan", "df_rel_index_table", "df_attn_workspace_size",
                 "df_attn_supported", "df_attn_get_device_status", "df_cross_attn_fwd", "df_cross_attn_bwd",
                 "df_embedding", "df_embedding_bwd", "df_self_attn_fwd", "df_self_attn_bwd", "df_rotary",
-                "df_rotary_table"):
+                "df_rotary_table", "df_cache_new", "df_cache_append", "df_cache_read", "df_cache_attn"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

@@ -1,0 +1,340 @@
+// The 8-bit cache: tokens appended to it, and read back in 16 bits.
+//
+// A block of 16 tokens of one head has one scale, the least power of two s with
+// max |x| <= 448 s; its codes are e4m3(x / s).  A power of two makes x / s exact, so that the
+// one rounding is that of the code, and lets a block that is filled token by token grow its
+// scale: the codes that it holds are halved as often as the scale doubles, which changes
+// nothing above e4m3's subnormals.
+//
+// A warp takes the keys or the values of one block and head: 4 lanes a token's 32 columns, 8
+// tokens at a time, so that its loads are 64-byte runs and its stores 256-byte ones.  HBM bound.
+#include <math.h>
+
+#include <algorithm>
+
+#include "df_cache.cuh"
+
+namespace dfa {
+namespace {
+
+struct StoreArgs {
+  CacheView c;
+  void *k, *v;        // [.., Hk, d]: read (append) or written (read)
+  const int32_t* cu;  // [B + 1], or NULL: `len` rows of each sequence
+  int B, len, total;
+  long long slots;    // blocks that warps look for, over all sequences
+  int32_t* status;
+};
+
+// Blocks are numbered so that no prefix sum is needed: a sequence of n rows that begins at
+// row r has at most n / 16 + 2 blocks, and so those numbered from r / 16 + 2 b on to itself.
+__device__ __forceinline__ long long slot_of(const StoreArgs& a, int b) {
+  if (!a.cu) return (long long)b * (a.len / kBlock + 2);
+  const int r = b <= a.B ? a.cu[b] : a.total;
+  return (r > 0 ? r : 0) / kBlock + 2ll * b;
+}
+// The sequence of a slot, of b < seqs: the last whose first slot is not behind it.
+__device__ __forceinline__ int sequence_of(const StoreArgs& a, int seqs, long long slot) {
+  if (!a.cu) return (int)(slot / (a.len / kBlock + 2));
+  int lo = 0, hi = seqs;  // slot_of(lo) <= slot, hi too far
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (slot_of(a, mid) <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The least power of two s, from 2^-100 on, with top <= 448 s; top >= 0, finite.
+__device__ __forceinline__ float block_scale(float top) {
+  const uint32_t u = __float_as_uint(top);
+  int e = (int)(u >> 23) - 127;           // top = m 2^e, m in [1, 2)
+  e += ((u & 0x7fffffu) > 0x600000u) - 8;  // 448 = 1.75 2^8
+  e = max(e, -100);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+// 1 / s of a power of two from 2^-100 to 2^120
+__device__ __forceinline__ float inverse_scale(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
+
+__device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) <= 3.4028235e38f ? x : __uint_as_float(0x7fffffffu); }
+
+template <typename T, int SLABS>
+__global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int which = (int)(item & 1);
+  const long long rest = item >> 1;
+  const int head = (int)(rest % a.c.Hk);
+  const long long slot = rest / a.c.Hk;
+  if (slot >= a.slots) return;
+  if (slot < a.B && head == 0 && which == 0 && lane == 0) {  // each sequence is looked over once
+    const CrossSide rows = {a.cu, a.len, a.total};
+    int at;
+    seq_rows(rows, (int)slot, a.status, &at);
+    if (a.c.lengths[slot] < 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
+  }
+  const int b = sequence_of(a, a.B, slot);
+  if (b >= a.B) return;
+  const CrossSide rows = {a.cu, a.len, a.total};
+  int first;
+  const int n = seq_rows(rows, b, nullptr, &first), held = a.c.lengths[b];
+  if (n == 0 || held < 0) return;
+  const int blk = held / kBlock + (int)(slot - slot_of(a, b));
+  const int from = max(held - blk * kBlock, 0);  // the block's tokens from here on are new,
+  const long long end = (long long)held + n - (long long)blk * kBlock;
+  if (end <= 0 || blk < 0) return;
+  const int to = (int)min((long long)kBlock, end);  // up to here
+  const int id = page_of(a.c, b, blk);
+  if (id < 0) {
+    if (lane == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
+    return;
+  }
+  uint8_t* rec = record_of(a.c, id, head, blk);
+  uint8_t* codes = rec + 16 * a.c.d * which;
+  float* scale_at = reinterpret_cast<float*>(rec + 32 * a.c.d + 4 * which);
+  const T* x = static_cast<const T*>(which ? a.v : a.k) +
+               ((long long)(first + (long long)blk * kBlock - held) * a.c.Hk + head) * a.c.d;  // the block's token 0
+  const int piece = lane & 3;
+  uint4 v[2 * SLABS];
+#pragma unroll
+  for (int j = 0; j < 2 * SLABS; ++j) {
+    const int row = (lane >> 2) + 8 * (j & 1);
+    v[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= from && row < to)
+      v[j] = *reinterpret_cast<const uint4*>(x + (long long)row * a.c.Hk * a.c.d + 32 * (j >> 1) + 8 * piece);
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2 * SLABS; ++j) {
+    const T* e = reinterpret_cast<const T*>(&v[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = fabsf(IO<T>::to_f(e[i]));
+      if (f <= 3.4028235e38f) top = fmaxf(top, f);
+    }
+  }
+  float s = block_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+  float grown = 1.f;  // old scale / new scale
+  if (from > 0) {
+    const float old = *scale_at;
+    s = fmaxf(s, old);
+    grown = old * inverse_scale(s);
+  }
+  const float inv = inverse_scale(s);
+  __syncwarp();  // every lane has read the scale
+#pragma unroll
+  for (int j = 0; j < 2 * SLABS; ++j) {
+    const int row = (lane >> 2) + 8 * (j & 1);
+    uint2* at = reinterpret_cast<uint2*>(codes + 512 * (j >> 1) + 32 * row + 8 * piece);
+    uint16_t w[4];
+    if (row >= from && row < to) {
+      const T* e = reinterpret_cast<const T*>(&v[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = f32_codes(finite_or_nan(IO<T>::to_f(e[2 * i])) * inv, finite_or_nan(IO<T>::to_f(e[2 * i + 1])) * inv);
+    } else if (row < from && grown != 1.f) {
+      const uint2 kept = *at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t h = codes_f16((uint16_t)((i < 2 ? kept.x : kept.y) >> (16 * (i & 1))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        w[i] = f32_codes(f.x * grown, f.y * grown);
+      }
+    } else {
+      continue;
+    }
+    *at = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+  }
+  if (lane == 0) *scale_at = s;
+}
+
+template <typename T>
+__device__ __forceinline__ T rounded(float f) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) f = fminf(fmaxf(f, -65504.f), 65504.f) + (f != f ? f : 0.f);
+  return IO<T>::from_f(f);
+}
+
+template <typename T, int SLABS>
+__global__ void __launch_bounds__(256) read_kernel(const StoreArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int which = (int)(item & 1);
+  const long long rest = item >> 1;
+  const int head = (int)(rest % a.c.Hk);
+  const long long slot = rest / a.c.Hk;
+  if (slot >= a.slots) return;
+  const CrossSide rows = {a.cu, a.len, a.total};
+  int first;
+  if (slot < a.B && head == 0 && which == 0 && lane == 0) {
+    seq_rows(rows, (int)slot, a.status, &first);
+    if (a.c.lengths[slot] < 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
+  }
+  // (packed: the rows behind the last sequence count as one more, which holds nothing)
+  const int seqs = a.cu ? a.B + 1 : a.B;
+  const int b = sequence_of(a, seqs, slot);
+  if (b >= seqs) return;
+  int n, held = 0;
+  if (b < a.B) {
+    n = seq_rows(rows, b, nullptr, &first);
+    held = max(a.c.lengths[b], 0);
+  } else {
+    first = min(max(a.cu[a.B], 0), a.total);
+    n = a.total - first;
+  }
+  const int blk = (int)(slot - slot_of(a, b));
+  if ((long long)blk * kBlock >= n) return;
+  const int here = min(kBlock, n - blk * kBlock);  // rows of the block,
+  int left = min(held - blk * kBlock, here);       // of which the cache holds these
+  const uint8_t* rec = nullptr;
+  if (left > 0) {
+    const int id = page_of(a.c, b, blk);
+    if (id < 0) {
+      if (lane == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
+      left = 0;
+    } else {
+      rec = record_of(a.c, id, head, blk);
+    }
+  }
+  const float s = rec ? *reinterpret_cast<const float*>(rec + 32 * a.c.d + 4 * which) : 0.f;
+  T* y = static_cast<T*>(which ? a.v : a.k) + ((long long)(first + (long long)blk * kBlock) * a.c.Hk + head) * a.c.d;
+  const int piece = lane & 3;
+  uint2 v[2 * SLABS];
+#pragma unroll
+  for (int j = 0; j < 2 * SLABS; ++j) {
+    const int row = (lane >> 2) + 8 * (j & 1);
+    v[j] = make_uint2(0u, 0u);
+    if (row < left) v[j] = *reinterpret_cast<const uint2*>(rec + 16 * a.c.d * which + 512 * (j >> 1) + 32 * row + 8 * piece);
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * SLABS; ++j) {
+    const int row = (lane >> 2) + 8 * (j & 1);
+    if (row >= here) continue;
+    alignas(16) T e[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = codes_f16((uint16_t)((i < 2 ? v[j].x : v[j].y) >> (16 * (i & 1))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      e[2 * i] = rounded<T>(row < left ? f.x * s : 0.f);
+      e[2 * i + 1] = rounded<T>(row < left ? f.y * s : 0.f);
+    }
+    uint4* at = reinterpret_cast<uint4*>(y + (long long)row * a.c.Hk * a.c.d + 32 * (j >> 1) + 8 * piece);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) at[i] = reinterpret_cast<const uint4*>(e)[i];
+  }
+}
+
+bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <bool READ, typename T>
+cudaError_t launch(const StoreArgs& a, cudaStream_t s) {
+  const long long warps = a.slots * a.c.Hk * 2, blocks = (warps + 7) / 8;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  void (*kernel)(StoreArgs) = nullptr;
+  switch (a.c.d / 32) {
+    case 1: kernel = READ ? read_kernel<T, 1> : append_kernel<T, 1>; break;
+    case 2: kernel = READ ? read_kernel<T, 2> : append_kernel<T, 2>; break;
+    case 3: kernel = READ ? read_kernel<T, 3> : append_kernel<T, 3>; break;
+    default: kernel = READ ? read_kernel<T, 4> : append_kernel<T, 4>; break;
+  }
+  kernel<<<(unsigned)blocks, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// What both calls check of their rows; fills the rest of *a.
+df_status rows_check(const int32_t* cu, int B, int len, int total, StoreArgs* a) {
+  if (len < 0 || total < 0 || (!cu && (long long)B * len != total)) return DF_ERR_INVALID_ARG;
+  if (total > (1 << 30)) return DF_ERR_UNSUPPORTED;
+  if (((uintptr_t)cu & 3u) != 0) return DF_ERR_ALIGNMENT;
+  a->cu = cu;
+  a->B = B;
+  a->len = len;
+  a->total = total;
+  a->slots = cu ? (long long)total / kBlock + 2ll * (B + 1) + 1 : (long long)B * (len / kBlock + 2);
+  return DF_OK;
+}
+
+}  // namespace
+
+df_status cache_check(const void* cache, const int32_t* pages, const int32_t* lengths, int B, int Hk, int d, int page,
+                      int n_pages, int max_pages, CacheView* c) {
+  if (B < 0 || Hk < 1 || d < 1 || page < 1 || n_pages < 0 || max_pages < 0) return DF_ERR_INVALID_ARG;
+  if (d % 32 != 0 || d > 128 || page % kBlock != 0 || page > (1 << 20) || Hk > 65536) return DF_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page > (1ll << 30)) return DF_ERR_UNSUPPORTED;
+  if ((n_pages > 0 && !cache) || (B > 0 && (!lengths || (max_pages > 0 && !pages)))) return DF_ERR_INVALID_ARG;
+  if (!al16(cache) || (((uintptr_t)pages | (uintptr_t)lengths) & 3u) != 0) return DF_ERR_ALIGNMENT;
+  c->base = const_cast<uint8_t*>(static_cast<const uint8_t*>(cache));
+  c->pages = pages;
+  c->lengths = lengths;
+  c->Hk = Hk;
+  c->d = d;
+  c->page = page;
+  c->n_pages = n_pages;
+  c->max_pages = max_pages;
+  return DF_OK;
+}
+
+}  // namespace dfa
+
+using namespace dfa;
+
+extern "C" size_t df_cache_bytes(int n_pages, int Hk, int page, int d) {
+  CacheView c;
+  static const int32_t none = 0;
+  if (n_pages < 1 || cache_check(&none - ((uintptr_t)&none % 16) / 4, &none, &none, 0, Hk, d, page, n_pages, 0, &c) != DF_OK)
+    return 0;
+  return cache_bytes(Hk, d, page, n_pages);
+}
+
+extern "C" df_status df_cache_append(const void* k, const void* v, const int32_t* cu_seqlens, int B, int Hk, int n,
+                                     int total, int d, df_dtype dtype, void* cache, int n_pages, int page,
+                                     const int32_t* pages, int max_pages, const int32_t* lengths, int32_t* status,
+                                     df_stream_t stream) {
+  StoreArgs a;
+  if (dtype != DF_BF16 && dtype != DF_FP16 && dtype != DF_FP32) return DF_ERR_INVALID_ARG;
+  df_status st = cache_check(cache, pages, lengths, B, Hk, d, page, n_pages, max_pages, &a.c);
+  if (st == DF_OK) st = rows_check(cu_seqlens, B, n, total, &a);
+  if (st != DF_OK) return st;
+  if (dtype == DF_FP32) return DF_ERR_UNSUPPORTED;
+  if (total == 0 || B == 0) return DF_OK;
+  if (!k || !v) return DF_ERR_INVALID_ARG;
+  if (!al16(k) || !al16(v)) return DF_ERR_ALIGNMENT;
+  const size_t bytes = (size_t)total * Hk * d * 2;
+  if (overlapping({{cache, cache_bytes(Hk, d, page, n_pages)}},
+                  {{k, bytes}, {v, bytes}, {pages, (size_t)B * max_pages * 4}, {lengths, (size_t)B * 4},
+                   {cu_seqlens, ((size_t)B + 1) * 4}}))
+    return DF_ERR_INVALID_ARG;
+  a.k = const_cast<void*>(k);
+  a.v = const_cast<void*>(v);
+  a.status = status;
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = dtype == DF_BF16 ? launch<false, __nv_bfloat16>(a, s) : launch<false, __half>(a, s);
+  return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+extern "C" df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t* pages, int max_pages,
+                                   const int32_t* lengths, const int32_t* cu_seqlens, int B, int Hk, int n, int total,
+                                   int d, df_dtype dtype, void* k, void* v, int32_t* status, df_stream_t stream) {
+  StoreArgs a;
+  if (dtype != DF_BF16 && dtype != DF_FP16 && dtype != DF_FP32) return DF_ERR_INVALID_ARG;
+  df_status st = cache_check(cache, pages, lengths, B, Hk, d, page, n_pages, max_pages, &a.c);
+  if (st == DF_OK) st = rows_check(cu_seqlens, B, n, total, &a);
+  if (st != DF_OK) return st;
+  if (total == 0) return DF_OK;
+  if (!k || !v) return DF_ERR_INVALID_ARG;
+  if (!al16(k) || !al16(v)) return DF_ERR_ALIGNMENT;
+  const size_t bytes = (size_t)total * Hk * d * (dtype == DF_FP32 ? 4 : 2);
+  if (overlapping({{k, bytes}, {v, bytes}},
+                  {{cache, cache_bytes(Hk, d, page, n_pages)}, {pages, (size_t)B * max_pages * 4}, {lengths, (size_t)B * 4},
+                   {cu_seqlens, ((size_t)B + 1) * 4}}))
+    return DF_ERR_INVALID_ARG;
+  a.k = k;
+  a.v = v;
+  a.status = status;
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = dtype == DF_BF16   ? launch<true, __nv_bfloat16>(a, s)
+                        : dtype == DF_FP16 ? launch<true, __half>(a, s)
+                                           : launch<true, float>(a, s);
+  return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}

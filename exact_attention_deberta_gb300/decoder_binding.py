@@ -1,5 +1,5 @@
 """The part of the binding that a decoder's own attention needs: causal attention with a
-window and sinks, rotary positions.  Argument marshalling only, as ``binding``, whose helpers it uses and
+window and sinks, rotary positions, the 8-bit paged cache.  Argument marshalling only, as ``binding``, whose helpers it uses and
 through which every call here is reached as well (``binding.df_self_attn_fwd``)."""
 
 from __future__ import annotations
@@ -10,7 +10,8 @@ import torch
 
 from . import binding as b
 
-__all__ = ["df_self_attn_fwd", "df_self_attn_bwd", "df_rotary", "df_rotary_table"]
+__all__ = ["df_self_attn_fwd", "df_self_attn_bwd", "df_rotary", "df_rotary_table", "df_cache_new",
+           "df_cache_append", "df_cache_read", "df_cache_attn"]
 
 b._lib.df_self_attn_fwd.argtypes = [b._vp] * 6 + [b._i] * 8 + [ctypes.c_float] + [b._i] * 3 + [b._vp] * 5
 b._lib.df_self_attn_fwd.restype = b._i
@@ -127,3 +128,146 @@ def df_rotary(x, positions, table, *, interleaved=False, inverse=False, amplitud
                         T, d, 2 * table.numel(), 1 if interleaved else 0, 1 if inverse else 0, table.data_ptr(),
                         float(amplitude), b._DTYPE[dt]), "df_rotary")
     return outs[0] if isinstance(x, torch.Tensor) else list(outs)
+
+
+b._lib.df_cache_bytes.argtypes = [b._i] * 4
+b._lib.df_cache_bytes.restype = b._sz
+b._lib.df_cache_append.argtypes = [b._vp] * 3 + [b._i] * 6 + [b._vp, b._i, b._i, b._vp, b._i, b._vp, b._vp, b._vp]
+b._lib.df_cache_append.restype = b._i
+b._lib.df_cache_read.argtypes = [b._vp, b._i, b._i, b._vp, b._i, b._vp, b._vp] + [b._i] * 6 + [b._vp] * 4
+b._lib.df_cache_read.restype = b._i
+b._lib.df_cache_attn.argtypes = ([b._vp, b._vp] + [b._i] * 6 + [ctypes.c_float] + [b._i] * 4 + [b._vp, b._i, b._i, b._vp,
+                                 b._i, b._vp, b._i] + [b._vp] * 4)
+b._lib.df_cache_attn.restype = b._i
+
+BLOCK = 16  # tokens that share a scale
+
+
+def df_cache_new(n_pages, heads, page, d, device="cuda"):
+    """Memory of a cache of ``n_pages`` pages of ``page`` tokens: uint8
+    [n_pages, heads, page / 16, 32 d + 16], not initialised."""
+    n_pages, heads, page, d = int(n_pages), int(heads), int(page), int(d)
+    b._int_sizes(n_pages=n_pages, heads=heads, page=page, d=d)
+    if b._lib.df_cache_bytes(n_pages, heads, page, d) == 0:
+        raise ValueError("pages must be multiples of 16 tokens, the head size a multiple of 32 up to 128")
+    return torch.empty((n_pages, heads, page // BLOCK, 32 * d + 16), dtype=torch.uint8, device=device)
+
+
+def _cache_shape(cache, page_table, lengths):
+    """(sequences, heads, head size, pages, tokens of a page, pages of a sequence)."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or cache.shape[3] < 48 or (cache.shape[3] - 16) % 32 != 0:
+        raise ValueError("cache must be uint8 [n_pages, heads, page / 16, 32 d + 16]")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    if lengths.dtype != torch.int32 or lengths.dim() != 1 or lengths.shape[0] != page_table.shape[0]:
+        raise ValueError("lengths must be int32 [B]")
+    n_pages, heads, per, record = cache.shape
+    b._int_sizes(n_pages=n_pages, page=per * BLOCK)
+    return lengths.shape[0], heads, (record - 16) // 32, n_pages, per * BLOCK, page_table.shape[1]
+
+
+def _cache_rows(name, x, cu, B):
+    """(length, rows) of [B, n, ..] or, with offsets, [total, ..]."""
+    if x.dim() != (4 if cu is None else 3):
+        raise ValueError(f"{name} must be [B, n, heads, d], or [total, heads, d] with cu_seqlens")
+    if cu is None:
+        if x.shape[0] != B:
+            raise ValueError(f"{name} and lengths disagree on the number of sequences")
+        n, total = x.shape[1], x.shape[0] * x.shape[1]
+    else:
+        if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must be an int32 vector [B + 1]")
+        n, total = 0, x.shape[0]
+    b._int_sizes(rows=total)
+    return n, total
+
+
+def df_cache_append(k, v, cache, page_table, lengths, cu_seqlens=None, *, status=None, stream=None):
+    """Appends tokens to ``cache`` (``df_cache_new``): k, v [B, n, heads, d], or packed
+    [total, heads, d] with cu_seqlens, become the tokens from ``lengths`` [B] on of their
+    sequences, whose pages are ``page_table`` [B, max_pages] (int32).  ``lengths`` itself is
+    the caller's to add to.  Returns ``cache``."""
+    if stream is not None:
+        with b._current(stream, k):
+            return df_cache_append(k, v, cache, page_table, lengths, cu_seqlens, status=status)
+    idx = b._on_device((k, v, cache, page_table, lengths, cu_seqlens, status),
+                       "k v cache page_table lengths cu_seqlens status")
+    B, heads, d, n_pages, page, max_pages = _cache_shape(cache, page_table, lengths)
+    if k.dtype not in b._DTYPE or v.dtype != k.dtype or v.shape != k.shape or tuple(k.shape[-2:]) != (heads, d):
+        raise ValueError("k and v must be bf16 or fp16, with the cache's heads and head size")
+    n, total = _cache_rows("k", k, cu_seqlens, B)
+    if status is not None:
+        b._status_word(status)
+    b._check(b._call_on(idx, b._lib.df_cache_append, k.data_ptr(), v.data_ptr(), b._addr(cu_seqlens), B, heads, n, total, d,
+                        b._DTYPE[k.dtype], cache.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
+                        lengths.data_ptr(), b._addr(status)), "df_cache_append")
+    return cache
+
+
+def df_cache_read(cache, page_table, lengths, cu_seqlens=None, *, rows=None, dtype=torch.bfloat16, out=None, status=None,
+                  stream=None):
+    """The tokens that sequences hold, as (k, v) in ``dtype``: [B, rows, heads, d], or
+    [rows, heads, d] packed by cu_seqlens.  Rows beyond a sequence's length are zeros."""
+    if stream is not None:
+        with b._current(stream, cache):
+            return df_cache_read(cache, page_table, lengths, cu_seqlens, rows=rows, dtype=dtype, out=out, status=status)
+    B, heads, d, n_pages, page, max_pages = _cache_shape(cache, page_table, lengths)
+    if out is None:
+        if rows is None:
+            raise ValueError("rows (of each sequence, or of all of them with cu_seqlens) or out must be given")
+        shape = (int(rows), heads, d) if cu_seqlens is not None else (B, int(rows), heads, d)
+        b._int_sizes(rows=shape[-3])
+        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    k, v = out
+    if k.dtype not in b._DTYPE or v.dtype != k.dtype or v.shape != k.shape or tuple(k.shape[-2:]) != (heads, d):
+        raise ValueError("out must be two tensors of bf16, fp16 or fp32, with the cache's heads and head size")
+    idx = b._on_device((cache, page_table, lengths, cu_seqlens, k, v, status),
+                       "cache page_table lengths cu_seqlens out out status")
+    n, total = _cache_rows("out", k, cu_seqlens, B)
+    if status is not None:
+        b._status_word(status)
+    b._check(b._call_on(idx, b._lib.df_cache_read, cache.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
+                        lengths.data_ptr(), b._addr(cu_seqlens), B, heads, n, total, d, b._DTYPE[k.dtype], k.data_ptr(),
+                        v.data_ptr(), b._addr(status)), "df_cache_read")
+    return k, v
+
+
+def df_cache_attn(q, cache, page_table, lengths, cu_seqlens_q=None, *, max_seqlen_q=None, max_length=None, causal=True,
+                  window=0, sinks=0, scale=None, out=None, lse=None, status=None, stream=None):
+    """Attention of a few queries for each sequence, [B, Lq, H, d] or packed [T, H, d] with
+    cu_seqlens_q, to the tokens in ``cache``.  ``causal``: the queries are the last of the
+    ``lengths`` tokens (append them first) and see those up to their own position, with
+    ``window`` and ``sinks`` as ``df_self_attn_fwd``; otherwise every token.  ``max_length``
+    bounds ``lengths`` (default: what the page table has room for).  ``lse`` may be a float32
+    tensor [..., H] that receives the rows' log-sum-exp."""
+    if stream is not None:
+        with b._current(stream, q):
+            return df_cache_attn(q, cache, page_table, lengths, cu_seqlens_q, max_seqlen_q=max_seqlen_q,
+                                 max_length=max_length, causal=causal, window=window, sinks=sinks, scale=scale, out=out,
+                                 lse=lse, status=status)
+    idx = b._on_device((q, cache, page_table, lengths, cu_seqlens_q, out, lse, status),
+                       "q cache page_table lengths cu_seqlens_q out lse status")
+    B, heads, d, n_pages, page, max_pages = _cache_shape(cache, page_table, lengths)
+    if q.dtype not in b._DTYPE or q.shape[-1] != d:
+        raise ValueError("q must be bf16 or fp16, with the cache's head size")
+    Lq, total = _cache_rows("q", q, cu_seqlens_q, B)
+    if cu_seqlens_q is not None:
+        if max_seqlen_q is None:
+            raise ValueError("packed q needs max_seqlen_q (an upper bound of every length)")
+        Lq = int(max_seqlen_q)
+    window, sinks = _reach(window, sinks)
+    max_length = min(max_pages * page, 2 ** 31 - 1) if max_length is None else int(max_length)
+    b._int_sizes(max_seqlen_q=Lq, max_length=max_length)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must match q in shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:-1]):
+        raise ValueError("lse must be float32, [..., H]")
+    if status is not None:
+        b._status_word(status)
+    b._check(b._call_on(idx, b._lib.df_cache_attn, q.data_ptr(), b._addr(cu_seqlens_q), B, q.shape[-2], heads, Lq, total, d,
+                        d ** -0.5 if scale is None else float(scale), 1 if causal else 0, window, sinks, b._DTYPE[q.dtype],
+                        cache.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, lengths.data_ptr(), max_length,
+                        out.data_ptr(), b._addr(lse), b._addr(status)), "df_cache_attn")
+    return out

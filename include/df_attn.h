@@ -622,6 +622,82 @@ df_status df_rotary_table(int rot, double base, double factor, double original_l
                           double high, uint64_t* turns);
 
 /* ---------------------------------------------------------------------------
+ * Keys and values held in 8 bits: a paged cache for generation (a decoder's own tokens, or the
+ * encoder's states that a cross attention reads at every token).
+ *
+ * A block is 16 consecutive tokens of one key head.  It has one scale for its keys and one for
+ * its values, each the least power of two s (2^-100 at least) with |x| <= 448 s for every
+ * finite x of the block; a value is held as the e4m3 code of x / s (nearest, ties to even; NaN
+ * and infinities as NaN).  The cache is [n_pages][Hk][page / 16] records of 32 d + 16 bytes:
+ *     keys' codes [d / 32][16 tokens][32 columns], values' codes likewise, the keys' and the
+ *     values' scale (fp32), 8 bytes unused
+ *   cache      16-byte aligned, df_cache_bytes() bytes; its contents need not be initialised
+ *   page       tokens of a page, a multiple of 16;  d a multiple of 32, at most 128
+ *   pages      int32 [B, max_pages]: the pages of each sequence in the order of its tokens.
+ *              Entries that no token of the call falls on are not looked at, those of pages that a
+ *              window has left behind for instance.
+ *   lengths    int32 [B]: tokens that each sequence holds
+ *   status     as for df_cross_attn_fwd: DF_ERR_INVALID_ARG also for a token whose page is
+ *              missing (not 0 <= id < n_pages, or behind max_pages; it is then neither written
+ *              nor attended to), and for a length below 0 or, of an attention, beyond
+ *              max_pages * page (taken as 0)
+ * Sequences may share pages to read; a page that tokens are appended to belongs to one.
+ * Errors of the calls below: DF_ERR_INVALID_ARG (NULL pointer, sizes, offsets, overlap of
+ * what is written), DF_ERR_UNSUPPORTED (fp32 where not named, d, page, max_pages * page > 2^30,
+ * over 2^30 rows), DF_ERR_ALIGNMENT (tensors 16 bytes, tables 4), DF_ERR_CUDA.  One launch each. */
+
+/* Bytes of a cache (0 for sizes that the calls reject). */
+size_t df_cache_bytes(int n_pages, int Hk, int page, int d);
+
+/* Appends tokens: k, v [B, n, Hk, d] (total = B n), or with cu_seqlens (int32 [B + 1])
+ * [total, Hk, d] (n is then ignored), bf16 or fp16.  Those of sequence b become its tokens
+ * lengths[b], lengths[b] + 1, ...; lengths itself is left as it is (the caller adds the new
+ * tokens before it reads them).  A block that already holds tokens keeps its scale, or, where
+ * the new tokens ask for a larger one, takes that and rounds the held codes again (halved as
+ * often as the scale doubles: exact but among e4m3's subnormals).  Calling again with the
+ * same arguments changes nothing. */
+df_status df_cache_append(const void* k, const void* v, const int32_t* cu_seqlens, int B, int Hk,
+                          int n, int total, int d, df_dtype dtype, void* cache, int n_pages,
+                          int page, const int32_t* pages, int max_pages, const int32_t* lengths,
+                          int32_t* status, df_stream_t stream);
+
+/* Reads tokens back: k, v [B, n, Hk, d] (total = B n) or packed by cu_seqlens [total, Hk, d] in
+ * `dtype` (bf16, fp16 or fp32; codes times scale, exact unless a value leaves the type's range:
+ * fp16 then gets +-65504): the first tokens of each sequence, as many as it has rows here; rows
+ * beyond lengths[b], and packed rows behind the last sequence, get zeros. */
+df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t* pages,
+                        int max_pages, const int32_t* lengths, const int32_t* cu_seqlens, int B,
+                        int Hk, int n, int total, int d, df_dtype dtype, void* k, void* v,
+                        int32_t* status, df_stream_t stream);
+
+/* Attention of a few queries per sequence to the cache, without unpacking it:
+ *     s_ij = scale q_i.k_j,  out_i = sum_j exp(s_ij - lse_i) v_j     over the tokens j that i sees
+ *   q, out     [B, Lq, H, d] or, with cu_seqlens_q (int32 [B + 1]), [total_q, H, d], bf16 or
+ *              fp16; H a multiple of Hk.  Packed rows that belong to no sequence are left alone.
+ *   causal     1: the queries are the sequence's last tokens (which the cache holds already):
+ *              row i of n, at position p = i + lengths[b] - n, sees the tokens j <= p with
+ *              window = 0, j > p - window or j < sinks (as df_self_attn_fwd).  0: every query
+ *              sees every token; window and sinks must be 0.
+ *   Lq         the padded length, or a bound of the packed ones (more rows than that in a
+ *              sequence are reported, and left alone)
+ *   max_length a bound of lengths that the split of the work goes by (any value is right)
+ *   lse        NULL, or float32 [B, Lq, H] / [total_q, H]: log of the row's sum of exp
+ * A row that sees no token gets zeros and lse = -infinity.  Scores, statistics and sums are fp32;
+ * codes enter the products exactly, q too (bf16: down to 2^-24 of the row's largest), the weights
+ * as fp16 times 2^14 (11 bits down to 2^-28 of a row's largest).  Tokens that no query of the
+ * call sees may hold anything (as may what lies behind the last token in its page); a NaN that a
+ * query sees makes results NaN, also those of the call's other queries of that sequence.
+ * No atomics, no workspace: equal inputs give equal bits.  Made for up to some 64 rows (Lq H / Hk)
+ * a sequence and key head, which are read once; for long prompts read the tokens back
+ * (df_cache_read) and use df_self_attn_fwd. */
+df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, int B, int H, int Hk, int Lq,
+                        int total_q, int d, float scale, int causal, int window, int sinks,
+                        df_dtype dtype, const void* cache, int n_pages, int page,
+                        const int32_t* pages, int max_pages, const int32_t* lengths,
+                        int max_length, void* out, float* lse, int32_t* status,
+                        df_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Token embeddings: the rows that enter the encoder (or a decoder that reads
  * its states), and the gradient of the table.
  *

@@ -30,3 +30,4 @@ from .embedding import embed, embed_grad  # noqa: F401,E402
 from .cross import cross_rows, cross_batch  # noqa: F401,E402
 from .causal import visible, causal_rows, causal_batch  # noqa: F401,E402
 from .rotary import rotary, rotary_angles, rotary_frequencies  # noqa: F401,E402
+from .cache import CacheOracle, e4m3_codes, block_scale, record, E4M3  # noqa: F401,E402
