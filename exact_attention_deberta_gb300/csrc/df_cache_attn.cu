@@ -21,6 +21,8 @@
 //   - A weight is held times 2^14, so that fp16 keeps its digits down to 2^-28 of the largest.
 // Sequences are cut over the CTAs of a cluster where there are few of them; the parts are joined
 // through distributed shared memory, without a workspace or a second launch.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "df_cache.cuh"
@@ -54,7 +56,7 @@ template <int SLABS, int WR>
 struct DecodeSmem {
   static constexpr int D = 32 * SLABS;
   static constexpr int kRings = kWarps / WR;
-  static constexpr int kStages = SLABS == 1 ? 6 : SLABS == 2 ? 4 : 3;
+  static constexpr int kStages = SLABS == 1 ? 6 : SLABS == 2 ? 3 : 2;
   static constexpr uint32_t kRecord = 32 * D + 16;
   static constexpr uint32_t kStageBytes = 2 * kRecord;
   static constexpr uint32_t ring = 0;  // [kRings][kStages][two records]
@@ -74,7 +76,7 @@ struct DecodeSmem {
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -89,9 +91,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, unsigned long long src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"((uint64_t)src), "r"(bytes), "r"(smem_u32(bar))
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
 
@@ -173,7 +175,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   // ---- copies: tile i of this ring into stage i % S
   const bool producer = part == 0;
   const uint32_t ring = smem_u32(sm + SL::ring) + group * S * SL::kStageBytes;
-  int held_at = -1, id0 = -1, id1 = -1;  // pages of tiles held_at + lane of this ring, one for each block
+  int held_at = -1;  // this ring's tiles held_at + lane: the records of their two blocks (0: no copy)
+  unsigned long long rec0 = 0, rec1 = 0;
   int issued = 0;
   auto tile_first = [&](int i) { return reach.tile(first + group + R * i) * kTile; };
   auto issue = [&](int i) {  // (a converged warp)
@@ -181,23 +184,27 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
       held_at = i;
       const int k0 = tile_first(i + lane);
       const bool in = i + lane < mine;
-      id0 = in && reach.any(k0, kBlock) ? page_of(a.c, b, k0 / kBlock) : -2;
-      id1 = in && reach.any(k0 + kBlock, kBlock) ? page_of(a.c, b, k0 / kBlock + 1) : -2;
-      if (id0 == -1 || id1 == -1) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);  // tokens without a page
+      auto record = [&](int key) -> unsigned long long {
+        if (!in || !reach.any(key, kBlock)) return 0;
+        const int id = page_of(a.c, b, key / kBlock);
+        if (id >= 0) return (unsigned long long)record_of(a.c, id, hk, key / kBlock);
+        cross_fail(a.status, (int)DF_ERR_INVALID_ARG);  // tokens without a page
+        return 0;
+      };
+      rec0 = record(k0);
+      rec1 = record(k0 + kBlock);
     }
-    const int x0 = __shfl_sync(0xffffffffu, id0, i - held_at), x1 = __shfl_sync(0xffffffffu, id1, i - held_at);
-    const int s = i % S, blk = tile_first(i) / kBlock;
+    const unsigned long long x0 = __shfl_sync(0xffffffffu, rec0, i - held_at), x1 = __shfl_sync(0xffffffffu, rec1, i - held_at);
+    const int s = i % S;
     if (lane == 0) {
       const uint32_t dst = ring + s * SL::kStageBytes;
-      const uint8_t* r0p = x0 >= 0 ? record_of(a.c, x0, hk, blk) : nullptr;
-      const uint8_t* r1p = x1 >= 0 ? record_of(a.c, x1, hk, blk + 1) : nullptr;
-      have[s] = (x0 >= 0 ? 1 : 0) | (x1 >= 0 ? 2 : 0);
-      mbar_expect_tx(full + s, ((x0 >= 0 ? 1u : 0u) + (x1 >= 0 ? 1u : 0u)) * SL::kRecord);
-      if (r0p && r1p == r0p + SL::kRecord) {
-        bulk_load(dst, r0p, 2 * SL::kRecord, full + s);
+      have[s] = (x0 != 0 ? 1 : 0) | (x1 != 0 ? 2 : 0);
+      mbar_expect_tx(full + s, ((x0 != 0 ? 1u : 0u) + (x1 != 0 ? 1u : 0u)) * SL::kRecord);
+      if (x0 != 0 && x1 == x0 + SL::kRecord) {
+        bulk_load(dst, x0, 2 * SL::kRecord, full + s);
       } else {
-        if (r0p) bulk_load(dst, r0p, SL::kRecord, full + s);
-        if (r1p) bulk_load(dst + SL::kRecord, r1p, SL::kRecord, full + s);
+        if (x0 != 0) bulk_load(dst, x0, SL::kRecord, full + s);
+        if (x1 != 0) bulk_load(dst + SL::kRecord, x1, SL::kRecord, full + s);
       }
     }
     __syncwarp();
@@ -373,7 +380,12 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(acc, pa[blk], codes_f16((uint16_t)(m & 1 ? x >> 16 : x)), codes_f16((uint16_t)(m & 1 ? y >> 16 : y)));
 #pragma unroll
-            for (int e = 0; e < 2 * kHalves; ++e) o[c][m][e] += vs[blk] * acc[e];
+            for (int h = 0; h < kHalves; ++h) {
+              const float2 sum = fma2(make_float2(acc[2 * h], acc[2 * h + 1]), make_float2(vs[blk], vs[blk]),
+                                      make_float2(o[c][m][2 * h], o[c][m][2 * h + 1]));
+              o[c][m][2 * h] = sum.x;
+              o[c][m][2 * h + 1] = sum.y;
+            }
           }
         }
       }
@@ -487,13 +499,42 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
+// CTAs of `items` that share one, 1 to 8 (a cluster): the number for which the CTAs' rounds,
+// each as long as its share of the tiles and what it costs to begin and to join, are shortest.
+int splits_for(long long items, long long tiles, int rings, long long slots) {
+  constexpr long long kBegin = 6;  // in tiles of a warp
+  int best = 1;
+  long long least = LLONG_MAX;
+  for (int n = 1; n <= 8; ++n) {
+    const long long rounds = (items * n + slots - 1) / slots;
+    const long long cost = rounds * ((tiles + (long long)n * rings - 1) / (n * rings) + kBegin);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
 template <int SLABS, int WR, bool HALF>
-cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch(DecodeArgs a, long long tiles, cudaStream_t s) {
   auto kernel = decode_kernel<SLABS, WR, HALF>;
   constexpr int bytes = DecodeSmem<SLABS, WR>::bytes;
   static std::atomic<uint64_t> done{0};
+  static std::atomic<int> resident{0};  // CTAs an SM holds
   cudaError_t e = prepare_kernel((const void*)kernel, bytes, 0, &done);
   if (e != cudaSuccess) return e;
+  int per_sm = resident.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, bytes);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(per_sm, 1);
+    resident.store(per_sm, std::memory_order_relaxed);
+  }
+  const long long items = (long long)a.B * a.c.Hk * a.row_tiles;
+  a.splits = splits_for(items, tiles, kWarps / WR, (long long)device_sms() * per_sm);
+  if (items * a.splits > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const int grid = (int)(items * a.splits);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
@@ -510,10 +551,10 @@ cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t s) {
 }
 
 template <int SLABS>
-cudaError_t launch_rows(const DecodeArgs& a, int wr, bool half, int grid, cudaStream_t s) {
-  if (half) return launch<SLABS, 1, true>(a, grid, s);
-  return wr == 1 ? launch<SLABS, 1, false>(a, grid, s)
-                 : wr == 2 ? launch<SLABS, 2, false>(a, grid, s) : launch<SLABS, 4, false>(a, grid, s);
+cudaError_t launch_rows(const DecodeArgs& a, int wr, bool half, long long tiles, cudaStream_t s) {
+  if (half) return launch<SLABS, 1, true>(a, tiles, s);
+  return wr == 1 ? launch<SLABS, 1, false>(a, tiles, s)
+                 : wr == 2 ? launch<SLABS, 2, false>(a, tiles, s) : launch<SLABS, 4, false>(a, tiles, s);
 }
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -565,23 +606,18 @@ extern "C" df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, i
   const int rows = Lq * a.G;
   const int wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   a.row_tiles = (rows + 16 * wr - 1) / (16 * wr);
-  const long long items = (long long)B * Hk * a.row_tiles;
+  if ((long long)B * Hk * a.row_tiles > 0x7fffffffll / 8) return DF_ERR_UNSUPPORTED;
   // the tokens that a tile of rows sees at most, in tiles
   long long tiles = ((long long)std::min<long long>(max_length, (long long)max_pages * page) + kTile - 1) / kTile;
   if (window > 0) tiles = std::min<long long>(tiles, ((long long)window + Lq + sinks) / kTile + 3);
-  const int sms = device_sms(), rings = kWarps / wr;
-  a.splits = 1;
-  while (a.splits < 8 && items * a.splits * 2 <= 4ll * sms && a.splits * 2ll * rings * 2 <= tiles) a.splits *= 2;
-  const long long grid = items * a.splits;
-  if (grid > 0x7fffffffll) return DF_ERR_UNSUPPORTED;
   cudaStream_t s = (cudaStream_t)stream;
   const bool half = rows <= 8;
   cudaError_t e;
   switch (d / 32) {
-    case 1: e = launch_rows<1>(a, wr, half, (int)grid, s); break;
-    case 2: e = launch_rows<2>(a, wr, half, (int)grid, s); break;
-    case 3: e = launch_rows<3>(a, wr, half, (int)grid, s); break;
-    default: e = launch_rows<4>(a, wr, half, (int)grid, s); break;
+    case 1: e = launch_rows<1>(a, wr, half, tiles, s); break;
+    case 2: e = launch_rows<2>(a, wr, half, tiles, s); break;
+    case 3: e = launch_rows<3>(a, wr, half, tiles, s); break;
+    default: e = launch_rows<4>(a, wr, half, tiles, s); break;
   }
   return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
