@@ -81,6 +81,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
@@ -148,7 +161,22 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   int rest = blockIdx.x / a.splits;
   const int rt = rest % a.row_tiles;
   rest /= a.row_tiles;
-  const int hk = rest % a.c.Hk, b = rest / a.c.Hk;
+  const int hk = rest % a.c.Hk;
+  int b = rest / a.c.Hk;
+  // Sequences in the order of their lengths, the longest first, so that the launch's last CTAs
+  // are short ones.
+  if (a.B > 1 && a.B <= kThreads) {
+    int* lens = reinterpret_cast<int*>(sm + SL::ml_cta);
+    int* which = reinterpret_cast<int*>(sm + SL::ml_warp);
+    const int n = threadIdx.x < a.B ? a.c.lengths[threadIdx.x] : 0;
+    lens[threadIdx.x] = n;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < a.B; ++i) rank += lens[i] > n || (lens[i] == n && i < threadIdx.x);
+    if (threadIdx.x < a.B && rank == b) *which = threadIdx.x;
+    __syncthreads();
+    b = *which;
+  }
   int q0;
   const CrossSide side = {a.cu_q, a.Lq, a.Tq};
   int nq = seq_rows(side, b, a.status, &q0);
@@ -295,13 +323,19 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
         vs[blk] = (here >> blk) & 1 ? __uint_as_float(sw.y) : 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          float acc[4];
           const uint32_t row = rec + 32 * key_of(g >> 1, 2 * j + (g & 1)) + 8 * t;
 #pragma unroll
           for (int c = 0; c < SLABS; ++c) {
             const uint2 w = lds64(row + 512 * c);
-            mma_f16(acc, qa[c][0], codes_f16((uint16_t)w.x), codes_f16((uint16_t)(w.x >> 16)));
-            mma_f16(acc, qa[c][1], codes_f16((uint16_t)w.y), codes_f16((uint16_t)(w.y >> 16)));
+            uint32_t b0, b1;
+            codes4_f16(w.x, b0, b1);
+            if (c == 0)
+              mma_f16_first(acc, qa[c][0], b0, b1);
+            else
+              mma_f16(acc, qa[c][0], b0, b1);
+            codes4_f16(w.y, b0, b1);
+            mma_f16(acc, qa[c][1], b0, b1);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[blk][j][e] = acc[e] * ksc * ks_row[e >> 1];
@@ -372,19 +406,23 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
               if ((gone >> (4 * blk + x)) & 1u) w[x] = 0u;
           }
           // four tokens of four columns -> four columns of four tokens
-          const uint32_t a0 = prmt(w[0], w[1], 0x5140), a1 = prmt(w[2], w[3], 0x5140);
-          const uint32_t b0 = prmt(w[0], w[1], 0x7362), b1 = prmt(w[2], w[3], 0x7362);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t x = m < 2 ? a0 : b0, y = m < 2 ? a1 : b1;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(acc, pa[blk], codes_f16((uint16_t)(m & 1 ? x >> 16 : x)), codes_f16((uint16_t)(m & 1 ? y >> 16 : y)));
+          for (int two = 0; two < 2; ++two) {  // columns 2 two, 2 two + 1
+            uint32_t x[2], y[2];
+            codes4_f16(prmt(w[0], w[1], two ? 0x7362 : 0x5140), x[0], x[1]);
+            codes4_f16(prmt(w[2], w[3], two ? 0x7362 : 0x5140), y[0], y[1]);
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-              const float2 sum = fma2(make_float2(acc[2 * h], acc[2 * h + 1]), make_float2(vs[blk], vs[blk]),
-                                      make_float2(o[c][m][2 * h], o[c][m][2 * h + 1]));
-              o[c][m][2 * h] = sum.x;
-              o[c][m][2 * h + 1] = sum.y;
+            for (int e = 0; e < 2; ++e) {
+              float acc[4];
+              float(&to)[4] = o[c][2 * two + e];
+              mma_f16_first(acc, pa[blk], x[e], y[e]);
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) {
+                const float2 sum = fma2(make_float2(acc[2 * h], acc[2 * h + 1]), make_float2(vs[blk], vs[blk]),
+                                        make_float2(to[2 * h], to[2 * h + 1]));
+                to[2 * h] = sum.x;
+                to[2 * h + 1] = sum.y;
+              }
             }
           }
         }
