@@ -34,7 +34,10 @@ namespace {
 using namespace ptx;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTile = 32;  // keys of a copy: two blocks
+// Blocks of a tile, the keys of one copy: four where rows are short, so that what a tile costs
+// beside its products is paid less often.
+template <int SLABS>
+constexpr int kTileBlocks = SLABS <= 2 ? 4 : 2;
 constexpr float kUp = 14.f;
 
 struct DecodeArgs {
@@ -46,6 +49,7 @@ struct DecodeArgs {
   int B, H, G, Lq, Tq;
   int row_tiles;        // CTAs that share a sequence's query rows
   int splits;           // and its keys (cluster size)
+  int longest_first;    // (at most kThreads sequences)
   int causal, window, sinks, bf16;
   float kscale;         // scale log2(e)
   int32_t* status;
@@ -56,10 +60,10 @@ template <int SLABS, int WR>
 struct DecodeSmem {
   static constexpr int D = 32 * SLABS;
   static constexpr int kRings = kWarps / WR;
-  static constexpr int kStages = SLABS == 1 ? 6 : SLABS == 2 ? 3 : 2;
+  static constexpr int kStages = SLABS == 1 ? 4 : 2;
   static constexpr uint32_t kRecord = 32 * D + 16;
-  static constexpr uint32_t kStageBytes = 2 * kRecord;
-  static constexpr uint32_t ring = 0;  // [kRings][kStages][two records]
+  static constexpr uint32_t kStageBytes = kTileBlocks<SLABS> * kRecord;
+  static constexpr uint32_t ring = 0;  // [kRings][kStages][records of a tile]
   static constexpr uint32_t ring_bytes = kRings * kStages * kStageBytes;
   // after the loop, over the ring: each warp's O, and the CTA's
   static constexpr int kPitch = D + 4;
@@ -71,7 +75,7 @@ struct DecodeSmem {
   static constexpr uint32_t bars = ml_cta + 64 * 16;                                // full, empty [kRings][kStages]
   static constexpr uint32_t have = bars + 2 * kRings * kStages * 8;                 // int [kRings][kStages]
   static constexpr uint32_t misc = have + kRings * kStages * 4;
-  static constexpr uint32_t bytes = misc + 16;
+  static constexpr uint32_t bytes = (misc + 4 + 15) & ~15u;
   static_assert(bytes <= 232448 && o_cta % 16 == 0 && joined % 16 == 0 && ml_warp % 16 == 0 && bars % 8 == 0, "layout");
 };
 
@@ -111,28 +115,407 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, unsigned long long src, 
 }
 
 // The tokens that a tile of query rows, at positions p0 .. p1, sees: those before `head` and
-// those from lo to end - 1; in tiles of kTile, the first `heads` and then those from `skip`
+// those from lo to end - 1; in tiles of N keys, the first `heads` and then those from `skip`
 // tiles further on.
+template <int N>
 struct Reach {
   int head, lo, end, heads, skip, tiles;
-  __device__ __forceinline__ int tile(int t) const { return t < heads ? t : t + skip; }
+  __device__ __forceinline__ int key(int t) const { return (t < heads ? t : t + skip) * N; }  // the tile's first
   __device__ __forceinline__ bool any(int first, int n) const {
     return first < end && (first < head || first + n > lo);
   }
 };
-__device__ __forceinline__ Reach reach_of(const DecodeArgs& a, int held, int p0, int p1) {
-  Reach r;
+template <int N>
+__device__ __forceinline__ Reach<N> reach_of(const DecodeArgs& a, int held, int p0, int p1) {
+  Reach<N> r;
   r.end = a.causal ? max(min(held, p1 + 1), 0) : held;
   r.lo = a.causal && a.window != 0 ? max(p0 - a.window + 1, 0) : 0;
   r.lo = min(r.lo, r.end);
   r.head = min(a.sinks, r.lo);
-  r.heads = (r.head + kTile - 1) / kTile;
-  r.skip = max(r.lo / kTile - r.heads, 0);
-  r.tiles = (r.end + kTile - 1) / kTile - r.skip;
+  r.heads = (r.head + N - 1) / N;
+  r.skip = max(r.lo / N - r.heads, 0);
+  r.tiles = (r.end + N - 1) / N - r.skip;
   return r;
 }
 
-// HALF: at most 8 query rows (the tile's upper half is empty).
+// The query rows of a CTA or worker and what they see.
+struct Rows {
+  int b, hk, r0, rows, nr;      // rows r0 .. r0 + nr - 1 of the sequence's `rows`: token r / G, head r % G
+  int q0, held, p_first;        // the sequence's first query row and its position; tokens held
+  int p0, p1;                   // positions of the first and the last of these rows
+};
+// A sequence's queries and tokens, as far as they can be believed (`tell`: what cannot is reported).
+__device__ __forceinline__ void sequence(const DecodeArgs& a, int b, bool tell, int* q0, int* nq, int* held) {
+  const CrossSide side = {a.cu_q, a.Lq, a.Tq};
+  *nq = seq_rows(side, b, tell ? a.status : nullptr, q0);
+  *held = a.c.lengths[b];
+  const bool bad = *held < 0 || *held > a.c.max_pages * a.c.page;  // (the product is at most 2^30)
+  if (bad) *held = 0;
+  if (tell && (bad || *nq > a.Lq)) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
+  *nq = min(*nq, a.Lq);  // rows that the launch has no worker for are left alone
+}
+__device__ __forceinline__ Rows rows_of(const DecodeArgs& a, int b, int hk, int rt, int per_tile, bool tell) {
+  Rows w;
+  int nq;
+  sequence(a, b, tell, &w.q0, &nq, &w.held);
+  w.b = b;
+  w.hk = hk;
+  w.rows = nq * a.G;
+  w.r0 = rt * per_tile;
+  w.nr = min(per_tile, w.rows - w.r0);
+  w.p_first = w.held - nq;
+  w.p0 = w.p_first + w.r0 / a.G;
+  w.p1 = w.p_first + (w.r0 + max(w.nr, 1) - 1) / a.G;
+  return w;
+}
+
+// The record of the block at token `key`, 0 where nothing is to be copied.
+template <int N>
+__device__ __forceinline__ unsigned long long record_at(const DecodeArgs& a, const Reach<N>& reach, int b, int hk, int key) {
+  if (!reach.any(key, kBlock)) return 0;
+  const int id = page_of(a.c, b, key / kBlock);
+  if (id >= 0) return (unsigned long long)record_of(a.c, id, hk, key / kBlock);
+  cross_fail(a.status, (int)DF_ERR_INVALID_ARG);  // tokens without a page
+  return 0;
+}
+
+// Key i of lane t's four in a block.
+__device__ __forceinline__ int key_of(int t, int i) { return 4 * i + ((t + 2 * (i & 1)) & 3); }
+
+// A warp's 16 query rows and their running state; HALF: the upper 8 are empty.
+template <int SLABS, bool HALF>
+struct Softmax {
+  static constexpr int D = 32 * SLABS, kHalves = HALF ? 1 : 2, NB = kTileBlocks<SLABS>, kKeys = NB * kBlock;
+  static constexpr uint32_t kRecord = 32 * D + 16;
+  int whole_from, whole_to;  // tiles that begin in between have no key that a row does not see
+  uint32_t qa[SLABS][2][4];  // the rows as fp16, operands of the scores
+  float ks_row[2];
+  int pos[2];                // rows g and g + 8: their positions
+  float o[SLABS][4][4];
+  float m_run[2], l_run[2];  // l_run: this lane's keys only
+
+  // (bf16 rows become fp16 times a power of two, exactly)
+  __device__ __forceinline__ void begin(const DecodeArgs& a, const Rows& w, int part) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    whole_to = (a.causal ? min(w.p0 + 1, w.held) : w.held) - kKeys;
+    whole_from = a.causal && a.window != 0 ? w.p1 - a.window + 1 : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = w.r0 + 16 * part + g + 8 * h;
+      const bool in = r < w.rows && h < kHalves;
+      pos[h] = in ? w.p_first + r / a.G : INT_MIN;
+      ks_row[h] = a.kscale;
+      m_run[h] = -INFINITY;
+      l_run[h] = 0.f;
+      uint4 v[SLABS];
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(a.q) +
+          ((size_t)(w.q0 + (in ? r / a.G : 0)) * a.H + (size_t)w.hk * a.G + (in ? r % a.G : 0)) * D + 8 * t);
+#pragma unroll
+      for (int c = 0; c < SLABS; ++c) v[c] = in ? src[4 * c] : make_uint4(0u, 0u, 0u, 0u);
+      if (a.bf16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < SLABS; ++c) {
+          const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = min(max(top >> 7, 1u), 253u);  // the largest is below 2^(e - 126)
+        const float down = __uint_as_float((254u - e) << 23);
+        ks_row[h] = a.kscale * __uint_as_float(e << 23);
+#pragma unroll
+        for (int c = 0; c < SLABS; ++c) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(&v[c]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = pack_f16x2(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < SLABS; ++c) {
+        qa[c][0][h] = v[c].x;
+        qa[c][0][2 + h] = v[c].y;
+        qa[c][1][h] = v[c].z;
+        qa[c][1][2 + h] = v[c].w;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < SLABS; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][m][e] = 0.f;
+  }
+
+  // One tile: its records at `base` (shared memory), of which those in `here` were copied.
+  __device__ __forceinline__ void tile(const DecodeArgs& a, const Rows& w, const Reach<kKeys>& reach, uint32_t base,
+                                       int first_key, int here) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // every key of the tile counts for every row
+    const bool whole = here == (1 << NB) - 1 && first_key <= whole_to &&
+                       (first_key >= whole_from || first_key + kKeys <= a.sinks);
+    float sc[NB][2][4], vs[NB], f[NB][kHalves];
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint32_t rec = base + blk * kRecord;
+      const uint2 sw = lds64(rec + 32 * D);
+      // (positive, so that a score of -infinity stays one)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) f[blk][h] = fmaxf(__uint_as_float(sw.x) * ks_row[h], 1.17549435e-38f);
+      vs[blk] = __uint_as_float(sw.y);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t row = rec + 32 * key_of(g >> 1, 2 * j + (g & 1)) + 8 * t;
+#pragma unroll
+        for (int c = 0; c < SLABS; ++c) {
+          const uint2 x = lds64(row + 512 * c);
+          uint32_t b0, b1;
+          codes4_f16(x.x, b0, b1);
+          if (c == 0)
+            mma_f16_first(sc[blk][j], qa[c][0], b0, b1);
+          else
+            mma_f16(sc[blk][j], qa[c][0], b0, b1);
+          codes4_f16(x.y, b0, b1);
+          mma_f16(sc[blk][j], qa[c][1], b0, b1);
+        }
+      }
+    }
+    uint32_t gone = 0;  // of this lane's keys (t, i), bit 4 blk + i: those that no row counts
+    if (!whole) {
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        if (!((here >> blk) & 1)) {  // (its scales are not there either)
+          vs[blk] = 0.f;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) f[blk][h] = 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = first_key + kBlock * blk + key_of(t, 2 * j + x);
+            const bool there = (here >> blk) & 1 && reach.any(key, 1);
+            if (!there) gone |= 1u << (4 * blk + 2 * j + x);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              const bool seen =
+                  there && (!a.causal || (key <= pos[h] && (a.window == 0 || key > pos[h] - a.window || key < a.sinks)));
+              if (!seen) sc[blk][j][2 * h + x] = -INFINITY;
+            }
+          }
+      }
+    }
+    uint32_t pa[NB][4];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        const float top = fmaxf(fmaxf(sc[blk][0][2 * h], sc[blk][0][2 * h + 1]), fmaxf(sc[blk][1][2 * h], sc[blk][1][2 * h + 1]));
+        mt = fmaxf(mt, top * f[blk][h]);
+      }
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2)) - kUp;
+      if (__any_sync(0xffffffffu, mt > m_run[h])) {
+        const float m_new = fmaxf(m_run[h], mt);
+        const float down = m_new > m_run[h] ? ex2(m_run[h] - m_new) : 1.f;
+        m_run[h] = m_new;
+        l_run[h] *= down;
+#pragma unroll
+        for (int c = 0; c < SLABS; ++c)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            o[c][m][2 * h] *= down;
+            o[c][m][2 * h + 1] *= down;
+          }
+      }
+      const float shift = m_run[h] == -INFINITY ? -INFINITY : -m_run[h];
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 z = fma2(make_float2(sc[blk][j][2 * h], sc[blk][j][2 * h + 1]), make_float2(f[blk][h], f[blk][h]),
+                                make_float2(shift, shift));
+          const float2 p = make_float2(ex2(z.x), ex2(z.y));
+          sum = add2(sum, p);
+          pa[blk][2 * j + h] = pack_f16x2(p.x, p.y);
+        }
+      l_run[h] += sum.x + sum.y;
+    }
+    if (HALF) {
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) pa[blk][1] = pa[blk][3] = 0u;
+    }
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      const uint32_t rec = base + blk * kRecord + 16 * D + 4 * g;
+#pragma unroll
+      for (int c = 0; c < SLABS; ++c) {
+        uint32_t v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = lds32(rec + 512 * c + 32 * key_of(t, x));
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if ((gone >> (4 * blk + x)) & 1u) v[x] = 0u;
+        }
+        // four tokens of four columns -> four columns of four tokens
+#pragma unroll
+        for (int two = 0; two < 2; ++two) {  // columns 2 two, 2 two + 1
+          uint32_t x[2], y[2];
+          codes4_f16(prmt(v[0], v[1], two ? 0x7362 : 0x5140), x[0], x[1]);
+          codes4_f16(prmt(v[2], v[3], two ? 0x7362 : 0x5140), y[0], y[1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float acc[4];
+            float(&to)[4] = o[c][2 * two + e];
+            mma_f16_first(acc, pa[blk], x[e], y[e]);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              const float2 sum = fma2(make_float2(acc[2 * h], acc[2 * h + 1]), make_float2(vs[blk], vs[blk]),
+                                      make_float2(to[2 * h], to[2 * h + 1]));
+              to[2 * h] = sum.x;
+              to[2 * h + 1] = sum.y;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // The sum of row g + 8 h over the lanes that share it.
+  __device__ __forceinline__ float row_sum(int h) const {
+    float l = l_run[h];
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    return l + __shfl_xor_sync(0xffffffffu, l, 2);
+  }
+  // Columns 32 c + 8 t + 4 x .. + 3 of row g + 8 h.
+  __device__ __forceinline__ float4 piece(int h, int c, int x) const {
+    return make_float4(o[c][0][2 * h + x], o[c][1][2 * h + x], o[c][2][2 * h + x], o[c][3][2 * h + x]);
+  }
+};
+
+// What stands for s (its maximum and sum) in a join whose maximum is m: the factor of its O, and
+// its part of the sum (a NaN stays one).
+__device__ __forceinline__ float join_factor(float s_max, float m) { return s_max != -INFINITY ? ex2(s_max - m) : 0.f; }
+__device__ __forceinline__ float join_sum(float s_sum, float f) {
+  return f > 0.f ? s_sum * f : s_sum != s_sum ? s_sum : 0.f;
+}
+__device__ __forceinline__ void add_scaled(float (&v)[4], float f, const float4& x) {
+  if (!(f > 0.f)) return;
+  v[0] += f * x.x;
+  v[1] += f * x.y;
+  v[2] += f * x.z;
+  v[3] += f * x.w;
+}
+
+// Four columns of query row r (of its sequence), divided by the row's sum and rounded; the first
+// ones bring lse.
+__device__ __forceinline__ void store4(const DecodeArgs& a, const Rows& w, int r, int D, int piece, float m, float l,
+                                       const float (&v)[4]) {
+  const float inv = l != 0.f ? rcp(l) : 0.f;  // (a NaN stays one)
+  const size_t at = (size_t)(w.q0 + r / a.G) * a.H + (size_t)w.hk * a.G + r % a.G;
+  const uint32_t lo = a.bf16 ? pack_bf16x2(v[0] * inv, v[1] * inv) : pack_f16x2(v[0] * inv, v[1] * inv);
+  const uint32_t hi = a.bf16 ? pack_bf16x2(v[2] * inv, v[3] * inv) : pack_f16x2(v[2] * inv, v[3] * inv);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * piece) = make_uint2(lo, hi);
+  if (a.lse && piece == 0) a.lse[at] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
+}
+
+// The copies of a ring: tiles 0 .. count - 1, tile i into stage i % S.  `find(i, x)` gives the
+// records of tile i's blocks (0: none); a lane does that for one tile of every 32.
+template <int S, int NB, uint32_t RECORD, typename Find>
+struct Feeder {
+  Find find;
+  uint32_t ring;
+  uint64_t* full;
+  volatile int* have;
+  int count, held_at = -1, issued = 0;
+  // the lane's tile: its records, and the first one with its low bits set where all of them follow
+  // one another (records start on 16 bytes)
+  unsigned long long rec[NB], run = 0;
+
+  __device__ __forceinline__ Feeder(Find f, uint32_t r, uint64_t* b, volatile int* h, int n)
+      : find(f), ring(r), full(b), have(h), count(n) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) rec[k] = 0;
+  }
+  // Tile i into stage s (a converged warp).
+  __device__ __forceinline__ void issue(int i, int s) {
+    const int lane = threadIdx.x & 31;
+    if (held_at < 0 || i >= held_at + 32) {
+      held_at = i;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) rec[k] = 0;
+      if (i + lane < count) find(i + lane, rec);
+      bool follow = rec[0] != 0;
+#pragma unroll
+      for (int k = 1; k < NB; ++k) follow = follow && rec[k] == rec[0] + k * RECORD;
+      run = follow ? rec[0] | 1 : 0;
+    }
+    const unsigned long long x = __shfl_sync(0xffffffffu, run, i - held_at);
+    const uint32_t dst = ring + s * NB * RECORD;
+    if (x != 0) {
+      if (lane == 0) {
+        have[s] = (1 << NB) - 1;
+        mbar_expect_tx(full + s, NB * RECORD);
+        bulk_load(dst, x - 1, NB * RECORD, full + s);
+      }
+    } else {
+      unsigned long long y[NB];
+      int here = 0;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        y[k] = __shfl_sync(0xffffffffu, rec[k], i - held_at);
+        here |= (y[k] != 0 ? 1 : 0) << k;
+      }
+      if (lane == 0) {
+        have[s] = here;
+        mbar_expect_tx(full + s, __popc(here) * RECORD);
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+          if (y[k] != 0) bulk_load(dst + k * RECORD, y[k], RECORD, full + s);
+      }
+    }
+    __syncwarp();
+    issued = i + 1;
+  }
+  __device__ __forceinline__ void drain(int done) const {
+    for (int i = done; i < issued; ++i) mbar_wait(full + i % S, (i / S) & 1, kDrainBudget);
+  }
+};
+
+// The stage of a ring's current tile, and how often the ring has gone round.
+template <int S>
+struct Stage {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == S) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+template <typename SL>
+__device__ __forceinline__ void init_bars(uint8_t* sm, int wr) {
+  constexpr int n = SL::kRings * SL::kStages;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < n; ++i) {
+      mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + i, 1);
+      mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + n + i, wr);
+    }
+    *reinterpret_cast<volatile int*>(sm + SL::misc) = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+}
+
+// A CTA, or a cluster of them, for each sequence, key head and tile of query rows.
 template <int SLABS, int WR, bool HALF>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   using SL = DecodeSmem<SLABS, WR>;
@@ -146,26 +529,16 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   uint64_t* empty = reinterpret_cast<uint64_t*>(sm + SL::bars) + (R + group) * S;
   volatile int* have = reinterpret_cast<volatile int*>(sm + SL::have) + group * S;
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SL::misc);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < R * S; ++i) {
-      mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + i, 1);
-      mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + R * S + i, WR);
-    }
-    *s_abort = 0;
-    mbar_fence_init();
-  }
-  __syncthreads();
+  init_bars<SL>(sm, WR);
 
-  // ---- the CTA's work: sequence, key head, query rows, part of the keys
   const int split = blockIdx.x % a.splits;
   int rest = blockIdx.x / a.splits;
   const int rt = rest % a.row_tiles;
   rest /= a.row_tiles;
-  const int hk = rest % a.c.Hk;
   int b = rest / a.c.Hk;
-  // Sequences in the order of their lengths, the longest first, so that the launch's last CTAs
+  // Sequences in the order of their lengths, the longest first, so that a launch's last CTAs
   // are short ones.
-  if (a.B > 1 && a.B <= kThreads) {
+  if (a.longest_first) {
     int* lens = reinterpret_cast<int*>(sm + SL::ml_cta);
     int* which = reinterpret_cast<int*>(sm + SL::ml_warp);
     const int n = threadIdx.x < a.B ? a.c.lengths[threadIdx.x] : 0;
@@ -177,271 +550,47 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
     __syncthreads();
     b = *which;
   }
-  int q0;
-  const CrossSide side = {a.cu_q, a.Lq, a.Tq};
-  int nq = seq_rows(side, b, a.status, &q0);
-  int held = a.c.lengths[b];
-  if (held < 0 || held > a.c.max_pages * a.c.page) {  // (the product is at most 2^30)
-    held = 0;
-    if (threadIdx.x == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
-  }
-  if (nq > a.Lq) {  // rows that the launch has no CTA for
-    if (threadIdx.x == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
-    nq = a.Lq;
-  }
-  const int rows = nq * a.G, r0 = rt * 16 * WR;  // rows: token r / G, head r % G
-  const int nr = min(16 * WR, rows - r0);
-  const int p_first = held - nq;                 // position of the sequence's first query
-  const int p0 = p_first + r0 / a.G, p1 = p_first + (r0 + max(nr, 1) - 1) / a.G;
-  Reach reach = reach_of(a, held, p0, p1);
-  if (nr <= 0) reach.tiles = 0;
+  const Rows w = rows_of(a, b, rest % a.c.Hk, rt, 16 * WR, threadIdx.x == 0);
+  constexpr int NB = kTileBlocks<SLABS>, kKeys = NB * kBlock;
+  Reach<kKeys> reach = reach_of<kKeys>(a, w.held, w.p0, w.p1);
+  if (w.nr <= 0) reach.tiles = 0;
   // this CTA's tiles, of which its rings take every R-th
   const int first = (int)((long long)reach.tiles * split / a.splits);
   const int count = (int)((long long)reach.tiles * (split + 1) / a.splits) - first;
   const int mine = (count - group + R - 1) / R;
-
-  // ---- copies: tile i of this ring into stage i % S
+  auto tile_first = [&](int i) { return reach.key(first + group + R * i); };
+  auto find = [&](int i, unsigned long long (&x)[NB]) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) x[k] = record_at(a, reach, w.b, w.hk, tile_first(i) + k * kBlock);
+  };
   const bool producer = part == 0;
   const uint32_t ring = smem_u32(sm + SL::ring) + group * S * SL::kStageBytes;
-  int held_at = -1;  // this ring's tiles held_at + lane: the records of their two blocks (0: no copy)
-  unsigned long long rec0 = 0, rec1 = 0;
-  int issued = 0;
-  auto tile_first = [&](int i) { return reach.tile(first + group + R * i) * kTile; };
-  auto issue = [&](int i) {  // (a converged warp)
-    if (held_at < 0 || i >= held_at + 32) {
-      held_at = i;
-      const int k0 = tile_first(i + lane);
-      const bool in = i + lane < mine;
-      auto record = [&](int key) -> unsigned long long {
-        if (!in || !reach.any(key, kBlock)) return 0;
-        const int id = page_of(a.c, b, key / kBlock);
-        if (id >= 0) return (unsigned long long)record_of(a.c, id, hk, key / kBlock);
-        cross_fail(a.status, (int)DF_ERR_INVALID_ARG);  // tokens without a page
-        return 0;
-      };
-      rec0 = record(k0);
-      rec1 = record(k0 + kBlock);
-    }
-    const unsigned long long x0 = __shfl_sync(0xffffffffu, rec0, i - held_at), x1 = __shfl_sync(0xffffffffu, rec1, i - held_at);
-    const int s = i % S;
-    if (lane == 0) {
-      const uint32_t dst = ring + s * SL::kStageBytes;
-      have[s] = (x0 != 0 ? 1 : 0) | (x1 != 0 ? 2 : 0);
-      mbar_expect_tx(full + s, ((x0 != 0 ? 1u : 0u) + (x1 != 0 ? 1u : 0u)) * SL::kRecord);
-      if (x0 != 0 && x1 == x0 + SL::kRecord) {
-        bulk_load(dst, x0, 2 * SL::kRecord, full + s);
-      } else {
-        if (x0 != 0) bulk_load(dst, x0, SL::kRecord, full + s);
-        if (x1 != 0) bulk_load(dst + SL::kRecord, x1, SL::kRecord, full + s);
-      }
-    }
-    __syncwarp();
-    issued = i + 1;
-  };
+  Feeder<S, NB, SL::kRecord, decltype(find)> feed(find, ring, full, have, mine);
   if (producer)
-    for (int i = 0; i < min(S, mine); ++i) issue(i);
+    for (int i = 0; i < min(S, mine); ++i) feed.issue(i, i);
 
-  // ---- query rows g and g + 8 of the warp, as fp16 (bf16: times a power of two, exactly)
-  uint32_t qa[SLABS][2][4];
-  float ks_row[2];
-  int pos[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = r0 + 16 * part + g + 8 * h;
-    const bool in = r < rows && h < kHalves;
-    pos[h] = in ? p_first + r / a.G : INT_MIN;
-    ks_row[h] = a.kscale;
-    uint4 v[SLABS];
-    const uint4* src = reinterpret_cast<const uint4*>(
-        static_cast<const uint16_t*>(a.q) + ((size_t)(q0 + (in ? r / a.G : 0)) * a.H + (size_t)hk * a.G + (in ? r % a.G : 0)) * D + 8 * t);
-#pragma unroll
-    for (int c = 0; c < SLABS; ++c) v[c] = in ? src[4 * c] : make_uint4(0u, 0u, 0u, 0u);
-    if (a.bf16) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int c = 0; c < SLABS; ++c) {
-        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const uint32_t e = min(max(top >> 7, 1u), 253u);  // the largest is below 2^(e - 126)
-      const float down = __uint_as_float((254u - e) << 23);
-      ks_row[h] = a.kscale * __uint_as_float(e << 23);
-#pragma unroll
-      for (int c = 0; c < SLABS; ++c) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v[c]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < SLABS; ++c) {
-      qa[c][0][h] = v[c].x;
-      qa[c][0][2 + h] = v[c].y;
-      qa[c][1][h] = v[c].z;
-      qa[c][1][2 + h] = v[c].w;
-    }
-  }
-
-  // ---- the loop
-  float o[SLABS][4][4];
-#pragma unroll
-  for (int c = 0; c < SLABS; ++c)
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[c][m][e] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-  // bytes from a record's start to this lane's reads: K row of key (g / 2, 2 j + g % 2), V row of key (t, i)
-  auto key_of = [](int tt, int i) { return 4 * i + ((tt + 2 * (i & 1)) & 3); };
-  const bool rows_here = 16 * part < nr;
+  Softmax<SLABS, HALF> st;
+  st.begin(a, w, part);
+  const bool rows_here = 16 * part < w.nr;
   bool ok = true;
   int done = 0;
+  Stage<S> stage;
 #pragma unroll 1
-  for (int i = 0; i < mine; ++i) {
-    const int s = i % S;
-    ok = ok && cross_wait(full + s, (i / S) & 1, a.budget, s_abort);
-    ok = __all_sync(0xffffffffu, ok);
+  for (int i = 0; i < mine; ++i, stage.next()) {
+    const int s = stage.at;
+    ok = __all_sync(0xffffffffu, cross_wait(full + s, stage.phase, a.budget, s_abort));
     if (!ok) break;
     done = i + 1;
-    const uint32_t base = ring + s * SL::kStageBytes;
-    const int first_key = tile_first(i), here = have[s];
-    // every key of the tile counts for every row of the CTA
-    const bool whole = here == 3 && (!a.causal ? first_key + kTile <= held
-                                               : first_key + kTile <= p0 + 1 &&
-                                                     (a.window == 0 || p1 - a.window < first_key || first_key + kTile <= a.sinks));
-    if (rows_here) {
-      float sc[2][2][4], vs[2];
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const uint32_t rec = base + blk * SL::kRecord;
-        const uint2 sw = lds64(rec + 32 * D);
-        const float ksc = __uint_as_float(sw.x);
-        vs[blk] = (here >> blk) & 1 ? __uint_as_float(sw.y) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float acc[4];
-          const uint32_t row = rec + 32 * key_of(g >> 1, 2 * j + (g & 1)) + 8 * t;
-#pragma unroll
-          for (int c = 0; c < SLABS; ++c) {
-            const uint2 w = lds64(row + 512 * c);
-            uint32_t b0, b1;
-            codes4_f16(w.x, b0, b1);
-            if (c == 0)
-              mma_f16_first(acc, qa[c][0], b0, b1);
-            else
-              mma_f16(acc, qa[c][0], b0, b1);
-            codes4_f16(w.y, b0, b1);
-            mma_f16(acc, qa[c][1], b0, b1);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[blk][j][e] = acc[e] * ksc * ks_row[e >> 1];
-        }
-      }
-      uint32_t gone = 0;  // of this lane's keys (t, i), bit 4 blk + i: those that no row counts
-      if (!whole) {
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int key = first_key + kBlock * blk + key_of(t, 2 * j + x);
-              const bool there = (here >> blk) & 1 && reach.any(key, 1);
-              if (!there) gone |= 1u << (4 * blk + 2 * j + x);
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h) {
-                const bool seen = there && (!a.causal || (key <= pos[h] && (a.window == 0 || key > pos[h] - a.window || key < a.sinks)));
-                if (!seen) sc[blk][j][2 * h + x] = -INFINITY;
-              }
-            }
-      }
-      uint32_t pa[2][4];
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        float mt = fmaxf(fmaxf(fmaxf(sc[0][0][2 * h], sc[0][0][2 * h + 1]), fmaxf(sc[0][1][2 * h], sc[0][1][2 * h + 1])),
-                         fmaxf(fmaxf(sc[1][0][2 * h], sc[1][0][2 * h + 1]), fmaxf(sc[1][1][2 * h], sc[1][1][2 * h + 1])));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2)) - kUp;
-        if (__any_sync(0xffffffffu, mt > m_run[h])) {
-          const float m_new = fmaxf(m_run[h], mt);
-          const float f = m_new > m_run[h] ? ex2(m_run[h] - m_new) : 1.f;
-          m_run[h] = m_new;
-          l_run[h] *= f;
-#pragma unroll
-          for (int c = 0; c < SLABS; ++c)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              o[c][m][2 * h] *= f;
-              o[c][m][2 * h + 1] *= f;
-            }
-        }
-        const float shift = m_run[h] == -INFINITY ? INFINITY : m_run[h];
-        float sum = 0.f;
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float x = ex2(sc[blk][j][2 * h] - shift), y = ex2(sc[blk][j][2 * h + 1] - shift);
-            sum += x + y;
-            pa[blk][2 * j + h] = pack_f16x2(x, y);
-          }
-        l_run[h] += sum;
-      }
-      if (HALF) pa[0][1] = pa[0][3] = pa[1][1] = pa[1][3] = 0u;
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const uint32_t rec = base + blk * SL::kRecord + 16 * D + 4 * g;
-#pragma unroll
-        for (int c = 0; c < SLABS; ++c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = lds32(rec + 512 * c + 32 * key_of(t, x));
-          if (!whole) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if ((gone >> (4 * blk + x)) & 1u) w[x] = 0u;
-          }
-          // four tokens of four columns -> four columns of four tokens
-#pragma unroll
-          for (int two = 0; two < 2; ++two) {  // columns 2 two, 2 two + 1
-            uint32_t x[2], y[2];
-            codes4_f16(prmt(w[0], w[1], two ? 0x7362 : 0x5140), x[0], x[1]);
-            codes4_f16(prmt(w[2], w[3], two ? 0x7362 : 0x5140), y[0], y[1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float acc[4];
-              float(&to)[4] = o[c][2 * two + e];
-              mma_f16_first(acc, pa[blk], x[e], y[e]);
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h) {
-                const float2 sum = fma2(make_float2(acc[2 * h], acc[2 * h + 1]), make_float2(vs[blk], vs[blk]),
-                                        make_float2(to[2 * h], to[2 * h + 1]));
-                to[2 * h] = sum.x;
-                to[2 * h + 1] = sum.y;
-              }
-            }
-          }
-        }
-      }
-    }
+    if (rows_here) st.tile(a, w, reach, ring + s * SL::kStageBytes, tile_first(i), have[s]);
     __syncwarp();
     if (WR > 1 && lane == 0) mbar_arrive(empty + s);
     if (producer && i + S < mine) {
-      if (WR > 1) {
-        ok = cross_wait(empty + s, (i / S) & 1, a.budget, s_abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
-      issue(i + S);
+      if (WR > 1 && !__all_sync(0xffffffffu, cross_wait(empty + s, stage.phase, a.budget, s_abort))) break;
+      feed.issue(i + S, s);
     }
   }
   // a wait ran out: no copy may still be landing when the ring is used again
-  if (producer)
-    for (int i = done; i < issued; ++i) mbar_wait(full + i % S, (i / S) & 1, kDrainBudget);
+  if (producer) feed.drain(done);
   __syncthreads();
 
   // ---- the CTA's rows: its warps' parts together
@@ -449,17 +598,14 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   float2* sml = reinterpret_cast<float2*>(sm + SL::ml_warp);
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
-    float l = l_run[h];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float l = st.row_sum(h);
     const int r = warp * 16 + g + 8 * h;
-    if (t == 0) sml[r] = make_float2(m_run[h], l);
+    if (t == 0) sml[r] = make_float2(st.m_run[h], l);
 #pragma unroll
     for (int c = 0; c < SLABS; ++c)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        *reinterpret_cast<float4*>(so + r * SL::kPitch + 32 * c + 8 * t + 4 * x) =
-            make_float4(o[c][0][2 * h + x], o[c][1][2 * h + x], o[c][2][2 * h + x], o[c][3][2 * h + x]);
+        *reinterpret_cast<float4*>(so + r * SL::kPitch + 32 * c + 8 * t + 4 * x) = st.piece(h, c, x);
   }
   __syncthreads();
   constexpr int kPieces = D / 4;
@@ -467,45 +613,21 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   float4* s_ml = reinterpret_cast<float4*>(sm + SL::ml_cta);
   float* s_o = reinterpret_cast<float*>(sm + SL::o_cta);
   const bool failed = *s_abort != 0;
-  auto store = [&](int row, int piece, float m, float l, float (&v)[4]) {
-    const float inv = l != 0.f ? rcp(l) : 0.f;  // (a NaN stays one)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] *= inv;
-    const int r = r0 + row;
-    const size_t at = (size_t)(q0 + r / a.G) * a.H + (size_t)hk * a.G + r % a.G;
-    uint32_t lo, hi;
-    if (a.bf16) {
-      lo = pack_bf16x2(v[0], v[1]);
-      hi = pack_bf16x2(v[2], v[3]);
-    } else {
-      lo = pack_f16x2(v[0], v[1]);
-      hi = pack_f16x2(v[2], v[3]);
-    }
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * piece) = make_uint2(lo, hi);
-    if (a.lse && piece == 0) a.lse[at] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
-  };
-  for (int i = threadIdx.x; i < max(nr, 0) * kPieces; i += kThreads) {
+  for (int i = threadIdx.x; i < max(w.nr, 0) * kPieces; i += kThreads) {
     const int row = i / kPieces, piece = i - row * kPieces;
-    const int w0 = row >> 4, rr = row & 15;
+    const int at = (row >> 4) * 16 + (row & 15);
     float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < R; ++k) m = fmaxf(m, sml[(k * WR + w0) * 16 + rr].x);
+    for (int k = 0; k < R; ++k) m = fmaxf(m, sml[k * WR * 16 + at].x);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const int at = (k * WR + w0) * 16 + rr;
-      const float2 s = sml[at];
-      const float f = s.x != -INFINITY ? ex2(s.x - m) : 0.f;
-      l += f > 0.f || s.y != s.y ? s.y * (f > 0.f ? f : 1.f) : 0.f;
-      const float4 x = *reinterpret_cast<const float4*>(so + at * SL::kPitch + 4 * piece);
-      if (f > 0.f) {
-        v[0] += f * x.x;
-        v[1] += f * x.y;
-        v[2] += f * x.z;
-        v[3] += f * x.w;
-      }
+      const float2 s = sml[k * WR * 16 + at];
+      const float f = join_factor(s.x, m);
+      l += join_sum(s.y, f);
+      add_scaled(v, f, *reinterpret_cast<const float4*>(so + (k * WR * 16 + at) * SL::kPitch + 4 * piece));
     }
     if (alone) {
-      if (!failed) store(row, piece, m, l, v);
+      if (!failed) store4(a, w, w.r0 + row, D, piece, m, l, v);
     } else {
       *reinterpret_cast<float4*>(s_o + row * D + 4 * piece) = make_float4(v[0], v[1], v[2], v[3]);
       if (piece == 0) s_ml[row] = make_float4(m, l, 0.f, 0.f);
@@ -514,23 +636,17 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   if (!alone) {
     cluster_sync();
     const uint32_t o_addr = smem_u32(s_o), ml_addr = smem_u32(s_ml);
-    for (int i = split * kThreads + threadIdx.x; i < max(nr, 0) * kPieces; i += kThreads * a.splits) {
+    for (int i = split * kThreads + threadIdx.x; i < max(w.nr, 0) * kPieces; i += kThreads * a.splits) {
       const int row = i / kPieces, piece = i - row * kPieces;
       float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
       for (int k = 0; k < a.splits; ++k) m = fmaxf(m, ld_cluster(map_rank(ml_addr + 16 * row, k)).x);
       for (int k = 0; k < a.splits; ++k) {
         const float4 s = ld_cluster(map_rank(ml_addr + 16 * row, k));
-        const float f = s.x != -INFINITY ? ex2(s.x - m) : 0.f;
-        l += f > 0.f || s.y != s.y ? s.y * (f > 0.f ? f : 1.f) : 0.f;
-        if (f > 0.f) {
-          const float4 x = ld_cluster(map_rank(o_addr + 4 * (row * D + 4 * piece), k));
-          v[0] += f * x.x;
-          v[1] += f * x.y;
-          v[2] += f * x.z;
-          v[3] += f * x.w;
-        }
+        const float f = join_factor(s.x, m);
+        l += join_sum(s.y, f);
+        if (f > 0.f) add_scaled(v, f, ld_cluster(map_rank(o_addr + 4 * (row * D + 4 * piece), k)));
       }
-      if (!failed) store(row, piece, m, l, v);
+      if (!failed) store4(a, w, w.r0 + row, D, piece, m, l, v);
     }
     cluster_sync();  // no CTA leaves while another one reads its shared memory
   }
@@ -554,27 +670,36 @@ int splits_for(long long items, long long tiles, int rings, long long slots) {
   return best;
 }
 
+// CTAs that an SM holds of a kernel (found once).
+cudaError_t residency(const void* kernel, int bytes, std::atomic<int>* known, int* per_sm) {
+  *per_sm = known->load(std::memory_order_relaxed);
+  if (*per_sm != 0) return cudaSuccess;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, kThreads, bytes);
+  if (e != cudaSuccess) return e;
+  *per_sm = std::max(*per_sm, 1);
+  known->store(*per_sm, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+// Warps that share a ring, by the query rows.
+int warps_a_ring(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
 template <int SLABS, int WR, bool HALF>
 cudaError_t launch(DecodeArgs a, long long tiles, cudaStream_t s) {
+  const long long items = (long long)a.B * a.c.Hk * a.row_tiles;
   auto kernel = decode_kernel<SLABS, WR, HALF>;
   constexpr int bytes = DecodeSmem<SLABS, WR>::bytes;
   static std::atomic<uint64_t> done{0};
-  static std::atomic<int> resident{0};  // CTAs an SM holds
+  static std::atomic<int> known{0};
+  int per_sm;
   cudaError_t e = prepare_kernel((const void*)kernel, bytes, 0, &done);
+  if (e == cudaSuccess) e = residency((const void*)kernel, bytes, &known, &per_sm);
   if (e != cudaSuccess) return e;
-  int per_sm = resident.load(std::memory_order_relaxed);
-  if (per_sm == 0) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, bytes);
-    if (e != cudaSuccess) return e;
-    per_sm = std::max(per_sm, 1);
-    resident.store(per_sm, std::memory_order_relaxed);
-  }
-  const long long items = (long long)a.B * a.c.Hk * a.row_tiles;
-  a.splits = splits_for(items, tiles, kWarps / WR, (long long)device_sms() * per_sm);
-  if (items * a.splits > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const int grid = (int)(items * a.splits);
+  const long long slots = (long long)device_sms() * per_sm;
+  a.splits = splits_for(items, tiles, kWarps / WR, slots);
+  a.longest_first = a.B > 1 && a.B <= kThreads && items * a.splits > slots;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)(items * a.splits));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
@@ -589,8 +714,8 @@ cudaError_t launch(DecodeArgs a, long long tiles, cudaStream_t s) {
 }
 
 template <int SLABS>
-cudaError_t launch_rows(const DecodeArgs& a, int wr, bool half, long long tiles, cudaStream_t s) {
-  if (half) return launch<SLABS, 1, true>(a, tiles, s);
+cudaError_t launch_rows(const DecodeArgs& a, int wr, long long tiles, cudaStream_t s) {
+  if (a.Lq * a.G <= 8) return launch<SLABS, 1, true>(a, tiles, s);
   return wr == 1 ? launch<SLABS, 1, false>(a, tiles, s)
                  : wr == 2 ? launch<SLABS, 2, false>(a, tiles, s) : launch<SLABS, 4, false>(a, tiles, s);
 }
@@ -641,21 +766,20 @@ extern "C" df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, i
   a.kscale = (float)((double)scale * 1.4426950408889634);
   a.status = status;
   a.budget = wait_budget();
-  const int rows = Lq * a.G;
-  const int wr = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  a.row_tiles = (rows + 16 * wr - 1) / (16 * wr);
+  const int wr = warps_a_ring(Lq * a.G);
+  a.row_tiles = (Lq * a.G + 16 * wr - 1) / (16 * wr);
   if ((long long)B * Hk * a.row_tiles > 0x7fffffffll / 8) return DF_ERR_UNSUPPORTED;
+  const int keys = (d <= 64 ? kTileBlocks<2> : kTileBlocks<4>) * kBlock;
   // the tokens that a tile of rows sees at most, in tiles
-  long long tiles = ((long long)std::min<long long>(max_length, (long long)max_pages * page) + kTile - 1) / kTile;
-  if (window > 0) tiles = std::min<long long>(tiles, ((long long)window + Lq + sinks) / kTile + 3);
+  long long tiles = (std::min<long long>(max_length, (long long)max_pages * page) + keys - 1) / keys;
+  if (window > 0) tiles = std::min<long long>(tiles, ((long long)window + Lq + sinks) / keys + 3);
   cudaStream_t s = (cudaStream_t)stream;
-  const bool half = rows <= 8;
   cudaError_t e;
   switch (d / 32) {
-    case 1: e = launch_rows<1>(a, wr, half, tiles, s); break;
-    case 2: e = launch_rows<2>(a, wr, half, tiles, s); break;
-    case 3: e = launch_rows<3>(a, wr, half, tiles, s); break;
-    default: e = launch_rows<4>(a, wr, half, tiles, s); break;
+    case 1: e = launch_rows<1>(a, wr, tiles, s); break;
+    case 2: e = launch_rows<2>(a, wr, tiles, s); break;
+    case 3: e = launch_rows<3>(a, wr, tiles, s); break;
+    default: e = launch_rows<4>(a, wr, tiles, s); break;
   }
   return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }

@@ -687,7 +687,7 @@ df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t*
  * as fp16 times 2^14 (11 bits down to 2^-28 of a row's largest).  Tokens that no query of the
  * call sees may hold anything (as may what lies behind the last token in its page); a NaN that a
  * query sees makes results NaN, also those of the call's other queries of that sequence.
- * No atomics, no workspace: equal inputs give equal bits.  Made for up to some 64 rows (Lq H / Hk)
+ * No atomics, no workspace: equal inputs (max_length among them) give equal bits.  Made for up to some 64 rows (Lq H / Hk)
  * a sequence and key head, which are read once; for long prompts read the tokens back
  * (df_cache_read) and use df_self_attn_fwd. */
 df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, int B, int H, int Hk, int Lq,

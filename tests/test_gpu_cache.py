@@ -105,6 +105,10 @@ def test_missing_pages_and_bad_lengths_are_reported(lib):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         out = lib.df_cache_attn(q, cache, t, held, status=status)
         assert int(status.item()) == lib.DF_ERR_INVALID_ARG
+        status.zero_()
+        wide = torch.cat([t, torch.full((3, 20000), bad, dtype=torch.int32, device="cuda")], dim=1)
+        assert bool(((lib.df_cache_attn(q, cache, wide, held, status=status).float() - out.float()).abs() <= 2.0 ** -6).all())
+        assert int(status.item()) == lib.DF_ERR_INVALID_ARG
         assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]) and bool(torch.isfinite(out).all())
         # the tokens of the missing page do not count
         want = oracles(calls, heads, d)[1]
@@ -194,19 +198,38 @@ def test_attention_matches_oracle(lib, B, H, Hk, d, Lq, page, longest, dtype, ca
     assert got is out
     w = want_attn(np64(q).reshape(-1, H, d), lens, [Lq] * B, both, causal, window, sinks, d ** -0.5)
     check_forward(out.view(-1, H, d), w, dtype, d, lse.view(-1, H))
-    assert torch.equal(lib.df_cache_attn(q.cuda(), cache, table, held, max_length=longest, **kw),
-                       lib.df_cache_attn(q.cuda(), cache, table, held, max_length=longest, **kw))
+    # another split (which goes by the room in the table)
+    wide = torch.cat([table, torch.full((B, 330_000 // page), -1, dtype=torch.int32, device="cuda")], dim=1)
+    out, lse = torch.full((B, Lq, H, d), float("nan"), dtype=dtype, device="cuda"), torch.zeros(B, Lq, H, device="cuda")
+    got = lib.df_cache_attn(q.cuda(), cache, wide, held, out=out, lse=lse, **kw)
+    check_forward(out.view(-1, H, d), w, dtype, d, lse.view(-1, H))
+    for t in (table, wide):
+        assert torch.equal(lib.df_cache_attn(q.cuda(), cache, t, held, **kw), lib.df_cache_attn(q.cuda(), cache, t, held, **kw))
     # packed, ragged, with rows behind the last sequence; another scale
     nq = [min(Lq, 1 + (3 * b) % (Lq + 1)) for b in range(B)]
     if B > 1:
         nq[-1] = 0
     x = torch.randn(sum(nq) + 3, H, d, generator=g).to(dtype)
-    out = torch.full_like(x, 7.0).cuda()
-    lib.df_cache_attn(x.cuda(), cache, table, held, offsets(nq).cuda(), max_seqlen_q=Lq, scale=0.31, out=out, **kw)
     w = want_attn(np64(x), lens, nq, both, causal, window, sinks, float(np.float32(0.31)))
-    check_forward(out[:sum(nq)], w, dtype, d)
-    assert int((out[sum(nq):] != 7.0).sum()) == 0
+    for t in (table, wide):
+        out = torch.full_like(x, 7.0).cuda()
+        lib.df_cache_attn(x.cuda(), cache, t, held, offsets(nq).cuda(), max_seqlen_q=Lq, scale=0.31, out=out, **kw)
+        check_forward(out[:sum(nq)], w, dtype, d)
+        assert int((out[sum(nq):] != 7.0).sum()) == 0
     assert int(status.item()) == lib.DF_OK
+
+
+@pytest.mark.parametrize("B,H,Hk,d,Lq,page,longest,dtype,causal,window,sinks", [
+    (30, 8, 8, 64, 1, 64, 1500, BF, True, 0, 0), (256, 4, 4, 32, 1, 16, 400, HF, True, 0, 0),
+    (20, 16, 4, 128, 4, 16, 4000, BF, True, 1000, 20), (12, 16, 8, 96, 9, 32, 4100, HF, False, 0, 0)])
+def test_more_work_than_a_round_of_the_gpu(lib, B, H, Hk, d, Lq, page, longest, dtype, causal, window, sinks):
+    lens = sequences(B, longest, Lq, seed=B)
+    calls = tokens([lens], Hk, d, dtype, seed=B)
+    cache, table, held = fill(lib, calls, Hk, d, page)
+    q = torch.randn(B, Lq, H, d, generator=torch.Generator().manual_seed(B)).to(dtype)
+    got = lib.df_cache_attn(q.cuda(), cache, table, held, causal=causal, window=window, sinks=sinks)
+    w = want_attn(np64(q).reshape(-1, H, d), lens, [Lq] * B, oracles(calls, Hk, d), causal, window, sinks, d ** -0.5)
+    check_forward(got.view(-1, H, d), w, dtype, d)
 
 
 def test_split_by_any_bound_of_the_length(lib):
@@ -215,6 +238,7 @@ def test_split_by_any_bound_of_the_length(lib):
     both = oracles(calls, 2, 64)
     q = torch.randn(1, 1, 4, 64, generator=torch.Generator().manual_seed(5)).to(BF)
     w = want_attn(np64(q)[0], [3000], [1], both, True, 0, 0, 0.125)
+    table = torch.cat([table, torch.full((1, 6000), -1, dtype=torch.int32, device="cuda")], dim=1)
     for bound in (0, 1, 200, 600, 3000, 1 << 20):
         check_forward(lib.df_cache_attn(q.cuda(), cache, table, held, max_length=bound)[0], w, BF, 64)
 
