@@ -6,8 +6,10 @@
 // scale: the codes that it holds are halved as often as the scale doubles, which changes
 // nothing above e4m3's subnormals.
 //
-// A warp takes the keys or the values of one block and head: 4 lanes a token's 32 columns, 8
-// tokens at a time, so that its loads are 64-byte runs and its stores 256-byte ones.  HBM bound.
+// A warp takes the keys or the values of one block and head at a time, several one after another
+// where there is much to do (what it costs to find a block is then paid once for them): 4 lanes a
+// token's 32 columns, 8 tokens at a time, so that its loads are 64-byte runs and its stores
+// 256-byte ones.  HBM bound.
 #include <math.h>
 
 #include <algorithm>
@@ -23,6 +25,7 @@ struct StoreArgs {
   const int32_t* cu;  // [B + 1], or NULL: `len` rows of each sequence
   int B, len, total;
   long long slots;    // blocks that warps look for, over all sequences
+  int pairs, warps;   // of the 2 Hk (head, keys or values) of a block: those that a warp takes, warps a block
   int32_t* status;
 };
 
@@ -60,21 +63,74 @@ __device__ __forceinline__ float inverse_scale(float s) { return __uint_as_float
 
 __device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) <= 3.4028235e38f ? x : __uint_as_float(0x7fffffffu); }
 
+// The larger magnitudes of two pairs (a NaN gives way to the other).
+__device__ __forceinline__ __nv_bfloat162 top2(__nv_bfloat162 m, __nv_bfloat162 x) { return __hmax2(m, __habs2(x)); }
+__device__ __forceinline__ __half2 top2(__half2 m, __half2 x) { return __hmax2(m, __habs2(x)); }
+template <typename T>
+using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+
+// Eight values times inv, a power of two, as codes; infinities as NaN.
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
+  const T* e = reinterpret_cast<const T*>(&v);
+  uint16_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = f32_codes(finite_or_nan(IO<T>::to_f(e[2 * i])) * inv, finite_or_nan(IO<T>::to_f(e[2 * i + 1])) * inv);
+  return make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+}
+// The same for values without an infinity, fewer instructions.  Products of 16-bit values with a
+// power of two are exact where they matter: what leaves the normal range is far below half of
+// the smallest code.  fp16: inv must be one, 2^-16 .. 2^15.
+__device__ __forceinline__ uint2 finite_codes8(const uint4& v, __nv_bfloat162 inv) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint16_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), inv);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
+    w[i] = f32_codes(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  return make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+}
+__device__ __forceinline__ uint2 finite_codes8(const uint4& v, __half2 inv) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint16_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[i]), inv);
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(w[i]) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+  }
+  return make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+}
+__device__ __forceinline__ __nv_bfloat162 both(float x, __nv_bfloat162) { return __float2bfloat162_rn(x); }
+__device__ __forceinline__ __half2 both(float x, __half2) { return __float2half2_rn(x); }
+
+// A warp's block and its first (head, keys or values): false behind the last one.
+__device__ __forceinline__ bool warp_block(const StoreArgs& a, long long* slot, int* pair) {
+  const unsigned id = blockIdx.x * 8u + (threadIdx.x >> 5);  // (below 2^31)
+  const unsigned at = id / (unsigned)a.warps;
+  *slot = at;
+  *pair = (int)(id - at * a.warps) * a.pairs;
+  return *slot < a.slots;
+}
+// Each sequence is looked over once.
+__device__ __forceinline__ void look_over(const StoreArgs& a, long long slot, int pair) {
+  if (slot >= a.B || pair != 0 || (threadIdx.x & 31) != 0) return;
+  const CrossSide rows = {a.cu, a.len, a.total};
+  int at;
+  seq_rows(rows, (int)slot, a.status, &at);
+  if (a.c.lengths[slot] < 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
+}
+
 template <typename T, int SLABS>
 __global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
+  constexpr int D = 32 * SLABS;
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int which = (int)(item & 1);
-  const long long rest = item >> 1;
-  const int head = (int)(rest % a.c.Hk);
-  const long long slot = rest / a.c.Hk;
-  if (slot >= a.slots) return;
-  if (slot < a.B && head == 0 && which == 0 && lane == 0) {  // each sequence is looked over once
-    const CrossSide rows = {a.cu, a.len, a.total};
-    int at;
-    seq_rows(rows, (int)slot, a.status, &at);
-    if (a.c.lengths[slot] < 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
-  }
+  long long slot;
+  int pair;
+  if (!warp_block(a, &slot, &pair)) return;
+  look_over(a, slot, pair);
   const int b = sequence_of(a, a.B, slot);
   if (b >= a.B) return;
   const CrossSide rows = {a.cu, a.len, a.total};
@@ -91,63 +147,89 @@ __global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
     if (lane == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
     return;
   }
-  uint8_t* rec = record_of(a.c, id, head, blk);
-  uint8_t* codes = rec + 16 * a.c.d * which;
-  float* scale_at = reinterpret_cast<float*>(rec + 32 * a.c.d + 4 * which);
-  const T* x = static_cast<const T*>(which ? a.v : a.k) +
-               ((long long)(first + (long long)blk * kBlock - held) * a.c.Hk + head) * a.c.d;  // the block's token 0
-  const int piece = lane & 3;
-  uint4 v[2 * SLABS];
+  const int piece = lane & 3, row0 = lane >> 2;
+  const long long step = (long long)a.c.Hk * D;  // elements from token to token
+  const long long base = (first + (long long)blk * kBlock - held + row0) * step + 8 * piece;  // the lane's, in head 0
+  const size_t stride = (size_t)(a.c.page / kBlock) * record_bytes(D);  // from head to head of a page
+  uint8_t* rec0 = record_of(a.c, id, 0, blk);
+  const int last = min(pair + a.pairs, 2 * a.c.Hk);
+#pragma unroll 1
+  for (int p = pair; p < last; ++p) {
+    const int which = p & 1, head = p >> 1;
+    uint8_t* rec = rec0 + head * stride;
+    uint8_t* codes = rec + 16 * D * which + 32 * row0 + 8 * piece;
+    float* scale_at = reinterpret_cast<float*>(rec + 32 * D + 4 * which);
+    const T* x = static_cast<const T*>(which ? a.v : a.k) + base + head * D;
+    uint4 v[2 * SLABS];
 #pragma unroll
-  for (int j = 0; j < 2 * SLABS; ++j) {
-    const int row = (lane >> 2) + 8 * (j & 1);
-    v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= from && row < to)
-      v[j] = *reinterpret_cast<const uint4*>(x + (long long)row * a.c.Hk * a.c.d + 32 * (j >> 1) + 8 * piece);
-  }
-  float top = 0.f;
-#pragma unroll
-  for (int j = 0; j < 2 * SLABS; ++j) {
-    const T* e = reinterpret_cast<const T*>(&v[j]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = fabsf(IO<T>::to_f(e[i]));
-      if (f <= 3.4028235e38f) top = fmaxf(top, f);
+    for (int j = 0; j < 2 * SLABS; ++j) {
+      const int row = row0 + 8 * (j & 1);
+      v[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (row >= from && row < to) v[j] = *reinterpret_cast<const uint4*>(x + (j & 1 ? 8 * step : 0) + 32 * (j >> 1));
     }
-  }
-  float s = block_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
-  float grown = 1.f;  // old scale / new scale
-  if (from > 0) {
-    const float old = *scale_at;
-    s = fmaxf(s, old);
-    grown = old * inverse_scale(s);
-  }
-  const float inv = inverse_scale(s);
-  __syncwarp();  // every lane has read the scale
+    Pair<T> m2 = both(0.f, Pair<T>());
 #pragma unroll
-  for (int j = 0; j < 2 * SLABS; ++j) {
-    const int row = (lane >> 2) + 8 * (j & 1);
-    uint2* at = reinterpret_cast<uint2*>(codes + 512 * (j >> 1) + 32 * row + 8 * piece);
-    uint16_t w[4];
-    if (row >= from && row < to) {
-      const T* e = reinterpret_cast<const T*>(&v[j]);
+    for (int j = 0; j < 2 * SLABS; ++j) {
+      const Pair<T>* e = reinterpret_cast<const Pair<T>*>(&v[j]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = f32_codes(finite_or_nan(IO<T>::to_f(e[2 * i])) * inv, finite_or_nan(IO<T>::to_f(e[2 * i + 1])) * inv);
-    } else if (row < from && grown != 1.f) {
-      const uint2 kept = *at;
+      for (int i = 0; i < 4; ++i) m2 = top2(m2, e[i]);
+    }
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(&m2);
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));  // (magnitudes: in order)
+    const uint16_t half_bits = (uint16_t)bits;
+    float top = IO<T>::to_f(*reinterpret_cast<const T*>(&half_bits));
+    const bool finite = top <= 3.4028235e38f;
+    if (!finite) {  // an infinity among them: the largest of the others
+      top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t h = codes_f16((uint16_t)((i < 2 ? kept.x : kept.y) >> (16 * (i & 1))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        w[i] = f32_codes(f.x * grown, f.y * grown);
+      for (int j = 0; j < 2 * SLABS; ++j) {
+        const T* e = reinterpret_cast<const T*>(&v[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = fabsf(IO<T>::to_f(e[i]));
+          if (f <= 3.4028235e38f) top = fmaxf(top, f);
+        }
       }
-    } else {
-      continue;
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     }
-    *at = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+    float s = block_scale(top);
+    float grown = 1.f;  // old scale / new scale
+    if (from > 0) {
+      const float old = *scale_at;
+      s = fmaxf(s, old);
+      grown = old * inverse_scale(s);
+    }
+    const float inv = inverse_scale(s);
+    __syncwarp();  // every lane has read the scale
+    auto code_of = [&](int j) { return reinterpret_cast<uint2*>(codes + 512 * (j >> 1) + 256 * (j & 1)); };
+    const bool plain = finite && (!std::is_same<T, __half>::value || (inv >= 1.52587890625e-5f && inv <= 32768.f));
+    if (plain) {
+      const Pair<T> inv2 = both(inv, Pair<T>());
+#pragma unroll
+      for (int j = 0; j < 2 * SLABS; ++j)
+        if (row0 + 8 * (j & 1) >= from && row0 + 8 * (j & 1) < to) *code_of(j) = finite_codes8(v[j], inv2);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2 * SLABS; ++j)
+        if (row0 + 8 * (j & 1) >= from && row0 + 8 * (j & 1) < to) *code_of(j) = codes8<T>(v[j], inv);
+    }
+    if (from > 0 && grown != 1.f) {  // the block's scale has grown: its older codes again
+#pragma unroll 1
+      for (int j = 0; j < 2 * SLABS; ++j) {
+        if (row0 + 8 * (j & 1) >= from) continue;
+        const uint2 kept = *code_of(j);
+        uint16_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t h = codes_f16((uint16_t)((i < 2 ? kept.x : kept.y) >> (16 * (i & 1))));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          w[i] = f32_codes(f.x * grown, f.y * grown);
+        }
+        *code_of(j) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+      }
+    }
+    if (lane == 0) *scale_at = s;
   }
-  if (lane == 0) *scale_at = s;
 }
 
 template <typename T>
@@ -158,24 +240,18 @@ __device__ __forceinline__ T rounded(float f) {
 
 template <typename T, int SLABS>
 __global__ void __launch_bounds__(256) read_kernel(const StoreArgs a) {
+  constexpr int D = 32 * SLABS;
   const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int which = (int)(item & 1);
-  const long long rest = item >> 1;
-  const int head = (int)(rest % a.c.Hk);
-  const long long slot = rest / a.c.Hk;
-  if (slot >= a.slots) return;
-  const CrossSide rows = {a.cu, a.len, a.total};
-  int first;
-  if (slot < a.B && head == 0 && which == 0 && lane == 0) {
-    seq_rows(rows, (int)slot, a.status, &first);
-    if (a.c.lengths[slot] < 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
-  }
+  long long slot;
+  int pair;
+  if (!warp_block(a, &slot, &pair)) return;
+  look_over(a, slot, pair);
   // (packed: the rows behind the last sequence count as one more, which holds nothing)
   const int seqs = a.cu ? a.B + 1 : a.B;
   const int b = sequence_of(a, seqs, slot);
   if (b >= seqs) return;
-  int n, held = 0;
+  const CrossSide rows = {a.cu, a.len, a.total};
+  int first, n, held = 0;
   if (b < a.B) {
     n = seq_rows(rows, b, nullptr, &first);
     held = max(a.c.lengths[b], 0);
@@ -187,50 +263,62 @@ __global__ void __launch_bounds__(256) read_kernel(const StoreArgs a) {
   if ((long long)blk * kBlock >= n) return;
   const int here = min(kBlock, n - blk * kBlock);  // rows of the block,
   int left = min(held - blk * kBlock, here);       // of which the cache holds these
-  const uint8_t* rec = nullptr;
+  int id = 0;
   if (left > 0) {
-    const int id = page_of(a.c, b, blk);
+    id = page_of(a.c, b, blk);
     if (id < 0) {
       if (lane == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
       left = 0;
-    } else {
-      rec = record_of(a.c, id, head, blk);
     }
   }
-  const float s = rec ? *reinterpret_cast<const float*>(rec + 32 * a.c.d + 4 * which) : 0.f;
-  T* y = static_cast<T*>(which ? a.v : a.k) + ((long long)(first + (long long)blk * kBlock) * a.c.Hk + head) * a.c.d;
-  const int piece = lane & 3;
-  uint2 v[2 * SLABS];
+  const int piece = lane & 3, row0 = lane >> 2;
+  const long long step = (long long)a.c.Hk * D;
+  const long long base = (first + (long long)blk * kBlock + row0) * step + 8 * piece;
+  const size_t stride = (size_t)(a.c.page / kBlock) * record_bytes(D);
+  const uint8_t* rec0 = left > 0 ? record_of(a.c, id, 0, blk) : nullptr;
+  const int last = min(pair + a.pairs, 2 * a.c.Hk);
+#pragma unroll 1
+  for (int p = pair; p < last; ++p) {
+    const int which = p & 1, head = p >> 1;
+    const uint8_t* rec = rec0 + head * stride;
+    T* y = static_cast<T*>(which ? a.v : a.k) + base + head * D;
+    float s = 0.f;
+    uint2 v[2 * SLABS];
 #pragma unroll
-  for (int j = 0; j < 2 * SLABS; ++j) {
-    const int row = (lane >> 2) + 8 * (j & 1);
-    v[j] = make_uint2(0u, 0u);
-    if (row < left) v[j] = *reinterpret_cast<const uint2*>(rec + 16 * a.c.d * which + 512 * (j >> 1) + 32 * row + 8 * piece);
-  }
-#pragma unroll
-  for (int j = 0; j < 2 * SLABS; ++j) {
-    const int row = (lane >> 2) + 8 * (j & 1);
-    if (row >= here) continue;
-    alignas(16) T e[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t h = codes_f16((uint16_t)((i < 2 ? v[j].x : v[j].y) >> (16 * (i & 1))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      e[2 * i] = rounded<T>(row < left ? f.x * s : 0.f);
-      e[2 * i + 1] = rounded<T>(row < left ? f.y * s : 0.f);
+    for (int j = 0; j < 2 * SLABS; ++j) {
+      v[j] = make_uint2(0u, 0u);
+      if (row0 + 8 * (j & 1) < left)
+        v[j] = *reinterpret_cast<const uint2*>(rec + 16 * D * which + 512 * (j >> 1) + 256 * (j & 1) + 32 * row0 + 8 * piece);
     }
-    uint4* at = reinterpret_cast<uint4*>(y + (long long)row * a.c.Hk * a.c.d + 32 * (j >> 1) + 8 * piece);
+    if (left > 0) s = *reinterpret_cast<const float*>(rec + 32 * D + 4 * which);
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) at[i] = reinterpret_cast<const uint4*>(e)[i];
+    for (int j = 0; j < 2 * SLABS; ++j) {
+      const int row = row0 + 8 * (j & 1);
+      if (row >= here) continue;
+      alignas(16) T e[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t h = codes_f16((uint16_t)((i < 2 ? v[j].x : v[j].y) >> (16 * (i & 1))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        e[2 * i] = rounded<T>(row < left ? f.x * s : 0.f);
+        e[2 * i + 1] = rounded<T>(row < left ? f.y * s : 0.f);
+      }
+      uint4* at = reinterpret_cast<uint4*>(y + (j & 1 ? 8 * step : 0) + 32 * (j >> 1));
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) at[i] = reinterpret_cast<const uint4*>(e)[i];
+    }
   }
 }
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <bool READ, typename T>
-cudaError_t launch(const StoreArgs& a, cudaStream_t s) {
-  const long long warps = a.slots * a.c.Hk * 2, blocks = (warps + 7) / 8;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+cudaError_t launch(StoreArgs a, cudaStream_t s) {
+  // one pair a warp where there are few, up to eight while some 2^16 warps are left
+  a.pairs = (int)std::min<long long>(8, std::max<long long>(1, a.slots * a.c.Hk * 2 >> 16));
+  a.warps = (2 * a.c.Hk + a.pairs - 1) / a.pairs;
+  const long long blocks = (a.slots * a.warps + 7) / 8;
+  if (blocks > 0x7fffffffll / 8) return cudaErrorInvalidConfiguration;
   void (*kernel)(StoreArgs) = nullptr;
   switch (a.c.d / 32) {
     case 1: kernel = READ ? read_kernel<T, 1> : append_kernel<T, 1>; break;

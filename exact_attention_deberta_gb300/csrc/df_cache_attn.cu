@@ -34,10 +34,9 @@ namespace {
 using namespace ptx;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-// Blocks of a tile, the keys of one copy: four where rows are short, so that what a tile costs
-// beside its products is paid less often.
-template <int SLABS>
-constexpr int kTileBlocks = SLABS <= 2 ? 4 : 2;
+// A tile is the keys of one copy: two blocks.  (Four at d = 64: 166 us where two take 160, for 24
+// heads and 64 requests of up to 8192 tokens; one at d = 128: the same as two.)
+constexpr int NB = 2, kKeys = NB * kBlock;
 constexpr float kUp = 14.f;
 
 struct DecodeArgs {
@@ -47,6 +46,7 @@ struct DecodeArgs {
   void* out;
   float* lse;           // or NULL
   int B, H, G, Lq, Tq;
+  unsigned by_G;        // 65536 / G + 1
   int row_tiles;        // CTAs that share a sequence's query rows
   int splits;           // and its keys (cluster size)
   int longest_first;    // (at most kThreads sequences)
@@ -60,9 +60,9 @@ template <int SLABS, int WR>
 struct DecodeSmem {
   static constexpr int D = 32 * SLABS;
   static constexpr int kRings = kWarps / WR;
-  static constexpr int kStages = SLABS == 1 ? 4 : 2;
+  static constexpr int kStages = SLABS == 1 ? 6 : SLABS == 2 ? 3 : 2;
   static constexpr uint32_t kRecord = 32 * D + 16;
-  static constexpr uint32_t kStageBytes = kTileBlocks<SLABS> * kRecord;
+  static constexpr uint32_t kStageBytes = NB * kRecord;
   static constexpr uint32_t ring = 0;  // [kRings][kStages][records of a tile]
   static constexpr uint32_t ring_bytes = kRings * kStages * kStageBytes;
   // after the loop, over the ring: each warp's O, and the CTA's
@@ -74,7 +74,9 @@ struct DecodeSmem {
   static constexpr uint32_t ml_cta = ml_warp + kWarps * 16 * 8;                     // float4 [16 WR]
   static constexpr uint32_t bars = ml_cta + 64 * 16;                                // full, empty [kRings][kStages]
   static constexpr uint32_t have = bars + 2 * kRings * kStages * 8;                 // int [kRings][kStages]
-  static constexpr uint32_t misc = have + kRings * kStages * 4;
+  static constexpr uint32_t recs = (have + kRings * kStages * 4 + 7) & ~7u;  // 64-bit [kRings][32 tiles][blocks]: records to copy
+  static constexpr uint32_t reach = recs + kRings * 32 * NB * 8;
+  static constexpr uint32_t misc = reach + 32;
   static constexpr uint32_t bytes = (misc + 4 + 15) & ~15u;
   static_assert(bytes <= 232448 && o_cta % 16 == 0 && joined % 16 == 0 && ml_warp % 16 == 0 && bars % 8 == 0, "layout");
 };
@@ -115,34 +117,38 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, unsigned long long src, 
 }
 
 // The tokens that a tile of query rows, at positions p0 .. p1, sees: those before `head` and
-// those from lo to end - 1; in tiles of N keys, the first `heads` and then those from `skip`
+// those from lo to end - 1; in tiles of kKeys, the first `heads` and then those from `skip`
 // tiles further on.
-template <int N>
 struct Reach {
   int head, lo, end, heads, skip, tiles;
-  __device__ __forceinline__ int key(int t) const { return (t < heads ? t : t + skip) * N; }  // the tile's first
   __device__ __forceinline__ bool any(int first, int n) const {
     return first < end && (first < head || first + n > lo);
   }
 };
-template <int N>
-__device__ __forceinline__ Reach<N> reach_of(const DecodeArgs& a, int held, int p0, int p1) {
-  Reach<N> r;
+__device__ __forceinline__ Reach reach_of(const DecodeArgs& a, int held, int p0, int p1) {
+  Reach r;
   r.end = a.causal ? max(min(held, p1 + 1), 0) : held;
   r.lo = a.causal && a.window != 0 ? max(p0 - a.window + 1, 0) : 0;
   r.lo = min(r.lo, r.end);
   r.head = min(a.sinks, r.lo);
-  r.heads = (r.head + N - 1) / N;
-  r.skip = max(r.lo / N - r.heads, 0);
-  r.tiles = (r.end + N - 1) / N - r.skip;
+  r.heads = (r.head + kKeys - 1) / kKeys;
+  r.skip = max(r.lo / kKeys - r.heads, 0);
+  r.tiles = (r.end + kKeys - 1) / kKeys - r.skip;
   return r;
 }
 
 // The query rows of a CTA or worker and what they see.
 struct Rows {
-  int b, hk, r0, rows, nr;      // rows r0 .. r0 + nr - 1 of the sequence's `rows`: token r / G, head r % G
-  int q0, held, p_first;        // the sequence's first query row and its position; tokens held
-  int p0, p1;                   // positions of the first and the last of these rows
+  int b, hk, nr;     // `nr` rows, token by token and head by head within the key head's G
+  int t0, h0;        // the first one's token (of the sequence's queries) and head
+  int q0, held;      // the sequence's first row of q; tokens held
+  int p0, p1;        // positions of the first and the last row
+  // Row i: its token, counted from t0, and its head
+  __device__ __forceinline__ void place(const DecodeArgs& a, int i, int* token, int* head) const {
+    const int x = h0 + i;  // below 192: the product is exact
+    *token = (int)((unsigned)x * a.by_G >> 16);
+    *head = x - *token * a.G;
+  }
 };
 // A sequence's queries and tokens, as far as they can be believed (`tell`: what cannot is reported).
 __device__ __forceinline__ void sequence(const DecodeArgs& a, int b, bool tell, int* q0, int* nq, int* held) {
@@ -160,23 +166,43 @@ __device__ __forceinline__ Rows rows_of(const DecodeArgs& a, int b, int hk, int 
   sequence(a, b, tell, &w.q0, &nq, &w.held);
   w.b = b;
   w.hk = hk;
-  w.rows = nq * a.G;
-  w.r0 = rt * per_tile;
-  w.nr = min(per_tile, w.rows - w.r0);
-  w.p_first = w.held - nq;
-  w.p0 = w.p_first + w.r0 / a.G;
-  w.p1 = w.p_first + (w.r0 + max(w.nr, 1) - 1) / a.G;
+  w.nr = min(per_tile, nq * a.G - rt * per_tile);
+  w.t0 = rt * per_tile / a.G;
+  w.h0 = rt * per_tile - w.t0 * a.G;
+  w.p0 = w.held - nq + w.t0;
+  int last, head;
+  w.place(a, max(w.nr, 1) - 1, &last, &head);
+  w.p1 = w.p0 + last;
   return w;
 }
 
-// The record of the block at token `key`, 0 where nothing is to be copied.
-template <int N>
-__device__ __forceinline__ unsigned long long record_at(const DecodeArgs& a, const Reach<N>& reach, int b, int hk, int key) {
-  if (!reach.any(key, kBlock)) return 0;
-  const int id = page_of(a.c, b, key / kBlock);
-  if (id >= 0) return (unsigned long long)record_of(a.c, id, hk, key / kBlock);
-  cross_fail(a.status, (int)DF_ERR_INVALID_ARG);  // tokens without a page
-  return 0;
+// The records of the NB blocks from token `key` on (a multiple of 16), 0 where nothing is to be
+// copied: blocks of which no token is seen, and those without a page.
+__device__ __forceinline__ void records_at(const DecodeArgs& a, const Reach& reach, int b, int hk, int key,
+                                           unsigned long long (&rec)[NB]) {
+  const unsigned per = (unsigned)a.c.page / kBlock;
+  unsigned at = (unsigned)key / kBlock / per, in = (unsigned)key / kBlock - at * per;
+  unsigned long long first = 0;  // the page's first record of the head
+  bool looked = false;
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    rec[k] = 0;
+    if (reach.any(key + k * kBlock, kBlock)) {
+      if (!looked) {
+        const int id = at < (unsigned)a.c.max_pages ? a.c.pages[(size_t)b * a.c.max_pages + at] : -1;
+        const bool good = (unsigned)id < (unsigned)a.c.n_pages;
+        if (!good) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);  // tokens without a page
+        first = good ? (unsigned long long)(a.c.base + ((size_t)id * a.c.Hk + hk) * per * record_bytes(a.c.d)) : 0;
+        looked = true;
+      }
+      if (first != 0) rec[k] = first + (unsigned long long)in * record_bytes(a.c.d);
+    }
+    if (++in == per) {
+      in = 0;
+      ++at;
+      looked = false;
+    }
+  }
 }
 
 // Key i of lane t's four in a block.
@@ -185,7 +211,7 @@ __device__ __forceinline__ int key_of(int t, int i) { return 4 * i + ((t + 2 * (
 // A warp's 16 query rows and their running state; HALF: the upper 8 are empty.
 template <int SLABS, bool HALF>
 struct Softmax {
-  static constexpr int D = 32 * SLABS, kHalves = HALF ? 1 : 2, NB = kTileBlocks<SLABS>, kKeys = NB * kBlock;
+  static constexpr int D = 32 * SLABS, kHalves = HALF ? 1 : 2;
   static constexpr uint32_t kRecord = 32 * D + 16;
   int whole_from, whole_to;  // tiles that begin in between have no key that a row does not see
   uint32_t qa[SLABS][2][4];  // the rows as fp16, operands of the scores
@@ -201,16 +227,18 @@ struct Softmax {
     whole_from = a.causal && a.window != 0 ? w.p1 - a.window + 1 : 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = w.r0 + 16 * part + g + 8 * h;
-      const bool in = r < w.rows && h < kHalves;
-      pos[h] = in ? w.p_first + r / a.G : INT_MIN;
+      const int i = 16 * part + g + 8 * h;
+      const bool in = i < w.nr && h < kHalves;
+      int token = 0, head = 0;
+      if (in) w.place(a, i, &token, &head);
+      pos[h] = in ? w.p0 + token : INT_MIN;
       ks_row[h] = a.kscale;
       m_run[h] = -INFINITY;
       l_run[h] = 0.f;
       uint4 v[SLABS];
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(a.q) +
-          ((size_t)(w.q0 + (in ? r / a.G : 0)) * a.H + (size_t)w.hk * a.G + (in ? r % a.G : 0)) * D + 8 * t);
+          ((size_t)(w.q0 + w.t0 + token) * a.H + w.hk * a.G + head) * D + 8 * t);
 #pragma unroll
       for (int c = 0; c < SLABS; ++c) v[c] = in ? src[4 * c] : make_uint4(0u, 0u, 0u, 0u);
       if (a.bf16) {
@@ -251,8 +279,8 @@ struct Softmax {
   }
 
   // One tile: its records at `base` (shared memory), of which those in `here` were copied.
-  __device__ __forceinline__ void tile(const DecodeArgs& a, const Rows& w, const Reach<kKeys>& reach, uint32_t base,
-                                       int first_key, int here) {
+  __device__ __forceinline__ void tile(const DecodeArgs& a, const Reach* reach, uint32_t base, int first_key,
+                                       int here) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // every key of the tile counts for every row
     const bool whole = here == (1 << NB) - 1 && first_key <= whole_to &&
@@ -297,7 +325,7 @@ struct Softmax {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int key = first_key + kBlock * blk + key_of(t, 2 * j + x);
-            const bool there = (here >> blk) & 1 && reach.any(key, 1);
+            const bool there = (here >> blk) & 1 && reach->any(key, 1);
             if (!there) gone |= 1u << (4 * blk + 2 * j + x);
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
@@ -352,6 +380,7 @@ struct Softmax {
     }
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
+      __syncwarp();  // (keeps the next block's loads, and so their registers, behind this one's products)
       const uint32_t rec = base + blk * kRecord + 16 * D + 4 * g;
 #pragma unroll
       for (int c = 0; c < SLABS; ++c) {
@@ -413,12 +442,14 @@ __device__ __forceinline__ void add_scaled(float (&v)[4], float f, const float4&
   v[3] += f * x.w;
 }
 
-// Four columns of query row r (of its sequence), divided by the row's sum and rounded; the first
+// Four columns of query row i, divided by the row's sum and rounded; the first
 // ones bring lse.
-__device__ __forceinline__ void store4(const DecodeArgs& a, const Rows& w, int r, int D, int piece, float m, float l,
+__device__ __forceinline__ void store4(const DecodeArgs& a, const Rows& w, int i, int D, int piece, float m, float l,
                                        const float (&v)[4]) {
   const float inv = l != 0.f ? rcp(l) : 0.f;  // (a NaN stays one)
-  const size_t at = (size_t)(w.q0 + r / a.G) * a.H + (size_t)w.hk * a.G + r % a.G;
+  int token, head;
+  w.place(a, i, &token, &head);
+  const size_t at = (size_t)(w.q0 + w.t0 + token) * a.H + w.hk * a.G + head;
   const uint32_t lo = a.bf16 ? pack_bf16x2(v[0] * inv, v[1] * inv) : pack_f16x2(v[0] * inv, v[1] * inv);
   const uint32_t hi = a.bf16 ? pack_bf16x2(v[2] * inv, v[3] * inv) : pack_f16x2(v[2] * inv, v[3] * inv);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * piece) = make_uint2(lo, hi);
@@ -426,58 +457,50 @@ __device__ __forceinline__ void store4(const DecodeArgs& a, const Rows& w, int r
 }
 
 // The copies of a ring: tiles 0 .. count - 1, tile i into stage i % S.  `find(i, x)` gives the
-// records of tile i's blocks (0: none); a lane does that for one tile of every 32.
-template <int S, int NB, uint32_t RECORD, typename Find>
+// records of tile i's blocks (0: none); a lane does that for one tile of every 32 and leaves them
+// in shared memory, the first one with its low bit set where the others follow it (records
+// start on 16 bytes), so that one copy brings them all.
+template <int S, uint32_t RECORD, typename Find>
 struct Feeder {
   Find find;
   uint32_t ring;
   uint64_t* full;
   volatile int* have;
-  int count, held_at = -1, issued = 0;
-  // the lane's tile: its records, and the first one with its low bits set where all of them follow
-  // one another (records start on 16 bytes)
-  unsigned long long rec[NB], run = 0;
+  volatile unsigned long long* recs;  // [32][NB]
+  int count, issued = 0;
 
-  __device__ __forceinline__ Feeder(Find f, uint32_t r, uint64_t* b, volatile int* h, int n)
-      : find(f), ring(r), full(b), have(h), count(n) {
-#pragma unroll
-    for (int k = 0; k < NB; ++k) rec[k] = 0;
-  }
   // Tile i into stage s (a converged warp).
   __device__ __forceinline__ void issue(int i, int s) {
     const int lane = threadIdx.x & 31;
-    if (held_at < 0 || i >= held_at + 32) {
-      held_at = i;
+    if ((i & 31) == 0) {
+      unsigned long long x[NB];
 #pragma unroll
-      for (int k = 0; k < NB; ++k) rec[k] = 0;
-      if (i + lane < count) find(i + lane, rec);
-      bool follow = rec[0] != 0;
+      for (int k = 0; k < NB; ++k) x[k] = 0;
+      if (i + lane < count) find(i + lane, x);
+      bool follow = x[0] != 0;
 #pragma unroll
-      for (int k = 1; k < NB; ++k) follow = follow && rec[k] == rec[0] + k * RECORD;
-      run = follow ? rec[0] | 1 : 0;
+      for (int k = 1; k < NB; ++k) follow = follow && x[k] == x[0] + k * RECORD;
+      recs[lane * NB] = follow ? x[0] | 1 : x[0];
+#pragma unroll
+      for (int k = 1; k < NB; ++k) recs[lane * NB + k] = x[k];
+      __syncwarp();
     }
-    const unsigned long long x = __shfl_sync(0xffffffffu, run, i - held_at);
-    const uint32_t dst = ring + s * NB * RECORD;
-    if (x != 0) {
-      if (lane == 0) {
+    if (lane == 0) {
+      const volatile unsigned long long* mine = recs + (i & 31) * NB;
+      const uint32_t dst = ring + s * NB * RECORD;
+      const unsigned long long x0 = mine[0];
+      if (x0 & 1) {
         have[s] = (1 << NB) - 1;
         mbar_expect_tx(full + s, NB * RECORD);
-        bulk_load(dst, x - 1, NB * RECORD, full + s);
-      }
-    } else {
-      unsigned long long y[NB];
-      int here = 0;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        y[k] = __shfl_sync(0xffffffffu, rec[k], i - held_at);
-        here |= (y[k] != 0 ? 1 : 0) << k;
-      }
-      if (lane == 0) {
+        bulk_load(dst, x0 - 1, NB * RECORD, full + s);
+      } else {
+        int here = 0;
+        for (int k = 0; k < NB; ++k) here |= (mine[k] != 0 ? 1 : 0) << k;
         have[s] = here;
         mbar_expect_tx(full + s, __popc(here) * RECORD);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < NB; ++k)
-          if (y[k] != 0) bulk_load(dst + k * RECORD, y[k], RECORD, full + s);
+          if ((here >> k) & 1) bulk_load(dst + k * RECORD, mine[k], RECORD, full + s);
       }
     }
     __syncwarp();
@@ -504,14 +527,12 @@ struct Stage {
 template <typename SL>
 __device__ __forceinline__ void init_bars(uint8_t* sm, int wr) {
   constexpr int n = SL::kRings * SL::kStages;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < n; ++i) {
-      mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + i, 1);
-      mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + n + i, wr);
-    }
-    *reinterpret_cast<volatile int*>(sm + SL::misc) = 0;
+  static_assert(2 * n <= kThreads, "a thread for each barrier");
+  if (threadIdx.x < 2 * n) {
+    mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + threadIdx.x, threadIdx.x < n ? 1 : wr);
     mbar_fence_init();
   }
+  if (threadIdx.x == 0) *reinterpret_cast<volatile int*>(sm + SL::misc) = 0;
   __syncthreads();
 }
 
@@ -539,33 +560,44 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   // Sequences in the order of their lengths, the longest first, so that a launch's last CTAs
   // are short ones.
   if (a.longest_first) {
-    int* lens = reinterpret_cast<int*>(sm + SL::ml_cta);
+    int4* lens = reinterpret_cast<int4*>(sm + SL::ml_cta);
     int* which = reinterpret_cast<int*>(sm + SL::ml_warp);
-    const int n = threadIdx.x < a.B ? a.c.lengths[threadIdx.x] : 0;
-    lens[threadIdx.x] = n;
+    const int me = threadIdx.x, n = me < a.B ? a.c.lengths[me] : INT_MIN;
+    reinterpret_cast<int*>(lens)[me] = n;
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < a.B; ++i) rank += lens[i] > n || (lens[i] == n && i < threadIdx.x);
-    if (threadIdx.x < a.B && rank == b) *which = threadIdx.x;
+    int rank = 0;  // sequences before this thread's
+    for (int i = 0; i < a.B; i += 4) {
+      const int4 x = lens[i / 4];
+      rank += (x.x > n || (x.x == n && i < me)) + (x.y > n || (x.y == n && i + 1 < me)) +
+              (x.z > n || (x.z == n && i + 2 < me)) + (x.w > n || (x.w == n && i + 3 < me));
+    }
+    if (me < a.B && rank == b) *which = me;
     __syncthreads();
     b = *which;
   }
   const Rows w = rows_of(a, b, rest % a.c.Hk, rt, 16 * WR, threadIdx.x == 0);
-  constexpr int NB = kTileBlocks<SLABS>, kKeys = NB * kBlock;
-  Reach<kKeys> reach = reach_of<kKeys>(a, w.held, w.p0, w.p1);
-  if (w.nr <= 0) reach.tiles = 0;
+  // (what only the finding of records and the tiles at an end need stays out of the registers)
+  Reach* s_reach = reinterpret_cast<Reach*>(sm + SL::reach);
+  if (threadIdx.x == 0) {
+    Reach reach = reach_of(a, w.held, w.p0, w.p1);
+    if (w.nr <= 0) reach.tiles = 0;
+    *s_reach = reach;
+  }
+  __syncthreads();
+  const int tiles = s_reach->tiles, heads = s_reach->heads, skip = s_reach->skip;
   // this CTA's tiles, of which its rings take every R-th
-  const int first = (int)((long long)reach.tiles * split / a.splits);
-  const int count = (int)((long long)reach.tiles * (split + 1) / a.splits) - first;
+  const int first = (int)((long long)tiles * split / a.splits);
+  const int count = (int)((long long)tiles * (split + 1) / a.splits) - first;
   const int mine = (count - group + R - 1) / R;
-  auto tile_first = [&](int i) { return reach.key(first + group + R * i); };
-  auto find = [&](int i, unsigned long long (&x)[NB]) {
-#pragma unroll
-    for (int k = 0; k < NB; ++k) x[k] = record_at(a, reach, w.b, w.hk, tile_first(i) + k * kBlock);
+  auto tile_first = [&](int i) {
+    const int t = first + group + R * i;
+    return (t < heads ? t : t + skip) * kKeys;
   };
+  auto find = [&](int i, unsigned long long (&x)[NB]) { records_at(a, *s_reach, w.b, w.hk, tile_first(i), x); };
   const bool producer = part == 0;
   const uint32_t ring = smem_u32(sm + SL::ring) + group * S * SL::kStageBytes;
-  Feeder<S, NB, SL::kRecord, decltype(find)> feed(find, ring, full, have, mine);
+  Feeder<S, SL::kRecord, decltype(find)> feed = {
+      find, ring, full, have, reinterpret_cast<volatile unsigned long long*>(sm + SL::recs) + group * 32 * NB, mine};
   if (producer)
     for (int i = 0; i < min(S, mine); ++i) feed.issue(i, i);
 
@@ -581,7 +613,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
     ok = __all_sync(0xffffffffu, cross_wait(full + s, stage.phase, a.budget, s_abort));
     if (!ok) break;
     done = i + 1;
-    if (rows_here) st.tile(a, w, reach, ring + s * SL::kStageBytes, tile_first(i), have[s]);
+    if (rows_here) st.tile(a, s_reach, ring + s * SL::kStageBytes, tile_first(i), have[s]);
     __syncwarp();
     if (WR > 1 && lane == 0) mbar_arrive(empty + s);
     if (producer && i + S < mine) {
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
       add_scaled(v, f, *reinterpret_cast<const float4*>(so + (k * WR * 16 + at) * SL::kPitch + 4 * piece));
     }
     if (alone) {
-      if (!failed) store4(a, w, w.r0 + row, D, piece, m, l, v);
+      if (!failed) store4(a, w, row, D, piece, m, l, v);
     } else {
       *reinterpret_cast<float4*>(s_o + row * D + 4 * piece) = make_float4(v[0], v[1], v[2], v[3]);
       if (piece == 0) s_ml[row] = make_float4(m, l, 0.f, 0.f);
@@ -646,7 +678,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
         l += join_sum(s.y, f);
         if (f > 0.f) add_scaled(v, f, ld_cluster(map_rank(o_addr + 4 * (row * D + 4 * piece), k)));
       }
-      if (!failed) store4(a, w, w.r0 + row, D, piece, m, l, v);
+      if (!failed) store4(a, w, row, D, piece, m, l, v);
     }
     cluster_sync();  // no CTA leaves while another one reads its shared memory
   }
@@ -697,7 +729,7 @@ cudaError_t launch(DecodeArgs a, long long tiles, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long slots = (long long)device_sms() * per_sm;
   a.splits = splits_for(items, tiles, kWarps / WR, slots);
-  a.longest_first = a.B > 1 && a.B <= kThreads && items * a.splits > slots;
+  a.longest_first = a.B > 1 && a.B <= kThreads && items * a.splits > device_sms();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * a.splits));
   cfg.blockDim = dim3(kThreads);
@@ -740,7 +772,7 @@ extern "C" df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, i
     return DF_ERR_INVALID_ARG;
   if (!self_reach(&window, &sinks) || (!causal && (window != 0 || sinks != 0))) return DF_ERR_INVALID_ARG;
   if (!cu_seqlens_q && (long long)B * Lq != total_q) return DF_ERR_INVALID_ARG;
-  if (dtype == DF_FP32 || total_q > (1 << 30) || H > 65536 || (long long)Lq * (H / Hk) > (1 << 30)) return DF_ERR_UNSUPPORTED;
+  if (dtype == DF_FP32 || total_q > (1 << 30) || H / Hk > 128 || (long long)Lq * (H / Hk) > (1 << 30)) return DF_ERR_UNSUPPORTED;
   if (((uintptr_t)cu_seqlens_q & 3u) != 0 || ((uintptr_t)lse & 3u) != 0) return DF_ERR_ALIGNMENT;
   if (total_q == 0 || B == 0 || Lq == 0) return DF_OK;
   if (!q || !out) return DF_ERR_INVALID_ARG;
@@ -757,6 +789,7 @@ extern "C" df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, i
   a.B = B;
   a.H = H;
   a.G = H / Hk;
+  a.by_G = 65536u / a.G + 1;
   a.Lq = Lq;
   a.Tq = total_q;
   a.causal = causal != 0;
@@ -769,10 +802,8 @@ extern "C" df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, i
   const int wr = warps_a_ring(Lq * a.G);
   a.row_tiles = (Lq * a.G + 16 * wr - 1) / (16 * wr);
   if ((long long)B * Hk * a.row_tiles > 0x7fffffffll / 8) return DF_ERR_UNSUPPORTED;
-  const int keys = (d <= 64 ? kTileBlocks<2> : kTileBlocks<4>) * kBlock;
-  // the tokens that a tile of rows sees at most, in tiles
-  long long tiles = (std::min<long long>(max_length, (long long)max_pages * page) + keys - 1) / keys;
-  if (window > 0) tiles = std::min<long long>(tiles, ((long long)window + Lq + sinks) / keys + 3);
+  long long tiles = (std::min<long long>(max_length, (long long)max_pages * page) + kKeys - 1) / kKeys;
+  if (window > 0) tiles = std::min<long long>(tiles, ((long long)window + Lq + sinks) / kKeys + 3);
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   switch (d / 32) {

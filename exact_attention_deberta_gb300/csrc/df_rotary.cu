@@ -195,22 +195,26 @@ extern "C" df_status df_rotary_table(int rot, double base, double factor, double
   return DF_OK;
 }
 
-extern "C" df_status df_rotary(int n, const void* const* x, const int* heads, const int64_t* x_stride, void* const* out,
-                               const int64_t* out_stride, const void* positions, int pos_64, int T, int d, int rot,
-                               int interleaved, int inverse, const uint64_t* turns, float amplitude, df_dtype dtype,
-                               df_stream_t stream) {
-  if (n < 1 || n > 2 || !x || !heads || !x_stride || !out || !out_stride || T < 0 || T > (1 << 30) || d < 1 || rot < 2 ||
-      rot % 2 != 0 || rot > d || !(fabsf(amplitude) <= 3.0e38f))
+extern "C" df_status df_rotary(const void* x, int heads, long long x_stride, void* out, long long out_stride,
+                               const void* x2, int heads2, long long x2_stride, void* out2, long long out2_stride,
+                               const void* positions, int pos_64, int T, int d, int rot, int interleaved, int inverse,
+                               const uint64_t* turns, float amplitude, df_dtype dtype, df_stream_t stream) {
+  const int n = heads2 != 0 ? 2 : 1;
+  const int h[2] = {heads, heads2};
+  const void* from[2] = {x, x2};
+  void* to[2] = {out, out2};
+  const long long xs[2] = {x_stride, x2_stride}, ys[2] = {out_stride, out2_stride};
+  if (T < 0 || T > (1 << 30) || d < 1 || rot < 2 || rot % 2 != 0 || rot > d || !(fabsf(amplitude) <= 3.0e38f))
     return DF_ERR_INVALID_ARG;
   if (dtype != DF_BF16 && dtype != DF_FP16 && dtype != DF_FP32) return DF_ERR_INVALID_ARG;
   if (d > 65536) return DF_ERR_UNSUPPORTED;
   const int size = dtype == DF_FP32 ? 4 : 2;
   RotaryArgs a = {};
   for (int i = 0; i < n; ++i) {
-    if (heads[i] < 1 || heads[i] > 65536) return DF_ERR_INVALID_ARG;
-    const long long width = (long long)heads[i] * d;
-    if (T > 1 && (x_stride[i] < width || out_stride[i] < width)) return DF_ERR_INVALID_ARG;
-    if (x_stride[i] < 0 || out_stride[i] < 0 || x_stride[i] > (1ll << 31) || out_stride[i] > (1ll << 31))
+    if (h[i] < 1 || h[i] > 65536) return DF_ERR_INVALID_ARG;
+    const long long width = (long long)h[i] * d;
+    if (T > 1 && (xs[i] < width || ys[i] < width)) return DF_ERR_INVALID_ARG;
+    if (xs[i] < 0 || ys[i] < 0 || xs[i] > (1ll << 31) || ys[i] > (1ll << 31))
       return DF_ERR_INVALID_ARG;
   }
   if (T == 0) return DF_OK;
@@ -220,28 +224,28 @@ extern "C" df_status df_rotary(int n, const void* const* x, const int* heads, co
   int width = 16 / size;
   while (width > 1 && ((interleaved ? rot : rot / 2) % width != 0 || (d - rot) % width != 0)) width /= 2;
   for (int i = 0; i < n; ++i) {
-    if (!x[i] || !out[i]) return DF_ERR_INVALID_ARG;
-    if (((uintptr_t)x[i] | (uintptr_t)out[i]) % size != 0) return DF_ERR_ALIGNMENT;
-    while (width > 1 && (((uintptr_t)x[i] | (uintptr_t)out[i]) % (width * size) != 0 || d % width != 0 ||
-                         (T > 1 && (x_stride[i] % width != 0 || out_stride[i] % width != 0))))
+    if (!from[i] || !to[i]) return DF_ERR_INVALID_ARG;
+    if (((uintptr_t)from[i] | (uintptr_t)to[i]) % size != 0) return DF_ERR_ALIGNMENT;
+    while (width > 1 && (((uintptr_t)from[i] | (uintptr_t)to[i]) % (width * size) != 0 || d % width != 0 ||
+                         (T > 1 && (xs[i] % width != 0 || ys[i] % width != 0))))
       width /= 2;
-    a.x[i] = x[i];
-    a.y[i] = out[i];
-    a.xs[i] = x_stride[i];
-    a.ys[i] = out_stride[i];
-    a.heads += heads[i];
+    a.x[i] = from[i];
+    a.y[i] = to[i];
+    a.xs[i] = xs[i];
+    a.ys[i] = ys[i];
+    a.heads += h[i];
   }
-  a.heads0 = heads[0];
+  a.heads0 = heads;
   for (int i = 0; i < n; ++i) {
-    const long long wi = (long long)heads[i] * d * size, si = T > 1 ? out_stride[i] * size : wi;
+    const long long wi = (long long)h[i] * d * size, si = T > 1 ? ys[i] * size : wi;
     for (int j = 0; j < n; ++j) {
-      const long long wj = (long long)heads[j] * d * size, sj = T > 1 ? x_stride[j] * size : wj;
-      const bool in_place = i == j && out[i] == x[j] && (T == 1 || out_stride[i] == x_stride[j]);
-      if (!in_place && !rows_apart(out[i], si, wi, x[j], sj, wj, T)) return DF_ERR_INVALID_ARG;
-      if (j > i && !rows_apart(out[i], si, wi, out[j], T > 1 ? out_stride[j] * size : wj, wj, T)) return DF_ERR_INVALID_ARG;
+      const long long wj = (long long)h[j] * d * size, sj = T > 1 ? xs[j] * size : wj;
+      const bool in_place = i == j && to[i] == from[j] && (T == 1 || ys[i] == xs[j]);
+      if (!in_place && !rows_apart(to[i], si, wi, from[j], sj, wj, T)) return DF_ERR_INVALID_ARG;
+      if (j > i && !rows_apart(to[i], si, wi, to[j], T > 1 ? ys[j] * size : wj, wj, T)) return DF_ERR_INVALID_ARG;
     }
     const size_t bytes = (size_t)((T - 1) * si + wi);
-    if (overlapping({{out[i], bytes}}, {{positions, (size_t)T * (pos_64 ? 8 : 4)}, {turns, (size_t)rot * 4}}))
+    if (overlapping({{to[i], bytes}}, {{positions, (size_t)T * (pos_64 ? 8 : 4)}, {turns, (size_t)rot * 4}}))
       return DF_ERR_INVALID_ARG;
   }
   a.pos = positions;

@@ -19,9 +19,13 @@ b._lib.df_self_attn_bwd.argtypes = [b._vp] * 10 + [b._i] * 8 + [ctypes.c_float] 
 b._lib.df_self_attn_bwd.restype = b._i
 
 
+_INT = 2 ** 31  # sizes go to the library as C ints
+
+
 def _reach(window, sinks):
     window, sinks = int(window or 0), int(sinks)
-    b._int_sizes(window=window, sinks=sinks)
+    if not (0 <= window < _INT and 0 <= sinks < _INT):
+        raise ValueError(f"window = {window} or sinks = {sinks} is out of range")
     return window, sinks
 
 
@@ -57,8 +61,8 @@ def df_self_attn_bwd(q, k, v, out, stats, dout, key_mask=None, cu_seqlens_q=None
 
 
 _ll = ctypes.c_longlong
-b._lib.df_rotary.argtypes = ([b._i, b._PP, ctypes.POINTER(b._i), ctypes.POINTER(_ll), b._PP, ctypes.POINTER(_ll), b._vp] +
-                             [b._i] * 6 + [b._vp, ctypes.c_float, b._i, b._vp])
+b._lib.df_rotary.argtypes = ([b._vp, b._i, _ll, b._vp, _ll] * 2 + [b._vp] + [b._i] * 6 +
+                             [b._vp, ctypes.c_float, b._i, b._vp])
 b._lib.df_rotary.restype = b._i
 b._lib.df_rotary_table.argtypes = [b._i] + [ctypes.c_double] * 5 + [b._vp]
 b._lib.df_rotary_table.restype = b._i
@@ -77,6 +81,8 @@ def df_rotary_table(rot, base=10000.0, factor=1.0, original_len=0.0, low=1.0, hi
 
 def _token_stride(name, x, lead):
     """Elements between tokens of [..., heads, d]: the leading dimensions as one."""
+    if x.is_contiguous():
+        return x.shape[-2] * x.shape[-1]
     st, n = x.stride(), 1
     if st[-1] != 1 and x.shape[-1] > 1 or st[-2] != x.shape[-1] and x.shape[-2] > 1:
         raise ValueError(f"{name}: heads and columns must be next to one another")
@@ -104,27 +110,34 @@ def df_rotary(x, positions, table, *, interleaved=False, inverse=False, amplitud
     n = len(xs)
     if not 1 <= n <= 2:
         raise ValueError("x must be one tensor or two")
-    dt, lead, d = xs[0].dtype, xs[0].shape[:-2], xs[0].shape[-1]
-    if dt not in b._DTYPE or any(t.dtype != dt or t.dim() < 3 or t.shape[:-2] != lead or t.shape[-1] != d for t in xs):
+    first, dt = xs[0], xs[0].dtype
+    lead, d = first.shape[:-2], first.shape[-1]
+    if dt not in b._DTYPE or len(lead) < 1 or (n == 2 and (xs[1].dtype != dt or xs[1].shape[:-2] != lead or
+                                                           xs[1].shape[-1] != d)):
         raise ValueError("x must be bf16, fp16 or fp32 tensors [..., heads, d] that share all but heads")
     if positions.dtype not in (torch.int32, torch.int64) or positions.shape != lead:
         raise ValueError("positions must be int32 or int64, of x's shape without heads and columns")
     if table.dtype != torch.int64 or table.dim() != 1:
         raise ValueError("table must be what df_rotary_table gives")
     if out is None:
-        outs = tuple(torch.empty(t.shape, dtype=dt, device=t.device) for t in xs)
+        outs = tuple([torch.empty(t.shape, dtype=dt, device=t.device) for t in xs])
     else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(outs) != n or any(o.dtype != dt or o.shape != t.shape for o, t in zip(outs, xs)):
             raise ValueError("out must match x in number, shape and dtype")
     idx = b._on_device((positions, table), "positions table")
-    if any(t.get_device() != idx for t in xs + outs):
-        raise ValueError("x and out must be CUDA tensors on the device of positions")
+    for t in xs + outs:
+        if t.get_device() != idx:
+            raise ValueError("x and out must be CUDA tensors on the device of positions")
     T, k = positions.numel(), len(lead)
-    b._int_sizes(tokens=T, columns=d)
-    strides = [(_ll * n)(*[_token_stride(name, t, k) for t in ts]) for name, ts in (("x", xs), ("out", outs))]
-    b._check(b._call_on(idx, b._lib.df_rotary, n, b._ptr_array(xs), (b._i * n)(*[t.shape[-2] for t in xs]), strides[0],
-                        b._ptr_array(outs), strides[1], positions.data_ptr(), 1 if positions.dtype == torch.int64 else 0,
+    if T >= _INT or d >= _INT:
+        raise ValueError("x is too large")
+    rows = []
+    for t, o in zip(xs, outs):
+        rows += (t.data_ptr(), t.shape[-2], _token_stride("x", t, k), o.data_ptr(), _token_stride("out", o, k))
+    if n == 1:
+        rows += (None, 0, 0, None, 0)
+    b._check(b._call_on(idx, b._lib.df_rotary, *rows, positions.data_ptr(), 1 if positions.dtype == torch.int64 else 0,
                         T, d, 2 * table.numel(), 1 if interleaved else 0, 1 if inverse else 0, table.data_ptr(),
                         float(amplitude), b._DTYPE[dt]), "df_rotary")
     return outs[0] if isinstance(x, torch.Tensor) else list(outs)
@@ -155,30 +168,34 @@ def df_cache_new(n_pages, heads, page, d, device="cuda"):
 
 def _cache_shape(cache, page_table, lengths):
     """(sequences, heads, head size, pages, tokens of a page, pages of a sequence)."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or cache.shape[3] < 48 or (cache.shape[3] - 16) % 32 != 0:
+    shape, pages = cache.shape, page_table.shape
+    if cache.dtype != torch.uint8 or len(shape) != 4 or shape[3] < 48 or shape[3] % 32 != 16:
         raise ValueError("cache must be uint8 [n_pages, heads, page / 16, 32 d + 16]")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    if page_table.dtype != torch.int32 or len(pages) != 2:
         raise ValueError("page_table must be int32 [B, max_pages]")
-    if lengths.dtype != torch.int32 or lengths.dim() != 1 or lengths.shape[0] != page_table.shape[0]:
+    if lengths.dtype != torch.int32 or lengths.shape != pages[:1]:
         raise ValueError("lengths must be int32 [B]")
-    n_pages, heads, per, record = cache.shape
-    b._int_sizes(n_pages=n_pages, page=per * BLOCK)
-    return lengths.shape[0], heads, (record - 16) // 32, n_pages, per * BLOCK, page_table.shape[1]
+    n_pages, heads, per, record = shape
+    if n_pages >= _INT or per >= _INT // BLOCK or pages[0] >= _INT or pages[1] >= _INT:
+        raise ValueError("the cache or its page table is too large")
+    return pages[0], heads, record // 32, n_pages, per * BLOCK, pages[1]
 
 
 def _cache_rows(name, x, cu, B):
     """(length, rows) of [B, n, ..] or, with offsets, [total, ..]."""
-    if x.dim() != (4 if cu is None else 3):
+    shape = x.shape
+    if len(shape) != (4 if cu is None else 3):
         raise ValueError(f"{name} must be [B, n, heads, d], or [total, heads, d] with cu_seqlens")
     if cu is None:
-        if x.shape[0] != B:
+        if shape[0] != B:
             raise ValueError(f"{name} and lengths disagree on the number of sequences")
-        n, total = x.shape[1], x.shape[0] * x.shape[1]
+        n, total = shape[1], shape[0] * shape[1]
     else:
         if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] != B + 1:
             raise ValueError("cu_seqlens must be an int32 vector [B + 1]")
-        n, total = 0, x.shape[0]
-    b._int_sizes(rows=total)
+        n, total = 0, shape[0]
+    if total >= _INT:
+        raise ValueError(f"{name} has too many rows")
     return n, total
 
 
@@ -216,7 +233,8 @@ def df_cache_read(cache, page_table, lengths, cu_seqlens=None, *, rows=None, dty
         if rows is None:
             raise ValueError("rows (of each sequence, or of all of them with cu_seqlens) or out must be given")
         shape = (int(rows), heads, d) if cu_seqlens is not None else (B, int(rows), heads, d)
-        b._int_sizes(rows=shape[-3])
+        if not 0 <= shape[-3] < _INT:
+            raise ValueError("rows is out of range")
         out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
     k, v = out
     if k.dtype not in b._DTYPE or v.dtype != k.dtype or v.shape != k.shape or tuple(k.shape[-2:]) != (heads, d):
@@ -256,8 +274,9 @@ def df_cache_attn(q, cache, page_table, lengths, cu_seqlens_q=None, *, max_seqle
             raise ValueError("packed q needs max_seqlen_q (an upper bound of every length)")
         Lq = int(max_seqlen_q)
     window, sinks = _reach(window, sinks)
-    max_length = min(max_pages * page, 2 ** 31 - 1) if max_length is None else int(max_length)
-    b._int_sizes(max_seqlen_q=Lq, max_length=max_length)
+    max_length = min(max_pages * page, _INT - 1) if max_length is None else int(max_length)
+    if not (0 <= Lq < _INT and 0 <= max_length < _INT):
+        raise ValueError("max_seqlen_q or max_length is out of range")
     if out is None:
         out = torch.empty_like(q)
     elif out.dtype != q.dtype or out.shape != q.shape:

@@ -588,27 +588,28 @@ df_status df_self_attn_bwd(const void* q, const void* k, const void* v, const vo
  * i < rot / 2, by the angle of positions[t] times the pair's frequency; the others are copied:
  *     out[a] = A (x[a] cos - x[b] sin),   out[b] = A (x[b] cos + x[a] sin)
  * `inverse` negates the sines: the gradient of the call without it.
- *   n          1 or 2 tensors (queries and keys) that share positions; x, heads, x_stride,
- *              out, out_stride are HOST arrays of n
- *   x[i]       [T, heads[i], d] of `dtype` (bf16, fp16 or fp32), x_stride[i] elements from
- *              token to token (at least heads[i] d: a part of wider rows, as a fused
- *              projection gives them), heads next to one another; out[i] likewise
+ *   x          [T, heads, d] of `dtype` (bf16, fp16 or fp32), x_stride elements from token to
+ *              token (at least heads d: a part of wider rows, as a fused projection gives
+ *              them), heads next to one another; out likewise
+ *   x2, out2   the same for a second tensor that shares the positions (keys beside queries);
+ *              heads2 = 0: there is none
  *   positions  int32 (pos_64 = 0) or int64 (pos_64 = 1), [T]; any values
  *   rot        even, 2 .. d
  *   turns      device uint64 [rot / 2]: each pair's turns a position times 2^64, modulo 2^64
  *              (df_rotary_table).  Angles are exact products of integers, so that far
  *              positions lose nothing.
  *   amplitude  A, 1 or what the scaling for long contexts asks for
- * The rotation is formed in fp32 and rounded once.  out[i] may be x[i] (with its stride); any
+ * The rotation is formed in fp32 and rounded once.  out may be x (with its stride), out2 x2; any
  * other overlap is refused.  T = 0 is a call that does nothing.  One launch; fastest where
  * rot / 2 (interleaved: rot) and d are multiples of 16 bytes and rows start on 16 bytes.
- * Errors: DF_ERR_INVALID_ARG (NULL pointer, n, sizes, rot, strides, amplitude not finite,
+ * Errors: DF_ERR_INVALID_ARG (NULL pointer, sizes, rot, strides, amplitude not finite,
  * overlap), DF_ERR_UNSUPPORTED (d > 65536), DF_ERR_ALIGNMENT (a pointer not aligned to its
  * elements), DF_ERR_CUDA. */
-df_status df_rotary(int n, const void* const* x, const int* heads, const int64_t* x_stride,
-                    void* const* out, const int64_t* out_stride, const void* positions,
-                    int pos_64, int T, int d, int rot, int interleaved, int inverse,
-                    const uint64_t* turns, float amplitude, df_dtype dtype, df_stream_t stream);
+df_status df_rotary(const void* x, int heads, long long x_stride, void* out, long long out_stride,
+                    const void* x2, int heads2, long long x2_stride, void* out2,
+                    long long out2_stride, const void* positions, int pos_64, int T, int d,
+                    int rot, int interleaved, int inverse, const uint64_t* turns,
+                    float amplitude, df_dtype dtype, df_stream_t stream);
 
 /* The frequencies of df_rotary for `rot` columns, into a HOST array turns [rot / 2]:
  *     f_i = base^(-2 i / rot)   radians a position,
@@ -673,7 +674,7 @@ df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t*
 /* Attention of a few queries per sequence to the cache, without unpacking it:
  *     s_ij = scale q_i.k_j,  out_i = sum_j exp(s_ij - lse_i) v_j     over the tokens j that i sees
  *   q, out     [B, Lq, H, d] or, with cu_seqlens_q (int32 [B + 1]), [total_q, H, d], bf16 or
- *              fp16; H a multiple of Hk.  Packed rows that belong to no sequence are left alone.
+ *              fp16; H a multiple of Hk, at most 128 query heads per key head.  Packed rows that belong to no sequence are left alone.
  *   causal     1: the queries are the sequence's last tokens (which the cache holds already):
  *              row i of n, at position p = i + lengths[b] - n, sees the tokens j <= p with
  *              window = 0, j > p - window or j < sinks (as df_self_attn_fwd).  0: every query

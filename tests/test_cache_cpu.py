@@ -107,7 +107,7 @@ def test_each_call_refuses_its_own(binding):
            dict(lse=0x200000), dict(out=0x1000000)]
     for over in bad:
         assert _attn(b, **over) == b.DF_ERR_INVALID_ARG, over
-    assert _attn(b, dtype=2) == b.DF_ERR_UNSUPPORTED
+    assert _attn(b, dtype=2) == b.DF_ERR_UNSUPPORTED and _attn(b, H=258, Hk=2) == b.DF_ERR_UNSUPPORTED
     assert _attn(b, lse=0x50002) == b.DF_ERR_ALIGNMENT and _attn(b, q=0x100008) == b.DF_ERR_ALIGNMENT
     assert _attn(b, Lq=0, total=0, q=None, out=None) == b.DF_OK
 

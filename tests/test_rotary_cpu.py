@@ -46,19 +46,17 @@ def test_oracle_rotates_by_complex_numbers():
 
 
 def _call(b, **over):
-    a = dict(n=2, x=(0x100000, 0x200000), heads=(4, 2), xs=(256, 128), out=(0x300000, 0x400000), os=(256, 128),
+    a = dict(x=(0x100000, 0x200000), heads=(4, 2), xs=(256, 128), out=(0x300000, 0x400000), os=(256, 128),
              pos=0x500000, pos_64=0, T=5, d=64, rot=64, turns=0x600000, amp=1.0, dtype=0)
     a.update(over)
     p = lambda n: None if a[n] is None else ctypes.c_void_p(a[n])  # noqa: E731
-    ptrs = lambda t: (ctypes.c_void_p * 2)(*t)  # noqa: E731
-    ll = lambda t: (ctypes.c_longlong * 2)(*t)  # noqa: E731
-    return b.raw_library.df_rotary(a["n"], ptrs(a["x"]), (ctypes.c_int * 2)(*a["heads"]), ll(a["xs"]), ptrs(a["out"]),
-                                   ll(a["os"]), p("pos"), a["pos_64"], a["T"], a["d"], a["rot"], 0, 0, p("turns"), a["amp"],
+    rows = [v for i in range(2) for v in (a["x"][i], a["heads"][i], a["xs"][i], a["out"][i], a["os"][i])]
+    return b.raw_library.df_rotary(*rows, p("pos"), a["pos_64"], a["T"], a["d"], a["rot"], 0, 0, p("turns"), a["amp"],
                                    a["dtype"], None)
 
 
 REFUSED = [
-    (dict(n=0), 1), (dict(n=3), 1), (dict(T=-1), 1), (dict(rot=0), 1), (dict(rot=63), 1), (dict(rot=66), 1),
+    (dict(T=-1), 1), (dict(heads=(4, -1)), 1), (dict(rot=0), 1), (dict(rot=63), 1), (dict(rot=66), 1),
     (dict(pos=None), 1), (dict(turns=None), 1), (dict(x=(None, 0x200000)), 1), (dict(out=(0x300000, None)), 1),
     (dict(heads=(0, 2)), 1), (dict(xs=(255, 128)), 1), (dict(os=(256, 127)), 1), (dict(xs=(256, -128)), 1),
     (dict(amp=float("nan")), 1), (dict(amp=float("inf")), 1), (dict(dtype=3), 1), (dict(pos=0x500002), 3),
