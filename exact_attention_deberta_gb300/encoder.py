@@ -10,8 +10,9 @@ embeddings (shared attention keys); disentangled attention (df_attn_fwd,
 packed); the output projection and a residual LayerNorm; the feed-forward
 block (projection with GELU, projection) and a residual LayerNorm.
 ``Encoder.embed`` gives the rows that enter the first layer (token embedding and
-LayerNorm), and ``CrossAttention`` is the layer of a decoder or a reader that
-attends to the encoder's states.
+LayerNorm), ``CrossAttention`` is the layer of a decoder or a reader that attends
+to the encoder's states, and ``SelfAttention`` the decoder's own: rotary positions,
+causal attention with a window and sinks, and generation from a cache in 8 bits.
 Weights are synthetic (no checkpoint is available): N(0, 0.02) matrices,
 N(0, 0.02) biases, LayerNorm gain 1 and shift 0.
 """
@@ -74,6 +75,19 @@ def synthetic_cross_weights(cfg: EncoderConfig, dtype=torch.bfloat16, device="cu
     h = cfg.hidden
     w = {n: rnd(h, h) for n in ("w_q", "w_k", "w_v", "w_o")}
     w.update({n: rnd(h) for n in ("b_q", "b_k", "b_v", "b_o")})
+    w.update(ln_g=torch.ones(h, dtype=dtype, device=device), ln_b=torch.zeros(h, dtype=dtype, device=device))
+    return w
+
+
+def synthetic_self_weights(cfg: EncoderConfig, key_heads=None, dtype=torch.bfloat16, device="cuda", seed=0):
+    """Weights of one SelfAttention layer of the encoder's width."""
+    g = torch.Generator().manual_seed(seed)
+
+    def rnd(*shape):
+        return (torch.randn(*shape, generator=g) * 0.02).to(dtype).to(device)
+
+    h, n = cfg.hidden, (key_heads or cfg.heads) * (cfg.hidden // cfg.heads)
+    w = dict(w_q=rnd(h, h), w_k=rnd(n, h), w_v=rnd(n, h), w_o=rnd(h, h), b_q=rnd(h), b_k=rnd(n), b_v=rnd(n), b_o=rnd(h))
     w.update(ln_g=torch.ones(h, dtype=dtype, device=device), ln_b=torch.zeros(h, dtype=dtype, device=device))
     return w
 
@@ -155,3 +169,95 @@ class CrossAttention:
                                         max_seqlen_k=max_seqlen_k, status=status, stream=stream)
         (o,) = binding.df_linear(ctx.view(T, hid), [w["w_o"]], [w["b_o"]], status=status, stream=stream)
         return binding.df_layernorm(o, w["ln_g"], w["ln_b"], residual=x, eps=cfg.eps, stream=stream)
+
+    def store(self, states, cache, page_table, cu_seqlens, stream=None, status=None):
+        """The states' keys and values into ``cache`` (``binding.df_cache_new``), half the bytes
+        that ``attend`` would read at every token: states [T, hidden], packed by cu_seqlens,
+        become the tokens of the sequences of ``page_table``."""
+        if stream is not None:
+            with binding._current(stream, states):
+                return self.store(states, cache, page_table, cu_seqlens, status=status)
+        k, v = self.project(states, status=status)
+        none = torch.zeros(page_table.shape[0], dtype=torch.int32, device=states.device)
+        return binding.df_cache_append(k, v, cache, page_table, none, cu_seqlens, status=status)
+
+    def attend_stored(self, x, cache, page_table, lengths, cu_seqlens_q=None, max_seqlen_q=1, max_length=None, stream=None,
+                      status=None):
+        """``attend`` to stored states, for a few rows of each sequence: x [Tq, hidden], packed by
+        cu_seqlens_q, or one row a sequence."""
+        if stream is not None:
+            with binding._current(stream, x):
+                return self.attend_stored(x, cache, page_table, lengths, cu_seqlens_q, max_seqlen_q, max_length, status=status)
+        w, cfg = self.w, self.cfg
+        T, hid = x.shape
+        (q,) = binding.df_linear(x, [w["w_q"]], [w["b_q"]], status=status)
+        heads = (cfg.heads, hid // cfg.heads)
+        ctx = binding.df_cache_attn(q.view(T, *heads) if cu_seqlens_q is not None else q.view(T, 1, *heads), cache,
+                                    page_table, lengths, cu_seqlens_q, max_seqlen_q=max_seqlen_q, max_length=max_length,
+                                    causal=False, status=status)
+        (o,) = binding.df_linear(ctx.view(T, hid), [w["w_o"]], [w["b_o"]], status=status)
+        return binding.df_layernorm(o, w["ln_g"], w["ln_b"], residual=x, eps=cfg.eps)
+
+
+class SelfAttention:
+    """A decoder's own attention layer: projections, rotary positions, causal attention (with a
+    window and sinks), output projection, residual LayerNorm.
+
+    ``prompt`` takes whole sequences and, with a cache, leaves their keys and values there;
+    ``step`` takes the next token or few of each sequence.  ``key_heads`` heads of keys and
+    values may be shared by several query heads (their columns together are a multiple of 256).
+    ``table`` holds the rotary frequencies (``binding.df_rotary_table``; a part of the head's
+    columns, or all).  ``status`` as for ``CrossAttention``."""
+
+    def __init__(self, cfg: EncoderConfig, weights: dict, table, key_heads=None, window=0, sinks=0, interleaved=False):
+        self.cfg, self.w, self.table = cfg, weights, table
+        self.key_heads = key_heads or cfg.heads
+        self.window, self.sinks, self.interleaved = window, sinks, interleaved
+
+    def _project(self, x, positions, status):
+        """q [T, heads, d], k and v [T, key_heads, d] of rows x [T, hidden]; q and k rotated."""
+        w, cfg = self.w, self.cfg
+        T, d = x.shape[0], cfg.hidden // cfg.heads
+        (q,) = binding.df_linear(x, [w["w_q"]], [w["b_q"]], status=status)
+        k, v = (t.view(T, self.key_heads, d) for t in
+                binding.df_linear(x, [w["w_k"], w["w_v"]], [w["b_k"], w["b_v"]], status=status))
+        q = q.view(T, cfg.heads, d)
+        binding.df_rotary((q, k), positions, self.table, interleaved=self.interleaved, out=(q, k))
+        return q, k, v
+
+    def _finish(self, ctx, x, status):
+        w = self.w
+        (o,) = binding.df_linear(ctx.view(x.shape), [w["w_o"]], [w["b_o"]], status=status)
+        return binding.df_layernorm(o, w["ln_g"], w["ln_b"], residual=x, eps=self.cfg.eps)
+
+    def prompt(self, x, positions, cu_seqlens, max_seqlen, cache=None, page_table=None, stream=None, status=None, trace=None):
+        """x [T, hidden], packed by cu_seqlens, at ``positions`` [T] -> [T, hidden].  With
+        ``cache`` the sequences begin there, on the pages of ``page_table``.  ``trace``: a list
+        that receives a dict of the attention's tensors."""
+        if stream is not None:
+            with binding._current(stream, x):
+                return self.prompt(x, positions, cu_seqlens, max_seqlen, cache, page_table, status=status, trace=trace)
+        q, k, v = self._project(x, positions, status)
+        if cache is not None:
+            none = torch.zeros(page_table.shape[0], dtype=torch.int32, device=x.device)
+            binding.df_cache_append(k, v, cache, page_table, none, cu_seqlens, status=status)
+        ctx = binding.df_self_attn_fwd(q, k, v, cu_seqlens_q=cu_seqlens, cu_seqlens_k=cu_seqlens, max_seqlen_q=max_seqlen,
+                                       max_seqlen_k=max_seqlen, window=self.window, sinks=self.sinks, status=status)
+        if trace is not None:
+            trace.append(dict(q=q, k=k, v=v, ctx=ctx))
+        return self._finish(ctx, x, status)
+
+    def step(self, x, positions, cache, page_table, lengths, max_length=None, stream=None, status=None, trace=None):
+        """The next n tokens of every sequence: x [B, n, hidden] at ``positions`` [B, n] ->
+        [B, n, hidden].  ``lengths`` [B] are the tokens held before; the caller adds n to them."""
+        if stream is not None:
+            with binding._current(stream, x):
+                return self.step(x, positions, cache, page_table, lengths, max_length, status=status, trace=trace)
+        B, n, hid = x.shape
+        q, k, v = (t.view(B, n, *t.shape[1:]) for t in self._project(x.view(B * n, hid), positions.view(B * n), status))
+        binding.df_cache_append(k, v, cache, page_table, lengths, status=status)
+        ctx = binding.df_cache_attn(q, cache, page_table, lengths + n, max_length=max_length, window=self.window,
+                                    sinks=self.sinks, status=status)
+        if trace is not None:
+            trace.append(dict(q=q, k=k, v=v, ctx=ctx))
+        return self._finish(ctx, x.view(B * n, hid), status).view(B, n, hid)

@@ -13,7 +13,17 @@ def calls(b, e):
     q, cu = dev(6, 8, 64), dev(3, dtype=torch.int32)
     paged = dev(4, 8, 2, 32 * 64 + 16, dtype=torch.uint8), dev(2, 2, dtype=torch.int32), dev(2, dtype=torch.int32)
     at = dict(cu_seqlens_q=cu, cu_seqlens_k=cu, max_seqlen_q=4, max_seqlen_k=4, window=3, sinks=1)
+    cfg = e.EncoderConfig(hidden=512, heads=8, layers=1, ffn=512)
+    put = lambda w: {n: dev(*t.shape) for n, t in w.items()}  # noqa: E731
+    own = e.SelfAttention(cfg, put(e.synthetic_self_weights(cfg, 4, device="cpu")), dev(32, dtype=torch.int64), key_heads=4)
+    cross = e.CrossAttention(cfg, put(e.synthetic_cross_weights(cfg, device="cpu")))
+    x, pos, x2, pos2 = dev(6, 512), dev(6, dtype=torch.int32), dev(2, 1, 512), dev(2, 1, dtype=torch.int32)
+    small = dev(4, 4, 2, 32 * 64 + 16, dtype=torch.uint8), *paged[1:]
     return {
+        "SelfAttention.prompt": lambda **s: own.prompt(x, pos, cu, 4, *small[:2], **s),
+        "SelfAttention.step": lambda **s: own.step(x2, pos2, *small, **s),
+        "CrossAttention.store": lambda **s: cross.store(x, *paged[:2], cu, **s),
+        "CrossAttention.attend_stored": lambda **s: cross.attend_stored(dev(2, 512), *paged, **s),
         "df_self_attn_fwd": lambda **s: b.df_self_attn_fwd(q, q, q, with_stats=True, **at, **s),
         "df_self_attn_bwd": lambda **s: b.df_self_attn_bwd(q, q, q, q, b.CrossStats(dev(6, 8, dtype=torch.float32), q), q,
                                                            **at, **s),
@@ -23,7 +33,8 @@ def calls(b, e):
     }
 
 
-NAMES = ["df_self_attn_fwd", "df_self_attn_bwd", "df_rotary", "df_cache_read", "df_cache_attn"]
+NAMES = ["df_self_attn_fwd", "df_self_attn_bwd", "df_rotary", "df_cache_read", "df_cache_attn", "SelfAttention.prompt",
+         "SelfAttention.step", "CrossAttention.store", "CrossAttention.attend_stored"]
 NOTHING = {"df_cache_append"}  # allocates nothing
 
 
