@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
           tmem_ld_wait2(r0, r1);
           const int kt = SELF ? band.tile(t0 + t) : t0 + t, left = it.no - kt * kKeys;
           const bool cut = SELF && !seen_whole(a, it.p0, it.nr, kt * kKeys);
+          bool live0 = true, live1 = true;  // SELF: whether any of this thread's columns counts in its warp
           if (a.key_mask || left < kKeys || cut) {
             uint32_t bits[kWords];
             const bool all =
@@ -499,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
                 const int p = it.p0 + sRow[row].x, first = kt * kKeys + (kKeys / 2) * half;
                 b0 &= seen_bits(a, p, first);
                 b1 &= seen_bits(a, p, first + 32);
+                live0 = __any_sync(0xffffffffu, b0 != 0);
+                live1 = __any_sync(0xffffffffu, b1 != 0);
               }
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
@@ -550,9 +553,23 @@ __global__ void __launch_bounds__(kThreads, 1) cross128_kernel(const FwdArgs arg
             }
             tmem_st16(to, w);
           };
+          auto zeros = [&](uint32_t to) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = 0u;
+            tmem_st16(to, w);
+          };
           // (P's 16 columns of a chunk fall on scores that are in registers)
-          exp_of(r0, tSw);
-          exp_of(r1, tSw + 16);
+          if (!SELF || live0) {
+            exp_of(r0, tSw);
+          } else {
+            zeros(tSw);
+          }
+          if (!SELF || live1) {
+            exp_of(r1, tSw + 16);
+          } else {
+            zeros(tSw + 16);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(exp_done + wg);
           l_run += (acc0.x + acc1.x) + (acc0.y + acc1.y);

@@ -10,8 +10,12 @@
 // of a turn, is rounded to fp32 for the sine and cosine.
 //
 // A thread keeps the sines and cosines of one vector of columns in registers and rotates
-// that vector in several heads, four at a time in flight; neighbouring lanes take
+// that vector in several heads, two at a time in flight; neighbouring lanes take
 // neighbouring columns, then heads, so that a warp's loads are whole lines.  HBM bound.
+//
+// Measured (GB300): 131072 tokens, 24 heads, d = 64, bf16: 131 us, 6.2 TB/s (four heads in
+// flight: 146, one: 137; 24 heads a thread: 137); 8191 tokens, 20 heads, d = 128, 48 columns
+// rotated in interleaved pairs, fp16: 19 us, 4.4 TB/s (one share of 2^20 threads: 23).
 #include <math.h>
 
 #include <algorithm>
@@ -32,6 +36,7 @@ struct RotaryArgs {
   int chunks, groups;      // vectors of a head that threads take, threads that share its heads
   float amplitude;
   int pos_64, inter, inverse;
+  int few;                 // fewer than 2^32 threads
 };
 
 // sin and cos of `phase` turns / 2^64.
@@ -70,12 +75,20 @@ template <typename T, int N, bool INTER>
 __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
   constexpr int kPairs = INTER && N > 1 ? N / 2 : N;
   constexpr bool kTwo = !INTER || N == 1;  // two vectors
-  constexpr int kFlight = 4;
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int c = (int)(id % a.chunks);
-  const long long rest = id / a.chunks;
-  const int g = (int)(rest % a.groups);
-  const long long t = rest / a.groups;
+  constexpr int kFlight = 2;
+  int c, g;
+  long long t;
+  if (a.few) {  // (32-bit divisions)
+    const unsigned id = blockIdx.x * 256u + threadIdx.x, rest = id / (unsigned)a.chunks;
+    c = (int)(id - rest * a.chunks);
+    t = rest / (unsigned)a.groups;
+    g = (int)(rest - (unsigned)t * a.groups);
+  } else {
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x, rest = id / a.chunks;
+    c = (int)(id - rest * a.chunks);
+    t = rest / a.groups;
+    g = (int)(rest - t * a.groups);
+  }
   if (t >= a.T) return;
   const int turned = a.rot / 2 / kPairs;  // chunks that are rotated
   const bool rotate = c < turned;
@@ -136,13 +149,14 @@ template <typename T, int N>
 cudaError_t launch(RotaryArgs a, cudaStream_t s) {
   const int pairs = a.inter && N > 1 ? N / 2 : N;
   a.chunks = a.rot / 2 / pairs + (a.d - a.rot) / N;
-  // heads a thread: as many as leave some 2^20 threads, to eight (the sines are formed once
+  // heads a thread: as many as leave some 2^19 threads, to twelve (the sines are formed once
   // for all of them); one where there is little to do
   const long long all = (long long)a.T * a.chunks;
-  const long long share = std::min<long long>(8, std::max<long long>(1, all * a.heads >> 20));
+  const long long share = std::min<long long>(12, std::max<long long>(1, all * a.heads >> 19));
   a.groups = (int)((a.heads + share - 1) / share);
   const long long blocks = (all * a.groups + 255) / 256;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  a.few = blocks < 1 << 24;
   if (a.inter)
     rotary_kernel<T, N, true><<<(unsigned)blocks, 256, 0, s>>>(a);
   else
