@@ -681,8 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
         if (!BF16 && t == 0) ds_mul = reinterpret_cast<const float*>(sm + SL::scale + s * 512)[row] * kPUnit;
         if constexpr (KEYS) {
-          // self attention: the keys are at or behind every query, and in its reach, or not all
-          const int pq = it.q0 + t * y_step;  // the position of the tile's first query
+          const int pq = it.q0 + t * y_step;  // self attention: the position of the tile's first query
           const bool cut = SELF && !(pq >= it.p0 + 127 && (a.window == 0 || pq + y_step - a.window <= it.p0 ||
                                                           it.p0 + 128 <= a.sinks));
           // A thread takes two columns of every eight in four rows (lane / 4 + 8 r),
@@ -712,6 +711,23 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
             tmem_ld_wait(rd1);
             auto half_rows = [&](const uint32_t (&rs)[16], const uint32_t (&rd)[16], int i) {
               uint32_t wp[8], wd[8];
+              const uint32_t to = lane_off + 16 * q + ((uint32_t)(16 * i) << 16);
+              const int* tok = reinterpret_cast<const int*>(sm + SL::tok) + 64 * h + 32 * q;
+              const int j0 = it.p0 + quad * 32 + 16 * i;  // the first of the 16 keys
+              bool mixed = false;
+              if (SELF && cut) {
+                // the least and the largest distance from a key to a query: a block that no query
+                // sees has no weights, one that all see nothing to select
+                const int near = pq + tok[0] - (j0 + 15), far = pq + tok[31] - j0;
+                if (far < 0 || (a.window != 0 && near >= a.window && j0 >= a.sinks)) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) wp[e] = wd[e] = 0u;
+                  tmem_st_rows16(tS(b) + to, wp);
+                  tmem_st_rows16(tdP(b) + to, wd);
+                  return;
+                }
+                mixed = near < 0 || (a.window != 0 && far >= a.window && j0 + 15 >= a.sinks);
+              }
               // (fp16: the scales of this thread's rows, fetched here: held over the loop they spill)
               const float m0 = BF16 ? 1.f : __shfl_sync(0xffffffffu, ds_mul, 16 * i + (lane >> 2));
               const float m1 = BF16 ? 1.f : __shfl_sync(0xffffffffu, ds_mul, 16 * i + 8 + (lane >> 2));
@@ -732,24 +748,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
                 for (int e = 0; e < 8; ++e)
                   if (!((rows_in >> (16 * i + 8 * (e & 1) + (lane >> 2))) & 1u)) wp[e] = wd[e] = 0u;
               }
-              if (SELF && cut) {
-                // rows 16 i + lane / 4 and 8 on: a key at j is seen from j on, for `reach` positions
-                const int j0 = it.p0 + quad * 32 + 16 * i + (lane >> 2), all = INT_MAX;
-                const int r0 = a.window == 0 || j0 < a.sinks ? all : a.window;
-                const int r1 = a.window == 0 || j0 + 8 < a.sinks ? all : a.window;
-                const int* tok = reinterpret_cast<const int*>(sm + SL::tok) + c2 + 32 * q;
+              if (SELF && mixed) {
+                // rows lane / 4 and 8 on: a key at j is seen from j on, for `reach` positions
+                const int j = j0 + (lane >> 2), all = INT_MAX;
+                const uint32_t r0 = a.window == 0 || j < a.sinks ? all : a.window;
+                const uint32_t r1 = a.window == 0 || j + 8 < a.sinks ? all : a.window;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  const int2 tt = *reinterpret_cast<const int2*>(tok + 8 * (e >> 1));
-                  const int j = j0 + 8 * (e & 1);
+                  const int2 tt = *reinterpret_cast<const int2*>(tok + 2 * (lane & 3) + 8 * (e >> 1));
+                  const int from = pq - j - 8 * (e & 1);
                   const uint32_t reach = e & 1 ? r1 : r0;
-                  const uint32_t keep = ((uint32_t)(pq + tt.x - j) < reach ? 0xffffu : 0u) |
-                                        ((uint32_t)(pq + tt.y - j) < reach ? 0xffff0000u : 0u);
+                  const uint32_t keep = ((uint32_t)(from + tt.x) < reach ? 0xffffu : 0u) |
+                                        ((uint32_t)(from + tt.y) < reach ? 0xffff0000u : 0u);
                   wp[e] &= keep;
                   wd[e] &= keep;
                 }
               }
-              const uint32_t to = lane_off + 16 * q + ((uint32_t)(16 * i) << 16);
               tmem_st_rows16(tS(b) + to, wp);
               tmem_st_rows16(tdP(b) + to, wd);
             };
@@ -764,10 +778,20 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           tmem_ld_wait2(rs0, rd0);
           tmem_ld32(tS(b) + lane_off + 32, rs1);
           tmem_ld32(tdP(b) + lane_off + 32, rd1);
+          const int first = SELF ? band.tile(t) * 128 : 0;
+          const bool cut = SELF && !seen_whole(a, it.p0, it.nr, first);
           auto columns = [&](const uint32_t (&rs)[32], const uint32_t (&rd)[32], int q) {
             uint32_t wd[16];
             uint32_t bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
-            if (SELF) bits &= seen_bits(a, it.p0 + row_tok, band.tile(t) * 128 + 64 * h + 32 * q);
+            if (SELF && cut) {
+              bits &= seen_bits(a, it.p0 + row_tok, first + 64 * h + 32 * q);
+              if (!__any_sync(0xffffffffu, bits != 0)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) wd[e] = 0u;
+                tmem_st16(tdP(b) + lane_off + 16 * q, wd);
+                return;
+              }
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 z =
