@@ -120,7 +120,8 @@ def df_rotary(x, positions, table, *, interleaved=False, inverse=False, amplitud
     if table.dtype != torch.int64 or table.dim() != 1:
         raise ValueError("table must be what df_rotary_table gives")
     if out is None:
-        outs = tuple([torch.empty(t.shape, dtype=dt, device=t.device) for t in xs])
+        outs = tuple([torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=dt, device=t.device)
+                      for t in xs])
     else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(outs) != n or any(o.dtype != dt or o.shape != t.shape for o, t in zip(outs, xs)):
@@ -166,6 +167,19 @@ def df_cache_new(n_pages, heads, page, d, device="cuda"):
     return torch.empty((n_pages, heads, page // BLOCK, 32 * d + 16), dtype=torch.uint8, device=device)
 
 
+def _on_device(tensors, names):
+    """``binding._on_device`` for tensors that are mostly as they should be (a small call is
+    bound by the host)."""
+    idx = tensors[0].get_device()
+    if idx >= 0:
+        for t in tensors:
+            if t is not None and not (t.get_device() == idx and t.is_contiguous()):
+                break
+        else:
+            return idx
+    return b._on_device(tensors, names)
+
+
 def _cache_shape(cache, page_table, lengths):
     """(sequences, heads, head size, pages, tokens of a page, pages of a sequence)."""
     shape, pages = cache.shape, page_table.shape
@@ -207,7 +221,7 @@ def df_cache_append(k, v, cache, page_table, lengths, cu_seqlens=None, *, status
     if stream is not None:
         with b._current(stream, k):
             return df_cache_append(k, v, cache, page_table, lengths, cu_seqlens, status=status)
-    idx = b._on_device((k, v, cache, page_table, lengths, cu_seqlens, status),
+    idx = _on_device((k, v, cache, page_table, lengths, cu_seqlens, status),
                        "k v cache page_table lengths cu_seqlens status")
     B, heads, d, n_pages, page, max_pages = _cache_shape(cache, page_table, lengths)
     if k.dtype not in b._DTYPE or v.dtype != k.dtype or v.shape != k.shape or tuple(k.shape[-2:]) != (heads, d):
@@ -235,11 +249,12 @@ def df_cache_read(cache, page_table, lengths, cu_seqlens=None, *, rows=None, dty
         shape = (int(rows), heads, d) if cu_seqlens is not None else (B, int(rows), heads, d)
         if not 0 <= shape[-3] < _INT:
             raise ValueError("rows is out of range")
-        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        out = k, torch.empty_like(k)
     k, v = out
     if k.dtype not in b._DTYPE or v.dtype != k.dtype or v.shape != k.shape or tuple(k.shape[-2:]) != (heads, d):
         raise ValueError("out must be two tensors of bf16, fp16 or fp32, with the cache's heads and head size")
-    idx = b._on_device((cache, page_table, lengths, cu_seqlens, k, v, status),
+    idx = _on_device((cache, page_table, lengths, cu_seqlens, k, v, status),
                        "cache page_table lengths cu_seqlens out out status")
     n, total = _cache_rows("out", k, cu_seqlens, B)
     if status is not None:
@@ -263,7 +278,7 @@ def df_cache_attn(q, cache, page_table, lengths, cu_seqlens_q=None, *, max_seqle
             return df_cache_attn(q, cache, page_table, lengths, cu_seqlens_q, max_seqlen_q=max_seqlen_q,
                                  max_length=max_length, causal=causal, window=window, sinks=sinks, scale=scale, out=out,
                                  lse=lse, status=status)
-    idx = b._on_device((q, cache, page_table, lengths, cu_seqlens_q, out, lse, status),
+    idx = _on_device((q, cache, page_table, lengths, cu_seqlens_q, out, lse, status),
                        "q cache page_table lengths cu_seqlens_q out lse status")
     B, heads, d, n_pages, page, max_pages = _cache_shape(cache, page_table, lengths)
     if q.dtype not in b._DTYPE or q.shape[-1] != d:
