@@ -685,32 +685,58 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
-// CTAs of `items` that share one, 1 to 8 (a cluster): the number for which the CTAs' rounds,
-// each as long as its share of the tiles and what it costs to begin and to join, are shortest.
-int splits_for(long long items, long long tiles, int rings, long long slots) {
+// Cluster sizes, and how many clusters of each a device holds at a time (found once for a kernel;
+// clusters stay within a part of the GPU, so that it is not the CTAs' number over their size).
+constexpr int kSizes[] = {1, 2, 3, 4, 6, 8, 12, 16}, kSizeCount = 8;
+struct Residency {
+  std::atomic<int> device{-1};
+  std::atomic<int> clusters[kSizeCount] = {};
+};
+
+template <typename Kernel>
+cudaError_t find_residency(Kernel kernel, int bytes, Residency* r) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || r->device.load(std::memory_order_acquire) == dev) return e;
+  e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int i = 0; i < kSizeCount && e == cudaSuccess; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSizes[i]);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSizes[i];
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    r->clusters[i].store(n, std::memory_order_relaxed);
+  }
+  if (e == cudaSuccess) r->device.store(dev, std::memory_order_release);
+  return e;
+}
+
+// CTAs that share an item (a cluster): the number for which the rounds, each as long as a CTA's
+// share of the tiles and what it costs to begin and to join, are shortest.  (8 key heads of 4
+// query heads, d = 128, one request: 16384 tokens 141 us with one CTA each, 24 with 8, 19 with
+// 16; four requests of 8192: 75 with one, 25 with 4, 20 with 8, 31 with 16.)
+int splits_for(long long items, long long tiles, int rings, const Residency& r) {
   constexpr long long kBegin = 6;  // in tiles of a warp
   int best = 1;
   long long least = LLONG_MAX;
-  for (int n = 1; n <= 8; ++n) {
-    const long long rounds = (items * n + slots - 1) / slots;
-    const long long cost = rounds * ((tiles + (long long)n * rings - 1) / (n * rings) + kBegin);
+  for (int i = 0; i < kSizeCount; ++i) {
+    const long long n = kSizes[i], held = r.clusters[i].load(std::memory_order_relaxed);
+    if (held < 1) continue;
+    const long long rounds = (items + held - 1) / held;
+    const long long cost = rounds * ((tiles + n * rings - 1) / (n * rings) + kBegin);
     if (cost < least) {
       least = cost;
-      best = n;
+      best = (int)n;
     }
   }
   return best;
-}
-
-// CTAs that an SM holds of a kernel (found once).
-cudaError_t residency(const void* kernel, int bytes, std::atomic<int>* known, int* per_sm) {
-  *per_sm = known->load(std::memory_order_relaxed);
-  if (*per_sm != 0) return cudaSuccess;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, kThreads, bytes);
-  if (e != cudaSuccess) return e;
-  *per_sm = std::max(*per_sm, 1);
-  known->store(*per_sm, std::memory_order_relaxed);
-  return cudaSuccess;
 }
 
 // Warps that share a ring, by the query rows.
@@ -722,13 +748,11 @@ cudaError_t launch(DecodeArgs a, long long tiles, cudaStream_t s) {
   auto kernel = decode_kernel<SLABS, WR, HALF>;
   constexpr int bytes = DecodeSmem<SLABS, WR>::bytes;
   static std::atomic<uint64_t> done{0};
-  static std::atomic<int> known{0};
-  int per_sm;
+  static Residency held;
   cudaError_t e = prepare_kernel((const void*)kernel, bytes, 0, &done);
-  if (e == cudaSuccess) e = residency((const void*)kernel, bytes, &known, &per_sm);
+  if (e == cudaSuccess) e = find_residency(kernel, bytes, &held);
   if (e != cudaSuccess) return e;
-  const long long slots = (long long)device_sms() * per_sm;
-  a.splits = splits_for(items, tiles, kWarps / WR, slots);
+  a.splits = splits_for(items, tiles, kWarps / WR, held);
   a.longest_first = a.B > 1 && a.B <= kThreads && items * a.splits > device_sms();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * a.splits));
@@ -801,7 +825,7 @@ extern "C" df_status df_cache_attn(const void* q, const int32_t* cu_seqlens_q, i
   a.budget = wait_budget();
   const int wr = warps_a_ring(Lq * a.G);
   a.row_tiles = (Lq * a.G + 16 * wr - 1) / (16 * wr);
-  if ((long long)B * Hk * a.row_tiles > 0x7fffffffll / 8) return DF_ERR_UNSUPPORTED;
+  if ((long long)B * Hk * a.row_tiles > 0x7fffffffll / 16) return DF_ERR_UNSUPPORTED;
   long long tiles = (std::min<long long>(max_length, (long long)max_pages * page) + kKeys - 1) / kKeys;
   if (window > 0) tiles = std::min<long long>(tiles, ((long long)window + Lq + sinks) / kKeys + 3);
   cudaStream_t s = (cudaStream_t)stream;
