@@ -116,6 +116,25 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, unsigned long long src, 
                : "memory");
 }
 
+// As cross_wait.  A copy lands within the time that one try may sleep, so that a budget below that
+// has to bound the try as well.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, unsigned long long budget,
+                                          volatile int* abort) {
+  if (budget > 100000) return cross_wait(bar, parity, budget, abort);
+  const long long t0 = clock64();
+  do {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((unsigned long long)(clock64() - t0) > budget) *abort = 1;
+  } while (*abort == 0);
+  return false;
+}
+
 // The tokens that a tile of query rows, at positions p0 .. p1, sees: those before `head` and
 // those from lo to end - 1; in tiles of kKeys, the first `heads` and then those from `skip`
 // tiles further on.
@@ -158,7 +177,6 @@ __device__ __forceinline__ void sequence(const DecodeArgs& a, int b, bool tell, 
   const bool bad = *held < 0 || *held > a.c.max_pages * a.c.page;  // (the product is at most 2^30)
   if (bad) *held = 0;
   if (tell && (bad || *nq > a.Lq)) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
-  *nq = min(*nq, a.Lq);  // rows that the launch has no worker for are left alone
 }
 __device__ __forceinline__ Rows rows_of(const DecodeArgs& a, int b, int hk, int rt, int per_tile, bool tell) {
   Rows w;
@@ -166,7 +184,8 @@ __device__ __forceinline__ Rows rows_of(const DecodeArgs& a, int b, int hk, int 
   sequence(a, b, tell, &w.q0, &nq, &w.held);
   w.b = b;
   w.hk = hk;
-  w.nr = min(per_tile, nq * a.G - rt * per_tile);
+  // (rows beyond Lq, for which there may be no worker, are left alone)
+  w.nr = min(per_tile, min(nq, a.Lq) * a.G - rt * per_tile);
   w.t0 = rt * per_tile / a.G;
   w.h0 = rt * per_tile - w.t0 * a.G;
   w.p0 = w.held - nq + w.t0;
@@ -610,14 +629,14 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
 #pragma unroll 1
   for (int i = 0; i < mine; ++i, stage.next()) {
     const int s = stage.at;
-    ok = __all_sync(0xffffffffu, cross_wait(full + s, stage.phase, a.budget, s_abort));
+    ok = __all_sync(0xffffffffu, ring_wait(full + s, stage.phase, a.budget, s_abort));
     if (!ok) break;
     done = i + 1;
     if (rows_here) st.tile(a, s_reach, ring + s * SL::kStageBytes, tile_first(i), have[s]);
     __syncwarp();
     if (WR > 1 && lane == 0) mbar_arrive(empty + s);
     if (producer && i + S < mine) {
-      if (WR > 1 && !__all_sync(0xffffffffu, cross_wait(empty + s, stage.phase, a.budget, s_abort))) break;
+      if (WR > 1 && !__all_sync(0xffffffffu, ring_wait(empty + s, stage.phase, a.budget, s_abort))) break;
       feed.issue(i + S, s);
     }
   }
