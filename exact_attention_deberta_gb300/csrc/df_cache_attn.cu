@@ -33,7 +33,6 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 // A tile is the keys of one copy: two blocks.  (Four at d = 64: 166 us where two take 160, for 24
 // heads and 64 requests of up to 8192 tokens; one at d = 128: the same as two.)
 constexpr int NB = 2, kKeys = NB * kBlock;
@@ -49,17 +48,17 @@ struct DecodeArgs {
   unsigned by_G;        // 65536 / G + 1
   int row_tiles;        // CTAs that share a sequence's query rows
   int splits;           // and its keys (cluster size)
-  int longest_first;    // (at most kThreads sequences)
+  int longest_first;    // (at most a CTA's threads)
   int causal, window, sinks, bf16;
   float kscale;         // scale log2(e)
   int32_t* status;
   unsigned long long budget;
 };
 
-template <int SLABS, int WR>
+template <int SLABS, int WR, int WARPS>
 struct DecodeSmem {
   static constexpr int D = 32 * SLABS;
-  static constexpr int kRings = kWarps / WR;
+  static constexpr int kRings = WARPS / WR;
   static constexpr int kStages = SLABS == 1 ? 6 : SLABS == 2 ? 3 : 2;
   static constexpr uint32_t kRecord = 32 * D + 16;
   static constexpr uint32_t kStageBytes = NB * kRecord;
@@ -67,11 +66,11 @@ struct DecodeSmem {
   static constexpr uint32_t ring_bytes = kRings * kStages * kStageBytes;
   // after the loop, over the ring: each warp's O, and the CTA's
   static constexpr int kPitch = D + 4;
-  static constexpr uint32_t o_warp = 0;  // float [kWarps][16][kPitch]
-  static constexpr uint32_t o_cta = kWarps * 16 * kPitch * 4;  // float [16 WR][D]
+  static constexpr uint32_t o_warp = 0;  // float [WARPS][16][kPitch]
+  static constexpr uint32_t o_cta = WARPS * 16 * kPitch * 4;  // float [16 WR][D]
   static constexpr uint32_t joined = o_cta + 16 * WR * D * 4;
-  static constexpr uint32_t ml_warp = (ring_bytes > joined ? ring_bytes : joined);  // float2 [kWarps][16]
-  static constexpr uint32_t ml_cta = ml_warp + kWarps * 16 * 8;                     // float4 [16 WR]
+  static constexpr uint32_t ml_warp = (ring_bytes > joined ? ring_bytes : joined);  // float2 [WARPS][16]
+  static constexpr uint32_t ml_cta = ml_warp + WARPS * 16 * 8;                     // float4 [16 WR]
   static constexpr uint32_t bars = ml_cta + 64 * 16;                                // full, empty [kRings][kStages]
   static constexpr uint32_t have = bars + 2 * kRings * kStages * 8;                 // int [kRings][kStages]
   static constexpr uint32_t recs = (have + kRings * kStages * 4 + 7) & ~7u;  // 64-bit [kRings][32 tiles][blocks]: records to copy
@@ -228,7 +227,7 @@ __device__ __forceinline__ void records_at(const DecodeArgs& a, const Reach& rea
 __device__ __forceinline__ int key_of(int t, int i) { return 4 * i + ((t + 2 * (i & 1)) & 3); }
 
 // A warp's 16 query rows and their running state; HALF: the upper 8 are empty.
-template <int SLABS, bool HALF>
+template <int SLABS, bool HALF, bool ACROSS>
 struct Softmax {
   static constexpr int D = 32 * SLABS, kHalves = HALF ? 1 : 2;
   static constexpr uint32_t kRecord = 32 * D + 16;
@@ -313,23 +312,35 @@ struct Softmax {
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) f[blk][h] = fmaxf(__uint_as_float(sw.x) * ks_row[h], 1.17549435e-38f);
       vs[blk] = __uint_as_float(sw.y);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t row = rec + 32 * key_of(g >> 1, 2 * j + (g & 1)) + 8 * t;
-#pragma unroll
-        for (int c = 0; c < SLABS; ++c) {
-          const uint2 x = lds64(row + 512 * c);
-          uint32_t b0, b1;
-          codes4_f16(x.x, b0, b1);
-          if (c == 0)
-            mma_f16_first(sc[blk][j], qa[c][0], b0, b1);
-          else
-            mma_f16(sc[blk][j], qa[c][0], b0, b1);
-          codes4_f16(x.y, b0, b1);
-          mma_f16(sc[blk][j], qa[c][1], b0, b1);
-        }
-      }
     }
+    // Products in the order of their sums, or, so that those that follow one another are of different
+    // sums, slab by slab of all keys: long rows that leave the registers for it (d = 128, a key head's
+    // 4 heads, one request of 65536 tokens: 53 -> 48 us; 8 rows of 16 tokens: 107 -> 102; but d = 64,
+    // 64 requests: 161 -> 162, and 16 rows of d = 128: 33.1 -> 33.8).
+    constexpr int kOuter = ACROSS ? 1 : 2 * NB, kInner = ACROSS ? 2 * NB : 1;
+#pragma unroll
+    for (int out = 0; out < kOuter; ++out)
+#pragma unroll
+      for (int c = 0; c < SLABS; ++c) {
+        uint2 x[kInner];
+#pragma unroll
+        for (int i = 0; i < kInner; ++i) {
+          const int at = out + i, blk = at >> 1, j = at & 1;
+          x[i] = lds64(base + blk * kRecord + 32 * key_of(g >> 1, 2 * j + (g & 1)) + 8 * t + 512 * c);
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int i = 0; i < kInner; ++i) {
+            float(&to)[4] = sc[(out + i) >> 1][(out + i) & 1];
+            uint32_t b0, b1;
+            codes4_f16(part ? x[i].y : x[i].x, b0, b1);
+            if (c == 0 && part == 0)
+              mma_f16_first(to, qa[0][0], b0, b1);
+            else
+              mma_f16(to, qa[c][part], b0, b1);
+          }
+      }
     uint32_t gone = 0;  // of this lane's keys (t, i), bit 4 blk + i: those that no row counts
     if (!whole) {
 #pragma unroll
@@ -546,7 +557,6 @@ struct Stage {
 template <typename SL>
 __device__ __forceinline__ void init_bars(uint8_t* sm, int wr) {
   constexpr int n = SL::kRings * SL::kStages;
-  static_assert(2 * n <= kThreads, "a thread for each barrier");
   if (threadIdx.x < 2 * n) {
     mbar_init(reinterpret_cast<uint64_t*>(sm + SL::bars) + threadIdx.x, threadIdx.x < n ? 1 : wr);
     mbar_fence_init();
@@ -556,9 +566,11 @@ __device__ __forceinline__ void init_bars(uint8_t* sm, int wr) {
 }
 
 // A CTA, or a cluster of them, for each sequence, key head and tile of query rows.
-template <int SLABS, int WR, bool HALF>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
-  using SL = DecodeSmem<SLABS, WR>;
+template <int SLABS, int WR, bool HALF, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) decode_kernel(const DecodeArgs a) {
+  using SL = DecodeSmem<SLABS, WR, WARPS>;
+  constexpr int kThreads = 32 * WARPS;
+  static_assert(2 * SL::kRings * SL::kStages <= kThreads && kThreads <= 256, "a thread for each barrier, room for lengths");
   constexpr int D = SL::D, S = SL::kStages, R = SL::kRings;
   constexpr int kHalves = HALF ? 1 : 2;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -620,7 +632,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const DecodeArgs a) {
   if (producer)
     for (int i = 0; i < min(S, mine); ++i) feed.issue(i, i);
 
-  Softmax<SLABS, HALF> st;
+  Softmax<SLABS, HALF, SLABS >= 3 && (HALF || WR == 4)> st;
   st.begin(a, w, part);
   const bool rows_here = 16 * part < w.nr;
   bool ok = true;
@@ -713,7 +725,7 @@ struct Residency {
 };
 
 template <typename Kernel>
-cudaError_t find_residency(Kernel kernel, int bytes, Residency* r) {
+cudaError_t find_residency(Kernel kernel, int threads, int bytes, Residency* r) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || r->device.load(std::memory_order_acquire) == dev) return e;
@@ -721,7 +733,7 @@ cudaError_t find_residency(Kernel kernel, int bytes, Residency* r) {
   for (int i = 0; i < kSizeCount && e == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSizes[i]);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = bytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -738,54 +750,81 @@ cudaError_t find_residency(Kernel kernel, int bytes, Residency* r) {
 }
 
 // CTAs that share an item (a cluster): the number for which the rounds, each as long as a CTA's
-// share of the tiles and what it costs to begin and to join, are shortest.  (8 key heads of 4
-// query heads, d = 128, one request: 16384 tokens 141 us with one CTA each, 24 with 8, 19 with
-// 16; four requests of 8192: 75 with one, 25 with 4, 20 with 8, 31 with 16.)
-int splits_for(long long items, long long tiles, int rings, const Residency& r) {
-  constexpr long long kBegin = 6;  // in tiles of a warp
-  int best = 1;
+// share of the tiles and what it costs to begin and to join, are shortest; their cost, in tiles of a
+// warp. (8 key heads of 4 query heads, d = 128, one request: 16384 tokens 141 us with one CTA
+// each, 24 with 8, 18 with 16; four requests of 8192: 75 with one, 25 with 4, 20 with 8, 31 with 16.)
+long long splits_for(long long items, long long tiles, int rings, const Residency& r, int* splits, long long* rounds) {
+  constexpr long long kBegin = 6;
   long long least = LLONG_MAX;
   for (int i = 0; i < kSizeCount; ++i) {
     const long long n = kSizes[i], held = r.clusters[i].load(std::memory_order_relaxed);
     if (held < 1) continue;
-    const long long rounds = (items + held - 1) / held;
-    const long long cost = rounds * ((tiles + n * rings - 1) / (n * rings) + kBegin);
+    const long long turns = (items + held - 1) / held;
+    const long long cost = turns * ((tiles + n * rings - 1) / (n * rings) + kBegin);
     if (cost < least) {
       least = cost;
-      best = (int)n;
+      *splits = (int)n;
+      *rounds = turns;
     }
   }
-  return best;
+  return least;
 }
 
 // Warps that share a ring, by the query rows.
 int warps_a_ring(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
+template <int SLABS, int WR, bool HALF, int WARPS>
+struct Launch {
+  static constexpr int bytes = DecodeSmem<SLABS, WR, WARPS>::bytes, threads = 32 * WARPS;
+  int splits = 1;
+  long long rounds = 0, cost = LLONG_MAX;
+
+  cudaError_t plan(long long items, long long tiles) {
+    static std::atomic<uint64_t> done{0};
+    static Residency held;
+    auto kernel = decode_kernel<SLABS, WR, HALF, WARPS>;
+    cudaError_t e = prepare_kernel((const void*)kernel, bytes, 0, &done);
+    if (e == cudaSuccess) e = find_residency(kernel, threads, bytes, &held);
+    if (e == cudaSuccess) cost = splits_for(items, tiles, WARPS / WR, held, &splits, &rounds);
+    return e;
+  }
+  cudaError_t run(DecodeArgs a, long long items, cudaStream_t s) const {
+    a.splits = splits;
+    a.longest_first = a.B > 1 && a.B <= threads && items * splits > device_sms();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * splits));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<SLABS, WR, HALF, WARPS>, a);
+  }
+};
+
 template <int SLABS, int WR, bool HALF>
-cudaError_t launch(DecodeArgs a, long long tiles, cudaStream_t s) {
+cudaError_t launch(const DecodeArgs& a, long long tiles, cudaStream_t s) {
   const long long items = (long long)a.B * a.c.Hk * a.row_tiles;
-  auto kernel = decode_kernel<SLABS, WR, HALF>;
-  constexpr int bytes = DecodeSmem<SLABS, WR>::bytes;
-  static std::atomic<uint64_t> done{0};
-  static Residency held;
-  cudaError_t e = prepare_kernel((const void*)kernel, bytes, 0, &done);
-  if (e == cudaSuccess) e = find_residency(kernel, bytes, &held);
+  Launch<SLABS, WR, HALF, 4> four;
+  cudaError_t e = four.plan(items, tiles);
   if (e != cudaSuccess) return e;
-  a.splits = splits_for(items, tiles, kWarps / WR, held);
-  a.longest_first = a.B > 1 && a.B <= kThreads && items * a.splits > device_sms();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * a.splits));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  // Few items of long rows: eight warps a CTA, for a cluster's size is limited, and what a tile takes a
+  // warp is latency (8 key heads of 4 heads, d = 128, one request: 4096 tokens 9.8 -> 8.4 us, 16384
+  // 18.4 -> 15.4, 65536 48 -> 37). In more than one round four are as good or better, their CTAs' ends
+  // and beginnings overlap (200 requests of 1000 tokens: 75 us, with eight 129); d = 64 gains nothing
+  // (2 requests of 16384, 24 heads: 24.5, with eight 29.2).
+  if constexpr (HALF && SLABS >= 3) {
+    Launch<SLABS, WR, HALF, 8> eight;
+    e = eight.plan(items, tiles);
+    if (e != cudaSuccess) return e;
+    if (eight.rounds == 1 && eight.cost <= four.cost) return eight.run(a, items, s);
+  }
+  return four.run(a, items, s);
 }
 
 template <int SLABS>
