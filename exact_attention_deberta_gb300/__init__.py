@@ -1,5 +1,6 @@
 """Exact DeBERTa-v2/v3 disentangled attention for NVIDIA GB300, with the steps around
-it: token embeddings, projections, and the cross attention that reads the states.
+it: token embeddings, projections, the cross attention that reads the states, and a
+decoder's own attention (rotary positions, causal attention, a cache in 8 bits).
 
 The computation lives in ``libdfattn.so`` (hand-written sm_103a CUDA behind the
 C ABI of ``include/df_attn.h``); ``binding`` is its ctypes marshalling layer and

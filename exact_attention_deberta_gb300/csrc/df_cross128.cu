@@ -34,6 +34,11 @@
 // of one team each per SM, whose ends overlap better but which cannot take turns,
 // took 1094 us where this layout took 1034.  An item's end costs about 5000 cycles:
 // its code has left the instruction caches by then, so it is kept short.
+//
+// SELF: causal attention with a window and sinks, as in df_cross64.cu; 64 columns that no
+// row of a warp sees get no exponentials.  Measured: 16 x 16 heads sharing 4, 2048 tokens,
+// bf16: 302 us, 910 TFLOP/s of what is seen; 8 x 16 heads sharing 4, 8192 tokens, a window of
+// 1024 and 4 sinks: 669 us.
 #include "df_cross_fwd.cuh"
 
 namespace dfa {

@@ -2,8 +2,10 @@
  * df_attn.h -- C ABI of the exact DeBERTa-v2/v3 disentangled attention for
  * NVIDIA GB300 (sm_103a): the fused forward pass, its backward pass, the
  * forward from host buffers, and the steps on either side of the attention
- * (padded <-> packed conversion, projections, LayerNorm, token embeddings, and
- * the cross attention of a decoder or reader to the encoder's states).
+ * (padded <-> packed conversion, projections, LayerNorm, token embeddings,
+ * the cross attention of a decoder or reader to the encoder's states, and a
+ * decoder's own attention: rotary positions, causal attention with a window, a
+ * cache of keys and values in 8 bits).
  *
  * The operation (DisentangledFlash 0.2.0 README, section "Status":
  * "DeBERTa-v2/v3-style C2P/P2C disentangled attention", "factorized 2-D padding
