@@ -66,11 +66,11 @@ int device_sms() {
   return sms;
 }
 
-long long cross_query_tiles(const CrossArgs& a) {
-  const long long per = (a.Lq + a.tpt - 1) / a.tpt;
+long long cross_query_tiles(const CrossArgs& a, int group) {
+  const long long step = (long long)group * a.tpt, per = (a.Lq + step - 1) / step;
   if (!a.cu_q) return per * a.B * a.Hk;
   // packed: every sequence and the rows behind the last one end in a tile of their own
-  return ((long long)a.Tq / a.tpt + a.B + 1) * a.Hk;
+  return ((long long)a.Tq / step + a.B + 1) * a.Hk;
 }
 
 bool self_reach(int* window, int* sinks) {
@@ -172,6 +172,10 @@ static df_status forward(bool self, int window, int sinks, const void* q, const 
   a.split_bits = a.splits == 8 ? 3 : a.splits / 2;
   const int grid = (int)items * a.splits;
   cudaStream_t s = (cudaStream_t)stream;
+  const long long pairs = cross_query_tiles(a.c, 2);
+  static const int kPairs = getenv("PAIRS") ? atoi(getenv("PAIRS")) : 1;
+  if (self && d <= 64 && a.splits == 1 && pairs >= kPairs * sms)
+    return launch_self64(a, maps, bf16, (int)pairs, s) == cudaSuccess ? DF_OK : DF_ERR_CUDA;
   const cudaError_t e =
       d <= 64 ? launch_cross64(a, maps, bf16, self, grid, s) : launch_cross128(a, maps, bf16, self, grid, s);
   return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;

@@ -363,8 +363,8 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
                       float scale, df_dtype dtype, int32_t* status, CrossArgs* a);
 // Self attention: whether window and sinks are in range; puts what sees everything as window 0.
 bool self_reach(int* window, int* sinks);
-// An upper bound of the number of query tiles.
-long long cross_query_tiles(const CrossArgs& a);
+// An upper bound of the number of query tiles, or of `group` of them.
+long long cross_query_tiles(const CrossArgs& a, int group = 1);
 unsigned long long wait_budget();
 
 }  // namespace dfa

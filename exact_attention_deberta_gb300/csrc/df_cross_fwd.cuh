@@ -22,6 +22,7 @@ struct FwdMaps {
 };
 
 cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s);
+cudaError_t launch_self64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s);
 cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s);
 constexpr int kFwdKeys = 128;  // keys per tile
 
