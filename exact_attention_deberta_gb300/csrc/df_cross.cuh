@@ -29,6 +29,7 @@ struct CrossArgs {
   int32_t* status;
   unsigned long long budget;
   int window, sinks;         // self attention: see below
+  int group;                 // self attention: key heads whose query tiles are numbered together
 };
 
 // A tile of one side's rows (queries, or keys in the backward's key kernel)
@@ -286,8 +287,18 @@ struct TileWalk {
         break;
       }
     }
-    it.hk = at / tiles;
-    const int turn = at - it.hk * tiles, tok = (SELF && !KEYS ? tiles - 1 - turn : turn) * step;
+    int turn;
+    if (SELF && !KEYS) {
+      const int group = at / (a.group * tiles), in = at - group * (a.group * tiles);
+      const int heads = min(a.group, a.Hk - group * a.group);
+      turn = in / heads;
+      it.hk = group * a.group + in - turn * heads;
+      turn = tiles - 1 - turn;
+    } else {
+      it.hk = at / tiles;
+      turn = at - it.hk * tiles;
+    }
+    const int tok = turn * step;
     it.r0 = first + tok;
     it.nr = min(step, len - tok);
     if (it.b < a.B) it.no = seq_rows(other, it.b, a.status, &it.o0);

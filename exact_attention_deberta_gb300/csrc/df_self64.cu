@@ -38,9 +38,9 @@ struct PairSmem {
   static constexpr uint32_t k = q + 4 * kTileBytes;                 // [kStages][K tile]
   static constexpr uint32_t v = k + kStages * kTileBytes;           // [kStages][V tile]
   static constexpr uint32_t bars = v + kStages * kTileBytes;
-  // q_full, q_empty [2]; k_full, k_empty, v_full, v_empty [kStages]; s_full,
-  // buf_free, drain [3]; p_full, pv_done [2][4]; item_full, item_empty; claim
-  static constexpr int kBars = 4 + 4 * kStages + 9 + 16 + 2 * (int)kItemRing + 1;
+  // q_full, q_empty [2]; k_full, k_empty, v_full, v_empty [kStages]; buf_free, drain [3];
+  // s_full, p_full, pv_done [2][4]; item_full, item_empty; claim
+  static constexpr int kBars = 4 + 4 * kStages + 6 + 24 + 2 * (int)kItemRing + 1;
   static constexpr uint32_t ring = (bars + kBars * 8 + 15) & ~15u;  // CrossItem slots of 32 bytes
   static constexpr uint32_t cur = ring + 32 * kItemRing;            // [2 warpgroups][2] current items
   static constexpr uint32_t claim = cur + 128;                      // 16 bytes
@@ -51,13 +51,13 @@ struct PairSmem {
 };
 
 // The key tiles of an item, `n` of both query tiles together: the first warpgroup sees the first
-// `na`, the second (if it has rows) all but `skip` from `from` on.
+// `na`, the second all but `skip` from `from` on (none where it has no rows).
 struct PairTiles {
   CrossBand band;
-  int n, na, from, skip;
-  bool second;
+  int n, na, from;
+  unsigned skip;
   __device__ __forceinline__ bool sees(int w, int t) const {
-    return w == 0 ? t < na : second && (unsigned)(t - from) >= (unsigned)skip;
+    return w == 0 ? t < na : (unsigned)(t - from) >= skip;
   }
 };
 __device__ __forceinline__ int band_tiles(const CrossBand& band, int keys) {
@@ -72,11 +72,11 @@ __device__ __forceinline__ PairTiles pair_tiles(const CrossArgs& a, const CrossI
   part.nr = min(it.nr, a.tpt);
   clip_causal(part);
   p.na = min(p.n, band_tiles(p.band, part.no));
-  p.second = it.nr > a.tpt;
   part.no = it.no;
   part.p0 = it.p0 + a.tpt;
-  p.from = p.band.sinks;
-  p.skip = key_band(a, part).skip - p.band.skip;
+  const bool second = it.nr > a.tpt;
+  p.from = second ? p.band.sinks : 0;
+  p.skip = second ? (unsigned)(key_band(a, part).skip - p.band.skip) : UINT_MAX;
   return p;
 }
 
@@ -102,13 +102,14 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
   uint64_t* k_empty = k_full + R;
   uint64_t* v_full = k_empty + R;
   uint64_t* v_empty = v_full + R;      // both P.V warps
-  uint64_t* s_full = v_empty + R;      // [3] S of the buffer computed
-  uint64_t* buf_free = s_full + 3;     // [3] the P.V that read the buffer is done
+  uint64_t* buf_free = v_empty + R;    // [3] the P.V that read the buffer is done
   uint64_t* drain = buf_free + 3;      // [3], one per issuing warp
-  // [wg][n & 3]: the four warps of wg stored P of its n-th step; P.V of it done.  A warp may be
-  // through with steps n + 1 and n + 2 before a sibling has stored n, but not with n + 3: its
-  // scores wait for a buffer that P.V of n, or of a step behind it, frees.
-  uint64_t* p_full = drain + 3;
+  // [wg][n & 3]: S of the n-th step of wg computed; its four warps stored P of it; P.V of it done.
+  // (By its own steps, not by buffers: a warpgroup without rows in some items is far ahead of the
+  // other's steps.)  A warp may be through with steps n + 1 and n + 2 before a sibling has stored
+  // n, but not with n + 3: its scores wait for a buffer that P.V of n, or of a step behind it, frees.
+  uint64_t* s_full = drain + 3;
+  uint64_t* p_full = s_full + 8;
   uint64_t* pv_done = p_full + 8;
   uint64_t* item_full = pv_done + 8;
   uint64_t* item_empty = item_full + kItemRing;
@@ -131,11 +132,11 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
       mbar_init(v_empty + s, 2);
     }
     for (int b = 0; b < 3; ++b) {
-      mbar_init(s_full + b, 1);
       mbar_init(buf_free + b, 1);
       mbar_init(drain + b, 1);
     }
     for (int b = 0; b < 8; ++b) {
+      mbar_init(s_full + b, 1);
       mbar_init(p_full + b, 4);
       mbar_init(pv_done + b, 1);
     }
@@ -267,12 +268,12 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
     const bool qk_role = warp == 1;
     const int pv_wg = warp == 3 ? 0 : 1;  // the warpgroup whose steps this warp multiplies
     uint32_t g = 0, qc = 0, pn = 0;       // key tiles and items before this one, steps whose P has been consumed
+    uint32_t n0 = 0, n1 = 0;              // the warpgroups' steps whose S has been issued
     uint32_t sb = 0, phase = 0;           // buffer of the next step of both, and how often it came round
-    auto next_step = [&]() {
-      if (++sb == 3) {
-        sb = 0;
-        phase ^= 1;
-      }
+    auto pass = [&](bool step) {
+      sb += step;
+      phase ^= sb == 3;
+      sb = sb == 3 ? 0 : sb;
     };
     const uint32_t to = uniform(tO(pv_wg));
     const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sm + SL::k), v_addr = smem_u32(sm + SL::v);
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
           const uint32_t gs = g + t, s = gs % R;
           const uint64_t dk = uniform(sdesc_sw128(k_addr + s * SL::kTileBytes, 16, 1024));
           ok = ok && cross_wait(k_full + s, (gs / R) & 1, budget, s_abort);
-#pragma unroll 1
+#pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!pt.sees(w, t)) continue;
             const uint64_t dq = uniform(sdesc_sw128(q_addr + (2 * qb + w) * SL::kTileBytes, 16, 1024));
@@ -309,11 +310,15 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
               if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) mma_ss(ts, dq + kmajor_step(k), dk + kmajor_step(k), kIdescQK, k > 0);
-                mma_commit(s_full + sb);
+                mma_commit(s_full + 4 * w + (w == 0 ? n0 & 3 : n1 & 3));
               }
               __syncwarp();
             }
-            next_step();
+            if (w == 0)
+              ++n0;
+            else
+              ++n1;
+            pass(true);
           }
           ok = __all_sync(0xffffffffu, ok);
           if (ok && elect_one()) mma_commit(k_empty + s);
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
 #pragma unroll 1
         for (int t = 0; t < pt.n; ++t) {
           const uint32_t gs = g + t, s = gs % R;
-          if (pv_wg == 1 && pt.sees(0, t)) next_step();
+          pass(pv_wg == 1 && pt.sees(0, t));
           if (!pt.sees(pv_wg, t)) {
             // (not before the tile has come: the arrival would count for the one before)
             ok = ok && cross_wait(v_full + s, (gs / R) & 1, budget, s_abort);
@@ -362,9 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
             }
             first = 1;
             ++pn;
-            next_step();
+            pass(true);
           }
-          if (pv_wg == 0 && pt.sees(1, t)) next_step();
+          pass(pv_wg == 0 && pt.sees(1, t));
         }
       }
       g += pt.n;
@@ -388,12 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
     const int row_tok = row / a.G, row_head = row - row_tok * a.G;
     CrossItem* s_cur = reinterpret_cast<CrossItem*>(sm + SL::cur) + 2 * wg;
     uint32_t own = 0;                        // this warpgroup's steps so far
-    uint32_t sb = 0, phase = 0;              // buffer of the next step of both, and how often it came round
-    auto next_step = [&]() {
-      if (++sb == 3) {
-        sb = 0;
-        phase ^= 1;
-      }
+    uint32_t sb = 0;                         // buffer of the next step of both
+    auto pass = [&](bool step) {
+      sb += step;
+      sb = sb == 3 ? 0 : sb;
     };
     auto pv_wait = [&](uint32_t n) {  // until P.V of its n-th step is done
       cross_wait(pv_done + 4 * wg + (n & 3), (n >> 2) & 1, budget, s_abort);
@@ -406,11 +409,18 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
     if (reader) s_cur[0] = read_item(0);
     named_sync(3 + wg, 128);
     for (;;) {
-      const CrossItem it = s_cur[~c & 1];
-      if (it.hk < 0) break;
-      const PairTiles pt = pair_tiles(a, it);
-      const int nr = min(it.nr - wg * a.tpt, a.tpt), p0 = it.p0 + wg * a.tpt;  // this warpgroup's tokens
-      const bool row_in = row_tok < nr;
+      // (what a step needs of the item is read again, and is in no register beside the scores)
+      const volatile CrossItem* it = s_cur + (~c & 1);
+      if (it->hk < 0) break;
+      PairTiles pt;
+      {
+        CrossItem x;
+        x.nr = it->nr;
+        x.no = it->no;
+        x.p0 = it->p0;
+        pt = pair_tiles(a, x);
+      }
+      const bool row_in = row_tok < min(it->nr - wg * a.tpt, a.tpt);
       // a row block without a valid row needs no weights: its P may hold anything,
       // since a row of P only reaches its own row of O
       const bool warp_in = __any_sync(0xffffffffu, row_in);
@@ -418,40 +428,25 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
       bool o_has = false;
 #pragma unroll 1
       for (int t = 0; t < pt.n; ++t) {
-        if (wg == 1 && pt.sees(0, t)) next_step();
+        pass(wg == 1 && pt.sees(0, t));
         if (pt.sees(wg, t)) {
           const uint32_t tSw = tmem + 128u * sb + lane_off;
-          cross_wait(s_full + sb, phase, budget, s_abort);
+          cross_wait(s_full + 4 * wg + (own & 3), (own >> 2) & 1, budget, s_abort);
           __syncwarp();
           tc_fence_after();
           if (warp_in) {
-            const int kt = pt.band.tile(t);
-            const bool cut = !seen_whole(a, p0, nr, kt * 128);
-            if (a.key_mask || it.no < kt * 128 + 128 || cut) {
-              const int left = it.no - kt * 128;
-              uint32_t bits[4];
+            const int kt = pt.band.tile(t), left = it->no - kt * 128, p0 = it->p0 + wg * a.tpt;
+            const bool cut = !seen_whole(a, p0, min(it->nr - wg * a.tpt, a.tpt), kt * 128);
+            uint32_t bits[4];
+            bool part = false;
+            if (a.key_mask || left < 128 || cut) {
               const bool all =
-                  key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)kt * 128 : nullptr, left, bits);
+                  key_bits(a.key_mask ? a.key_mask + (size_t)it->b * a.Lk + (size_t)kt * 128 : nullptr, left, bits);
               if (cut) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) bits[w] &= seen_bits(a, p0 + row_tok, kt * 128 + 32 * w);
               }
-              if (!all || cut) {
-                // the scores of keys that do not count become -inf in place (kept out of
-                // the straight code below, which the instruction caches have to hold)
-#pragma unroll 1
-                for (int w = 0; w < 4; ++w) {
-                  const uint32_t word = w == 0 ? bits[0] : w == 1 ? bits[1] : w == 2 ? bits[2] : bits[3];
-                  uint32_t r[32];
-                  tmem_ld32(tSw + 32 * w, r);
-                  tmem_ld_wait(r);
-#pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (!((word >> j) & 1u)) r[j] = 0xff800000u;
-                  tmem_st32(tSw + 32 * w, r);
-                }
-                tmem_st_wait();
-              }
+              part = !all || cut;
             }
             float x[128];
             {
@@ -468,6 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
                 x[64 + e] = __uint_as_float(r2[e]);
                 x[96 + e] = __uint_as_float(r3[e]);
               }
+            }
+            if (__builtin_expect(part, 0)) {
+#pragma unroll
+              for (int j = 0; j < 128; ++j)
+                if (!((bits[j >> 5] >> (j & 31)) & 1u)) x[j] = -INFINITY;
             }
             // row maximum of the raw scores (the scale is positive)
             float mx[8];
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
           mbar_arrive_if(lane == 0, p_full + 4 * wg + (own & 3));
           o_has = true;
           ++own;
-          next_step();
+          pass(true);
         }
-        if (wg == 0 && pt.sees(1, t)) next_step();
+        pass(wg == 0 && pt.sees(1, t));
       }
       // ---- the item's end
       if (reader) s_cur[c & 1] = read_item(c);  // the next one
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
       // (a NaN among the scores of keys that count is in l, and stays in the row)
       const float inv = l_run != 0.f ? rcp(l_run) : 0.f;
       const bool any = o_has && l_run != 0.f;
-      const size_t orow = ((size_t)(it.r0 + wg * a.tpt + row_tok) * a.H + (size_t)it.hk * a.G + row_head);
+      const size_t orow = ((size_t)(it->r0 + wg * a.tpt + row_tok) * a.H + (size_t)it->hk * a.G + row_head);
 #pragma unroll 1
       for (int col = 0; warp_in && col < D; col += 16) {
         uint32_t r[16];
