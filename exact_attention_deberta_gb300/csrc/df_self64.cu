@@ -26,8 +26,8 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 384;
-constexpr int kRegs = 168;  // launched; after the split eight softmax warps have 224, four others 56
-static_assert(256 * 224 + 128 * 56 <= kThreads * kRegs, "setmaxnreg.inc must not wait");
+constexpr int kRegs = 168;  // launched; after the split eight softmax warps have 216, four others 72
+static_assert(256 * 216 + 128 * 72 <= kThreads * kRegs, "setmaxnreg.inc must not wait");
 constexpr uint32_t kItemRing = 4;
 
 struct PairSmem {
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
 
   if (warp == 0) {
     // ------------------------------------------------------------ items and loads
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<72>();
     // (the whole warp runs every step, and one lane of it issues)
     TileWalk<true> walk;
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
   } else if (warp < 4) {
     // ------------------------------------------------------------ MMA issuers
     // (whole warps, so that the one that issues a P.V can zero rows of V first)
-    setmaxnreg_dec<56>();
+    setmaxnreg_dec<72>();
     const bool qk_role = warp == 1;
     const int pv_wg = warp == 3 ? 0 : 1;  // the warpgroup whose steps this warp multiplies
     uint32_t g = 0, qc = 0, pn = 0;       // key tiles and items before this one, steps whose P has been consumed
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax warpgroups
-    setmaxnreg_inc<224>();
+    setmaxnreg_inc<216>();
     const int wg = (warp - 4) >> 2;
     const int quad = warp & 3;               // TMEM lane quadrant of this warp
     const int row = quad * 32 + lane;
