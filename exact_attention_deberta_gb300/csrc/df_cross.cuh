@@ -223,7 +223,8 @@ __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
 // the rows behind the last sequence count as one more sequence, whose other
 // side is empty.  The walk over packed sequences goes on from the last call's number,
 // in either direction.  SELF: a sequence's query tiles are numbered from its end, which
-// sees most keys (long items first), and a key tile meets the queries that see it.
+// sees most keys, `group` key heads together (long items first), and a key tile meets the
+// queries that see it.
 template <bool SELF = false, bool KEYS = false>
 struct TileWalk {
   int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones

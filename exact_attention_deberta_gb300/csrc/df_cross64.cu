@@ -38,15 +38,12 @@
 // (828) and one warp issuing both products in order (1138) were slower (735 at the
 // time).
 //
-// SELF: causal attention with a window and sinks (df_cross.cuh).  Key tiles that no row
-// of an item sees are not on its list; where some row does not see a key, a thread finds
-// its row's bits from two positions, and a tile that every row sees whole takes the path
-// without bits.  Sequences' query tiles run from the last, which has the most keys, to the
-// first.  Measured: 4 x 12 heads, 8192 tokens, bf16: 413 us, 998 TFLOP/s of what is seen
-// (4 flops a score and column); 16 x 12 heads, 8192 tokens, a window of 1024 and 4 sinks:
-// 730 us (without sinks 658).  There an item has nine or ten tiles, and its end costs as
-// much as eight: 951 cycles a tile, 7600 an item, of which 2300 are the rows' bits in the
-// tiles at the window's ends, 1400 the rows' stores, 1200 the reading of both O.
+// SELF: causal attention with a window and sinks (df_cross.cuh) where there is little of it
+// (df_self64.cu: more).  Key tiles that no row of an item sees are not on its list; where some
+// row does not see a key, a thread finds its row's bits from two positions, and a tile that
+// every row sees whole takes the path without bits.  Sequences' query tiles run from the last,
+// which has the most keys, to the first.  Measured: 12 heads, one sequence of 1024 tokens: 12 us,
+// 2048: 16; 8 heads of 4096: 25 us, 690 TFLOP/s of what is seen (4 flops a score and column).
 #include "df_cross_fwd.cuh"
 
 namespace dfa {

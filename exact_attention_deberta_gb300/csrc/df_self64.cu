@@ -17,6 +17,18 @@
 //               the rows of V whose keys do not count first;
 //   warps 4-11  softmax: one thread per row, P (rounded to the I/O type) written over its S.
 // Three score buffers rotate over the steps of both.
+//
+// Keys that a row does not see: the scores of a tile that not every row sees whole become -inf in
+// registers, in code of its own (in place in tensor memory, as the whole tile's code is shorter then:
+// 546 us against 481 with a window of 1024; by a minimum with infinities, a block for each end of the
+// window: 523).  The loop's length in instructions and what its warps spill decide here: a split of 224
+// and 56 registers, which spills, takes 506 us where this one takes 483.
+//
+// Measured (GB300, bf16): 16 x 12 heads, 8192 tokens, a window of 1024: 481 us, 800 TFLOP/s of what is
+// seen, with 4 sinks 547 (one query tile an item: 658 and 729); 4 x 12 heads, 8192 tokens, no window: 359
+// us, 1148 TFLOP/s (412); 64 x 12 heads of 512: 62 us (96).  A step, a key tile for one warpgroup, takes it
+// about 2050 cycles: 1560 for softmax, 260 waiting for its scores, the rest hand-offs; one that is cut
+// 2600, an item's end 2400, its beginning 1200 (stamps of the SM clock).
 #include "df_cross_fwd.cuh"
 
 namespace dfa {
@@ -37,7 +49,8 @@ struct PairSmem {
   static constexpr uint32_t q = 0;                                  // [2 buffers][2 warpgroups][Q tile]
   static constexpr uint32_t k = q + 4 * kTileBytes;                 // [kStages][K tile]
   static constexpr uint32_t v = k + kStages * kTileBytes;           // [kStages][V tile]
-  static constexpr uint32_t bars = v + kStages * kTileBytes;
+  static constexpr uint32_t rows = v + kStages * kTileBytes;        // [8 softmax warps] on their way out
+  static constexpr uint32_t bars = rows + 8 * kRowStage;
   // q_full, q_empty [2]; k_full, k_empty, v_full, v_empty [kStages]; buf_free, drain [3];
   // s_full, p_full, pv_done [2][4]; item_full, item_empty; claim
   static constexpr int kBars = 4 + 4 * kStages + 6 + 24 + 2 * (int)kItemRing + 1;
@@ -80,7 +93,8 @@ __device__ __forceinline__ PairTiles pair_tiles(const CrossArgs& a, const CrossI
   return p;
 }
 
-template <bool BF16>
+// LO: what the rounding of the results drops is asked for too.
+template <bool BF16, bool LO>
 __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args, const __grid_constant__ FwdMaps maps) {
   using SL = PairSmem;
   constexpr int D = SL::D;
@@ -547,24 +561,54 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
       // (a NaN among the scores of keys that count is in l, and stays in the row)
       const float inv = l_run != 0.f ? rcp(l_run) : 0.f;
       const bool any = o_has && l_run != 0.f;
-      const size_t orow = ((size_t)(it->r0 + wg * a.tpt + row_tok) * a.H + (size_t)it->hk * a.G + row_head);
+      // (With what the rounding drops, rows go by way of shared memory: a thread's own row is a line for
+      // each of a warp's 32, which two results' stores wait for: 16 x 12 heads, 8192 tokens, a window of 1024,
+      // 565 -> 518 us; one result's do not, and the code is shorter: 493 -> 481.)
+      if constexpr (LO) {
+        const size_t row0 = (size_t)(it->r0 + wg * a.tpt) * a.H + (size_t)it->hk * a.G;
+        const int rel = row_in && *s_abort == 0 ? row_tok * a.H + row_head : -1;
+        uint8_t* stage = sm + SL::rows + (warp - 4) * kRowStage;
+        T* const out = static_cast<T*>(args.out) + row0 * a.d;
+        T* const out_lo = static_cast<T*>(args.out_lo) + row0 * a.d;
 #pragma unroll 1
-      for (int col = 0; warp_in && col < D; col += 16) {
-        uint32_t r[16];
-        tmem_ld16(tOw + col, r);
-        tmem_ld_wait(r);
-        if (!row_in || *s_abort != 0) continue;
+        for (int col = 0; warp_in && col < D && col < a.d; col += 32) {
+          uint32_t r[32], w[16];
+          tmem_ld32(tOw + col, r);
+          tmem_ld_wait(r);
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          if (col + e >= a.d) continue;
-          float o[8];
+          for (int e = 0; e < 32; ++e) r[e] = any ? __float_as_uint(__uint_as_float(r[e]) * inv) : 0u;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = any ? __uint_as_float(r[e + k]) * inv : 0.f;
-          const size_t at = orow * a.d + col + e;
-          store_rounded<T, 8>(static_cast<T*>(args.out) + at, args.out_lo ? static_cast<T*>(args.out_lo) + at : nullptr, o);
+          for (int e = 0; e < 16; ++e) w[e] = pack2<BF16>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          store_rows32(stage, w, rel, out + col, a.d, a.d - col);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            T h[2];
+            *reinterpret_cast<uint32_t*>(h) = w[e];
+            w[e] = pack2<BF16>(__uint_as_float(r[2 * e]) - IO<T>::to_f(h[0]),
+                               __uint_as_float(r[2 * e + 1]) - IO<T>::to_f(h[1]));
+          }
+          store_rows32(stage, w, rel, out_lo + col, a.d, a.d - col);
         }
+        if (args.lse && rel >= 0) args.lse[row0 + rel] = l_run != 0.f ? (m_run + lg2(l_run)) * kLn2 : -INFINITY;
+      } else {
+        const size_t orow = ((size_t)(it->r0 + wg * a.tpt + row_tok) * a.H + (size_t)it->hk * a.G + row_head);
+#pragma unroll 1
+        for (int col = 0; warp_in && col < D; col += 16) {
+          uint32_t r[16];
+          tmem_ld16(tOw + col, r);
+          tmem_ld_wait(r);
+          if (!row_in || *s_abort != 0) continue;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            if (col + e >= a.d) continue;
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = any ? __uint_as_float(r[e + k]) * inv : 0.f;
+            store_rounded<T, 8>(static_cast<T*>(args.out) + orow * a.d + col + e, nullptr, o);
+          }
+        }
+        if (args.lse && row_in && *s_abort == 0) args.lse[orow] = l_run != 0.f ? (m_run + lg2(l_run)) * kLn2 : -INFINITY;
       }
-      if (args.lse && row_in && *s_abort == 0) args.lse[orow] = l_run != 0.f ? (m_run + lg2(l_run)) * kLn2 : -INFINITY;
       tc_fence_before();
       named_sync(3 + wg, 128);  // every thread has read O; s_cur[c & 1] is there
     }
@@ -577,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
   if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
-template <bool BF16>
+template <bool BF16, bool LO>
 cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t s) {
-  auto kernel = self64_kernel<BF16>;
+  auto kernel = self64_kernel<BF16, LO>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = prepare_kernel((const void*)kernel, (int)PairSmem::alloc, kRegs, &done);
   return e != cudaSuccess ? e : launch_clusters(kernel, a, maps, grid, kThreads, PairSmem::alloc, s);
@@ -588,7 +632,8 @@ cudaError_t launch(const FwdArgs& a, const FwdMaps& maps, int grid, cudaStream_t
 }  // namespace
 
 cudaError_t launch_self64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s) {
-  return bf16 ? launch<true>(a, maps, grid, s) : launch<false>(a, maps, grid, s);
+  if (a.out_lo) return bf16 ? launch<true, true>(a, maps, grid, s) : launch<false, true>(a, maps, grid, s);
+  return bf16 ? launch<true, false>(a, maps, grid, s) : launch<false, false>(a, maps, grid, s);
 }
 
 }  // namespace dfa
