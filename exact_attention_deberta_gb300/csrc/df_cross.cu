@@ -127,19 +127,20 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
 
 using namespace dfa;
 
-// Causal attention, d to 64: whether items of two query tiles (df_self64.cu) end sooner than those of
-// one.  An item of one tile takes 3.5 us and 0.525 a key tile, both warpgroups at it; one of two 2.8
-// and 0.96.  A launch takes as long as its longest item, or, with more items than SMs, as an SM's share
-// of them and half an item.  (12 heads, one sequence, us, one / two: 1024 tokens 12.1 / 15.0, 2048 16.3 /
-// 22.7, 8192 105 / 101; 4 sequences of 512: 13.9 / 11.4; 8 of 200: 12.9 / 9.5; 16 of 8192, a window of
-// 1024: 658 / 475.)
+// Causal attention: whether items of two query tiles (df_self64.cu, df_self128.cu) end sooner than those
+// of one.  An item takes a time and one for each key tile (us; of one tile both halves of the CTA share
+// them).  A launch takes as long as its longest item, or, with more items than SMs, as an SM's share of
+// them and half an item.  (us, one / two.  d = 64, 12 heads, one sequence: 1024 tokens 12.1 / 15.0, 2048
+// 16.3 / 22.7, 8192 105 / 101; 4 sequences of 512: 13.9 / 11.4; 8 of 200: 12.9 / 9.5; 16 of 8192, a window
+// of 1024: 658 / 481.  d = 128, 8 heads, 4 sequences of 1024: 22.1 / 23.6, one of 4096: 35 / 62; 16 heads, 2
+// of 2048: 42.9 / 39.2; 8 of 8192, a window of 1024: 614 / 512.)
 static bool pairs_are_shorter(const CrossArgs& a, long long items, long long pairs, int key_tiles, int sms) {
   const double most = key_tiles, mean = a.window > 0 ? most : std::max(most - a.Lq / 256., 0.5 * most);
   auto time = [&](long long n, double base, double tile) {
     const double longest = base + tile * most, middle = base + tile * mean;
     return n <= sms ? longest : std::max(longest, (double)n / sms * middle + 0.5 * middle);
   };
-  return time(pairs, 2.8, 0.96) <= time(items, 3.5, 0.525);
+  return a.d <= 64 ? time(pairs, 2.8, 0.96) <= time(items, 3.5, 0.525) : time(pairs, 3.6, 1.83) <= time(items, 3.4, 0.9);
 }
 
 // `self`: causal, with a window and sinks (the caller has checked them).
@@ -190,10 +191,12 @@ static df_status forward(bool self, int window, int sinks, const void* q, const 
   a.split_bits = a.splits == 8 ? 3 : a.splits / 2;
   const int grid = (int)items * a.splits;
   cudaStream_t s = (cudaStream_t)stream;
-  if (self && d <= 64 && a.splits == 1) {
+  if (self && a.splits == 1) {
     const long long pairs = cross_query_tiles(a.c, 2);
-    if (pairs_are_shorter(a.c, items, pairs, key_tiles, sms))
-      return launch_self64(a, maps, bf16, (int)pairs, s) == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+    if (pairs_are_shorter(a.c, items, pairs, key_tiles, sms)) {
+      const cudaError_t e = d <= 64 ? launch_self64(a, maps, bf16, (int)pairs, s) : launch_self128(a, maps, bf16, (int)pairs, s);
+      return e == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+    }
   }
   const cudaError_t e =
       d <= 64 ? launch_cross64(a, maps, bf16, self, grid, s) : launch_cross128(a, maps, bf16, self, grid, s);

@@ -35,10 +35,9 @@
 // took 1094 us where this layout took 1034.  An item's end costs about 5000 cycles:
 // its code has left the instruction caches by then, so it is kept short.
 //
-// SELF: causal attention with a window and sinks, as in df_cross64.cu; 64 columns that no
-// row of a warp sees get no exponentials.  Measured: 16 x 16 heads sharing 4, 2048 tokens,
-// bf16: 302 us, 910 TFLOP/s of what is seen; 8 x 16 heads sharing 4, 8192 tokens, a window of
-// 1024 and 4 sinks: 669 us.
+// SELF: causal attention with a window and sinks where there is little of it (df_self128.cu: more),
+// as in df_cross64.cu; 64 columns that no row of a warp sees get no exponentials.  Measured:
+// 8 heads, one sequence of 4096 tokens, bf16: 35 us, 980 TFLOP/s of what is seen; 4 of 1024: 22 us.
 #include "df_cross_fwd.cuh"
 
 namespace dfa {

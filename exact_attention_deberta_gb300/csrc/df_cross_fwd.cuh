@@ -23,6 +23,7 @@ struct FwdMaps {
 
 cudaError_t launch_cross64(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s);
 cudaError_t launch_self64(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s);
+cudaError_t launch_self128(const FwdArgs& a, const FwdMaps& maps, bool bf16, int grid, cudaStream_t s);
 cudaError_t launch_cross128(const FwdArgs& a, const FwdMaps& maps, bool bf16, bool self, int grid, cudaStream_t s);
 constexpr int kFwdKeys = 128;  // keys per tile
 
@@ -35,6 +36,11 @@ constexpr int kFwdKeys = 128;  // keys per tile
 template <bool BF16>
 constexpr float kBelow = BF16 ? 0.f : 7.f;
 
+// Key tiles of a band among `keys` keys.
+__device__ __forceinline__ int band_tiles(const CrossBand& band, int keys) {
+  const int all = (keys + 127) / 128;
+  return max(all - band.skip, min(band.sinks, all));
+}
 // This CTA's key tiles [*t0, *t0 + n) of an item (of those that it meets); returns n.
 __device__ __forceinline__ int key_part(const FwdArgs& args, const CrossItem& it, const CrossBand& band, uint32_t rank,
                                         int* t0) {

@@ -73,10 +73,6 @@ struct PairTiles {
     return w == 0 ? t < na : (unsigned)(t - from) >= skip;
   }
 };
-__device__ __forceinline__ int band_tiles(const CrossBand& band, int keys) {
-  const int all = (keys + 127) / 128;
-  return max(all - band.skip, min(band.sinks, all));
-}
 __device__ __forceinline__ PairTiles pair_tiles(const CrossArgs& a, const CrossItem& it) {
   PairTiles p;
   p.band = key_band(a, it);

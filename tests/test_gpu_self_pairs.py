@@ -1,5 +1,5 @@
 """Causal attention where there is more work than a round of the SMs: items of two query tiles
-that follow one another (head sizes to 64), against the float64 oracle; what one of the tiles
+that follow one another, against the float64 oracle; what one of the tiles
 sees and the other does not, tiles without a partner, keys that are not numbers."""
 
 import numpy as np
@@ -29,6 +29,18 @@ CASES = [  # B, H, Hk, d, Lq, Lk, dtype, q, k, window, sinks
     (60, 8, 8, 64, 260, 300, HF, "packed", "masked", 77, 2),
     (2, 130, 2, 64, 90, 90, BF, "padded", "full", 40, 3),       # one token a tile, 65 heads
     (4, 128, 1, 64, 60, 60, HF, "packed", "packed", 0, 0),
+    (50, 6, 6, 128, 256, 256, BF, "padded", "full", 0, 0),
+    (40, 6, 6, 128, 300, 300, HF, "padded", "full", 0, 0),
+    (24, 8, 8, 96, 520, 520, BF, "padded", "full", 64, 3),
+    (24, 8, 8, 128, 520, 520, HF, "padded", "full", 128, 130),
+    (20, 8, 8, 128, 700, 700, BF, "padded", "full", 257, 1),
+    (30, 6, 2, 72, 200, 200, BF, "padded", "masked", 70, 2),
+    (40, 12, 4, 128, 170, 90, HF, "padded", "full", 33, 1),
+    (60, 8, 8, 128, 330, 330, BF, "packed", "packed", 0, 0),
+    (60, 8, 4, 120, 330, 400, HF, "packed", "packed", 100, 5),
+    (50, 8, 8, 128, 260, 300, BF, "packed", "masked", 77, 2),
+    (2, 130, 2, 128, 90, 90, HF, "padded", "full", 40, 3),
+    (90, 8, 8, 128, 140, 140, BF, "packed", "packed", 1, 0),    # items of a tile or two
 ]
 
 
@@ -49,10 +61,11 @@ def test_matches_oracle(lib, B, H, Hk, d, Lq, Lk, dtype, q, k, window, sinks):
     assert int(status.item()) == lib.DF_OK
 
 
-def test_many_items_a_cta(lib):
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_items_a_cta(lib, d):
     """Every CTA takes many items of unequal length, one after another."""
     n = [int(i) for i in np.random.default_rng(0).integers(0, 700, 220)]
-    x = inputs(220, 12, 12, 64, 700, 700, BF, "packed", "packed", seed=3, nq=n, nk=n)
+    x = inputs(220, 12, 12, d, 700, 700, BF, "packed", "packed", seed=3, nq=n, nk=n)
     dev = to_dev(x)
     got, stats = call(lib, x, dev, with_stats=True, window=150, sinks=2)
     at = np.concatenate([[0], np.cumsum(n)])
@@ -60,18 +73,19 @@ def test_many_items_a_cta(lib):
         rows = slice(int(at[b]), int(at[b + 1]))
         part = {name: x[name][rows] for name in ("q", "k", "v", "dout")}
         cu = torch.tensor([0, n[b]], dtype=torch.int32)
-        w = want(oracle, dict(part, key_mask=None, cu_q=cu, cu_k=cu), 0.125, 150, 2)
-        check_forward(got[rows], w, BF, 64, stats.lse[rows], stats.out_lo[rows])
+        w = want(oracle, dict(part, key_mask=None, cu_q=cu, cu_k=cu), d ** -0.5, 150, 2)
+        check_forward(got[rows], w, BF, d, stats.lse[rows], stats.out_lo[rows])
     for _ in range(3):
         assert torch.equal(call(lib, x, dev, window=150, sinks=2), got)
 
 
-def test_keys_that_are_not_numbers(lib):
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_that_are_not_numbers(lib, d):
     """Masked ones stay out; one that counts makes its rows, and no other sequence's, NaN."""
     B, L = 60, 256
     n = [int(i) for i in np.random.default_rng(1).integers(3, L + 1, B)]
     n[0] = 200
-    x = inputs(B, 6, 6, 64, L, L, BF, "padded", "masked", seed=4, nk=n)
+    x = inputs(B, 6, 6, d, L, L, BF, "padded", "masked", seed=4, nk=n)
     x["key_mask"][0, :200] = 1
     dev = to_dev(x)
     clean = call(lib, x, dev, window=100, sinks=2)
@@ -90,7 +104,7 @@ def test_keys_that_are_not_numbers(lib):
     others = [h for h in range(6) if h != 3]
     assert torch.equal(got[0][:, others], clean[0][:, others])
     # without a mask, in both tiles of an item
-    x = inputs(B, 6, 6, 64, L, L, HF, "padded", "full", seed=5)
+    x = inputs(B, 6, 6, d, L, L, HF, "padded", "full", seed=5)
     dev = to_dev(x)
     clean = call(lib, x, dev, window=100, sinks=2)
     for at in (1, 60, 127, 128, 200):
