@@ -19,9 +19,9 @@
 // 64 columns that no row of a warp sees get no exponentials.
 //
 // Measured (GB300, bf16): 8 x 16 heads, 8192 tokens, d = 128, a window of 1024: 512 us, 1007 TFLOP/s of what
-// is seen (one query tile an item: 614); 16 x 16 heads sharing 4, 2048 tokens: 267 us, 1032 TFLOP/s (301);
-// 64 x 16 heads sharing 4, 512 tokens: 134 us (162).  Without a window, items are long and the gain is
-// small: 2 x 16 heads sharing 4, 8192 tokens: 410 us, 1341 TFLOP/s (422).
+// is seen (one query tile an item: 614); 16 x 16 heads sharing 4, 2048 tokens: 262 us, 1050 TFLOP/s (301);
+// 64 x 16 heads sharing 4, 512 tokens: 132 us (162).  Without a window, items are long and the gain is
+// small: 2 x 16 heads sharing 4, 8192 tokens: 405 us, 1358 TFLOP/s (422).
 #include "df_cross_fwd.cuh"
 
 namespace dfa {
@@ -73,46 +73,35 @@ __device__ __forceinline__ CrossItem team_item(const CrossArgs& a, CrossItem it,
   return it;
 }
 
-// 64 columns of a warp's rows, o = a f, rounded, and (out_lo) what that rounding dropped.  A step of
-// 16 columns at a time changes hands through 1 KB of shared memory, so that rows go out as 32 bytes
-// each.  (A short loop: code that runs once per item has left the instruction caches by then.)
+// 64 columns of a warp's rows, o = a f, rounded, and (out_lo) what that rounding dropped, 32 at a time by
+// way of shared memory (16 at a time: 606 us against 590 for 8 x 16 heads sharing 4, 8192 tokens, a window
+// of 1024 and 4 sinks, 663 against 637 with what rounding drops).
 template <bool BF16, typename T>
 __device__ __forceinline__ void store_own(const FwdArgs& args, uint8_t* stage, uint32_t ta, float f, bool empty, int rel,
                                           size_t row0, int col) {
-  const int lane = threadIdx.x & 31, d = args.c.d;
+  const int d = args.c.d;
   const float2 f2 = make_float2(f, f);
-  uint8_t* mine = stage + lane * 32 + 16 * ((lane >> 2) & 1);  // the row's first 8 columns; the others at ^ 16
 #pragma unroll 1
-  for (int end = min(col + 64, d); col < end; col += 16, ta += 16) {
-    uint32_t ra[16];
-    tmem_ld16(ta, ra);
-    tmem_ld_wait(ra);
-    uint32_t hi[8], lo[8];
+  for (int end = min(col + 64, d); col < end; col += 32, ta += 32) {
+    uint32_t r[32], w[16];
+    tmem_ld32(ta, r);
+    tmem_ld_wait(r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 o = mul2(make_float2(__uint_as_float(ra[2 * e]), __uint_as_float(ra[2 * e + 1])), f2);
-      hi[e] = empty ? 0u : pack2<BF16>(o.x, o.y);
-      const T* t = reinterpret_cast<const T*>(&hi[e]);
-      lo[e] = empty ? 0u : pack2<BF16>(o.x - IO<T>::to_f(t[0]), o.y - IO<T>::to_f(t[1]));
+    for (int e = 0; e < 16; ++e) {
+      const float2 o = mul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), f2);
+      r[2 * e] = empty ? 0u : __float_as_uint(o.x);
+      r[2 * e + 1] = empty ? 0u : __float_as_uint(o.y);
+      w[e] = pack2<BF16>(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
     }
-    const size_t at = row0 * d + col;
+    store_rows32(stage, w, rel, static_cast<T*>(args.out) + row0 * d + col, d, d - col);
+    if (!args.out_lo) continue;
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      if (pass == 1 && !args.out_lo) break;
-      const uint32_t (&w)[8] = pass ? lo : hi;
-      *reinterpret_cast<uint4*>(mine) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>((uintptr_t)mine ^ 16) = make_uint4(w[4], w[5], w[6], w[7]);
-      __syncwarp();
-      T* dst = static_cast<T*>(pass ? args.out_lo : args.out) + at + 8 * (lane & 1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 16 * i + (lane >> 1);
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 32 + 16 * ((lane ^ (r >> 2)) & 1));
-        const int to = __shfl_sync(0xffffffffu, rel, r);
-        if (to >= 0 && col + 8 * (lane & 1) < d) *reinterpret_cast<uint4*>(dst + (size_t)to * d) = v;
-      }
-      __syncwarp();
+    for (int e = 0; e < 16; ++e) {
+      T h[2];
+      *reinterpret_cast<uint32_t*>(h) = w[e];
+      w[e] = pack2<BF16>(__uint_as_float(r[2 * e]) - IO<T>::to_f(h[0]), __uint_as_float(r[2 * e + 1]) - IO<T>::to_f(h[1]));
     }
+    store_rows32(stage, w, rel, static_cast<T*>(args.out_lo) + row0 * d + col, d, d - col);
   }
 }
 
