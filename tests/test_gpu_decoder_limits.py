@@ -48,9 +48,11 @@ def test_waits_of_the_cache_run_out_and_recover(lib, H, Hk, d, Lq):
     assert int(status.item()) == lib.DF_OK
 
 
+@pytest.mark.parametrize("B,H,Hk,L", [(2, 4, 2, 700), (30, 8, 8, 300)])
 @pytest.mark.parametrize("d,dtype", [(64, BF), (128, HF)])
-def test_waits_of_causal_attention_run_out_and_recover(lib, d, dtype):
-    x = inputs(2, 4, 2, d, 700, 700, dtype, "padded", "full", seed=d)
+def test_waits_of_causal_attention_run_out_and_recover(lib, d, dtype, B, H, Hk, L):
+    """(Items of one query tile, and of two.)"""
+    x = inputs(B, H, Hk, d, L, L, dtype, "padded", "full", seed=d)
     dev = to_dev(x)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     kw = dict(window=300, sinks=2)
