@@ -13,7 +13,7 @@
 //
 // Measured (GB300): 64 ragged prompts of up to 8192 tokens, 12 heads, d = 64, bf16, appended and
 // read back: 465 us, 6.4 TB/s; a token for each of 64 sequences of 499, 8 heads, d = 128, fp16, whose
-// rows are then read: 32 us, 3.9 TB/s.
+// rows are then read: 30 us, 4.2 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -318,8 +318,11 @@ bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <bool READ, typename T>
 cudaError_t launch(StoreArgs a, cudaStream_t s) {
-  // one pair a warp where there are few, up to eight while some 2^16 warps are left
-  a.pairs = (int)std::min<long long>(8, std::max<long long>(1, a.slots * a.c.Hk * 2 >> 16));
+  // one pair a warp where there are few, up to eight while some 2^16 warps are left; reading, two where
+  // one each would be more than a round of the SMs' warps (64 sequences of 500 rows, 8 heads, d = 128,
+  // after a token each was appended: 32.5 -> 30.0 us; four: 32.8)
+  const long long all = a.slots * a.c.Hk * 2;
+  a.pairs = (int)std::min<long long>(8, std::max<long long>(READ && all > 16384 ? 2 : 1, all >> 16));
   a.warps = (2 * a.c.Hk + a.pairs - 1) / a.pairs;
   const long long blocks = (a.slots * a.warps + 7) / 8;
   if (blocks > 0x7fffffffll / 8) return cudaErrorInvalidConfiguration;
