@@ -132,8 +132,8 @@ using namespace dfa;
 // them).  A launch takes as long as its longest item, or, with more items than SMs, as an SM's share of
 // them and half an item.  (us, one / two.  d = 64, 12 heads, one sequence: 1024 tokens 12.1 / 15.0, 2048
 // 16.3 / 22.7, 8192 105 / 101; 4 sequences of 512: 13.9 / 11.4; 8 of 200: 12.9 / 9.5; 16 of 8192, a window
-// of 1024: 658 / 481.  d = 128, 8 heads, 4 sequences of 1024: 22.1 / 23.6, one of 4096: 35 / 62; 16 heads, 2
-// of 2048: 42.9 / 39.2; 8 of 8192, a window of 1024: 614 / 512.)
+// of 1024: 658 / 460.  d = 128, 8 heads, 4 sequences of 1024: 22.1 / 23.6, one of 4096: 35 / 62; 16 heads, 2
+// of 2048: 42.9 / 38.1; 8 of 8192, a window of 1024: 614 / 491.)
 static bool pairs_are_shorter(const CrossArgs& a, long long items, long long pairs, int key_tiles, int sms) {
   const double most = key_tiles, mean = a.window > 0 ? most : std::max(most - a.Lq / 256., 0.5 * most);
   auto time = [&](long long n, double base, double tile) {

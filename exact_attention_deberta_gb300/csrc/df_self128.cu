@@ -15,13 +15,14 @@
 //   warps 4-19   softmax: a row's scores are shared by two threads (a half of the
 //                columns each), which exchange their maxima through shared memory;
 //                P (rounded to the I/O type) overwrites the scores it came from.
-// Keys that do not count get weight 0 by selection and their rows of V are zeroed, as in df_cross128.cu;
-// 64 columns that no row of a warp sees get no exponentials.
+// Keys that do not count get weight 0 by selection, by bits that are found before the scores are awaited,
+// and their rows of V are zeroed, as in df_cross128.cu; 32 columns that no row of a warp sees get no
+// exponentials.
 //
-// Measured (GB300, bf16): 8 x 16 heads, 8192 tokens, d = 128, a window of 1024: 512 us, 1007 TFLOP/s of what
-// is seen (one query tile an item: 614); 16 x 16 heads sharing 4, 2048 tokens: 262 us, 1050 TFLOP/s (301);
-// 64 x 16 heads sharing 4, 512 tokens: 132 us (162).  Without a window, items are long and the gain is
-// small: 2 x 16 heads sharing 4, 8192 tokens: 405 us, 1358 TFLOP/s (422).
+// Measured (GB300, bf16): 8 x 16 heads, 8192 tokens, d = 128, a window of 1024: 491 us, 1050 TFLOP/s of what
+// is seen (one query tile an item: 614); 16 x 16 heads sharing 4, 2048 tokens: 253 us, 1088 TFLOP/s (301);
+// 64 x 16 heads sharing 4, 512 tokens: 127 us (162).  Without a window, items are long and the gain is
+// smaller: 2 x 16 heads sharing 4, 8192 tokens: 394 us, 1395 TFLOP/s (422).
 #include "df_cross_fwd.cuh"
 
 namespace dfa {
@@ -427,6 +428,24 @@ __global__ void __launch_bounds__(kThreads, 1) self128_kernel(const FwdArgs args
       // last tile.  While a team waits for tile m, the other one may be through with m + 2, not with m + 3:
       // that waits for the one before which this team stands.  So m's phase is told from the next of four.
       for (int t = 0; t < nt; ++t, ++n) {
+        // (found while the scores are on their way)
+        const int first = kKeys * band.tile(t), left = it.no - first;
+        const bool cut = !seen_whole(a, it.p0, it.nr, first);
+        bool part = false, live0 = true, live1 = true;  // live: whether any of this thread's columns counts in its warp
+        uint32_t b0 = ~0u, b1 = ~0u;
+        if (a.key_mask || left < kKeys || cut) {
+          uint32_t bits[kWords];
+          part = !key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + first : nullptr, left, bits) || cut;
+          b0 = half ? bits[kWords / 2] : bits[0];
+          b1 = half ? bits[kWords / 2 + 1] : bits[1];
+          if (cut) {
+            const int p = it.p0 + sRow[row].x, mine = first + (kKeys / 2) * half;
+            b0 &= seen_bits(a, p, mine);
+            b1 &= seen_bits(a, p, mine + 32);
+            live0 = __any_sync(0xffffffffu, b0 != 0);
+            live1 = __any_sync(0xffffffffu, b1 != 0);
+          }
+        }
         cross_wait(s_full + wg, n & 1, budget, s_abort);
         __syncwarp();
         tc_fence_after();
@@ -435,27 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) self128_kernel(const FwdArgs args
           tmem_ld32(tSw, r0);
           tmem_ld32(tSw + 32, r1);
           tmem_ld_wait2(r0, r1);
-          const int kt = band.tile(t), left = it.no - kt * kKeys;
-          const bool cut = !seen_whole(a, it.p0, it.nr, kt * kKeys);
-          bool live0 = true, live1 = true;  // whether any of this thread's columns counts in its warp
-          if (a.key_mask || left < kKeys || cut) {
-            uint32_t bits[kWords];
-            const bool all =
-                key_bits(a.key_mask ? a.key_mask + (size_t)it.b * a.Lk + (size_t)kt * kKeys : nullptr, left, bits);
-            if (!all || cut) {
-              uint32_t b0 = half ? bits[kWords / 2] : bits[0], b1 = half ? bits[kWords / 2 + 1] : bits[1];
-              if (cut) {
-                const int p = it.p0 + sRow[row].x, first = kt * kKeys + (kKeys / 2) * half;
-                b0 &= seen_bits(a, p, first);
-                b1 &= seen_bits(a, p, first + 32);
-                live0 = __any_sync(0xffffffffu, b0 != 0);
-                live1 = __any_sync(0xffffffffu, b1 != 0);
-              }
+          if (part) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                if (!((b0 >> j) & 1u)) r0[j] = 0xff800000u;  // -infinity
-                if (!((b1 >> j) & 1u)) r1[j] = 0xff800000u;
-              }
+            for (int j = 0; j < 32; ++j) {
+              if (!((b0 >> j) & 1u)) r0[j] = 0xff800000u;  // -infinity
+              if (!((b1 >> j) & 1u)) r1[j] = 0xff800000u;
             }
           }
           // row maximum of the raw scores (the scale is positive)

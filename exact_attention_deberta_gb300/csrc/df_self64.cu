@@ -21,14 +21,15 @@
 // Keys that a row does not see: the scores of a tile that not every row sees whole become -inf in
 // registers, in code of its own (in place in tensor memory, as the whole tile's code is shorter then:
 // 546 us against 481 with a window of 1024; by a minimum with infinities, a block for each end of the
-// window: 523).  The loop's length in instructions and what its warps spill decide here: a split of 224
-// and 56 registers, which spills, takes 506 us where this one takes 483.
+// window: 523), by bits that are found before the scores are awaited (481 -> 461; 549 -> 514 with 4 sinks).
+// The loop's length in instructions and what its warps spill decide here: a split of 224 and 56
+// registers, which spills, took 506 us where this one took 483.
 //
-// Measured (GB300, bf16): 16 x 12 heads, 8192 tokens, a window of 1024: 481 us, 800 TFLOP/s of what is
-// seen, with 4 sinks 547 (one query tile an item: 658 and 729); 4 x 12 heads, 8192 tokens, no window: 359
-// us, 1148 TFLOP/s (412); 64 x 12 heads of 512: 62 us (96).  A step, a key tile for one warpgroup, takes it
-// about 2050 cycles: 1560 for softmax, 260 waiting for its scores, the rest hand-offs; one that is cut
-// 2600, an item's end 2400, its beginning 1200 (stamps of the SM clock).
+// Measured (GB300, bf16): 16 x 12 heads, 8192 tokens, a window of 1024: 460 us, 841 TFLOP/s of what is
+// seen, with 4 sinks 511 to 519 (one query tile an item: 658 and 729); 4 x 12 heads, 8192 tokens, no window:
+// 356 us, 1160 TFLOP/s (412); 64 x 12 heads of 512: 61 us (96).  A step, a key tile for one warpgroup, takes
+// it some 2000 cycles, of which softmax is 1560 and 260 are a wait for its scores; an item's end takes
+// 2400, its beginning 1200 (stamps of the SM clock, before the last change).
 #include "df_cross_fwd.cuh"
 
 namespace dfa {
@@ -441,23 +442,19 @@ __global__ void __launch_bounds__(kThreads, 1) self64_kernel(const FwdArgs args,
         pass(wg == 1 && pt.sees(0, t));
         if (pt.sees(wg, t)) {
           const uint32_t tSw = tmem + 128u * sb + lane_off;
+          // (found while the scores are on their way; keys behind the sequence's last lie behind every row)
+          const int first = 128 * pt.band.tile(t), p0 = it->p0 + wg * a.tpt;
+          const bool cut = !seen_whole(a, p0, min(it->nr - wg * a.tpt, a.tpt), first), part = cut || a.key_mask;
+          uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+          if (a.key_mask) key_bits(a.key_mask + (size_t)it->b * a.Lk + first, it->no - first, bits);
+          if (cut) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bits[w] &= seen_bits(a, p0 + row_tok, first + 32 * w);
+          }
           cross_wait(s_full + 4 * wg + (own & 3), (own >> 2) & 1, budget, s_abort);
           __syncwarp();
           tc_fence_after();
           if (warp_in) {
-            const int kt = pt.band.tile(t), left = it->no - kt * 128, p0 = it->p0 + wg * a.tpt;
-            const bool cut = !seen_whole(a, p0, min(it->nr - wg * a.tpt, a.tpt), kt * 128);
-            uint32_t bits[4];
-            bool part = false;
-            if (a.key_mask || left < 128 || cut) {
-              const bool all =
-                  key_bits(a.key_mask ? a.key_mask + (size_t)it->b * a.Lk + (size_t)kt * 128 : nullptr, left, bits);
-              if (cut) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w) bits[w] &= seen_bits(a, p0 + row_tok, kt * 128 + 32 * w);
-              }
-              part = !all || cut;
-            }
             float x[128];
             {
               uint32_t r0[32], r1[32], r2[32], r3[32];
