@@ -51,11 +51,11 @@
 // SELF: causal attention with a window and sinks (df_cross.cuh).  A key tile streams the
 // queries that see one of its keys (those of the sinks: all from their own on), a query tile
 // the key tiles that it sees; 16 columns of a half that no row of a warp sees get weight 0
-// without exponentials, selections run only where rows differ.  Measured (bf16): 4 x 12
-// heads, 8192 tokens, d = 64: 1.26 ms, 820 TFLOP/s of what is seen (10 flops a score and
-// column); 16 x 12 heads, 8192 tokens, a window of 1024: 1.66 ms, with 4 sinks 1.80 (their
-// tiles stream whole sequences; numbered before all others: 1.79); 16 x 16 heads sharing 4,
-// 2048 tokens, d = 128: 0.90 ms, 760 TFLOP/s.
+// without exponentials, selections run only where rows differ; which keys a row sees is found
+// while the scores are on their way.  Measured (bf16): 4 x 12 heads, 8192 tokens, d = 64: 1.24
+// ms, 830 TFLOP/s of what is seen (10 flops a score and column); 16 x 12 heads, 8192 tokens, a
+// window of 1024: 1.66 ms, with 4 sinks 1.79 (their tiles stream whole sequences; numbered
+// before all others 0.7 % less); 16 x 16 heads sharing 4, 2048 tokens, d = 128: 0.89 ms, 770 TFLOP/s.
 #include "df_cross.cuh"
 
 #include <algorithm>
@@ -684,15 +684,25 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
         const uint32_t s = (g + t) % kStages, u = 2 * (g + t) + h, b = u % kBufs;
         // (the buffer's previous half is the other warpgroup's u - 3 at three buffers;
         // its scores stand before those of u - 2, which this warp has seen)
+        // (found while the scores are on their way)
+        const int pq = it.q0 + t * y_step;  // self attention, key tiles: the position of the tile's first query
+        const int first = SELF && !KEYS ? band.tile(t) * 128 : 0;
+        bool cut = false;
+        if (SELF && KEYS)
+          cut = !(pq >= it.p0 + 127 && (a.window == 0 || pq + y_step - a.window <= it.p0 || it.p0 + 128 <= a.sinks));
+        else if (SELF)
+          cut = !seen_whole(a, it.p0, it.nr, first);
+        uint32_t sees[2] = {~0u, ~0u};
+        if (SELF && !KEYS && cut) {
+          sees[0] = seen_bits(a, it.p0 + row_tok, first + 64 * h);
+          sees[1] = seen_bits(a, it.p0 + row_tok, first + 64 * h + 32);
+        }
         cross_wait(s_full + b, (u / kBufs) & 1, budget, s_abort);
         __syncwarp();
         tc_fence_after();
         const float* col = reinterpret_cast<const float*>(sm + SL::col + s * 1024);
         if (!BF16 && t == 0) ds_mul = reinterpret_cast<const float*>(sm + SL::scale + s * 512)[row] * kPUnit;
         if constexpr (KEYS) {
-          const int pq = it.q0 + t * y_step;  // self attention: the position of the tile's first query
-          const bool cut = SELF && !(pq >= it.p0 + 127 && (a.window == 0 || pq + y_step - a.window <= it.p0 ||
-                                                          it.p0 + 128 <= a.sinks));
           // A thread takes two columns of every eight in four rows (lane / 4 + 8 r),
           // not 64 columns of one row: it then reads a quarter of the columns' values
           // from shared memory (one row per thread: 898 us against 835 on 8 x 12 heads,
@@ -787,13 +797,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
           tmem_ld_wait2(rs0, rd0);
           tmem_ld32(tS(b) + lane_off + 32, rs1);
           tmem_ld32(tdP(b) + lane_off + 32, rd1);
-          const int first = SELF ? band.tile(t) * 128 : 0;
-          const bool cut = SELF && !seen_whole(a, it.p0, it.nr, first);
           auto columns = [&](const uint32_t (&rs)[32], const uint32_t (&rd)[32], int q) {
             uint32_t wd[16];
             uint32_t bits = reinterpret_cast<const uint32_t*>(col)[2 * h + q];
             if (SELF && cut) {
-              bits &= seen_bits(a, it.p0 + row_tok, first + 64 * h + 32 * q);
+              bits &= sees[q];
               if (!__any_sync(0xffffffffu, bits != 0)) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) wd[e] = 0u;
