@@ -117,9 +117,6 @@ df_status cross_check(const void* q, const void* k, const void* v, const uint8_t
   a->status = status;
   a->budget = wait_budget();
   a->window = a->sinks = 0;
-  // (as many as make a launch's last items short ones, while their keys and values stay in L2: 4 x 12
-  // heads, 8192 tokens, d = 64: 386 us one by one, 379 by 8, 356 by 12)
-  a->group = (int)std::max<long long>(1, std::min<long long>({(long long)Hk, 16ll, (64ll << 20) / std::max(4ll * Lk * d, 1ll)}));
   return DF_OK;
 }
 
