@@ -217,6 +217,13 @@ __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
   return 0;
 }
 
+// Self attention: key heads whose query tiles are numbered together, as many as make a launch's last
+// items short ones, while their keys and values, 64 MB at most, stay in L2 (4 x 12 heads, 8192 tokens, d
+// = 64: 386 us one by one, 379 by 8, 356 by 12).
+__device__ __forceinline__ int heads_together(const CrossArgs& a) {
+  return max(1, min(min(a.Hk, 16), (1 << 24) / max(a.Lk, 1) / a.d));
+}
+
 // Finds the tiles of one side by number, warp-collectively.  Tiles of `step`
 // tokens are numbered by sequence, then key head, then position; in packed mode
 // the rows behind the last sequence count as one more sequence, whose other
@@ -226,6 +233,7 @@ __device__ __forceinline__ int masked_length(const uint8_t* mask, int n) {
 // queries that see it.
 template <bool SELF = false, bool KEYS = false>
 struct TileWalk {
+  int together = 1;    // SELF, query tiles: heads_together
   int b0 = 0;          // sequences b0 .. b0 + 31 are the lanes' current ones
   long long done = 0;  // tiles of the sequences before b0
 
@@ -289,10 +297,6 @@ struct TileWalk {
     }
     int turn;
     if (SELF && !KEYS) {
-      // key heads together: as many as make a launch's last items short ones, while their keys and
-      // values, 64 MB at most, stay in L2 (4 x 12 heads, 8192 tokens, d = 64: 386 us one by one, 379 by
-      // 8, 356 by 12)
-      const int together = max(1, min(min(a.Hk, 16), (1 << 24) / max(a.Lk, 1) / a.d));
       const int group = at / (together * tiles), in = at - group * (together * tiles);
       const int heads = min(together, a.Hk - group * together);
       turn = in / heads;

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross64_kernel(const FwdArgs args
     // (the whole warp runs every step, and one lane of it issues: this loop's length
     // in instructions is what a tile's period comes down to)
     TileWalk<SELF> walk;
+    if (SELF) walk.together = heads_together(a);
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, qc = 0, k_issued = 0, v_issued = 0;
     int mask_b = -1, mask_n = 0;  // the last masked row measured

@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_kernel(const BwdArgs ar
     // (the whole warp runs every step, and one lane of it issues; so do the warps of
     // the products)
     TileWalk<SELF, KEYS> walk;
+    if (SELF && !KEYS) walk.together = heads_together(a);
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t g = 0, xc = 0, g_issued = 0, x_issued = 0;
     const uint32_t q_box = (uint32_t)(a.G * a.tpt) * 128u;  // bytes of a 64-column box of a query tile

@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) self128_kernel(const FwdArgs args
     setmaxnreg_dec<kOtherRegs>();
     // (the whole warp runs every step, and one lane of it issues)
     TileWalk<true> walk;
+    walk.together = heads_together(a);
     TileClaim claim = {claim_bar, reinterpret_cast<uint4*>(sm + SL::claim)};
     uint32_t kn0 = 0, kn1 = 0, vn0 = 0, vn1 = 0;  // tiles loaded for each team
     uint32_t qn0 = 0, qn1 = 0;
