@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(256) read_kernel(const StoreArgs a) {
     n = a.total - first;
   }
   const int blk = (int)(slot - slot_of(a, b));
-  if ((long long)blk * kBlock >= n) return;
+  if (blk < 0 || (long long)blk * kBlock >= n) return;  // (below 0: a slot of the rows in front of the first sequence)
   const int here = min(kBlock, n - blk * kBlock);  // rows of the block,
   int left = min(held - blk * kBlock, here);       // of which the cache holds these
   int id = 0;

@@ -667,7 +667,8 @@ df_status df_cache_append(const void* k, const void* v, const int32_t* cu_seqlen
 /* Reads tokens back: k, v [B, n, Hk, d] (total = B n) or packed by cu_seqlens [total, Hk, d] in
  * `dtype` (bf16, fp16 or fp32; codes times scale, exact unless a value leaves the type's range:
  * fp16 then gets +-65504): the first tokens of each sequence, as many as it has rows here; rows
- * beyond lengths[b], and packed rows behind the last sequence, get zeros. */
+ * beyond lengths[b], and packed rows behind the last sequence, get zeros.  With cu_seqlens[0] > 0 the
+ * rows before the first one are left alone, as are those of a sequence whose offsets are refused. */
 df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t* pages,
                         int max_pages, const int32_t* lengths, const int32_t* cu_seqlens, int B,
                         int Hk, int n, int total, int d, df_dtype dtype, void* k, void* v,
