@@ -141,11 +141,13 @@ __global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
   int first;
   const int n = seq_rows(rows, b, nullptr, &first), held = a.c.lengths[b];
   if (n == 0 || held < 0) return;
-  const int blk = held / kBlock + (int)(slot - slot_of(a, b));
-  const int from = max(held - blk * kBlock, 0);  // the block's tokens from here on are new,
-  const long long end = (long long)held + n - (long long)blk * kBlock;
-  if (end <= 0 || blk < 0) return;
-  const int to = (int)min((long long)kBlock, end);  // up to here
+  // the sequence's blocks from its first new token on, of which the first holds `part` older ones (k
+  // below 0: a slot of the rows in front of the first sequence, whose blocks are none of the call's)
+  const int k = (int)(slot - slot_of(a, b)), part = held % kBlock;
+  if (k < 0 || (long long)k * kBlock >= part + n) return;
+  const int blk = held / kBlock + k;
+  const int from = k == 0 ? part : 0;                  // the block's tokens from here on are new,
+  const int to = min(kBlock, part + n - k * kBlock);  // up to here
   const int id = page_of(a.c, b, blk);
   if (id < 0) {
     if (lane == 0) cross_fail(a.status, (int)DF_ERR_INVALID_ARG);
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
   }
   const int piece = lane & 3, row0 = lane >> 2;
   const long long step = (long long)a.c.Hk * D;  // elements from token to token
-  const long long base = (first + (long long)blk * kBlock - held + row0) * step + 8 * piece;  // the lane's, in head 0
+  const long long base = ((long long)first + k * kBlock - part + row0) * step + 8 * piece;  // the lane's, in head 0
   const size_t stride = (size_t)(a.c.page / kBlock) * record_bytes(D);  // from head to head of a page
   uint8_t* rec0 = record_of(a.c, id, 0, blk);
   const int last = min(pair + a.pairs, 2 * a.c.Hk);
