@@ -207,12 +207,14 @@ class SelfAttention:
     ``step`` takes the next token or few of each sequence.  ``key_heads`` heads of keys and
     values may be shared by several query heads (their columns together are a multiple of 256).
     ``table`` holds the rotary frequencies (``binding.df_rotary_table``; a part of the head's
-    columns, or all).  ``status`` as for ``CrossAttention``."""
+    columns, or all), ``amplitude`` what frequencies stretched for long contexts ask for (q and k are
+    both rotated with it).  ``status`` as for ``CrossAttention``."""
 
-    def __init__(self, cfg: EncoderConfig, weights: dict, table, key_heads=None, window=0, sinks=0, interleaved=False):
+    def __init__(self, cfg: EncoderConfig, weights: dict, table, key_heads=None, window=0, sinks=0, interleaved=False,
+                 amplitude=1.0):
         self.cfg, self.w, self.table = cfg, weights, table
         self.key_heads = key_heads or cfg.heads
-        self.window, self.sinks, self.interleaved = window, sinks, interleaved
+        self.window, self.sinks, self.interleaved, self.amplitude = window, sinks, interleaved, amplitude
 
     def _project(self, x, positions, status):
         """q [T, heads, d], k and v [T, key_heads, d] of rows x [T, hidden]; q and k rotated."""
@@ -222,7 +224,7 @@ class SelfAttention:
         k, v = (t.view(T, self.key_heads, d) for t in
                 binding.df_linear(x, [w["w_k"], w["w_v"]], [w["b_k"], w["b_v"]], status=status))
         q = q.view(T, cfg.heads, d)
-        binding.df_rotary((q, k), positions, self.table, interleaved=self.interleaved, out=(q, k))
+        binding.df_rotary((q, k), positions, self.table, interleaved=self.interleaved, amplitude=self.amplitude, out=(q, k))
         return q, k, v
 
     def _finish(self, ctx, x, status):
