@@ -18,7 +18,8 @@
 //     (lane / 4, lane % 4) takes 8 columns of a K row at once and 4 tokens x 4 columns of V,
 //     transposed by byte permutes; key i of lane t is 4 i + ((t + 2 (i & 1)) & 3), for which
 //     neither read meets a bank conflict and the scores a lane gets are the weights it needs.
-//   - A weight is held times 2^14, so that fp16 keeps its digits down to 2^-28 of the largest.
+//   - A weight is held times 2^14, so that fp16 keeps its digits down to 2^-28 of the largest; the scale of
+//     V takes that back, so that O is a sum of weights of 1 at most.
 // Sequences are cut over the CTAs of a cluster where there are few of them; the parts are joined
 // through distributed shared memory, without a workspace or a second launch.
 //
@@ -44,7 +45,7 @@ using namespace ptx;
 // A tile is the keys of one copy: two blocks.  (Four at d = 64: 166 us where two take 160, for 24
 // heads and 64 requests of up to 8192 tokens; one at d = 128: the same as two.)
 constexpr int NB = 2, kKeys = NB * kBlock;
-constexpr float kUp = 14.f;
+constexpr float kUp = 14.f, kDown = 1.f / 16384.f;
 
 struct DecodeArgs {
   CacheView c;
@@ -319,7 +320,7 @@ struct Softmax {
       // (positive, so that a score of -infinity stays one)
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) f[blk][h] = fmaxf(__uint_as_float(sw.x) * ks_row[h], 1.17549435e-38f);
-      vs[blk] = __uint_as_float(sw.y);
+      vs[blk] = __uint_as_float(sw.y) * kDown;  // (a scale is 2^-100 at least)
     }
     // Products in the order of their sums, or, so that those that follow one another are of different
     // sums, slab by slab of all keys: long rows that leave the registers for it (d = 128, a key head's
@@ -484,7 +485,7 @@ __device__ __forceinline__ void add_scaled(float (&v)[4], float f, const float4&
 // ones bring lse.
 __device__ __forceinline__ void store4(const DecodeArgs& a, const Rows& w, int i, int D, int piece, float m, float l,
                                        const float (&v)[4]) {
-  const float inv = l != 0.f ? rcp(l) : 0.f;  // (a NaN stays one)
+  const float inv = l != 0.f ? rcp(l * kDown) : 0.f;  // (a NaN stays one)
   int token, head;
   w.place(a, i, &token, &head);
   const size_t at = (size_t)(w.q0 + w.t0 + token) * a.H + w.hk * a.G + head;
