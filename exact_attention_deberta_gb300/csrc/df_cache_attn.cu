@@ -247,7 +247,8 @@ struct Softmax {
   float o[SLABS][4][4];
   float m_run[2], l_run[2];  // l_run: this lane's keys only
 
-  // (bf16 rows become fp16 times a power of two, exactly)
+  // (bf16 rows become fp16 times a power of two, exactly down to 2^-32 of a row's largest, which comes to
+  // 2^15 .. 65280: fp16's smallest step is 2^-24, and eight digits are to stand above it)
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Rows& w, int part) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     whole_to = (a.causal ? min(w.p0 + 1, w.held) : w.held) - kKeys;
@@ -278,9 +279,10 @@ struct Softmax {
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t e = min(max(top >> 7, 1u), 253u);  // the largest is below 2^(e - 126)
-        const float down = __uint_as_float((254u - e) << 23);
-        ks_row[h] = a.kscale * __uint_as_float(e << 23);
+        // the largest is below 2^(e - 126); where it is below 2^-94, every step of bf16 is one of fp16 at 33
+        const uint32_t e = min(max(top >> 7, 33u), 254u);
+        const float down = __uint_as_float((269u - e) << 23);  // 2^(142 - e)
+        ks_row[h] = a.kscale * __uint_as_float((e - 15u) << 23);
 #pragma unroll
         for (int c = 0; c < SLABS; ++c) {
           uint32_t* x = reinterpret_cast<uint32_t*>(&v[c]);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from _cache import fill, oracles, tokens
-from _cross import check_forward, np64
+from _cross import U32, check_forward, np64
 from test_gpu_cache import want_attn
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +44,48 @@ def test_one_value_at_the_top_and_equal_ones(lib):
         calls = [([v.shape[0]], torch.zeros_like(v), v)]
         out, lse, w = attend(lib, calls, torch.ones(1, 1, 2, d, dtype=BF), 1, d)
         check_forward(out, w, BF, d, lse)
+
+
+@pytest.mark.parametrize("B,H,Hk,d,Lq", [(2, 4, 2, 64, 1), (1, 8, 8, 32, 1), (2, 16, 2, 128, 3)])
+@pytest.mark.parametrize("below", [17, 20, 23])
+def test_small_digits_of_a_query_beside_a_large_one(lib, B, H, Hk, d, Lq, below):
+    """A column that is 2^below of the others and whose keys are 0: the scores are the others', with all
+    digits of theirs."""
+    lens = [120, 50][:B]
+    calls = []
+    for n, k, v in tokens([lens], Hk, d, BF, seed=below):
+        k = k.float() * 2.0 ** 6
+        k[..., 0] = 0
+        calls.append((n, k.to(BF), v))
+    q = torch.randn(B, Lq, H, d, generator=torch.Generator().manual_seed(below)) * 2.0 ** -6
+    q[..., 0] = 2.0 ** (below - 6)
+    out, lse, w = attend(lib, calls, q.to(BF), Hk, d)
+    check_forward(out, w, BF, d, lse)
+
+
+@pytest.mark.parametrize("e", [-132, -126, -118, -110, -95, -94, -93, 0, 95])
+def test_queries_of_any_exponent(lib, e):
+    """bf16 queries from subnormal ones to where their keys are subnormal codes, scores of some 1."""
+    d = 64
+    up = min(max(-e, -97), 120)
+    calls = [(n, (k.float() * 2.0 ** up).to(BF), v) for n, k, v in tokens([[90, 33]], 2, d, BF, seed=3)]
+    q = (torch.randn(2, 2, 4, d, generator=torch.Generator().manual_seed(9)) * 2.0 ** e).to(BF)
+    out, lse, w = attend(lib, calls, q, 2, d)
+    check_forward(out, w, BF, d, lse)
+
+
+def test_the_largest_query_of_all(lib):
+    """The column of the type's largest value meets keys of 0."""
+    d = 64
+    (n, k, v), = tokens([[90]], 2, d, BF, seed=4)
+    k = k.float() * 2.0 ** -96
+    k[..., 5] = 0
+    q = torch.randn(1, 1, 4, d, generator=torch.Generator().manual_seed(10)) * 2.0 ** 97
+    q[..., 5] = torch.finfo(BF).max
+    out, lse, w = attend(lib, [(n, k.to(BF), v)], q.to(BF), 2, d)
+    # Columns around 2^-30 of the largest have some that lie below 2^-32 of it.  Those are off by half of fp16's
+    # smallest step, 2^-25, where the largest is 2^15 at least, 2^-40 of it; a score by that many times the sum
+    # of its key's columns, scaled; a weight by twice that (its own score, and the row's sum).
+    off = d ** -0.5 * 2.0 ** -40 * float(torch.finfo(BF).max) * float(k.to(BF).double().abs().sum(-1).max()) * (1 + 2.0 ** -4)
+    w["score_mass"] = w["score_mass"] + off / ((d + 4) * U32)  # (of which score_error takes 2 (d + 4) roundings)
+    check_forward(out, w, BF, d, lse)
