@@ -1,7 +1,8 @@
 // The 8-bit cache: tokens appended to it, and read back in 16 bits.
 //
 // A block of 16 tokens of one head has one scale, the least power of two s with
-// max |x| <= 448 s; its codes are e4m3(x / s).  A power of two makes x / s exact, so that the
+// max |x| <= 448 s; its codes are e4m3(x / s) (with the largest s, which 1.75 2^127 asks for, 240 at most:
+// 255 would round to 256, an infinity; 240 is off by less than e4m3's half a step still).  A power of two makes x / s exact, so that the
 // one rounding is that of the code, and lets a block that is filled token by token grow its
 // scale: the codes that it holds are halved as often as the scale doubles, which changes
 // nothing above e4m3's subnormals.
@@ -73,17 +74,23 @@ __device__ __forceinline__ __half2 top2(__half2 m, __half2 x) { return __hmax2(m
 template <typename T>
 using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
 
-// Eight values times inv, a power of two, as codes; infinities as NaN.
+// The largest scale, of which a code above 240 would stand for an infinity.
+constexpr float kTopScale = 1.329227995784916e36f;  // 2^120
+
+// Eight values times inv, a power of two, as codes, `most` in magnitude at most; infinities as NaN.
 template <typename T>
-__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
+__device__ __forceinline__ uint2 codes8(const uint4& v, float inv, float most) {
   const T* e = reinterpret_cast<const T*>(&v);
+  auto times = [&](T x) {
+    const float f = finite_or_nan(IO<T>::to_f(x)) * inv;
+    return fabsf(f) > most ? copysignf(most, f) : f;  // (a NaN stays one)
+  };
   uint16_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = f32_codes(finite_or_nan(IO<T>::to_f(e[2 * i])) * inv, finite_or_nan(IO<T>::to_f(e[2 * i + 1])) * inv);
+  for (int i = 0; i < 4; ++i) w[i] = f32_codes(times(e[2 * i]), times(e[2 * i + 1]));
   return make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
 }
-// The same for values without an infinity, fewer instructions.  Products of 16-bit values with a
+// The same for values without an infinity and smaller scales, fewer instructions.  Products of 16-bit values with a
 // power of two are exact where they matter: what leaves the normal range is far below half of
 // the smallest code.  fp16: inv must be one, 2^-16 .. 2^15.
 __device__ __forceinline__ uint2 finite_codes8(const uint4& v, __nv_bfloat162 inv) {
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
     const float inv = inverse_scale(s);
     __syncwarp();  // every lane has read the scale
     auto code_of = [&](int j) { return reinterpret_cast<uint2*>(codes + 512 * (j >> 1) + 256 * (j & 1)); };
-    const bool plain = finite && (!std::is_same<T, __half>::value || (inv >= 1.52587890625e-5f && inv <= 32768.f));
+    const bool plain = finite && (std::is_same<T, __half>::value ? inv >= 1.52587890625e-5f && inv <= 32768.f : s < kTopScale);
     if (plain) {
       const Pair<T> inv2 = both(inv, Pair<T>());
 #pragma unroll
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(256) append_kernel(const StoreArgs a) {
     } else {
 #pragma unroll
       for (int j = 0; j < 2 * SLABS; ++j)
-        if (row0 + 8 * (j & 1) >= from && row0 + 8 * (j & 1) < to) *code_of(j) = codes8<T>(v[j], inv);
+        if (row0 + 8 * (j & 1) >= from && row0 + 8 * (j & 1) < to) *code_of(j) = codes8<T>(v[j], inv, s < kTopScale ? 448.f : 240.f);
     }
     if (from > 0 && grown != 1.f) {  // the block's scale has grown: its older codes again
 #pragma unroll 1

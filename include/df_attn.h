@@ -631,7 +631,7 @@ df_status df_rotary_table(int rot, double base, double factor, double original_l
  * A block is 16 consecutive tokens of one key head.  It has one scale for its keys and one for
  * its values, each the least power of two s (2^-100 at least) with |x| <= 448 s for every
  * finite x of the block; a value is held as the e4m3 code of x / s (nearest, ties to even; NaN
- * and infinities as NaN).  The cache is [n_pages][Hk][page / 16] records of 32 d + 16 bytes:
+ * and infinities as NaN; at the largest s, 2^120, 240 at most, so that what is finite stays so).  The cache is [n_pages][Hk][page / 16] records of 32 d + 16 bytes:
  *     keys' codes [d / 32][16 tokens][32 columns], values' codes likewise, the keys' and the
  *     values' scale (fp32), 8 bytes unused
  *   cache      16-byte aligned, df_cache_bytes() bytes; its contents need not be initialised

@@ -43,6 +43,14 @@ def block_scale(x):
     return 2.0 ** e
 
 
+def block_codes(x, s):
+    """Codes of a block's values at scale s, whose values float32 and bfloat16 hold: those that would
+    round to 2^128 (|x| beyond 248 2^120) get the one below."""
+    x = np.asarray(x, np.float64) / s
+    near = np.isfinite(x) & (np.abs(x) * s >= 248.0 * 2.0 ** 120)
+    return e4m3_codes(np.where(near, np.copysign(240.0, x), x))
+
+
 class CacheOracle:
     """One sequence's keys or values, [tokens, heads, d], as its blocks hold them."""
 
@@ -69,7 +77,7 @@ class CacheOracle:
                     old = self.scale[blk, h]
                     s = max(s, old)
                     self.codes[blk, h, :lo] = e4m3_codes(E4M3[self.codes[blk, h, :lo]] * old / s)
-                self.codes[blk, h, lo:hi] = e4m3_codes(rows / s)
+                self.codes[blk, h, lo:hi] = block_codes(rows, s)
                 self.scale[blk, h] = s
         self.n = end
         return self

@@ -89,3 +89,27 @@ def test_the_largest_query_of_all(lib):
     off = d ** -0.5 * 2.0 ** -40 * float(torch.finfo(BF).max) * float(k.to(BF).double().abs().sum(-1).max()) * (1 + 2.0 ** -4)
     w["score_mass"] = w["score_mass"] + off / ((d + 4) * U32)  # (of which score_error takes 2 (d + 4) roundings)
     check_forward(out, w, BF, d, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF])
+def test_finite_values_stay_finite(lib, dtype):
+    """The largest values of the type: held, read back in every type and attended to."""
+    d, top = 32, float(torch.finfo(dtype).max)
+    v = torch.zeros(4, 1, d)
+    v[0], v[1], v[2, 0, :8], v[3] = top, -top, top, top * torch.linspace(0.8, 1, d)
+    v = v.to(dtype)
+    calls = [([1], torch.zeros_like(v[:1]), v[i:i + 1]) for i in range(4)]
+    cache, table, held = fill(lib, calls, 1, d, 16)
+    want = oracles(calls, 1, d)[0][1].values()
+    half = 2.0 ** -4  # of e4m3
+    assert np.isfinite(want).all() and (np.abs(want - np64(v)) <= half * np.abs(np64(v))).all()
+    for t in (F32, BF, HF):
+        _, got = lib.df_cache_read(cache, table, held, rows=4, dtype=t)
+        assert np.array_equal(np64(got[0]), np.clip(want, -65504, 65504) if t == HF else want)
+    for i in range(4):
+        # a window of one token: its values themselves
+        out = lib.df_cache_attn(torch.ones(1, 1, 1, d, dtype=dtype, device="cuda"), cache, table,
+                                torch.full_like(held, i + 1), window=1)
+        got, ref = np64(out[0, 0, 0]), want[i, 0]
+        ref = np.clip(ref, -65504, 65504) if dtype == HF else ref
+        assert np.isfinite(got).all() and (np.abs(got - ref) <= torch.finfo(dtype).eps * np.abs(ref)).all()
