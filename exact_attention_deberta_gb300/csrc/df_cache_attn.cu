@@ -491,8 +491,12 @@ __device__ __forceinline__ void store4(const DecodeArgs& a, const Rows& w, int i
   int token, head;
   w.place(a, i, &token, &head);
   const size_t at = (size_t)(w.q0 + w.t0 + token) * a.H + w.hk * a.G + head;
-  const uint32_t lo = a.bf16 ? pack_bf16x2(v[0] * inv, v[1] * inv) : pack_f16x2(v[0] * inv, v[1] * inv);
-  const uint32_t hi = a.bf16 ? pack_bf16x2(v[2] * inv, v[3] * inv) : pack_f16x2(v[2] * inv, v[3] * inv);
+  // (fp16: held values may be larger, 65504 is as 65536; what reading back clips is clipped here)
+  auto pack = [&](float x, float y) {
+    if (a.bf16) return pack_bf16x2(x, y);
+    return pack_f16x2(fabsf(x) > 65504.f ? copysignf(65504.f, x) : x, fabsf(y) > 65504.f ? copysignf(65504.f, y) : y);
+  };
+  const uint32_t lo = pack(v[0] * inv, v[1] * inv), hi = pack(v[2] * inv, v[3] * inv);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + 4 * piece) = make_uint2(lo, hi);
   if (a.lse && piece == 0) a.lse[at] = l != 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
 }

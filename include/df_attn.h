@@ -686,7 +686,8 @@ df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t*
  *              sequence are reported, and left alone)
  *   max_length a bound of lengths that the split of the work goes by (any value is right)
  *   lse        NULL, or float32 [B, Lq, H] / [total_q, H]: log of the row's sum of exp
- * A row that sees no token gets zeros and lse = -infinity.  Scores, statistics and sums are fp32;
+ * A row that sees no token gets zeros and lse = -infinity; fp16 results beyond its range (held values
+ * may be) are +-65504, as df_cache_read gives them.  Scores, statistics and sums are fp32;
  * codes enter the products exactly, q too (bf16: down to 2^-32 of the row's largest, in steps of 2^-39 of
  * it below that), the weights as fp16 times 2^14 (11 bits down to 2^-28 of a row's largest).  Tokens that no query of the
  * call sees may hold anything (as may what lies behind the last token in its page); a NaN that a

@@ -91,7 +91,7 @@ def test_the_largest_query_of_all(lib):
     check_forward(out, w, BF, d, lse)
 
 
-@pytest.mark.parametrize("dtype", [BF])
+@pytest.mark.parametrize("dtype", [BF, HF])
 def test_finite_values_stay_finite(lib, dtype):
     """The largest values of the type: held, read back in every type and attended to."""
     d, top = 32, float(torch.finfo(dtype).max)
@@ -113,3 +113,27 @@ def test_finite_values_stay_finite(lib, dtype):
         got, ref = np64(out[0, 0, 0]), want[i, 0]
         ref = np.clip(ref, -65504, 65504) if dtype == HF else ref
         assert np.isfinite(got).all() and (np.abs(got - ref) <= torch.finfo(dtype).eps * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("brought", [HF, BF])
+def test_results_in_fp16_are_those_that_reading_back_gives(lib, brought):
+    """fp16 results of held values beyond its range (65504 itself is held as 65536): +-65504, as they are read
+    back; NaN stays NaN."""
+    d = 32
+    v = torch.zeros(5, 1, d)
+    v[0, 0, :3] = torch.tensor([65504.0, -65504.0, 64000.0])
+    v[1], v[2, 0, 4], v[3] = 65504.0, float("nan"), 1.0
+    v[4] = torch.linspace(-1, 1, d) * (1e6 if brought == BF else 65504.0)
+    calls = [([5], torch.zeros(5, 1, d, dtype=brought), v.to(brought))]
+    cache, table, held = fill(lib, calls, 1, d, 16)
+    read = np64(lib.df_cache_read(cache, table, held, rows=5, dtype=HF)[1])[0, :, 0]
+    q = torch.ones(1, 1, 1, d, dtype=HF, device="cuda")
+    for i in range(5):
+        # a window of one token: its values themselves (the sum's reciprocal is an approximation: a step)
+        got = np64(lib.df_cache_attn(q, cache, table, torch.full_like(held, i + 1), window=1))[0, 0, 0]
+        nan = np.isnan(read[i])
+        assert np.array_equal(np.isnan(got), nan) and np.isfinite(got[~nan]).all()
+        assert (np.abs(got - read[i])[~nan] <= torch.finfo(HF).eps * np.abs(read[i][~nan])).all()
+    # the mean of two that are held as 65536
+    out = lib.df_cache_attn(q, cache, table, torch.full_like(held, 2), window=2)
+    assert float(out[0, 0, 0, 0]) == 65504.0
