@@ -393,6 +393,7 @@ struct Softmax {
         const float down = m_new > m_run[h] ? ex2(m_run[h] - m_new) : 1.f;
         m_run[h] = m_new;
         l_run[h] *= down;
+        if (mt == INFINITY) l_run[h] = __uint_as_float(0x7fffffffu);  // (finite products, an infinite score: else weights of 0)
 #pragma unroll
         for (int c = 0; c < SLABS; ++c)
 #pragma unroll

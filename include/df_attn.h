@@ -691,7 +691,8 @@ df_status df_cache_read(const void* cache, int n_pages, int page, const int32_t*
  * codes enter the products exactly, q too (bf16: down to 2^-32 of the row's largest, in steps of 2^-39 of
  * it below that), the weights as fp16 times 2^14 (11 bits down to 2^-28 of a row's largest).  Tokens that no query of the
  * call sees may hold anything (as may what lies behind the last token in its page); a NaN that a
- * query sees makes results NaN, also those of the call's other queries of that sequence.
+ * query sees makes results NaN, also those of the call's other queries of that sequence, and a score
+ * beyond fp32's range makes its row NaN (a weight of 0, if negative).
  * No atomics, no workspace: equal inputs (max_length among them) give equal bits.  Made for up to some 64 rows (Lq H / Hk)
  * a sequence and key head, which are read once; for long prompts read the tokens back
  * (df_cache_read) and use df_self_attn_fwd. */

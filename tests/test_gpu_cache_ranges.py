@@ -137,3 +137,27 @@ def test_results_in_fp16_are_those_that_reading_back_gives(lib, brought):
     # the mean of two that are held as 65536
     out = lib.df_cache_attn(q, cache, table, torch.full_like(held, 2), window=2)
     assert float(out[0, 0, 0, 0]) == 65504.0
+
+
+def test_scores_beyond_the_range_are_not_a_number(lib):
+    """+infinity among the scores that a query sees: NaN, also where the parts of a sequence are joined;
+    -infinity is a weight of 0."""
+    d, top = 32, float(torch.finfo(BF).max)
+    x = torch.zeros(4, 1, d)
+    x[0], x[1], x[2, 0, :8], x[3] = top, -top, top, top * torch.linspace(0.8, 1, d)
+    x = x.to(BF)
+    cache, table, held = fill(lib, [([1], x[i:i + 1], x[i:i + 1]) for i in range(4)], 1, d, 16)
+    q, lse = torch.ones(1, 1, 1, d, dtype=BF, device="cuda"), torch.zeros(1, 1, 1, device="cuda")
+    for i in range(4):
+        out = lib.df_cache_attn(q, cache, table, torch.full_like(held, i + 1), window=1, lse=lse)
+        if i == 1:
+            assert bool((out == 0).all()) and float(lse) == float("-inf")
+        else:
+            assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    k, v = torch.zeros(3000, 1, d), torch.ones(3000, 1, d)
+    k[1234] = top
+    cache, table, held = fill(lib, [([3000], k.to(BF), v.to(BF))], 1, d, 16)
+    both = torch.cat([q, -q], 2)
+    for bound in (1, 3000):
+        out = lib.df_cache_attn(both, cache, table, held, max_length=bound)[0, 0]
+        assert bool(out[0].isnan().all()) and bool((out[1] == 1).all())
