@@ -736,19 +736,23 @@ __global__ void __launch_bounds__(32 * WARPS) decode_kernel(const DecodeArgs a) 
   if (threadIdx.x == 0) cross_report(s_abort, a.status);
 }
 
-// Cluster sizes, and how many clusters of each a device holds at a time (found once for a kernel;
+// Cluster sizes, and how many clusters of each a device holds at a time (found once for a kernel and device;
 // clusters stay within a part of the GPU, so that it is not the CTAs' number over their size).
 constexpr int kSizes[] = {1, 2, 3, 4, 6, 8, 12, 16}, kSizeCount = 8;
 struct Residency {
-  std::atomic<int> device{-1};
+  std::atomic<bool> known{false};
   std::atomic<int> clusters[kSizeCount] = {};
 };
+constexpr int kDevices = 64;
 
+// The current device's table of `all`, or, of a device beyond those, *own filled anew.
 template <typename Kernel>
-cudaError_t find_residency(Kernel kernel, int threads, int bytes, Residency* r) {
+cudaError_t find_residency(Kernel kernel, int threads, int bytes, Residency (&all)[kDevices], Residency* own, Residency** found) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || r->device.load(std::memory_order_acquire) == dev) return e;
+  if (e != cudaSuccess) return e;
+  Residency* r = *found = dev < kDevices ? all + dev : own;
+  if (r->known.load(std::memory_order_acquire)) return e;
   e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   for (int i = 0; i < kSizeCount && e == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg = {};
@@ -765,7 +769,7 @@ cudaError_t find_residency(Kernel kernel, int threads, int bytes, Residency* r) 
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     r->clusters[i].store(n, std::memory_order_relaxed);
   }
-  if (e == cudaSuccess) r->device.store(dev, std::memory_order_release);
+  if (e == cudaSuccess) r->known.store(true, std::memory_order_release);
   return e;
 }
 
@@ -801,11 +805,12 @@ struct Launch {
 
   cudaError_t plan(long long items, long long tiles) {
     static std::atomic<uint64_t> done{0};
-    static Residency held;
+    static Residency all[kDevices];
+    Residency own, *held = nullptr;
     auto kernel = decode_kernel<SLABS, WR, HALF, WARPS>;
     cudaError_t e = prepare_kernel((const void*)kernel, bytes, 0, &done);
-    if (e == cudaSuccess) e = find_residency(kernel, threads, bytes, &held);
-    if (e == cudaSuccess) cost = splits_for(items, tiles, WARPS / WR, held, &splits, &rounds);
+    if (e == cudaSuccess) e = find_residency(kernel, threads, bytes, all, &own, &held);
+    if (e == cudaSuccess) cost = splits_for(items, tiles, WARPS / WR, *held, &splits, &rounds);
     return e;
   }
   cudaError_t run(DecodeArgs a, long long items, cudaStream_t s) const {
