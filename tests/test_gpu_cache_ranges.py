@@ -161,3 +161,20 @@ def test_scores_beyond_the_range_are_not_a_number(lib):
     for bound in (1, 3000):
         out = lib.df_cache_attn(both, cache, table, held, max_length=bound)[0, 0]
         assert bool(out[0].isnan().all()) and bool((out[1] == 1).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_a_token_that_is_not_a_number_leaves_its_block_alone(lib, dtype):
+    """NaN and infinities appended behind 35 tokens: those are read and attended to as before, bit for bit."""
+    d = 64
+    calls = tokens([[35]], 2, d, dtype, seed=13)
+    cache, table, held = fill(lib, calls, 2, d, 32, spare_pages=1)
+    q = torch.randn(1, 1, 4, d, generator=torch.Generator().manual_seed(14)).to(dtype).cuda()
+    before, rows = lib.df_cache_attn(q, cache, table, held), lib.df_cache_read(cache, table, held, rows=35)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        bad = torch.full((1, 1, 2, d), value, dtype=dtype, device="cuda")
+        lib.df_cache_append(bad, bad, cache, table, held)
+        assert torch.equal(lib.df_cache_attn(q, cache, table, held), before)
+        assert all(torch.equal(a, b) for a, b in zip(lib.df_cache_read(cache, table, held, rows=35), rows))
+        assert bool(lib.df_cache_attn(q, cache, table, held + 1).isnan().all())
+        assert bool(lib.df_cache_read(cache, table, held + 1, rows=36)[0][:, 35].isnan().all())
