@@ -5,7 +5,7 @@
 //   s_ij = scale ks_j (q_i . ck_j),  o_i = sum_j exp(s_ij - lse_i) vs_j cv_j
 // over the visible tokens j, with codes ck, cv and scales ks, vs of j's block.
 //
-// Bound by reading the cache once: 2 d + 1/2 bytes a token and key head, for 4 d G n flops.  So
+// Bound by reading the cache once: 2 d + 1 bytes a token and key head, for 4 d G n flops.  So
 // nothing but the tensor core's old instructions (m16n8k16: a tile of 16 query rows, one block
 // of 16 keys) stands between the bytes and the sums:
 //   - A CTA has four warps (or eight), each on its own: a ring of bulk copies (two blocks' records, one
@@ -23,10 +23,10 @@
 // Sequences are cut over the CTAs of a cluster where there are few of them; the parts are joined
 // through distributed shared memory, without a workspace or a second launch.
 //
-// Measured (GB300): 64 requests of up to 8192 tokens, 24 heads, d = 64, bf16 (1.0 GB): 160 us, 6.3 TB/s;
+// Measured (GB300): 64 requests of up to 8192 tokens, 24 heads, d = 64, bf16 (1.0 GB): 161 us, 6.3 TB/s;
 // 64 sequences of up to 4096 states, 4 key heads of 4 heads, d = 128, fp16: 40 us, 4.3 TB/s; 16 x 4
-// tokens of 32 heads sharing 8, a window of 4096, d = 128, bf16: 38 us, 3.5 TB/s; one request of 512
-// tokens, 12 heads: 6.3 us. A tile of 32 keys takes a warp some 650 instructions at d = 128, and alone
+// tokens of 32 heads sharing 8, a window of 4096, d = 128, bf16: 39 us, 3.5 TB/s; one request of 512
+// tokens, 12 heads: 6.5 us. A tile of 32 keys takes a warp some 650 instructions at d = 128, and alone
 // on its scheduler 2600 cycles: most of them wait for a result of the one before (counters: an
 // instruction every 4 cycles, no pipe above a fifth). So long rows are bound by the number of warps,
 // 12 an SM where the records of d = 128 lie in shared memory (8 with all 16 rows in registers).

@@ -184,7 +184,8 @@ class CrossAttention:
     def attend_stored(self, x, cache, page_table, lengths, cu_seqlens_q=None, max_seqlen_q=1, max_length=None, stream=None,
                       status=None):
         """``attend`` to stored states, for a few rows of each sequence: x [Tq, hidden], packed by
-        cu_seqlens_q, or one row a sequence."""
+        cu_seqlens_q (``max_seqlen_q`` bounds their number; what goes beyond it is reported through ``status``
+        and not computed), or one row a sequence."""
         if stream is not None:
             with binding._current(stream, x):
                 return self.attend_stored(x, cache, page_table, lengths, cu_seqlens_q, max_seqlen_q, max_length, status=status)

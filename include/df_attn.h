@@ -642,8 +642,9 @@ df_status df_rotary_table(int rot, double base, double factor, double original_l
  *   lengths    int32 [B]: tokens that each sequence holds
  *   status     as for df_cross_attn_fwd: DF_ERR_INVALID_ARG also for a token whose page is
  *              missing (not 0 <= id < n_pages, or behind max_pages; it is then neither written
- *              nor attended to), and for a length below 0 or, of an attention, beyond
- *              max_pages * page (taken as 0)
+ *              nor attended to), and for a length below 0 (taken as 0; nothing is appended to such a
+ *              sequence) or, of an attention, beyond max_pages * page (taken as 0).  Where offsets go
+ *              back, appending and reading may leave out other sequences than the reported one, too
  * Sequences may share pages to read; a page that tokens are appended to belongs to one.
  * Errors of the calls below: DF_ERR_INVALID_ARG (NULL pointer, sizes, offsets, overlap of
  * what is written), DF_ERR_UNSUPPORTED (fp32 where not named, d, page, max_pages * page > 2^30,
